@@ -479,6 +479,147 @@ mamba_status mamba_scan_bwd_complex_ex(const void* u, const void* delta, const f
                                        void* workspace, size_t workspace_bytes, void* stream,
                                        int segments);
 
+/* ------------------------------------------------------------------------
+ * Multi-head scan: one decay a head and step, token-major rows.
+ *
+ * Channels are grouped into `heads` of `headdim` (P) channels; the decay is
+ * one scalar A per head, and B, C are shared by the heads of a group (head h
+ * reads group h / (heads / groups)).  Per batch row and head, with the state
+ * h a (P, N) matrix:
+ *
+ *   delta_t = softplus(delta_raw_t + delta_bias)   (or without softplus)
+ *   h_t = exp(delta_t A) h_{t-1} + w_t u_t B_t^T,  h_{-1} = h0 (or 0)
+ *   out_t = h_t C_t + D u_t
+ *   w_t = (exp(delta_t A) - 1) / A  (ZOH; delta_t where A = 0),  delta_t (EULER)
+ *
+ * This is the recurrence at the head of this file with A equal over the
+ * channels and states of a head, in the layout a joined projection writes:
+ *   u, dout, out, du    (batch, seqlen, heads, headdim)
+ *   delta, ddelta       (batch, seqlen, heads)
+ *   B, C, dB, dC        (batch, seqlen, groups, dstate)
+ *   A, D, delta_bias and their gradients   (heads)
+ *   h0, last_state, state, dlast_state, dh0   (batch, heads, headdim, dstate)
+ * u, delta, B and C may be views of wider rows: the shape gives their batch
+ * and token strides in elements (>= 0; 0 repeats one row); the elements of a
+ * token's row are contiguous.  Everything else is dense.
+ * Types: u, delta, B, C, dout, out and du, ddelta, dB, dC in `dtype` (each
+ * rounded once, from float32); the rest float32.
+ * Limits: 1 <= headdim <= 128, 1 <= dstate <= 256, heads a multiple of
+ * groups; pointers aligned to their element (16-byte aligned rows are read
+ * in wider loads).  A of any sign.  reset (nullable, (batch, seqlen) bytes):
+ * the state entering a flagged step is zero, as for mamba_scan_fwd_varlen.
+ * Non-finite values: one in a token of a packed sequence never reaches
+ * another sequence's rows, nor earlier rows of its own, in the forward.
+ * ------------------------------------------------------------------------ */
+typedef struct mamba_heads_shape {
+  int64_t batch, seqlen, heads, headdim, groups, dstate;
+  int64_t u_batch_stride, u_token_stride;
+  int64_t delta_batch_stride, delta_token_stride;
+  int64_t B_batch_stride, B_token_stride;
+  int64_t C_batch_stride, C_token_stride;
+  int delta_softplus;   /* 0 or 1 */
+  int disc;             /* mamba_disc */
+  int dtype;            /* mamba_dtype */
+  int segments;         /* pieces of the sequence run in parallel: 0 = automatic, k = k */
+} mamba_heads_shape;
+
+/* Bytes of device workspace (0 possible; SIZE_MAX for sizes outside the
+ * limits).  Unlike mamba_scan_fwd's it is required. */
+size_t mamba_heads_scan_fwd_workspace_size(const mamba_heads_shape* shape);
+size_t mamba_heads_scan_bwd_workspace_size(const mamba_heads_shape* shape);
+
+/* Forward.  D, delta_bias, h0, reset, last_state may be NULL. */
+mamba_status mamba_heads_scan_fwd(const mamba_heads_shape* shape, const void* u,
+                                  const void* delta, const float* A, const void* B,
+                                  const void* C, const float* D, const float* delta_bias,
+                                  const float* h0, const uint8_t* reset, void* out,
+                                  float* last_state, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Backward, the states recomputed.  dlast_state (nullable) is the gradient
+ * into the last state.  dD, ddelta_bias and dh0 are written where their input
+ * is given (each may be NULL); the others are required.  Sums run in a fixed
+ * order: equal inputs give equal bits. */
+mamba_status mamba_heads_scan_bwd(const mamba_heads_shape* shape, const void* u,
+                                  const void* delta, const float* A, const void* B,
+                                  const void* C, const float* D, const float* delta_bias,
+                                  const float* h0, const uint8_t* reset, const void* dout,
+                                  const float* dlast_state, void* du, void* ddelta, float* dA,
+                                  void* dB, void* dC, float* dD, float* ddelta_bias, float* dh0,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* One step (shape->seqlen must be 1; the batch strides apply), in place on
+ * `state`, a pool of `pool` states (pool, heads, headdim, dstate).  slots
+ * (nullable, batch int32): the state each batch row steps; without it row b
+ * steps state b and pool must be at least batch.  A row whose slot is outside
+ * [0, pool) touches no state and its out is zero; a slot may appear once. */
+mamba_status mamba_heads_state_update(const mamba_heads_shape* shape, float* state,
+                                      const int32_t* slots, int64_t pool, const void* u,
+                                      const void* delta, const float* A, const void* B,
+                                      const void* C, const float* D, const float* delta_bias,
+                                      void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Short causal convolution + SiLU over token-major rows x (batch, seqlen,
+ * dim), the stage before the multi-head scan (the formula of
+ * mamba_conv1d_silu_fwd; w (dim, width) and b (dim) float32, width 2..4).
+ * x may be a view (batch and token strides in elements); out, dout, dx
+ * (batch, seqlen, dim) are dense, of x's type.
+ *   window (nullable): the width - 1 inputs before x, (batch, width - 1,
+ *     dim) of x's type, oldest first; absent = zero.
+ *   window_out (nullable): the last width - 1 inputs of the sequence that
+ *     goes on (zero before its start), to continue from.  Not window itself.
+ *   reset (nullable): inputs before a flagged step do not reach it.
+ * The update is the one-token form over a pool of windows (pool, width - 1,
+ * dim), in place, with slots as for mamba_heads_state_update. */
+mamba_status mamba_conv1d_tokens_fwd(const void* x, int64_t x_batch_stride,
+                                     int64_t x_token_stride, const float* w, const float* b,
+                                     const void* window, const uint8_t* reset, int64_t width,
+                                     mamba_dtype dt, int64_t batch, int64_t dim, int64_t seqlen,
+                                     void* out, void* window_out, void* stream);
+
+/* Bytes of device workspace of the backward (SIZE_MAX if unsupported). */
+size_t mamba_conv1d_tokens_bwd_workspace_size(int64_t batch, int64_t dim, int64_t seqlen,
+                                              int64_t width);
+
+/* dw (dim, width) and db (dim, nullable) float32; dwindow (nullable) like
+ * window.  Sums run in a fixed order. */
+mamba_status mamba_conv1d_tokens_bwd(const void* x, int64_t x_batch_stride,
+                                     int64_t x_token_stride, const float* w, const float* b,
+                                     const void* window, const uint8_t* reset, const void* dout,
+                                     int64_t width, mamba_dtype dt, int64_t batch, int64_t dim,
+                                     int64_t seqlen, void* dx, float* dw, float* db,
+                                     void* dwindow, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+mamba_status mamba_conv1d_tokens_update(const void* x, int64_t x_batch_stride, void* window,
+                                        const int32_t* slots, int64_t pool, const float* w,
+                                        const float* b, int64_t width, mamba_dtype dt,
+                                        int64_t batch, int64_t dim, void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gated group norm of rows (rows, dim), the stage after the scan.  With the
+ * dim channels in `groups` equal groups and g = SiLU(z) (1 without z):
+ *   gate_first:   v = x g,  out = v / sqrt(mean_group(v^2) + eps) * weight
+ *   otherwise:    out = x / sqrt(mean_group(x^2) + eps) * weight * g
+ * x and z may be views (row strides in elements); out, dout, dx, dz dense, of
+ * x's type; weight (nullable = 1) and dweight (dim) float32. */
+mamba_status mamba_gated_norm_fwd(const void* x, int64_t x_row_stride, const void* z,
+                                  int64_t z_row_stride, const float* weight, int64_t rows,
+                                  int64_t dim, int64_t groups, float eps, int gate_first,
+                                  mamba_dtype dt, void* out, void* stream);
+
+size_t mamba_gated_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t groups);
+
+/* dz is required with z, dweight with weight.  The row statistics are formed
+ * again from x and z; sums run in a fixed order. */
+mamba_status mamba_gated_norm_bwd(const void* x, int64_t x_row_stride, const void* z,
+                                  int64_t z_row_stride, const float* weight, const void* dout,
+                                  int64_t rows, int64_t dim, int64_t groups, float eps,
+                                  int gate_first, mamba_dtype dt, void* dx, void* dz,
+                                  float* dweight, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif

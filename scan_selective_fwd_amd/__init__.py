@@ -539,3 +539,14 @@ class SelectiveScanFn(torch.autograd.Function):
 def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softplus=True,
                    disc="zoh"):
     return SelectiveScanFn.apply(u, delta, A, B, C, D, z, delta_bias, delta_softplus, disc)
+
+
+from .heads import (conv1d_tokens, conv1d_tokens_bwd, conv1d_tokens_fwd,  # noqa: E402
+                    conv1d_tokens_update, gated_norm, gated_norm_bwd, gated_norm_fwd,
+                    heads_bwd_workspace_bytes, heads_fwd_workspace_bytes, heads_scan,
+                    heads_scan_bwd, heads_scan_fwd, heads_state_update)
+
+__all__ += ["heads_scan_fwd", "heads_scan_bwd", "heads_scan", "heads_state_update",
+            "heads_fwd_workspace_bytes", "heads_bwd_workspace_bytes",
+            "conv1d_tokens_fwd", "conv1d_tokens_bwd", "conv1d_tokens", "conv1d_tokens_update",
+            "gated_norm_fwd", "gated_norm_bwd", "gated_norm"]

@@ -34,6 +34,11 @@ EXPORTS = (
     "mamba_scan_bwd_complex_ex", "mamba_state_update_complex",
     "mamba_scan_fwd_complex_workspace_size", "mamba_scan_fwd_complex_workspace_size_ex",
     "mamba_scan_bwd_complex_workspace_size_ex", "mamba_scan_bwd_noalloc",
+    "mamba_heads_scan_fwd_workspace_size", "mamba_heads_scan_bwd_workspace_size",
+    "mamba_heads_scan_fwd", "mamba_heads_scan_bwd", "mamba_heads_state_update",
+    "mamba_conv1d_tokens_fwd", "mamba_conv1d_tokens_bwd_workspace_size",
+    "mamba_conv1d_tokens_bwd", "mamba_conv1d_tokens_update",
+    "mamba_gated_norm_fwd", "mamba_gated_norm_bwd_workspace_size", "mamba_gated_norm_bwd",
 )
 
 
@@ -47,6 +52,19 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _sz = ctypes.c_size_t
+
+_f32 = ctypes.c_float
+
+
+class HeadsShape(ctypes.Structure):
+    """mamba_heads_shape."""
+
+    _fields_ = ([(n, _i64) for n in (
+        "batch", "seqlen", "heads", "headdim", "groups", "dstate",
+        "u_batch_stride", "u_token_stride", "delta_batch_stride", "delta_token_stride",
+        "B_batch_stride", "B_token_stride", "C_batch_stride", "C_token_stride")]
+        + [(n, _int) for n in ("delta_softplus", "disc", "dtype", "segments")])
+
 
 _lib = None
 
@@ -128,6 +146,32 @@ def load(path: str = LIB_PATH):
                                                + [_vp, _vp])
     lib.mamba_state_update.restype = _int
     lib.mamba_state_update.argtypes = [_vp] * 9 + [_int, _int, _int] + [_i64] * 3 + [_vp, _vp]
+    shape = ctypes.POINTER(HeadsShape)
+    for name in ("mamba_heads_scan_fwd_workspace_size", "mamba_heads_scan_bwd_workspace_size"):
+        f = getattr(lib, name)
+        f.restype = _sz
+        f.argtypes = [shape]
+    lib.mamba_heads_scan_fwd.argtypes = [shape] + [_vp] * 12 + [_sz, _vp]
+    lib.mamba_heads_scan_bwd.argtypes = [shape] + [_vp] * 20 + [_sz, _vp]
+    lib.mamba_heads_state_update.argtypes = [shape, _vp, _vp, _i64] + [_vp] * 9
+    lib.mamba_conv1d_tokens_fwd.argtypes = ([_vp, _i64, _i64] + [_vp] * 4 + [_i64, _int]
+                                            + [_i64] * 3 + [_vp] * 3)
+    lib.mamba_conv1d_tokens_bwd_workspace_size.restype = _sz
+    lib.mamba_conv1d_tokens_bwd_workspace_size.argtypes = [_i64] * 4
+    lib.mamba_conv1d_tokens_bwd.argtypes = ([_vp, _i64, _i64] + [_vp] * 5 + [_i64, _int]
+                                            + [_i64] * 3 + [_vp] * 5 + [_sz, _vp])
+    lib.mamba_conv1d_tokens_update.argtypes = ([_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _int]
+                                               + [_i64] * 2 + [_vp] * 2)
+    lib.mamba_gated_norm_fwd.argtypes = ([_vp, _i64, _vp, _i64, _vp] + [_i64] * 3
+                                         + [_f32, _int, _int, _vp, _vp])
+    lib.mamba_gated_norm_bwd_workspace_size.restype = _sz
+    lib.mamba_gated_norm_bwd_workspace_size.argtypes = [_i64] * 3
+    lib.mamba_gated_norm_bwd.argtypes = ([_vp, _i64, _vp, _i64, _vp, _vp] + [_i64] * 3
+                                         + [_f32, _int, _int] + [_vp] * 4 + [_sz, _vp])
+    for name in ("mamba_heads_scan_fwd", "mamba_heads_scan_bwd", "mamba_heads_state_update",
+                 "mamba_conv1d_tokens_fwd", "mamba_conv1d_tokens_bwd",
+                 "mamba_conv1d_tokens_update", "mamba_gated_norm_fwd", "mamba_gated_norm_bwd"):
+        getattr(lib, name).restype = _int
     _lib = lib
     return lib
 

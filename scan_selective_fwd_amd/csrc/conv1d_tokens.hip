@@ -1,0 +1,348 @@
+// Short causal depthwise convolution + SiLU over token-major rows:
+//   pre_t = b + sum_k w[k] x_{t-k} over the lags k < W that stay in t's
+//   sequence, out_t = pre_t sigmoid(pre_t)
+// and its backward, dpre_t = dout_t silu'(pre_t):
+//   dx_s = sum_k w[k] dpre_{s+k},  dw[k] = sum_t dpre_t x_{t-k},  db = sum_t dpre_t.
+//
+// Channels are contiguous, so a lane owns 16 bytes of them and marches along a
+// run of tokens with the last three inputs (and, backwards, the four open
+// sums of dx) in registers: every row is read once by its run and the three
+// rows between runs twice.  Both kernels are bound by HBM.
+#include "heads_common.hpp"
+
+namespace mscan {
+
+namespace {
+
+constexpr int kLags = 4;
+constexpr int kFwdRun = 16;   // tokens a lane takes in the forward
+
+// Weights by lag: w4[k] multiplies x_{t-k}; lags past the width are zero.
+template <int V>
+__device__ __forceinline__ void load_lags(const float* w, int W, int64_t c, float (&w4)[kLags][V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int k = 0; k < kLags; ++k) w4[k][v] = k < W ? w[(c + v) * W + (W - 1 - k)] : 0.0f;
+}
+
+// Input row s of batch row b, s in [-3, L): from x, the window before it, or zero.
+template <typename T, int V>
+__device__ __forceinline__ void input_row(const TokConvParams& p, int64_t b, int64_t s, int64_t c,
+                                          float (&v)[V]) {
+  if (s >= 0) {
+    load_vec<T, V>(p.x.p, b * p.x.batch + s * p.x.token + c, v);
+  } else if (p.window && s + p.W - 1 >= 0) {
+    load_vec<T, V>(p.window, (b * (p.W - 1) + s + p.W - 1) * p.dim + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+  }
+}
+
+// The inputs at lags 1..3 of step t0: h[k] = x_{t0-1-k}, zero outside the
+// sequence that reaches t0 - 1.
+template <typename T, int V, bool RST>
+__device__ __forceinline__ void history(const TokConvParams& p, const uint8_t* rst, int64_t b,
+                                        int64_t t0, int64_t c, float (&h)[3][V]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) input_row<T, V>(p, b, t0 - 1 - k, c, h[k]);
+  if constexpr (RST) {
+    // a flag at t0 - 1 - k hides the inputs before that step
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (t0 - 1 - k >= 0 && rst[t0 - 1 - k] != 0)
+#pragma unroll
+        for (int j = k + 1; j < 3; ++j)
+#pragma unroll
+          for (int v = 0; v < V; ++v) h[j][v] = 0.0f;
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void clear(float (&h)[3][V]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[k][v] = 0.0f;
+}
+
+template <int V>
+__device__ __forceinline__ void push(float (&h)[3][V], const float (&x)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    h[2][v] = h[1][v];
+    h[1][v] = h[0][v];
+    h[0][v] = x[v];
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void pre_act(const float (&w4)[kLags][V], const float (&cb)[V],
+                                        const float (&x)[V], const float (&h)[3][V],
+                                        float (&pre)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float a = __builtin_fmaf(w4[0][v], x[v], cb[v]);
+#pragma unroll
+    for (int k = 1; k < kLags; ++k) a = __builtin_fmaf(w4[k][v], h[k - 1][v], a);
+    pre[v] = a;
+  }
+}
+
+template <typename T, int V, bool RST>
+__global__ __launch_bounds__(256) void tokconv_fwd_kernel(const TokConvParams p) {
+  const int64_t nvec = p.dim / V;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t run = i / nvec;
+  if (run >= p.batch * p.tiles) return;
+  const int64_t c = (i - run * nvec) * V;
+  const int64_t b = run / p.tiles;
+  const int64_t t0 = (run - b * p.tiles) * kFwdRun;
+  const uint8_t* rst = RST ? p.reset + b * p.L : nullptr;
+  float w4[kLags][V], cb[V], h[3][V];
+  load_lags<V>(p.w, p.W, c, w4);
+#pragma unroll
+  for (int v = 0; v < V; ++v) cb[v] = p.b ? p.b[c + v] : 0.0f;
+  history<T, V, RST>(p, rst, b, t0, c, h);
+  const int64_t n = p.L - t0 < kFwdRun ? p.L - t0 : kFwdRun;
+  const int64_t x0 = b * p.x.batch + t0 * p.x.token + c;
+  const int64_t o0 = (b * p.L + t0) * p.dim + c;
+  auto step = [&](int64_t j, const float (&x)[V]) {
+    if constexpr (RST)
+      if (rst[t0 + j] != 0) clear<V>(h);
+    float pre[V];
+    pre_act<V>(w4, cb, x, h, pre);
+    push<V>(h, x);
+#pragma unroll
+    for (int v = 0; v < V; ++v) pre[v] = silu(pre[v]);
+    store_vec<T, V>(p.out, o0 + j * p.dim, pre);
+  };
+  if (n == kFwdRun) {
+    float x[kFwdRun][V];
+#pragma unroll
+    for (int j = 0; j < kFwdRun; ++j) load_vec<T, V>(p.x.p, x0 + j * p.x.token, x[j]);
+#pragma unroll
+    for (int j = 0; j < kFwdRun; ++j) step(j, x[j]);
+  } else {
+    for (int64_t j = 0; j < n; ++j) {
+      float x[V];
+      load_vec<T, V>(p.x.p, x0 + j * p.x.token, x);
+      step(j, x);
+    }
+  }
+  if (p.window_out && t0 + n == p.L) {
+    // h holds the last three inputs of the sequence that goes on
+    for (int k = 0; k < p.W - 1; ++k)
+      store_vec<T, V>(p.window_out, (b * (p.W - 1) + (p.W - 2 - k)) * p.dim + c,
+                      k == 0 ? h[0] : k == 1 ? h[1] : h[2]);
+  }
+}
+
+// d silu(a) / da.
+__device__ __forceinline__ float dsilu(float a) {
+  const float sg = sigmoid(a);
+  return sg * __builtin_fmaf(a, 1.0f - sg, 1.0f);
+}
+
+// A block: 64 lanes of channels by 4 waves, each a run of kTokConvRun tokens.
+template <typename T, int V, bool RST>
+__global__ __launch_bounds__(256) void tokconv_bwd_kernel(const TokConvParams p) {
+  __shared__ float red[4][kLags + 1][64 * V];
+  const int64_t ctiles = (p.dim + 64 * V - 1) / (64 * V);
+  const int64_t tile = blockIdx.x / ctiles;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (blockIdx.x - tile * ctiles) * (64 * V) + lane * V;
+  const int64_t b = tile / p.tiles;
+  const int64_t t0 = (tile - b * p.tiles) * kTokConvTile + wave * kTokConvRun;
+  float dw[kLags][V], db[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    db[v] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kLags; ++k) dw[k][v] = 0.0f;
+  }
+  if (c < p.dim && t0 < p.L) {
+    const uint8_t* rst = RST ? p.reset + b * p.L : nullptr;
+    float w4[kLags][V], cb[V], h[3][V], acc[3][V];   // acc[k]: dx_{t-1-k} so far
+    load_lags<V>(p.w, p.W, c, w4);
+#pragma unroll
+    for (int v = 0; v < V; ++v) cb[v] = p.b ? p.b[c + v] : 0.0f;
+    history<T, V, RST>(p, rst, b, t0, c, h);
+    clear<V>(acc);
+    // lags of step t that stay in its sequence: up to `age`
+    int age = 3;
+    if constexpr (RST)
+      for (int k = 3; k >= 1; --k)
+        if (t0 - k >= 0) age = rst[t0 - k] != 0 ? 0 : (age < 3 ? age + 1 : 3);
+    const int64_t x0 = b * p.x.batch + c, o0 = b * p.L * p.dim + c;
+    for (int j = 0; j < kTokConvRun + 3; ++j) {
+      const int64_t t = t0 + j;
+      const bool live = t < p.L;
+      float x[V], g[V], pre[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = g[v] = 0.0f;
+      if (live) {
+        load_vec<T, V>(p.x.p, x0 + t * p.x.token, x);
+        load_vec<T, V>(p.dout, o0 + t * p.dim, g);
+        if constexpr (RST) {
+          if (rst[t] != 0) {
+            clear<V>(h);
+            age = 0;
+          } else {
+            age = age < 3 ? age + 1 : 3;
+          }
+        }
+        pre_act<V>(w4, cb, x, h, pre);
+#pragma unroll
+        for (int v = 0; v < V; ++v) g[v] *= dsilu(pre[v]);
+        if (j < kTokConvRun) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            db[v] += g[v];
+            dw[0][v] = __builtin_fmaf(g[v], x[v], dw[0][v]);
+#pragma unroll
+            for (int k = 1; k < kLags; ++k) dw[k][v] = __builtin_fmaf(g[v], h[k - 1][v], dw[k][v]);
+          }
+        }
+      }
+      // dx_{t-3} is complete with this step's share
+      float done[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        done[v] = (!RST || age >= 3) ? __builtin_fmaf(w4[3][v], g[v], acc[2][v]) : acc[2][v];
+        acc[2][v] = (!RST || age >= 2) ? __builtin_fmaf(w4[2][v], g[v], acc[1][v]) : acc[1][v];
+        acc[1][v] = (!RST || age >= 1) ? __builtin_fmaf(w4[1][v], g[v], acc[0][v]) : acc[0][v];
+        acc[0][v] = w4[0][v] * g[v];
+      }
+      push<V>(h, x);
+      const int64_t s = t - 3;
+      if (j >= 3) {
+        if (s < p.L) store_vec<T, V>(p.dx, o0 + s * p.dim, done);
+      } else if (t0 == 0 && p.dwindow && s + p.W - 1 >= 0) {
+        store_vec<T, V>(p.dwindow, (b * (p.W - 1) + s + p.W - 1) * p.dim + c, done);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int k = 0; k < kLags; ++k) red[wave][k][v * 64 + lane] = dw[k][v];
+    red[wave][kLags][v * 64 + lane] = db[v];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < (kLags + 1) * 64 * V; i += 256) {
+    const int k = i / (64 * V), r = i - k * (64 * V);
+    const int64_t ch = (blockIdx.x - tile * ctiles) * (64 * V) + (r & 63) * V + (r >> 6);
+    const float sum = (red[0][k][r] + red[1][k][r]) + (red[2][k][r] + red[3][k][r]);
+    // rows 0..W-1: dw by position (lag W-1-row), row W: db
+    if (ch < p.dim && (k < p.W || k == kLags))
+      p.part[(tile * (p.W + 1) + (k == kLags ? p.W : p.W - 1 - k)) * p.dim + ch] = sum;
+  }
+}
+
+// dw, db: the tiles' shares summed in order, 8 slices of them by 32 channels.
+__global__ __launch_bounds__(256) void tokconv_sum_kernel(const TokConvParams p) {
+  __shared__ float red[8][32];
+  const int64_t ctiles = (p.dim + 31) / 32;
+  const int k = (int)(blockIdx.x / ctiles);
+  const int cl = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int64_t c = (blockIdx.x - (int64_t)k * ctiles) * 32 + cl;
+  const int64_t n = p.batch * p.tiles;
+  float sum = 0.0f;
+  if (c < p.dim)
+    for (int64_t i = sl; i < n; i += 8) sum += p.part[(i * (p.W + 1) + k) * p.dim + c];
+  red[sl][cl] = sum;
+  __syncthreads();
+  if (sl == 0 && c < p.dim) {
+    for (int j = 1; j < 8; ++j) sum += red[j][cl];
+    if (k < p.W) p.dw[c * p.W + k] = sum;
+    else if (p.db) p.db[c] = sum;
+  }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(256) void tokconv_step_kernel(const TokConvStepParams p) {
+  const int64_t nvec = p.dim / V;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t b = i / nvec;
+  if (b >= p.batch) return;
+  const int64_t c = (i - b * nvec) * V;
+  const int64_t slot = p.slots ? (int64_t)p.slots[b] : b;
+  float pre[V];
+  if (slot < 0 || slot >= p.pool) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) pre[v] = 0.0f;
+    store_vec<T, V>(p.out, b * p.dim + c, pre);
+    return;
+  }
+  const int64_t w0 = slot * (p.W - 1) * p.dim + c;
+  float w4[kLags][V], cb[V], x[V], h[3][V];
+  clear<V>(h);
+  load_vec<T, V>(p.x, b * p.x_batch + c, x);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (k < p.W - 1) load_vec<T, V>(p.window, w0 + (p.W - 2 - k) * p.dim, h[k]);
+  load_lags<V>(p.w, p.W, c, w4);
+#pragma unroll
+  for (int v = 0; v < V; ++v) cb[v] = p.b ? p.b[c + v] : 0.0f;
+  pre_act<V>(w4, cb, x, h, pre);
+#pragma unroll
+  for (int v = 0; v < V; ++v) pre[v] = silu(pre[v]);
+  store_vec<T, V>(p.out, b * p.dim + c, pre);
+  // the window moves on by one token
+  push<V>(h, x);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (k < p.W - 1) store_vec<T, V>(p.window, w0 + (p.W - 2 - k) * p.dim, h[k]);
+}
+
+unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); }
+
+template <typename T, int V>
+hipError_t fwd_tv(TokConvParams p, hipStream_t s) {
+  p.tiles = (p.L + kFwdRun - 1) / kFwdRun;
+  const dim3 grid(blocks_of(p.batch * p.tiles * (p.dim / V)));
+  if (p.reset) hipLaunchKernelGGL((tokconv_fwd_kernel<T, V, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((tokconv_fwd_kernel<T, V, false>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t bwd_tv(const TokConvParams& p, hipStream_t s) {
+  const int64_t ctiles = (p.dim + 64 * V - 1) / (64 * V);
+  const dim3 grid((unsigned)(p.batch * p.tiles * ctiles));
+  if (p.reset) hipLaunchKernelGGL((tokconv_bwd_kernel<T, V, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((tokconv_bwd_kernel<T, V, false>), grid, dim3(256), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const unsigned sums = (unsigned)((p.W + 1) * ((p.dim + 31) / 32));
+  hipLaunchKernelGGL(tokconv_sum_kernel, dim3(sums), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t step_tv(const TokConvStepParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((tokconv_step_kernel<T, V>), dim3(blocks_of(p.batch * (p.dim / V))),
+                     dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t dispatch_tokconv_fwd(const TokConvParams& p, int dtype, hipStream_t s) {
+  if (dtype == 0) return p.vec ? fwd_tv<float, 4>(p, s) : fwd_tv<float, 1>(p, s);
+  return p.vec ? fwd_tv<bf16_t, 8>(p, s) : fwd_tv<bf16_t, 1>(p, s);
+}
+
+hipError_t dispatch_tokconv_bwd(const TokConvParams& p, int dtype, hipStream_t s) {
+  if (dtype == 0) return p.vec ? bwd_tv<float, 4>(p, s) : bwd_tv<float, 1>(p, s);
+  return p.vec ? bwd_tv<bf16_t, 8>(p, s) : bwd_tv<bf16_t, 1>(p, s);
+}
+
+hipError_t dispatch_tokconv_step(const TokConvStepParams& p, int dtype, hipStream_t s) {
+  if (dtype == 0) return p.vec ? step_tv<float, 4>(p, s) : step_tv<float, 1>(p, s);
+  return p.vec ? step_tv<bf16_t, 8>(p, s) : step_tv<bf16_t, 1>(p, s);
+}
+
+}  // namespace mscan

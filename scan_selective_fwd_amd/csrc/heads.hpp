@@ -1,0 +1,133 @@
+// Parameters and dispatchers of the multi-head operators: the scan with one
+// decay a head, its single-token form, the token-major convolution and the
+// gated group norm.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mscan {
+
+// A batch of token rows: element (b, t, i) at p[b * batch + t * token + i].
+struct Rows {
+  const void* p;
+  int64_t batch, token;
+};
+
+struct HeadsParams {
+  Rows u, delta, B, C;
+  const float* A;
+  const float* D;        // nullable
+  const float* bias;     // nullable
+  const float* h0;       // nullable
+  const uint8_t* reset;  // nullable
+  int64_t batch, L;
+  int H, P, G, N;
+  int softplus, zoh;
+  int vec;               // rows of u, B, C (and dout, out) start 16-byte aligned
+};
+
+struct HeadsFwdParams : HeadsParams {
+  void* out;
+  float* last;           // nullable
+};
+
+struct HeadsBwdParams : HeadsParams {
+  const void* dout;
+  const float* dlast;    // nullable
+  void* du;
+  void* ddelta;
+  float* dA;
+  void* dB;
+  void* dC;
+  float* dD;             // nullable
+  float* dbias;          // nullable
+  float* dh0;            // nullable
+  // workspace
+  float* states;         // (batch, H, L) times one padded state
+  float* dB_part;        // (batch, L, H, N)
+  float* dC_part;        // (batch, L, H, N)
+  float* head_part;      // (batch, H, 3): dA, dD, dbias
+};
+
+struct HeadsStepParams : HeadsParams {
+  float* state;
+  const int32_t* slots;  // nullable
+  int64_t pool;
+  void* out;
+};
+
+hipError_t dispatch_heads_fwd(const HeadsFwdParams& p, int dtype, hipStream_t s);
+hipError_t dispatch_heads_bwd(const HeadsBwdParams& p, int dtype, hipStream_t s);
+hipError_t dispatch_heads_step(const HeadsStepParams& p, int dtype, hipStream_t s);
+
+struct TokConvParams {
+  Rows x;
+  const float* w;
+  const float* b;        // nullable
+  const void* window;    // nullable
+  const uint8_t* reset;  // nullable
+  int64_t batch, dim, L;
+  int W;
+  bool vec;              // rows start 16-byte aligned: 16-byte loads
+  int64_t tiles;         // token tiles of the launch
+  // forward
+  void* out;
+  void* window_out;      // nullable
+  // backward
+  const void* dout;
+  void* dx;
+  float* dw;
+  float* db;             // nullable
+  void* dwindow;         // nullable
+  float* part;           // (batch * tiles, W + 1, dim): the tiles' shares of dw, db
+};
+
+// Token tile of the backward: a block's 4 waves take kTokConvRun tokens each.
+constexpr int kTokConvRun = 16;
+constexpr int kTokConvTile = 4 * kTokConvRun;
+
+hipError_t dispatch_tokconv_fwd(const TokConvParams& p, int dtype, hipStream_t s);
+hipError_t dispatch_tokconv_bwd(const TokConvParams& p, int dtype, hipStream_t s);
+
+struct TokConvStepParams {
+  const void* x;
+  int64_t x_batch;
+  void* window;
+  const int32_t* slots;  // nullable
+  int64_t pool, batch, dim;
+  const float* w;
+  const float* b;        // nullable
+  void* out;
+  int W;
+  bool vec;
+};
+
+hipError_t dispatch_tokconv_step(const TokConvStepParams& p, int dtype, hipStream_t s);
+
+struct NormParams {
+  const void* x;
+  const void* z;         // nullable
+  const float* w;        // nullable
+  int64_t x_row, z_row;
+  int64_t rows, dim, gs; // gs = dim / groups
+  int groups;
+  float eps;
+  bool gate_first, vec;
+  void* out;
+  // backward
+  const void* dout;
+  void* dx;
+  void* dz;              // nullable
+  float* dw;             // nullable
+  float* part;           // (parts, dim)
+  int64_t parts;
+};
+
+// Blocks that share the rows of one group in the norm's backward.
+int64_t norm_parts(int64_t rows, int64_t groups);
+
+hipError_t dispatch_norm_fwd(const NormParams& p, int dtype, hipStream_t s);
+hipError_t dispatch_norm_bwd(const NormParams& p, int dtype, hipStream_t s);
+
+}  // namespace mscan

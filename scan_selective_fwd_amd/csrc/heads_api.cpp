@@ -1,0 +1,403 @@
+// C ABI of the multi-head operators: argument checks, workspace carving and
+// dispatch.  Nothing here allocates, frees or synchronizes; every launch goes
+// on the caller's stream.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "heads.hpp"
+#include "mamba_scan.h"
+
+namespace {
+
+constexpr int64_t kMaxHeadDim = 128;
+constexpr int64_t kMaxHeadState = 256;
+constexpr int64_t kLim = (int64_t)1 << 62;
+constexpr int64_t kGridLim = 0x7FFFFFFF;
+
+int esize(int dt) { return dt == MAMBA_F32 ? 4 : 2; }
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// Nullable pointers pass.
+bool aligned_f32(const void* p) { return aligned(p, 4); }
+
+mamba_status hip_status(hipError_t e) { return e == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP; }
+
+hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
+
+// a * b <= kLim for a, b >= 0.
+bool mul_ok(int64_t a, int64_t b) { return b == 0 || a <= kLim / b; }
+
+// Whether (batch, tokens) rows at these strides stay inside 2^62 elements.
+bool span_ok(int64_t batch, int64_t sb, int64_t tokens, int64_t st) {
+  return mul_ok(batch, sb) && mul_ok(tokens, st) && batch * sb <= kLim - tokens * st;
+}
+
+// Whether rows at p with these strides can be read in 16-byte pieces.
+bool rows16(const void* p, int64_t sb, int64_t st, int64_t run, int es) {
+  const int64_t v = 16 / es;
+  return aligned(p, 16) && sb % v == 0 && st % v == 0 && run % v == 0;
+}
+
+mamba_status check_shape(const mamba_heads_shape* s) {
+  if (!s) return MAMBA_ERR_NULL_PTR;
+  if (s->dtype != MAMBA_F32 && s->dtype != MAMBA_BF16) return MAMBA_ERR_DTYPE;
+  if (s->disc != MAMBA_DISC_ZOH && s->disc != MAMBA_DISC_EULER) return MAMBA_ERR_DTYPE;
+  if (s->batch <= 0 || s->seqlen <= 0 || s->heads <= 0 || s->headdim <= 0 || s->groups <= 0 ||
+      s->dstate <= 0)
+    return MAMBA_ERR_SHAPE;
+  if (s->heads % s->groups != 0) return MAMBA_ERR_SHAPE;
+  if (s->segments < 0) return MAMBA_ERR_INVALID;
+  if (s->headdim > kMaxHeadDim || s->dstate > kMaxHeadState) return MAMBA_ERR_UNSUPPORTED;
+  if (s->heads > (1 << 20) || s->batch > kGridLim / s->heads) return MAMBA_ERR_UNSUPPORTED;
+  // dense (batch, seqlen, heads, headdim or dstate) arrays, in bytes
+  if (s->seqlen > kLim / 1024 / (s->batch * s->heads)) return MAMBA_ERR_UNSUPPORTED;
+  const int64_t strides[] = {s->u_batch_stride, s->u_token_stride, s->delta_batch_stride,
+                             s->delta_token_stride, s->B_batch_stride, s->B_token_stride,
+                             s->C_batch_stride, s->C_token_stride};
+  for (int i = 0; i < 8; i += 2) {
+    if (strides[i] < 0 || strides[i + 1] < 0) return MAMBA_ERR_SHAPE;
+    if (!span_ok(s->batch, strides[i], s->seqlen, strides[i + 1])) return MAMBA_ERR_UNSUPPORTED;
+  }
+  return MAMBA_OK;
+}
+
+// The parameters all forms share; `vec` covers u, B and C only.
+mscan::HeadsParams common(const mamba_heads_shape* s, const void* u, const void* delta,
+                          const float* A, const void* B, const void* C, const float* D,
+                          const float* bias, const float* h0, const uint8_t* reset) {
+  mscan::HeadsParams p{};
+  p.u = {u, s->u_batch_stride, s->u_token_stride};
+  p.delta = {delta, s->delta_batch_stride, s->delta_token_stride};
+  p.B = {B, s->B_batch_stride, s->B_token_stride};
+  p.C = {C, s->C_batch_stride, s->C_token_stride};
+  p.A = A; p.D = D; p.bias = bias; p.h0 = h0; p.reset = reset;
+  p.batch = s->batch; p.L = s->seqlen;
+  p.H = (int)s->heads; p.P = (int)s->headdim; p.G = (int)s->groups; p.N = (int)s->dstate;
+  p.softplus = s->delta_softplus != 0; p.zoh = s->disc == MAMBA_DISC_ZOH;
+  const int es = esize(s->dtype);
+  p.vec = rows16(u, p.u.batch, p.u.token, p.P, es) && rows16(B, p.B.batch, p.B.token, p.N, es) &&
+          rows16(C, p.C.batch, p.C.token, p.N, es);
+  return p;
+}
+
+mamba_status check_inputs(const mamba_heads_shape* s, const void* u, const void* delta,
+                          const float* A, const void* B, const void* C, const float* D,
+                          const float* bias, const float* h0) {
+  if (!u || !delta || !A || !B || !C) return MAMBA_ERR_NULL_PTR;
+  const size_t es = (size_t)esize(s->dtype);
+  if (!aligned(u, es) || !aligned(delta, es) || !aligned(B, es) || !aligned(C, es))
+    return MAMBA_ERR_ALIGNMENT;
+  if (!aligned_f32(A) || !aligned_f32(D) || !aligned_f32(bias) || !aligned_f32(h0))
+    return MAMBA_ERR_ALIGNMENT;
+  return MAMBA_OK;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspace of the backward: see HeadsBwdParams.
+struct BwdLayout {
+  size_t states, dB_part, dC_part, head_part, total;
+};
+
+bool bwd_layout(const mamba_heads_shape* s, BwdLayout* l) {
+  const size_t th = (size_t)(s->batch * s->heads) * (size_t)s->seqlen;
+  size_t at = 0;
+  const size_t n = s->dstate <= 16 ? 16 : s->dstate <= 64 ? 64 : s->dstate <= 128 ? 128 : 256;
+  l->states = at; at += up256(th * 128 * n * 4);
+  l->dB_part = at; at += up256(th * (size_t)s->dstate * 4);
+  l->dC_part = at; at += up256(th * (size_t)s->dstate * 4);
+  l->head_part = at; at += up256((size_t)(s->batch * s->heads) * 12);
+  l->total = at;
+  return true;
+}
+
+mamba_status check_conv(const void* x, const float* w, const float* b, int64_t width,
+                        mamba_dtype dt, int64_t batch, int64_t dim, int64_t L) {
+  if (dt != MAMBA_F32 && dt != MAMBA_BF16) return MAMBA_ERR_DTYPE;
+  if (batch <= 0 || dim <= 0 || L <= 0 || width <= 0) return MAMBA_ERR_SHAPE;
+  if (width < 2 || width > 4) return MAMBA_ERR_UNSUPPORTED;
+  // dense (batch, L, dim) arrays in bytes; a 32-bit grid of channel tiles
+  if (batch > kGridLim / 4 || L > kLim / 16 / batch || dim > kLim / 16 / (batch * L) ||
+      dim > (int64_t)1 << 24)
+    return MAMBA_ERR_UNSUPPORTED;
+  if (!x || !w) return MAMBA_ERR_NULL_PTR;
+  if (!aligned(x, (size_t)esize(dt)) || !aligned_f32(w) || !aligned_f32(b))
+    return MAMBA_ERR_ALIGNMENT;
+  return MAMBA_OK;
+}
+
+int64_t conv_tiles(int64_t L, int64_t tile) { return (L + tile - 1) / tile; }
+
+// Whether (tiles of tokens) x (batch rows) x (channel tiles) is a legal grid.
+bool conv_grid_ok(int64_t batch, int64_t dim, int64_t tiles) {
+  const int64_t cb = (dim + 63) / 64;
+  return tiles <= kGridLim / batch && tiles * batch <= kGridLim / cb;
+}
+
+mamba_status check_norm(const void* x, int64_t x_row, const void* z, int64_t z_row,
+                        const float* weight, int64_t rows, int64_t dim, int64_t groups, float eps,
+                        mamba_dtype dt) {
+  if (dt != MAMBA_F32 && dt != MAMBA_BF16) return MAMBA_ERR_DTYPE;
+  if (rows <= 0 || dim <= 0 || groups <= 0 || dim % groups != 0) return MAMBA_ERR_SHAPE;
+  if (x_row < 0 || (z && z_row < 0)) return MAMBA_ERR_SHAPE;
+  if (!(eps >= 0.0f)) return MAMBA_ERR_INVALID;
+  if (dim > (1 << 28) || rows > kLim / 16 / dim || groups > kGridLim / rows ||
+      !mul_ok(rows, x_row) || !mul_ok(rows, z_row))
+    return MAMBA_ERR_UNSUPPORTED;
+  if (!x) return MAMBA_ERR_NULL_PTR;
+  const size_t es = (size_t)esize(dt);
+  if (!aligned(x, es) || !aligned(z, es) || !aligned_f32(weight)) return MAMBA_ERR_ALIGNMENT;
+  return MAMBA_OK;
+}
+
+mscan::NormParams norm_params(const void* x, int64_t x_row, const void* z, int64_t z_row,
+                              const float* weight, int64_t rows, int64_t dim, int64_t groups,
+                              float eps, int gate_first, mamba_dtype dt) {
+  mscan::NormParams p{};
+  p.x = x; p.z = z; p.w = weight; p.x_row = x_row; p.z_row = z_row;
+  p.rows = rows; p.dim = dim; p.gs = dim / groups; p.groups = (int)groups; p.eps = eps;
+  p.gate_first = gate_first != 0;
+  const int es = esize(dt);
+  // every group starts on 16 bytes in x, z, the weights and the dense outputs
+  p.vec = rows16(x, 0, x_row, p.gs, es) && (!z || rows16(z, 0, z_row, p.gs, es)) &&
+          aligned(weight, 16);
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mamba_heads_scan_fwd_workspace_size(const mamba_heads_shape* shape) {
+  return check_shape(shape) == MAMBA_OK ? 0 : SIZE_MAX;
+}
+
+mamba_status mamba_heads_scan_fwd(const mamba_heads_shape* shape, const void* u,
+                                  const void* delta, const float* A, const void* B,
+                                  const void* C, const float* D, const float* delta_bias,
+                                  const float* h0, const uint8_t* reset, void* out,
+                                  float* last_state, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  mamba_status st = check_shape(shape);
+  if (st != MAMBA_OK) return st;
+  st = check_inputs(shape, u, delta, A, B, C, D, delta_bias, h0);
+  if (st != MAMBA_OK) return st;
+  if (!out) return MAMBA_ERR_NULL_PTR;
+  if (!aligned(out, (size_t)esize(shape->dtype)) || !aligned_f32(last_state))
+    return MAMBA_ERR_ALIGNMENT;
+  (void)workspace;
+  (void)workspace_bytes;
+  mscan::HeadsFwdParams p{};
+  static_cast<mscan::HeadsParams&>(p) =
+      common(shape, u, delta, A, B, C, D, delta_bias, h0, reset);
+  p.out = out; p.last = last_state;
+  p.vec = p.vec && aligned(out, 16);
+  return hip_status(mscan::dispatch_heads_fwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,
+                                              as_stream(stream)));
+}
+
+size_t mamba_heads_scan_bwd_workspace_size(const mamba_heads_shape* shape) {
+  BwdLayout l;
+  return check_shape(shape) == MAMBA_OK && bwd_layout(shape, &l) ? l.total : SIZE_MAX;
+}
+
+mamba_status mamba_heads_scan_bwd(const mamba_heads_shape* shape, const void* u,
+                                  const void* delta, const float* A, const void* B,
+                                  const void* C, const float* D, const float* delta_bias,
+                                  const float* h0, const uint8_t* reset, const void* dout,
+                                  const float* dlast_state, void* du, void* ddelta, float* dA,
+                                  void* dB, void* dC, float* dD, float* ddelta_bias, float* dh0,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  mamba_status st = check_shape(shape);
+  if (st != MAMBA_OK) return st;
+  st = check_inputs(shape, u, delta, A, B, C, D, delta_bias, h0);
+  if (st != MAMBA_OK) return st;
+  if (!dout || !du || !ddelta || !dA || !dB || !dC) return MAMBA_ERR_NULL_PTR;
+  if ((dD && !D) || (ddelta_bias && !delta_bias) || (dh0 && !h0)) return MAMBA_ERR_INVALID;
+  const size_t es = (size_t)esize(shape->dtype);
+  if (!aligned(dout, es) || !aligned(du, es) || !aligned(ddelta, es) || !aligned(dB, es) ||
+      !aligned(dC, es) || !aligned_f32(dlast_state) || !aligned_f32(dA) || !aligned_f32(dD) ||
+      !aligned_f32(ddelta_bias) || !aligned_f32(dh0))
+    return MAMBA_ERR_ALIGNMENT;
+  BwdLayout l;
+  if (!bwd_layout(shape, &l)) return MAMBA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
+  mscan::HeadsBwdParams p{};
+  static_cast<mscan::HeadsParams&>(p) =
+      common(shape, u, delta, A, B, C, D, delta_bias, h0, reset);
+  p.dout = dout; p.dlast = dlast_state; p.du = du; p.ddelta = ddelta; p.dA = dA; p.dB = dB;
+  p.dC = dC; p.dD = dD; p.dbias = ddelta_bias; p.dh0 = dh0;
+  p.vec = p.vec && aligned(dout, 16) && aligned(du, 16) && aligned(dB, 16) && aligned(dC, 16);
+  char* ws = static_cast<char*>(workspace);
+  p.states = reinterpret_cast<float*>(ws + l.states);
+  p.dB_part = reinterpret_cast<float*>(ws + l.dB_part);
+  p.dC_part = reinterpret_cast<float*>(ws + l.dC_part);
+  p.head_part = reinterpret_cast<float*>(ws + l.head_part);
+  return hip_status(mscan::dispatch_heads_bwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,
+                                              as_stream(stream)));
+}
+
+mamba_status mamba_heads_state_update(const mamba_heads_shape* shape, float* state,
+                                      const int32_t* slots, int64_t pool, const void* u,
+                                      const void* delta, const float* A, const void* B,
+                                      const void* C, const float* D, const float* delta_bias,
+                                      void* out, void* stream) {
+  mamba_status st = check_shape(shape);
+  if (st != MAMBA_OK) return st;
+  if (shape->seqlen != 1 || pool <= 0 || (!slots && pool < shape->batch)) return MAMBA_ERR_SHAPE;
+  if (pool > kLim / (kMaxHeadDim * kMaxHeadState * 4) / shape->heads) return MAMBA_ERR_UNSUPPORTED;
+  st = check_inputs(shape, u, delta, A, B, C, D, delta_bias, nullptr);
+  if (st != MAMBA_OK) return st;
+  if (!state || !out) return MAMBA_ERR_NULL_PTR;
+  if (!aligned(out, (size_t)esize(shape->dtype)) || !aligned_f32(state) || !aligned(slots, 4))
+    return MAMBA_ERR_ALIGNMENT;
+  mscan::HeadsStepParams p{};
+  static_cast<mscan::HeadsParams&>(p) =
+      common(shape, u, delta, A, B, C, D, delta_bias, nullptr, nullptr);
+  p.state = state; p.slots = slots; p.pool = pool; p.out = out;
+  return hip_status(mscan::dispatch_heads_step(p, shape->dtype == MAMBA_F32 ? 0 : 1,
+                                               as_stream(stream)));
+}
+
+mamba_status mamba_conv1d_tokens_fwd(const void* x, int64_t x_batch_stride,
+                                     int64_t x_token_stride, const float* w, const float* b,
+                                     const void* window, const uint8_t* reset, int64_t width,
+                                     mamba_dtype dt, int64_t batch, int64_t dim, int64_t seqlen,
+                                     void* out, void* window_out, void* stream) {
+  mamba_status st = check_conv(x, w, b, width, dt, batch, dim, seqlen);
+  if (st != MAMBA_OK) return st;
+  if (x_batch_stride < 0 || x_token_stride < 0) return MAMBA_ERR_SHAPE;
+  const int64_t tiles = conv_tiles(seqlen, 1);
+  if (!span_ok(batch, x_batch_stride, seqlen, x_token_stride) || !conv_grid_ok(batch, dim, tiles / 4 + 1))
+    return MAMBA_ERR_UNSUPPORTED;
+  if (!out) return MAMBA_ERR_NULL_PTR;
+  const int es = esize(dt);
+  if (!aligned(out, (size_t)es) || !aligned(window, (size_t)es) || !aligned(window_out, (size_t)es))
+    return MAMBA_ERR_ALIGNMENT;
+  if (window && window == window_out) return MAMBA_ERR_INVALID;
+  mscan::TokConvParams p{};
+  p.x = {x, x_batch_stride, x_token_stride};
+  p.w = w; p.b = b; p.window = window; p.reset = reset;
+  p.batch = batch; p.dim = dim; p.L = seqlen; p.W = (int)width;
+  p.out = out; p.window_out = window_out;
+  p.vec = rows16(x, x_batch_stride, x_token_stride, dim, es) && aligned(out, 16) &&
+          aligned(window, 16) && aligned(window_out, 16) && aligned(w, 16) && aligned(b, 16);
+  return hip_status(mscan::dispatch_tokconv_fwd(p, dt == MAMBA_F32 ? 0 : 1, as_stream(stream)));
+}
+
+size_t mamba_conv1d_tokens_bwd_workspace_size(int64_t batch, int64_t dim, int64_t seqlen,
+                                              int64_t width) {
+  static const float dummy[4] = {};
+  if (check_conv(dummy, dummy, nullptr, width, MAMBA_F32, batch, dim, seqlen) != MAMBA_OK)
+    return SIZE_MAX;
+  const int64_t tiles = conv_tiles(seqlen, mscan::kTokConvTile);
+  if (!conv_grid_ok(batch, dim, tiles)) return SIZE_MAX;
+  return up256((size_t)(batch * tiles) * (size_t)(width + 1) * (size_t)dim * 4);
+}
+
+mamba_status mamba_conv1d_tokens_bwd(const void* x, int64_t x_batch_stride,
+                                     int64_t x_token_stride, const float* w, const float* b,
+                                     const void* window, const uint8_t* reset, const void* dout,
+                                     int64_t width, mamba_dtype dt, int64_t batch, int64_t dim,
+                                     int64_t seqlen, void* dx, float* dw, float* db,
+                                     void* dwindow, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  mamba_status st = check_conv(x, w, b, width, dt, batch, dim, seqlen);
+  if (st != MAMBA_OK) return st;
+  if (x_batch_stride < 0 || x_token_stride < 0) return MAMBA_ERR_SHAPE;
+  if (!span_ok(batch, x_batch_stride, seqlen, x_token_stride)) return MAMBA_ERR_UNSUPPORTED;
+  if (!dout || !dx || !dw) return MAMBA_ERR_NULL_PTR;
+  if ((db && !b) || (dwindow && !window)) return MAMBA_ERR_INVALID;
+  const int es = esize(dt);
+  if (!aligned(dout, (size_t)es) || !aligned(dx, (size_t)es) || !aligned(window, (size_t)es) ||
+      !aligned(dwindow, (size_t)es) || !aligned_f32(dw) || !aligned_f32(db))
+    return MAMBA_ERR_ALIGNMENT;
+  const size_t need = mamba_conv1d_tokens_bwd_workspace_size(batch, dim, seqlen, width);
+  if (need == SIZE_MAX) return MAMBA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
+  mscan::TokConvParams p{};
+  p.x = {x, x_batch_stride, x_token_stride};
+  p.w = w; p.b = b; p.window = window; p.reset = reset;
+  p.batch = batch; p.dim = dim; p.L = seqlen; p.W = (int)width;
+  p.tiles = conv_tiles(seqlen, mscan::kTokConvTile);
+  p.dout = dout; p.dx = dx; p.dw = dw; p.db = db; p.dwindow = dwindow;
+  p.part = static_cast<float*>(workspace);
+  p.vec = rows16(x, x_batch_stride, x_token_stride, dim, es) && aligned(dout, 16) &&
+          aligned(dx, 16) && aligned(window, 16) && aligned(dwindow, 16) && aligned(w, 16) &&
+          aligned(b, 16);
+  return hip_status(mscan::dispatch_tokconv_bwd(p, dt == MAMBA_F32 ? 0 : 1, as_stream(stream)));
+}
+
+mamba_status mamba_conv1d_tokens_update(const void* x, int64_t x_batch_stride, void* window,
+                                        const int32_t* slots, int64_t pool, const float* w,
+                                        const float* b, int64_t width, mamba_dtype dt,
+                                        int64_t batch, int64_t dim, void* out, void* stream) {
+  mamba_status st = check_conv(x, w, b, width, dt, batch, dim, 1);
+  if (st != MAMBA_OK) return st;
+  if (x_batch_stride < 0 || pool <= 0 || (!slots && pool < batch)) return MAMBA_ERR_SHAPE;
+  if (!mul_ok(batch, x_batch_stride) || pool > kLim / 64 / dim || !conv_grid_ok(batch, dim, 1))
+    return MAMBA_ERR_UNSUPPORTED;
+  if (!window || !out) return MAMBA_ERR_NULL_PTR;
+  const int es = esize(dt);
+  if (!aligned(out, (size_t)es) || !aligned(window, (size_t)es) || !aligned(slots, 4))
+    return MAMBA_ERR_ALIGNMENT;
+  mscan::TokConvStepParams p{};
+  p.x = x; p.x_batch = x_batch_stride; p.window = window; p.slots = slots; p.pool = pool;
+  p.batch = batch; p.dim = dim; p.w = w; p.b = b; p.out = out; p.W = (int)width;
+  p.vec = rows16(x, x_batch_stride, 0, dim, es) && aligned(window, 16) && aligned(out, 16) &&
+          aligned(w, 16) && aligned(b, 16);
+  return hip_status(mscan::dispatch_tokconv_step(p, dt == MAMBA_F32 ? 0 : 1, as_stream(stream)));
+}
+
+mamba_status mamba_gated_norm_fwd(const void* x, int64_t x_row_stride, const void* z,
+                                  int64_t z_row_stride, const float* weight, int64_t rows,
+                                  int64_t dim, int64_t groups, float eps, int gate_first,
+                                  mamba_dtype dt, void* out, void* stream) {
+  mamba_status st = check_norm(x, x_row_stride, z, z_row_stride, weight, rows, dim, groups, eps, dt);
+  if (st != MAMBA_OK) return st;
+  if (!out) return MAMBA_ERR_NULL_PTR;
+  if (!aligned(out, (size_t)esize(dt))) return MAMBA_ERR_ALIGNMENT;
+  mscan::NormParams p = norm_params(x, x_row_stride, z, z_row_stride, weight, rows, dim, groups,
+                                    eps, gate_first, dt);
+  p.out = out;
+  p.vec = p.vec && aligned(out, 16);
+  return hip_status(mscan::dispatch_norm_fwd(p, dt == MAMBA_F32 ? 0 : 1, as_stream(stream)));
+}
+
+size_t mamba_gated_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t groups) {
+  static const float dummy[4] = {};
+  if (check_norm(dummy, dim, nullptr, 0, nullptr, rows, dim, groups, 0.0f, MAMBA_F32) != MAMBA_OK)
+    return SIZE_MAX;
+  return up256((size_t)mscan::norm_parts(rows, groups) * (size_t)dim * 4);
+}
+
+mamba_status mamba_gated_norm_bwd(const void* x, int64_t x_row_stride, const void* z,
+                                  int64_t z_row_stride, const float* weight, const void* dout,
+                                  int64_t rows, int64_t dim, int64_t groups, float eps,
+                                  int gate_first, mamba_dtype dt, void* dx, void* dz,
+                                  float* dweight, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  mamba_status st = check_norm(x, x_row_stride, z, z_row_stride, weight, rows, dim, groups, eps, dt);
+  if (st != MAMBA_OK) return st;
+  if (!dout || !dx) return MAMBA_ERR_NULL_PTR;
+  if ((z != nullptr) != (dz != nullptr) || (weight != nullptr) != (dweight != nullptr))
+    return MAMBA_ERR_INVALID;
+  const size_t es = (size_t)esize(dt);
+  if (!aligned(dout, es) || !aligned(dx, es) || !aligned(dz, es) || !aligned_f32(dweight))
+    return MAMBA_ERR_ALIGNMENT;
+  const size_t need = mamba_gated_norm_bwd_workspace_size(rows, dim, groups);
+  if (need == SIZE_MAX) return MAMBA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
+  mscan::NormParams p = norm_params(x, x_row_stride, z, z_row_stride, weight, rows, dim, groups,
+                                    eps, gate_first, dt);
+  p.dout = dout; p.dx = dx; p.dz = dz; p.dw = dweight;
+  p.part = static_cast<float*>(workspace);
+  p.parts = mscan::norm_parts(rows, groups);
+  p.vec = p.vec && aligned(dout, 16) && aligned(dx, 16) && aligned(dz, 16);
+  return hip_status(mscan::dispatch_norm_bwd(p, dt == MAMBA_F32 ? 0 : 1, as_stream(stream)));
+}
+
+}  // extern "C"
