@@ -25,6 +25,12 @@ struct HeadsParams {
   int H, P, G, N;
   int softplus, zoh;
   int vec;               // rows of u, B, C (and dout, out) start 16-byte aligned
+  int PB;                // blocks of 64 channels a head
+  // the sequence in nseg segments of seg_len steps (whole chunks)
+  int nseg;
+  int64_t seg_len;
+  float* seg_state;      // workspace, (batch, H, PB, nseg - 1) states
+  float* seg_dec;        // and their segments' decays
 };
 
 struct HeadsFwdParams : HeadsParams {

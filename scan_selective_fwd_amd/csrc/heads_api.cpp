@@ -92,7 +92,55 @@ mamba_status check_inputs(const mamba_heads_shape* s, const void* u, const void*
   return MAMBA_OK;
 }
 
+constexpr int64_t kHeadCols = 64;   // channels a block takes
+
+int64_t chunk_len(const mamba_heads_shape* s) { return s->dtype == MAMBA_BF16 ? 64 : 32; }
+int64_t col_blocks(const mamba_heads_shape* s) { return (s->headdim + kHeadCols - 1) / kHeadCols; }
+// States as the kernels hold them: 64 columns by the next kernel size of dstate.
+int64_t pad_state(const mamba_heads_shape* s) {
+  return s->dstate <= 32 ? 32 : s->dstate <= 64 ? 64 : s->dstate <= 128 ? 128 : 256;
+}
+
+// Segments: as many as bring the blocks to about kTargetBlocks, each of at
+// least kMinChunks chunks.
+constexpr int64_t kTargetBlocks = 512;
+constexpr int64_t kMinChunks = 4;
+
+void split(const mamba_heads_shape* s, int* nseg, int64_t* seg_len) {
+  const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
+  const int64_t blocks = s->batch * s->heads * col_blocks(s);
+  int64_t n = s->segments;
+  if (n == 0) {
+    n = (kTargetBlocks + blocks / 2) / blocks;
+    if (n > chunks / kMinChunks) n = chunks / kMinChunks;
+  }
+  if (n > chunks) n = chunks;
+  if (n > 4096) n = 4096;
+  if (n < 1) n = 1;
+  const int64_t per = (chunks + n - 1) / n;
+  *seg_len = per * q;
+  *nseg = (int)((chunks + per - 1) / per);
+}
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspace of the forward: the segments' states and decays.
+struct FwdLayout {
+  int nseg;
+  int64_t seg_len;
+  size_t state, dec, total;
+};
+
+bool fwd_layout(const mamba_heads_shape* s, FwdLayout* l) {
+  split(s, &l->nseg, &l->seg_len);
+  const int64_t cols = s->batch * s->heads * col_blocks(s);
+  if (cols > kGridLim / l->nseg || cols > kGridLim / 16) return false;
+  const size_t n = (size_t)cols * (size_t)(l->nseg - 1);
+  l->state = 0;
+  l->dec = up256(n * (size_t)(kHeadCols * pad_state(s)) * 4);
+  l->total = l->dec + up256(n * 4);
+  return true;
+}
 
 // Workspace of the backward: see HeadsBwdParams.
 struct BwdLayout {
@@ -169,7 +217,8 @@ mscan::NormParams norm_params(const void* x, int64_t x_row, const void* z, int64
 extern "C" {
 
 size_t mamba_heads_scan_fwd_workspace_size(const mamba_heads_shape* shape) {
-  return check_shape(shape) == MAMBA_OK ? 0 : SIZE_MAX;
+  FwdLayout l;
+  return check_shape(shape) == MAMBA_OK && fwd_layout(shape, &l) ? l.total : SIZE_MAX;
 }
 
 mamba_status mamba_heads_scan_fwd(const mamba_heads_shape* shape, const void* u,
@@ -185,11 +234,19 @@ mamba_status mamba_heads_scan_fwd(const mamba_heads_shape* shape, const void* u,
   if (!out) return MAMBA_ERR_NULL_PTR;
   if (!aligned(out, (size_t)esize(shape->dtype)) || !aligned_f32(last_state))
     return MAMBA_ERR_ALIGNMENT;
-  (void)workspace;
-  (void)workspace_bytes;
+  FwdLayout l;
+  if (!fwd_layout(shape, &l)) return MAMBA_ERR_UNSUPPORTED;
+  if (l.total != 0) {
+    if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
+  }
   mscan::HeadsFwdParams p{};
   static_cast<mscan::HeadsParams&>(p) =
       common(shape, u, delta, A, B, C, D, delta_bias, h0, reset);
+  p.PB = (int)col_blocks(shape);
+  p.nseg = l.nseg; p.seg_len = l.seg_len;
+  p.seg_state = static_cast<float*>(workspace);
+  p.seg_dec = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.dec);
   p.out = out; p.last = last_state;
   p.vec = p.vec && aligned(out, 16);
   return hip_status(mscan::dispatch_heads_fwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,

@@ -1,6 +1,6 @@
-// The multi-head scan, one token after the other: per (batch row, head)
+// The backward of the multi-head scan, one token after the other: per (batch row, head)
 //   h_t = a_t h_{t-1} + w_t u_t B_t^T,   out_t = h_t C_t + D u_t,   h (P, N)
-// and its backward: with the adjoint g_t = dout_t C_t^T + a_{t+1} g_{t+1},
+// with the adjoint g_t = dout_t C_t^T + a_{t+1} g_{t+1},
 //   du = w g B + D dout,  dB = w g^T u,  dC = h^T dout,  dw = u . (g B),
 //   dlog_t = <a_t g_t, h_{t-1}>, the gradient of the log decay.
 // The backward keeps every state of its forward sweep in the workspace.
@@ -16,61 +16,6 @@ namespace {
 template <typename T>
 __device__ __forceinline__ float elem(const Rows& r, int64_t b, int64_t t, int64_t i) {
   return Elem<T>::load1(static_cast<const T*>(r.p) + b * r.batch + t * r.token + i);
-}
-
-template <typename T, int J>
-__global__ __launch_bounds__(256) void heads_fwd_kernel(const HeadsFwdParams p) {
-  const int64_t b = blockIdx.x / p.H;
-  const int hd = (int)(blockIdx.x - b * p.H), g = hd / (p.H / p.G);
-  const int pi = threadIdx.x >> 2, nq = threadIdx.x & 3;
-  const uint8_t* rst = reset_row(p.reset, b, p.L);
-  const float A = p.A[hd], bias = p.bias ? p.bias[hd] : 0.0f, D = p.D ? p.D[hd] : 0.0f;
-  const int64_t s0 = (b * p.H + hd) * (int64_t)p.P * p.N;
-  float h[2][J];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int pp = pi + 64 * i, n = nq + 4 * j;
-      h[i][j] = p.h0 && pp < p.P && n < p.N ? p.h0[s0 + (int64_t)pp * p.N + n] : 0.0f;
-    }
-  for (int64_t t = 0; t < p.L; ++t) {
-    const Step q = make_step(elem<T>(p.delta, b, t, hd) + bias, A, p.softplus, p.zoh);
-    const float a = exp2f(q.lg);
-    const bool cut = rst && rst[t] != 0;
-    float u[2], y[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      u[i] = pi + 64 * i < p.P ? elem<T>(p.u, b, t, (int64_t)hd * p.P + pi + 64 * i) : 0.0f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int n = nq + 4 * j;
-      const float Bn = n < p.N ? elem<T>(p.B, b, t, (int64_t)g * p.N + n) : 0.0f;
-      const float Cn = n < p.N ? elem<T>(p.C, b, t, (int64_t)g * p.N + n) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        h[i][j] = __builtin_fmaf(u[i] * q.w, Bn, cut ? 0.0f : a * h[i][j]);
-        y[i] = __builtin_fmaf(h[i][j], Cn, y[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      y[i] += __shfl_xor(y[i], 1);
-      y[i] += __shfl_xor(y[i], 2);
-      const int pp = pi + 64 * i;
-      if (nq == 0 && pp < p.P)
-        Elem<T>::store1(static_cast<T*>(p.out) + ((b * p.L + t) * p.H + hd) * p.P + pp,
-                        __builtin_fmaf(D, u[i], y[i]));
-    }
-  }
-  if (p.last)
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int pp = pi + 64 * i, n = nq + 4 * j;
-        if (pp < p.P && n < p.N) p.last[s0 + (int64_t)pp * p.N + n] = h[i][j];
-      }
 }
 
 // Sums over the block's 64 rows of v[j] (state n = nq + 4 j): result in sh[n].
@@ -262,20 +207,6 @@ __global__ __launch_bounds__(256) void heads_bwd_head_kernel(const HeadsBwdParam
 }
 
 template <typename T, int J>
-hipError_t fwd_go(const HeadsFwdParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((heads_fwd_kernel<T, J>), dim3((unsigned)(p.batch * p.H)), dim3(256), 0, s, p);
-  return hipGetLastError();
-}
-
-template <typename T>
-hipError_t fwd_t(const HeadsFwdParams& p, hipStream_t s) {
-  if (p.N <= 16) return fwd_go<T, 4>(p, s);
-  if (p.N <= 64) return fwd_go<T, 16>(p, s);
-  if (p.N <= 128) return fwd_go<T, 32>(p, s);
-  return fwd_go<T, 64>(p, s);
-}
-
-template <typename T, int J>
 hipError_t bwd_go(const HeadsBwdParams& p, hipStream_t s) {
   hipLaunchKernelGGL((heads_bwd_kernel<T, J>), dim3((unsigned)(p.batch * p.H)), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
@@ -297,10 +228,6 @@ hipError_t bwd_t(const HeadsBwdParams& p, hipStream_t s) {
 }
 
 }  // namespace
-
-hipError_t dispatch_heads_fwd(const HeadsFwdParams& p, int dtype, hipStream_t s) {
-  return dtype == 0 ? fwd_t<float>(p, s) : fwd_t<bf16_t>(p, s);
-}
 
 hipError_t dispatch_heads_bwd(const HeadsBwdParams& p, int dtype, hipStream_t s) {
   return dtype == 0 ? bwd_t<float>(p, s) : bwd_t<bf16_t>(p, s);
