@@ -25,11 +25,13 @@ struct HeadsParams {
   int H, P, G, N;
   int softplus, zoh;
   int vec;               // rows of u, B, C (and dout, out) start 16-byte aligned
-  int PB;                // blocks of 64 channels a head
+  // a block's four waves take slices of 32 channels: of one head, or of hpw
+  int slices, hpw, hblocks;   // slices a head, heads a block, blocks a group
   // the sequence in nseg segments of seg_len steps (whole chunks)
   int nseg;
   int64_t seg_len;
-  float* seg_state;      // workspace, (batch, H, PB, nseg - 1) states
+  void* scal;            // workspace, (batch, chunks, H) chunk scalars
+  float* seg_state;      // workspace, (batch, H, slices, nseg - 1) states
   float* seg_dec;        // and their segments' decays
 };
 
@@ -63,6 +65,7 @@ struct HeadsStepParams : HeadsParams {
   void* out;
 };
 
+hipError_t dispatch_heads_scal(const HeadsParams& p, int dtype, hipStream_t s);
 hipError_t dispatch_heads_fwd(const HeadsFwdParams& p, int dtype, hipStream_t s);
 hipError_t dispatch_heads_bwd(const HeadsBwdParams& p, int dtype, hipStream_t s);
 hipError_t dispatch_heads_step(const HeadsStepParams& p, int dtype, hipStream_t s);

@@ -33,9 +33,11 @@ bool span_ok(int64_t batch, int64_t sb, int64_t tokens, int64_t st) {
 }
 
 // Whether rows at p with these strides can be read in 16-byte pieces.
+// (a chunk of 64 rows and one more within 2^31 bytes: the kernels' offsets inside one).
 bool rows16(const void* p, int64_t sb, int64_t st, int64_t run, int es) {
   const int64_t v = 16 / es;
-  return aligned(p, 16) && sb % v == 0 && st % v == 0 && run % v == 0;
+  return aligned(p, 16) && sb % v == 0 && st % v == 0 && run % v == 0 && st <= (1 << 21) &&
+         run <= (1 << 21);
 }
 
 mamba_status check_shape(const mamba_heads_shape* s) {
@@ -48,7 +50,7 @@ mamba_status check_shape(const mamba_heads_shape* s) {
   if (s->heads % s->groups != 0) return MAMBA_ERR_SHAPE;
   if (s->segments < 0) return MAMBA_ERR_INVALID;
   if (s->headdim > kMaxHeadDim || s->dstate > kMaxHeadState) return MAMBA_ERR_UNSUPPORTED;
-  if (s->heads > (1 << 20) || s->batch > kGridLim / s->heads) return MAMBA_ERR_UNSUPPORTED;
+  if (s->heads > (1 << 16) || s->batch > kGridLim / s->heads) return MAMBA_ERR_UNSUPPORTED;
   // dense (batch, seqlen, heads, headdim or dstate) arrays, in bytes
   if (s->seqlen > kLim / 1024 / (s->batch * s->heads)) return MAMBA_ERR_UNSUPPORTED;
   const int64_t strides[] = {s->u_batch_stride, s->u_token_stride, s->delta_batch_stride,
@@ -92,11 +94,25 @@ mamba_status check_inputs(const mamba_heads_shape* s, const void* u, const void*
   return MAMBA_OK;
 }
 
-constexpr int64_t kHeadCols = 64;   // channels a block takes
+constexpr int64_t kSlice = 32;   // channels a wave takes
 
 int64_t chunk_len(const mamba_heads_shape* s) { return s->dtype == MAMBA_BF16 ? 64 : 32; }
-int64_t col_blocks(const mamba_heads_shape* s) { return (s->headdim + kHeadCols - 1) / kHeadCols; }
-// States as the kernels hold them: 64 columns by the next kernel size of dstate.
+
+// How heads map to the four waves of a block.
+struct Map {
+  int64_t slices, hpw, hblocks;
+};
+
+Map map_of(const mamba_heads_shape* s) {
+  Map m;
+  m.slices = (s->headdim + kSlice - 1) / kSlice;
+  m.hpw = m.slices == 1 ? 4 : m.slices == 2 ? 2 : 1;
+  const int64_t per = s->heads / s->groups;
+  m.hblocks = (per + m.hpw - 1) / m.hpw;
+  return m;
+}
+
+// dstate as the kernels hold it.
 int64_t pad_state(const mamba_heads_shape* s) {
   return s->dstate <= 32 ? 32 : s->dstate <= 64 ? 64 : s->dstate <= 128 ? 128 : 256;
 }
@@ -108,7 +124,7 @@ constexpr int64_t kMinChunks = 4;
 
 void split(const mamba_heads_shape* s, int* nseg, int64_t* seg_len) {
   const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
-  const int64_t blocks = s->batch * s->heads * col_blocks(s);
+  const int64_t blocks = s->batch * s->groups * map_of(s).hblocks;
   int64_t n = s->segments;
   if (n == 0) {
     n = (kTargetBlocks + blocks / 2) / blocks;
@@ -128,16 +144,19 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 struct FwdLayout {
   int nseg;
   int64_t seg_len;
-  size_t state, dec, total;
+  size_t scal, state, dec, total;
 };
 
 bool fwd_layout(const mamba_heads_shape* s, FwdLayout* l) {
   split(s, &l->nseg, &l->seg_len);
-  const int64_t cols = s->batch * s->heads * col_blocks(s);
+  const int64_t cols = s->batch * s->heads * map_of(s).slices;
   if (cols > kGridLim / l->nseg || cols > kGridLim / 16) return false;
   const size_t n = (size_t)cols * (size_t)(l->nseg - 1);
-  l->state = 0;
-  l->dec = up256(n * (size_t)(kHeadCols * pad_state(s)) * 4);
+  const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
+  if (chunks > kGridLim / (s->batch * s->heads)) return false;
+  l->scal = 0;
+  l->state = up256((size_t)(s->batch * s->heads * chunks) * (size_t)(24 * q + 16));
+  l->dec = l->state + up256(n * (size_t)(kSlice * pad_state(s)) * 4);
   l->total = l->dec + up256(n * 4);
   return true;
 }
@@ -236,16 +255,16 @@ mamba_status mamba_heads_scan_fwd(const mamba_heads_shape* shape, const void* u,
     return MAMBA_ERR_ALIGNMENT;
   FwdLayout l;
   if (!fwd_layout(shape, &l)) return MAMBA_ERR_UNSUPPORTED;
-  if (l.total != 0) {
-    if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
-    if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
-  }
+  if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
   mscan::HeadsFwdParams p{};
   static_cast<mscan::HeadsParams&>(p) =
       common(shape, u, delta, A, B, C, D, delta_bias, h0, reset);
-  p.PB = (int)col_blocks(shape);
+  const Map m = map_of(shape);
+  p.slices = (int)m.slices; p.hpw = (int)m.hpw; p.hblocks = (int)m.hblocks;
   p.nseg = l.nseg; p.seg_len = l.seg_len;
-  p.seg_state = static_cast<float*>(workspace);
+  p.scal = workspace;
+  p.seg_state = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.state);
   p.seg_dec = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.dec);
   p.out = out; p.last = last_state;
   p.vec = p.vec && aligned(out, 16);

@@ -29,7 +29,11 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kCols = 64;      // channels of a head a block takes: 16 a wave
+// Channels: a wave takes a slice of 32 of one head (two tiles of 16), a block
+// four slices.  With two tiles a fragment of B or C read from LDS feeds two
+// matrix instructions; with one, the LDS reads took longer than the products.
+constexpr int kSlice = 32;
+constexpr int kCols = 4 * kSlice;
 
 // Per type: tokens a chunk, parts of an input operand, row padding of a tile.
 // Padding by 16 bytes spreads the rows of a fragment's read over the banks.
@@ -93,9 +97,11 @@ __device__ __forceinline__ Frag<NP> acc_frag(const f32x4& lo, const f32x4& hi) {
   return to_frag<NP>(x);
 }
 
-// acc += A B^T over 32 inner elements, part products down to 2^-24.
-template <int NA, int NB>
-__device__ __forceinline__ void mma(f32x4& acc, const Frag<NA>& a, const Frag<NB>& b) {
+// acc[r][c] += A[r] B[c]^T over 32 inner elements, part products down to 2^-24.
+// The accumulators alternate, so that no instruction waits for the one before.
+template <int NA, int NB, int R, int C>
+__device__ __forceinline__ void mma(f32x4 (&acc)[R][C], const Frag<NA> (&a)[R],
+                                    const Frag<NB> (&b)[C]) {
   constexpr int NM = NA > NB ? NA : NB;
 #pragma unroll
   for (int s = NM - 1; s >= 0; --s)
@@ -103,9 +109,18 @@ __device__ __forceinline__ void mma(f32x4& acc, const Frag<NA>& a, const Frag<NB
     for (int i = 0; i < NA; ++i) {
       const int j = s - i;
       if (j >= 0 && j < NB)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[j], acc, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            acc[r][c] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[r].v[i], b[c].v[j], acc[r][c], 0, 0, 0);
     }
 }
+
+// Keeps the scheduler from moving one phase's loads into another, where they
+// would only hold registers.
+__device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
 
 __device__ __forceinline__ int lane_i() { return threadIdx.x & 15; }
 __device__ __forceinline__ int lane_g() { return (threadIdx.x >> 4) & 3; }
@@ -162,97 +177,146 @@ __device__ __forceinline__ Frag<Mx<T>::PARTS> load_cols(const T* tile, int strid
   }
 }
 
-// The same fragment with its inner elements weighted by c, as three parts; an
-// inner element of weight 0 counts as zero whatever it holds.
+// The values of such a fragment, and the fragment weighted by c along its
+// inner elements, as three parts.
 template <typename T>
-__device__ __forceinline__ Frag<3> load_cols_weighted(const T* tile, int stride, int o0, int k0,
-                                                      const float* c) {
-  float x[8];
-  if constexpr (sizeof(T) == 2) {
-    const u32x4 r = __builtin_bit_cast(u32x4, load_cols_raw(tile, stride, o0, k0));
+struct Cols {
+  bf16x8 raw;    // bfloat16
+  float x[8];    // float32
+  __device__ __forceinline__ void load(const T* tile, int stride, int o0, int k0) {
+    if constexpr (sizeof(T) == 2) raw = load_cols_raw(tile, stride, o0, k0);
+    else load_cols_f32(tile, stride, o0, k0, x);
+  }
+  __device__ __forceinline__ Frag<Mx<T>::PARTS> frag() const {
+    if constexpr (sizeof(T) == 2) {
+      Frag<1> f;
+      f.v[0] = raw;
+      return f;
+    } else {
+      return to_frag<3>(x);
+    }
+  }
+  __device__ __forceinline__ Frag<3> weighted(const float* c, int k0) const {
+    const f32x4 c0 = *reinterpret_cast<const f32x4*>(c + k0 + 4 * lane_g());
+    const f32x4 c1 = *reinterpret_cast<const f32x4*>(c + k0 + 16 + 4 * lane_g());
+    float y[8];
+    if constexpr (sizeof(T) == 2) {
+      const u32x4 r = __builtin_bit_cast(u32x4, raw);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[2 * j] = bf16_lo(r[j]);
+        y[2 * j + 1] = bf16_hi(r[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = x[j];
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      x[2 * j] = bf16_lo(r[j]);
-      x[2 * j + 1] = bf16_hi(r[j]);
+      y[j] *= c0[j];
+      y[4 + j] *= c1[j];
     }
-  } else {
-    load_cols_f32(tile, stride, o0, k0, x);
+    return to_frag<3>(y);
   }
-  const f32x4 c0 = *reinterpret_cast<const f32x4*>(c + k0 + 4 * lane_g());
-  const f32x4 c1 = *reinterpret_cast<const f32x4*>(c + k0 + 16 + 4 * lane_g());
+  // Part of an operand that is NaN or infinite wherever a value is.
+  __device__ __forceinline__ bf16x8 top() const {
+    if constexpr (sizeof(T) == 2) {
+      return raw;
+    } else {
+      u32x4 r;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[j] = c0[j] == 0.0f ? 0.0f : x[j] * c0[j];
-    x[4 + j] = c1[j] == 0.0f ? 0.0f : x[4 + j] * c1[j];
+      for (int j = 0; j < 4; ++j) r[j] = pack_hi(x[2 * j], x[2 * j + 1]);
+      return as_frag(r);
+    }
   }
-  return to_frag<3>(x);
-}
+};
+
+// ---------------------------------------------------------------------------
+// A range of global memory read with the hardware's range check: 16 bytes at an
+// offset, zeros from `bytes` on.  The base and the range are uniform.
+// ---------------------------------------------------------------------------
+struct Buffer {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Buffer(const void* base, uint32_t bytes)
+      : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00027000)) {}
+  __device__ __forceinline__ u32x4 load(uint32_t off) const {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+  }
+};
+constexpr uint32_t kOutside = 0x80000000u;   // beyond every range: they stay below 2^31
 
 // ---------------------------------------------------------------------------
 // Staging: ROWS tokens by COLS elements from global rows to an LDS tile, in
 // 16-byte pieces held in registers between the two.
 // ---------------------------------------------------------------------------
-template <typename T, int ROWS, int COLS>
+// The tile's columns are `sub` wide parts (heads); part j's elements are the
+// row's [at + j * run, at + j * run + n), n <= run, n <= sub.
+template <typename T, int ROWS, int COLS, bool VEC>
 struct Stage {
   static constexpr int V = 16 / sizeof(T);
   static constexpr int PER_ROW = COLS / V;
   static constexpr int COUNT = (ROWS * PER_ROW + 255) / 256;
-  static_assert(COLS % V == 0, "COLS");
+  static_assert(COLS % V == 0 && ROWS * PER_ROW % 256 == 0, "whole pieces a thread");
+  static constexpr int STEP = 256 / PER_ROW;   // rows between a thread's pieces
+  static_assert(256 % PER_ROW == 0, "a thread keeps its column");
   u32x4 v[COUNT];
+  uint32_t off;    // bytes from the chunk's first row to the thread's first piece
+  int n_;          // elements of the thread's piece inside the row
+  int part, cc;    // the piece's place
 
-  // Rows t0 .. t0 + len - 1 of batch row b, elements [at, at + n) of each; the
-  // rest of the tile is zero.  VEC: rows start on 16 bytes and n is whole
-  // pieces.
-  template <bool VEC>
+  __device__ __forceinline__ void init(const Rows& r, int64_t at, int sub, int run, int n,
+                                       int parts) {
+    const int c = (threadIdx.x % PER_ROW) * V;
+    part = c / sub;
+    cc = c - part * sub;
+    n_ = part < parts && cc < n ? n - cc : 0;
+    // a piece outside the row is out of the buffer's range
+    off = n_ > 0 ? (uint32_t)((at + (int64_t)part * run + cc +
+                               (int64_t)(threadIdx.x / PER_ROW) * r.token) * (int)sizeof(T))
+                 : kOutside;
+  }
+  // Rows t0 .. t0 + len - 1 of batch row b.  VEC: rows start on 16 bytes, n is
+  // whole pieces, and a chunk spans less than 2^31 bytes (the caller's check);
+  // the loads carry the chunk's range, and outside it they give zeros.
   __device__ __forceinline__ void load(const Rows& r, int64_t b, int64_t t0, int len, int64_t at,
-                                       int n) {
-    const T* base = static_cast<const T*>(r.p) + b * r.batch + t0 * r.token + at;
+                                       int run, int width) {
+    const char* base = static_cast<const char*>(r.p) + (b * r.batch + t0 * r.token) * (int)sizeof(T);
+    if constexpr (VEC) {
+      const uint32_t stride = (uint32_t)(r.token * (int)sizeof(T));
+      // width: elements from the row's start that belong to the tile's rows
+      const Buffer buf(base, (uint32_t)(len - 1) * stride + (uint32_t)(width * (int)sizeof(T)));
+      const uint32_t o = (uint32_t)opaque_int((int)off);
 #pragma unroll
-    for (int k = 0; k < COUNT; ++k) {
-      const int idx = k * 256 + threadIdx.x;
-      const int row = idx / PER_ROW, c = (idx % PER_ROW) * V;
-      v[k] = u32x4{0, 0, 0, 0};
-      if (row < len && c < n) {
-        const T* q = base + row * r.token + c;
-        if constexpr (VEC) {
-          v[k] = *reinterpret_cast<const u32x4*>(q);
-        } else {
+      for (int k = 0; k < COUNT; ++k) v[k] = buf.load(o + (uint32_t)(k * STEP) * stride);
+    } else {
+      const int row0 = threadIdx.x / PER_ROW;
+      const T* q0 = reinterpret_cast<const T*>(base) + at + (int64_t)part * run + cc;
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            if (c + e < n) {
-              if constexpr (sizeof(T) == 2) v[k][e / 2] |= (uint32_t)q[e] << (16 * (e & 1));
-              else v[k][e] = __builtin_bit_cast(uint32_t, q[e]);
-            }
+      for (int k = 0; k < COUNT; ++k) {
+        const int row = row0 + k * STEP;
+        const T* q = q0 + row * r.token;
+        v[k] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if (e < n_ && row < len) {
+            if constexpr (sizeof(T) == 2) v[k][e / 2] |= (uint32_t)q[e] << (16 * (e & 1));
+            else v[k][e] = __builtin_bit_cast(uint32_t, q[e]);
           }
         }
       }
     }
   }
   __device__ __forceinline__ void store(T* tile, int stride) const {
+    T* q = tile + (threadIdx.x / PER_ROW) * stride + (threadIdx.x % PER_ROW) * V;
 #pragma unroll
-    for (int k = 0; k < COUNT; ++k) {
-      const int idx = k * 256 + threadIdx.x;
-      const int row = idx / PER_ROW, c = (idx % PER_ROW) * V;
-      if (ROWS * PER_ROW % 256 == 0 || row < ROWS)
-        *reinterpret_cast<u32x4*>(tile + row * stride + c) = v[k];
-    }
-  }
-  // Nonzero when an infinity or a NaN is among the values.
-  __device__ __forceinline__ uint32_t non_finite() const {
-    constexpr uint32_t e = sizeof(T) == 2 ? 0x7F807F80u : 0x7F800000u;
-    constexpr uint32_t one = sizeof(T) == 2 ? 0x00800080u : 0x00800000u;
-    constexpr uint32_t top = sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
-    uint32_t bad = 0;
-#pragma unroll
-    for (int k = 0; k < COUNT; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) bad |= (v[k][j] & e) + one;
-    return bad & top;
+    for (int k = 0; k < COUNT; ++k) *reinterpret_cast<u32x4*>(q + k * STEP * stride) = v[k];
   }
 };
 
 // ---------------------------------------------------------------------------
-// The scalars of a chunk, one token a lane of one wave.
+// The scalars of a head's chunk.  They are prepared once for all passes, one
+// token a lane: in the passes themselves the softplus, the exponentials and the
+// sum over the chunk kept three waves waiting for one.
 // ---------------------------------------------------------------------------
 template <int Q>
 struct alignas(16) Scal {
@@ -260,157 +324,267 @@ struct alignas(16) Scal {
   float w[Q];    // weight of the token's input
   float c[Q];    // its weight in the state at the chunk's end (0 if a flag follows)
   float e[Q];    // weight of the entering state in the token's row (0 after a flag)
+  float g[Q];    // w times the decay to the end of the token's tile of 16
   int id[Q];     // flags up to the token
   float dec;     // weight of the entering state in the state at the chunk's end
-  float pad[3];
+  int flags;     // flags in the chunk
+  float pad[2];
 };
 
-// Raw step and flag of this lane's token of a chunk, loaded ahead of time.
-struct StepIn {
-  float raw;
-  int flag;
-};
-
-template <typename T>
-__device__ __forceinline__ StepIn load_step(const HeadsParams& p, int64_t b, int h, float bias,
-                                            int64_t t0, int len) {
-  const int l = threadIdx.x & 63;
-  StepIn s = {0.0f, 0};
-  if (l < len) {
-    s.raw = Elem<T>::load1(static_cast<const T*>(p.delta.p) + b * p.delta.batch +
-                           (t0 + l) * p.delta.token + h) +
-            bias;
-    if (p.reset) s.flag = p.reset[b * p.L + t0 + l] != 0;
-  }
-  return s;
-}
-
+// The heads' scalars of one chunk, on their way from global memory to LDS.
 template <int Q>
-__device__ __forceinline__ void chunk_scalars(const HeadsParams& p, const StepIn& in, float A,
-                                              int len, Scal<Q>* o) {
-  const int l = threadIdx.x & 63;
-  const Step st = make_step(in.raw, A, p.softplus != 0, p.zoh != 0);
-  float S = l < len ? st.lg : 0.0f;
-  const float w = l < len ? st.w : 0.0f;
-  const uint64_t flags = __ballot(in.flag && l < len);
-  const uint64_t upto = flags & ((2ull << l) - 1ull);
-  const int start = upto ? 63 - __builtin_clzll(upto) : 0;
-  const int id = __builtin_popcountll(upto), id_end = __builtin_popcountll(flags);
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const float t = __shfl_up(S, off);
-    if (l - off >= start) S += t;
+struct ScalStage {
+  static constexpr int PIECES = sizeof(Scal<Q>) / 16;
+  u32x4 v[2];
+  __device__ __forceinline__ void load(const void* scal, int64_t at, int heads) {
+    const Buffer buf(static_cast<const Scal<Q>*>(scal) + at, (uint32_t)(heads * PIECES * 16));
+    const uint32_t o = 16u * (uint32_t)opaque_int((int)threadIdx.x);
+    v[0] = buf.load(o);
+    v[1] = u32x4{0, 0, 0, 0};
+    if (heads * PIECES > 256) v[1] = buf.load(o + 256 * 16);
   }
-  const float end = __shfl(S, 63);
-  if (l < Q) {
-    o->S[l] = S;
-    o->w[l] = w;
-    o->c[l] = id == id_end ? fast_exp2(end - S) * w : 0.0f;
-    o->e[l] = id == 0 ? fast_exp2(S) : 0.0f;
-    o->id[l] = id;
+  __device__ __forceinline__ void store(Scal<Q>* lds, int heads) const {
+    u32x4* q = reinterpret_cast<u32x4*>(lds);
+    const int n = heads * PIECES;
+    const int i = threadIdx.x;
+    if (i < n) q[i] = v[0];
+    if (i + 256 < n) q[i + 256] = v[1];
   }
-  if (l == 0) o->dec = id_end == 0 ? fast_exp2(end) : 0.0f;
-}
+};
 
 // x weighted by f; 0 for a weight of 0, whatever x holds.
 __device__ __forceinline__ float weigh(float x, float f) { return f == 0.0f ? 0.0f : x * f; }
 
 // ---------------------------------------------------------------------------
 // Infinities and NaN.  A matrix product spreads one over its whole row and
-// column even where the other factor's weight is zero, so in a chunk that holds
-// one, u's are taken out (zeros in their place, and a mark by column), and the
-// rows of B that a flag keeps from the state at the chunk's end are cleared.
-// What the marked values reach is then set to NaN: the rows of the same
-// sequence from the mark on, and the state if the sequence goes on.  All other
-// rows keep the bits they have without it.  Called by the whole block, between
-// barriers of its own; B's rows must not be read for M afterwards.
+// column even where the other factor's weight is zero.  Where a wave's columns
+// of a chunk hold one, they are taken out (zeros in their place) and kept as
+// marks by column; what they reach is then set to NaN: the rows of the same
+// sequence from the mark on, and the state if the sequence goes on.  In a chunk
+// with flags the rows of B that a flag keeps from the state are cleared when
+// they hold one.  All other rows keep the bits they have without it.
 // ---------------------------------------------------------------------------
-template <typename T, int Q, int NP>
-__device__ __forceinline__ void take_out(T* Xs, int xstride, T* Bs, int bstride,
-                                         const Scal<Q>& sc, uint64_t* marks) {
-  const int id_end = sc.id[Q - 1];
-  if (threadIdx.x < kCols) {
-    uint64_t m = 0;
-    for (int q = 0; q < Q; ++q) {
-      const float x = Elem<T>::load1(Xs + q * xstride + threadIdx.x);
-      if (!(__builtin_fabsf(x) < __builtin_inff())) {
-        m |= 1ull << q;
-        Xs[q * xstride + threadIdx.x] = T(0);
-      }
-    }
-    marks[threadIdx.x] = m;
-  }
-  for (int i = threadIdx.x; i < Q * NP; i += 256)
-    if (sc.id[i / NP] != id_end) Bs[(i / NP) * bstride + i % NP] = T(0);
-  __syncthreads();
+__device__ __forceinline__ bool not_finite(float x) {
+  return !(__builtin_fabsf(x) < __builtin_inff());
 }
 
-// The marks that reach token q: those of its sequence up to it.
+// The marks of column c of a tile (bit q: row q), its values taken out.
+template <typename T, int Q>
+__device__ __forceinline__ uint64_t take_out(T* tile, int stride, int c) {
+  uint64_t m = 0;
+#pragma unroll 1
+  for (int q = 0; q < Q; ++q)
+    if (not_finite(Elem<T>::load1(tile + q * stride + c))) {
+      m |= 1ull << q;
+      tile[q * stride + c] = T(0);
+    }
+  return m;
+}
+
+// Whether a mark reaches token q: one of its sequence up to it.
 template <int Q>
-__device__ __forceinline__ bool marked(uint64_t marks, const Scal<Q>& sc, int q) {
+__device__ __forceinline__ bool marked(uint64_t marks, const int* id, int q) {
+#pragma unroll 1
   for (int s = 0; s <= q; ++s)
-    if ((marks >> s & 1) != 0 && sc.id[s] == sc.id[q]) return true;
+    if ((marks >> s & 1) != 0 && id[s] == id[q]) return true;
   return false;
 }
 
-// ---------------------------------------------------------------------------
-// The state of a head's 64 columns, rows n, columns p: wave w holds columns
-// 16 w + i and, in tile nt, states 16 nt + 4 g + (0..3).
-// ---------------------------------------------------------------------------
-// Between kernels a state is kept in this order, kCols * 32 NK floats.
-template <int NK>
-__device__ __forceinline__ int64_t frag_at(int nt) {
-  return (((threadIdx.x >> 6) * (2 * NK) + nt) * 64 + (threadIdx.x & 63)) * 4;
+// Whether the wave's 32 columns from c0 of a tile hold an infinity or a NaN:
+// zero times anything else is zero.
+template <typename T, int Q>
+__device__ __forceinline__ bool tile_odd(const T* tile, int stride, int c0) {
+  const bf16x8 zero = as_frag(u32x4{0, 0, 0, 0});
+  f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int ks = 0; ks < Q / 32; ++ks)
+#pragma unroll
+    for (int pt = 0; pt < 2; ++pt) {
+      Cols<T> x;
+      x.load(tile, stride, c0 + 16 * pt, 32 * ks);
+      r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(zero, x.top(), r, 0, 0, 0);
+    }
+  return __any(r[0] != 0.0f);
 }
 
-// From or to (batch, heads, headdim, dstate) arrays; c0: the block's first channel.
+// Clears the non-finite values of the rows that a flag keeps from the chunk's
+// end.  Called by the whole block.
+template <typename T, int Q, int NP>
+__device__ __forceinline__ void clear_kept(T* tile, int stride, const int* id) {
+#pragma unroll 1
+  for (int i = threadIdx.x; i < Q * NP; i += 256) {
+    T* x = tile + (i / NP) * stride + i % NP;
+    if (id[i / NP] != id[Q - 1] && not_finite(Elem<T>::load1(x))) *x = T(0);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The state of a slice, rows n, columns p: tile (nt, pt) holds states
+// 16 nt + 4 g + (0..3) of column 16 pt + i.
+// ---------------------------------------------------------------------------
+// Between kernels a slice's state is 32 NK kSlice floats in this order.
 template <int NK>
-__device__ __forceinline__ void load_state(const float* st, int c0, int P, int N, f32x4 (&h)[2 * NK]) {
-  const int pp = c0 + 16 * (threadIdx.x >> 6) + lane_i();
+__device__ __forceinline__ int64_t frag_at(int nt, int pt) {
+  return ((nt * 2 + pt) * 64 + (int)(threadIdx.x & 63)) * 4;
+}
+template <int NK>
+constexpr int64_t slice_floats() { return 32 * NK * kSlice; }
+
+template <int NK>
+__device__ __forceinline__ void load_frags(const float* st, f32x4 (&h)[2 * NK][2]) {
 #pragma unroll
-  for (int nt = 0; nt < 2 * NK; ++nt) {
-    const int n = 16 * nt + 4 * lane_g();
+  for (int nt = 0; nt < 2 * NK; ++nt)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      h[nt][j] = st && pp < P && n + j < N ? st[(int64_t)pp * N + n + j] : 0.0f;
+    for (int pt = 0; pt < 2; ++pt) h[nt][pt] = *reinterpret_cast<const f32x4*>(st + frag_at<NK>(nt, pt));
+}
+
+template <int NK>
+__device__ __forceinline__ void store_frags(float* st, const f32x4 (&h)[2 * NK][2]) {
+#pragma unroll
+  for (int nt = 0; nt < 2 * NK; ++nt)
+#pragma unroll
+    for (int pt = 0; pt < 2; ++pt) *reinterpret_cast<f32x4*>(st + frag_at<NK>(nt, pt)) = h[nt][pt];
+}
+
+template <int NK>
+__device__ __forceinline__ void fill(f32x4 (&h)[2 * NK][2], float v) {
+#pragma unroll
+  for (int nt = 0; nt < 2 * NK; ++nt)
+#pragma unroll
+    for (int pt = 0; pt < 2; ++pt) h[nt][pt] = f32x4{v, v, v, v};
+}
+
+// From or to one head's (headdim, dstate) state; c0: the slice's first channel.
+template <int NK>
+__device__ __forceinline__ void load_state(const float* st, int c0, int P, int N,
+                                           f32x4 (&h)[2 * NK][2]) {
+#pragma unroll
+  for (int pt = 0; pt < 2; ++pt) {
+    const int pp = c0 + 16 * pt + lane_i();
+#pragma unroll
+    for (int nt = 0; nt < 2 * NK; ++nt) {
+      const int n = 16 * nt + 4 * lane_g();
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        h[nt][pt][j] = st && pp < P && n + j < N ? st[(int64_t)pp * N + n + j] : 0.0f;
+    }
   }
 }
 
 template <int NK>
 __device__ __forceinline__ void store_state(float* st, int c0, int P, int N,
-                                            const f32x4 (&h)[2 * NK]) {
-  const int pp = c0 + 16 * (threadIdx.x >> 6) + lane_i();
-  if (pp >= P) return;
+                                            const f32x4 (&h)[2 * NK][2]) {
+  const bool whole = N % 4 == 0 && (reinterpret_cast<uintptr_t>(st) & 15) == 0;
 #pragma unroll
-  for (int nt = 0; nt < 2 * NK; ++nt) {
-    const int n = 16 * nt + 4 * lane_g();
-    if (N % 4 == 0 && (reinterpret_cast<uintptr_t>(st) & 15) == 0) {
-      if (n < N) *reinterpret_cast<f32x4*>(st + (int64_t)pp * N + n) = h[nt];
-    } else {
+  for (int pt = 0; pt < 2; ++pt) {
+    const int pp = c0 + 16 * pt + lane_i();
+    if (pp >= P) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n + j < N) st[(int64_t)pp * N + n + j] = h[nt][j];
+    for (int nt = 0; nt < 2 * NK; ++nt) {
+      const int n = 16 * nt + 4 * lane_g();
+      if (whole) {
+        if (n < N) *reinterpret_cast<f32x4*>(st + (int64_t)pp * N + n) = h[nt][pt];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < N) st[(int64_t)pp * N + n + j] = h[nt][pt][j];
+      }
     }
   }
 }
 
-// h <- dec h + sum_t c_t keys_t vals_t^T over a chunk's tiles.
-template <typename T, int NK>
-__device__ __forceinline__ void update_state(f32x4 (&h)[2 * NK], float dec, const T* keys,
-                                             int kstride, const T* vals, int vstride,
-                                             const float* c) {
-  constexpr int Q = Mx<T>::Q;
-#pragma unroll
-  for (int nt = 0; nt < 2 * NK; ++nt)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[nt][j] = weigh(h[nt][j], dec);
-#pragma unroll
-  for (int ks = 0; ks < Q / 32; ++ks) {
-    const Frag<3> x = load_cols_weighted<T>(vals, vstride, 16 * (threadIdx.x >> 6), 32 * ks, c);
+// h <- dec h; zero where dec is, whatever h holds.  dec is the wave's.
+template <int NK>
+__device__ __forceinline__ void decay_state(f32x4 (&h)[2 * NK][2], float dec) {
+  if (dec == 0.0f) {
+    fill<NK>(h, 0.0f);
+  } else {
 #pragma unroll
     for (int nt = 0; nt < 2 * NK; ++nt)
-      mma(h[nt], load_cols<T>(keys, kstride, 16 * nt, 32 * ks), x);
+#pragma unroll
+      for (int pt = 0; pt < 2; ++pt) h[nt][pt] *= dec;
   }
+}
+
+// h += sum_t c_t keys_t x_t^T over 32 tokens, x given as fragments.
+template <typename T, int NK, int NX>
+__device__ __forceinline__ void add_outer(f32x4 (&h)[2 * NK][2], const T* keys, int kstride, int k0,
+                                          const Frag<NX> (&x)[2]) {
+#pragma unroll
+  for (int nt = 0; nt < 2 * NK; nt += 2) {
+    const Frag<Mx<T>::PARTS> b[2] = {load_cols<T>(keys, kstride, 16 * nt, k0),
+                                     load_cols<T>(keys, kstride, 16 * nt + 16, k0)};
+    f32x4 (&pair)[2][2] = *reinterpret_cast<f32x4(*)[2][2]>(&h[nt]);
+    mma(pair, b, x);
+    if (nt % 4 == 2) phase();
+  }
+}
+
+// A chunk's step of a slice's state: h <- dec h + sum_t c_t B_t u_t^T.
+template <typename T, int NK>
+__device__ __forceinline__ void step_state(f32x4 (&h)[2 * NK][2], const Scal<Mx<T>::Q>& sc,
+                                           const T* Bs, int bstride, const T* Xs, int xstride,
+                                           int col, const uint64_t (&marks)[2]) {
+  constexpr int Q = Mx<T>::Q;
+  decay_state<NK>(h, sc.dec);
+#pragma unroll
+  for (int ks = 0; ks < Q / 32; ++ks) {
+    Frag<3> x[2];
+#pragma unroll
+    for (int pt = 0; pt < 2; ++pt) {
+      Cols<T> c;
+      c.load(Xs, xstride, col + 16 * pt, 32 * ks);
+      x[pt] = c.weighted(sc.c, 32 * ks);
+    }
+    add_outer<T, NK>(h, Bs, bstride, 32 * ks, x);
+  }
+#pragma unroll
+  for (int pt = 0; pt < 2; ++pt)
+    if (marks[pt] != 0 && marked<Q>(marks[pt], sc.id, Q - 1))
+#pragma unroll
+      for (int nt = 0; nt < 2 * NK; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[nt][pt][j] = __builtin_nanf("");
+}
+
+// Which heads and columns a block and its waves take.
+struct Place {
+  int64_t b;
+  int seg, g, h0;      // first head of the block
+  int heads;           // heads of the block
+  int h, slice;        // the wave's
+  bool on;             // whether the wave has columns
+  int c0, ncol;        // its first channel in the head, channels left there
+  int col;             // its first column in the block's tile
+};
+
+// Blocks in order: batch row, segment, group, head block; contiguous ranges
+// share an XCD, whose L2 then serves B and C to all heads of a row.
+__device__ __forceinline__ Place place_of(const HeadsParams& p, int nseg) {
+  int id = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+  Place k;
+  const int per = p.H / p.G, hb = id % p.hblocks;
+  id /= p.hblocks;
+  k.g = id % p.G;
+  id /= p.G;
+  k.seg = id % nseg;
+  k.b = id / nseg;
+  const int first = hb * p.hpw, left = per - first;
+  k.heads = left < p.hpw ? left : p.hpw;
+  k.h0 = k.g * per + first;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hh = wave / p.slices;
+  k.slice = wave - hh * p.slices;
+  k.on = hh < k.heads;
+  k.h = k.h0 + (k.on ? hh : 0);
+  k.c0 = k.slice * kSlice;
+  k.ncol = p.P - k.c0;
+  k.col = wave * kSlice;
+  return k;
+}
+
+__device__ __forceinline__ int64_t slice_slot(const HeadsParams& p, const Place& k, int n, int i) {
+  return ((k.b * p.H + k.h) * p.slices + k.slice) * n + i;
 }
 
 }  // namespace mscan

@@ -1,0 +1,64 @@
+// The scalars of every chunk of the multi-head scan (Scal, heads_mma.hpp): one
+// wave a (batch row, chunk, head), one token a lane.
+#include "heads_mma.hpp"
+
+namespace mscan {
+
+namespace {
+
+template <typename T>
+__global__ __launch_bounds__(256) void heads_scal_kernel(const HeadsParams p) {
+  constexpr int Q = Mx<T>::Q;
+  const int64_t chunks = (p.L + Q - 1) / Q;
+  const int l = threadIdx.x & 63;
+  const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= p.batch * chunks * p.H) return;
+  const int h = (int)(id % p.H);
+  const int64_t bc = id / p.H, b = bc / chunks, t0 = (bc - b * chunks) * Q;
+  const int len = p.L - t0 < Q ? (int)(p.L - t0) : Q;
+  const int64_t t = t0 + (l < len ? l : len - 1);
+  const float raw =
+      Elem<T>::load1(static_cast<const T*>(p.delta.p) + b * p.delta.batch + t * p.delta.token + h) +
+      (p.bias ? p.bias[h] : 0.0f);
+  const int flag = p.reset ? p.reset[b * p.L + t] : 0;
+  const Step st = make_step(raw, p.A[h], p.softplus != 0, p.zoh != 0);
+  float S = l < len ? st.lg : 0.0f;
+  const float w = l < len ? st.w : 0.0f;
+  const uint64_t flags = __ballot(flag != 0 && l < len);
+  const uint64_t upto = flags & ((2ull << l) - 1ull);
+  const int start = upto ? 63 - __builtin_clzll(upto) : 0;
+  const int n = __builtin_popcountll(upto), n_end = __builtin_popcountll(flags);
+  // sums restart at a flag: no value of one sequence enters another's
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const float x = __shfl_up(S, off);
+    if (l - off >= start) S += x;
+  }
+  const float end = __shfl(S, 63), tile_end = __shfl(S, l | 15);
+  Scal<Q>* o = static_cast<Scal<Q>*>(p.scal) + id;
+  if (l < Q) {
+    o->S[l] = S;
+    o->w[l] = w;
+    o->c[l] = n == n_end ? fast_exp2(end - S) * w : 0.0f;
+    o->e[l] = n == 0 ? fast_exp2(S) : 0.0f;
+    o->g[l] = fast_exp2(tile_end - S) * w;
+    o->id[l] = n;
+  }
+  if (l == 0) {
+    o->dec = n_end == 0 ? fast_exp2(end) : 0.0f;
+    o->flags = n_end;
+  }
+}
+
+}  // namespace
+
+hipError_t dispatch_heads_scal(const HeadsParams& p, int dtype, hipStream_t s) {
+  const int q = dtype == 0 ? Mx<float>::Q : Mx<bf16_t>::Q;
+  const int64_t waves = p.batch * ((p.L + q - 1) / q) * p.H;
+  const dim3 grid((unsigned)((waves + 3) / 4));
+  if (dtype == 0) hipLaunchKernelGGL((heads_scal_kernel<float>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((heads_scal_kernel<bf16_t>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace mscan

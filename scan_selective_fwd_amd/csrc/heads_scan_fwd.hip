@@ -1,289 +1,359 @@
 // Forward of the multi-head scan over a prompt (the formulas: heads_mma.hpp).
 //
-// A block of 4 waves walks one head's 64 columns along a segment of the
-// sequence, chunk by chunk, the (64, N) state in its registers: what is read is
-// u, delta, B, C, what is written is out.  Where the heads alone do not fill
-// the chip the sequence is cut into segments: a first pass over the segments
-// leaves each one's end state from zero and its decay, a carry joins them, and
-// the output pass starts each segment from the state entering it.
+// A block of 4 waves walks along a segment of the sequence, chunk by chunk, a
+// slice of 32 channels a wave, the slice's (N, 32) state in its registers: what
+// is read is u, delta, B, C, what is written is out.  The heads of a block
+// share B, C and the products C_q . B_s.  Where the heads alone do not fill the
+// chip the sequence is cut into segments: a first pass over the segments leaves
+// each one's end state from zero and its decay, a carry joins them, and the
+// output pass starts each segment from the state entering it.
 #include "heads_mma.hpp"
 
 namespace mscan {
 
 namespace {
 
-struct Block {
-  int64_t b;
-  int h, pb, seg, g;
+template <typename T, int NK>
+struct FwdTiles {
+  static constexpr int Q = Mx<T>::Q, PAD = Mx<T>::PAD, NP = 32 * NK;
+  static constexpr int SX = kCols + PAD, SN = NP + PAD, SM = Q + PAD, QT = Q / 16;
+  static constexpr int TILES = QT * (QT + 1) / 2;
+  static constexpr int PARTS = Mx<T>::PARTS;
 };
 
-// Blocks in order: batch row, segment, head, column block; contiguous ranges
-// share an XCD, whose L2 then serves B and C to all heads of a row.
-__device__ __forceinline__ Block block_of(const HeadsParams& p, int nseg) {
-  int id = xcd_remap((int)blockIdx.x, (int)gridDim.x);
-  Block k;
-  k.pb = id % p.PB;
-  id /= p.PB;
-  k.h = id % p.H;
-  id /= p.H;
-  k.seg = id % nseg;
-  k.b = id / nseg;
-  k.g = k.h / (p.H / p.G);
-  return k;
+// Dynamic LDS: the heads' scalars and, in the output pass, their M tiles.
+template <typename T>
+size_t scal_bytes(int hpw) {
+  return (size_t)hpw * sizeof(Scal<Mx<T>::Q>);
 }
-
-__device__ __forceinline__ int64_t slot_of(const HeadsParams& p, int64_t b, int h, int pb, int n,
-                                           int k) {
-  return ((b * p.H + h) * p.PB + pb) * n + k;
-}
-
-template <int NK>
-__device__ __forceinline__ void spoil(f32x4 (&h)[2 * NK]) {
-#pragma unroll
-  for (int nt = 0; nt < 2 * NK; ++nt)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[nt][j] = __builtin_nanf("");
+template <typename T, int NK>
+size_t m_bytes(int hpw) {
+  return (size_t)hpw * FwdTiles<T, NK>::Q * FwdTiles<T, NK>::SM * sizeof(T);
 }
 
 template <typename T, int NK, bool VEC>
-__global__ __launch_bounds__(256, 2) void heads_fwd_kernel(const HeadsFwdParams p) {
-  constexpr int Q = Mx<T>::Q, PAD = Mx<T>::PAD, NP = 32 * NK;
-  constexpr int SX = kCols + PAD, SN = NP + PAD, SM = Q + PAD, QT = Q / 16;
-  constexpr int PARTS = Mx<T>::PARTS;
+__global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const HeadsFwdParams p) {
+  using F = FwdTiles<T, NK>;
+  constexpr int Q = F::Q, NP = F::NP, SX = F::SX, SN = F::SN, SM = F::SM, QT = F::QT;
+  constexpr int PARTS = F::PARTS;
   __shared__ __align__(16) T Xs[Q * SX];
   __shared__ __align__(16) T Bs[Q * SN];
   __shared__ __align__(16) T Cs[Q * SN];
-  __shared__ __align__(16) T Ms[Q * SM];
-  __shared__ Scal<Q> scal[2];
-  __shared__ uint32_t bad[2];
-  __shared__ uint64_t marks[kCols];
-  const Block k = block_of(p, p.nseg);
-  const int wave = threadIdx.x >> 6;
-  const int c0 = k.pb * kCols, ncol = p.P - c0 < kCols ? p.P - c0 : kCols;
-  const float A = p.A[k.h], bias = p.bias ? p.bias[k.h] : 0.0f, D = p.D ? p.D[k.h] : 0.0f;
+  extern __shared__ __align__(16) char dyn[];
+  Scal<Q>* const scal = reinterpret_cast<Scal<Q>*>(dyn);
+  T* const Mall = reinterpret_cast<T*>(dyn + p.hpw * sizeof(Scal<Q>));
+  const Place k = place_of(p, p.nseg);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t begin = (int64_t)k.seg * p.seg_len;
   const int64_t end = k.seg + 1 == p.nseg ? p.L : begin + p.seg_len;
-  const int64_t ucol = (int64_t)k.h * p.P + c0, ncols = (int64_t)k.g * p.N;
+  const int64_t ucol = (int64_t)k.h0 * p.P, ncols = (int64_t)k.g * p.N;
+  const int uwidth = (k.h0 + k.heads) * p.P, nwidth = (k.g + 1) * p.N;
+  const int sub = p.slices * kSlice, hh = wave / p.slices;
+  const float D = p.D ? p.D[k.h] : 0.0f;
+  const int64_t chunks = (p.L + Q - 1) / Q;
 
-  f32x4 h[2 * NK];
-  if (k.seg == 0) {
-    load_state<NK>(p.h0 ? p.h0 + (k.b * p.H + k.h) * (int64_t)p.P * p.N : nullptr, c0, p.P, p.N, h);
-  } else {
-    const float* st = p.seg_state + slot_of(p, k.b, k.h, k.pb, p.nseg - 1, k.seg - 1) * (kCols * NP);
-#pragma unroll
-    for (int nt = 0; nt < 2 * NK; ++nt)
-      h[nt] = *reinterpret_cast<const f32x4*>(st + frag_at<NK>(nt));
-  }
+  f32x4 h[2 * NK][2];
+  if (!k.on)
+    fill<NK>(h, 0.0f);
+  else if (k.seg == 0)
+    load_state<NK>(p.h0 ? p.h0 + (k.b * p.H + k.h) * (int64_t)p.P * p.N : nullptr, k.c0, p.P, p.N, h);
+  else
+    load_frags<NK>(p.seg_state + slice_slot(p, k, p.nseg - 1, k.seg - 1) * slice_floats<NK>(), h);
   // tiles above the diagonal are read as part of a 32-step and stay zero
-  for (int i = threadIdx.x; i < Q * SM; i += 256) Ms[i] = T(0);
-  if (threadIdx.x < 2) bad[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < p.hpw * Q * SM; i += 256) Mall[i] = T(0);
 
-  Stage<T, Q, kCols> sx;
-  Stage<T, Q, NP> sb, sc;
-  StepIn in{};
+  Stage<T, Q, kCols, VEC> sx;
+  Stage<T, Q, NP, VEC> sb, sc;
+  ScalStage<Q> ss;
+  sx.init(p.u, ucol, sub, p.P, p.P, k.heads);
+  sb.init(p.B, ncols, NP, 0, p.N, 1);
+  sc.init(p.C, ncols, NP, 0, p.N, 1);
+  auto rows = [&](int64_t t) { return end - t < Q ? (int)(end - t) : Q; };
   auto fetch = [&](int64_t t) {
-    const int len = end - t < Q ? (int)(end - t) : Q;
-    sx.template load<VEC>(p.u, k.b, t, len, ucol, ncol);
-    sb.template load<VEC>(p.B, k.b, t, len, ncols, p.N);
-    sc.template load<VEC>(p.C, k.b, t, len, ncols, p.N);
-    if (wave == 3) in = load_step<T>(p, k.b, k.h, bias, t, len);
+    const int len = rows(t);
+    ss.load(p.scal, (k.b * chunks + t / Q) * p.H + k.h0, k.heads);
+    sx.load(p.u, k.b, t, len, ucol, p.P, uwidth);
+    sb.load(p.B, k.b, t, len, ncols, 0, nwidth);
+    sc.load(p.C, k.b, t, len, ncols, 0, nwidth);
   };
   fetch(begin);
-  if (wave == 3) chunk_scalars<Q>(p, in, A, end - begin < Q ? (int)(end - begin) : Q, &scal[0]);
-  int buf = 0;
   __syncthreads();
-  for (int64_t t = begin; t < end;) {
-    const int len = end - t < Q ? (int)(end - t) : Q;
+  for (int64_t t = begin; t < end; t += Q) {
+    const int len = rows(t);
     sx.store(Xs, SX);
     sb.store(Bs, SN);
     sc.store(Cs, SN);
-    if (sx.non_finite() | sb.non_finite()) bad[buf] = 1;
+    ss.store(scal, k.heads);
     __syncthreads();
-    const int64_t next = t + Q;
-    if (next < end) fetch(next);
-    const Scal<Q>& sc_ = scal[buf];
+    // the next chunk's loads have this whole one to arrive
+    if (t + Q < end) fetch(t + Q);
+    const Scal<Q>& me = scal[k.on ? hh : 0];
+    const bool flagged = scal[0].flags != 0;   // flags are the batch row's
 
-    // M^T tiles (rows s, columns q) on and below the diagonal, stored as M rows
+    // M^T tiles (rows s, columns q) on and below the diagonal, stored as M's
+    // rows: C_q . B_s once for the block, weighted for each head.  Up to three
+    // tiles a wave, side by side.
     {
-      constexpr int TILES = QT * (QT + 1) / 2;
-      // wave 3 also prepares the next chunk's scalars
-      const int t0 = wave * (TILES / 3), t1 = wave == 3 ? TILES : t0 + TILES / 3;
-      for (int i = t0; i < t1; ++i) {
-        int qt = 0, st = i;
-        while (st > qt) st -= ++qt;
-        f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+      constexpr int MINE = QT == 4 ? 3 : 1;
+      int qt[MINE], st[MINE];
+      f32x4 a[MINE][1][1];
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk)
-          mma(a, load_rows<T>(Bs, SN, 16 * st, 32 * kk), load_rows<T>(Cs, SN, 16 * qt, 32 * kk));
-        const int q = 16 * qt + lane_i(), s = 16 * st + 4 * lane_g();
-        const float Sq = sc_.S[q];
-        const int idq = sc_.id[q];
-        float m[4];
+      for (int i = 0; i < MINE; ++i) {
+        const int id = wave + 4 * i < F::TILES ? wave + 4 * i : F::TILES - 1;
+        qt[i] = id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3;
+        st[i] = id - qt[i] * (qt[i] + 1) / 2;
+        a[i][0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool on = s + j <= q && sc_.id[s + j] == idq;
-          m[j] = on ? a[j] * (fast_exp2(Sq - sc_.S[s + j]) * sc_.w[s + j]) : 0.0f;
+      for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+          const Frag<PARTS> bf[1] = {load_rows<T>(Bs, SN, 16 * st[i], 32 * kk)};
+          const Frag<PARTS> cf[1] = {load_rows<T>(Cs, SN, 16 * qt[i], 32 * kk)};
+          mma(a[i], bf, cf);
         }
-        if constexpr (sizeof(T) == 2) {
-          // rounded to bfloat16, as out is
-          *reinterpret_cast<u32x2*>(Ms + q * SM + s) =
-              u32x2{pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3])};
-        } else {
-          *reinterpret_cast<f32x4*>(Ms + q * SM + s) = f32x4{m[0], m[1], m[2], m[3]};
+      for (int x = 0; x < k.heads; ++x) {
+        const Scal<Q>& o = scal[x];
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+          const int q = 16 * qt[i] + lane_i(), s = 16 * st[i] + 4 * lane_g();
+          const float Sq = o.S[q];
+          float m[4];
+          if (st[i] < qt[i] && p.softplus) {
+            // below the diagonal the decay is the product of two, to the end of
+            // s's tile and on to q: with steps that are never negative neither
+            // leaves the range that their product keeps
+            const float f = fast_exp2(Sq - o.S[16 * st[i] + 15]);
+            const f32x4 gs = *reinterpret_cast<const f32x4*>(o.g + s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m[j] = a[i][0][0][j] * (gs[j] * f);
+          } else {
+            const f32x4 Ss = *reinterpret_cast<const f32x4*>(o.S + s);
+            const f32x4 w = *reinterpret_cast<const f32x4*>(o.w + s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              m[j] = a[i][0][0][j] * (fast_exp2(Sq - Ss[j]) * w[j]);
+              m[j] = s + j <= q ? m[j] : 0.0f;
+            }
+          }
+          if (flagged) {
+            const int idq = o.id[q];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m[j] = o.id[s + j] == idq ? m[j] : 0.0f;
+          }
+          if (wave + 4 * i < F::TILES) {
+            T* Ms = Mall + x * Q * SM + q * SM + s;
+            if constexpr (sizeof(T) == 2)   // rounded to bfloat16, as out is
+              *reinterpret_cast<u32x2*>(Ms) = u32x2{pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3])};
+            else
+              *reinterpret_cast<f32x4*>(Ms) = f32x4{m[0], m[1], m[2], m[3]};
+          }
         }
       }
     }
+    phase();
     // out^T (rows p, columns q): the entering state's share.  The state is
     // rounded to bfloat16 for it where out is.
-    f32x4 y[QT];
+    f32x4 y[2][QT];
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt) y[qt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
-    for (int kk = 0; kk < NK; ++kk) {
-      const Frag<PARTS> hf = acc_frag<PARTS>(h[2 * kk], h[2 * kk + 1]);
+      for (int qt = 0; qt < QT; ++qt) y[pt][qt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (k.on) {
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) mma(y[qt], hf, load_rows<T>(Cs, SN, 16 * qt, 32 * kk));
-    }
+      for (int kk = 0; kk < NK; ++kk) {
+        const Frag<PARTS> hf[2] = {acc_frag<PARTS>(h[2 * kk][0], h[2 * kk + 1][0]),
+                                   acc_frag<PARTS>(h[2 * kk][1], h[2 * kk + 1][1])};
+        Frag<PARTS> cf[QT];
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-      const float e = sc_.e[16 * qt + lane_i()];
+        for (int qt = 0; qt < QT; ++qt) cf[qt] = load_rows<T>(Cs, SN, 16 * qt, 32 * kk);
+        mma(y, hf, cf);
+        phase();
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[qt][j] = weigh(y[qt][j], e);
-    }
-    if (wave == 3 && next < end)
-      chunk_scalars<Q>(p, in, A, end - next < Q ? (int)(end - next) : Q, &scal[buf ^ 1]);
-    if (threadIdx.x == 0) bad[buf ^ 1] = 0;
-    __syncthreads();
-    const bool odd = bad[buf] != 0;
-    if (odd) take_out<T, Q, NP>(Xs, SX, Bs, SN, sc_, marks);
-    // ... and the chunk's own inputs'
+      for (int qt = 0; qt < QT; ++qt) {
+        const float e = me.e[16 * qt + lane_i()];
 #pragma unroll
-    for (int ks = 0; ks < Q / 32; ++ks) {
-      const Frag<PARTS> x = load_cols<T>(Xs, SX, 16 * wave, 32 * ks);
-#pragma unroll
-      for (int qt = 2 * ks; qt < QT; ++qt) mma(y[qt], x, load_rows<T>(Ms, SM, 16 * qt, 32 * ks));
-    }
-    update_state<T, NK>(h, sc_.dec, Bs, SN, Xs, SX, sc_.c);
-    // four columns of a token a lane
-    const int col = 16 * wave + 4 * lane_g();
-    if (odd) {
-      if (marked(marks[16 * wave + lane_i()], sc_, Q - 1)) spoil<NK>(h);
-      for (int qt = 0; qt < QT; ++qt)
-        for (int j = 0; j < 4; ++j)
-          if (marked(marks[col + j], sc_, 16 * qt + lane_i()))
-#pragma unroll
-            for (int a = 0; a < QT; ++a)
-#pragma unroll
-              for (int b = 0; b < 4; ++b)
-                if (a == qt && b == j) y[a][b] = __builtin_nanf("");
-    }
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-      const int q = 16 * qt + lane_i();
-      if (q < len && col < ncol) {
-        const T* ur = Xs + q * SX + col;
-        T* o = static_cast<T*>(p.out) + ((k.b * p.L + t + q) * p.H + k.h) * (int64_t)p.P + c0 + col;
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(D, Elem<T>::load1(ur + j), y[qt][j]);
-        if constexpr (VEC) {
-          if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<u32x2*>(o) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-          else
-            *reinterpret_cast<f32x4*>(o) = f32x4{v[0], v[1], v[2], v[3]};
-        } else {
+        for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (col + j < ncol) Elem<T>::store1(o + j, v[j]);
-        }
+            y[pt][qt][j] = flagged ? weigh(y[pt][qt][j], e) : y[pt][qt][j] * e;
       }
     }
-    t = next;
-    buf ^= 1;
+    __syncthreads();
+    if (flagged) {
+      clear_kept<T, Q, NP>(Bs, SN, scal[0].id);
+      __syncthreads();
+    }
+    if (k.on) {
+      // ... and the chunk's own inputs'
+      uint64_t marks[2] = {0, 0};
+      const bool odd = tile_odd<T, Q>(Xs, SX, k.col);
+      if (odd) {
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt)
+          marks[pt] = take_out<T, Q>(Xs, SX, k.col + 16 * pt + lane_i());
+      }
+      const T* Ms = Mall + hh * Q * SM;
+#pragma unroll
+      for (int ks = 0; ks < Q / 32; ++ks) {
+        const Frag<PARTS> xf[2] = {load_cols<T>(Xs, SX, k.col, 32 * ks),
+                                   load_cols<T>(Xs, SX, k.col + 16, 32 * ks)};
+#pragma unroll
+        for (int qt = 2 * ks; qt < QT; qt += 2) {
+          const Frag<PARTS> mf[2] = {load_rows<T>(Ms, SM, 16 * qt, 32 * ks),
+                                     load_rows<T>(Ms, SM, 16 * qt + 16, 32 * ks)};
+          f32x4 yy[2][2] = {{y[0][qt], y[0][qt + 1]}, {y[1][qt], y[1][qt + 1]}};
+          mma(yy, xf, mf);
+          y[0][qt] = yy[0][0];
+          y[0][qt + 1] = yy[0][1];
+          y[1][qt] = yy[1][0];
+          y[1][qt + 1] = yy[1][1];
+          phase();
+        }
+      }
+      if (odd) {
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // column 4 g + j's marks are with the lane of that column
+            const int from = 4 * lane_g() + j;
+            const uint64_t m = (uint64_t)(uint32_t)__shfl((int)(uint32_t)marks[pt], from) |
+                               (uint64_t)(uint32_t)__shfl((int)(uint32_t)(marks[pt] >> 32), from) << 32;
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt)
+              if (marked<Q>(m, me.id, 16 * qt + lane_i())) y[pt][qt][j] = __builtin_nanf("");
+          }
+      }
+      phase();
+      // four columns of a token a lane
+      const int64_t row = (int64_t)p.H * p.P;
+      T* const o0 = static_cast<T*>(p.out) + (k.b * p.L + t) * row + (int64_t)k.h * p.P + k.c0;
+      // one offset a lane, the tiles' bases uniform; a chunk of out spans less
+      // than 2^31 bytes
+      const uint32_t off = (uint32_t)opaque_int(
+          (int)((uint32_t)lane_i() * (uint32_t)(row * sizeof(T)) + 4u * lane_g() * sizeof(T)));
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) {
+        const int q = 16 * qt + lane_i();
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) {
+          const int c = 16 * pt + 4 * lane_g();
+          const T* ur = Xs + q * SX + k.col + c;
+          float v[4];
+          if constexpr (sizeof(T) == 2) {
+            const u32x2 u = *reinterpret_cast<const u32x2*>(ur);
+            v[0] = bf16_lo(u[0]); v[1] = bf16_hi(u[0]); v[2] = bf16_lo(u[1]); v[3] = bf16_hi(u[1]);
+          } else {
+            const f32x4 u = *reinterpret_cast<const f32x4*>(ur);
+            v[0] = u[0]; v[1] = u[1]; v[2] = u[2]; v[3] = u[3];
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(D, v[j], y[pt][qt][j]);
+          if (q < len && c < k.ncol) {
+            if constexpr (VEC) {
+              char* o = reinterpret_cast<char*>(o0 + 16 * qt * row + 16 * pt) + off;
+              if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<u32x2*>(o) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+              else
+                *reinterpret_cast<f32x4*>(o) = f32x4{v[0], v[1], v[2], v[3]};
+            } else {
+              T* o = o0 + q * row + c;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (c + j < k.ncol) Elem<T>::store1(o + j, v[j]);
+            }
+          }
+        }
+        phase();
+      }
+      phase();
+      step_state<T, NK>(h, me, Bs, SN, Xs, SX, k.col, marks);
+    }
     __syncthreads();
   }
-  if (p.last && k.seg + 1 == p.nseg)
-    store_state<NK>(p.last + (k.b * p.H + k.h) * (int64_t)p.P * p.N, c0, p.P, p.N, h);
+  if (p.last && k.on && k.seg + 1 == p.nseg)
+    store_state<NK>(p.last + (k.b * p.H + k.h) * (int64_t)p.P * p.N, k.c0, p.P, p.N, h);
 }
 
 // A segment's end state from zero and its decay.
 template <typename T, int NK, bool VEC>
-__global__ __launch_bounds__(256, 2) void heads_seg_kernel(const HeadsFwdParams p) {
-  constexpr int Q = Mx<T>::Q, PAD = Mx<T>::PAD, NP = 32 * NK;
-  constexpr int SX = kCols + PAD, SN = NP + PAD;
+__global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const HeadsFwdParams p) {
+  using F = FwdTiles<T, NK>;
+  constexpr int Q = F::Q, NP = F::NP, SX = F::SX, SN = F::SN;
   __shared__ __align__(16) T Xs[Q * SX];
   __shared__ __align__(16) T Bs[Q * SN];
-  __shared__ Scal<Q> scal[2];
-  __shared__ uint32_t bad[2];
-  __shared__ uint64_t marks[kCols];
-  const Block k = block_of(p, p.nseg - 1);
-  const int wave = threadIdx.x >> 6;
-  const int c0 = k.pb * kCols, ncol = p.P - c0 < kCols ? p.P - c0 : kCols;
-  const float A = p.A[k.h], bias = p.bias ? p.bias[k.h] : 0.0f;
-  const int64_t begin = (int64_t)k.seg * p.seg_len, end = begin + p.seg_len;
-  const int64_t ucol = (int64_t)k.h * p.P + c0, ncols = (int64_t)k.g * p.N;
-  f32x4 h[2 * NK];
-#pragma unroll
-  for (int nt = 0; nt < 2 * NK; ++nt) h[nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  extern __shared__ __align__(16) char dyn[];
+  Scal<Q>* const scal = reinterpret_cast<Scal<Q>*>(dyn);
+  const Place k = place_of(p, p.nseg - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t begin = (int64_t)k.seg * p.seg_len, end = begin + p.seg_len;   // whole chunks
+  const int64_t ucol = (int64_t)k.h0 * p.P, ncols = (int64_t)k.g * p.N;
+  const int uwidth = (k.h0 + k.heads) * p.P, nwidth = (k.g + 1) * p.N;
+  const int sub = p.slices * kSlice, hh = wave / p.slices;
+  const int64_t chunks = (p.L + Q - 1) / Q;
+  f32x4 h[2 * NK][2];
+  fill<NK>(h, 0.0f);
   float dec = 1.0f;
-  Stage<T, Q, kCols> sx;
-  Stage<T, Q, NP> sb;
-  StepIn in{};
-  if (threadIdx.x < 2) bad[threadIdx.x] = 0;
+  Stage<T, Q, kCols, VEC> sx;
+  Stage<T, Q, NP, VEC> sb;
+  ScalStage<Q> ss;
+  sx.init(p.u, ucol, sub, p.P, p.P, k.heads);
+  sb.init(p.B, ncols, NP, 0, p.N, 1);
   auto fetch = [&](int64_t t) {
-    const int len = end - t < Q ? (int)(end - t) : Q;
-    sx.template load<VEC>(p.u, k.b, t, len, ucol, ncol);
-    sb.template load<VEC>(p.B, k.b, t, len, ncols, p.N);
-    if (wave == 3) in = load_step<T>(p, k.b, k.h, bias, t, len);
+    ss.load(p.scal, (k.b * chunks + t / Q) * p.H + k.h0, k.heads);
+    sx.load(p.u, k.b, t, Q, ucol, p.P, uwidth);
+    sb.load(p.B, k.b, t, Q, ncols, 0, nwidth);
   };
   fetch(begin);
-  if (wave == 3) chunk_scalars<Q>(p, in, A, end - begin < Q ? (int)(end - begin) : Q, &scal[0]);
-  int buf = 0;
-  __syncthreads();
-  for (int64_t t = begin; t < end;) {
+  for (int64_t t = begin; t < end; t += Q) {
     sx.store(Xs, SX);
     sb.store(Bs, SN);
-    if (sx.non_finite() | sb.non_finite()) bad[buf] = 1;
+    ss.store(scal, k.heads);
     __syncthreads();
-    const int64_t next = t + Q;
-    if (next < end) fetch(next);
-    if (threadIdx.x == 0) bad[buf ^ 1] = 0;
-    const bool odd = bad[buf] != 0;
-    if (odd) take_out<T, Q, NP>(Xs, SX, Bs, SN, scal[buf], marks);
-    update_state<T, NK>(h, scal[buf].dec, Bs, SN, Xs, SX, scal[buf].c);
-    if (odd && marked(marks[16 * wave + lane_i()], scal[buf], Q - 1)) spoil<NK>(h);
-    dec = weigh(dec, scal[buf].dec);
-    if (wave == 3 && next < end)
-      chunk_scalars<Q>(p, in, A, end - next < Q ? (int)(end - next) : Q, &scal[buf ^ 1]);
-    t = next;
-    buf ^= 1;
+    if (t + Q < end) fetch(t + Q);
+    const Scal<Q>& me = scal[k.on ? hh : 0];
+    if (scal[0].flags != 0) {
+      clear_kept<T, Q, NP>(Bs, SN, scal[0].id);
+      __syncthreads();
+    }
+    if (k.on) {
+      uint64_t marks[2] = {0, 0};
+      if (tile_odd<T, Q>(Xs, SX, k.col)) {
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt)
+          marks[pt] = take_out<T, Q>(Xs, SX, k.col + 16 * pt + lane_i());
+      }
+      step_state<T, NK>(h, me, Bs, SN, Xs, SX, k.col, marks);
+      dec *= me.dec;
+    }
     __syncthreads();
   }
-  const int64_t slot = slot_of(p, k.b, k.h, k.pb, p.nseg - 1, k.seg);
-  float* st = p.seg_state + slot * (kCols * NP);
-#pragma unroll
-  for (int nt = 0; nt < 2 * NK; ++nt) *reinterpret_cast<f32x4*>(st + frag_at<NK>(nt)) = h[nt];
-  if (threadIdx.x == 0) p.seg_dec[slot] = dec;
+  if (!k.on) return;
+  const int64_t slot = slice_slot(p, k, p.nseg - 1, k.seg);
+  store_frags<NK>(p.seg_state + slot * slice_floats<NK>(), h);
+  if ((threadIdx.x & 63) == 0) p.seg_dec[slot] = dec;
 }
 
 // The state entering each segment, in place of the one before's end state.
 template <int NK>
 __global__ __launch_bounds__(256) void heads_carry_kernel(const HeadsFwdParams p) {
-  constexpr int NP = 32 * NK, PER = kCols * NP / 4 / 256;   // blocks a column block
+  constexpr int PER = NK;   // blocks a slice: 1024 NK floats, four a thread
   const int64_t id = blockIdx.x / PER;
   const int e = (int)(blockIdx.x - id * PER) * 256 + threadIdx.x;   // float4 of the state
-  const int pb = (int)(id % p.PB);
-  const int64_t bh = id / p.PB;
-  const int nt = (e >> 6) % (2 * NK), w = (e >> 6) / (2 * NK), l = e & 63;
-  const int pp = pb * kCols + 16 * w + (l & 15), n = 16 * nt + 4 * (l >> 4);
+  const int slice = (int)(id % p.slices);
+  const int64_t bh = id / p.slices;
+  const int nt = e >> 7, pt = (e >> 6) & 1, l = e & 63;
+  const int pp = slice * kSlice + 16 * pt + (l & 15), n = 16 * nt + 4 * (l >> 4);
   f32x4 h = {0.0f, 0.0f, 0.0f, 0.0f};
   if (p.h0 && pp < p.P)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (n + j < p.N) h[j] = p.h0[(bh * p.P + pp) * p.N + n + j];
   const int segs = p.nseg - 1;
-  f32x4* st = reinterpret_cast<f32x4*>(p.seg_state + id * segs * (int64_t)(kCols * NP)) + e;
-  constexpr int64_t STEP = kCols * NP / 4;
+  f32x4* st = reinterpret_cast<f32x4*>(p.seg_state + id * segs * slice_floats<NK>()) + e;
+  constexpr int64_t STEP = slice_floats<NK>() / 4;
 #pragma unroll 4
   for (int k = 0; k < segs; ++k) {
     const f32x4 s = st[k * STEP];
@@ -296,18 +366,25 @@ __global__ __launch_bounds__(256) void heads_carry_kernel(const HeadsFwdParams p
 
 template <typename T, int NK, bool VEC>
 hipError_t fwd_go(const HeadsFwdParams& p, hipStream_t s) {
-  const int64_t cols = p.batch * p.H * p.PB;
+  {
+    const hipError_t e = dispatch_heads_scal(p, sizeof(T) == 4 ? 0 : 1, s);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t blocks = p.batch * p.G * p.hblocks;
   if (p.nseg > 1) {
-    hipLaunchKernelGGL((heads_seg_kernel<T, NK, VEC>), dim3((unsigned)(cols * (p.nseg - 1))), dim3(256),
-                       0, s, p);
+    const size_t lds = scal_bytes<T>(p.hpw);
+    hipLaunchKernelGGL((heads_seg_kernel<T, NK, VEC>), dim3((unsigned)(blocks * (p.nseg - 1))),
+                       dim3(256), lds, s, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((heads_carry_kernel<NK>), dim3((unsigned)(cols * (kCols * 32 * NK / 1024))),
+    hipLaunchKernelGGL((heads_carry_kernel<NK>), dim3((unsigned)(p.batch * p.H * p.slices * NK)),
                        dim3(256), 0, s, p);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((heads_fwd_kernel<T, NK, VEC>), dim3((unsigned)(cols * p.nseg)), dim3(256), 0, s, p);
+  const size_t lds = scal_bytes<T>(p.hpw) + m_bytes<T, NK>(p.hpw);
+  hipLaunchKernelGGL((heads_fwd_kernel<T, NK, VEC>), dim3((unsigned)(blocks * p.nseg)), dim3(256),
+                     lds, s, p);
   return hipGetLastError();
 }
 
