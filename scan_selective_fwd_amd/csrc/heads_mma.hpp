@@ -510,13 +510,18 @@ __device__ __forceinline__ void decay_state(f32x4 (&h)[2 * NK][2], float dec) {
 template <typename T, int NK, int NX>
 __device__ __forceinline__ void add_outer(f32x4 (&h)[2 * NK][2], const T* keys, int kstride, int k0,
                                           const Frag<NX> (&x)[2]) {
+  Frag<Mx<T>::PARTS> b[2][2];
+  b[0][0] = load_cols<T>(keys, kstride, 0, k0);
+  b[0][1] = load_cols<T>(keys, kstride, 16, k0);
 #pragma unroll
-  for (int nt = 0; nt < 2 * NK; nt += 2) {
-    const Frag<Mx<T>::PARTS> b[2] = {load_cols<T>(keys, kstride, 16 * nt, k0),
-                                     load_cols<T>(keys, kstride, 16 * nt + 16, k0)};
-    f32x4 (&pair)[2][2] = *reinterpret_cast<f32x4(*)[2][2]>(&h[nt]);
-    mma(pair, b, x);
-    if (nt % 4 == 2) phase();
+  for (int i = 0; i < NK; ++i) {
+    if (i + 1 < NK) {
+      b[(i + 1) & 1][0] = load_cols<T>(keys, kstride, 32 * i + 32, k0);
+      b[(i + 1) & 1][1] = load_cols<T>(keys, kstride, 32 * i + 48, k0);
+    }
+    phase();
+    f32x4 (&pair)[2][2] = *reinterpret_cast<f32x4(*)[2][2]>(&h[2 * i]);
+    mma(pair, b[i & 1], x);
   }
 }
 

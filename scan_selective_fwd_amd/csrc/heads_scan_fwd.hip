@@ -31,6 +31,109 @@ size_t m_bytes(int hpw) {
   return (size_t)hpw * FwdTiles<T, NK>::Q * FwdTiles<T, NK>::SM * sizeof(T);
 }
 
+// The block's M tiles.  Wave w takes the diagonal tile w and up to two below.
+template <typename T, int NK>
+__device__ __forceinline__ void decayed_products(const HeadsParams& p, int heads, bool flagged,
+                                                 const T* Bs, const T* Cs,
+                                                 const Scal<Mx<T>::Q>* scal, T* Mall) {
+  using F = FwdTiles<T, NK>;
+  constexpr int Q = F::Q, SN = F::SN, SM = F::SM, QT = F::QT, PARTS = F::PARTS;
+  constexpr int OFF = QT == 4 ? 2 : 1;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int qt[1 + OFF], st[1 + OFF];
+  bool on[1 + OFF];
+  on[0] = wave < QT;
+  qt[0] = st[0] = on[0] ? wave : 0;
+  if constexpr (QT == 4) {
+    // (3, wave) for waves 0..2 and (1, 0); then (2, wave) for waves 0, 1
+    qt[1] = wave < 3 ? 3 : 1;
+    st[1] = wave < 3 ? wave : 0;
+    on[1] = true;
+    qt[2] = 2;
+    st[2] = wave & 1;
+    on[2] = wave < 2;
+  } else {
+    qt[1] = 1;
+    st[1] = 0;
+    on[1] = wave == 2;
+  }
+  f32x4 a[1 + OFF][1][1];
+  Frag<PARTS> bf[2][1 + OFF][1], cf[2][1 + OFF][1];
+#pragma unroll
+  for (int i = 0; i <= OFF; ++i) {
+    a[i][0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    bf[0][i][0] = load_rows<T>(Bs, SN, 16 * st[i], 0);
+    cf[0][i][0] = load_rows<T>(Cs, SN, 16 * qt[i], 0);
+  }
+#pragma unroll
+  for (int kk = 0; kk < NK; ++kk) {
+    if (kk + 1 < NK) {
+#pragma unroll
+      for (int i = 0; i <= OFF; ++i) {
+        bf[(kk + 1) & 1][i][0] = load_rows<T>(Bs, SN, 16 * st[i], 32 * kk + 32);
+        cf[(kk + 1) & 1][i][0] = load_rows<T>(Cs, SN, 16 * qt[i], 32 * kk + 32);
+      }
+    }
+    phase();
+#pragma unroll
+    for (int i = 0; i <= OFF; ++i) mma(a[i], bf[kk & 1][i], cf[kk & 1][i]);
+  }
+  const int li = lane_i(), lg = 4 * lane_g();
+#pragma unroll 1
+  for (int x = 0; x < heads; ++x) {
+    const Scal<Q>& o = scal[x];
+    float m[1 + OFF][4], Sq[1 + OFF], Se[1 + OFF];
+    f32x4 g[1 + OFF];
+    const f32x4 Ss = *reinterpret_cast<const f32x4*>(o.S + 16 * st[0] + lg);
+    const f32x4 w = *reinterpret_cast<const f32x4*>(o.w + 16 * st[0] + lg);
+#pragma unroll
+    for (int i = 0; i <= OFF; ++i) {
+      Sq[i] = o.S[16 * qt[i] + li];
+      Se[i] = o.S[16 * st[i] + 15];
+      g[i] = *reinterpret_cast<const f32x4*>(o.g + 16 * st[i] + lg);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      m[0][j] = lg + j <= li ? a[0][0][0][j] * (fast_exp2(Sq[0] - Ss[j]) * w[j]) : 0.0f;
+    // Below the diagonal the decay is the product of two, to the end of s's
+    // tile and on to q: with steps that are never negative neither leaves the
+    // range that their product keeps.
+#pragma unroll
+    for (int i = 1; i <= OFF; ++i) {
+      const float f = fast_exp2(Sq[i] - Se[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[i][j] = a[i][0][0][j] * (g[i][j] * f);
+    }
+    if (!p.softplus) {
+#pragma unroll
+      for (int i = 1; i <= OFF; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          m[i][j] = a[i][0][0][j] *
+                    (fast_exp2(Sq[i] - o.S[16 * st[i] + lg + j]) * o.w[16 * st[i] + lg + j]);
+    }
+    if (flagged) {
+#pragma unroll
+      for (int i = 0; i <= OFF; ++i) {
+        const int idq = o.id[16 * qt[i] + li];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[i][j] = o.id[16 * st[i] + lg + j] == idq ? m[i][j] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i <= OFF; ++i) {
+      if (on[i]) {
+        T* Ms = Mall + x * Q * SM + (16 * qt[i] + li) * SM + 16 * st[i] + lg;
+        if constexpr (sizeof(T) == 2)   // rounded to bfloat16, as out is
+          *reinterpret_cast<u32x2*>(Ms) =
+              u32x2{pack_bf16(m[i][0], m[i][1]), pack_bf16(m[i][2], m[i][3])};
+        else
+          *reinterpret_cast<f32x4*>(Ms) = f32x4{m[i][0], m[i][1], m[i][2], m[i][3]};
+      }
+    }
+  }
+}
+
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const HeadsFwdParams p) {
   using F = FwdTiles<T, NK>;
@@ -91,66 +194,8 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
     const bool flagged = scal[0].flags != 0;   // flags are the batch row's
 
     // M^T tiles (rows s, columns q) on and below the diagonal, stored as M's
-    // rows: C_q . B_s once for the block, weighted for each head.  Up to three
-    // tiles a wave, side by side.
-    {
-      constexpr int MINE = QT == 4 ? 3 : 1;
-      int qt[MINE], st[MINE];
-      f32x4 a[MINE][1][1];
-#pragma unroll
-      for (int i = 0; i < MINE; ++i) {
-        const int id = wave + 4 * i < F::TILES ? wave + 4 * i : F::TILES - 1;
-        qt[i] = id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3;
-        st[i] = id - qt[i] * (qt[i] + 1) / 2;
-        a[i][0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      }
-#pragma unroll
-      for (int kk = 0; kk < NK; ++kk)
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-          const Frag<PARTS> bf[1] = {load_rows<T>(Bs, SN, 16 * st[i], 32 * kk)};
-          const Frag<PARTS> cf[1] = {load_rows<T>(Cs, SN, 16 * qt[i], 32 * kk)};
-          mma(a[i], bf, cf);
-        }
-      for (int x = 0; x < k.heads; ++x) {
-        const Scal<Q>& o = scal[x];
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-          const int q = 16 * qt[i] + lane_i(), s = 16 * st[i] + 4 * lane_g();
-          const float Sq = o.S[q];
-          float m[4];
-          if (st[i] < qt[i] && p.softplus) {
-            // below the diagonal the decay is the product of two, to the end of
-            // s's tile and on to q: with steps that are never negative neither
-            // leaves the range that their product keeps
-            const float f = fast_exp2(Sq - o.S[16 * st[i] + 15]);
-            const f32x4 gs = *reinterpret_cast<const f32x4*>(o.g + s);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m[j] = a[i][0][0][j] * (gs[j] * f);
-          } else {
-            const f32x4 Ss = *reinterpret_cast<const f32x4*>(o.S + s);
-            const f32x4 w = *reinterpret_cast<const f32x4*>(o.w + s);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              m[j] = a[i][0][0][j] * (fast_exp2(Sq - Ss[j]) * w[j]);
-              m[j] = s + j <= q ? m[j] : 0.0f;
-            }
-          }
-          if (flagged) {
-            const int idq = o.id[q];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m[j] = o.id[s + j] == idq ? m[j] : 0.0f;
-          }
-          if (wave + 4 * i < F::TILES) {
-            T* Ms = Mall + x * Q * SM + q * SM + s;
-            if constexpr (sizeof(T) == 2)   // rounded to bfloat16, as out is
-              *reinterpret_cast<u32x2*>(Ms) = u32x2{pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3])};
-            else
-              *reinterpret_cast<f32x4*>(Ms) = f32x4{m[0], m[1], m[2], m[3]};
-          }
-        }
-      }
-    }
+    // rows: C_q . B_s once for the block, weighted for each head.
+    decayed_products<T, NK>(p, k.heads, flagged, Bs, Cs, scal, Mall);
     phase();
     // out^T (rows p, columns q): the entering state's share.  The state is
     // rounded to bfloat16 for it where out is.
@@ -160,15 +205,20 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
 #pragma unroll
       for (int qt = 0; qt < QT; ++qt) y[pt][qt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (k.on) {
+      Frag<PARTS> cf[2][QT];
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) cf[0][qt] = load_rows<T>(Cs, SN, 16 * qt, 0);
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk) {
+        if (kk + 1 < NK) {
+#pragma unroll
+          for (int qt = 0; qt < QT; ++qt)
+            cf[(kk + 1) & 1][qt] = load_rows<T>(Cs, SN, 16 * qt, 32 * kk + 32);
+        }
         const Frag<PARTS> hf[2] = {acc_frag<PARTS>(h[2 * kk][0], h[2 * kk + 1][0]),
                                    acc_frag<PARTS>(h[2 * kk][1], h[2 * kk + 1][1])};
-        Frag<PARTS> cf[QT];
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) cf[qt] = load_rows<T>(Cs, SN, 16 * qt, 32 * kk);
-        mma(y, hf, cf);
         phase();
+        mma(y, hf, cf[kk & 1]);
       }
 #pragma unroll
       for (int qt = 0; qt < QT; ++qt) {
@@ -195,22 +245,31 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
           marks[pt] = take_out<T, Q>(Xs, SX, k.col + 16 * pt + lane_i());
       }
       const T* Ms = Mall + hh * Q * SM;
+      // (tile pair, 32-step): the first step reaches all rows, the second the last half
+      constexpr int STEPS = Q == 64 ? 3 : 1;
+      Frag<PARTS> xf[Q / 32][2], mf[2][2];
 #pragma unroll
-      for (int ks = 0; ks < Q / 32; ++ks) {
-        const Frag<PARTS> xf[2] = {load_cols<T>(Xs, SX, k.col, 32 * ks),
-                                   load_cols<T>(Xs, SX, k.col + 16, 32 * ks)};
+      for (int ks = 0; ks < Q / 32; ++ks)
 #pragma unroll
-        for (int qt = 2 * ks; qt < QT; qt += 2) {
-          const Frag<PARTS> mf[2] = {load_rows<T>(Ms, SM, 16 * qt, 32 * ks),
-                                     load_rows<T>(Ms, SM, 16 * qt + 16, 32 * ks)};
-          f32x4 yy[2][2] = {{y[0][qt], y[0][qt + 1]}, {y[1][qt], y[1][qt + 1]}};
-          mma(yy, xf, mf);
-          y[0][qt] = yy[0][0];
-          y[0][qt + 1] = yy[0][1];
-          y[1][qt] = yy[1][0];
-          y[1][qt + 1] = yy[1][1];
-          phase();
-        }
+        for (int pt = 0; pt < 2; ++pt)
+          xf[ks][pt] = load_cols<T>(Xs, SX, k.col + 16 * pt, 32 * ks);
+      auto load_m = [&](int i, Frag<PARTS> (&f)[2]) {
+        const int qt = i == 0 ? 0 : 2, ks = i == 2 ? 1 : 0;
+        f[0] = load_rows<T>(Ms, SM, 16 * qt, 32 * ks);
+        f[1] = load_rows<T>(Ms, SM, 16 * qt + 16, 32 * ks);
+      };
+      load_m(0, mf[0]);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int qt = i == 0 ? 0 : 2, ks = i == 2 ? 1 : 0;
+        if (i + 1 < STEPS) load_m(i + 1, mf[(i + 1) & 1]);
+        phase();
+        f32x4 yy[2][2] = {{y[0][qt], y[0][qt + 1]}, {y[1][qt], y[1][qt + 1]}};
+        mma(yy, xf[ks], mf[i & 1]);
+        y[0][qt] = yy[0][0];
+        y[0][qt + 1] = yy[0][1];
+        y[1][qt] = yy[1][0];
+        y[1][qt + 1] = yy[1][1];
       }
       if (odd) {
 #pragma unroll
