@@ -51,11 +51,22 @@ struct HeadsBwdParams : HeadsParams {
   float* dD;             // nullable
   float* dbias;          // nullable
   float* dh0;            // nullable
+  int splits;            // blocks that share the heads of a chunk
   // workspace
-  float* states;         // (batch, H, L) times one padded state
-  float* dB_part;        // (batch, L, H, N)
-  float* dC_part;        // (batch, L, H, N)
-  float* head_part;      // (batch, H, 3): dA, dD, dbias
+  float* h_chunk;        // (batch, chunks, H, slices) states at the chunks' starts,
+  float* g_chunk;        // adjoints behind their ends: from zero within a segment
+  float* h_pre;          // (batch, chunks, H): weight in them of what enters the segment
+  float* g_pre;
+  float* h_seg;          // (batch, H, slices, nseg): the same of the segments
+  float* g_seg;
+  float* h_dec;
+  float* g_dec;
+  float* F;              // (batch, H, blocks of 64 channels, L): gradient of the log decay
+  float* W;              // and of the inputs' weight
+  float* dB_part;        // (splits, batch, L, G, N)
+  float* dC_part;
+  float* ud_part;        // (batch, chunks, H, blocks of 64 channels): sum of u dout
+  float* head_part;      // (batch, chunks, H, 3): dA, dD, dbias
 };
 
 struct HeadsStepParams : HeadsParams {

@@ -78,7 +78,8 @@ mscan::HeadsParams common(const mamba_heads_shape* s, const void* u, const void*
   p.softplus = s->delta_softplus != 0; p.zoh = s->disc == MAMBA_DISC_ZOH;
   const int es = esize(s->dtype);
   p.vec = rows16(u, p.u.batch, p.u.token, p.P, es) && rows16(B, p.B.batch, p.B.token, p.N, es) &&
-          rows16(C, p.C.batch, p.C.token, p.N, es);
+          rows16(C, p.C.batch, p.C.token, p.N, es) &&
+          s->heads * s->headdim <= (1 << 21);   // a chunk of dense rows within 2^31 bytes too
   return p;
 }
 
@@ -155,7 +156,7 @@ bool fwd_layout(const mamba_heads_shape* s, FwdLayout* l) {
   const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
   if (chunks > kGridLim / (s->batch * s->heads)) return false;
   l->scal = 0;
-  l->state = up256((size_t)(s->batch * s->heads * chunks) * (size_t)(24 * q + 16));
+  l->state = up256((size_t)(s->batch * s->heads * chunks) * (size_t)(28 * q + 16));
   l->dec = l->state + up256(n * (size_t)(kSlice * pad_state(s)) * 4);
   l->total = l->dec + up256(n * 4);
   return true;
@@ -163,17 +164,48 @@ bool fwd_layout(const mamba_heads_shape* s, FwdLayout* l) {
 
 // Workspace of the backward: see HeadsBwdParams.
 struct BwdLayout {
-  size_t states, dB_part, dC_part, head_part, total;
+  int nseg, splits;
+  int64_t seg_len;
+  size_t scal, h_chunk, g_chunk, h_pre, g_pre, h_seg, g_seg, h_dec, g_dec, F, W, dB_part, dC_part,
+      ud_part, head_part, total;
 };
 
 bool bwd_layout(const mamba_heads_shape* s, BwdLayout* l) {
-  const size_t th = (size_t)(s->batch * s->heads) * (size_t)s->seqlen;
+  split(s, &l->nseg, &l->seg_len);
+  const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
+  const Map m = map_of(s);
+  const int64_t bh = s->batch * s->heads, cols = bh * m.slices;
+  const int64_t cb = (s->headdim + 63) / 64, units = s->heads / s->groups * cb;
+  if (chunks > kGridLim / 16 / cols || cols > kGridLim / 32 / l->nseg) return false;
+  // enough blocks to fill the chip, each with at least one head
+  const int64_t blocks = s->batch * s->groups * chunks;
+  int64_t sp = (kTargetBlocks + blocks - 1) / blocks;
+  if (sp > units) sp = units;
+  l->splits = (int)sp;
+  const size_t state = (size_t)(kSlice * pad_state(s)) * 4;
+  const size_t bch = (size_t)(bh * chunks), bl = (size_t)s->batch * (size_t)s->seqlen;
+  const size_t gn = (size_t)(s->groups * s->dstate);
   size_t at = 0;
-  const size_t n = s->dstate <= 16 ? 16 : s->dstate <= 64 ? 64 : s->dstate <= 128 ? 128 : 256;
-  l->states = at; at += up256(th * 128 * n * 4);
-  l->dB_part = at; at += up256(th * (size_t)s->dstate * 4);
-  l->dC_part = at; at += up256(th * (size_t)s->dstate * 4);
-  l->head_part = at; at += up256((size_t)(s->batch * s->heads) * 12);
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += up256(bytes);
+    return o;
+  };
+  l->scal = take(bch * (size_t)(28 * q + 16));
+  l->h_chunk = take(bch * (size_t)m.slices * state);
+  l->g_chunk = take(bch * (size_t)m.slices * state);
+  l->h_pre = take(bch * 4);
+  l->g_pre = take(bch * 4);
+  l->h_seg = take((size_t)cols * (size_t)l->nseg * state);
+  l->g_seg = take((size_t)cols * (size_t)l->nseg * state);
+  l->h_dec = take((size_t)cols * (size_t)l->nseg * 4);
+  l->g_dec = take((size_t)cols * (size_t)l->nseg * 4);
+  l->F = take(bl * (size_t)(s->heads * cb) * 4);
+  l->W = take(bl * (size_t)(s->heads * cb) * 4);
+  l->dB_part = take((size_t)sp * bl * gn * 4);
+  l->dC_part = take((size_t)sp * bl * gn * 4);
+  l->ud_part = take(bch * (size_t)cb * 4);
+  l->head_part = take(bch * 12);
   l->total = at;
   return true;
 }
@@ -306,10 +338,15 @@ mamba_status mamba_heads_scan_bwd(const mamba_heads_shape* shape, const void* u,
   p.dC = dC; p.dD = dD; p.dbias = ddelta_bias; p.dh0 = dh0;
   p.vec = p.vec && aligned(dout, 16) && aligned(du, 16) && aligned(dB, 16) && aligned(dC, 16);
   char* ws = static_cast<char*>(workspace);
-  p.states = reinterpret_cast<float*>(ws + l.states);
-  p.dB_part = reinterpret_cast<float*>(ws + l.dB_part);
-  p.dC_part = reinterpret_cast<float*>(ws + l.dC_part);
-  p.head_part = reinterpret_cast<float*>(ws + l.head_part);
+  auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  const Map m = map_of(shape);
+  p.slices = (int)m.slices; p.hpw = (int)m.hpw; p.hblocks = (int)m.hblocks;
+  p.nseg = l.nseg; p.seg_len = l.seg_len; p.splits = l.splits;
+  p.scal = ws + l.scal;
+  p.h_chunk = f(l.h_chunk); p.g_chunk = f(l.g_chunk); p.h_pre = f(l.h_pre); p.g_pre = f(l.g_pre);
+  p.h_seg = f(l.h_seg); p.g_seg = f(l.g_seg); p.h_dec = f(l.h_dec); p.g_dec = f(l.g_dec);
+  p.F = f(l.F); p.W = f(l.W); p.dB_part = f(l.dB_part); p.dC_part = f(l.dC_part);
+  p.ud_part = f(l.ud_part); p.head_part = f(l.head_part);
   return hip_status(mscan::dispatch_heads_bwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,
                                               as_stream(stream)));
 }

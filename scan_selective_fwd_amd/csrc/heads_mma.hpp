@@ -325,6 +325,7 @@ struct alignas(16) Scal {
   float c[Q];    // its weight in the state at the chunk's end (0 if a flag follows)
   float e[Q];    // weight of the entering state in the token's row (0 after a flag)
   float g[Q];    // w times the decay to the end of the token's tile of 16
+  float r[Q];    // decay to the chunk's end (0 if a flag follows)
   int id[Q];     // flags up to the token
   float dec;     // weight of the entering state in the state at the chunk's end
   int flags;     // flags in the chunk
@@ -383,10 +384,19 @@ __device__ __forceinline__ uint64_t take_out(T* tile, int stride, int c) {
 
 // Whether a mark reaches token q: one of its sequence up to it.
 template <int Q>
-__device__ __forceinline__ bool marked(uint64_t marks, const int* id, int q) {
+__device__ __forceinline__ bool marked_upto(uint64_t marks, const int* id, int q) {
 #pragma unroll 1
   for (int s = 0; s <= q; ++s)
     if ((marks >> s & 1) != 0 && id[s] == id[q]) return true;
+  return false;
+}
+
+// Whether a mark is in sequence number n.
+template <int Q>
+__device__ __forceinline__ bool marked(uint64_t marks, const int* id, int n) {
+#pragma unroll 1
+  for (int s = 0; s < Q; ++s)
+    if ((marks >> s & 1) != 0 && id[s] == n) return true;
   return false;
 }
 
@@ -407,14 +417,14 @@ __device__ __forceinline__ bool tile_odd(const T* tile, int stride, int c0) {
   return __any(r[0] != 0.0f);
 }
 
-// Clears the non-finite values of the rows that a flag keeps from the chunk's
-// end.  Called by the whole block.
+// Clears the non-finite values of the rows of other sequences than number
+// `stays`.  Called by the whole block.
 template <typename T, int Q, int NP>
-__device__ __forceinline__ void clear_kept(T* tile, int stride, const int* id) {
+__device__ __forceinline__ void clear_kept(T* tile, int stride, const int* id, int stays) {
 #pragma unroll 1
   for (int i = threadIdx.x; i < Q * NP; i += 256) {
     T* x = tile + (i / NP) * stride + i % NP;
-    if (id[i / NP] != id[Q - 1] && not_finite(Elem<T>::load1(x))) *x = T(0);
+    if (id[i / NP] != stays && not_finite(Elem<T>::load1(x))) *x = T(0);
   }
 }
 
@@ -525,31 +535,33 @@ __device__ __forceinline__ void add_outer(f32x4 (&h)[2 * NK][2], const T* keys, 
   }
 }
 
-// A chunk's step of a slice's state: h <- dec h + sum_t c_t B_t u_t^T.
+// A chunk's step of a slice's state: h <- dec h + sum_t c_t keys_t vals_t^T.
 template <typename T, int NK>
-__device__ __forceinline__ void step_state(f32x4 (&h)[2 * NK][2], const Scal<Mx<T>::Q>& sc,
-                                           const T* Bs, int bstride, const T* Xs, int xstride,
-                                           int col, const uint64_t (&marks)[2]) {
+__device__ __forceinline__ void step_state(f32x4 (&h)[2 * NK][2], float dec, const float* c,
+                                           const T* keys, int kstride, const T* vals, int vstride,
+                                           int col) {
   constexpr int Q = Mx<T>::Q;
-  decay_state<NK>(h, sc.dec);
+  decay_state<NK>(h, dec);
 #pragma unroll
   for (int ks = 0; ks < Q / 32; ++ks) {
     Frag<3> x[2];
 #pragma unroll
     for (int pt = 0; pt < 2; ++pt) {
-      Cols<T> c;
-      c.load(Xs, xstride, col + 16 * pt, 32 * ks);
-      x[pt] = c.weighted(sc.c, 32 * ks);
+      Cols<T> v;
+      v.load(vals, vstride, col + 16 * pt, 32 * ks);
+      x[pt] = v.weighted(c, 32 * ks);
     }
-    add_outer<T, NK>(h, Bs, bstride, 32 * ks, x);
+    add_outer<T, NK>(h, keys, kstride, 32 * ks, x);
   }
+}
+
+// A lane's column of tile column pt becomes NaN.
+template <int NK>
+__device__ __forceinline__ void spoil(f32x4 (&h)[2 * NK][2], int pt) {
 #pragma unroll
-  for (int pt = 0; pt < 2; ++pt)
-    if (marks[pt] != 0 && marked<Q>(marks[pt], sc.id, Q - 1))
+  for (int nt = 0; nt < 2 * NK; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < 2 * NK; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[nt][pt][j] = __builtin_nanf("");
+    for (int j = 0; j < 4; ++j) (pt == 0 ? h[nt][0] : h[nt][1])[j] = __builtin_nanf("");
 }
 
 // Which heads and columns a block and its waves take.
@@ -565,8 +577,8 @@ struct Place {
 
 // Blocks in order: batch row, segment, group, head block; contiguous ranges
 // share an XCD, whose L2 then serves B and C to all heads of a row.
-__device__ __forceinline__ Place place_of(const HeadsParams& p, int nseg) {
-  int id = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+__device__ __forceinline__ Place place_at(const HeadsParams& p, int nseg, int block) {
+  int id = xcd_remap(block, (int)(p.batch * nseg * p.G * p.hblocks));
   Place k;
   const int per = p.H / p.G, hb = id % p.hblocks;
   id /= p.hblocks;
@@ -586,6 +598,10 @@ __device__ __forceinline__ Place place_of(const HeadsParams& p, int nseg) {
   k.ncol = p.P - k.c0;
   k.col = wave * kSlice;
   return k;
+}
+
+__device__ __forceinline__ Place place_of(const HeadsParams& p, int nseg) {
+  return place_at(p, nseg, (int)blockIdx.x);
 }
 
 __device__ __forceinline__ int64_t slice_slot(const HeadsParams& p, const Place& k, int n, int i) {

@@ -42,6 +42,7 @@ __global__ __launch_bounds__(256) void heads_scal_kernel(const HeadsParams p) {
     o->c[l] = n == n_end ? fast_exp2(end - S) * w : 0.0f;
     o->e[l] = n == 0 ? fast_exp2(S) : 0.0f;
     o->g[l] = fast_exp2(tile_end - S) * w;
+    o->r[l] = n == n_end ? fast_exp2(end - S) : 0.0f;
     o->id[l] = n;
   }
   if (l == 0) {

@@ -1,230 +1,814 @@
-// The backward of the multi-head scan, one token after the other: per (batch row, head)
-//   h_t = a_t h_{t-1} + w_t u_t B_t^T,   out_t = h_t C_t + D u_t,   h (P, N)
-// with the adjoint g_t = dout_t C_t^T + a_{t+1} g_{t+1},
-//   du = w g B + D dout,  dB = w g^T u,  dC = h^T dout,  dw = u . (g B),
-//   dlog_t = <a_t g_t, h_{t-1}>, the gradient of the log decay.
-// The backward keeps every state of its forward sweep in the workspace.
+// Backward of the multi-head scan.  With the adjoint g of the state (what
+// everything after a step makes of it),
+//   du_s = w_s g_s B_s + D dout_s,  dB_s = w_s g_s^T u_s,  dC_q = h_q^T dout_q,
+//   dw_s = u_s . (g_s B_s),  F_t = <a_t g_t, h_{t-1}>, the gradient of the log decay.
+// Within a chunk, with the entering state h, the adjoint g behind its end, the
+// decays L_qs = e^{S_q - S_s}, r_s to the chunk's end and e_q from its start:
+//   g_s B_s  = sum_{q >= s} L_qs (C_q . B_s) dout_q + r_s g B_s
+//   g_s^T u_s = sum_{q >= s} L_qs (dout_q . u_s) C_q + r_s g^T u_s
+//   dC_q     = sum_{s <= q} L_qs w_s (dout_q . u_s) B_s + e_q h^T dout_q
+//   F_t = dec <g, h> + sum_{q >= t} e_q dout_q . (h C_q) + sum_{s < t} w_s r_s u_s . (g B_s)
+//         + sum_{s < t <= q} K_qs,   K_qs = L_qs w_s (C_q . B_s)(dout_q . u_s):
+// the paths through step t from before the chunk or inside it to inside or
+// behind it.  Summing whole rows and taking differences over the sequence
+// instead would lose F to cancellation.
 //
-// A block of 256 threads holds one head's state in registers: thread (row
-// pi, quarter nq) holds rows pi and pi + 64, states nq, nq + 4, ...
-#include "heads_common.hpp"
+// Passes: the chunks' scalars; the states at every chunk's start and the
+// adjoints behind every chunk's end (segments of the sequence in parallel from
+// zero, then their carries); the chunks, all independent, each block looping
+// over heads with dB and dC in registers; sums over the blocks' shares.
+#include "heads_mma.hpp"
 
 namespace mscan {
 
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float elem(const Rows& r, int64_t b, int64_t t, int64_t i) {
-  return Elem<T>::load1(static_cast<const T*>(r.p) + b * r.batch + t * r.token + i);
-}
+template <typename T, int NK>
+struct BwdTiles {
+  static constexpr int Q = Mx<T>::Q, PAD = Mx<T>::PAD, NP = 32 * NK, QT = Q / 16;
+  static constexpr int PARTS = Mx<T>::PARTS;
+  static constexpr int SX = 64 + PAD, SN = NP + PAD, SM = Q + PAD;
+  static constexpr int NTW = NK >= 2 ? NK / 2 : 1;   // state tiles a wave holds of dB, dC
+  // region that holds a head's states, then its two matrices
+  static constexpr int ZSTATE = 64 * SN, ZM = 2 * Q * SM;
+  static constexpr int Z = ZSTATE > ZM ? ZSTATE : ZM;
+};
 
-// Sums over the block's 64 rows of v[j] (state n = nq + 4 j): result in sh[n].
-template <int J>
-__device__ __forceinline__ void sum_rows(float (&v)[J], float (*sh)[4 * J]) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  __syncthreads();
+// ---------------------------------------------------------------------------
+// States at the chunks' starts (REV false: keys B, inputs u) or adjoints behind
+// their ends (REV true: keys C, inputs dout), from zero within a segment; pre:
+// the weight in them of the segment's entering state or adjoint.
+// ---------------------------------------------------------------------------
+template <typename T, int NK, bool VEC, bool REV>
+__device__ __forceinline__ void states_of(const HeadsBwdParams& p, int block, T* Xs, T* Ks,
+                                          Scal<Mx<T>::Q>* scal) {
+  using F = BwdTiles<T, NK>;
+  constexpr int Q = F::Q, NP = F::NP, SX = kCols + F::PAD, SN = F::SN;
+  const Place k = place_at(p, p.nseg, block);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t begin = (int64_t)k.seg * p.seg_len;
+  const int64_t end = k.seg + 1 == p.nseg ? p.L : begin + p.seg_len;
+  const int64_t ucol = (int64_t)k.h0 * p.P, ncols = (int64_t)k.g * p.N;
+  const int uwidth = (k.h0 + k.heads) * p.P, nwidth = (k.g + 1) * p.N;
+  const int sub = p.slices * kSlice, hh = wave / p.slices;
+  const int64_t chunks = (p.L + Q - 1) / Q;
+  const Rows vals = REV ? Rows{p.dout, p.L * p.H * p.P, (int64_t)p.H * p.P} : p.u;
+  const Rows keys = REV ? p.C : p.B;
+  f32x4 h[2 * NK][2];
+  fill<NK>(h, 0.0f);
+  float pre = 1.0f;
+  Stage<T, Q, kCols, VEC> sx;
+  Stage<T, Q, NP, VEC> sk;
+  ScalStage<Q> ss;
+  sx.init(vals, ucol, sub, p.P, p.P, k.heads);
+  sk.init(keys, ncols, NP, 0, p.N, 1);
+  auto fetch = [&](int64_t t) {
+    const int len = end - t < Q ? (int)(end - t) : Q;
+    ss.load(p.scal, (k.b * chunks + t / Q) * p.H + k.h0, k.heads);
+    sx.load(vals, k.b, t, len, ucol, p.P, uwidth);
+    sk.load(keys, k.b, t, len, ncols, 0, nwidth);
+  };
+  const int64_t n = (end - begin + Q - 1) / Q;
+  auto at = [&](int64_t i) { return begin + (REV ? n - 1 - i : i) * Q; };
+  fetch(at(0));
+  for (int64_t i = 0; i < n; ++i) {
+    sx.store(Xs, SX);
+    sk.store(Ks, SN);
+    ss.store(scal, k.heads);
+    __syncthreads();
+    if (i + 1 < n) fetch(at(i + 1));
+    const Scal<Q>& me = scal[k.on ? hh : 0];
+    if (scal[0].flags != 0) {
+      clear_kept<T, Q, NP>(Ks, SN, scal[0].id, REV ? 0 : scal[0].flags);
+      __syncthreads();
+    }
+    if (k.on) {
+      const int64_t c = (k.b * chunks + at(i) / Q) * p.H + k.h;
+      float* st = (REV ? p.g_chunk : p.h_chunk) + (c * p.slices + k.slice) * slice_floats<NK>();
+      store_frags<NK>(st, h);
+      if (k.slice == 0 && (threadIdx.x & 63) == 0) (REV ? p.g_pre : p.h_pre)[c] = pre;
+      uint64_t marks[2] = {0, 0};
+      if (tile_odd<T, Q>(Xs, SX, k.col)) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
+        for (int pt = 0; pt < 2; ++pt)
+          marks[pt] = take_out<T, Q>(Xs, SX, k.col + 16 * pt + lane_i());
+      }
+      step_state<T, NK>(h, me.dec, REV ? me.e : me.c, Ks, SN, Xs, SX, k.col);
 #pragma unroll
-    for (int off = 4; off < 64; off <<= 1) v[j] += __shfl_xor(v[j], off);
-    if (lane < 4) sh[wave][lane + 4 * j] = v[j];
+      for (int pt = 0; pt < 2; ++pt)
+        if (marks[pt] != 0 && marked<Q>(marks[pt], me.id, REV ? 0 : me.flags)) spoil<NK>(h, pt);
+      pre *= me.dec;
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  for (int n = threadIdx.x; n < 4 * J; n += 256)
-    sh[0][n] = (sh[0][n] + sh[1][n]) + (sh[2][n] + sh[3][n]);
-  __syncthreads();
+  if (!k.on) return;
+  const int64_t slot = slice_slot(p, k, p.nseg, k.seg);
+  store_frags<NK>((REV ? p.g_seg : p.h_seg) + slot * slice_floats<NK>(), h);
+  if ((threadIdx.x & 63) == 0) (REV ? p.g_dec : p.h_dec)[slot] = pre;
 }
 
-__device__ __forceinline__ float block_sum(float v, float* sh) {
+template <typename T, int NK, bool VEC>
+__global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_states_kernel(const HeadsBwdParams p) {
+  using F = BwdTiles<T, NK>;
+  __shared__ __align__(16) T Xs[F::Q * (kCols + F::PAD)];
+  __shared__ __align__(16) T Ks[F::Q * F::SN];
+  extern __shared__ __align__(16) char dyn[];
+  Scal<F::Q>* const scal = reinterpret_cast<Scal<F::Q>*>(dyn);
+  // both directions in one launch
+  const int half = gridDim.x / 2;
+  if ((int)blockIdx.x < half) states_of<T, NK, VEC, false>(p, (int)blockIdx.x, Xs, Ks, scal);
+  else states_of<T, NK, VEC, true>(p, (int)blockIdx.x - half, Xs, Ks, scal);
+}
+
+// What enters each segment, in place of what the one before left: states from
+// h0 on, or adjoints from the last state's gradient back, and dh0 behind them.
+template <int NK, bool REV>
+__device__ __forceinline__ void carry_of(const HeadsBwdParams& p, int64_t block) {
+  constexpr int PER = NK;
+  const int64_t id = block / PER;
+  const int e = (int)(block - id * PER) * 256 + threadIdx.x;
+  const int slice = (int)(id % p.slices);
+  const int64_t bh = id / p.slices;
+  const int nt = e >> 7, pt = (e >> 6) & 1, l = e & 63;
+  const int pp = slice * kSlice + 16 * pt + (l & 15), n = 16 * nt + 4 * (l >> 4);
+  const float* first = REV ? p.dlast : p.h0;
+  f32x4 h = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (first && pp < p.P)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < p.N) h[j] = first[(bh * p.P + pp) * p.N + n + j];
+  f32x4* st = reinterpret_cast<f32x4*>((REV ? p.g_seg : p.h_seg) + id * p.nseg * slice_floats<NK>()) + e;
+  const float* dec = (REV ? p.g_dec : p.h_dec) + id * p.nseg;
+  constexpr int64_t STEP = slice_floats<NK>() / 4;
+#pragma unroll 4
+  for (int i = 0; i < p.nseg; ++i) {
+    const int k = REV ? p.nseg - 1 - i : i;
+    const f32x4 s = st[k * STEP];
+    const float d = dec[k];
+    st[k * STEP] = h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = weigh(h[j], d) + s[j];
+  }
+  if (REV && p.dh0 && pp < p.P)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < p.N) p.dh0[(bh * p.P + pp) * p.N + n + j] = h[j];
+}
+
+template <int NK>
+__global__ __launch_bounds__(256) void heads_bwd_carry_kernel(const HeadsBwdParams p) {
+  const int half = gridDim.x / 2;
+  if ((int)blockIdx.x < half) carry_of<NK, false>(p, blockIdx.x);
+  else carry_of<NK, true>(p, (int64_t)blockIdx.x - half);
+}
+
+// ---------------------------------------------------------------------------
+// The chunks.
+// ---------------------------------------------------------------------------
+// Sums over the lanes of equal column (g = 0..3).
+__device__ __forceinline__ float sum_g(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+// Sums over the lanes of equal g (i = 0..15).
+__device__ __forceinline__ float sum_i(float v) {
+#pragma unroll
+  for (int off = 1; off < 16; off <<= 1) v += __shfl_xor(v, off);
+  return v;
+}
+__device__ __forceinline__ float sum_wave(float v) {
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return (sh[0] + sh[1]) + (sh[2] + sh[3]);
+  return v;
 }
 
-template <typename T, int J>
-__global__ __launch_bounds__(256) void heads_bwd_kernel(const HeadsBwdParams p) {
-  __shared__ float shn[4][4 * J];
-  __shared__ float sh4[4];
-  const int64_t b = blockIdx.x / p.H;
-  const int hd = (int)(blockIdx.x - b * p.H), g = hd / (p.H / p.G);
-  const int pi = threadIdx.x >> 2, nq = threadIdx.x & 3;
-  const uint8_t* rst = reset_row(p.reset, b, p.L);
-  const float A = p.A[hd], bias = p.bias ? p.bias[hd] : 0.0f, D = p.D ? p.D[hd] : 0.0f;
-  const int64_t s0 = (b * p.H + hd) * (int64_t)p.P * p.N;
-  // this thread's share of the state after each step, 2 J floats at a stride of 256
-  float* keep = p.states + (b * p.H + hd) * p.L * (512 * J) + threadIdx.x;
-  float h[2][J], v[J];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int pp = pi + 64 * i, n = nq + 4 * j;
-      h[i][j] = p.h0 && pp < p.P && n < p.N ? p.h0[s0 + (int64_t)pp * p.N + n] : 0.0f;
-    }
-  auto dyv = [&](int64_t t, int i) {
-    return pi + 64 * i < p.P
-               ? Elem<T>::load1(static_cast<const T*>(p.dout) +
-                                ((b * p.L + t) * p.H + hd) * p.P + pi + 64 * i)
-               : 0.0f;
-  };
-  auto uv = [&](int64_t t, int i) {
-    return pi + 64 * i < p.P ? elem<T>(p.u, b, t, (int64_t)hd * p.P + pi + 64 * i) : 0.0f;
-  };
-  // forward in time: the states, dC and z
-  for (int64_t t = 0; t < p.L; ++t) {
-    const Step q = make_step(elem<T>(p.delta, b, t, hd) + bias, A, p.softplus, p.zoh);
-    const float a = exp2f(q.lg);
-    const bool cut = rst && rst[t] != 0;
-    const float u[2] = {uv(t, 0), uv(t, 1)}, dy[2] = {dyv(t, 0), dyv(t, 1)};
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int n = nq + 4 * j;
-      const float Bn = n < p.N ? elem<T>(p.B, b, t, (int64_t)g * p.N + n) : 0.0f;
-      v[j] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        h[i][j] = __builtin_fmaf(u[i] * q.w, Bn, cut ? 0.0f : a * h[i][j]);
-        v[j] = __builtin_fmaf(h[i][j], dy[i], v[j]);
-        keep[t * (512 * J) + (i * J + j) * 256] = h[i][j];
-      }
-    }
-    sum_rows<J>(v, shn);
-    for (int n = threadIdx.x; n < p.N; n += 256)
-      p.dC_part[((b * p.L + t) * p.H + hd) * p.N + n] = shn[0][n];
+// Four consecutive elements of a tile as floats.
+template <typename T>
+__device__ __forceinline__ f32x4 four(const T* q) {
+  if constexpr (sizeof(T) == 2) {
+    const u32x2 u = *reinterpret_cast<const u32x2*>(q);
+    return f32x4{bf16_lo(u[0]), bf16_hi(u[0]), bf16_lo(u[1]), bf16_hi(u[1])};
+  } else {
+    return *reinterpret_cast<const f32x4*>(q);
   }
-  // backward in time: the adjoint
-  float gr[2][J];
+}
+template <typename T>
+__device__ __forceinline__ void put4(T* q, const f32x4& v) {
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<u32x2*>(q) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  else
+    *reinterpret_cast<f32x4*>(q) = v;
+}
+
+template <int Q>
+struct alignas(16) BwdSums {
+  float row[Q / 16][Q];   // by tile of s: sum over s < q of K_qs
+  float col[Q / 16][Q];   // by tile of q: sum over q > s of K_qs / w_s
+  float diag[Q];          // K_ss / w_s
+  float in[4][Q];         // by wave: u_s . (g B_s)
+  float out[4][Q];        // by wave: dout_q . (h C_q)
+  float gh[4], ud[4];     // by wave: <g, h>, sum of u dout
+};
+
+template <typename T, int NK, bool VEC>
+__global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_chunk_kernel(const HeadsBwdParams p) {
+  using F = BwdTiles<T, NK>;
+  constexpr int Q = F::Q, NP = F::NP, QT = F::QT, SX = F::SX, SN = F::SN, SM = F::SM;
+  constexpr int PARTS = F::PARTS, NTW = F::NTW;
+  __shared__ __align__(16) T Bs[Q * SN];
+  __shared__ __align__(16) T Cs[Q * SN];
+  __shared__ __align__(16) T Xs[Q * SX];
+  __shared__ __align__(16) T Ys[Q * SX];   // dout
+  __shared__ __align__(16) T Zs[F::Z];
+  __shared__ Scal<Q> sc[1];
+  __shared__ BwdSums<Q> sums;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, li = lane_i(), lg = 4 * lane_g();
+  const int64_t chunks = (p.L + Q - 1) / Q;
+  // blocks: split, chunk, group, batch row
+  int id = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+  const int split = id % p.splits;
+  id /= p.splits;
+  const int64_t chunk = id % chunks;
+  id /= (int)chunks;
+  const int grp = id % p.G;
+  const int64_t b = id / p.G;
+  const int64_t t0 = chunk * Q;
+  const int len = p.L - t0 < Q ? (int)(p.L - t0) : Q;
+  const int seg = (int)(t0 / p.seg_len);
+  const int per = p.H / p.G, CB = (p.P + 63) / 64;
+  const int units = per * CB;                      // (head, 64 columns)
+  const int u0 = (int)((int64_t)units * split / p.splits);
+  const int u1 = (int)((int64_t)units * (split + 1) / p.splits);
+  const Rows dy{p.dout, p.L * p.H * p.P, (int64_t)p.H * p.P};
+  const int64_t ncols = (int64_t)grp * p.N;
+
+  Stage<T, Q, 64, VEC> sx, sy;
+  ScalStage<Q> ss;
+  f32x4 g[2 * NK], h[2 * NK];
+  auto head_of = [&](int u) { return grp * per + u / CB; };
+  auto fetch = [&](int u) {
+    const int hd = head_of(u), c0 = (u % CB) * 64;
+    const int n = p.P - c0 < 64 ? p.P - c0 : 64;
+    const int64_t at = (int64_t)hd * p.P + c0;
+    ss.load(p.scal, (b * chunks + chunk) * p.H + hd, 1);
+    sx.init(p.u, at, 64, 0, n, 1);
+    sy.init(dy, at, 64, 0, n, 1);
+    sx.load(p.u, b, t0, len, at, 0, (int)at + n);
+    sy.load(dy, b, t0, len, at, 0, (int)at + n);
+  };
+  // A wave's 16 columns of a state: half of a slice.
+  auto slice_of = [&](int u) { return (u % CB) * 2 + (wave >> 1); };
+  auto load_half = [&](const float* st, f32x4 (&r)[2 * NK]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int nt = 0; nt < 2 * NK; ++nt)
+      r[nt] = *reinterpret_cast<const f32x4*>(st + frag_at<NK>(nt, wave & 1));
+  };
+  auto clear_half = [&](f32x4 (&r)[2 * NK]) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int pp = pi + 64 * i, n = nq + 4 * j;
-      gr[i][j] = p.dlast && pp < p.P && n < p.N ? p.dlast[s0 + (int64_t)pp * p.N + n] : 0.0f;
-    }
-  float dA = 0.0f, dD = 0.0f, dbias = 0.0f;
-  for (int64_t t = p.L - 1; t >= 0; --t) {
-    const float raw = elem<T>(p.delta, b, t, hd) + bias;
-    const Step q = make_step(raw, A, p.softplus, p.zoh);
-    const float a = exp2f(q.lg);
-    const bool cut = rst && rst[t] != 0;
-    const float u[2] = {uv(t, 0), uv(t, 1)}, dy[2] = {dyv(t, 0), dyv(t, 1)};
-    float gB[2] = {0.0f, 0.0f}, F = 0.0f;
+    for (int nt = 0; nt < 2 * NK; ++nt) r[nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  auto fetch_state = [&](const float* base, int u, f32x4 (&r)[2 * NK]) {
+    if (slice_of(u) < p.slices)
+      load_half(base + (((b * chunks + chunk) * p.H + head_of(u)) * p.slices + slice_of(u)) *
+                           slice_floats<NK>(), r);
+    else
+      clear_half(r);
+  };
+  // adds the segment's entering state or adjoint
+  auto add_entering = [&](const float* base, float pre, int u, f32x4 (&r)[2 * NK]) {
+    if (pre != 0.0f && slice_of(u) < p.slices) {
+      const float* st = base + (((b * p.H + head_of(u)) * p.slices + slice_of(u)) * (int64_t)p.nseg + seg) *
+                                   slice_floats<NK>();
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int n = nq + 4 * j;
-      const float Bn = n < p.N ? elem<T>(p.B, b, t, (int64_t)g * p.N + n) : 0.0f;
-      const float Cn = n < p.N ? elem<T>(p.C, b, t, (int64_t)g * p.N + n) : 0.0f;
-      v[j] = 0.0f;
+      for (int nt = 0; nt < 2 * NK; ++nt) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(st + frag_at<NK>(nt, wave & 1));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        gr[i][j] = __builtin_fmaf(dy[i], Cn, gr[i][j]);
-        gB[i] = __builtin_fmaf(gr[i][j], Bn, gB[i]);
-        v[j] = __builtin_fmaf(gr[i][j], u[i] * q.w, v[j]);
-        gr[i][j] = cut ? 0.0f : a * gr[i][j];
-        const int pp = pi + 64 * i;
-        const float before =
-            t > 0 ? keep[(t - 1) * (512 * J) + (i * J + j) * 256]
-                  : (p.h0 && pp < p.P && n < p.N ? p.h0[s0 + (int64_t)pp * p.N + n] : 0.0f);
-        F = __builtin_fmaf(gr[i][j], before, F);
+        for (int j = 0; j < 4; ++j) r[nt][j] = __builtin_fmaf(pre, x[j], r[nt][j]);
       }
     }
-    F = block_sum(F, sh4);
-    float W = 0.0f, ud = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      gB[i] += __shfl_xor(gB[i], 1);
-      gB[i] += __shfl_xor(gB[i], 2);
-      const int pp = pi + 64 * i;
-      if (nq == 0) {
-        W = __builtin_fmaf(gB[i], u[i], W);
-        ud = __builtin_fmaf(u[i], dy[i], ud);
-        if (pp < p.P)
-          Elem<T>::store1(static_cast<T*>(p.du) + ((b * p.L + t) * p.H + hd) * p.P + pp,
-                          __builtin_fmaf(D, dy[i], gB[i] * q.w));
-      }
-    }
-    W = block_sum(W, sh4);
-    ud = block_sum(ud, sh4);
-    sum_rows<J>(v, shn);
-    for (int n = threadIdx.x; n < p.N; n += 256)
-      p.dB_part[((b * p.L + t) * p.H + hd) * p.N + n] = shn[0][n];
-    float by_dt, by_A;
-    step_weight_grad(q.dt, A, p.zoh, by_dt, by_A);
-    const float ddt = (A * F + W * by_dt) * q.draw;
-    dA += q.dt * F + W * by_A;
-    dD += ud;
-    dbias += ddt;
-    if (threadIdx.x == 0)
-      Elem<T>::store1(static_cast<T*>(p.ddelta) + (b * p.L + t) * p.H + hd, ddt);
+  };
+  const bool enters = seg > 0 || p.h0 != nullptr;
+  const bool enters_back = seg + 1 < p.nseg || p.dlast != nullptr;
+
+  {
+    Stage<T, Q, NP, VEC> sb, sk;
+    sb.init(p.B, ncols, NP, 0, p.N, 1);
+    sk.init(p.C, ncols, NP, 0, p.N, 1);
+    sb.load(p.B, b, t0, len, ncols, 0, (grp + 1) * p.N);
+    sk.load(p.C, b, t0, len, ncols, 0, (grp + 1) * p.N);
+    fetch(u0);
+    sb.store(Bs, SN);
+    sk.store(Cs, SN);
   }
-  if (p.dh0)
+  fetch_state(p.g_chunk, u0, g);
+  fetch_state(p.h_chunk, u0, h);
+  __syncthreads();
+
+  // C_q . B_s (rows q, columns s): the diagonal tile of the wave and up to two
+  // below it, the same for all heads
+  constexpr int OFF = QT == 4 ? 2 : 1;
+  int qt[1 + OFF], st[1 + OFF];
+  bool on[1 + OFF];
+  on[0] = wave < QT;
+  qt[0] = st[0] = on[0] ? wave : 0;
+  if constexpr (QT == 4) {
+    qt[1] = wave < 3 ? 3 : 1;
+    st[1] = wave < 3 ? wave : 0;
+    on[1] = true;
+    qt[2] = 2;
+    st[2] = wave & 1;
+    on[2] = wave < 2;
+  } else {
+    qt[1] = 1;
+    st[1] = 0;
+    on[1] = wave == 2;
+  }
+  f32x4 cb[1 + OFF][1][1];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int i = 0; i <= OFF; ++i) cb[i][0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int pp = pi + 64 * i, n = nq + 4 * j;
-        if (pp < p.P && n < p.N) p.dh0[s0 + (int64_t)pp * p.N + n] = gr[i][j];
+  for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+    for (int i = 0; i <= OFF; ++i) {
+      const Frag<PARTS> cf[1] = {load_rows<T>(Cs, SN, 16 * qt[i], 32 * kk)};
+      const Frag<PARTS> bf[1] = {load_rows<T>(Bs, SN, 16 * st[i], 32 * kk)};
+      mma(cb[i], cf, bf);
+    }
+
+  // dB, dC (rows n, columns tokens) of the wave's state tiles, all heads
+  const bool has_n = wave * NTW < 2 * NK;
+  const int n0 = has_n ? 16 * wave * NTW : 0;
+  f32x4 dB[NTW][QT], dC[NTW][QT];
+#pragma unroll
+  for (int i = 0; i < NTW; ++i)
+#pragma unroll
+    for (int j = 0; j < QT; ++j) dB[i][j] = dC[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const int64_t row = (int64_t)p.H * p.P;
+  for (int u = u0; u < u1; ++u) {
+    const int hd = head_of(u), c0 = (u % CB) * 64;
+    const float D = p.D ? p.D[hd] : 0.0f;
+    sx.store(Xs, SX);
+    sy.store(Ys, SX);
+    ss.store(sc, 1);
+    __syncthreads();
+    if (u + 1 < u1) fetch(u + 1);
+    const bool flagged = sc->flags != 0;
+    const int64_t cu = (b * chunks + chunk) * p.H + hd;
+    if (enters_back) add_entering(p.g_seg, p.g_pre[cu], u, g);
+    if (enters) add_entering(p.h_seg, p.h_pre[cu], u, h);
+
+    // <g, h>; g rounded to the stored type for dB, rows p
+    float gh = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < 2 * NK; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) gh = __builtin_fmaf(g[nt][j], h[nt][j], gh);
+      put4<T>(Zs + (16 * wave + li) * SN + 16 * nt + lg, g[nt]);
+    }
+    gh = sum_wave(gh);
+    // (g B_s)^T (rows p, columns s)
+    f32x4 du[1][QT];
+#pragma unroll
+    for (int s = 0; s < QT; ++s) du[0][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk) {
+      const Frag<3> gf[1] = {acc_frag<3>(g[2 * kk], g[2 * kk + 1])};
+      Frag<PARTS> bf[QT];
+#pragma unroll
+      for (int s = 0; s < QT; ++s) bf[s] = load_rows<T>(Bs, SN, 16 * s, 32 * kk);
+      mma(du, gf, bf);
+    }
+    float ud = 0.0f;
+#pragma unroll
+    for (int s = 0; s < QT; ++s) {
+      const f32x4 x = four<T>(Xs + (16 * s + li) * SX + 16 * wave + lg);
+      const f32x4 y = four<T>(Ys + (16 * s + li) * SX + 16 * wave + lg);
+      float v = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v = __builtin_fmaf(x[j], du[0][s][j], v);
+        ud = __builtin_fmaf(x[j], y[j], ud);
       }
-  if (threadIdx.x == 0) {
-    float* hp = p.head_part + (b * p.H + hd) * 3;
-    hp[0] = dA;
-    hp[1] = dD;
-    hp[2] = dbias;
+      v = sum_g(v);
+      if (lane < 16) sums.in[wave][16 * s + li] = v;
+      const float r = sc->r[16 * s + li];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) du[0][s][j] *= r;
+    }
+    ud = sum_wave(ud);
+    if (lane == 0) {
+      sums.gh[wave] = gh;
+      sums.ud[wave] = ud;
+    }
+    // dout_q . u_s, and from it K's sums and the two matrices of the chunk
+    f32x4 lg_[1 + OFF], lr[1 + OFF];
+    {
+      f32x4 a[1 + OFF][1][1];
+#pragma unroll
+      for (int i = 0; i <= OFF; ++i) a[i][0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i <= OFF; ++i) {
+          const Frag<PARTS> yf[1] = {load_rows<T>(Ys, SX, 16 * qt[i], 32 * kk)};
+          const Frag<PARTS> xf[1] = {load_rows<T>(Xs, SX, 16 * st[i], 32 * kk)};
+          mma(a[i], yf, xf);
+        }
+#pragma unroll
+      for (int i = 0; i <= OFF; ++i) {
+        const int s = 16 * st[i] + li, q = 16 * qt[i] + lg;
+        const float Ss = sc->S[s], ws = sc->w[s];
+        const f32x4 Sq = *reinterpret_cast<const f32x4*>(sc->S + q);
+        float colsum = 0.0f, dg = 0.0f;
+        f32x4 k;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = q + j >= s && (!flagged || sc->id[q + j] == sc->id[s]);
+          const float L = in ? fast_exp2(Sq[j] - Ss) : 0.0f;
+          const float G = cb[i][0][0][j], R = a[i][0][0][j];
+          lg_[i][j] = in ? G * L : 0.0f;
+          lr[i][j] = in ? R * L * ws : 0.0f;
+          const float kn = in ? G * R * L : 0.0f;
+          if (q + j == s) dg = kn;
+          else colsum += kn;
+          k[j] = q + j == s ? 0.0f : kn * ws;
+        }
+        colsum = sum_g(colsum);
+        if (i == 0) dg = sum_g(dg);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = sum_i(k[j]);
+        if (on[i]) {
+          if (lane < 16) {
+            sums.col[qt[i]][s] = colsum;
+            if (i == 0) sums.diag[s] = dg;
+          }
+          if (li == 0) *reinterpret_cast<f32x4*>(&sums.row[st[i]][q]) = k;
+        }
+      }
+    }
+    __syncthreads();
+    // dB from behind the chunk: g^T u_s (rows n, columns s), weighted by token
+    auto inter = [&](const T* tile, const float* f1, const float* f2, f32x4 (&acc)[NTW][QT]) {
+      f32x4 t[NTW][QT];
+#pragma unroll
+      for (int i = 0; i < NTW; ++i)
+#pragma unroll
+        for (int j = 0; j < QT; ++j) t[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        Frag<PARTS> zf[NTW], xf[QT];
+#pragma unroll
+        for (int i = 0; i < NTW; ++i) zf[i] = load_cols<T>(Zs, SN, n0 + 16 * i, 32 * kk);
+#pragma unroll
+        for (int j = 0; j < QT; ++j) xf[j] = load_rows<T>(tile, SX, 16 * j, 32 * kk);
+        mma(t, zf, xf);
+      }
+#pragma unroll
+      for (int j = 0; j < QT; ++j) {
+        const float f = f1[16 * j + li] * (f2 ? f2[16 * j + li] : 1.0f);
+#pragma unroll
+        for (int i = 0; i < NTW; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(f, t[i][j][e], acc[i][j][e]);
+      }
+    };
+    if (has_n) inter(Xs, sc->c, nullptr, dB);
+    // the next head's adjoint takes this one's registers
+    if (u + 1 < u1) fetch_state(p.g_chunk, u + 1, g);
+    // (h C_q)^T (rows p, columns q)
+    {
+      f32x4 y[1][QT];
+#pragma unroll
+      for (int q = 0; q < QT; ++q) y[0][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk) {
+        const Frag<3> hf[1] = {acc_frag<3>(h[2 * kk], h[2 * kk + 1])};
+        Frag<PARTS> cf[QT];
+#pragma unroll
+        for (int q = 0; q < QT; ++q) cf[q] = load_rows<T>(Cs, SN, 16 * q, 32 * kk);
+        mma(y, hf, cf);
+      }
+#pragma unroll
+      for (int q = 0; q < QT; ++q) {
+        const f32x4 d = four<T>(Ys + (16 * q + li) * SX + 16 * wave + lg);
+        float v = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v = __builtin_fmaf(d[j], y[0][q][j], v);
+        v = sum_g(v);
+        if (lane < 16) sums.out[wave][16 * q + li] = v;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < 2 * NK; ++nt)
+      put4<T>(Zs + (16 * wave + li) * SN + 16 * nt + lg, h[nt]);
+    if (u + 1 < u1) fetch_state(p.h_chunk, u + 1, h);
+    __syncthreads();
+    if (has_n) inter(Ys, sc->e, nullptr, dC);
+    __syncthreads();
+    // the chunk's matrices, rows s, columns q; the tiles beside the diagonal
+    // that a 32-step also reads are zero
+    T* const M1 = Zs;
+    T* const M2 = Zs + Q * SM;
+    // M1 in two parts: du weighs heads of very different steps, and a matrix
+    // rounded once shows in the heads' larger terms.  u's tile is done with.
+    T* const M1b = Xs;
+    static_assert(SX >= SM || Q < 64, "the second part fits u's tile");
+#pragma unroll
+    for (int i = 0; i <= OFF; ++i)
+      if (on[i]) {
+        const int o = (16 * st[i] + li) * SM + 16 * qt[i] + lg;
+        put4<T>(M1 + o, lg_[i]);
+        if constexpr (PARTS == 1) put4<T>(M1b + o, lg_[i] - four<T>(M1 + o));
+        put4<T>(M2 + o, lr[i]);
+      }
+    if (wave >= 4 - QT / 2) {
+      const int z = wave - (4 - QT / 2);           // tiles (q, s) = (2 z, 2 z + 1)
+      const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      put4<T>(M1 + (32 * z + 16 + li) * SM + 32 * z + lg, zero);
+      if constexpr (PARTS == 1) put4<T>(M1b + (32 * z + 16 + li) * SM + 32 * z + lg, zero);
+      put4<T>(M2 + (32 * z + 16 + li) * SM + 32 * z + lg, zero);
+    }
+    __syncthreads();
+    // du within the chunk
+#pragma unroll
+    for (int ks = 0; ks < Q / 32; ++ks) {
+      const Frag<PARTS> yf[1] = {load_cols<T>(Ys, SX, 16 * wave, 32 * ks)};
+#pragma unroll
+      for (int s = 0; s < 2 * ks + 2; s += 2) {
+        f32x4 d[1][2] = {{du[0][s], du[0][s + 1]}};
+        if constexpr (PARTS == 1) {
+          Frag<2> mf[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mf[i].v[0] = load_rows<T>(M1, SM, 16 * s + 16 * i, 32 * ks).v[0];
+            mf[i].v[1] = load_rows<T>(M1b, SM, 16 * s + 16 * i, 32 * ks).v[0];
+          }
+          mma(d, yf, mf);
+        } else {
+          const Frag<PARTS> mf[2] = {load_rows<T>(M1, SM, 16 * s, 32 * ks),
+                                     load_rows<T>(M1, SM, 16 * s + 16, 32 * ks)};
+          mma(d, yf, mf);
+        }
+        du[0][s] = d[0][0];
+        du[0][s + 1] = d[0][1];
+      }
+    }
+    // dB (from C, rows q of M2) and dC (from B, columns of M2) within the chunk
+    if (has_n) {
+#pragma unroll
+      for (int ks = 0; ks < Q / 32; ++ks) {
+        Frag<PARTS> cf[NTW], bf[NTW];
+#pragma unroll
+        for (int i = 0; i < NTW; ++i) {
+          cf[i] = load_cols<T>(Cs, SN, n0 + 16 * i, 32 * ks);
+          bf[i] = load_cols<T>(Bs, SN, n0 + 16 * i, 32 * ks);
+        }
+#pragma unroll
+        for (int s = 0; s < 2 * ks + 2; ++s) {
+          const Frag<PARTS> mf[1] = {load_rows<T>(M2, SM, 16 * s, 32 * ks)};
+          f32x4 d[NTW][1];
+#pragma unroll
+          for (int i = 0; i < NTW; ++i) d[i][0] = dB[i][s];
+          mma(d, cf, mf);
+#pragma unroll
+          for (int i = 0; i < NTW; ++i) dB[i][s] = d[i][0];
+        }
+#pragma unroll
+        for (int q = 2 * ks; q < QT; ++q) {
+          const Frag<PARTS> mf[1] = {load_cols<T>(M2, SM, 16 * q, 32 * ks)};
+          f32x4 d[NTW][1];
+#pragma unroll
+          for (int i = 0; i < NTW; ++i) d[i][0] = dC[i][q];
+          mma(d, bf, mf);
+#pragma unroll
+          for (int i = 0; i < NTW; ++i) dC[i][q] = d[i][0];
+        }
+      }
+    }
+    // du: four columns of a token a lane
+    {
+      const int c = 16 * wave + lg, ncol = p.P - c0;
+      T* const o0 = static_cast<T*>(p.du) + (b * p.L + t0) * row + (int64_t)hd * p.P + c0;
+      const uint32_t off = (uint32_t)opaque_int(
+          (int)((uint32_t)li * (uint32_t)(row * sizeof(T)) + (uint32_t)(c * sizeof(T))));
+#pragma unroll
+      for (int s = 0; s < QT; ++s) {
+        const f32x4 y = four<T>(Ys + (16 * s + li) * SX + c);
+        const float w = sc->w[16 * s + li];
+        f32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(D, y[j], w * du[0][s][j]);
+        if (16 * s + li < len && c < ncol) {
+          if constexpr (VEC) {
+            put4<T>(reinterpret_cast<T*>(reinterpret_cast<char*>(o0 + 16 * s * row) + off), v);
+          } else {
+            T* o = o0 + (16 * s + li) * row + c;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (c + j < ncol) Elem<T>::store1(o + j, v[j]);
+          }
+        }
+      }
+    }
+    // F and dw of every token
+    if (wave == 0) {
+      const int t = lane < Q ? lane : Q - 1;
+      const bool in = lane < Q;
+      float rowS = 0.0f, colS = 0.0f, zi = 0.0f, wi = 0.0f;
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        rowS += i <= t / 16 ? sums.row[i][t] : 0.0f;
+        colS += i >= t / 16 ? sums.col[i][t] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        zi += sums.out[i][t];
+        wi += sums.in[i][t];
+      }
+      const float w = sc->w[t];
+      zi = in ? weigh(zi, sc->e[t]) : 0.0f;
+      wi = weigh(wi, sc->r[t]);
+      const float dw = colS + sums.diag[t] + wi;
+      // by token: paths that start at it less those that end there, and those
+      // that leave the chunk from it
+      float x = in ? w * (colS + wi) - rowS : 0.0f, pre = x, suf = zi;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const float a = __shfl_up(pre, o), c = __shfl_down(suf, o);
+        if (lane >= o) pre += a;
+        if (lane + o < 64) suf += c;
+      }
+      pre -= x;
+      const float T4 =
+          weigh((sums.gh[0] + sums.gh[1]) + (sums.gh[2] + sums.gh[3]), sc->dec);
+      float Fv = T4 + suf + pre;
+      if (flagged && sc->id[t] != (t > 0 ? sc->id[t - 1] : 0)) Fv = 0.0f;
+      if (lane < len) {
+        const int64_t o = ((b * p.H + hd) * CB + u % CB) * p.L + t0 + lane;
+        p.F[o] = Fv;
+        p.W[o] = dw;
+      }
+      if (lane == 0)
+        p.ud_part[cu * CB + u % CB] =
+            (sums.ud[0] + sums.ud[1]) + (sums.ud[2] + sums.ud[3]);
+    }
+    __syncthreads();
+  }
+  // the block's shares of dB, dC
+  if (has_n) {
+    const int64_t o = (((int64_t)split * p.batch + b) * p.L + t0) * p.G * p.N + (int64_t)grp * p.N;
+#pragma unroll
+    for (int j = 0; j < QT; ++j) {
+      const int t = 16 * j + li;
+      if (t < len)
+#pragma unroll
+        for (int i = 0; i < NTW; ++i) {
+          const int n = n0 + 16 * i + lg;
+          const int64_t at = o + (int64_t)t * p.G * p.N + n;
+          if (p.N % 4 == 0) {
+            if (n < p.N) {
+              *reinterpret_cast<f32x4*>(p.dB_part + at) = dB[i][j];
+              *reinterpret_cast<f32x4*>(p.dC_part + at) = dC[i][j];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n + e < p.N) {
+                p.dB_part[at + e] = dB[i][j][e];
+                p.dC_part[at + e] = dC[i][j][e];
+              }
+          }
+        }
+    }
   }
 }
 
-// dB, dC: the heads of a group summed in order.
+// dB, dC: the splits' shares summed in order.
 template <typename T>
 __global__ __launch_bounds__(256) void heads_bwd_sum_kernel(const HeadsBwdParams p) {
+  const int64_t n = p.batch * p.L * p.G * p.N;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = i / (p.G * p.N);
-  if (row >= p.batch * p.L) return;
-  const int gn = (int)(i - row * (p.G * p.N)), g = gn / p.N, n = gn - g * p.N;
-  const int per = p.H / p.G;
+  if (i >= n) return;
   float sB = 0.0f, sC = 0.0f;
-  for (int k = 0; k < per; ++k) {
-    const int64_t at = (row * p.H + g * per + k) * p.N + n;
-    sB += p.dB_part[at];
-    sC += p.dC_part[at];
+  for (int k = 0; k < p.splits; ++k) {
+    sB += p.dB_part[k * n + i];
+    sC += p.dC_part[k * n + i];
   }
   Elem<T>::store1(static_cast<T*>(p.dB) + i, sB);
   Elem<T>::store1(static_cast<T*>(p.dC) + i, sC);
 }
 
-__global__ __launch_bounds__(256) void heads_bwd_head_kernel(const HeadsBwdParams p) {
-  const int h = blockIdx.x * 256 + threadIdx.x;
-  if (h >= p.H) return;
-  float s[3] = {0.0f, 0.0f, 0.0f};
-  for (int64_t b = 0; b < p.batch; ++b)
-#pragma unroll
-    for (int k = 0; k < 3; ++k) s[k] += p.head_part[(b * p.H + h) * 3 + k];
-  p.dA[h] = s[0];
-  if (p.dD) p.dD[h] = s[1];
-  if (p.dbias) p.dbias[h] = s[2];
+// ddelta of every token from F and dw; a chunk's shares of dA, dD, dbias.  One
+// wave a (batch row, chunk, head).
+template <typename T>
+__global__ __launch_bounds__(256) void heads_bwd_delta_kernel(const HeadsBwdParams p) {
+  constexpr int Q = Mx<T>::Q;
+  const int64_t chunks = (p.L + Q - 1) / Q;
+  const int l = threadIdx.x & 63, CB = (p.P + 63) / 64;
+  const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= p.batch * chunks * p.H) return;
+  const int hd = (int)(id % p.H);
+  const int64_t bc = id / p.H, b = bc / chunks, t = (bc - b * chunks) * Q + l;
+  const bool in = l < Q && t < p.L;
+  float dA = 0.0f, dbias = 0.0f;
+  if (in) {
+    const float raw =
+        Elem<T>::load1(static_cast<const T*>(p.delta.p) + b * p.delta.batch + t * p.delta.token + hd) +
+        (p.bias ? p.bias[hd] : 0.0f);
+    const float A = p.A[hd];
+    const Step q = make_step(raw, A, p.softplus != 0, p.zoh != 0);
+    float by_dt, by_A, F = 0.0f, W = 0.0f;
+    step_weight_grad(q.dt, A, p.zoh != 0, by_dt, by_A);
+    for (int c = 0; c < CB; ++c) {
+      F += p.F[((b * p.H + hd) * CB + c) * p.L + t];
+      W += p.W[((b * p.H + hd) * CB + c) * p.L + t];
+    }
+    dbias = (A * F + W * by_dt) * q.draw;
+    dA = q.dt * F + W * by_A;
+    Elem<T>::store1(static_cast<T*>(p.ddelta) + (b * p.L + t) * p.H + hd, dbias);
+  }
+  dA = sum_wave(dA);
+  dbias = sum_wave(dbias);
+  if (l == 0) {
+    float ud = 0.0f;
+    for (int c = 0; c < CB; ++c) ud += p.ud_part[id * CB + c];
+    p.head_part[id * 3] = dA;
+    p.head_part[id * 3 + 1] = ud;
+    p.head_part[id * 3 + 2] = dbias;
+  }
 }
 
-template <typename T, int J>
+// dA, dD, dbias of a head: its chunks' shares, in a fixed order.
+__global__ __launch_bounds__(256) void heads_bwd_head_kernel(const HeadsBwdParams p, int64_t rows) {
+  __shared__ float red[4][3];
+  const int h = blockIdx.x;
+  float s[3] = {0.0f, 0.0f, 0.0f};
+  for (int64_t i = threadIdx.x; i < rows; i += 256)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s[k] += p.head_part[(i * p.H + h) * 3 + k];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    s[k] = sum_wave(s[k]);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][k] = s[k];
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s[k] = (red[0][k] + red[1][k]) + (red[2][k] + red[3][k]);
+    p.dA[h] = s[0];
+    if (p.dD) p.dD[h] = s[1];
+    if (p.dbias) p.dbias[h] = s[2];
+  }
+}
+
+template <typename T, int NK, bool VEC>
 hipError_t bwd_go(const HeadsBwdParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((heads_bwd_kernel<T, J>), dim3((unsigned)(p.batch * p.H)), dim3(256), 0, s, p);
-  hipError_t e = hipGetLastError();
+  constexpr int Q = Mx<T>::Q;
+  const int dtype = sizeof(T) == 4 ? 0 : 1;
+  hipError_t e = dispatch_heads_scal(p, dtype, s);
+  if (e != hipSuccess) return e;
+  const int64_t chunks = (p.L + Q - 1) / Q;
+  const int64_t seg_blocks = p.batch * p.G * p.hblocks * p.nseg;
+  const size_t lds = (size_t)p.hpw * sizeof(Scal<Q>);
+  hipLaunchKernelGGL((heads_states_kernel<T, NK, VEC>), dim3((unsigned)(2 * seg_blocks)), dim3(256),
+                     lds, s, p);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((heads_bwd_carry_kernel<NK>),
+                     dim3((unsigned)(2 * p.batch * p.H * p.slices * NK)), dim3(256), 0, s, p);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((heads_chunk_kernel<T, NK, VEC>),
+                     dim3((unsigned)(p.batch * p.G * chunks * p.splits)), dim3(256), 0, s, p);
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t n = p.batch * p.L * p.G * p.N;
   hipLaunchKernelGGL((heads_bwd_sum_kernel<T>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(heads_bwd_head_kernel, dim3((unsigned)((p.H + 255) / 256)), dim3(256), 0, s, p);
+  const int64_t waves = p.batch * chunks * p.H;
+  hipLaunchKernelGGL((heads_bwd_delta_kernel<T>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, p);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(heads_bwd_head_kernel, dim3((unsigned)p.H), dim3(256), 0, s, p,
+                     p.batch * chunks);
   return hipGetLastError();
+}
+
+template <typename T, int NK>
+hipError_t bwd_nk(const HeadsBwdParams& p, hipStream_t s) {
+  return p.vec ? bwd_go<T, NK, true>(p, s) : bwd_go<T, NK, false>(p, s);
 }
 
 template <typename T>
 hipError_t bwd_t(const HeadsBwdParams& p, hipStream_t s) {
-  if (p.N <= 16) return bwd_go<T, 4>(p, s);
-  if (p.N <= 64) return bwd_go<T, 16>(p, s);
-  if (p.N <= 128) return bwd_go<T, 32>(p, s);
-  return bwd_go<T, 64>(p, s);
+  if (p.N <= 32) return bwd_nk<T, 1>(p, s);
+  if (p.N <= 64) return bwd_nk<T, 2>(p, s);
+  if (p.N <= 128) return bwd_nk<T, 4>(p, s);
+  return bwd_nk<T, 8>(p, s);
 }
 
 }  // namespace

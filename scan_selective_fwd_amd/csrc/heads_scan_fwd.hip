@@ -232,7 +232,7 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
     }
     __syncthreads();
     if (flagged) {
-      clear_kept<T, Q, NP>(Bs, SN, scal[0].id);
+      clear_kept<T, Q, NP>(Bs, SN, scal[0].id, scal[0].flags);
       __syncthreads();
     }
     if (k.on) {
@@ -282,7 +282,7 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
                                (uint64_t)(uint32_t)__shfl((int)(uint32_t)(marks[pt] >> 32), from) << 32;
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt)
-              if (marked<Q>(m, me.id, 16 * qt + lane_i())) y[pt][qt][j] = __builtin_nanf("");
+              if (marked_upto<Q>(m, me.id, 16 * qt + lane_i())) y[pt][qt][j] = __builtin_nanf("");
           }
       }
       phase();
@@ -328,7 +328,10 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
         phase();
       }
       phase();
-      step_state<T, NK>(h, me, Bs, SN, Xs, SX, k.col, marks);
+      step_state<T, NK>(h, me.dec, me.c, Bs, SN, Xs, SX, k.col);
+#pragma unroll
+      for (int pt = 0; pt < 2; ++pt)
+        if (marks[pt] != 0 && marked<Q>(marks[pt], me.id, me.flags)) spoil<NK>(h, pt);
     }
     __syncthreads();
   }
@@ -374,7 +377,7 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const H
     if (t + Q < end) fetch(t + Q);
     const Scal<Q>& me = scal[k.on ? hh : 0];
     if (scal[0].flags != 0) {
-      clear_kept<T, Q, NP>(Bs, SN, scal[0].id);
+      clear_kept<T, Q, NP>(Bs, SN, scal[0].id, scal[0].flags);
       __syncthreads();
     }
     if (k.on) {
@@ -384,7 +387,10 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const H
         for (int pt = 0; pt < 2; ++pt)
           marks[pt] = take_out<T, Q>(Xs, SX, k.col + 16 * pt + lane_i());
       }
-      step_state<T, NK>(h, me, Bs, SN, Xs, SX, k.col, marks);
+      step_state<T, NK>(h, me.dec, me.c, Bs, SN, Xs, SX, k.col);
+#pragma unroll
+      for (int pt = 0; pt < 2; ++pt)
+        if (marks[pt] != 0 && marked<Q>(marks[pt], me.id, me.flags)) spoil<NK>(h, pt);
       dec *= me.dec;
     }
     __syncthreads();
