@@ -122,6 +122,9 @@ int64_t pad_state(const mamba_heads_shape* s) {
 // least kMinChunks chunks.
 constexpr int64_t kTargetBlocks = 512;
 constexpr int64_t kMinChunks = 4;
+// Blocks that the backward's chunks are to bring, over batch rows, groups,
+// chunks and shares of the heads.
+constexpr int64_t kChunkBlocks = 512;
 
 void split(const mamba_heads_shape* s, int* nseg, int64_t* seg_len) {
   const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
@@ -179,7 +182,7 @@ bool bwd_layout(const mamba_heads_shape* s, BwdLayout* l) {
   if (chunks > kGridLim / 16 / cols || cols > kGridLim / 32 / l->nseg) return false;
   // enough blocks to fill the chip, each with at least one head
   const int64_t blocks = s->batch * s->groups * chunks;
-  int64_t sp = (kTargetBlocks + blocks - 1) / blocks;
+  int64_t sp = (kChunkBlocks + blocks - 1) / blocks;
   if (sp > units) sp = units;
   l->splits = (int)sp;
   const size_t state = (size_t)(kSlice * pad_state(s)) * 4;

@@ -118,6 +118,9 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[R][C], const Frag<NA> (&a)[R],
     }
 }
 
+// A thread's place among the 256 that stage a tile together.
+__device__ __forceinline__ int tid256() { return (int)(threadIdx.x & 255); }
+
 // Keeps the scheduler from moving one phase's loads into another, where they
 // would only hold registers.
 __device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
@@ -125,11 +128,24 @@ __device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
 __device__ __forceinline__ int lane_i() { return threadIdx.x & 15; }
 __device__ __forceinline__ int lane_g() { return (threadIdx.x >> 4) & 3; }
 
+// A lane's place in a fragment.  lane_fresh() hides it from the optimizer, so
+// that addresses made from it are formed again where they are used instead of
+// being kept, and spilled, across a loop.
+struct Lane {
+  int i, g;
+};
+__device__ __forceinline__ Lane lane_kept() { return {lane_i(), lane_g()}; }
+__device__ __forceinline__ Lane lane_fresh() {
+  const int t = opaque_int((int)threadIdx.x);
+  return {t & 15, (t >> 4) & 3};
+}
+
 // Fragment of a tile whose rows are the outer elements: rows o0 + i, inner
 // elements k0 + ...
 template <typename T>
-__device__ __forceinline__ Frag<Mx<T>::PARTS> load_rows(const T* tile, int stride, int o0, int k0) {
-  const T* q = tile + (o0 + lane_i()) * stride + k0 + 4 * lane_g();
+__device__ __forceinline__ Frag<Mx<T>::PARTS> load_rows(const T* tile, int stride, int o0, int k0,
+                                                           Lane ln = lane_kept()) {
+  const T* q = tile + ln.i * stride + 4 * ln.g + (o0 * stride + k0);
   if constexpr (sizeof(T) == 2) {
     const u32x2 a = *reinterpret_cast<const u32x2*>(q);
     const u32x2 b = *reinterpret_cast<const u32x2*>(q + 16);
@@ -144,10 +160,10 @@ __device__ __forceinline__ Frag<Mx<T>::PARTS> load_rows(const T* tile, int strid
 // The eight values of a fragment of a tile whose rows are the inner elements:
 // rows k0 + ..., outer element o0 + i.  bfloat16 tiles use the transposing LDS
 // read: a group of 16 lanes reads 4 rows of 16 elements and lane i gets column i.
-__device__ __forceinline__ bf16x8 load_cols_raw(const bf16_t* tile, int stride, int o0, int k0) {
+__device__ __forceinline__ bf16x8 load_cols_raw(const bf16_t* tile, int stride, int o0, int k0,
+                                                Lane ln = lane_kept()) {
   typedef s16x4 __attribute__((address_space(3))) * lds_ptr;
-  const int i = lane_i();
-  const bf16_t* q = tile + (k0 + 4 * lane_g() + (i >> 2)) * stride + o0 + 4 * (i & 3);
+  const bf16_t* q = tile + (4 * ln.g + (ln.i >> 2)) * stride + 4 * (ln.i & 3) + (k0 * stride + o0);
   const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)q);
   const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(q + 16 * stride));
   const u32x2 ua = __builtin_bit_cast(u32x2, a), ub = __builtin_bit_cast(u32x2, b);
@@ -155,8 +171,8 @@ __device__ __forceinline__ bf16x8 load_cols_raw(const bf16_t* tile, int stride, 
 }
 
 __device__ __forceinline__ void load_cols_f32(const float* tile, int stride, int o0, int k0,
-                                              float (&x)[8]) {
-  const float* q = tile + (k0 + 4 * lane_g()) * stride + o0 + lane_i();
+                                              float (&x)[8], Lane ln = lane_kept()) {
+  const float* q = tile + 4 * ln.g * stride + ln.i + (k0 * stride + o0);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     x[j] = q[j * stride];
@@ -165,14 +181,15 @@ __device__ __forceinline__ void load_cols_f32(const float* tile, int stride, int
 }
 
 template <typename T>
-__device__ __forceinline__ Frag<Mx<T>::PARTS> load_cols(const T* tile, int stride, int o0, int k0) {
+__device__ __forceinline__ Frag<Mx<T>::PARTS> load_cols(const T* tile, int stride, int o0, int k0,
+                                                           Lane ln = lane_kept()) {
   if constexpr (sizeof(T) == 2) {
     Frag<1> f;
-    f.v[0] = load_cols_raw(tile, stride, o0, k0);
+    f.v[0] = load_cols_raw(tile, stride, o0, k0, ln);
     return f;
   } else {
     float x[8];
-    load_cols_f32(tile, stride, o0, k0, x);
+    load_cols_f32(tile, stride, o0, k0, x, ln);
     return to_frag<3>(x);
   }
 }
@@ -266,13 +283,13 @@ struct Stage {
 
   __device__ __forceinline__ void init(const Rows& r, int64_t at, int sub, int run, int n,
                                        int parts) {
-    const int c = (threadIdx.x % PER_ROW) * V;
+    const int c = (tid256() % PER_ROW) * V;
     part = c / sub;
     cc = c - part * sub;
     n_ = part < parts && cc < n ? n - cc : 0;
     // a piece outside the row is out of the buffer's range
     off = n_ > 0 ? (uint32_t)((at + (int64_t)part * run + cc +
-                               (int64_t)(threadIdx.x / PER_ROW) * r.token) * (int)sizeof(T))
+                               (int64_t)(tid256() / PER_ROW) * r.token) * (int)sizeof(T))
                  : kOutside;
   }
   // Rows t0 .. t0 + len - 1 of batch row b.  VEC: rows start on 16 bytes, n is
@@ -289,7 +306,7 @@ struct Stage {
 #pragma unroll
       for (int k = 0; k < COUNT; ++k) v[k] = buf.load(o + (uint32_t)(k * STEP) * stride);
     } else {
-      const int row0 = threadIdx.x / PER_ROW;
+      const int row0 = tid256() / PER_ROW;
       const T* q0 = reinterpret_cast<const T*>(base) + at + (int64_t)part * run + cc;
 #pragma unroll
       for (int k = 0; k < COUNT; ++k) {
@@ -306,8 +323,37 @@ struct Stage {
       }
     }
   }
+  // The same of rows at `base` (the chunk's first, at the tile's first element)
+  // that are `stride` elements apart, n elements each.
+  __device__ __forceinline__ void load_at(const T* base, int64_t stride, int len, int n) {
+    const int t = opaque_int(tid256());
+    const int c = (t % PER_ROW) * V, row0 = t / PER_ROW;
+    if constexpr (VEC) {
+      const uint32_t bytes = (uint32_t)(stride * (int)sizeof(T));
+      const Buffer buf(base, (uint32_t)(len - 1) * bytes + (uint32_t)(n * (int)sizeof(T)));
+      const uint32_t o =
+          c < n ? (uint32_t)row0 * bytes + (uint32_t)(c * (int)sizeof(T)) : kOutside;
+#pragma unroll
+      for (int k = 0; k < COUNT; ++k) v[k] = buf.load(o + (uint32_t)(k * STEP) * bytes);
+    } else {
+#pragma unroll
+      for (int k = 0; k < COUNT; ++k) {
+        const int row = row0 + k * STEP;
+        const T* q = base + row * stride + c;
+        v[k] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if (c + e < n && row < len) {
+            if constexpr (sizeof(T) == 2) v[k][e / 2] |= (uint32_t)q[e] << (16 * (e & 1));
+            else v[k][e] = __builtin_bit_cast(uint32_t, q[e]);
+          }
+        }
+      }
+    }
+  }
   __device__ __forceinline__ void store(T* tile, int stride) const {
-    T* q = tile + (threadIdx.x / PER_ROW) * stride + (threadIdx.x % PER_ROW) * V;
+    const int t = opaque_int(tid256());
+    T* q = tile + (t / PER_ROW) * stride + (t % PER_ROW) * V;
 #pragma unroll
     for (int k = 0; k < COUNT; ++k) *reinterpret_cast<u32x4*>(q + k * STEP * stride) = v[k];
   }
@@ -333,23 +379,27 @@ struct alignas(16) Scal {
 };
 
 // The heads' scalars of one chunk, on their way from global memory to LDS.
-template <int Q>
+template <int Q, int HEADS = 4>
 struct ScalStage {
   static constexpr int PIECES = sizeof(Scal<Q>) / 16;
-  u32x4 v[2];
+  static constexpr int COUNT = (HEADS * PIECES + 255) / 256;   // two at most
+  u32x4 v[COUNT];
   __device__ __forceinline__ void load(const void* scal, int64_t at, int heads) {
     const Buffer buf(static_cast<const Scal<Q>*>(scal) + at, (uint32_t)(heads * PIECES * 16));
-    const uint32_t o = 16u * (uint32_t)opaque_int((int)threadIdx.x);
+    const uint32_t o = 16u * (uint32_t)opaque_int((int)tid256());
     v[0] = buf.load(o);
-    v[1] = u32x4{0, 0, 0, 0};
-    if (heads * PIECES > 256) v[1] = buf.load(o + 256 * 16);
+    if constexpr (COUNT == 2) {
+      v[1] = u32x4{0, 0, 0, 0};
+      if (heads * PIECES > 256) v[1] = buf.load(o + 256 * 16);
+    }
   }
   __device__ __forceinline__ void store(Scal<Q>* lds, int heads) const {
     u32x4* q = reinterpret_cast<u32x4*>(lds);
     const int n = heads * PIECES;
-    const int i = threadIdx.x;
+    const int i = tid256();
     if (i < n) q[i] = v[0];
-    if (i + 256 < n) q[i + 256] = v[1];
+    if constexpr (COUNT == 2)
+      if (i + 256 < n) q[i + 256] = v[1];
   }
 };
 
@@ -434,8 +484,8 @@ __device__ __forceinline__ void clear_kept(T* tile, int stride, const int* id, i
 // ---------------------------------------------------------------------------
 // Between kernels a slice's state is 32 NK kSlice floats in this order.
 template <int NK>
-__device__ __forceinline__ int64_t frag_at(int nt, int pt) {
-  return ((nt * 2 + pt) * 64 + (int)(threadIdx.x & 63)) * 4;
+__device__ __forceinline__ int frag_at(int nt, int pt, int lane = (int)(threadIdx.x & 63)) {
+  return lane * 4 + (nt * 2 + pt) * 256;
 }
 template <int NK>
 constexpr int64_t slice_floats() { return 32 * NK * kSlice; }

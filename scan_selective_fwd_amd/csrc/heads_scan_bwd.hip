@@ -28,7 +28,6 @@ struct BwdTiles {
   static constexpr int Q = Mx<T>::Q, PAD = Mx<T>::PAD, NP = 32 * NK, QT = Q / 16;
   static constexpr int PARTS = Mx<T>::PARTS;
   static constexpr int SX = 64 + PAD, SN = NP + PAD, SM = Q + PAD;
-  static constexpr int NTW = NK >= 2 ? NK / 2 : 1;   // state tiles a wave holds of dB, dC
   // region that holds a head's states, then its two matrices
   static constexpr int ZSTATE = 64 * SN, ZM = 2 * Q * SM;
   static constexpr int Z = ZSTATE > ZM ? ZSTATE : ZM;
@@ -165,20 +164,22 @@ __global__ __launch_bounds__(256) void heads_bwd_carry_kernel(const HeadsBwdPara
 // ---------------------------------------------------------------------------
 // The chunks.
 // ---------------------------------------------------------------------------
-// Sums over the lanes of equal column (g = 0..3).
+// Sums over the lanes of equal column (g = 0..3), in all of them.
 __device__ __forceinline__ float sum_g(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  v = rs_pair16(v, v);
+  return rs_pair32(v, v);
 }
-// Sums over the lanes of equal g (i = 0..15).
-__device__ __forceinline__ float sum_i(float v) {
-#pragma unroll
-  for (int off = 1; off < 16; off <<= 1) v += __shfl_xor(v, off);
-  return v;
-}
-__device__ __forceinline__ float sum_wave(float v) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off);
+// Sum over the wave, in the last lane of every 16.
+__device__ __forceinline__ float sum_wave(float v) { return sum_g(row_sum_to_last(v)); }
+
+// Inclusive sums over the lanes, in order.
+__device__ __forceinline__ float prefix(float v) {
+  v += dpp_mov<kRowShr1>(0.0f, v);
+  v += dpp_mov<kRowShr2>(0.0f, v);
+  v += dpp_mov<kRowShr4>(0.0f, v);
+  v += dpp_mov<kRowShr8>(0.0f, v);
+  v += dpp_mov<kRowBcast15, 0xA>(0.0f, v);
+  v += dpp_mov<kRowBcast31, 0xC>(0.0f, v);
   return v;
 }
 
@@ -210,26 +211,39 @@ struct alignas(16) BwdSums {
   float gh[4], ud[4];     // by wave: <g, h>, sum of u dout
 };
 
+// Heads a block takes side by side, 4 waves each: with two, a wave holds half
+// of dB and dC and keeps its registers; N > 128 leaves LDS for one.
+template <int NK>
+constexpr int kSide = NK == 8 ? 1 : 2;
+
 template <typename T, int NK, bool VEC>
-__global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_chunk_kernel(const HeadsBwdParams p) {
+__global__ __launch_bounds__(256 * kSide<NK>, NK == 8 ? 1 : 2)
+void heads_chunk_kernel(const HeadsBwdParams p) {
   using F = BwdTiles<T, NK>;
   constexpr int Q = F::Q, NP = F::NP, QT = F::QT, SX = F::SX, SN = F::SN, SM = F::SM;
-  constexpr int PARTS = F::PARTS, NTW = F::NTW;
+  constexpr int PARTS = F::PARTS, SIDE = kSide<NK>, WAVES = 4 * SIDE;
+  constexpr int NTW = 2 * NK > WAVES ? 2 * NK / WAVES : 1;   // tiles of dB, dC a wave
   __shared__ __align__(16) T Bs[Q * SN];
   __shared__ __align__(16) T Cs[Q * SN];
-  __shared__ __align__(16) T Xs[Q * SX];
-  __shared__ __align__(16) T Ys[Q * SX];   // dout
-  __shared__ __align__(16) T Zs[F::Z];
-  __shared__ Scal<Q> sc[1];
-  __shared__ BwdSums<Q> sums;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ __align__(16) T Xall[SIDE][Q * SX];
+  __shared__ __align__(16) T Yall[SIDE][Q * SX];   // dout
+  __shared__ __align__(16) T Zall[SIDE][F::Z];
+  __shared__ Scal<Q> scall[SIDE];
+  __shared__ BwdSums<Q> sums_all[SIDE];
+  const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int side = wave8 >> 2, wave = wave8 & 3;
   const int lane = threadIdx.x & 63, li = lane_i(), lg = 4 * lane_g();
+  T* const Xs = Xall[side];
+  T* const Ys = Yall[side];
+  T* const Zs = Zall[side];
+  Scal<Q>* const sc = &scall[side];
+  BwdSums<Q>& sums = sums_all[side];
   const int64_t chunks = (p.L + Q - 1) / Q;
   // blocks: split, chunk, group, batch row
   int id = xcd_remap((int)blockIdx.x, (int)gridDim.x);
   const int split = id % p.splits;
   id /= p.splits;
-  const int64_t chunk = id % chunks;
+  const int64_t chunk = id % (int)chunks;
   id /= (int)chunks;
   const int grp = id % p.G;
   const int64_t b = id / p.G;
@@ -240,49 +254,49 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_chunk_kernel(const
   const int units = per * CB;                      // (head, 64 columns)
   const int u0 = (int)((int64_t)units * split / p.splits);
   const int u1 = (int)((int64_t)units * (split + 1) / p.splits);
-  const Rows dy{p.dout, p.L * p.H * p.P, (int64_t)p.H * p.P};
-  const int64_t ncols = (int64_t)grp * p.N;
+  const int64_t row = (int64_t)p.H * p.P;
+  const T* const ub = static_cast<const T*>(p.u.p) + b * p.u.batch + t0 * p.u.token;
+  const T* const yb = static_cast<const T*>(p.dout) + (b * p.L + t0) * row;
+  const int64_t ch0 = (b * chunks + chunk) * p.H;
 
   Stage<T, Q, 64, VEC> sx, sy;
-  ScalStage<Q> ss;
+  ScalStage<Q, 1> ss;
   f32x4 g[2 * NK], h[2 * NK];
   auto head_of = [&](int u) { return grp * per + u / CB; };
+  // the side's unit, its last one again where there is none: nothing of that is kept
+  auto mine = [&](int u) { return u + side < u1 ? u + side : u1 - 1; };
   auto fetch = [&](int u) {
     const int hd = head_of(u), c0 = (u % CB) * 64;
     const int n = p.P - c0 < 64 ? p.P - c0 : 64;
     const int64_t at = (int64_t)hd * p.P + c0;
-    ss.load(p.scal, (b * chunks + chunk) * p.H + hd, 1);
-    sx.init(p.u, at, 64, 0, n, 1);
-    sy.init(dy, at, 64, 0, n, 1);
-    sx.load(p.u, b, t0, len, at, 0, (int)at + n);
-    sy.load(dy, b, t0, len, at, 0, (int)at + n);
+    ss.load(p.scal, ch0 + hd, 1);
+    sx.load_at(ub + at, p.u.token, len, n);
+    sy.load_at(yb + at, row, len, n);
   };
   // A wave's 16 columns of a state: half of a slice.
   auto slice_of = [&](int u) { return (u % CB) * 2 + (wave >> 1); };
-  auto load_half = [&](const float* st, f32x4 (&r)[2 * NK]) {
-#pragma unroll
-    for (int nt = 0; nt < 2 * NK; ++nt)
-      r[nt] = *reinterpret_cast<const f32x4*>(st + frag_at<NK>(nt, wave & 1));
-  };
-  auto clear_half = [&](f32x4 (&r)[2 * NK]) {
-#pragma unroll
-    for (int nt = 0; nt < 2 * NK; ++nt) r[nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  };
   auto fetch_state = [&](const float* base, int u, f32x4 (&r)[2 * NK]) {
-    if (slice_of(u) < p.slices)
-      load_half(base + (((b * chunks + chunk) * p.H + head_of(u)) * p.slices + slice_of(u)) *
-                           slice_floats<NK>(), r);
-    else
-      clear_half(r);
+    if (slice_of(u) < p.slices) {
+      const float* st = base + ((ch0 + head_of(u)) * p.slices + slice_of(u)) * slice_floats<NK>() +
+                        frag_at<NK>(0, wave & 1, 0);
+      const uint32_t o = 4u * (uint32_t)(opaque_int((int)threadIdx.x) & 63);
+#pragma unroll
+      for (int nt = 0; nt < 2 * NK; ++nt)
+        r[nt] = *reinterpret_cast<const f32x4*>(st + o + frag_at<NK>(nt, 0, 0));
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < 2 * NK; ++nt) r[nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
   };
   // adds the segment's entering state or adjoint
   auto add_entering = [&](const float* base, float pre, int u, f32x4 (&r)[2 * NK]) {
     if (pre != 0.0f && slice_of(u) < p.slices) {
       const float* st = base + (((b * p.H + head_of(u)) * p.slices + slice_of(u)) * (int64_t)p.nseg + seg) *
-                                   slice_floats<NK>();
+                                   slice_floats<NK>() + frag_at<NK>(0, wave & 1, 0);
+      const uint32_t o = 4u * (uint32_t)(opaque_int((int)threadIdx.x) & 63);
 #pragma unroll
       for (int nt = 0; nt < 2 * NK; ++nt) {
-        const f32x4 x = *reinterpret_cast<const f32x4*>(st + frag_at<NK>(nt, wave & 1));
+        const f32x4 x = *reinterpret_cast<const f32x4*>(st + o + frag_at<NK>(nt, 0, 0));
 #pragma unroll
         for (int j = 0; j < 4; ++j) r[nt][j] = __builtin_fmaf(pre, x[j], r[nt][j]);
       }
@@ -292,17 +306,21 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_chunk_kernel(const
   const bool enters_back = seg + 1 < p.nseg || p.dlast != nullptr;
 
   {
-    Stage<T, Q, NP, VEC> sb, sk;
-    sb.init(p.B, ncols, NP, 0, p.N, 1);
-    sk.init(p.C, ncols, NP, 0, p.N, 1);
-    sb.load(p.B, b, t0, len, ncols, 0, (grp + 1) * p.N);
-    sk.load(p.C, b, t0, len, ncols, 0, (grp + 1) * p.N);
-    fetch(u0);
-    sb.store(Bs, SN);
-    sk.store(Cs, SN);
+    Stage<T, Q, NP, VEC> sb;
+    const T* const kb = static_cast<const T*>(p.B.p) + b * p.B.batch + t0 * p.B.token + (int64_t)grp * p.N;
+    const T* const kc = static_cast<const T*>(p.C.p) + b * p.C.batch + t0 * p.C.token + (int64_t)grp * p.N;
+    if (SIDE == 1 || side == 0) {
+      sb.load_at(kb, p.B.token, len, p.N);
+      sb.store(Bs, SN);
+    }
+    if (SIDE == 1 || side == 1) {
+      sb.load_at(kc, p.C.token, len, p.N);
+      sb.store(Cs, SN);
+    }
   }
-  fetch_state(p.g_chunk, u0, g);
-  fetch_state(p.h_chunk, u0, h);
+  fetch(mine(u0));
+  fetch_state(p.g_chunk, mine(u0), g);
+  fetch_state(p.h_chunk, mine(u0), h);
   __syncthreads();
 
   // C_q . B_s (rows q, columns s): the diagonal tile of the wave and up to two
@@ -337,50 +355,105 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_chunk_kernel(const
     }
 
   // dB, dC (rows n, columns tokens) of the wave's state tiles, all heads
-  const bool has_n = wave * NTW < 2 * NK;
-  const int n0 = has_n ? 16 * wave * NTW : 0;
+  const bool has_n = wave8 * NTW < 2 * NK;
+  const int n0 = has_n ? 16 * wave8 * NTW : 0;
   f32x4 dB[NTW][QT], dC[NTW][QT];
 #pragma unroll
   for (int i = 0; i < NTW; ++i)
 #pragma unroll
     for (int j = 0; j < QT; ++j) dB[i][j] = dC[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const int64_t row = (int64_t)p.H * p.P;
-  for (int u = u0; u < u1; ++u) {
-    const int hd = head_of(u), c0 = (u % CB) * 64;
+  // acc += f Z^T tile^T of every side's unit (rows n, columns tokens), weighted
+  // by token: what reaches dB from behind the chunk, dC from before it
+  auto inter = [&](int u, const T (*tiles)[Q * SX], bool second, f32x4 (&acc)[NTW][QT]) {
+#pragma unroll
+    for (int x = 0; x < SIDE; ++x) {
+      if (u + x >= u1) break;
+      const Lane ln = lane_fresh();
+      const int li = ln.i;
+      f32x4 t[NTW][QT];
+#pragma unroll
+      for (int i = 0; i < NTW; ++i)
+#pragma unroll
+        for (int j = 0; j < QT; ++j) t[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      Frag<PARTS> zf[2][NTW], xf[2][QT];
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+        for (int i = 0; i < NTW; ++i) zf[kk][i] = load_cols<T>(Zall[x] + n0, SN, 16 * i, 32 * kk, ln);
+#pragma unroll
+        for (int j = 0; j < QT; ++j) xf[kk][j] = load_rows<T>(tiles[x], SX, 16 * j, 32 * kk, ln);
+      }
+      phase();
+      mma(t, zf[0], xf[0]);
+      mma(t, zf[1], xf[1]);
+#pragma unroll
+      for (int j = 0; j < QT; ++j) {
+        const float f = second ? scall[x].e[16 * j + li] : scall[x].c[16 * j + li];
+#pragma unroll
+        for (int i = 0; i < NTW; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(f, t[i][j][e], acc[i][j][e]);
+      }
+      phase();
+    }
+  };
+  // acc = state fragments (rows p) times tile rows (columns), three exact parts
+  auto project = [&](const f32x4 (&r)[2 * NK], const T* tile, f32x4 (&acc)[1][QT]) {
+#pragma unroll
+    for (int j = 0; j < QT; ++j) acc[0][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const Lane ln = lane_fresh();
+    Frag<PARTS> bf[2][QT];
+#pragma unroll
+    for (int j = 0; j < QT; ++j) bf[0][j] = load_rows<T>(tile, SN, 16 * j, 0, ln);
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk) {
+      if (kk + 1 < NK) {
+#pragma unroll
+        for (int j = 0; j < QT; ++j)
+          bf[(kk + 1) & 1][j] = load_rows<T>(tile, SN, 16 * j, 32 * kk + 32, ln);
+      }
+      const Frag<3> rf[1] = {acc_frag<3>(r[2 * kk], r[2 * kk + 1])};
+      phase();
+      mma(acc, rf, bf[kk & 1]);
+    }
+  };
+  auto put_state = [&](const f32x4 (&r)[2 * NK]) {
+    const Lane ln = lane_fresh();
+    T* const q = Zs + 16 * wave * SN + ln.i * SN + 4 * ln.g;
+#pragma unroll
+    for (int nt = 0; nt < 2 * NK; ++nt) put4<T>(q + 16 * nt, r[nt]);
+  };
+
+  for (int u = u0; u < u1; u += SIDE) {
+    const int mu = mine(u);
+    const bool live = u + side < u1;
+    const int hd = head_of(mu), c0 = (mu % CB) * 64;
     const float D = p.D ? p.D[hd] : 0.0f;
     sx.store(Xs, SX);
     sy.store(Ys, SX);
     ss.store(sc, 1);
     __syncthreads();
-    if (u + 1 < u1) fetch(u + 1);
-    const bool flagged = sc->flags != 0;
-    const int64_t cu = (b * chunks + chunk) * p.H + hd;
-    if (enters_back) add_entering(p.g_seg, p.g_pre[cu], u, g);
-    if (enters) add_entering(p.h_seg, p.h_pre[cu], u, h);
+    const bool more = u + SIDE < u1;
+    if (more) fetch(mine(u + SIDE));
+    const bool flagged = scall[0].flags != 0;       // flags are the batch row's
+    if (enters_back) add_entering(p.g_seg, p.g_pre[ch0 + hd], mu, g);
+    if (enters) add_entering(p.h_seg, p.h_pre[ch0 + hd], mu, h);
 
     // <g, h>; g rounded to the stored type for dB, rows p
     float gh = 0.0f;
 #pragma unroll
-    for (int nt = 0; nt < 2 * NK; ++nt) {
+    for (int nt = 0; nt < 2 * NK; ++nt)
 #pragma unroll
       for (int j = 0; j < 4; ++j) gh = __builtin_fmaf(g[nt][j], h[nt][j], gh);
-      put4<T>(Zs + (16 * wave + li) * SN + 16 * nt + lg, g[nt]);
-    }
-    gh = sum_wave(gh);
+    put_state(g);
     // (g B_s)^T (rows p, columns s)
     f32x4 du[1][QT];
-#pragma unroll
-    for (int s = 0; s < QT; ++s) du[0][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk) {
-      const Frag<3> gf[1] = {acc_frag<3>(g[2 * kk], g[2 * kk + 1])};
-      Frag<PARTS> bf[QT];
-#pragma unroll
-      for (int s = 0; s < QT; ++s) bf[s] = load_rows<T>(Bs, SN, 16 * s, 32 * kk);
-      mma(du, gf, bf);
-    }
+    project(g, Bs, du);
     float ud = 0.0f;
+    {
+    const Lane ln = lane_fresh();
+    const int li = ln.i, lg = 4 * ln.g, lane = li + 16 * ln.g;
 #pragma unroll
     for (int s = 0; s < QT; ++s) {
       const f32x4 x = four<T>(Xs + (16 * s + li) * SX + 16 * wave + lg);
@@ -397,99 +470,94 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_chunk_kernel(const
 #pragma unroll
       for (int j = 0; j < 4; ++j) du[0][s][j] *= r;
     }
+    gh = sum_wave(gh);
     ud = sum_wave(ud);
-    if (lane == 0) {
+    if (lane == 15) {
       sums.gh[wave] = gh;
       sums.ud[wave] = ud;
     }
+    }
+    phase();
     // dout_q . u_s, and from it K's sums and the two matrices of the chunk
-    f32x4 lg_[1 + OFF], lr[1 + OFF];
+    u32x2 lg_hi[1 + OFF], lg_lo[1 + OFF], lr_hi[1 + OFF];   // bfloat16, packed
+    f32x4 lg_f[1 + OFF], lr_f[1 + OFF];                     // float32
     {
+    const Lane ln = lane_fresh();
+    const int li = ln.i, lg = 4 * ln.g, lane = li + 16 * ln.g;
       f32x4 a[1 + OFF][1][1];
-#pragma unroll
-      for (int i = 0; i <= OFF; ++i) a[i][0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      Frag<PARTS> yf[2][1 + OFF][1], xf[2][1 + OFF][1];
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
         for (int i = 0; i <= OFF; ++i) {
-          const Frag<PARTS> yf[1] = {load_rows<T>(Ys, SX, 16 * qt[i], 32 * kk)};
-          const Frag<PARTS> xf[1] = {load_rows<T>(Xs, SX, 16 * st[i], 32 * kk)};
-          mma(a[i], yf, xf);
+          a[i][0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          yf[kk][i][0] = load_rows<T>(Ys + 16 * qt[i] * SX, SX, 0, 32 * kk, ln);
+          xf[kk][i][0] = load_rows<T>(Xs + 16 * st[i] * SX, SX, 0, 32 * kk, ln);
         }
+      phase();
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i <= OFF; ++i) mma(a[i], yf[kk][i], xf[kk][i]);
 #pragma unroll
       for (int i = 0; i <= OFF; ++i) {
         const int s = 16 * st[i] + li, q = 16 * qt[i] + lg;
         const float Ss = sc->S[s], ws = sc->w[s];
         const f32x4 Sq = *reinterpret_cast<const f32x4*>(sc->S + q);
+        f32x4 L;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) L[j] = i > 0 || q + j >= s ? fast_exp2(Sq[j] - Ss) : 0.0f;
+        if (flagged)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) L[j] = sc->id[q + j] == sc->id[s] ? L[j] : 0.0f;
         float colsum = 0.0f, dg = 0.0f;
-        f32x4 k;
+        f32x4 k, m1, m2;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bool in = q + j >= s && (!flagged || sc->id[q + j] == sc->id[s]);
-          const float L = in ? fast_exp2(Sq[j] - Ss) : 0.0f;
           const float G = cb[i][0][0][j], R = a[i][0][0][j];
-          lg_[i][j] = in ? G * L : 0.0f;
-          lr[i][j] = in ? R * L * ws : 0.0f;
-          const float kn = in ? G * R * L : 0.0f;
-          if (q + j == s) dg = kn;
-          else colsum += kn;
-          k[j] = q + j == s ? 0.0f : kn * ws;
+          const bool in = L[j] != 0.0f;
+          m1[j] = in ? G * L[j] : 0.0f;
+          m2[j] = in ? R * L[j] * ws : 0.0f;
+          const float kn = in ? m1[j] * R : 0.0f;
+          if (i == 0 && q + j == s) {
+            dg = kn;
+            k[j] = 0.0f;
+          } else {
+            colsum += kn;
+            k[j] = kn * ws;
+          }
         }
         colsum = sum_g(colsum);
         if (i == 0) dg = sum_g(dg);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) k[j] = sum_i(k[j]);
+        for (int j = 0; j < 4; ++j) k[j] = row_sum_to_last(k[j]);
         if (on[i]) {
           if (lane < 16) {
             sums.col[qt[i]][s] = colsum;
             if (i == 0) sums.diag[s] = dg;
           }
-          if (li == 0) *reinterpret_cast<f32x4*>(&sums.row[st[i]][q]) = k;
+          if (li == 15) *reinterpret_cast<f32x4*>(&sums.row[st[i]][q]) = k;
+        }
+        if constexpr (PARTS == 1) {
+          lg_hi[i] = u32x2{pack_bf16(m1[0], m1[1]), pack_bf16(m1[2], m1[3])};
+          lg_lo[i] = u32x2{pack_bf16(m1[0] - bf16_lo(lg_hi[i][0]), m1[1] - bf16_hi(lg_hi[i][0])),
+                           pack_bf16(m1[2] - bf16_lo(lg_hi[i][1]), m1[3] - bf16_hi(lg_hi[i][1]))};
+          lr_hi[i] = u32x2{pack_bf16(m2[0], m2[1]), pack_bf16(m2[2], m2[3])};
+        } else {
+          lg_f[i] = m1;
+          lr_f[i] = m2;
         }
       }
     }
     __syncthreads();
-    // dB from behind the chunk: g^T u_s (rows n, columns s), weighted by token
-    auto inter = [&](const T* tile, const float* f1, const float* f2, f32x4 (&acc)[NTW][QT]) {
-      f32x4 t[NTW][QT];
-#pragma unroll
-      for (int i = 0; i < NTW; ++i)
-#pragma unroll
-        for (int j = 0; j < QT; ++j) t[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        Frag<PARTS> zf[NTW], xf[QT];
-#pragma unroll
-        for (int i = 0; i < NTW; ++i) zf[i] = load_cols<T>(Zs, SN, n0 + 16 * i, 32 * kk);
-#pragma unroll
-        for (int j = 0; j < QT; ++j) xf[j] = load_rows<T>(tile, SX, 16 * j, 32 * kk);
-        mma(t, zf, xf);
-      }
-#pragma unroll
-      for (int j = 0; j < QT; ++j) {
-        const float f = f1[16 * j + li] * (f2 ? f2[16 * j + li] : 1.0f);
-#pragma unroll
-        for (int i = 0; i < NTW; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(f, t[i][j][e], acc[i][j][e]);
-      }
-    };
-    if (has_n) inter(Xs, sc->c, nullptr, dB);
-    // the next head's adjoint takes this one's registers
-    if (u + 1 < u1) fetch_state(p.g_chunk, u + 1, g);
+    if (has_n) inter(u, Xall, false, dB);
     // (h C_q)^T (rows p, columns q)
     {
       f32x4 y[1][QT];
-#pragma unroll
-      for (int q = 0; q < QT; ++q) y[0][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int kk = 0; kk < NK; ++kk) {
-        const Frag<3> hf[1] = {acc_frag<3>(h[2 * kk], h[2 * kk + 1])};
-        Frag<PARTS> cf[QT];
-#pragma unroll
-        for (int q = 0; q < QT; ++q) cf[q] = load_rows<T>(Cs, SN, 16 * q, 32 * kk);
-        mma(y, hf, cf);
-      }
+      project(h, Cs, y);
+    const Lane ln = lane_fresh();
+    const int li = ln.i, lg = 4 * ln.g, lane = li + 16 * ln.g;
+
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
         const f32x4 d = four<T>(Ys + (16 * q + li) * SX + 16 * wave + lg);
@@ -501,95 +569,121 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_chunk_kernel(const
       }
     }
     __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < 2 * NK; ++nt)
-      put4<T>(Zs + (16 * wave + li) * SN + 16 * nt + lg, h[nt]);
-    if (u + 1 < u1) fetch_state(p.h_chunk, u + 1, h);
+    put_state(h);
+    phase();
+    // the next heads' states take these registers
+    if (more) {
+      fetch_state(p.g_chunk, mine(u + SIDE), g);
+      fetch_state(p.h_chunk, mine(u + SIDE), h);
+    }
     __syncthreads();
-    if (has_n) inter(Ys, sc->e, nullptr, dC);
+    if (has_n) inter(u, Yall, true, dC);
     __syncthreads();
     // the chunk's matrices, rows s, columns q; the tiles beside the diagonal
-    // that a 32-step also reads are zero
+    // that a 32-step also reads are zero.  M1 in two parts: du weighs heads of
+    // very different steps, and a matrix rounded once shows in the larger terms.
     T* const M1 = Zs;
     T* const M2 = Zs + Q * SM;
-    // M1 in two parts: du weighs heads of very different steps, and a matrix
-    // rounded once shows in the heads' larger terms.  u's tile is done with.
-    T* const M1b = Xs;
-    static_assert(SX >= SM || Q < 64, "the second part fits u's tile");
+    T* const M1b = Xs;          // u's tile is done with
+    static_assert(SX >= SM, "the second part fits u's tile");
+    {
+    const Lane ln = lane_fresh();
+    const int li = ln.i, lg = 4 * ln.g, lane = li + 16 * ln.g;
 #pragma unroll
     for (int i = 0; i <= OFF; ++i)
       if (on[i]) {
         const int o = (16 * st[i] + li) * SM + 16 * qt[i] + lg;
-        put4<T>(M1 + o, lg_[i]);
-        if constexpr (PARTS == 1) put4<T>(M1b + o, lg_[i] - four<T>(M1 + o));
-        put4<T>(M2 + o, lr[i]);
+        if constexpr (PARTS == 1) {
+          *reinterpret_cast<u32x2*>(M1 + o) = lg_hi[i];
+          *reinterpret_cast<u32x2*>(M1b + o) = lg_lo[i];
+          *reinterpret_cast<u32x2*>(M2 + o) = lr_hi[i];
+        } else {
+          put4<T>(M1 + o, lg_f[i]);
+          put4<T>(M2 + o, lr_f[i]);
+        }
       }
     if (wave >= 4 - QT / 2) {
       const int z = wave - (4 - QT / 2);           // tiles (q, s) = (2 z, 2 z + 1)
+      const int o = (32 * z + 16 + li) * SM + 32 * z + lg;
       const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-      put4<T>(M1 + (32 * z + 16 + li) * SM + 32 * z + lg, zero);
-      if constexpr (PARTS == 1) put4<T>(M1b + (32 * z + 16 + li) * SM + 32 * z + lg, zero);
-      put4<T>(M2 + (32 * z + 16 + li) * SM + 32 * z + lg, zero);
+      put4<T>(M1 + o, zero);
+      if constexpr (PARTS == 1) put4<T>(M1b + o, zero);
+      put4<T>(M2 + o, zero);
+    }
     }
     __syncthreads();
     // du within the chunk
+    {
+    const Lane ln = lane_fresh();
 #pragma unroll
     for (int ks = 0; ks < Q / 32; ++ks) {
-      const Frag<PARTS> yf[1] = {load_cols<T>(Ys, SX, 16 * wave, 32 * ks)};
+      const Frag<PARTS> yf[1] = {load_cols<T>(Ys + 16 * wave, SX, 0, 32 * ks, ln)};
+      constexpr int MP = PARTS == 1 ? 2 : PARTS;
+      Frag<MP> mf[QT];
 #pragma unroll
-      for (int s = 0; s < 2 * ks + 2; s += 2) {
-        f32x4 d[1][2] = {{du[0][s], du[0][s + 1]}};
+      for (int s = 0; s < 2 * ks + 2; ++s) {
         if constexpr (PARTS == 1) {
-          Frag<2> mf[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mf[i].v[0] = load_rows<T>(M1, SM, 16 * s + 16 * i, 32 * ks).v[0];
-            mf[i].v[1] = load_rows<T>(M1b, SM, 16 * s + 16 * i, 32 * ks).v[0];
-          }
-          mma(d, yf, mf);
+          mf[s].v[0] = load_rows<T>(M1, SM, 16 * s, 32 * ks, ln).v[0];
+          mf[s].v[1] = load_rows<T>(M1b, SM, 16 * s, 32 * ks, ln).v[0];
         } else {
-          const Frag<PARTS> mf[2] = {load_rows<T>(M1, SM, 16 * s, 32 * ks),
-                                     load_rows<T>(M1, SM, 16 * s + 16, 32 * ks)};
-          mma(d, yf, mf);
+          mf[s] = load_rows<T>(M1, SM, 16 * s, 32 * ks, ln);
         }
-        du[0][s] = d[0][0];
-        du[0][s + 1] = d[0][1];
+      }
+      phase();
+      if (ks == 0) {
+        f32x4 (&d)[1][2] = *reinterpret_cast<f32x4(*)[1][2]>(&du[0][0]);
+        mma(d, yf, *reinterpret_cast<const Frag<MP>(*)[2]>(&mf[0]));
+      } else {
+        mma(du, yf, mf);
       }
     }
-    // dB (from C, rows q of M2) and dC (from B, columns of M2) within the chunk
+    }
+    // dB (from C, rows of M2) and dC (from B, columns of M2) within the chunk
     if (has_n) {
 #pragma unroll
-      for (int ks = 0; ks < Q / 32; ++ks) {
-        Frag<PARTS> cf[NTW], bf[NTW];
+      for (int x = 0; x < SIDE; ++x) {
+        if (u + x >= u1) break;
+        const T* const m2 = Zall[x] + Q * SM;
+        const Lane ln = lane_fresh();
 #pragma unroll
-        for (int i = 0; i < NTW; ++i) {
-          cf[i] = load_cols<T>(Cs, SN, n0 + 16 * i, 32 * ks);
-          bf[i] = load_cols<T>(Bs, SN, n0 + 16 * i, 32 * ks);
-        }
+        for (int ks = 0; ks < Q / 32; ++ks) {
+          Frag<PARTS> cf[NTW], bf[NTW], rf[QT], kf[QT];
 #pragma unroll
-        for (int s = 0; s < 2 * ks + 2; ++s) {
-          const Frag<PARTS> mf[1] = {load_rows<T>(M2, SM, 16 * s, 32 * ks)};
-          f32x4 d[NTW][1];
+          for (int i = 0; i < NTW; ++i) {
+            cf[i] = load_cols<T>(Cs + n0, SN, 16 * i, 32 * ks, ln);
+            bf[i] = load_cols<T>(Bs + n0, SN, 16 * i, 32 * ks, ln);
+          }
 #pragma unroll
-          for (int i = 0; i < NTW; ++i) d[i][0] = dB[i][s];
-          mma(d, cf, mf);
+          for (int s = 0; s < 2 * ks + 2; ++s) rf[s] = load_rows<T>(m2, SM, 16 * s, 32 * ks, ln);
 #pragma unroll
-          for (int i = 0; i < NTW; ++i) dB[i][s] = d[i][0];
-        }
+          for (int q = 2 * ks; q < QT; ++q) kf[q] = load_cols<T>(m2, SM, 16 * q, 32 * ks, ln);
+          phase();
 #pragma unroll
-        for (int q = 2 * ks; q < QT; ++q) {
-          const Frag<PARTS> mf[1] = {load_cols<T>(M2, SM, 16 * q, 32 * ks)};
-          f32x4 d[NTW][1];
+          for (int i = 0; i < NTW; ++i) {
 #pragma unroll
-          for (int i = 0; i < NTW; ++i) d[i][0] = dC[i][q];
-          mma(d, bf, mf);
-#pragma unroll
-          for (int i = 0; i < NTW; ++i) dC[i][q] = d[i][0];
+            for (int s = 0; s < QT; ++s) {
+              if (s < 2 * ks + 2) {
+                f32x4 d[1][1] = {{dB[i][s]}};
+                mma(d, *reinterpret_cast<const Frag<PARTS>(*)[1]>(&cf[i]),
+                    *reinterpret_cast<const Frag<PARTS>(*)[1]>(&rf[s]));
+                dB[i][s] = d[0][0];
+              }
+              if (s >= 2 * ks) {
+                f32x4 d[1][1] = {{dC[i][s]}};
+                mma(d, *reinterpret_cast<const Frag<PARTS>(*)[1]>(&bf[i]),
+                    *reinterpret_cast<const Frag<PARTS>(*)[1]>(&kf[s]));
+                dC[i][s] = d[0][0];
+              }
+            }
+          }
+          phase();
         }
       }
     }
     // du: four columns of a token a lane
-    {
+    if (live) {
+    const Lane ln = lane_fresh();
+    const int li = ln.i, lg = 4 * ln.g, lane = li + 16 * ln.g;
       const int c = 16 * wave + lg, ncol = p.P - c0;
       T* const o0 = static_cast<T*>(p.du) + (b * p.L + t0) * row + (int64_t)hd * p.P + c0;
       const uint32_t off = (uint32_t)opaque_int(
@@ -613,9 +707,11 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_chunk_kernel(const
         }
       }
     }
-    // F and dw of every token
-    if (wave == 0) {
-      const int t = lane < Q ? lane : Q - 1;
+    // F and dw of every token, one a lane
+    if (wave == 0 && live) {
+    const Lane ln = lane_fresh();
+    const int li = ln.i, lg = 4 * ln.g, lane = li + 16 * ln.g;
+      const int t = lane < Q ? lane : Q - 1, tr = Q - 1 - t;   // and from the end
       const bool in = lane < Q;
       float rowS = 0.0f, colS = 0.0f, zi = 0.0f, wi = 0.0f;
 #pragma unroll
@@ -625,34 +721,28 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_chunk_kernel(const
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        zi += sums.out[i][t];
+        zi += sums.out[i][tr];
         wi += sums.in[i][t];
       }
       const float w = sc->w[t];
-      zi = in ? weigh(zi, sc->e[t]) : 0.0f;
+      zi = in ? weigh(zi, sc->e[tr]) : 0.0f;
       wi = weigh(wi, sc->r[t]);
       const float dw = colS + sums.diag[t] + wi;
-      // by token: paths that start at it less those that end there, and those
-      // that leave the chunk from it
-      float x = in ? w * (colS + wi) - rowS : 0.0f, pre = x, suf = zi;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const float a = __shfl_up(pre, o), c = __shfl_down(suf, o);
-        if (lane >= o) pre += a;
-        if (lane + o < 64) suf += c;
-      }
-      pre -= x;
+      // paths that start at a token less those that end there, and those that
+      // leave the chunk from it, before t; those that enter it, from t on
+      const float x = in ? w * (colS + wi) - rowS : 0.0f;
+      const float pre = prefix(x) - x, suf = __shfl(prefix(zi), tr);
       const float T4 =
           weigh((sums.gh[0] + sums.gh[1]) + (sums.gh[2] + sums.gh[3]), sc->dec);
       float Fv = T4 + suf + pre;
       if (flagged && sc->id[t] != (t > 0 ? sc->id[t - 1] : 0)) Fv = 0.0f;
       if (lane < len) {
-        const int64_t o = ((b * p.H + hd) * CB + u % CB) * p.L + t0 + lane;
+        const int64_t o = ((b * p.H + hd) * CB + mu % CB) * p.L + t0 + lane;
         p.F[o] = Fv;
         p.W[o] = dw;
       }
       if (lane == 0)
-        p.ud_part[cu * CB + u % CB] =
+        p.ud_part[(ch0 + hd) * CB + mu % CB] =
             (sums.ud[0] + sums.ud[1]) + (sums.ud[2] + sums.ud[3]);
     }
     __syncthreads();
@@ -732,7 +822,7 @@ __global__ __launch_bounds__(256) void heads_bwd_delta_kernel(const HeadsBwdPara
   }
   dA = sum_wave(dA);
   dbias = sum_wave(dbias);
-  if (l == 0) {
+  if (l == 15) {
     float ud = 0.0f;
     for (int c = 0; c < CB; ++c) ud += p.ud_part[id * CB + c];
     p.head_part[id * 3] = dA;
@@ -752,7 +842,7 @@ __global__ __launch_bounds__(256) void heads_bwd_head_kernel(const HeadsBwdParam
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     s[k] = sum_wave(s[k]);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][k] = s[k];
+    if ((threadIdx.x & 63) == 15) red[threadIdx.x >> 6][k] = s[k];
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -782,7 +872,7 @@ hipError_t bwd_go(const HeadsBwdParams& p, hipStream_t s) {
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((heads_chunk_kernel<T, NK, VEC>),
-                     dim3((unsigned)(p.batch * p.G * chunks * p.splits)), dim3(256), 0, s, p);
+                     dim3((unsigned)(p.batch * p.G * chunks * p.splits)), dim3(256 * kSide<NK>), 0, s, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t n = p.batch * p.L * p.G * p.N;
