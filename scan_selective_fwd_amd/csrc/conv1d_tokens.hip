@@ -4,10 +4,11 @@
 // and its backward, dpre_t = dout_t silu'(pre_t):
 //   dx_s = sum_k w[k] dpre_{s+k},  dw[k] = sum_t dpre_t x_{t-k},  db = sum_t dpre_t.
 //
-// Channels are contiguous, so a lane owns 16 bytes of them and marches along a
-// run of tokens with the last three inputs (and, backwards, the four open
-// sums of dx) in registers: every row is read once by its run and the three
-// rows between runs twice.  Both kernels are bound by HBM.
+// Channels are contiguous, so a lane owns four of them and marches along a run
+// of tokens with the last three inputs (and, backwards, the open sums of dx) in
+// registers: every row is read once by its run and the three rows between runs
+// twice.  Rows are loaded ahead in groups and kept packed until used.  Both
+// kernels are bound by HBM.
 #include "heads_common.hpp"
 
 namespace mscan {
@@ -16,6 +17,7 @@ namespace {
 
 constexpr int kLags = 4;
 constexpr int kFwdRun = 16;   // tokens a lane takes in the forward
+constexpr int kAhead = 4;     // rows the backward loads ahead
 
 // Weights by lag: w4[k] multiplies x_{t-k}; lags past the width are zero.
 template <int V>
@@ -108,10 +110,11 @@ __global__ __launch_bounds__(256) void tokconv_fwd_kernel(const TokConvParams p)
   const int64_t n = p.L - t0 < kFwdRun ? p.L - t0 : kFwdRun;
   const int64_t x0 = b * p.x.batch + t0 * p.x.token + c;
   const int64_t o0 = (b * p.L + t0) * p.dim + c;
-  auto step = [&](int64_t j, const float (&x)[V]) {
+  auto step = [&](int64_t j, const Raw<T, V>& r) {
     if constexpr (RST)
       if (rst[t0 + j] != 0) clear<V>(h);
-    float pre[V];
+    float x[V], pre[V];
+    r.get(x);
     pre_act<V>(w4, cb, x, h, pre);
     push<V>(h, x);
 #pragma unroll
@@ -119,15 +122,15 @@ __global__ __launch_bounds__(256) void tokconv_fwd_kernel(const TokConvParams p)
     store_vec<T, V>(p.out, o0 + j * p.dim, pre);
   };
   if (n == kFwdRun) {
-    float x[kFwdRun][V];
+    Raw<T, V> x[kFwdRun];
 #pragma unroll
-    for (int j = 0; j < kFwdRun; ++j) load_vec<T, V>(p.x.p, x0 + j * p.x.token, x[j]);
+    for (int j = 0; j < kFwdRun; ++j) x[j].load(p.x.p, x0 + j * p.x.token);
 #pragma unroll
     for (int j = 0; j < kFwdRun; ++j) step(j, x[j]);
   } else {
     for (int64_t j = 0; j < n; ++j) {
-      float x[V];
-      load_vec<T, V>(p.x.p, x0 + j * p.x.token, x);
+      Raw<T, V> x;
+      x.load(p.x.p, x0 + j * p.x.token);
       step(j, x);
     }
   }
@@ -176,15 +179,13 @@ __global__ __launch_bounds__(256) void tokconv_bwd_kernel(const TokConvParams p)
       for (int k = 3; k >= 1; --k)
         if (t0 - k >= 0) age = rst[t0 - k] != 0 ? 0 : (age < 3 ? age + 1 : 3);
     const int64_t x0 = b * p.x.batch + c, o0 = b * p.L * p.dim + c;
-    for (int j = 0; j < kTokConvRun + 3; ++j) {
+    // one step: t = t0 + j, own ones below kTokConvRun
+    auto step = [&](int j, const Raw<T, V>& xr, const Raw<T, V>& gr) {
       const int64_t t = t0 + j;
-      const bool live = t < p.L;
       float x[V], g[V], pre[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = g[v] = 0.0f;
-      if (live) {
-        load_vec<T, V>(p.x.p, x0 + t * p.x.token, x);
-        load_vec<T, V>(p.dout, o0 + t * p.dim, g);
+      xr.get(x);
+      gr.get(g);
+      if (t < p.L) {
         if constexpr (RST) {
           if (rst[t] != 0) {
             clear<V>(h);
@@ -222,7 +223,35 @@ __global__ __launch_bounds__(256) void tokconv_bwd_kernel(const TokConvParams p)
       } else if (t0 == 0 && p.dwindow && s + p.W - 1 >= 0) {
         store_vec<T, V>(p.dwindow, (b * (p.W - 1) + s + p.W - 1) * p.dim + c, done);
       }
+    };
+    auto load = [&](int j, Raw<T, V>& x, Raw<T, V>& g) {
+      const int64_t t = t0 + j;
+      x.zero();
+      g.zero();
+      if (t < p.L) {
+        x.load(p.x.p, x0 + t * p.x.token);
+        g.load(p.dout, o0 + t * p.dim);
+      }
+    };
+    static_assert(kTokConvRun % kAhead == 0, "whole groups");
+    Raw<T, V> xr[2][kAhead], gr[2][kAhead], xe[3], ge[3];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i, xr[0][i], gr[0][i]);
+#pragma unroll
+    for (int j = 0; j < kTokConvRun; j += kAhead) {
+      const int k = (j / kAhead) & 1;
+      if (j + kAhead < kTokConvRun) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load(j + kAhead + i, xr[k ^ 1][i], gr[k ^ 1][i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) load(kTokConvRun + i, xe[i], ge[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) step(j + i, xr[k][i], gr[k][i]);
     }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) step(kTokConvRun + i, xe[i], ge[i]);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -332,17 +361,17 @@ hipError_t step_tv(const TokConvStepParams& p, hipStream_t s) {
 
 hipError_t dispatch_tokconv_fwd(const TokConvParams& p, int dtype, hipStream_t s) {
   if (dtype == 0) return p.vec ? fwd_tv<float, 4>(p, s) : fwd_tv<float, 1>(p, s);
-  return p.vec ? fwd_tv<bf16_t, 8>(p, s) : fwd_tv<bf16_t, 1>(p, s);
+  return p.vec ? fwd_tv<bf16_t, 4>(p, s) : fwd_tv<bf16_t, 1>(p, s);
 }
 
 hipError_t dispatch_tokconv_bwd(const TokConvParams& p, int dtype, hipStream_t s) {
   if (dtype == 0) return p.vec ? bwd_tv<float, 4>(p, s) : bwd_tv<float, 1>(p, s);
-  return p.vec ? bwd_tv<bf16_t, 8>(p, s) : bwd_tv<bf16_t, 1>(p, s);
+  return p.vec ? bwd_tv<bf16_t, 4>(p, s) : bwd_tv<bf16_t, 1>(p, s);
 }
 
 hipError_t dispatch_tokconv_step(const TokConvStepParams& p, int dtype, hipStream_t s) {
   if (dtype == 0) return p.vec ? step_tv<float, 4>(p, s) : step_tv<float, 1>(p, s);
-  return p.vec ? step_tv<bf16_t, 8>(p, s) : step_tv<bf16_t, 1>(p, s);
+  return p.vec ? step_tv<bf16_t, 4>(p, s) : step_tv<bf16_t, 1>(p, s);
 }
 
 }  // namespace mscan

@@ -23,11 +23,12 @@ constexpr int kNormBlocks = 1024;   // blocks of the backward: four a CU
 // Sums of a and b over a team of TEAM threads (64: the wave; 256: the block).
 template <int TEAM>
 __device__ __forceinline__ void team_sum(float& a, float& b, float (*sh)[2]) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    a += __shfl_xor(a, off);
-    b += __shfl_xor(b, off);
-  }
+  a = row_sum_to_last(a);
+  b = row_sum_to_last(b);
+  a = rs_pair32(rs_pair16(a, a), rs_pair16(a, a));   // over the rows, in their last lanes
+  b = rs_pair32(rs_pair16(b, b), rs_pair16(b, b));
+  a = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, a), 63));
+  b = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, b), 63));
   if constexpr (TEAM == 256) {
     __syncthreads();   // the previous row's sums have been read
     if ((threadIdx.x & 63) == 0) {
@@ -177,25 +178,42 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const NormParams p) {
     }
     if (p.w && k < p.gs) load_f32<V>(p.w, c0 + k, w[j]);
   }
-  for (int64_t row = part * TEAMS + team; row < p.rows; row += p.parts * TEAMS) {
-    float x[NV][V], z[NV][V], dy[NV][V];
-    float s2 = 0.0f, sv = 0.0f;
+  // the next row's loads are in flight while this one is worked on
+  Raw<T, V> xr[NV], zr[NV], yr[NV];
+  auto load = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int64_t k = (int64_t)(j * TEAM + tid) * V;
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[j][v] = z[j][v] = dy[j][v] = 0.0f;
-      if (k < p.gs) {
-        load_vec<T, V>(p.x, row * p.x_row + c0 + k, x[j]);
-        if (p.z) load_vec<T, V>(p.z, row * p.z_row + c0 + k, z[j]);
-        load_vec<T, V>(p.dout, row * p.dim + c0 + k, dy[j]);
+      xr[j].zero();
+      zr[j].zero();
+      yr[j].zero();
+      if (k < p.gs && row < p.rows) {
+        xr[j].load(p.x, row * p.x_row + c0 + k);
+        if (p.z) zr[j].load(p.z, row * p.z_row + c0 + k);
+        yr[j].load(p.dout, row * p.dim + c0 + k);
       }
     }
+  };
+  const int64_t step = p.parts * TEAMS;
+  load(part * TEAMS + team);
+  for (int64_t row = part * TEAMS + team; row < p.rows; row += step) {
+    float x[NV][V], dy[NV][V];
+    Gate q[NV][V];
+    float s2 = 0.0f, sv = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float z[V];
+      xr[j].get(x[j]);
+      zr[j].get(z);
+      yr[j].get(dy[j]);
+#pragma unroll
+      for (int v = 0; v < V; ++v) q[j][v] = p.z ? gate_of(z[v]) : Gate{1.0f, 0.0f};
+    }
+    load(row + step);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        bwd_sums(p, x[j][v], p.z ? silu(z[j][v]) : 1.0f, dy[j][v], w[j][v], s2, sv);
+      for (int v = 0; v < V; ++v) bwd_sums(p, x[j][v], q[j][v].g, dy[j][v], w[j][v], s2, sv);
     team_sum<TEAM>(s2, sv, sh);
     const float r = 1.0f / __builtin_sqrtf(s2 / (float)p.gs + p.eps);
     const float kk = r * r * (sv / (float)p.gs);
@@ -204,10 +222,8 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const NormParams p) {
       const int64_t k = (int64_t)(j * TEAM + tid) * V;
       float dx[V], dz[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Gate q = p.z ? gate_of(z[j][v]) : Gate{1.0f, 0.0f};
-        bwd_elem(p, x[j][v], q, dy[j][v], w[j][v], r, kk, dx[v], dz[v], dw[j][v]);
-      }
+      for (int v = 0; v < V; ++v)
+        bwd_elem(p, x[j][v], q[j][v], dy[j][v], w[j][v], r, kk, dx[v], dz[v], dw[j][v]);
       if (k < p.gs) {
         store_vec<T, V>(p.dx, row * p.dim + c0 + k, dx);
         if (p.z) store_vec<T, V>(p.dz, row * p.dim + c0 + k, dz);
@@ -328,11 +344,12 @@ hipError_t bwd_go(const NormParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int V>
+template <typename T>
 hipError_t bwd_t(const NormParams& p, hipStream_t s) {
+  constexpr int V = 4;
   const int64_t nv = (p.gs + V - 1) / V;
   hipError_t e;
-  if (!p.vec || nv > 1024) {
+  if (!p.vec || nv > 2048) {
     hipLaunchKernelGGL((norm_bwd_walk_kernel<T>), dim3((unsigned)(p.parts * p.groups)), dim3(256),
                        0, s, p);
     e = hipGetLastError();
@@ -340,12 +357,16 @@ hipError_t bwd_t(const NormParams& p, hipStream_t s) {
     e = bwd_go<T, V, 64, 1>(p, s);
   } else if (nv <= 128) {
     e = bwd_go<T, V, 64, 2>(p, s);
+  } else if (nv <= 192) {
+    e = bwd_go<T, V, 64, 3>(p, s);
   } else if (nv <= 256) {
     e = bwd_go<T, V, 256, 1>(p, s);
   } else if (nv <= 512) {
     e = bwd_go<T, V, 256, 2>(p, s);
-  } else {
+  } else if (nv <= 1024) {
     e = bwd_go<T, V, 256, 4>(p, s);
+  } else {
+    e = bwd_go<T, V, 256, 8>(p, s);
   }
   if (e != hipSuccess || !p.dw) return e;
   hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((p.dim + 31) / 32)), dim3(256), 0, s, p);
@@ -365,7 +386,7 @@ hipError_t dispatch_norm_fwd(const NormParams& p, int dtype, hipStream_t s) {
 }
 
 hipError_t dispatch_norm_bwd(const NormParams& p, int dtype, hipStream_t s) {
-  return dtype == 0 ? bwd_t<float, 4>(p, s) : bwd_t<bf16_t, 8>(p, s);
+  return dtype == 0 ? bwd_t<float>(p, s) : bwd_t<bf16_t>(p, s);
 }
 
 }  // namespace mscan

@@ -16,12 +16,56 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
+// Four consecutive elements as they lie in memory (8 or 16 aligned bytes), or,
+// with V = 1, one: kept so while loads are in flight, unpacked where used.
+template <typename T, int V>
+struct Raw {
+  static constexpr int WORDS = V * sizeof(T) <= 4 ? 1 : V * sizeof(T) / 4;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const T* q = static_cast<const T*>(p) + at;
+    if constexpr (V == 1) {
+      if constexpr (sizeof(T) == 2) w[0] = *q;
+      else w[0] = __float_as_uint(*q);
+    } else if constexpr (WORDS == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(q);
+      w[0] = x.x; w[1] = x.y;
+    } else {
+      const uint4 x = *reinterpret_cast<const uint4*>(q);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (V == 1) {
+      v[0] = bf16_lo(w[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+      }
+    }
+  }
+};
+
 // V consecutive elements at p: V = 1, or 16 bytes of them at a 16-byte aligned p.
 template <typename T, int V>
 __device__ __forceinline__ void load_vec(const void* p, int64_t at, float (&v)[V]) {
   const T* q = static_cast<const T*>(p) + at;
-  if constexpr (V == 1) v[0] = Elem<T>::load1(q);
-  else Elem<T>::template load_k<V>(q, v);
+  if constexpr (V == 8) {
+    Elem<T>::template load_k<V>(q, v);
+  } else {
+    Raw<T, V> r;
+    r.load(q, 0);
+    r.get(v);
+  }
 }
 
 template <typename T, int V>
@@ -30,6 +74,8 @@ __device__ __forceinline__ void store_vec(void* p, int64_t at, const float (&v)[
   if constexpr (sizeof(T) == 2) {
     if constexpr (V == 1) {
       *q = (bf16_t)pack_bf16(v[0], v[0]);
+    } else if constexpr (V == 4) {
+      *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     } else {
       static_assert(V == 8, "V");
       uint4 x;
