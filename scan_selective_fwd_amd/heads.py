@@ -19,10 +19,28 @@ current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from . import MambaScanError, _disc_code, _dtype_code, _flags, _lib, _ptr, _req, _stream, lib
+from . import MambaScanError, _disc_code, _dtype_code, _flags, _lib, _ptr, lib
+from . import _req as _refuse
+
+_F32 = torch.float32
+
+
+def _stream(dev):
+    """The raw handle of the current stream (torch.cuda.current_stream makes an
+    object around it first, which costs a small call a tenth of its time)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _req(t, name, dtype, shape, device):
+    """The package's check of a dense tensor; _refuse words what is wrong."""
+    if t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                     and t.is_contiguous() and t.device == device):
+        return t
+    return _refuse(t, name, dtype, shape, device)
 
 
 def _gpu(t, name):
@@ -40,22 +58,35 @@ def _view(t, name, dtype, shape, device, lead):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    run = 1
-    for n, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
-        if n != 1 and st != run:
-            raise ValueError(f"the last {t.dim() - lead} dimensions of {name} must be contiguous")
+    strides, run = t.stride(), 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        n = shape[i]
+        if n != 1 and strides[i] != run:
+            raise ValueError(f"the last {len(shape) - lead} dimensions of {name} must be "
+                             "contiguous")
         run *= n
-    return [t.stride(i) if t.shape[i] > 1 else 0 for i in range(lead)]
+    if lead == 1:
+        return (strides[0] if shape[0] > 1 else 0,)
+    return (strides[0] if shape[0] > 1 else 0, strides[1] if shape[1] > 1 else 0)
+
+
+@functools.lru_cache(maxsize=1024)
+def _struct(*fields):
+    """mamba_heads_shape of these fields, in their order, and a reference to it.
+    The calls only read it."""
+    s = _lib.HeadsShape(*fields)
+    return s, ctypes.byref(s)
 
 
 def _dims(t, name, n):
-    if t.dim() != n:
-        raise ValueError(f"{name} has {t.dim()} dimensions, expected {n}")
-    return tuple(t.shape)
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} has {len(shape)} dimensions, expected {n}")
+    return shape
 
 
 def _shape(u, delta, B, C, delta_softplus, disc, segments):
@@ -65,19 +96,18 @@ def _shape(u, delta, B, C, delta_softplus, disc, segments):
         _gpu(t, name)
     batch, L, H, P = _dims(u, "u", 4)
     G, N = _dims(B, "B", 4)[2:]
-    s = _lib.HeadsShape(batch=batch, seqlen=L, heads=H, headdim=P, groups=G, dstate=N,
-                        delta_softplus=int(bool(delta_softplus)), disc=_disc_code(disc),
-                        dtype=_dtype_code(u), segments=int(segments))
-    s.u_batch_stride, s.u_token_stride = _view(u, "u", u.dtype, (batch, L, H, P), dev, 2)
-    s.delta_batch_stride, s.delta_token_stride = _view(delta, "delta", u.dtype, (batch, L, H),
-                                                       dev, 2)
-    s.B_batch_stride, s.B_token_stride = _view(B, "B", u.dtype, (batch, L, G, N), dev, 2)
-    s.C_batch_stride, s.C_token_stride = _view(C, "C", u.dtype, (batch, L, G, N), dev, 2)
-    return s, dev
+    dt = u.dtype
+    code = _dtype_code(u)
+    s, ref = _struct(batch, L, H, P, G, N, *_view(u, "u", dt, (batch, L, H, P), dev, 2),
+                     *_view(delta, "delta", dt, (batch, L, H), dev, 2),
+                     *_view(B, "B", dt, (batch, L, G, N), dev, 2),
+                     *_view(C, "C", dt, (batch, L, G, N), dev, 2),
+                     1 if delta_softplus else 0, _disc_code(disc), code, int(segments))
+    return s, ref, dev
 
 
 def _head_args(s, A, D, delta_bias, h0, dev):
-    f32, H = torch.float32, s.heads
+    f32, H = _F32, s.heads
     _req(A, "A", f32, (H,), dev)
     _req(D, "D", f32, (H,), dev)
     _req(delta_bias, "delta_bias", f32, (H,), dev)
@@ -127,17 +157,18 @@ def heads_scan_fwd(u, delta, A, B, C, D=None, delta_bias=None, h0=None, *, delta
     sequences.  `segments`: pieces of the sequence run in parallel, 0 =
     automatic.  `workspace`: a tensor of at least heads_fwd_workspace_bytes
     reused across calls (allocated when absent)."""
-    s, dev = _shape(u, delta, B, C, delta_softplus, disc, segments)
+    s, ref, dev = _shape(u, delta, B, C, delta_softplus, disc, segments)
     _head_args(s, A, D, delta_bias, h0, dev)
     reset = _flags(reset, (s.batch, s.seqlen), dev)
     if out is None:
         out = torch.empty(u.shape, dtype=u.dtype, device=dev)
-    _req(out, "out", u.dtype, u.shape, dev)
+    else:
+        _req(out, "out", u.dtype, u.shape, dev)
     states = (s.batch, s.heads, s.headdim, s.dstate)
     if return_last_state and last_state is None:
-        last_state = torch.empty(states, dtype=torch.float32, device=dev)
-    _req(last_state, "last_state", torch.float32, states, dev)
-    ref = ctypes.byref(s)
+        last_state = torch.empty(states, dtype=_F32, device=dev)
+    else:
+        _req(last_state, "last_state", _F32, states, dev)
     n = lib().mamba_heads_scan_fwd_workspace_size(ref)
     ws = _workspace(n, _sizes(s), "mamba_heads_scan_fwd", workspace, dev)
     st = lib().mamba_heads_scan_fwd(ref, _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
@@ -153,7 +184,7 @@ def heads_scan_bwd(u, delta, A, B, C, D, delta_bias, dout, h0=None, *, dlast_sta
     `dlast_state` at the last state.  Returns a dict: du, ddelta, dB, dC in
     their tensors' type, dA and (where the input is given) dD, ddelta_bias, dh0
     in float32."""
-    s, dev = _shape(u, delta, B, C, delta_softplus, disc, segments)
+    s, ref, dev = _shape(u, delta, B, C, delta_softplus, disc, segments)
     _head_args(s, A, D, delta_bias, h0, dev)
     reset = _flags(reset, (s.batch, s.seqlen), dev)
     states = (s.batch, s.heads, s.headdim, s.dstate)
@@ -167,7 +198,6 @@ def heads_scan_bwd(u, delta, A, B, C, D, delta_bias, dout, h0=None, *, dlast_sta
         g["ddelta_bias"] = new(delta_bias)
     if h0 is not None:
         g["dh0"] = new(h0)
-    ref = ctypes.byref(s)
     n = lib().mamba_heads_scan_bwd_workspace_size(ref)
     ws = _workspace(n, _sizes(s), "mamba_heads_scan_bwd", workspace, dev)
     st = lib().mamba_heads_scan_bwd(ref, _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
@@ -196,20 +226,21 @@ def heads_state_update(state, u, delta, A, B, C, D=None, delta_bias=None, *, slo
     batch, H, P = _dims(u, "u", 3)
     G, N = _dims(_checked(B, "B"), "B", 3)[1:]
     pool = state.shape[0]
-    s = _lib.HeadsShape(batch=batch, seqlen=1, heads=H, headdim=P, groups=G, dstate=N,
-                        delta_softplus=int(bool(delta_softplus)), disc=_disc_code(disc),
-                        dtype=_dtype_code(u))
-    s.u_batch_stride, = _view(u, "u", u.dtype, (batch, H, P), dev, 1)
-    s.delta_batch_stride, = _view(delta, "delta", u.dtype, (batch, H), dev, 1)
-    s.B_batch_stride, = _view(B, "B", u.dtype, (batch, G, N), dev, 1)
-    s.C_batch_stride, = _view(C, "C", u.dtype, (batch, G, N), dev, 1)
+    dt = u.dtype
+    code = _dtype_code(u)
+    s, ref = _struct(batch, 1, H, P, G, N, *_view(u, "u", dt, (batch, H, P), dev, 1), 0,
+                     *_view(delta, "delta", dt, (batch, H), dev, 1), 0,
+                     *_view(B, "B", dt, (batch, G, N), dev, 1), 0,
+                     *_view(C, "C", dt, (batch, G, N), dev, 1), 0,
+                     1 if delta_softplus else 0, _disc_code(disc), code, 0)
     _head_args(s, A, D, delta_bias, None, dev)
-    _req(state, "state", torch.float32, (pool, H, P, N), dev)
+    _req(state, "state", _F32, (pool, H, P, N), dev)
     slots = _slots(slots, batch, dev)
     if out is None:
-        out = torch.empty((batch, H, P), dtype=u.dtype, device=dev)
-    _req(out, "out", u.dtype, (batch, H, P), dev)
-    st = lib().mamba_heads_state_update(ctypes.byref(s), _ptr(state), _ptr(slots), pool, _ptr(u),
+        out = torch.empty((batch, H, P), dtype=dt, device=dev)
+    else:
+        _req(out, "out", dt, (batch, H, P), dev)
+    st = lib().mamba_heads_state_update(ref, _ptr(state), _ptr(slots), pool, _ptr(u),
                                         _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                         _ptr(delta_bias), _ptr(out), _stream(dev))
     _lib.check(st, "mamba_heads_state_update")
@@ -240,7 +271,8 @@ def conv1d_tokens_fwd(x, w, b=None, *, window=None, reset=None, return_window=Fa
     dev, batch, L, dim, W, (sb, st_), reset = _conv_args(x, w, b, window, reset)
     if out is None:
         out = torch.empty((batch, L, dim), dtype=x.dtype, device=dev)
-    _req(out, "out", x.dtype, (batch, L, dim), dev)
+    else:
+        _req(out, "out", x.dtype, (batch, L, dim), dev)
     after = torch.empty((batch, W - 1, dim), dtype=x.dtype, device=dev) if return_window else None
     st = lib().mamba_conv1d_tokens_fwd(_ptr(x), sb, st_, _ptr(w), _ptr(b), _ptr(window),
                                        _ptr(reset), W, _dtype_code(x), batch, dim, L, _ptr(out),
@@ -283,7 +315,8 @@ def conv1d_tokens_update(x, window, w, b=None, *, slots=None, out=None):
     slots = _slots(slots, batch, dev)
     if out is None:
         out = torch.empty((batch, dim), dtype=x.dtype, device=dev)
-    _req(out, "out", x.dtype, (batch, dim), dev)
+    else:
+        _req(out, "out", x.dtype, (batch, dim), dev)
     st = lib().mamba_conv1d_tokens_update(_ptr(x), sb, _ptr(window), _ptr(slots), pool, _ptr(w),
                                           _ptr(b), W, _dtype_code(x), batch, dim, _ptr(out),
                                           _stream(dev))
@@ -321,7 +354,8 @@ def gated_norm_fwd(x, z=None, weight=None, *, groups=1, eps=1e-5, gate_first=Tru
     dev, x2, sx, z2, sz, rows, dim, groups = _norm_args(x, z, weight, groups)
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _req(out, "out", x.dtype, x.shape, dev)
+    else:
+        _req(out, "out", x.dtype, x.shape, dev)
     st = lib().mamba_gated_norm_fwd(_ptr(x2), sx, _ptr(z2), sz, _ptr(weight), rows, dim, groups,
                                     float(eps), int(bool(gate_first)), _dtype_code(x), _ptr(out),
                                     _stream(dev))
