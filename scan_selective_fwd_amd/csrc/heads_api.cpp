@@ -118,20 +118,20 @@ int64_t pad_state(const mamba_heads_shape* s) {
   return s->dstate <= 32 ? 32 : s->dstate <= 64 ? 64 : s->dstate <= 128 ? 128 : 256;
 }
 
-// Segments: as many as bring the blocks to about kTargetBlocks, each of at
-// least kMinChunks chunks.
+// Segments: as many as fit `target` blocks, the ones the chip holds at once (one
+// more and they take two rounds), each of at least kMinChunks chunks.
 constexpr int64_t kTargetBlocks = 512;
 constexpr int64_t kMinChunks = 4;
 // Blocks that the backward's chunks are to bring, over batch rows, groups,
 // chunks and shares of the heads.
 constexpr int64_t kChunkBlocks = 512;
 
-void split(const mamba_heads_shape* s, int* nseg, int64_t* seg_len) {
+void split(const mamba_heads_shape* s, int64_t target, int* nseg, int64_t* seg_len) {
   const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
   const int64_t blocks = s->batch * s->groups * map_of(s).hblocks;
   int64_t n = s->segments;
   if (n == 0) {
-    n = (kTargetBlocks + blocks / 2) / blocks;
+    n = target / blocks;
     if (n > chunks / kMinChunks) n = chunks / kMinChunks;
   }
   if (n > chunks) n = chunks;
@@ -152,7 +152,7 @@ struct FwdLayout {
 };
 
 bool fwd_layout(const mamba_heads_shape* s, FwdLayout* l) {
-  split(s, &l->nseg, &l->seg_len);
+  split(s, kTargetBlocks, &l->nseg, &l->seg_len);
   const int64_t cols = s->batch * s->heads * map_of(s).slices;
   if (cols > kGridLim / l->nseg || cols > kGridLim / 16) return false;
   const size_t n = (size_t)cols * (size_t)(l->nseg - 1);
@@ -174,7 +174,7 @@ struct BwdLayout {
 };
 
 bool bwd_layout(const mamba_heads_shape* s, BwdLayout* l) {
-  split(s, &l->nseg, &l->seg_len);
+  split(s, kTargetBlocks / 2, &l->nseg, &l->seg_len);   // both directions run at once
   const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
   const Map m = map_of(s);
   const int64_t bh = s->batch * s->heads, cols = bh * m.slices;

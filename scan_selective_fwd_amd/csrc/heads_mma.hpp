@@ -36,16 +36,18 @@ constexpr int kSlice = 32;
 constexpr int kCols = 4 * kSlice;
 
 // Per type: tokens a chunk, parts of an input operand, row padding of a tile.
-// Padding by 16 bytes spreads the rows of a fragment's read over the banks.
+// The LDS serves 16 lanes of 8 bytes at a time over 128 bytes of banks: rows 8
+// bytes apart there (PAD) serve fragments along the rows without conflicts,
+// rows 32 bytes apart (PADT) the transposing reads; 16 (PADB) serves both in two.
 template <typename T>
 struct Mx;
 template <>
 struct Mx<bf16_t> {
-  static constexpr int Q = 64, PARTS = 1, PAD = 8, V = 8;
+  static constexpr int Q = 64, PARTS = 1, PAD = 4, PADT = 16, PADB = 8, V = 8;
 };
 template <>
 struct Mx<float> {
-  static constexpr int Q = 32, PARTS = 3, PAD = 4, V = 4;
+  static constexpr int Q = 32, PARTS = 3, PAD = 4, PADT = 4, PADB = 4, V = 4;
 };
 
 template <int NP>
@@ -355,7 +357,15 @@ struct Stage {
     const int t = opaque_int(tid256());
     T* q = tile + (t / PER_ROW) * stride + (t % PER_ROW) * V;
 #pragma unroll
-    for (int k = 0; k < COUNT; ++k) *reinterpret_cast<u32x4*>(q + k * STEP * stride) = v[k];
+    for (int k = 0; k < COUNT; ++k) {
+      if constexpr (sizeof(T) == 2) {   // rows may start on 8 bytes
+        u32x2* o = reinterpret_cast<u32x2*>(q + k * STEP * stride);
+        o[0] = u32x2{v[k][0], v[k][1]};
+        o[1] = u32x2{v[k][2], v[k][3]};
+      } else {
+        *reinterpret_cast<u32x4*>(q + k * STEP * stride) = v[k];
+      }
+    }
   }
 };
 

@@ -25,7 +25,8 @@ namespace {
 
 template <typename T, int NK>
 struct BwdTiles {
-  static constexpr int Q = Mx<T>::Q, PAD = Mx<T>::PAD, NP = 32 * NK, QT = Q / 16;
+  static constexpr int Q = Mx<T>::Q, PAD = Mx<T>::PAD, PADT = Mx<T>::PADT;
+  static constexpr int NP = 32 * NK, QT = Q / 16;
   static constexpr int PARTS = Mx<T>::PARTS;
   static constexpr int SX = 64 + PAD, SN = NP + PAD, SM = Q + PAD;
   // region that holds a head's states, then its two matrices
@@ -42,7 +43,7 @@ template <typename T, int NK, bool VEC, bool REV>
 __device__ __forceinline__ void states_of(const HeadsBwdParams& p, int block, T* Xs, T* Ks,
                                           Scal<Mx<T>::Q>* scal) {
   using F = BwdTiles<T, NK>;
-  constexpr int Q = F::Q, NP = F::NP, SX = kCols + F::PAD, SN = F::SN;
+  constexpr int Q = F::Q, NP = F::NP, SX = kCols + F::PADT, SN = NP + F::PADT;
   const Place k = place_at(p, p.nseg, block);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t begin = (int64_t)k.seg * p.seg_len;
@@ -109,8 +110,8 @@ __device__ __forceinline__ void states_of(const HeadsBwdParams& p, int block, T*
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_states_kernel(const HeadsBwdParams p) {
   using F = BwdTiles<T, NK>;
-  __shared__ __align__(16) T Xs[F::Q * (kCols + F::PAD)];
-  __shared__ __align__(16) T Ks[F::Q * F::SN];
+  __shared__ __align__(16) T Xs[F::Q * (kCols + F::PADT)];
+  __shared__ __align__(16) T Ks[F::Q * (F::NP + F::PADT)];
   extern __shared__ __align__(16) char dyn[];
   Scal<F::Q>* const scal = reinterpret_cast<Scal<F::Q>*>(dyn);
   // both directions in one launch

@@ -16,7 +16,8 @@ namespace {
 template <typename T, int NK>
 struct FwdTiles {
   static constexpr int Q = Mx<T>::Q, PAD = Mx<T>::PAD, NP = 32 * NK;
-  static constexpr int SX = kCols + PAD, SN = NP + PAD, SM = Q + PAD, QT = Q / 16;
+  static constexpr int PADT = Mx<T>::PADT;
+  static constexpr int SX = kCols + PADT, SB = NP + Mx<T>::PADB, SN = NP + PAD, SM = Q + PAD, QT = Q / 16;
   static constexpr int TILES = QT * (QT + 1) / 2;
   static constexpr int PARTS = Mx<T>::PARTS;
 };
@@ -62,7 +63,7 @@ __device__ __forceinline__ void decayed_products(const HeadsParams& p, int heads
 #pragma unroll
   for (int i = 0; i <= OFF; ++i) {
     a[i][0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    bf[0][i][0] = load_rows<T>(Bs, SN, 16 * st[i], 0);
+    bf[0][i][0] = load_rows<T>(Bs, F::SB, 16 * st[i], 0);
     cf[0][i][0] = load_rows<T>(Cs, SN, 16 * qt[i], 0);
   }
 #pragma unroll
@@ -70,7 +71,7 @@ __device__ __forceinline__ void decayed_products(const HeadsParams& p, int heads
     if (kk + 1 < NK) {
 #pragma unroll
       for (int i = 0; i <= OFF; ++i) {
-        bf[(kk + 1) & 1][i][0] = load_rows<T>(Bs, SN, 16 * st[i], 32 * kk + 32);
+        bf[(kk + 1) & 1][i][0] = load_rows<T>(Bs, F::SB, 16 * st[i], 32 * kk + 32);
         cf[(kk + 1) & 1][i][0] = load_rows<T>(Cs, SN, 16 * qt[i], 32 * kk + 32);
       }
     }
@@ -79,8 +80,7 @@ __device__ __forceinline__ void decayed_products(const HeadsParams& p, int heads
     for (int i = 0; i <= OFF; ++i) mma(a[i], bf[kk & 1][i], cf[kk & 1][i]);
   }
   const int li = lane_i(), lg = 4 * lane_g();
-#pragma unroll 1
-  for (int x = 0; x < heads; ++x) {
+  auto weight = [&](int x) {
     const Scal<Q>& o = scal[x];
     float m[1 + OFF][4], Sq[1 + OFF], Se[1 + OFF];
     f32x4 g[1 + OFF];
@@ -131,16 +131,22 @@ __device__ __forceinline__ void decayed_products(const HeadsParams& p, int heads
           *reinterpret_cast<f32x4*>(Ms) = f32x4{m[i][0], m[i][1], m[i][2], m[i][3]};
       }
     }
+  };
+  // two heads at a time: their reads and exponentials overlap
+#pragma unroll 1
+  for (int x = 0; x < heads; x += 2) {
+    weight(x);
+    if (x + 1 < heads) weight(x + 1);
   }
 }
 
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const HeadsFwdParams p) {
   using F = FwdTiles<T, NK>;
-  constexpr int Q = F::Q, NP = F::NP, SX = F::SX, SN = F::SN, SM = F::SM, QT = F::QT;
+  constexpr int Q = F::Q, NP = F::NP, SX = F::SX, SB = F::SB, SN = F::SN, SM = F::SM, QT = F::QT;
   constexpr int PARTS = F::PARTS;
   __shared__ __align__(16) T Xs[Q * SX];
-  __shared__ __align__(16) T Bs[Q * SN];
+  __shared__ __align__(16) T Bs[Q * SB];
   __shared__ __align__(16) T Cs[Q * SN];
   extern __shared__ __align__(16) char dyn[];
   Scal<Q>* const scal = reinterpret_cast<Scal<Q>*>(dyn);
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
   for (int64_t t = begin; t < end; t += Q) {
     const int len = rows(t);
     sx.store(Xs, SX);
-    sb.store(Bs, SN);
+    sb.store(Bs, SB);
     sc.store(Cs, SN);
     ss.store(scal, k.heads);
     __syncthreads();
@@ -232,7 +238,7 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
     }
     __syncthreads();
     if (flagged) {
-      clear_kept<T, Q, NP>(Bs, SN, scal[0].id, scal[0].flags);
+      clear_kept<T, Q, NP>(Bs, SB, scal[0].id, scal[0].flags);
       __syncthreads();
     }
     if (k.on) {
@@ -328,7 +334,7 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
         phase();
       }
       phase();
-      step_state<T, NK>(h, me.dec, me.c, Bs, SN, Xs, SX, k.col);
+      step_state<T, NK>(h, me.dec, me.c, Bs, SB, Xs, SX, k.col);
 #pragma unroll
       for (int pt = 0; pt < 2; ++pt)
         if (marks[pt] != 0 && marked<Q>(marks[pt], me.id, me.flags)) spoil<NK>(h, pt);
@@ -343,9 +349,9 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const HeadsFwdParams p) {
   using F = FwdTiles<T, NK>;
-  constexpr int Q = F::Q, NP = F::NP, SX = F::SX, SN = F::SN;
+  constexpr int Q = F::Q, NP = F::NP, SX = F::SX, SB = NP + F::PADT;   // only read transposed
   __shared__ __align__(16) T Xs[Q * SX];
-  __shared__ __align__(16) T Bs[Q * SN];
+  __shared__ __align__(16) T Bs[Q * SB];
   extern __shared__ __align__(16) char dyn[];
   Scal<Q>* const scal = reinterpret_cast<Scal<Q>*>(dyn);
   const Place k = place_of(p, p.nseg - 1);
@@ -371,13 +377,13 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const H
   fetch(begin);
   for (int64_t t = begin; t < end; t += Q) {
     sx.store(Xs, SX);
-    sb.store(Bs, SN);
+    sb.store(Bs, SB);
     ss.store(scal, k.heads);
     __syncthreads();
     if (t + Q < end) fetch(t + Q);
     const Scal<Q>& me = scal[k.on ? hh : 0];
     if (scal[0].flags != 0) {
-      clear_kept<T, Q, NP>(Bs, SN, scal[0].id, scal[0].flags);
+      clear_kept<T, Q, NP>(Bs, SB, scal[0].id, scal[0].flags);
       __syncthreads();
     }
     if (k.on) {
@@ -387,7 +393,7 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const H
         for (int pt = 0; pt < 2; ++pt)
           marks[pt] = take_out<T, Q>(Xs, SX, k.col + 16 * pt + lane_i());
       }
-      step_state<T, NK>(h, me.dec, me.c, Bs, SN, Xs, SX, k.col);
+      step_state<T, NK>(h, me.dec, me.c, Bs, SB, Xs, SX, k.col);
 #pragma unroll
       for (int pt = 0; pt < 2; ++pt)
         if (marks[pt] != 0 && marked<Q>(marks[pt], me.id, me.flags)) spoil<NK>(h, pt);
