@@ -224,11 +224,14 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
   constexpr int Q = F::Q, NP = F::NP, QT = F::QT, SX = F::SX, SN = F::SN, SM = F::SM;
   constexpr int PARTS = F::PARTS, SIDE = kSide<NK>, WAVES = 4 * SIDE;
   constexpr int NTW = 2 * NK > WAVES ? 2 * NK / WAVES : 1;   // tiles of dB, dC a wave
+  // room for both of a head's states: fewer barriers
+  constexpr bool BOTH = sizeof(T) == 2 && NK <= 4;
   __shared__ __align__(16) T Bs[Q * SN];
   __shared__ __align__(16) T Cs[Q * SN];
   __shared__ __align__(16) T Xall[SIDE][Q * SX];
   __shared__ __align__(16) T Yall[SIDE][Q * SX];   // dout
-  __shared__ __align__(16) T Zall[SIDE][F::Z];
+  __shared__ __align__(16) T Zall[SIDE][F::Z];     // g, then h or the matrices
+  __shared__ __align__(16) T Hall[BOTH ? SIDE : 1][BOTH ? F::ZSTATE : 8];   // h
   __shared__ Scal<Q> scall[SIDE];
   __shared__ BwdSums<Q> sums_all[SIDE];
   const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -263,7 +266,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
   Stage<T, Q, 64, VEC> sx, sy;
   ScalStage<Q, 1> ss;
   f32x4 g[2 * NK], h[2 * NK];
-  auto head_of = [&](int u) { return grp * per + u / CB; };
+  auto head_of = [&](int u) { return grp * per + (CB == 1 ? u : u / CB); };
   // the side's unit, its last one again where there is none: nothing of that is kept
   auto mine = [&](int u) { return u + side < u1 ? u + side : u1 - 1; };
   auto fetch = [&](int u) {
@@ -367,6 +370,10 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
   // acc += f Z^T tile^T of every side's unit (rows n, columns tokens), weighted
   // by token: what reaches dB from behind the chunk, dC from before it
   auto inter = [&](int u, const T (*tiles)[Q * SX], bool second, f32x4 (&acc)[NTW][QT]) {
+    auto state_tile = [&](int x) -> const T* {
+      if constexpr (BOTH) return second ? Hall[x] : Zall[x];
+      else return Zall[x];
+    };
 #pragma unroll
     for (int x = 0; x < SIDE; ++x) {
       if (u + x >= u1) break;
@@ -381,7 +388,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-        for (int i = 0; i < NTW; ++i) zf[kk][i] = load_cols<T>(Zall[x] + n0, SN, 16 * i, 32 * kk, ln);
+        for (int i = 0; i < NTW; ++i) zf[kk][i] = load_cols<T>(state_tile(x) + n0, SN, 16 * i, 32 * kk, ln);
 #pragma unroll
         for (int j = 0; j < QT; ++j) xf[kk][j] = load_rows<T>(tiles[x], SX, 16 * j, 32 * kk, ln);
       }
@@ -419,9 +426,9 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       mma(acc, rf, bf[kk & 1]);
     }
   };
-  auto put_state = [&](const f32x4 (&r)[2 * NK]) {
+  auto put_state = [&](T* tile, const f32x4 (&r)[2 * NK]) {
     const Lane ln = lane_fresh();
-    T* const q = Zs + 16 * wave * SN + ln.i * SN + 4 * ln.g;
+    T* const q = tile + 16 * wave * SN + ln.i * SN + 4 * ln.g;
 #pragma unroll
     for (int nt = 0; nt < 2 * NK; ++nt) put4<T>(q + 16 * nt, r[nt]);
   };
@@ -447,7 +454,8 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     for (int nt = 0; nt < 2 * NK; ++nt)
 #pragma unroll
       for (int j = 0; j < 4; ++j) gh = __builtin_fmaf(g[nt][j], h[nt][j], gh);
-    put_state(g);
+    put_state(Zs, g);
+    if constexpr (BOTH) put_state(Hall[side], h);
     // (g B_s)^T (rows p, columns s)
     f32x4 du[1][QT];
     project(g, Bs, du);
@@ -479,6 +487,24 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     }
     }
     phase();
+    // (h C_q)^T (rows p, columns q)
+    auto from_before = [&]() {
+      f32x4 y[1][QT];
+      project(h, Cs, y);
+    const Lane ln = lane_fresh();
+    const int li = ln.i, lg = 4 * ln.g, lane = li + 16 * ln.g;
+
+#pragma unroll
+      for (int q = 0; q < QT; ++q) {
+        const f32x4 d = four<T>(Ys + (16 * q + li) * SX + 16 * wave + lg);
+        float v = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v = __builtin_fmaf(d[j], y[0][q][j], v);
+        v = sum_g(v);
+        if (lane < 16) sums.out[wave][16 * q + li] = v;
+      }
+    };
+    if constexpr (BOTH) from_before();
     // dout_q . u_s, and from it K's sums and the two matrices of the chunk
     u32x2 lg_hi[1 + OFF], lg_lo[1 + OFF], lr_hi[1 + OFF];   // bfloat16, packed
     f32x4 lg_f[1 + OFF], lr_f[1 + OFF];                     // float32
@@ -551,33 +577,18 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       }
     }
     __syncthreads();
+    // the next heads' states take these registers as soon as they are free:
+    // their loads are the longest and come for all blocks at about one time
+    if (more) fetch_state(p.g_chunk, mine(u + SIDE), g);
     if (has_n) inter(u, Xall, false, dB);
-    // (h C_q)^T (rows p, columns q)
-    {
-      f32x4 y[1][QT];
-      project(h, Cs, y);
-    const Lane ln = lane_fresh();
-    const int li = ln.i, lg = 4 * ln.g, lane = li + 16 * ln.g;
-
-#pragma unroll
-      for (int q = 0; q < QT; ++q) {
-        const f32x4 d = four<T>(Ys + (16 * q + li) * SX + 16 * wave + lg);
-        float v = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v = __builtin_fmaf(d[j], y[0][q][j], v);
-        v = sum_g(v);
-        if (lane < 16) sums.out[wave][16 * q + li] = v;
-      }
+    if constexpr (!BOTH) from_before();
+    if constexpr (!BOTH) {
+      __syncthreads();
+      put_state(Zs, h);
+      phase();
     }
-    __syncthreads();
-    put_state(h);
-    phase();
-    // the next heads' states take these registers
-    if (more) {
-      fetch_state(p.g_chunk, mine(u + SIDE), g);
-      fetch_state(p.h_chunk, mine(u + SIDE), h);
-    }
-    __syncthreads();
+    if (more) fetch_state(p.h_chunk, mine(u + SIDE), h);
+    if constexpr (!BOTH) __syncthreads();
     if (has_n) inter(u, Yall, true, dC);
     __syncthreads();
     // the chunk's matrices, rows s, columns q; the tiles beside the diagonal
