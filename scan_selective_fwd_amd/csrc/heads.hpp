@@ -35,7 +35,13 @@ struct HeadsParams {
   float* seg_dec;        // and their segments' decays
 };
 
+// Segments up to which the forward's output pass carries the state itself: its
+// blocks then read (nseg - 1) / 2 states each on average, where a carry pass
+// reads and writes every state once more.
+constexpr int kSelfCarry = 8;
+
 struct HeadsFwdParams : HeadsParams {
+  bool carried;          // a carry pass joins the segments
   void* out;
   float* last;           // nullable
 };

@@ -119,20 +119,24 @@ int64_t pad_state(const mamba_heads_shape* s) {
 }
 
 // Segments: as many as fit `target` blocks, the ones the chip holds at once (one
-// more and they take two rounds), each of at least kMinChunks chunks.
+// more and they take two rounds), each of at least `least` chunks.  The forward
+// takes 1: 200 steps of 24 heads take 22.8 us in four segments and 27.6 in one,
+// 1000 steps 35.6 in 16, 37.8 in 8, 44.1 in 4.  The backward, whose segments
+// serve its states pass alone, takes 2: 512 steps take 59.4 us in four segments,
+// 62.8 in two, 57.2 in eight; 4 x 512 take 76.7 in two, 81.0 in four, 91.2 in
+// eight.
 constexpr int64_t kTargetBlocks = 512;
-constexpr int64_t kMinChunks = 4;
-// Blocks that the backward's chunks are to bring, over batch rows, groups,
-// chunks and shares of the heads.
-constexpr int64_t kChunkBlocks = 512;
+// Blocks of the backward's chunks that run at once: one a CU.
+constexpr int64_t kChunkBlocks = 256;
 
-void split(const mamba_heads_shape* s, int64_t target, int* nseg, int64_t* seg_len) {
+void split(const mamba_heads_shape* s, int64_t target, int64_t least, int* nseg,
+           int64_t* seg_len) {
   const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
   const int64_t blocks = s->batch * s->groups * map_of(s).hblocks;
   int64_t n = s->segments;
   if (n == 0) {
     n = target / blocks;
-    if (n > chunks / kMinChunks) n = chunks / kMinChunks;
+    if (n > chunks / least) n = chunks / least;
   }
   if (n > chunks) n = chunks;
   if (n > 4096) n = 4096;
@@ -152,7 +156,7 @@ struct FwdLayout {
 };
 
 bool fwd_layout(const mamba_heads_shape* s, FwdLayout* l) {
-  split(s, kTargetBlocks, &l->nseg, &l->seg_len);
+  split(s, kTargetBlocks, 1, &l->nseg, &l->seg_len);
   const int64_t cols = s->batch * s->heads * map_of(s).slices;
   if (cols > kGridLim / l->nseg || cols > kGridLim / 16) return false;
   const size_t n = (size_t)cols * (size_t)(l->nseg - 1);
@@ -174,16 +178,19 @@ struct BwdLayout {
 };
 
 bool bwd_layout(const mamba_heads_shape* s, BwdLayout* l) {
-  split(s, kTargetBlocks / 2, &l->nseg, &l->seg_len);   // both directions run at once
+  split(s, kTargetBlocks / 2, 2, &l->nseg, &l->seg_len);   // both directions run at once
   const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
   const Map m = map_of(s);
   const int64_t bh = s->batch * s->heads, cols = bh * m.slices;
   const int64_t cb = (s->headdim + 63) / 64, units = s->heads / s->groups * cb;
   if (chunks > kGridLim / 16 / cols || cols > kGridLim / 32 / l->nseg) return false;
-  // enough blocks to fill the chip, each with at least one head
+  // The heads of a chunk are shared among as many blocks as run at once, each
+  // with at least one: 2 x 2048 x 80 heads take 330 us with 256 blocks, 336 with
+  // 512, 387 with 1024; their shares of dB and dC are summed after.
   const int64_t blocks = s->batch * s->groups * chunks;
-  int64_t sp = (kChunkBlocks + blocks - 1) / blocks;
+  int64_t sp = kChunkBlocks / blocks;
   if (sp > units) sp = units;
+  if (sp < 1) sp = 1;
   l->splits = (int)sp;
   const size_t state = (size_t)(kSlice * pad_state(s)) * 4;
   const size_t bch = (size_t)(bh * chunks), bl = (size_t)s->batch * (size_t)s->seqlen;
@@ -301,7 +308,7 @@ mamba_status mamba_heads_scan_fwd(const mamba_heads_shape* shape, const void* u,
   p.scal = workspace;
   p.seg_state = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.state);
   p.seg_dec = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.dec);
-  p.out = out; p.last = last_state;
+  p.out = out; p.last = last_state; p.carried = p.nseg > mscan::kSelfCarry;
   p.vec = p.vec && aligned(out, 16);
   return hip_status(mscan::dispatch_heads_fwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,
                                               as_stream(stream)));

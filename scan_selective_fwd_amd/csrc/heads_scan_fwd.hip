@@ -6,7 +6,8 @@
 // share B, C and the products C_q . B_s.  Where the heads alone do not fill the
 // chip the sequence is cut into segments: a first pass over the segments leaves
 // each one's end state from zero and its decay, a carry joins them, and the
-// output pass starts each segment from the state entering it.
+// output pass starts each segment from the state entering it.  Up to
+// kSelfCarry segments the output pass joins those before its own by itself.
 #include "heads_mma.hpp"
 
 namespace mscan {
@@ -162,12 +163,24 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
   const int64_t chunks = (p.L + Q - 1) / Q;
 
   f32x4 h[2 * NK][2];
-  if (!k.on)
+  if (!k.on) {
     fill<NK>(h, 0.0f);
-  else if (k.seg == 0)
-    load_state<NK>(p.h0 ? p.h0 + (k.b * p.H + k.h) * (int64_t)p.P * p.N : nullptr, k.c0, p.P, p.N, h);
-  else
+  } else if (p.carried && k.seg > 0) {
     load_frags<NK>(p.seg_state + slice_slot(p, k, p.nseg - 1, k.seg - 1) * slice_floats<NK>(), h);
+  } else {
+    load_state<NK>(p.h0 ? p.h0 + (k.b * p.H + k.h) * (int64_t)p.P * p.N : nullptr, k.c0, p.P, p.N, h);
+    // few segments: each joins the ones before it by itself
+    const int64_t slot = slice_slot(p, k, p.nseg - 1, 0);
+    for (int i = 0; i < k.seg; ++i) {
+      f32x4 x[2 * NK][2];
+      load_frags<NK>(p.seg_state + (slot + i) * slice_floats<NK>(), x);
+      decay_state<NK>(h, p.seg_dec[slot + i]);
+#pragma unroll
+      for (int nt = 0; nt < 2 * NK; ++nt)
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) h[nt][pt] += x[nt][pt];
+    }
+  }
   // tiles above the diagonal are read as part of a 32-step and stay zero
   for (int i = threadIdx.x; i < p.hpw * Q * SM; i += 256) Mall[i] = T(0);
 
@@ -226,14 +239,22 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
         phase();
         mma(y, hf, cf[kk & 1]);
       }
+      if (flagged) {
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) {
-        const float e = me.e[16 * qt + lane_i()];
+        for (int qt = 0; qt < QT; ++qt) {
+          const float e = me.e[16 * qt + lane_i()];
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt)
+          for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            y[pt][qt][j] = flagged ? weigh(y[pt][qt][j], e) : y[pt][qt][j] * e;
+            for (int j = 0; j < 4; ++j) y[pt][qt][j] = weigh(y[pt][qt][j], e);
+        }
+      } else {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+          const float e = me.e[16 * qt + lane_i()];
+          y[0][qt] *= e;
+          y[1][qt] *= e;
+        }
       }
     }
     __syncthreads();
@@ -448,10 +469,12 @@ hipError_t fwd_go(const HeadsFwdParams& p, hipStream_t s) {
                        dim3(256), lds, s, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((heads_carry_kernel<NK>), dim3((unsigned)(p.batch * p.H * p.slices * NK)),
-                       dim3(256), 0, s, p);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (p.carried) {
+      hipLaunchKernelGGL((heads_carry_kernel<NK>), dim3((unsigned)(p.batch * p.H * p.slices * NK)),
+                         dim3(256), 0, s, p);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
   const size_t lds = scal_bytes<T>(p.hpw) + m_bytes<T, NK>(p.hpw);
   hipLaunchKernelGGL((heads_fwd_kernel<T, NK, VEC>), dim3((unsigned)(blocks * p.nseg)), dim3(256),
