@@ -126,8 +126,9 @@ int64_t pad_state(const mamba_heads_shape* s) {
 // 62.8 in two, 57.2 in eight; 4 x 512 take 76.7 in two, 81.0 in four, 91.2 in
 // eight.
 constexpr int64_t kTargetBlocks = 512;
-// Blocks of the backward's chunks that run at once: one a CU.
-constexpr int64_t kChunkBlocks = 256;
+// Blocks of the backward's chunks that run at once: one a CU, two where N <= 64
+// leaves them the LDS.
+int64_t chunk_blocks(const mamba_heads_shape* s) { return s->dstate <= 64 ? 512 : 256; }
 
 void split(const mamba_heads_shape* s, int64_t target, int64_t least, int* nseg,
            int64_t* seg_len) {
@@ -184,11 +185,12 @@ bool bwd_layout(const mamba_heads_shape* s, BwdLayout* l) {
   const int64_t bh = s->batch * s->heads, cols = bh * m.slices;
   const int64_t cb = (s->headdim + 63) / 64, units = s->heads / s->groups * cb;
   if (chunks > kGridLim / 16 / cols || cols > kGridLim / 32 / l->nseg) return false;
+  if (s->batch * s->seqlen > kGridLim * 128 / (s->groups * s->dstate)) return false;
   // The heads of a chunk are shared among as many blocks as run at once, each
-  // with at least one: 2 x 2048 x 80 heads take 330 us with 256 blocks, 336 with
-  // 512, 387 with 1024; their shares of dB and dC are summed after.
+  // with at least one: 2 x 2048 x 80 heads take 308 us with 256 blocks (336
+  // and 387 against 330 with 512 and 1024); their shares of dB and dC are summed after.
   const int64_t blocks = s->batch * s->groups * chunks;
-  int64_t sp = kChunkBlocks / blocks;
+  int64_t sp = chunk_blocks(s) / blocks;
   if (sp > units) sp = units;
   if (sp < 1) sp = 1;
   l->splits = (int)sp;

@@ -212,10 +212,13 @@ struct alignas(16) BwdSums {
   float gh[4], ud[4];     // by wave: <g, h>, sum of u dout
 };
 
-// Heads a block takes side by side, 4 waves each: with two, a wave holds half
-// of dB and dC and keeps its registers; N > 128 leaves LDS for one.
+// Heads a block takes side by side, 4 waves each.  With two, a wave holds half
+// of dB and dC and keeps its registers (2 x 2048 x 80 x 64, N = 128: 204 us, one
+// head 244).  N <= 64 has a tile of dB and dC for 4 waves at most, and two blocks
+// of one head fit a CU (4 x 777 x 16 in float32: 112 -> 100 us; 2 x 2048 x 80 in
+// bfloat16: 210 -> 201); N > 128 leaves LDS for one.
 template <int NK>
-constexpr int kSide = NK == 8 ? 1 : 2;
+constexpr int kSide = NK == 4 ? 2 : 1;
 
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256 * kSide<NK>, NK == 8 ? 1 : 2)
@@ -788,29 +791,39 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
   }
 }
 
-// dB, dC: the splits' shares summed in order.
-template <typename T>
-__global__ __launch_bounds__(256) void heads_bwd_sum_kernel(const HeadsBwdParams p) {
-  const int64_t n = p.batch * p.L * p.G * p.N;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// dB, dC: the splits' shares summed in order, V elements a thread.
+template <typename T, int V>
+__device__ __forceinline__ void sum_splits(const HeadsBwdParams& p, int64_t n, int64_t i) {
   if (i >= n) return;
-  float sB = 0.0f, sC = 0.0f;
+  float sB[V] = {}, sC[V] = {};
   for (int k = 0; k < p.splits; ++k) {
-    sB += p.dB_part[k * n + i];
-    sC += p.dC_part[k * n + i];
+    float b[V], c[V];
+    load_vec<float, V>(p.dB_part, k * n + i, b);
+    load_vec<float, V>(p.dC_part, k * n + i, c);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      sB[j] += b[j];
+      sC[j] += c[j];
+    }
   }
-  Elem<T>::store1(static_cast<T*>(p.dB) + i, sB);
-  Elem<T>::store1(static_cast<T*>(p.dC) + i, sC);
+  store_vec<T, V>(p.dB, i, sB);
+  store_vec<T, V>(p.dC, i, sC);
 }
 
-// ddelta of every token from F and dw; a chunk's shares of dA, dD, dbias.  One
-// wave a (batch row, chunk, head).
-template <typename T>
-__global__ __launch_bounds__(256) void heads_bwd_delta_kernel(const HeadsBwdParams p) {
+// One launch for what the chunks leave: dB and dC, and, in the blocks from `sums`
+// on, ddelta of every token from F and dw with a chunk's shares of dA, dD, dbias,
+// one wave a (batch row, chunk, head).  Two launches took 3 us more.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void heads_bwd_tail_kernel(const HeadsBwdParams p, int sums) {
   constexpr int Q = Mx<T>::Q;
+  if ((int)blockIdx.x < sums) {
+    sum_splits<T, V>(p, p.batch * p.L * p.G * p.N, ((int64_t)blockIdx.x * 256 + threadIdx.x) * V);
+    return;
+  }
   const int64_t chunks = (p.L + Q - 1) / Q;
   const int l = threadIdx.x & 63, CB = (p.P + 63) / 64;
-  const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t id =
+      ((int64_t)blockIdx.x - sums) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= p.batch * chunks * p.H) return;
   const int hd = (int)(id % p.H);
   const int64_t bc = id / p.H, b = bc / chunks, t = (bc - b * chunks) * Q + l;
@@ -887,12 +900,16 @@ hipError_t bwd_go(const HeadsBwdParams& p, hipStream_t s) {
                      dim3((unsigned)(p.batch * p.G * chunks * p.splits)), dim3(256 * kSide<NK>), 0, s, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t n = p.batch * p.L * p.G * p.N;
-  hipLaunchKernelGGL((heads_bwd_sum_kernel<T>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int64_t waves = p.batch * chunks * p.H;
-  hipLaunchKernelGGL((heads_bwd_delta_kernel<T>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, p);
+  const int64_t n = p.batch * p.L * p.G * p.N, waves = p.batch * chunks * p.H;
+  // four elements a thread where they stay together
+  const bool four = n % 4 == 0 &&
+                    ((uintptr_t)p.dB | (uintptr_t)p.dC) % (4 * sizeof(T)) == 0;
+  const int64_t per = four ? 1024 : 256, sums = (n + per - 1) / per;
+  const dim3 grid((unsigned)(sums + (waves + 3) / 4));
+  if (four)
+    hipLaunchKernelGGL((heads_bwd_tail_kernel<T, 4>), grid, dim3(256), 0, s, p, (int)sums);
+  else
+    hipLaunchKernelGGL((heads_bwd_tail_kernel<T, 1>), grid, dim3(256), 0, s, p, (int)sums);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(heads_bwd_head_kernel, dim3((unsigned)p.H), dim3(256), 0, s, p,
