@@ -15,17 +15,17 @@ namespace mscan {
 
 namespace {
 
-constexpr int kLags = 4;
 constexpr int kFwdRun = 16;   // tokens a lane takes in the forward
 constexpr int kAhead = 4;     // rows the backward loads ahead
 
-// Weights by lag: w4[k] multiplies x_{t-k}; lags past the width are zero.
-template <int V>
-__device__ __forceinline__ void load_lags(const float* w, int W, int64_t c, float (&w4)[kLags][V]) {
+// Weights by lag: w4[k] multiplies x_{t-k}.  The width W is a template argument:
+// an input at a lag past it must not be multiplied, not even by zero.
+template <int W, int V>
+__device__ __forceinline__ void load_lags(const float* w, int64_t c, float (&w4)[W][V]) {
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int k = 0; k < kLags; ++k) w4[k][v] = k < W ? w[(c + v) * W + (W - 1 - k)] : 0.0f;
+    for (int k = 0; k < W; ++k) w4[k][v] = w[(c + v) * W + (W - 1 - k)];
 }
 
 // Input row s of batch row b, s in [-3, L): from x, the window before it, or zero.
@@ -79,20 +79,20 @@ __device__ __forceinline__ void push(float (&h)[3][V], const float (&x)[V]) {
   }
 }
 
-template <int V>
-__device__ __forceinline__ void pre_act(const float (&w4)[kLags][V], const float (&cb)[V],
+template <int W, int V>
+__device__ __forceinline__ void pre_act(const float (&w4)[W][V], const float (&cb)[V],
                                         const float (&x)[V], const float (&h)[3][V],
                                         float (&pre)[V]) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     float a = __builtin_fmaf(w4[0][v], x[v], cb[v]);
 #pragma unroll
-    for (int k = 1; k < kLags; ++k) a = __builtin_fmaf(w4[k][v], h[k - 1][v], a);
+    for (int k = 1; k < W; ++k) a = __builtin_fmaf(w4[k][v], h[k - 1][v], a);
     pre[v] = a;
   }
 }
 
-template <typename T, int V, bool RST>
+template <typename T, int V, int W, bool RST>
 __global__ __launch_bounds__(256) void tokconv_fwd_kernel(const TokConvParams p) {
   const int64_t nvec = p.dim / V;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -102,8 +102,8 @@ __global__ __launch_bounds__(256) void tokconv_fwd_kernel(const TokConvParams p)
   const int64_t b = run / p.tiles;
   const int64_t t0 = (run - b * p.tiles) * kFwdRun;
   const uint8_t* rst = RST ? p.reset + b * p.L : nullptr;
-  float w4[kLags][V], cb[V], h[3][V];
-  load_lags<V>(p.w, p.W, c, w4);
+  float w4[W][V], cb[V], h[3][V];
+  load_lags<W, V>(p.w, c, w4);
 #pragma unroll
   for (int v = 0; v < V; ++v) cb[v] = p.b ? p.b[c + v] : 0.0f;
   history<T, V, RST>(p, rst, b, t0, c, h);
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(256) void tokconv_fwd_kernel(const TokConvParams p)
       if (rst[t0 + j] != 0) clear<V>(h);
     float x[V], pre[V];
     r.get(x);
-    pre_act<V>(w4, cb, x, h, pre);
+    pre_act<W, V>(w4, cb, x, h, pre);
     push<V>(h, x);
 #pragma unroll
     for (int v = 0; v < V; ++v) pre[v] = silu(pre[v]);
@@ -136,8 +136,8 @@ __global__ __launch_bounds__(256) void tokconv_fwd_kernel(const TokConvParams p)
   }
   if (p.window_out && t0 + n == p.L) {
     // h holds the last three inputs of the sequence that goes on
-    for (int k = 0; k < p.W - 1; ++k)
-      store_vec<T, V>(p.window_out, (b * (p.W - 1) + (p.W - 2 - k)) * p.dim + c,
+    for (int k = 0; k < W - 1; ++k)
+      store_vec<T, V>(p.window_out, (b * (W - 1) + (W - 2 - k)) * p.dim + c,
                       k == 0 ? h[0] : k == 1 ? h[1] : h[2]);
   }
 }
@@ -149,26 +149,26 @@ __device__ __forceinline__ float dsilu(float a) {
 }
 
 // A block: 64 lanes of channels by 4 waves, each a run of kTokConvRun tokens.
-template <typename T, int V, bool RST>
+template <typename T, int V, int W, bool RST>
 __global__ __launch_bounds__(256) void tokconv_bwd_kernel(const TokConvParams p) {
-  __shared__ float red[4][kLags + 1][64 * V];
+  __shared__ float red[4][W + 1][64 * V];
   const int64_t ctiles = (p.dim + 64 * V - 1) / (64 * V);
   const int64_t tile = blockIdx.x / ctiles;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (blockIdx.x - tile * ctiles) * (64 * V) + lane * V;
   const int64_t b = tile / p.tiles;
   const int64_t t0 = (tile - b * p.tiles) * kTokConvTile + wave * kTokConvRun;
-  float dw[kLags][V], db[V];
+  float dw[W][V], db[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     db[v] = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kLags; ++k) dw[k][v] = 0.0f;
+    for (int k = 0; k < W; ++k) dw[k][v] = 0.0f;
   }
   if (c < p.dim && t0 < p.L) {
     const uint8_t* rst = RST ? p.reset + b * p.L : nullptr;
-    float w4[kLags][V], cb[V], h[3][V], acc[3][V];   // acc[k]: dx_{t-1-k} so far
-    load_lags<V>(p.w, p.W, c, w4);
+    float w4[W][V], cb[V], h[3][V], acc[3][V];   // acc[k]: dx_{t-1-k} so far
+    load_lags<W, V>(p.w, c, w4);
 #pragma unroll
     for (int v = 0; v < V; ++v) cb[v] = p.b ? p.b[c + v] : 0.0f;
     history<T, V, RST>(p, rst, b, t0, c, h);
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(256) void tokconv_bwd_kernel(const TokConvParams p)
             age = age < 3 ? age + 1 : 3;
           }
         }
-        pre_act<V>(w4, cb, x, h, pre);
+        pre_act<W, V>(w4, cb, x, h, pre);
 #pragma unroll
         for (int v = 0; v < V; ++v) g[v] *= dsilu(pre[v]);
         if (j < kTokConvRun) {
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(256) void tokconv_bwd_kernel(const TokConvParams p)
             db[v] += g[v];
             dw[0][v] = __builtin_fmaf(g[v], x[v], dw[0][v]);
 #pragma unroll
-            for (int k = 1; k < kLags; ++k) dw[k][v] = __builtin_fmaf(g[v], h[k - 1][v], dw[k][v]);
+            for (int k = 1; k < W; ++k) dw[k][v] = __builtin_fmaf(g[v], h[k - 1][v], dw[k][v]);
           }
         }
       }
@@ -211,8 +211,10 @@ __global__ __launch_bounds__(256) void tokconv_bwd_kernel(const TokConvParams p)
       float done[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        done[v] = (!RST || age >= 3) ? __builtin_fmaf(w4[3][v], g[v], acc[2][v]) : acc[2][v];
-        acc[2][v] = (!RST || age >= 2) ? __builtin_fmaf(w4[2][v], g[v], acc[1][v]) : acc[1][v];
+        done[v] = acc[2][v];
+        if constexpr (W > 3) done[v] = (!RST || age >= 3) ? __builtin_fmaf(w4[3][v], g[v], done[v]) : done[v];
+        acc[2][v] = acc[1][v];
+        if constexpr (W > 2) acc[2][v] = (!RST || age >= 2) ? __builtin_fmaf(w4[2][v], g[v], acc[2][v]) : acc[2][v];
         acc[1][v] = (!RST || age >= 1) ? __builtin_fmaf(w4[1][v], g[v], acc[0][v]) : acc[0][v];
         acc[0][v] = w4[0][v] * g[v];
       }
@@ -220,8 +222,8 @@ __global__ __launch_bounds__(256) void tokconv_bwd_kernel(const TokConvParams p)
       const int64_t s = t - 3;
       if (j >= 3) {
         if (s < p.L) store_vec<T, V>(p.dx, o0 + s * p.dim, done);
-      } else if (t0 == 0 && p.dwindow && s + p.W - 1 >= 0) {
-        store_vec<T, V>(p.dwindow, (b * (p.W - 1) + s + p.W - 1) * p.dim + c, done);
+      } else if (t0 == 0 && p.dwindow && s + W - 1 >= 0) {
+        store_vec<T, V>(p.dwindow, (b * (W - 1) + s + W - 1) * p.dim + c, done);
       }
     };
     auto load = [&](int j, Raw<T, V>& x, Raw<T, V>& g) {
@@ -256,17 +258,16 @@ __global__ __launch_bounds__(256) void tokconv_bwd_kernel(const TokConvParams p)
 #pragma unroll
   for (int v = 0; v < V; ++v) {
 #pragma unroll
-    for (int k = 0; k < kLags; ++k) red[wave][k][v * 64 + lane] = dw[k][v];
-    red[wave][kLags][v * 64 + lane] = db[v];
+    for (int k = 0; k < W; ++k) red[wave][k][v * 64 + lane] = dw[k][v];
+    red[wave][W][v * 64 + lane] = db[v];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < (kLags + 1) * 64 * V; i += 256) {
+  for (int i = threadIdx.x; i < (W + 1) * 64 * V; i += 256) {
     const int k = i / (64 * V), r = i - k * (64 * V);
     const int64_t ch = (blockIdx.x - tile * ctiles) * (64 * V) + (r & 63) * V + (r >> 6);
     const float sum = (red[0][k][r] + red[1][k][r]) + (red[2][k][r] + red[3][k][r]);
     // rows 0..W-1: dw by position (lag W-1-row), row W: db
-    if (ch < p.dim && (k < p.W || k == kLags))
-      p.part[(tile * (p.W + 1) + (k == kLags ? p.W : p.W - 1 - k)) * p.dim + ch] = sum;
+    if (ch < p.dim) p.part[(tile * (W + 1) + (k == W ? W : W - 1 - k)) * p.dim + ch] = sum;
   }
 }
 
@@ -290,7 +291,28 @@ __global__ __launch_bounds__(256) void tokconv_sum_kernel(const TokConvParams p)
   }
 }
 
-template <typename T, int V>
+// One token of every sequence.  What it costs is its latency, so it rounds each
+// product and sum by itself, the oldest input first, and takes the library's exp
+// and a true division: the bits that a chain of elementwise float operations
+// gives.  The result is rounded to the stored type and enters a state, where one
+// unit of bfloat16 would show.
+template <int W, int V>
+__device__ __forceinline__ void step_act(const float (&w4)[W][V], const float (&cb)[V],
+                                         const float (&x)[V], const float (&h)[3][V],
+                                         float (&out)[V]) {
+#pragma clang fp contract(off)
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float a = w4[W - 1][v] * h[W - 2][v];
+#pragma unroll
+    for (int k = W - 2; k >= 1; --k) a = a + w4[k][v] * h[k - 1][v];
+    a = a + w4[0][v] * x[v];
+    a = a + cb[v];
+    out[v] = a * (1.0f / (1.0f + expf(-a)));
+  }
+}
+
+template <typename T, int V, int W>
 __global__ __launch_bounds__(256) void tokconv_step_kernel(const TokConvStepParams p) {
   const int64_t nvec = p.dim / V;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -298,80 +320,107 @@ __global__ __launch_bounds__(256) void tokconv_step_kernel(const TokConvStepPara
   if (b >= p.batch) return;
   const int64_t c = (i - b * nvec) * V;
   const int64_t slot = p.slots ? (int64_t)p.slots[b] : b;
-  float pre[V];
+  float out[V];
   if (slot < 0 || slot >= p.pool) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) pre[v] = 0.0f;
-    store_vec<T, V>(p.out, b * p.dim + c, pre);
+    for (int v = 0; v < V; ++v) out[v] = 0.0f;
+    store_vec<T, V>(p.out, b * p.dim + c, out);
     return;
   }
-  const int64_t w0 = slot * (p.W - 1) * p.dim + c;
-  float w4[kLags][V], cb[V], x[V], h[3][V];
-  clear<V>(h);
+  const int64_t w0 = slot * (W - 1) * p.dim + c;
+  float w4[W][V], cb[V], x[V], h[3][V];
   load_vec<T, V>(p.x, b * p.x_batch + c, x);
 #pragma unroll
-  for (int k = 0; k < 3; ++k)
-    if (k < p.W - 1) load_vec<T, V>(p.window, w0 + (p.W - 2 - k) * p.dim, h[k]);
-  load_lags<V>(p.w, p.W, c, w4);
+  for (int k = 0; k < W - 1; ++k) load_vec<T, V>(p.window, w0 + (W - 2 - k) * p.dim, h[k]);
+  load_lags<W, V>(p.w, c, w4);
 #pragma unroll
   for (int v = 0; v < V; ++v) cb[v] = p.b ? p.b[c + v] : 0.0f;
-  pre_act<V>(w4, cb, x, h, pre);
-#pragma unroll
-  for (int v = 0; v < V; ++v) pre[v] = silu(pre[v]);
-  store_vec<T, V>(p.out, b * p.dim + c, pre);
+  step_act<W, V>(w4, cb, x, h, out);
+  store_vec<T, V>(p.out, b * p.dim + c, out);
   // the window moves on by one token
-  push<V>(h, x);
 #pragma unroll
-  for (int k = 0; k < 3; ++k)
-    if (k < p.W - 1) store_vec<T, V>(p.window, w0 + (p.W - 2 - k) * p.dim, h[k]);
+  for (int k = W - 2; k >= 1; --k) store_vec<T, V>(p.window, w0 + (W - 2 - k) * p.dim, h[k - 1]);
+  store_vec<T, V>(p.window, w0 + (W - 2) * p.dim, x);
 }
 
 unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); }
 
-template <typename T, int V>
-hipError_t fwd_tv(TokConvParams p, hipStream_t s) {
+template <typename T, int V, int W>
+hipError_t fwd_go(TokConvParams p, hipStream_t s) {
   p.tiles = (p.L + kFwdRun - 1) / kFwdRun;
   const dim3 grid(blocks_of(p.batch * p.tiles * (p.dim / V)));
-  if (p.reset) hipLaunchKernelGGL((tokconv_fwd_kernel<T, V, true>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((tokconv_fwd_kernel<T, V, false>), grid, dim3(256), 0, s, p);
+  if (p.reset) hipLaunchKernelGGL((tokconv_fwd_kernel<T, V, W, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((tokconv_fwd_kernel<T, V, W, false>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
-template <typename T, int V>
-hipError_t bwd_tv(const TokConvParams& p, hipStream_t s) {
+template <typename T, int V, int W>
+hipError_t bwd_go(const TokConvParams& p, hipStream_t s) {
   const int64_t ctiles = (p.dim + 64 * V - 1) / (64 * V);
   const dim3 grid((unsigned)(p.batch * p.tiles * ctiles));
-  if (p.reset) hipLaunchKernelGGL((tokconv_bwd_kernel<T, V, true>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((tokconv_bwd_kernel<T, V, false>), grid, dim3(256), 0, s, p);
+  if (p.reset) hipLaunchKernelGGL((tokconv_bwd_kernel<T, V, W, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((tokconv_bwd_kernel<T, V, W, false>), grid, dim3(256), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const unsigned sums = (unsigned)((p.W + 1) * ((p.dim + 31) / 32));
+  const unsigned sums = (unsigned)((W + 1) * ((p.dim + 31) / 32));
   hipLaunchKernelGGL(tokconv_sum_kernel, dim3(sums), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
-template <typename T, int V>
-hipError_t step_tv(const TokConvStepParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((tokconv_step_kernel<T, V>), dim3(blocks_of(p.batch * (p.dim / V))),
+template <typename T, int V, int W>
+hipError_t step_go(const TokConvStepParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((tokconv_step_kernel<T, V, W>), dim3(blocks_of(p.batch * (p.dim / V))),
                      dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
+// f.go<T, V, W>() for the call's type, vector length and width (2 to 4).
+template <typename T, int V, typename F>
+hipError_t by_width(int64_t W, const F& f) {
+  switch (W) {
+    case 2: return f.template go<T, V, 2>();
+    case 3: return f.template go<T, V, 3>();
+    case 4: return f.template go<T, V, 4>();
+  }
+  return hipErrorInvalidValue;
+}
+template <typename F>
+hipError_t by_type(int dtype, bool vec, int64_t W, const F& f) {
+  if (dtype == 0) return vec ? by_width<float, 4>(W, f) : by_width<float, 1>(W, f);
+  return vec ? by_width<bf16_t, 4>(W, f) : by_width<bf16_t, 1>(W, f);
+}
+
+struct Fwd {
+  const TokConvParams& p;
+  hipStream_t s;
+  template <typename T, int V, int W>
+  hipError_t go() const { return fwd_go<T, V, W>(p, s); }
+};
+struct Bwd {
+  const TokConvParams& p;
+  hipStream_t s;
+  template <typename T, int V, int W>
+  hipError_t go() const { return bwd_go<T, V, W>(p, s); }
+};
+struct Token {
+  const TokConvStepParams& p;
+  hipStream_t s;
+  template <typename T, int V, int W>
+  hipError_t go() const { return step_go<T, V, W>(p, s); }
+};
+
 }  // namespace
 
 hipError_t dispatch_tokconv_fwd(const TokConvParams& p, int dtype, hipStream_t s) {
-  if (dtype == 0) return p.vec ? fwd_tv<float, 4>(p, s) : fwd_tv<float, 1>(p, s);
-  return p.vec ? fwd_tv<bf16_t, 4>(p, s) : fwd_tv<bf16_t, 1>(p, s);
+  return by_type(dtype, p.vec, p.W, Fwd{p, s});
 }
 
 hipError_t dispatch_tokconv_bwd(const TokConvParams& p, int dtype, hipStream_t s) {
-  if (dtype == 0) return p.vec ? bwd_tv<float, 4>(p, s) : bwd_tv<float, 1>(p, s);
-  return p.vec ? bwd_tv<bf16_t, 4>(p, s) : bwd_tv<bf16_t, 1>(p, s);
+  return by_type(dtype, p.vec, p.W, Bwd{p, s});
 }
 
 hipError_t dispatch_tokconv_step(const TokConvStepParams& p, int dtype, hipStream_t s) {
-  if (dtype == 0) return p.vec ? step_tv<float, 4>(p, s) : step_tv<float, 1>(p, s);
-  return p.vec ? step_tv<bf16_t, 4>(p, s) : step_tv<bf16_t, 1>(p, s);
+  return by_type(dtype, p.vec, p.W, Token{p, s});
 }
 
 }  // namespace mscan

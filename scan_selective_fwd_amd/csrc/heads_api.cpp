@@ -126,6 +126,15 @@ int64_t pad_state(const mamba_heads_shape* s) {
 // 62.8 in two, 57.2 in eight; 4 x 512 take 76.7 in two, 81.0 in four, 91.2 in
 // eight.
 constexpr int64_t kTargetBlocks = 512;
+// The backward's states pass runs both directions at once.  In bfloat16 with
+// N > 64 it is bound by the states it writes, more blocks gain nothing, and the
+// chunks add an entering state where a segment does not begin the row: with 160
+// blocks for 256 2 x 2048 x 80 heads take 292 us for 308, 8 x 2048 x 24 333 for
+// 346.  Otherwise the products bound it: N = 64 takes 204 us for 196, float32 242
+// for 234.
+int64_t state_blocks(const mamba_heads_shape* s) {
+  return s->dtype == MAMBA_BF16 && s->dstate > 64 ? 160 : kTargetBlocks / 2;
+}
 // Blocks of the backward's chunks that run at once: one a CU, two where N <= 64
 // leaves them the LDS.
 int64_t chunk_blocks(const mamba_heads_shape* s) { return s->dstate <= 64 ? 512 : 256; }
@@ -179,7 +188,7 @@ struct BwdLayout {
 };
 
 bool bwd_layout(const mamba_heads_shape* s, BwdLayout* l) {
-  split(s, kTargetBlocks / 2, 2, &l->nseg, &l->seg_len);   // both directions run at once
+  split(s, state_blocks(s), 2, &l->nseg, &l->seg_len);
   const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
   const Map m = map_of(s);
   const int64_t bh = s->batch * s->heads, cols = bh * m.slices;

