@@ -6,7 +6,7 @@ namespace mscan {
 
 namespace {
 
-template <typename T>
+template <typename T, bool LOW>
 __global__ __launch_bounds__(256) void heads_scal_kernel(const HeadsParams p) {
   constexpr int Q = Mx<T>::Q;
   const int64_t chunks = (p.L + Q - 1) / Q;
@@ -22,7 +22,9 @@ __global__ __launch_bounds__(256) void heads_scal_kernel(const HeadsParams p) {
       (p.bias ? p.bias[h] : 0.0f);
   const int flag = p.reset ? p.reset[b * p.L + t] : 0;
   const Step st = make_step(raw, p.A[h], p.softplus != 0, p.zoh != 0);
-  float S = l < len ? st.lg : 0.0f;
+  // Sums in 64 bits: of two near each other far below zero the difference is the
+  // exponent of a weight near 1, and 32 bits would lose 1e-6 of it.
+  double S = l < len ? (double)st.lg : 0.0;
   const float w = l < len ? st.w : 0.0f;
   const uint64_t flags = __ballot(flag != 0 && l < len);
   const uint64_t upto = flags & ((2ull << l) - 1ull);
@@ -31,34 +33,40 @@ __global__ __launch_bounds__(256) void heads_scal_kernel(const HeadsParams p) {
   // sums restart at a flag: no value of one sequence enters another's
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const float x = __shfl_up(S, off);
+    const double x = __shfl_up(S, off);
     if (l - off >= start) S += x;
   }
-  const float end = __shfl(S, 63), tile_end = __shfl(S, l | 15);
+  const double end = __shfl(S, 63), tile_end = __shfl(S, l | 15);
+  const float high = (float)S, to_end = fast_exp2((float)(end - S));
   Scal<Q>* o = static_cast<Scal<Q>*>(p.scal) + id;
   if (l < Q) {
-    o->S[l] = S;
+    o->S[l] = high;
     o->w[l] = w;
-    o->c[l] = n == n_end ? fast_exp2(end - S) * w : 0.0f;
-    o->e[l] = n == 0 ? fast_exp2(S) : 0.0f;
-    o->g[l] = fast_exp2(tile_end - S) * w;
-    o->r[l] = n == n_end ? fast_exp2(end - S) : 0.0f;
+    o->c[l] = n == n_end ? to_end * w : 0.0f;
+    o->e[l] = n == 0 ? fast_exp2(high) : 0.0f;
+    o->g[l] = LOW ? (float)(S - (double)high) : fast_exp2((float)(tile_end - S)) * w;
+    o->r[l] = n == n_end ? to_end : 0.0f;
     o->id[l] = n;
   }
   if (l == 0) {
-    o->dec = n_end == 0 ? fast_exp2(end) : 0.0f;
+    o->dec = n_end == 0 ? fast_exp2((float)end) : 0.0f;
     o->flags = n_end;
   }
 }
 
 }  // namespace
 
-hipError_t dispatch_heads_scal(const HeadsParams& p, int dtype, hipStream_t s) {
+hipError_t dispatch_heads_scal(const HeadsParams& p, int dtype, bool low, hipStream_t s) {
   const int q = dtype == 0 ? Mx<float>::Q : Mx<bf16_t>::Q;
   const int64_t waves = p.batch * ((p.L + q - 1) / q) * p.H;
   const dim3 grid((unsigned)((waves + 3) / 4));
-  if (dtype == 0) hipLaunchKernelGGL((heads_scal_kernel<float>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((heads_scal_kernel<bf16_t>), grid, dim3(256), 0, s, p);
+  if (dtype == 0) {
+    if (low) hipLaunchKernelGGL((heads_scal_kernel<float, true>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((heads_scal_kernel<float, false>), grid, dim3(256), 0, s, p);
+  } else {
+    if (low) hipLaunchKernelGGL((heads_scal_kernel<bf16_t, true>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((heads_scal_kernel<bf16_t, false>), grid, dim3(256), 0, s, p);
+  }
   return hipGetLastError();
 }
 

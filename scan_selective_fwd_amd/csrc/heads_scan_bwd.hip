@@ -184,6 +184,26 @@ __device__ __forceinline__ float prefix(float v) {
   return v;
 }
 
+// The same over the 16 lanes of a row, and from its end.
+enum : int { kRowShl1 = 0x101, kRowShl2 = 0x102, kRowShl4 = 0x104, kRowShl8 = 0x108 };
+__device__ __forceinline__ float prefix16(float v) {
+  v += dpp_mov<kRowShr1>(0.0f, v);
+  v += dpp_mov<kRowShr2>(0.0f, v);
+  v += dpp_mov<kRowShr4>(0.0f, v);
+  v += dpp_mov<kRowShr8>(0.0f, v);
+  return v;
+}
+__device__ __forceinline__ float suffix16(float v) {
+  v += dpp_mov<kRowShl1>(0.0f, v);
+  v += dpp_mov<kRowShl2>(0.0f, v);
+  v += dpp_mov<kRowShl4>(0.0f, v);
+  v += dpp_mov<kRowShl8>(0.0f, v);
+  return v;
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+
 // Four consecutive elements of a tile as floats.
 template <typename T>
 __device__ __forceinline__ f32x4 four(const T* q) {
@@ -532,11 +552,13 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
 #pragma unroll
       for (int i = 0; i <= OFF; ++i) {
         const int s = 16 * st[i] + li, q = 16 * qt[i] + lg;
-        const float Ss = sc->S[s], ws = sc->w[s];
+        const float Ss = sc->S[s], Ls = sc->g[s], ws = sc->w[s];
         const f32x4 Sq = *reinterpret_cast<const f32x4*>(sc->S + q);
+        const f32x4 Lq = *reinterpret_cast<const f32x4*>(sc->g + q);
         f32x4 L;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) L[j] = i > 0 || q + j >= s ? fast_exp2(Sq[j] - Ss) : 0.0f;
+        for (int j = 0; j < 4; ++j) 
+          L[j] = i > 0 || q + j >= s ? fast_exp2((Sq[j] - Ss) + (Lq[j] - Ls)) : 0.0f;
         if (flagged)
 #pragma unroll
           for (int j = 0; j < 4; ++j) L[j] = sc->id[q + j] == sc->id[s] ? L[j] : 0.0f;
@@ -728,11 +750,20 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     const int li = ln.i, lg = 4 * ln.g, lane = li + 16 * ln.g;
       const int t = lane < Q ? lane : Q - 1, tr = Q - 1 - t;   // and from the end
       const bool in = lane < Q;
-      float rowS = 0.0f, colS = 0.0f, zi = 0.0f, wi = 0.0f;
+      const int tile = t / 16;
+      float row[QT], col[QT], rowO = 0.0f, colO = 0.0f, rowD = 0.0f, colD = 0.0f;
+      float zi = 0.0f, wi = 0.0f;
 #pragma unroll
       for (int i = 0; i < QT; ++i) {
-        rowS += i <= t / 16 ? sums.row[i][t] : 0.0f;
-        colS += i >= t / 16 ? sums.col[i][t] : 0.0f;
+        row[i] = sums.row[i][t];
+        col[i] = sums.col[i][t];
+      }
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        rowO += i < tile ? row[i] : 0.0f;
+        colO += i > tile ? col[i] : 0.0f;
+        rowD = i == tile ? row[i] : rowD;
+        colD = i == tile ? col[i] : colD;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -742,14 +773,28 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       const float w = sc->w[t];
       zi = in ? weigh(zi, sc->e[tr]) : 0.0f;
       wi = weigh(wi, sc->r[t]);
-      const float dw = colS + sums.diag[t] + wi;
-      // paths that start at a token less those that end there, and those that
-      // leave the chunk from it, before t; those that enter it, from t on
-      const float x = in ? w * (colS + wi) - rowS : 0.0f;
-      const float pre = prefix(x) - x, suf = __shfl(prefix(zi), tr);
+      const float dw = (colO + colD) + sums.diag[t] + wi;
+      // F: the paths that cross into t.  Those that leave the chunk from before t
+      // and those that enter it and end from t on ...
+      const float leave = in ? w * wi : 0.0f;
+      const float pre = prefix(leave) - leave, suf = __shfl(prefix(zi), tr);
+      // ... those between t's tile and others, and over it: sums without
+      // cancellation (starts less ends over the whole chunk lost 2e-6 of dA) ...
+      const float starts = in ? w * colO : 0.0f;
+      float F = suffix16(in ? rowO : 0.0f) + (prefix16(starts) - starts);
+      if constexpr (QT == 4) {
+        // read outside any branch: a lane that is off there may hold no value
+        const float r0 = prefix16(tile >= 2 ? row[0] : 0.0f);
+        const float r1 = prefix16(tile == 3 ? row[1] : 0.0f);
+        const float r02 = lane_value(r0, 47), r03 = lane_value(r0, 63), r13 = lane_value(r1, 63);
+        F += tile == 1 ? r02 + r03 : tile == 2 ? r03 + r13 : 0.0f;
+      }
+      // ... and within it, those that start before t less those that end there
+      const float x = in ? w * colD - rowD : 0.0f;
+      F += prefix16(x) - x;
       const float T4 =
           weigh((sums.gh[0] + sums.gh[1]) + (sums.gh[2] + sums.gh[3]), sc->dec);
-      float Fv = T4 + suf + pre;
+      float Fv = T4 + suf + pre + F;
       if (flagged && sc->id[t] != (t > 0 ? sc->id[t - 1] : 0)) Fv = 0.0f;
       if (lane < len) {
         const int64_t o = ((b * p.H + hd) * CB + mu % CB) * p.L + t0 + lane;
@@ -883,7 +928,7 @@ template <typename T, int NK, bool VEC>
 hipError_t bwd_go(const HeadsBwdParams& p, hipStream_t s) {
   constexpr int Q = Mx<T>::Q;
   const int dtype = sizeof(T) == 4 ? 0 : 1;
-  hipError_t e = dispatch_heads_scal(p, dtype, s);
+  hipError_t e = dispatch_heads_scal(p, dtype, true, s);
   if (e != hipSuccess) return e;
   const int64_t chunks = (p.L + Q - 1) / Q;
   const int64_t seg_blocks = p.batch * p.G * p.hblocks * p.nseg;

@@ -470,7 +470,7 @@ __global__ __launch_bounds__(256) void heads_carry_kernel(const HeadsFwdParams p
 template <typename T, int NK, bool VEC>
 hipError_t fwd_go(const HeadsFwdParams& p, hipStream_t s) {
   {
-    const hipError_t e = dispatch_heads_scal(p, sizeof(T) == 4 ? 0 : 1, s);
+    const hipError_t e = dispatch_heads_scal(p, sizeof(T) == 4 ? 0 : 1, false, s);
     if (e != hipSuccess) return e;
   }
   const int64_t blocks = p.batch * p.G * p.hblocks;
