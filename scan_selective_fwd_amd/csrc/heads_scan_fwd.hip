@@ -8,6 +8,15 @@
 // each one's end state from zero and its decay, a carry joins them, and the
 // output pass starts each segment from the state entering it.  Up to
 // kSelfCarry segments the output pass joins those before its own by itself.
+//
+// What bounds it: the phases of a chunk (stage, products of C and B, the state's
+// share, the chunk's own, the update), not HBM or the matrix units.  Two blocks
+// share a CU and a chunk of both takes 21 thousand clocks, of which a SIMD issues
+// VALU for 8, MFMA for 2.5 and the LDS serves 3.7.  One block of four slices
+// fills two heads of 64 channels, so that B and C are read by half as many blocks
+// (with the scalars made once: 167 -> 110 us).  8 x 2048 tokens, 24 heads of 64,
+// N = 128, bfloat16: 95 us in all (1.2 TB/s of what has to move, 136 TFLOP/s);
+// 131072 tokens of one row 594 us (1.5 TB/s).
 #include "heads_mma.hpp"
 
 namespace mscan {
@@ -141,6 +150,7 @@ __device__ __forceinline__ void decayed_products(const HeadsParams& p, int heads
   }
 }
 
+// The output pass; 65 us of the 95, 403 of the 594.
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const HeadsFwdParams p) {
   using F = FwdTiles<T, NK>;
@@ -366,7 +376,8 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
     store_state<NK>(p.last + (k.b * p.H + k.h) * (int64_t)p.P * p.N, k.c0, p.P, p.N, h);
 }
 
-// A segment's end state from zero and its decay.
+// A segment's end state from zero and its decay: the output pass's update alone,
+// which reads u and B and writes a state a segment; 30 us of the 95, 182 of the 594.
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const HeadsFwdParams p) {
   using F = FwdTiles<T, NK>;
@@ -428,7 +439,8 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const H
   if ((threadIdx.x & 63) == 0) p.seg_dec[slot] = dec;
 }
 
-// The state entering each segment, in place of the one before's end state.
+// The state entering each segment, in place of the one before's end state: four
+// floats a thread, bound by the trips to memory (42 segments of 24 heads: 13 us).
 template <int NK>
 __global__ __launch_bounds__(256) void heads_carry_kernel(const HeadsFwdParams p) {
   constexpr int PER = NK;   // blocks a slice: 1024 NK floats, four a thread
