@@ -105,6 +105,33 @@ def test_segments(ms, segments, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("segments", [8, 9, 10, 17])
+def test_where_a_pass_of_its_own_joins_the_segments(ms, segments, dtype):
+    """More segments than the output pass joins by itself, and as many."""
+    q = 32 if dtype == "f32" else 64
+    i = R.scan_inputs(41, DT[dtype], 2, q * segments - 5, 3, 40, 1, 48, h0=True, reset="edges")
+    out, last = run_fwd(ms, dev(i, DT[dtype]), segments=segments)
+    ro, rl = ref_fwd(i)
+    R.check("out", out, ro)
+    R.check("last_state", last, rl)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_strong_decays_keep_the_last_state(ms, dtype):
+    """Decays whose sum over a chunk is far below zero.  What reaches the state is
+    near its end, with weights near 1 whose exponents are differences of such
+    sums: 4 units of the step's softplus, 2 of the exponent, 2 of product and sum,
+    2 for the float32 rounding of the reference's inputs' sum, of 2^-24 each."""
+    i = R.scan_inputs(42, DT[dtype], 2, 256, 4, 64, 1, 128)
+    i["A"][:] = -16.0
+    i["delta_bias"][:] = -1.5
+    last = run_fwd(ms, dev(i, DT[dtype]), disc="euler")[1]
+    want = ref_fwd(i, disc="euler")[1]
+    e = (last.double().cpu() - want).norm() / want.norm()
+    assert float(e) <= 10 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("disc", ["zoh", "euler"])
 def test_growing_still_and_undecayed_heads(ms, disc, dtype):
     i = R.scan_inputs(15, DT[dtype], 2, 190, 6, 32, 1, 64, h0=True, A="mixed")
