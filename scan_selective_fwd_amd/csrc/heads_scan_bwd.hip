@@ -263,7 +263,9 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
   __shared__ __align__(16) T Xall[SIDE][Q * SX];
   __shared__ __align__(16) T Yall[SIDE][Q * SX];   // dout
   __shared__ __align__(16) T Zall[SIDE][F::Z];     // g, then h or the matrices
-  __shared__ __align__(16) T Hall[BOTH ? SIDE : 1][BOTH ? F::ZSTATE : 8];   // h
+  // h, then the low part of the second matrix
+  constexpr int HSIZE = F::ZSTATE > Q * SM ? F::ZSTATE : Q * SM;
+  __shared__ __align__(16) T Hall[BOTH ? SIDE : 1][BOTH ? HSIZE : 8];
   __shared__ Scal<Q> scall[SIDE];
   __shared__ BwdSums<Q> sums_all[SIDE];
   const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -538,7 +540,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     };
     if constexpr (BOTH) from_before();
     // dout_q . u_s, and from it K's sums and the two matrices of the chunk
-    u32x2 lg_hi[1 + OFF], lg_lo[1 + OFF], lr_hi[1 + OFF];   // bfloat16, packed
+    u32x2 lg_hi[1 + OFF], lg_lo[1 + OFF], lr_hi[1 + OFF], lr_lo[1 + OFF];   // bfloat16, packed
     f32x4 lg_f[1 + OFF], lr_f[1 + OFF];                     // float32
     {
     const Lane ln = lane_fresh();
@@ -604,6 +606,8 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
           lg_lo[i] = u32x2{pack_bf16(m1[0] - bf16_lo(lg_hi[i][0]), m1[1] - bf16_hi(lg_hi[i][0])),
                            pack_bf16(m1[2] - bf16_lo(lg_hi[i][1]), m1[3] - bf16_hi(lg_hi[i][1]))};
           lr_hi[i] = u32x2{pack_bf16(m2[0], m2[1]), pack_bf16(m2[2], m2[3])};
+          lr_lo[i] = u32x2{pack_bf16(m2[0] - bf16_lo(lr_hi[i][0]), m2[1] - bf16_hi(lr_hi[i][0])),
+                           pack_bf16(m2[2] - bf16_lo(lr_hi[i][1]), m2[3] - bf16_hi(lr_hi[i][1]))};
         } else {
           lg_f[i] = m1;
           lr_f[i] = m2;
@@ -626,11 +630,19 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     if (has_n) inter(u, Yall, true, dC);
     __syncthreads();
     // the chunk's matrices, rows s, columns q; the tiles beside the diagonal
-    // that a 32-step also reads are zero.  M1 in two parts: du weighs heads of
-    // very different steps, and a matrix rounded once shows in the larger terms.
+    // that a 32-step also reads are zero.  Both in two parts: du weighs heads of
+    // very different steps, and a matrix rounded once shows in the larger terms;
+    // of dB and dC it is nearly all, and rounded once made their error 1.4 times
+    // that of the stored type (for 3 % of the time).
     T* const M1 = Zs;
     T* const M2 = Zs + Q * SM;
     T* const M1b = Xs;          // u's tile is done with
+    auto low_of = [&](int x) -> T* {   // and h
+      if constexpr (BOTH) return Hall[x];
+      else return Zall[x] + 2 * Q * SM;
+    };
+    T* const M2b = low_of(side);
+    static_assert(PARTS > 1 || BOTH || F::Z >= 3 * Q * SM, "the low part fits");
     static_assert(SX >= SM, "the second part fits u's tile");
     {
     const Lane ln = lane_fresh();
@@ -643,6 +655,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
           *reinterpret_cast<u32x2*>(M1 + o) = lg_hi[i];
           *reinterpret_cast<u32x2*>(M1b + o) = lg_lo[i];
           *reinterpret_cast<u32x2*>(M2 + o) = lr_hi[i];
+          *reinterpret_cast<u32x2*>(M2b + o) = lr_lo[i];
         } else {
           put4<T>(M1 + o, lg_f[i]);
           put4<T>(M2 + o, lr_f[i]);
@@ -653,7 +666,10 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       const int o = (32 * z + 16 + li) * SM + 32 * z + lg;
       const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
       put4<T>(M1 + o, zero);
-      if constexpr (PARTS == 1) put4<T>(M1b + o, zero);
+      if constexpr (PARTS == 1) {
+        put4<T>(M1b + o, zero);
+        put4<T>(M2b + o, zero);
+      }
       put4<T>(M2 + o, zero);
     }
     }
@@ -689,8 +705,11 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
 #pragma unroll
       for (int x = 0; x < SIDE; ++x) {
         if (u + x >= u1) break;
-        const T* const m2 = Zall[x] + Q * SM;
         const Lane ln = lane_fresh();
+        // in bfloat16 its low part too: of a few tokens the matrix is all of dB, dC
+#pragma unroll
+        for (int part = 0; part < (PARTS == 1 ? 2 : 1); ++part) {
+        const T* const m2 = part == 0 ? Zall[x] + Q * SM : low_of(x);
 #pragma unroll
         for (int ks = 0; ks < Q / 32; ++ks) {
           Frag<PARTS> cf[NTW], bf[NTW], rf[QT], kf[QT];
@@ -723,6 +742,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
             }
           }
           phase();
+        }
         }
       }
     }
