@@ -18,7 +18,7 @@
 // zero, then their carries); the chunks, all independent, each block looping
 // over heads with dB and dC in registers; sums over the blocks' shares.
 //
-// 2 x 2048 tokens, 80 heads of 64, N = 128, bfloat16: 295 us in all.  Bound by the
+// 2 x 2048 tokens, 80 heads of 64, N = 128, bfloat16: 304 us in all.  Bound by the
 // states (335 MB written, then read) and by the phases of the chunks.
 #include "heads_mma.hpp"
 
@@ -111,7 +111,7 @@ __device__ __forceinline__ void states_of(const HeadsBwdParams& p, int block, T*
 }
 
 // Both directions in one launch, the update of the forward's pass; the state in
-// registers is written at every chunk: 102 us of the 295 (348 MB at 3.4 TB/s).
+// registers is written at every chunk: 98 us of the 304 (357 MB at 3.6 TB/s).
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_states_kernel(const HeadsBwdParams p) {
   using F = BwdTiles<T, NK>;
@@ -239,14 +239,14 @@ struct alignas(16) BwdSums {
 };
 
 // Heads a block takes side by side, 4 waves each.  With two, a wave holds half
-// of dB and dC and keeps its registers (2 x 2048 x 80 x 64, N = 128: 204 us, one
+// of dB and dC and keeps its registers (2 x 2048 x 80 x 64, N = 128: 207 us when tried, one
 // head 244).  N <= 64 has a tile of dB and dC for 4 waves at most, and two blocks
 // of one head fit a CU (4 x 777 x 16 in float32: 112 -> 100 us; 2 x 2048 x 80 in
 // bfloat16: 210 -> 201); N > 128 leaves LDS for one.
 template <int NK>
 constexpr int kSide = NK == 4 ? 2 : 1;
 
-// One chunk, its heads in turn: 177 us of the 295, 18 us a pair of heads, of which
+// One chunk, its heads in turn: 190 us of the 304, 19 us a pair of heads, of which
 // the matrix units are busy 2.5; the waits for the next states (up to 3) and the
 // phases between barriers, one block a CU, are the rest.
 template <typename T, int NK, bool VEC>
@@ -886,7 +886,7 @@ __device__ __forceinline__ void sum_splits(const HeadsBwdParams& p, int64_t n, i
 
 // One launch for what the chunks leave: dB and dC, and, in the blocks from `sums`
 // on, ddelta of every token from F and dw with a chunk's shares of dA, dD, dbias,
-// one wave a (batch row, chunk, head): 9 us of the 295.  Two launches took 3 us more.
+// one wave a (batch row, chunk, head): 9 us of the 304.  Two launches took 3 us more.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void heads_bwd_tail_kernel(const HeadsBwdParams p, int sums) {
   constexpr int Q = Mx<T>::Q;
