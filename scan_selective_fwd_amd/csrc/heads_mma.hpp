@@ -15,8 +15,9 @@
 // Precision.  bfloat16 inputs are exact operands.  A float32 operand (states,
 // decay-weighted inputs, float32 inputs) is the exact sum of three bfloat16
 // parts of 8 bits each; products of parts are kept down to 2^-24 of the whole,
-// so such a product is as good as float32's.  Where a result is stored in
-// bfloat16 one rounded part is used instead and said so.
+// so such a product is as good as float32's.  Where the result is stored in
+// bfloat16 two parts are used instead, which keep 2^-17 of the operand: the
+// result's own rounding, 2^-9, is then all that shows.
 #pragma once
 
 #include "heads_common.hpp"
@@ -65,7 +66,8 @@ __device__ __forceinline__ float top8(float x) {
   return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
 }
 
-// Eight floats as one rounded part, or as three exact ones.
+// Eight floats as one rounded part, as two (2^-17 of each is lost), or as three
+// exact ones.
 template <int NP>
 __device__ __forceinline__ Frag<NP> to_frag(const float (&x)[8]) {
   Frag<NP> f;
@@ -74,6 +76,16 @@ __device__ __forceinline__ Frag<NP> to_frag(const float (&x)[8]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) r[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
     f.v[0] = as_frag(r);
+  } else if constexpr (NP == 2) {
+    u32x4 r[2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = x[2 * j], b = x[2 * j + 1];
+      r[0][j] = pack_hi(a, b);
+      r[1][j] = pack_bf16(a - top8(a), b - top8(b));
+    }
+    f.v[0] = as_frag(r[0]);
+    f.v[1] = as_frag(r[1]);
   } else {
     static_assert(NP == 3, "NP");
     u32x4 r[3];

@@ -30,9 +30,18 @@ struct FwdTiles {
   static constexpr int SX = kCols + PADT, SB = NP + Mx<T>::PADB, SN = NP + PAD, SM = Q + PAD, QT = Q / 16;
   static constexpr int TILES = QT * (QT + 1) / 2;
   static constexpr int PARTS = Mx<T>::PARTS;
+  static constexpr int HP = PARTS == 1 ? 2 : 3;   // parts of the entering state
+  static constexpr int MP = PARTS == 1 ? 2 : 3;   // and of M
+  static constexpr int OFF = QT == 4 ? 2 : 1;     // M's tiles of a wave below the diagonal
+  // Where M's low parts wait (bfloat16): with N <= 64 in registers, to take the high
+  // parts' place after those are multiplied, as two blocks of four heads fit a CU only
+  // so (8 x 2048 x 48 heads of 32, N = 64: 89 us for 118); else C's place.
+  static constexpr bool TWICE = PARTS == 1 && NK <= 2;
+  using Low = u32x2[TWICE ? 4 : 1][1 + OFF];
 };
 
-// Dynamic LDS: the heads' scalars and, in the output pass, their M tiles.
+// Dynamic LDS: the heads' scalars and, in the output pass, their M tiles, then C's
+// tile, whose place M's low parts (bfloat16) take once C is done with.
 template <typename T>
 size_t scal_bytes(int hpw) {
   return (size_t)hpw * sizeof(Scal<Mx<T>::Q>);
@@ -41,34 +50,47 @@ template <typename T, int NK>
 size_t m_bytes(int hpw) {
   return (size_t)hpw * FwdTiles<T, NK>::Q * FwdTiles<T, NK>::SM * sizeof(T);
 }
-
-// The block's M tiles.  Wave w takes the diagonal tile w and up to two below.
 template <typename T, int NK>
-__device__ __forceinline__ void decayed_products(const HeadsParams& p, int heads, bool flagged,
-                                                 const T* Bs, const T* Cs,
-                                                 const Scal<Mx<T>::Q>* scal, T* Mall) {
-  using F = FwdTiles<T, NK>;
-  constexpr int Q = F::Q, SN = F::SN, SM = F::SM, QT = F::QT, PARTS = F::PARTS;
-  constexpr int OFF = QT == 4 ? 2 : 1;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+size_t c_bytes(int hpw) {
+  const size_t c = (size_t)FwdTiles<T, NK>::Q * FwdTiles<T, NK>::SN * sizeof(T);
+  const size_t m = FwdTiles<T, NK>::MP == 2 && !FwdTiles<T, NK>::TWICE ? m_bytes<T, NK>(hpw) : 0;
+  return c > m ? c : m;
+}
+
+// The tiles of M that a wave takes: the diagonal tile of its number and up to two
+// below: (3, wave) for waves 0..2 and (1, 0); then (2, wave) for waves 0, 1.
+template <int QT>
+struct MTiles {
+  static constexpr int OFF = QT == 4 ? 2 : 1;
   int qt[1 + OFF], st[1 + OFF];
   bool on[1 + OFF];
-  on[0] = wave < QT;
-  qt[0] = st[0] = on[0] ? wave : 0;
-  if constexpr (QT == 4) {
-    // (3, wave) for waves 0..2 and (1, 0); then (2, wave) for waves 0, 1
-    qt[1] = wave < 3 ? 3 : 1;
-    st[1] = wave < 3 ? wave : 0;
-    on[1] = true;
-    qt[2] = 2;
-    st[2] = wave & 1;
-    on[2] = wave < 2;
-  } else {
-    qt[1] = 1;
-    st[1] = 0;
-    on[1] = wave == 2;
+  __device__ __forceinline__ explicit MTiles(int wave) {
+    on[0] = wave < QT;
+    qt[0] = st[0] = on[0] ? wave : 0;
+    if constexpr (QT == 4) {
+      qt[1] = wave < 3 ? 3 : 1;
+      st[1] = wave < 3 ? wave : 0;
+      on[1] = true;
+      qt[2] = 2;
+      st[2] = wave & 1;
+      on[2] = wave < 2;
+    } else {
+      qt[1] = 1;
+      st[1] = 0;
+      on[1] = wave == 2;
+    }
   }
-  f32x4 a[1 + OFF][1][1];
+};
+
+// C_q . B_s of the wave's tiles (columns q, rows s).
+template <typename T, int NK>
+__device__ __forceinline__ void products(const T* Bs, const T* Cs,
+                                         f32x4 (&a)[1 + FwdTiles<T, NK>::OFF][1][1]) {
+  using F = FwdTiles<T, NK>;
+  constexpr int SN = F::SN, QT = F::QT, PARTS = F::PARTS, OFF = F::OFF;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const MTiles<QT> tiles(wave);
+  const int (&qt)[1 + OFF] = tiles.qt, (&st)[1 + OFF] = tiles.st;
   Frag<PARTS> bf[2][1 + OFF][1], cf[2][1 + OFF][1];
 #pragma unroll
   for (int i = 0; i <= OFF; ++i) {
@@ -89,7 +111,23 @@ __device__ __forceinline__ void decayed_products(const HeadsParams& p, int heads
 #pragma unroll
     for (int i = 0; i <= OFF; ++i) mma(a[i], bf[kk & 1][i], cf[kk & 1][i]);
   }
-  const int li = lane_i(), lg = 4 * lane_g();
+}
+
+// The block's M tiles from these, weighted for each head, as M's rows; in bfloat16
+// M's high parts, and its low ones to Low.
+template <typename T, int NK>
+__device__ __forceinline__ void decayed_products(
+    const HeadsParams& p, int heads, bool flagged,
+    const f32x4 (&a)[1 + FwdTiles<T, NK>::OFF][1][1], const Scal<Mx<T>::Q>* scal, T* Mall, T* Low,
+    typename FwdTiles<T, NK>::Low& low) {
+  using F = FwdTiles<T, NK>;
+  constexpr int Q = F::Q, SM = F::SM, QT = F::QT, OFF = F::OFF;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const MTiles<QT> tiles(wave);
+  const int (&qt)[1 + OFF] = tiles.qt, (&st)[1 + OFF] = tiles.st;
+  const bool (&on)[1 + OFF] = tiles.on;
+  const Lane ln = lane_fresh();
+  const int li = ln.i, lg = 4 * ln.g;
   auto weight = [&](int x) {
     const Scal<Q>& o = scal[x];
     float m[1 + OFF][4], Sq[1 + OFF], Se[1 + OFF];
@@ -132,23 +170,62 @@ __device__ __forceinline__ void decayed_products(const HeadsParams& p, int heads
     }
 #pragma unroll
     for (int i = 0; i <= OFF; ++i) {
+      u32x2 rest = {0, 0};
+      if constexpr (F::MP == 2)
+        rest = u32x2{pack_bf16(m[i][0] - top8(m[i][0]), m[i][1] - top8(m[i][1])),
+                     pack_bf16(m[i][2] - top8(m[i][2]), m[i][3] - top8(m[i][3]))};
+      if constexpr (F::TWICE) low[x][i] = rest;
       if (on[i]) {
-        T* Ms = Mall + x * Q * SM + (16 * qt[i] + li) * SM + 16 * st[i] + lg;
-        if constexpr (sizeof(T) == 2)   // rounded to bfloat16, as out is
-          *reinterpret_cast<u32x2*>(Ms) =
-              u32x2{pack_bf16(m[i][0], m[i][1]), pack_bf16(m[i][2], m[i][3])};
-        else
-          *reinterpret_cast<f32x4*>(Ms) = f32x4{m[i][0], m[i][1], m[i][2], m[i][3]};
+        const int o = x * Q * SM + (16 * qt[i] + li) * SM + 16 * st[i] + lg;
+        if constexpr (F::MP == 2) {
+          *reinterpret_cast<u32x2*>(Mall + o) =
+              u32x2{pack_hi(m[i][0], m[i][1]), pack_hi(m[i][2], m[i][3])};
+          if constexpr (!F::TWICE) *reinterpret_cast<u32x2*>(Low + o) = rest;
+        } else {
+          *reinterpret_cast<f32x4*>(Mall + o) = f32x4{m[i][0], m[i][1], m[i][2], m[i][3]};
+        }
+      }
+    }
+    // Low's tiles above the diagonal that a 32-step reads with the others
+    if constexpr (F::MP == 2 && !F::TWICE) {
+      if (wave >= 4 - QT / 2) {
+        const int z = 2 * (wave - (4 - QT / 2));
+        *reinterpret_cast<u32x2*>(Low + x * Q * SM + (16 * z + li) * SM + 16 * z + 16 + lg) =
+            u32x2{0, 0};
       }
     }
   };
   // two heads at a time: their reads and exponentials overlap
+  if constexpr (F::TWICE) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (x < heads) weight(x);
+  } else {
 #pragma unroll 1
-  for (int x = 0; x < heads; x += 2) {
-    weight(x);
-    if (x + 1 < heads) weight(x + 1);
+    for (int x = 0; x < heads; x += 2) {
+      weight(x);
+      if (x + 1 < heads) weight(x + 1);
+    }
   }
 }
+
+// M's low parts in place of the high ones.
+template <typename T, int NK>
+__device__ __forceinline__ void store_low(int heads, T* Mall,
+                                          const typename FwdTiles<T, NK>::Low& low) {
+  using F = FwdTiles<T, NK>;
+  const MTiles<F::QT> tiles(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+  const Lane ln = lane_fresh();
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    if (x < heads)
+#pragma unroll
+      for (int i = 0; i <= F::OFF; ++i)
+        if (tiles.on[i])
+          *reinterpret_cast<u32x2*>(Mall + x * F::Q * F::SM + (16 * tiles.qt[i] + ln.i) * F::SM +
+                                    16 * tiles.st[i] + 4 * ln.g) = low[x][i];
+}
+
 
 // The output pass; 65 us of the 95, 403 of the 594.
 template <typename T, int NK, bool VEC>
@@ -158,16 +235,16 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
   constexpr int PARTS = F::PARTS;
   __shared__ __align__(16) T Xs[Q * SX];
   __shared__ __align__(16) T Bs[Q * SB];
-  __shared__ __align__(16) T Cs[Q * SN];
   extern __shared__ __align__(16) char dyn[];
   Scal<Q>* const scal = reinterpret_cast<Scal<Q>*>(dyn);
   T* const Mall = reinterpret_cast<T*>(dyn + p.hpw * sizeof(Scal<Q>));
+  T* const Cs = Mall + p.hpw * Q * SM;
   const Place k = place_of(p, p.nseg);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t begin = (int64_t)k.seg * p.seg_len;
   const int64_t end = k.seg + 1 == p.nseg ? p.L : begin + p.seg_len;
   const int64_t ucol = (int64_t)k.h0 * p.P, ncols = (int64_t)k.g * p.N;
-  const int uwidth = (k.h0 + k.heads) * p.P, nwidth = (k.g + 1) * p.N;
+  const int uwidth = (k.h0 + k.heads) * p.P;
   const int sub = p.slices * kSlice, hh = wave / p.slices;
   const float D = p.D ? p.D[k.h] : 0.0f;
   const int64_t chunks = (p.L + Q - 1) / Q;
@@ -198,15 +275,16 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
   Stage<T, Q, NP, VEC> sb, sc;
   ScalStage<Q> ss;
   sx.init(p.u, ucol, sub, p.P, p.P, k.heads);
-  sb.init(p.B, ncols, NP, 0, p.N, 1);
-  sc.init(p.C, ncols, NP, 0, p.N, 1);
   auto rows = [&](int64_t t) { return end - t < Q ? (int)(end - t) : Q; };
+  auto row_of = [&](const Rows& r, int64_t t) {
+    return static_cast<const T*>(r.p) + k.b * r.batch + t * r.token + ncols;
+  };
   auto fetch = [&](int64_t t) {
     const int len = rows(t);
     ss.load(p.scal, (k.b * chunks + t / Q) * p.H + k.h0, k.heads);
     sx.load(p.u, k.b, t, len, ucol, p.P, uwidth);
-    sb.load(p.B, k.b, t, len, ncols, 0, nwidth);
-    sc.load(p.C, k.b, t, len, ncols, 0, nwidth);
+    sb.load_at(row_of(p.B, t), p.B.token, len, p.N);
+    sc.load_at(row_of(p.C, t), p.C.token, len, p.N);
   };
   fetch(begin);
   __syncthreads();
@@ -222,32 +300,46 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
     const Scal<Q>& me = scal[k.on ? hh : 0];
     const bool flagged = scal[0].flags != 0;   // flags are the batch row's
 
-    // M^T tiles (rows s, columns q) on and below the diagonal, stored as M's
-    // rows: C_q . B_s once for the block, weighted for each head.
-    decayed_products<T, NK>(p, k.heads, flagged, Bs, Cs, scal, Mall);
+    // M^T tiles (rows s, columns q) on and below the diagonal: C_q . B_s once for
+    // the block, weighted for each head
+    f32x4 cb[1 + F::OFF][1][1];
+    products<T, NK>(Bs, Cs, cb);
+    typename F::Low low;
+    constexpr bool IN_C = F::MP == 2 && !F::TWICE;   // M's low parts take C's place
+    if constexpr (!IN_C)
+      decayed_products<T, NK>(p, k.heads, flagged, cb, scal, Mall, nullptr, low);
     phase();
-    // out^T (rows p, columns q): the entering state's share.  The state is
-    // rounded to bfloat16 for it where out is.
+    // out^T (rows p, columns q): the entering state's share
     f32x4 y[2][QT];
 #pragma unroll
     for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
       for (int qt = 0; qt < QT; ++qt) y[pt][qt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (k.on) {
-      Frag<PARTS> cf[2][QT];
+      // two tiles of rows a step, their fragments loaded a step ahead
+      constexpr int PAIRS = QT / 2, STEPS = NK * PAIRS;
+      Frag<PARTS> cf[2][2];
+      auto load_c = [&](int i, Frag<PARTS> (&f)[2]) {
+        f[0] = load_rows<T>(Cs, SN, 32 * (i % PAIRS), 32 * (i / PAIRS));
+        f[1] = load_rows<T>(Cs, SN, 32 * (i % PAIRS) + 16, 32 * (i / PAIRS));
+      };
+      load_c(0, cf[0]);
+      Frag<F::HP> hf[2];
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) cf[0][qt] = load_rows<T>(Cs, SN, 16 * qt, 0);
-#pragma unroll
-      for (int kk = 0; kk < NK; ++kk) {
-        if (kk + 1 < NK) {
-#pragma unroll
-          for (int qt = 0; qt < QT; ++qt)
-            cf[(kk + 1) & 1][qt] = load_rows<T>(Cs, SN, 16 * qt, 32 * kk + 32);
+      for (int i = 0; i < STEPS; ++i) {
+        const int kk = i / PAIRS, qt = 2 * (i % PAIRS);
+        if (i + 1 < STEPS) load_c(i + 1, cf[(i + 1) & 1]);
+        if (i % PAIRS == 0) {
+          hf[0] = acc_frag<F::HP>(h[2 * kk][0], h[2 * kk + 1][0]);
+          hf[1] = acc_frag<F::HP>(h[2 * kk][1], h[2 * kk + 1][1]);
         }
-        const Frag<PARTS> hf[2] = {acc_frag<PARTS>(h[2 * kk][0], h[2 * kk + 1][0]),
-                                   acc_frag<PARTS>(h[2 * kk][1], h[2 * kk + 1][1])};
         phase();
-        mma(y, hf, cf[kk & 1]);
+        f32x4 yy[2][2] = {{y[0][qt], y[0][qt + 1]}, {y[1][qt], y[1][qt + 1]}};
+        mma(yy, hf, cf[i & 1]);
+        y[0][qt] = yy[0][0];
+        y[0][qt + 1] = yy[0][1];
+        y[1][qt] = yy[1][0];
+        y[1][qt + 1] = yy[1][1];
       }
       if (flagged) {
 #pragma unroll
@@ -268,32 +360,37 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
       }
     }
     __syncthreads();
-    if (flagged) {
-      clear_kept<T, Q, NP>(Bs, SB, scal[0].id, scal[0].flags);
-      __syncthreads();
-    }
+    if constexpr (IN_C) decayed_products<T, NK>(p, k.heads, flagged, cb, scal, Mall, Cs, low);
+    if (flagged) clear_kept<T, Q, NP>(Bs, SB, scal[0].id, scal[0].flags);
+    if (IN_C || flagged) __syncthreads();
+    // ... and the chunk's own inputs'
+    uint64_t marks[2] = {0, 0};
+    bool odd = false;
     if (k.on) {
-      // ... and the chunk's own inputs'
-      uint64_t marks[2] = {0, 0};
-      const bool odd = tile_odd<T, Q>(Xs, SX, k.col);
+      odd = tile_odd<T, Q>(Xs, SX, k.col);
       if (odd) {
 #pragma unroll
         for (int pt = 0; pt < 2; ++pt)
           marks[pt] = take_out<T, Q>(Xs, SX, k.col + 16 * pt + lane_i());
       }
-      const T* Ms = Mall + hh * Q * SM;
-      // (tile pair, 32-step): the first step reaches all rows, the second the last half
-      constexpr int STEPS = Q == 64 ? 3 : 1;
-      Frag<PARTS> xf[Q / 32][2], mf[2][2];
-#pragma unroll
-      for (int ks = 0; ks < Q / 32; ++ks)
-#pragma unroll
-        for (int pt = 0; pt < 2; ++pt)
-          xf[ks][pt] = load_cols<T>(Xs, SX, k.col + 16 * pt, 32 * ks);
-      auto load_m = [&](int i, Frag<PARTS> (&f)[2]) {
+    }
+    // (tile pair, 32-step): the first step reaches all rows, the second the last half
+    constexpr int STEPS = Q == 64 ? 3 : 1, MR = IN_C ? 2 : PARTS;   // parts read at a time
+    const T* const Ms = Mall + (k.on ? hh : 0) * Q * SM;
+    Frag<PARTS> xf[Q / 32][2];
+    auto within = [&]() {
+      Frag<MR> mf[2][2];
+      auto load_m = [&](int i, Frag<MR> (&f)[2]) {
         const int qt = i == 0 ? 0 : 2, ks = i == 2 ? 1 : 0;
-        f[0] = load_rows<T>(Ms, SM, 16 * qt, 32 * ks);
-        f[1] = load_rows<T>(Ms, SM, 16 * qt + 16, 32 * ks);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if constexpr (IN_C) {
+            f[c].v[0] = load_rows<T>(Ms, SM, 16 * qt + 16 * c, 32 * ks).v[0];
+            f[c].v[1] = load_rows<T>(Cs + hh * Q * SM, SM, 16 * qt + 16 * c, 32 * ks).v[0];
+          } else {
+            f[c] = load_rows<T>(Ms, SM, 16 * qt + 16 * c, 32 * ks);
+          }
+        }
       };
       load_m(0, mf[0]);
 #pragma unroll
@@ -308,6 +405,22 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
         y[1][qt] = yy[1][0];
         y[1][qt + 1] = yy[1][1];
       }
+    };
+    if (k.on) {
+#pragma unroll
+      for (int ks = 0; ks < Q / 32; ++ks)
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt)
+          xf[ks][pt] = load_cols<T>(Xs, SX, k.col + 16 * pt, 32 * ks);
+      within();
+    }
+    if constexpr (F::TWICE) {
+      __syncthreads();
+      store_low<T, NK>(k.heads, Mall, low);
+      __syncthreads();
+      if (k.on) within();
+    }
+    if (k.on) {
       if (odd) {
 #pragma unroll
         for (int pt = 0; pt < 2; ++pt)
@@ -328,14 +441,15 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
       T* const o0 = static_cast<T*>(p.out) + (k.b * p.L + t) * row + (int64_t)k.h * p.P + k.c0;
       // one offset a lane, the tiles' bases uniform; a chunk of out spans less
       // than 2^31 bytes
-      const uint32_t off = (uint32_t)opaque_int(
-          (int)((uint32_t)lane_i() * (uint32_t)(row * sizeof(T)) + 4u * lane_g() * sizeof(T)));
+      const Lane ln = lane_fresh();
+      const uint32_t off =
+          (uint32_t)ln.i * (uint32_t)(row * sizeof(T)) + 4u * (uint32_t)ln.g * sizeof(T);
 #pragma unroll
       for (int qt = 0; qt < QT; ++qt) {
-        const int q = 16 * qt + lane_i();
+        const int q = 16 * qt + ln.i;
 #pragma unroll
         for (int pt = 0; pt < 2; ++pt) {
-          const int c = 16 * pt + 4 * lane_g();
+          const int c = 16 * pt + 4 * ln.g;
           const T* ur = Xs + q * SX + k.col + c;
           float v[4];
           if constexpr (sizeof(T) == 2) {
@@ -499,7 +613,7 @@ hipError_t fwd_go(const HeadsFwdParams& p, hipStream_t s) {
       if (e != hipSuccess) return e;
     }
   }
-  const size_t lds = scal_bytes<T>(p.hpw) + m_bytes<T, NK>(p.hpw);
+  const size_t lds = scal_bytes<T>(p.hpw) + m_bytes<T, NK>(p.hpw) + c_bytes<T, NK>(p.hpw);
   hipLaunchKernelGGL((heads_fwd_kernel<T, NK, VEC>), dim3((unsigned)(blocks * p.nseg)), dim3(256),
                      lds, s, p);
   return hipGetLastError();

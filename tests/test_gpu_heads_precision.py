@@ -1,0 +1,36 @@
+"""How far the multi-head scan's results are from 64 bits.
+
+A bfloat16 result is rounded once.  What it is made of carries 32 bits, or two
+bfloat16 parts that keep 2^-17 of each operand: at most two such operands and
+float32 sums, together below 2^-15 of the result's 2-norm, 4 % of the 8e-4 or
+more that one rounding to bfloat16 leaves.  So a result's error is that of
+rounding the exact one, times 1.05 at most.
+"""
+import pytest
+import torch
+
+import heads_reference as R
+from test_gpu_heads import DT, check_bwd, dev, ms, ref_fwd, run_bwd, run_fwd  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# (batch, L, heads, P, groups, N): every width of the state, one to four heads a block
+SIZES = [(2, 257, 4, 64, 2, 128), (1, 300, 2, 128, 1, 256), (3, 130, 6, 48, 3, 80),
+         (1, 700, 8, 32, 1, 64), (2, 190, 8, 20, 2, 32), (1, 640, 1, 100, 1, 200)]
+ROUNDED_ONCE = 1.05
+
+
+def rounded_once(name, got, ref):
+    assert got.dtype == torch.bfloat16
+    least = (ref.to(torch.bfloat16).double() - ref).norm()
+    e = (got.double().cpu() - ref).norm()
+    assert float(e) <= ROUNDED_ONCE * float(least), (name, float(e / least))
+
+
+@pytest.mark.parametrize("reset", [None, "random"])
+@pytest.mark.parametrize("size", SIZES)
+def test_bfloat16_out_is_rounded_once(ms, size, reset):  # noqa: F811
+    i = R.scan_inputs(61, torch.bfloat16, *size, h0=True, reset=reset)
+    for segments in (0, 1):
+        out = run_fwd(ms, dev(i, torch.bfloat16), segments=segments)[0]
+        rounded_once("out", out, ref_fwd(i)[0])
