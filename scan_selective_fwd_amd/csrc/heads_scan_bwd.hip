@@ -256,16 +256,15 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
   constexpr int Q = F::Q, NP = F::NP, QT = F::QT, SX = F::SX, SN = F::SN, SM = F::SM;
   constexpr int PARTS = F::PARTS, SIDE = kSide<NK>, WAVES = 4 * SIDE;
   constexpr int NTW = 2 * NK > WAVES ? 2 * NK / WAVES : 1;   // tiles of dB, dC a wave
-  // room for both of a head's states: fewer barriers
-  constexpr bool BOTH = sizeof(T) == 2 && NK <= 4;
+  constexpr int ZP = PARTS == 1 ? 2 : PARTS;   // parts of a state, of a chunk's matrix
   __shared__ __align__(16) T Bs[Q * SN];
   __shared__ __align__(16) T Cs[Q * SN];
   __shared__ __align__(16) T Xall[SIDE][Q * SX];
   __shared__ __align__(16) T Yall[SIDE][Q * SX];   // dout
-  __shared__ __align__(16) T Zall[SIDE][F::Z];     // g, then h or the matrices
-  // h, then the low part of the second matrix
-  constexpr int HSIZE = F::ZSTATE > Q * SM ? F::ZSTATE : Q * SM;
-  __shared__ __align__(16) T Hall[BOTH ? SIDE : 1][BOTH ? HSIZE : 8];
+  __shared__ __align__(16) T Zall[SIDE][F::Z];     // g, then h, then the matrices
+  // in bfloat16 the states' low parts, then the second matrix's
+  constexpr int LSIZE = F::ZSTATE > Q * SM ? F::ZSTATE : Q * SM;
+  __shared__ __align__(16) T Lall[PARTS == 1 ? SIDE : 1][PARTS == 1 ? LSIZE : 8];
   __shared__ Scal<Q> scall[SIDE];
   __shared__ BwdSums<Q> sums_all[SIDE];
   const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -404,10 +403,6 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
   // acc += f Z^T tile^T of every side's unit (rows n, columns tokens), weighted
   // by token: what reaches dB from behind the chunk, dC from before it
   auto inter = [&](int u, const T (*tiles)[Q * SX], bool second, f32x4 (&acc)[NTW][QT]) {
-    auto state_tile = [&](int x) -> const T* {
-      if constexpr (BOTH) return second ? Hall[x] : Zall[x];
-      else return Zall[x];
-    };
 #pragma unroll
     for (int x = 0; x < SIDE; ++x) {
       if (u + x >= u1) break;
@@ -418,17 +413,24 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       for (int i = 0; i < NTW; ++i)
 #pragma unroll
         for (int j = 0; j < QT; ++j) t[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      Frag<PARTS> zf[2][NTW], xf[2][QT];
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
+        Frag<ZP> zf[NTW];
+        Frag<PARTS> xf[QT];
 #pragma unroll
-        for (int i = 0; i < NTW; ++i) zf[kk][i] = load_cols<T>(state_tile(x) + n0, SN, 16 * i, 32 * kk, ln);
+        for (int i = 0; i < NTW; ++i) {
+          if constexpr (PARTS == 1) {
+            zf[i].v[0] = load_cols<T>(Zall[x] + n0, SN, 16 * i, 32 * kk, ln).v[0];
+            zf[i].v[1] = load_cols<T>(Lall[x] + n0, SN, 16 * i, 32 * kk, ln).v[0];
+          } else {
+            zf[i] = load_cols<T>(Zall[x] + n0, SN, 16 * i, 32 * kk, ln);
+          }
+        }
 #pragma unroll
-        for (int j = 0; j < QT; ++j) xf[kk][j] = load_rows<T>(tiles[x], SX, 16 * j, 32 * kk, ln);
+        for (int j = 0; j < QT; ++j) xf[j] = load_rows<T>(tiles[x], SX, 16 * j, 32 * kk, ln);
+        phase();
+        mma(t, zf, xf);
       }
-      phase();
-      mma(t, zf[0], xf[0]);
-      mma(t, zf[1], xf[1]);
 #pragma unroll
       for (int j = 0; j < QT; ++j) {
         const float f = second ? scall[x].e[16 * j + li] : scall[x].c[16 * j + li];
@@ -460,11 +462,24 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       mma(acc, rf, bf[kk & 1]);
     }
   };
-  auto put_state = [&](T* tile, const f32x4 (&r)[2 * NK]) {
+  // a state's tile, rows p
+  auto put_state = [&](const f32x4 (&r)[2 * NK]) {
     const Lane ln = lane_fresh();
-    T* const q = tile + 16 * wave * SN + ln.i * SN + 4 * ln.g;
+    const int o = 16 * wave * SN + ln.i * SN + 4 * ln.g;
 #pragma unroll
-    for (int nt = 0; nt < 2 * NK; ++nt) put4<T>(q + 16 * nt, r[nt]);
+    for (int nt = 0; nt < 2 * NK; ++nt) {
+      if constexpr (PARTS == 1) {
+        // rounded, not cut as in project(): the compiler would keep the rests for both
+        const f32x4& v = r[nt];
+        const u32x2 hi = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        *reinterpret_cast<u32x2*>(Zs + o + 16 * nt) = hi;
+        *reinterpret_cast<u32x2*>(Lall[side] + o + 16 * nt) =
+            u32x2{pack_bf16(v[0] - bf16_lo(hi[0]), v[1] - bf16_hi(hi[0])),
+                  pack_bf16(v[2] - bf16_lo(hi[1]), v[3] - bf16_hi(hi[1]))};
+      } else {
+        put4<T>(Zs + o + 16 * nt, r[nt]);
+      }
+    }
   };
 
   for (int u = u0; u < u1; u += SIDE) {
@@ -482,14 +497,13 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     if (enters_back) add_entering(p.g_seg, p.g_pre[ch0 + hd], mu, g);
     if (enters) add_entering(p.h_seg, p.h_pre[ch0 + hd], mu, h);
 
-    // <g, h>; g rounded to the stored type for dB, rows p
+    // <g, h>; g's tile, for dB
     float gh = 0.0f;
 #pragma unroll
     for (int nt = 0; nt < 2 * NK; ++nt)
 #pragma unroll
       for (int j = 0; j < 4; ++j) gh = __builtin_fmaf(g[nt][j], h[nt][j], gh);
-    put_state(Zs, g);
-    if constexpr (BOTH) put_state(Hall[side], h);
+    put_state(g);
     // (g B_s)^T (rows p, columns s)
     f32x4 du[1][QT];
     project(g, Bs, du);
@@ -538,7 +552,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
         if (lane < 16) sums.out[wave][16 * q + li] = v;
       }
     };
-    if constexpr (BOTH) from_before();
+    if constexpr (PARTS == 1) from_before();
     // dout_q . u_s, and from it K's sums and the two matrices of the chunk
     u32x2 lg_hi[1 + OFF], lg_lo[1 + OFF], lr_hi[1 + OFF], lr_lo[1 + OFF];   // bfloat16, packed
     f32x4 lg_f[1 + OFF], lr_f[1 + OFF];                     // float32
@@ -619,14 +633,12 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     // their loads are the longest and come for all blocks at about one time
     if (more) fetch_state(p.g_chunk, mine(u + SIDE), g);
     if (has_n) inter(u, Xall, false, dB);
-    if constexpr (!BOTH) from_before();
-    if constexpr (!BOTH) {
-      __syncthreads();
-      put_state(Zs, h);
-      phase();
-    }
+    if constexpr (PARTS != 1) from_before();
+    __syncthreads();
+    put_state(h);
+    phase();
     if (more) fetch_state(p.h_chunk, mine(u + SIDE), h);
-    if constexpr (!BOTH) __syncthreads();
+    __syncthreads();
     if (has_n) inter(u, Yall, true, dC);
     __syncthreads();
     // the chunk's matrices, rows s, columns q; the tiles beside the diagonal
@@ -637,12 +649,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     T* const M1 = Zs;
     T* const M2 = Zs + Q * SM;
     T* const M1b = Xs;          // u's tile is done with
-    auto low_of = [&](int x) -> T* {   // and h
-      if constexpr (BOTH) return Hall[x];
-      else return Zall[x] + 2 * Q * SM;
-    };
-    T* const M2b = low_of(side);
-    static_assert(PARTS > 1 || BOTH || F::Z >= 3 * Q * SM, "the low part fits");
+    T* const M2b = Lall[PARTS == 1 ? side : 0];
     static_assert(SX >= SM, "the second part fits u's tile");
     {
     const Lane ln = lane_fresh();
@@ -709,7 +716,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
         // in bfloat16 its low part too: of a few tokens the matrix is all of dB, dC
 #pragma unroll
         for (int part = 0; part < (PARTS == 1 ? 2 : 1); ++part) {
-        const T* const m2 = part == 0 ? Zall[x] + Q * SM : low_of(x);
+        const T* const m2 = part == 0 ? Zall[x] + Q * SM : Lall[x];
 #pragma unroll
         for (int ks = 0; ks < Q / 32; ++ks) {
           Frag<PARTS> cf[NTW], bf[NTW], rf[QT], kf[QT];

@@ -34,3 +34,15 @@ def test_bfloat16_out_is_rounded_once(ms, size, reset):  # noqa: F811
     for segments in (0, 1):
         out = run_fwd(ms, dev(i, torch.bfloat16), segments=segments)[0]
         rounded_once("out", out, ref_fwd(i)[0])
+
+
+@pytest.mark.parametrize("reset", [None, "random"])
+@pytest.mark.parametrize("size", SIZES)
+def test_bfloat16_gradients_are_rounded_once(ms, size, reset):  # noqa: F811
+    i = R.scan_inputs(62, torch.bfloat16, *size, h0=True, reset=reset)
+    ref = R.scan_bwd(i["u"], i["delta"], i["A"], i["B"], i["C"], i["D"], i["delta_bias"],
+                     i["dout"], i["h0"], i["dlast"], i["reset"])[0]
+    for segments in (0, 1):
+        got = run_bwd(ms, dev(i, torch.bfloat16), segments=segments)
+        for k in ("du", "ddelta", "dB", "dC"):
+            rounded_once(k, got[k], ref[k])
