@@ -82,7 +82,7 @@ struct HeadsStepParams : HeadsParams {
   void* out;
 };
 
-hipError_t dispatch_heads_scal(const HeadsParams& p, int dtype, bool low, hipStream_t s);
+hipError_t dispatch_heads_scal(const HeadsParams& p, int dtype, bool bwd, hipStream_t s);
 hipError_t dispatch_heads_fwd(const HeadsFwdParams& p, int dtype, hipStream_t s);
 hipError_t dispatch_heads_bwd(const HeadsBwdParams& p, int dtype, hipStream_t s);
 hipError_t dispatch_heads_step(const HeadsStepParams& p, int dtype, hipStream_t s);

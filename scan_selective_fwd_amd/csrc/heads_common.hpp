@@ -114,8 +114,8 @@ struct Step {
 
 constexpr float kTinyA = 1e-30f;   // below it the ZOH weight is its limit, delta
 
-// The log2 decay is held at -150: 2^-150 is zero in float32, and a sum of
-// them stays small enough that differences keep their bits.
+// The log2 decay is held at -150: 2^-150 is zero in float32, and sums of them, made
+// in 64 bits and kept as two floats, stay finite with bits to spare.
 constexpr float kLgMin = -150.0f;
 
 __device__ __forceinline__ float step_weight(float dt, float A, bool zoh) {

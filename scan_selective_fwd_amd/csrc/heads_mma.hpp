@@ -394,7 +394,8 @@ struct alignas(16) Scal {
   float e[Q];    // weight of the entering state in the token's row (0 after a flag)
   float g[Q];    // forward: w times the decay to the end of the token's tile of 16;
                  // backward: what S lost when it was rounded
-  float r[Q];    // decay to the chunk's end (0 if a flag follows)
+  float r[Q];    // forward: what S lost; backward: decay to the chunk's end (0 if a
+                 // flag follows)
   int id[Q];     // flags up to the token
   float dec;     // weight of the entering state in the state at the chunk's end
   int flags;     // flags in the chunk

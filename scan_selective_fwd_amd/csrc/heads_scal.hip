@@ -8,7 +8,7 @@ namespace mscan {
 
 namespace {
 
-template <typename T, bool LOW>
+template <typename T, bool BWD>
 __global__ __launch_bounds__(256) void heads_scal_kernel(const HeadsParams p) {
   constexpr int Q = Mx<T>::Q;
   const int64_t chunks = (p.L + Q - 1) / Q;
@@ -46,8 +46,9 @@ __global__ __launch_bounds__(256) void heads_scal_kernel(const HeadsParams p) {
     o->w[l] = w;
     o->c[l] = n == n_end ? to_end * w : 0.0f;
     o->e[l] = n == 0 ? fast_exp2(high) : 0.0f;
-    o->g[l] = LOW ? (float)(S - (double)high) : fast_exp2((float)(tile_end - S)) * w;
-    o->r[l] = n == n_end ? to_end : 0.0f;
+    const float low = (float)(S - (double)high);
+    o->g[l] = BWD ? low : fast_exp2((float)(tile_end - S)) * w;
+    o->r[l] = !BWD ? low : n == n_end ? to_end : 0.0f;
     o->id[l] = n;
   }
   if (l == 0) {
@@ -58,15 +59,15 @@ __global__ __launch_bounds__(256) void heads_scal_kernel(const HeadsParams p) {
 
 }  // namespace
 
-hipError_t dispatch_heads_scal(const HeadsParams& p, int dtype, bool low, hipStream_t s) {
+hipError_t dispatch_heads_scal(const HeadsParams& p, int dtype, bool bwd, hipStream_t s) {
   const int q = dtype == 0 ? Mx<float>::Q : Mx<bf16_t>::Q;
   const int64_t waves = p.batch * ((p.L + q - 1) / q) * p.H;
   const dim3 grid((unsigned)((waves + 3) / 4));
   if (dtype == 0) {
-    if (low) hipLaunchKernelGGL((heads_scal_kernel<float, true>), grid, dim3(256), 0, s, p);
+    if (bwd) hipLaunchKernelGGL((heads_scal_kernel<float, true>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((heads_scal_kernel<float, false>), grid, dim3(256), 0, s, p);
   } else {
-    if (low) hipLaunchKernelGGL((heads_scal_kernel<bf16_t, true>), grid, dim3(256), 0, s, p);
+    if (bwd) hipLaunchKernelGGL((heads_scal_kernel<bf16_t, true>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((heads_scal_kernel<bf16_t, false>), grid, dim3(256), 0, s, p);
   }
   return hipGetLastError();

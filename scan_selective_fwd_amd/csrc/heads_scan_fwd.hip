@@ -130,25 +130,32 @@ __device__ __forceinline__ void decayed_products(
   const int li = ln.i, lg = 4 * ln.g;
   auto weight = [&](int x) {
     const Scal<Q>& o = scal[x];
-    float m[1 + OFF][4], Sq[1 + OFF], Se[1 + OFF];
+    float m[1 + OFF][4], Sq[1 + OFF], Lq[1 + OFF], Se[1 + OFF], Le[1 + OFF];
     f32x4 g[1 + OFF];
+    // differences of the sums with what their rounding lost: after a step that
+    // forgets nearly all the sums are large and the weights near 1 again
     const f32x4 Ss = *reinterpret_cast<const f32x4*>(o.S + 16 * st[0] + lg);
+    const f32x4 Ls = *reinterpret_cast<const f32x4*>(o.r + 16 * st[0] + lg);
     const f32x4 w = *reinterpret_cast<const f32x4*>(o.w + 16 * st[0] + lg);
 #pragma unroll
     for (int i = 0; i <= OFF; ++i) {
       Sq[i] = o.S[16 * qt[i] + li];
+      Lq[i] = o.r[16 * qt[i] + li];
       Se[i] = o.S[16 * st[i] + 15];
+      Le[i] = o.r[16 * st[i] + 15];
       g[i] = *reinterpret_cast<const f32x4*>(o.g + 16 * st[i] + lg);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      m[0][j] = lg + j <= li ? a[0][0][0][j] * (fast_exp2(Sq[0] - Ss[j]) * w[j]) : 0.0f;
+      m[0][j] = lg + j <= li
+                    ? a[0][0][0][j] * (fast_exp2((Sq[0] - Ss[j]) + (Lq[0] - Ls[j])) * w[j])
+                    : 0.0f;
     // Below the diagonal the decay is the product of two, to the end of s's
     // tile and on to q: with steps that are never negative neither leaves the
     // range that their product keeps.
 #pragma unroll
     for (int i = 1; i <= OFF; ++i) {
-      const float f = fast_exp2(Sq[i] - Se[i]);
+      const float f = fast_exp2((Sq[i] - Se[i]) + (Lq[i] - Le[i]));
 #pragma unroll
       for (int j = 0; j < 4; ++j) m[i][j] = a[i][0][0][j] * (g[i][j] * f);
     }
@@ -156,9 +163,10 @@ __device__ __forceinline__ void decayed_products(
 #pragma unroll
       for (int i = 1; i <= OFF; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          m[i][j] = a[i][0][0][j] *
-                    (fast_exp2(Sq[i] - o.S[16 * st[i] + lg + j]) * o.w[16 * st[i] + lg + j]);
+        for (int j = 0; j < 4; ++j) {
+          const int s = 16 * st[i] + lg + j;
+          m[i][j] = a[i][0][0][j] * (fast_exp2((Sq[i] - o.S[s]) + (Lq[i] - o.r[s])) * o.w[s]);
+        }
     }
     if (flagged) {
 #pragma unroll

@@ -46,3 +46,41 @@ def test_bfloat16_gradients_are_rounded_once(ms, size, reset):  # noqa: F811
         got = run_bwd(ms, dev(i, torch.bfloat16), segments=segments)
         for k in ("du", "ddelta", "dB", "dC"):
             rounded_once(k, got[k], ref[k])
+
+
+def forgetting(seed, dtype, kind, softplus):
+    """Steps that forget all that was before them among steps that keep nearly all:
+    the log decays' sums are far below zero where weights are near 1."""
+    b, L, H = 2, 200, 4
+    i = R.scan_inputs(seed, dtype, b, L, H, 64, 1, 128)
+    i["A"][:] = -16.0
+    i["delta_bias"][:] = 0.0
+    if kind == "alternating":
+        dt = torch.full((b, L, H), 0.01, dtype=torch.float64)
+        dt[:, ::2] = 8.0
+    elif kind == "one in eight":
+        dt = torch.full((b, L, H), 0.002, dtype=torch.float64)
+        dt[:, 3::8] = 20.0
+    else:
+        dt = torch.nn.functional.softplus(R.Inputs(seed + 1, dtype).seq(b, L, H, scale=3.0))
+    i["delta"] = (dt.expm1().log() if softplus else dt).to(dtype).double()
+    return i
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("disc", ["zoh", "euler"])
+@pytest.mark.parametrize("softplus", [True, False])
+@pytest.mark.parametrize("kind", ["alternating", "one in eight", "spread"])
+def test_out_under_forgetting_steps(ms, kind, softplus, disc, dtype):  # noqa: F811
+    """float32: units of 2^-24 for the step (4), its exponent (2), the weight and its
+    product (2), and the square root of the 160 terms that the two products sum (13)
+    for the rounding of their sums, rounded up to 32 for all of them."""
+    i = forgetting(63, DT[dtype], kind, softplus)
+    out, last = run_fwd(ms, dev(i, DT[dtype]), softplus=softplus, disc=disc)
+    want, want_last = ref_fwd(i, softplus=softplus, disc=disc)
+    if dtype == "bf16":
+        rounded_once("out", out, want)
+    for name, x, y in (("out", out, want), ("last", last, want_last)):
+        if x.dtype == torch.float32:
+            e = float((x.double().cpu() - y).norm() / y.norm())
+            assert e <= 32 * 2.0 ** -24, (name, e)
