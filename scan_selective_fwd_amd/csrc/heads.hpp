@@ -58,6 +58,7 @@ struct HeadsBwdParams : HeadsParams {
   float* dbias;          // nullable
   float* dh0;            // nullable
   int splits;            // blocks that share the heads of a chunk
+  int chunk;             // its tokens
   // workspace
   float* h_chunk;        // (batch, chunks, H, slices) states at the chunks' starts,
   float* g_chunk;        // adjoints behind their ends: from zero within a segment

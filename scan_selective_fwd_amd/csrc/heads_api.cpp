@@ -363,6 +363,7 @@ mamba_status mamba_heads_scan_bwd(const mamba_heads_shape* shape, const void* u,
   const Map m = map_of(shape);
   p.slices = (int)m.slices; p.hpw = (int)m.hpw; p.hblocks = (int)m.hblocks;
   p.nseg = l.nseg; p.seg_len = l.seg_len; p.splits = l.splits;
+  p.chunk = (int)chunk_len(shape);
   p.scal = ws + l.scal;
   p.h_chunk = f(l.h_chunk); p.g_chunk = f(l.g_chunk); p.h_pre = f(l.h_pre); p.g_pre = f(l.g_pre);
   p.h_seg = f(l.h_seg); p.g_seg = f(l.g_seg); p.h_dec = f(l.h_dec); p.g_dec = f(l.g_dec);

@@ -382,6 +382,19 @@ struct Stage {
 };
 
 // ---------------------------------------------------------------------------
+// Weights of what crosses a chunk.  One that a flag makes nothing is kBlocked:
+// nothing passes, whatever it would weigh.  A decay that underflows is 0 and still
+// multiplies, so that an infinity or NaN before it stays, as it does step by step.
+// ---------------------------------------------------------------------------
+constexpr float kBlocked = -0.0f;
+__device__ __forceinline__ bool blocked(float f) { return __float_as_uint(f) == 0x80000000u; }
+__device__ __forceinline__ float weigh(float x, float f) { return blocked(f) ? 0.0f : x * f; }
+// The weight of passing two.
+__device__ __forceinline__ float join(float a, float b) {
+  return blocked(a) || blocked(b) ? kBlocked : a * b;
+}
+
+// ---------------------------------------------------------------------------
 // The scalars of a head's chunk.  They are prepared once for all passes, one
 // token a lane: in the passes themselves the softplus, the exponentials and the
 // sum over the chunk kept three waves waiting for one.
@@ -390,12 +403,12 @@ template <int Q>
 struct alignas(16) Scal {
   float S[Q];    // sum of the log2 decays from the chunk's start, or from the last flag
   float w[Q];    // weight of the token's input
-  float c[Q];    // its weight in the state at the chunk's end (0 if a flag follows)
-  float e[Q];    // weight of the entering state in the token's row (0 after a flag)
+  float c[Q];    // its weight in the state at the chunk's end (blocked if a flag follows)
+  float e[Q];    // weight of the entering state in the token's row (blocked after a flag)
   float g[Q];    // forward: w times the decay to the end of the token's tile of 16;
                  // backward: what S lost when it was rounded
-  float r[Q];    // forward: what S lost; backward: decay to the chunk's end (0 if a
-                 // flag follows)
+  float r[Q];    // forward: what S lost; backward: decay to the chunk's end (blocked if
+                 // a flag follows)
   int id[Q];     // flags up to the token
   float dec;     // weight of the entering state in the state at the chunk's end
   int flags;     // flags in the chunk
@@ -426,9 +439,6 @@ struct ScalStage {
       if (i + 256 < n) q[i + 256] = v[1];
   }
 };
-
-// x weighted by f; 0 for a weight of 0, whatever x holds.
-__device__ __forceinline__ float weigh(float x, float f) { return f == 0.0f ? 0.0f : x * f; }
 
 // ---------------------------------------------------------------------------
 // Infinities and NaN.  A matrix product spreads one over its whole row and
@@ -577,10 +587,10 @@ __device__ __forceinline__ void store_state(float* st, int c0, int P, int N,
   }
 }
 
-// h <- dec h; zero where dec is, whatever h holds.  dec is the wave's.
+// h <- dec h.  dec is the wave's.
 template <int NK>
 __device__ __forceinline__ void decay_state(f32x4 (&h)[2 * NK][2], float dec) {
-  if (dec == 0.0f) {
+  if (blocked(dec)) {
     fill<NK>(h, 0.0f);
   } else {
 #pragma unroll

@@ -44,15 +44,16 @@ __global__ __launch_bounds__(256) void heads_scal_kernel(const HeadsParams p) {
   if (l < Q) {
     o->S[l] = high;
     o->w[l] = w;
-    o->c[l] = n == n_end ? to_end * w : 0.0f;
-    o->e[l] = n == 0 ? fast_exp2(high) : 0.0f;
+    // (the sum turns a -0 of a weight below zero into 0: that one underflowed)
+    o->c[l] = n == n_end ? to_end * w + 0.0f : kBlocked;
+    o->e[l] = n == 0 ? fast_exp2(high) : kBlocked;
     const float low = (float)(S - (double)high);
     o->g[l] = BWD ? low : fast_exp2((float)(tile_end - S)) * w;
-    o->r[l] = !BWD ? low : n == n_end ? to_end : 0.0f;
+    o->r[l] = !BWD ? low : n == n_end ? to_end : kBlocked;
     o->id[l] = n;
   }
   if (l == 0) {
-    o->dec = n_end == 0 ? fast_exp2((float)end) : 0.0f;
+    o->dec = n_end == 0 ? fast_exp2((float)end) : kBlocked;
     o->flags = n_end;
   }
 }

@@ -100,7 +100,7 @@ __device__ __forceinline__ void states_of(const HeadsBwdParams& p, int block, T*
 #pragma unroll
       for (int pt = 0; pt < 2; ++pt)
         if (marks[pt] != 0 && marked<Q>(marks[pt], me.id, REV ? 0 : me.flags)) spoil<NK>(h, pt);
-      pre *= me.dec;
+      pre = join(pre, me.dec);
     }
     __syncthreads();
   }
@@ -123,6 +123,20 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_states_kernel(cons
   const int half = gridDim.x / 2;
   if ((int)blockIdx.x < half) states_of<T, NK, VEC, false>(p, (int)blockIdx.x, Xs, Ks, scal);
   else states_of<T, NK, VEC, true>(p, (int)blockIdx.x - half, Xs, Ks, scal);
+}
+
+// The chunks leave out an entering state whose weight is 0, blocked or underflowed
+// (8 us of 328).  A non-finite one must still reach them: the underflowed weights of
+// its segment become the least float above 0.  Blocks of one head may write the same
+// weight, all of them this value.
+template <bool REV>
+__device__ __forceinline__ void let_pass(const HeadsBwdParams& p, int64_t bh, int seg) {
+  const int64_t b = bh / p.H, h = bh - b * p.H;
+  const int64_t q = p.chunk, chunks = (p.L + q - 1) / q, per = p.seg_len / q;
+  const int64_t end = (seg + 1) * per < chunks ? (seg + 1) * per : chunks;
+  float* const pre = (REV ? p.g_pre : p.h_pre) + b * chunks * p.H + h;
+  for (int64_t c = seg * per + (threadIdx.x & 63); c < end; c += 64)
+    if (__float_as_uint(pre[c * p.H]) == 0) pre[c * p.H] = __uint_as_float(1);
 }
 
 // What enters each segment, in place of what the one before left: states from
@@ -151,6 +165,8 @@ __device__ __forceinline__ void carry_of(const HeadsBwdParams& p, int64_t block)
     const f32x4 s = st[k * STEP];
     const float d = dec[k];
     st[k * STEP] = h;
+    if (__any(not_finite(h[0]) || not_finite(h[1]) || not_finite(h[2]) || not_finite(h[3])))
+      let_pass<REV>(p, bh, k);
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[j] = weigh(h[j], d) + s[j];
   }
@@ -325,7 +341,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       for (int nt = 0; nt < 2 * NK; ++nt) r[nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
   };
-  // adds the segment's entering state or adjoint
+  // adds the segment's entering state or adjoint, unless its weight is nothing
   auto add_entering = [&](const float* base, float pre, int u, f32x4 (&r)[2 * NK]) {
     if (pre != 0.0f && slice_of(u) < p.slices) {
       const float* st = base + (((b * p.H + head_of(u)) * p.slices + slice_of(u)) * (int64_t)p.nseg + seg) *
@@ -580,22 +596,23 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
         const float Ss = sc->S[s], Ls = sc->g[s], ws = sc->w[s];
         const f32x4 Sq = *reinterpret_cast<const f32x4*>(sc->S + q);
         const f32x4 Lq = *reinterpret_cast<const f32x4*>(sc->g + q);
+        bool in[4];     // whether s reaches q: not before it, nor across a flag
         f32x4 L;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) 
-          L[j] = i > 0 || q + j >= s ? fast_exp2((Sq[j] - Ss) + (Lq[j] - Ls)) : 0.0f;
+        for (int j = 0; j < 4; ++j) in[j] = i > 0 || q + j >= s;
         if (flagged)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) L[j] = sc->id[q + j] == sc->id[s] ? L[j] : 0.0f;
+          for (int j = 0; j < 4; ++j) in[j] = in[j] && sc->id[q + j] == sc->id[s];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) L[j] = fast_exp2((Sq[j] - Ss) + (Lq[j] - Ls));
         float colsum = 0.0f, dg = 0.0f;
         f32x4 k, m1, m2;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float G = cb[i][0][0][j], R = a[i][0][0][j];
-          const bool in = L[j] != 0.0f;
-          m1[j] = in ? G * L[j] : 0.0f;
-          m2[j] = in ? R * L[j] * ws : 0.0f;
-          const float kn = in ? m1[j] * R : 0.0f;
+          m1[j] = in[j] ? G * L[j] : 0.0f;
+          m2[j] = in[j] ? R * L[j] * ws : 0.0f;
+          const float kn = in[j] ? m1[j] * R : 0.0f;
           if (i == 0 && q + j == s) {
             dg = kn;
             k[j] = 0.0f;

@@ -551,7 +551,7 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const H
 #pragma unroll
       for (int pt = 0; pt < 2; ++pt)
         if (marks[pt] != 0 && marked<Q>(marks[pt], me.id, me.flags)) spoil<NK>(h, pt);
-      dec *= me.dec;
+      dec = join(dec, me.dec);
     }
     __syncthreads();
   }
