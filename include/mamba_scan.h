@@ -509,7 +509,10 @@ mamba_status mamba_scan_bwd_complex_ex(const void* u, const void* delta, const f
  * in wider loads).  A of any sign.  reset (nullable, (batch, seqlen) bytes):
  * the state entering a flagged step is zero, as for mamba_scan_fwd_varlen.
  * Non-finite values: one in a token of a packed sequence never reaches
- * another sequence's rows, nor earlier rows of its own, in the forward.
+ * another sequence's rows, nor, in the forward, earlier rows of its own; what
+ * follows it in its sequence it reaches also through decays that underflow.
+ * In the backward it may reach all of its sequence's gradients, and the sums
+ * over tokens (dA, dD, ddelta_bias).
  * ------------------------------------------------------------------------ */
 typedef struct mamba_heads_shape {
   int64_t batch, seqlen, heads, headdim, groups, dstate;

@@ -135,6 +135,10 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[R][C], const Frag<NA> (&a)[R],
 // A thread's place among the 256 that stage a tile together.
 __device__ __forceinline__ int tid256() { return (int)(threadIdx.x & 255); }
 
+__device__ __forceinline__ bool not_finite(float x) {
+  return !(__builtin_fabsf(x) < __builtin_inff());
+}
+
 // Keeps the scheduler from moving one phase's loads into another, where they
 // would only hold registers.
 __device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
@@ -365,6 +369,18 @@ struct Stage {
       }
     }
   }
+  // Whether a value is infinite or NaN.
+  __device__ __forceinline__ bool odd() const {
+    bool r = false;
+#pragma unroll
+    for (int k = 0; k < COUNT; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r = r || not_finite(__uint_as_float(v[k][i]));     // bfloat16: the upper one
+        if constexpr (sizeof(T) == 2) r = r || not_finite(bf16_lo(v[k][i]));
+      }
+    return r;
+  }
   __device__ __forceinline__ void store(T* tile, int stride) const {
     const int t = opaque_int(tid256());
     T* q = tile + (t / PER_ROW) * stride + (t % PER_ROW) * V;
@@ -430,6 +446,15 @@ struct ScalStage {
       if (heads * PIECES > 256) v[1] = buf.load(o + 256 * 16);
     }
   }
+  // Whether a scalar is infinite or NaN (the numbers of flags never look so).
+  __device__ __forceinline__ bool odd() const {
+    bool r = false;
+#pragma unroll
+    for (int k = 0; k < COUNT; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r = r || not_finite(__uint_as_float(v[k][i]));
+    return r;
+  }
   __device__ __forceinline__ void store(Scal<Q>* lds, int heads) const {
     u32x4* q = reinterpret_cast<u32x4*>(lds);
     const int n = heads * PIECES;
@@ -449,10 +474,6 @@ struct ScalStage {
 // with flags the rows of B that a flag keeps from the state are cleared when
 // they hold one.  All other rows keep the bits they have without it.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ bool not_finite(float x) {
-  return !(__builtin_fabsf(x) < __builtin_inff());
-}
-
 // The marks of column c of a tile (bit q: row q), its values taken out.
 template <typename T, int Q>
 __device__ __forceinline__ uint64_t take_out(T* tile, int stride, int c) {

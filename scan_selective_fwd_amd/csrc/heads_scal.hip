@@ -55,6 +55,7 @@ __global__ __launch_bounds__(256) void heads_scal_kernel(const HeadsParams p) {
   if (l == 0) {
     o->dec = n_end == 0 ? fast_exp2((float)end) : kBlocked;
     o->flags = n_end;
+    o->pad[0] = o->pad[1] = 0.0f;
   }
 }
 

@@ -20,6 +20,8 @@
 //
 // 2 x 2048 tokens, 80 heads of 64, N = 128, bfloat16: 304 us in all.  Bound by the
 // states (335 MB written, then read) and by the phases of the chunks.
+#include <type_traits>
+
 #include "heads_mma.hpp"
 
 namespace mscan {
@@ -283,6 +285,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
   __shared__ __align__(16) T Lall[PARTS == 1 ? SIDE : 1][PARTS == 1 ? LSIZE : 8];
   __shared__ Scal<Q> scall[SIDE];
   __shared__ BwdSums<Q> sums_all[SIDE];
+  __shared__ int odd_all[WAVES];
   const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int side = wave8 >> 2, wave = wave8 & 3;
   const int lane = threadIdx.x & 63, li = lane_i(), lg = 4 * lane_g();
@@ -355,22 +358,28 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       }
     }
   };
+  const int flags = static_cast<const Scal<Q>*>(p.scal)[ch0 + head_of(u0)].flags;   // the batch row's
+  const bool flagged = flags != 0;
   const bool enters = seg > 0 || p.h0 != nullptr;
   const bool enters_back = seg + 1 < p.nseg || p.dlast != nullptr;
 
+  const T* const kb = static_cast<const T*>(p.B.p) + b * p.B.batch + t0 * p.B.token + (int64_t)grp * p.N;
+  const T* const kc = static_cast<const T*>(p.C.p) + b * p.C.batch + t0 * p.C.token + (int64_t)grp * p.N;
+  bool keys_odd = false;
   {
     Stage<T, Q, NP, VEC> sb;
-    const T* const kb = static_cast<const T*>(p.B.p) + b * p.B.batch + t0 * p.B.token + (int64_t)grp * p.N;
-    const T* const kc = static_cast<const T*>(p.C.p) + b * p.C.batch + t0 * p.C.token + (int64_t)grp * p.N;
     if (SIDE == 1 || side == 0) {
       sb.load_at(kb, p.B.token, len, p.N);
       sb.store(Bs, SN);
+      if (flagged) keys_odd = sb.odd();
     }
     if (SIDE == 1 || side == 1) {
       sb.load_at(kc, p.C.token, len, p.N);
       sb.store(Cs, SN);
+      if (flagged) keys_odd = sb.odd() || keys_odd;
     }
   }
+  keys_odd = __any(keys_odd);
   fetch(mine(u0));
   fetch_state(p.g_chunk, mine(u0), g);
   fetch_state(p.h_chunk, mine(u0), h);
@@ -447,6 +456,16 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
         phase();
         mma(t, zf, xf);
       }
+      if (flagged) {
+#pragma unroll
+        for (int j = 0; j < QT; ++j) {
+          const bool off = blocked(second ? scall[x].e[16 * j + li] : scall[x].c[16 * j + li]);
+#pragma unroll
+          for (int i = 0; i < NTW; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[i][j][e] = off ? 0.0f : t[i][j][e];
+        }
+      }
 #pragma unroll
       for (int j = 0; j < QT; ++j) {
         const float f = second ? scall[x].e[16 * j + li] : scall[x].c[16 * j + li];
@@ -498,28 +517,66 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     }
   };
 
-  for (int u = u0; u < u1; u += SIDE) {
+  // B and C of sequence number n of the chunk alone, zeros for the others' rows; of
+  // all for n < 0.  Element by element: seldom used.
+  auto copy_keys = [&](int n) {
+#pragma unroll 1
+    for (int i = opaque_int((int)threadIdx.x); i < Q * NP; i += 256 * SIDE) {
+      const int r = i / NP, c = i - r * NP;
+      const bool keep = r < len && c < p.N && (n < 0 || scall[0].id[r] == n);
+      Bs[r * SN + c] = keep ? kb[r * p.B.token + c] : T(0);
+      Cs[r * SN + c] = keep ? kc[r * p.C.token + c] : T(0);
+    }
+  };
+
+  // Where a chunk with flags holds an infinity or NaN the products would carry it
+  // into the other sequences' rows: such a chunk's sequences are taken one by one,
+  // the others' rows zero and their weights blocked.
+  int pass = 0;
+  for (int u = u0; u < u1;) {
     const int mu = mine(u);
     const bool live = u + side < u1;
     const int hd = head_of(mu), c0 = (mu % CB) * 64;
     const float D = p.D ? p.D[hd] : 0.0f;
-    sx.store(Xs, SX);
-    sy.store(Ys, SX);
-    ss.store(sc, 1);
-    __syncthreads();
-    const bool more = u + SIDE < u1;
-    if (more) fetch(mine(u + SIDE));
-    const bool flagged = scall[0].flags != 0;       // flags are the batch row's
     if (enters_back) add_entering(p.g_seg, p.g_pre[ch0 + hd], mu, g);
     if (enters) add_entering(p.h_seg, p.h_pre[ch0 + hd], mu, h);
-
-    // <g, h>; g's tile, for dB
-    float gh = 0.0f;
+    float gh = 0.0f;    // <g, h>
 #pragma unroll
     for (int nt = 0; nt < 2 * NK; ++nt)
 #pragma unroll
       for (int j = 0; j < 4; ++j) gh = __builtin_fmaf(g[nt][j], h[nt][j], gh);
-    put_state(g);
+    if (flagged) {
+      const int odd = __any(keys_odd || sx.odd() || sy.odd() || ss.odd() || not_finite(gh));
+      if ((opaque_int((int)threadIdx.x) & 63) == 0) odd_all[wave8] = odd;
+    }
+    sx.store(Xs, SX);
+    sy.store(Ys, SX);
+    ss.store(sc, 1);
+    __syncthreads();
+    if (u + SIDE < u1) fetch(mine(u + SIDE));
+    bool odd = false;
+    if (flagged) {
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) odd = odd || odd_all[i] != 0;
+      odd = __builtin_amdgcn_readfirstlane(odd);
+    }
+    if (odd) {
+      const int t = opaque_int(tid256());
+#pragma unroll 1
+      for (int i = t; i < Q * 64; i += 256)
+        if (sc->id[i / 64] != pass) Xs[i / 64 * SX + i % 64] = Ys[i / 64 * SX + i % 64] = T(0);
+      if (t < Q && sc->id[t] != pass) {
+        sc->e[t] = sc->c[t] = sc->r[t] = kBlocked;
+        sc->S[t] = sc->g[t] = sc->w[t] = 0.0f;
+      }
+      copy_keys(pass);
+      if (pass < flags) fetch(mu);    // once more, for the next sequence
+      __syncthreads();
+    }
+    const bool again = odd && pass < flags;
+    const int next = again ? u : u + SIDE;
+    const bool more = next < u1;
+    put_state(g);    // for dB
     // (g B_s)^T (rows p, columns s)
     f32x4 du[1][QT];
     project(g, Bs, du);
@@ -541,7 +598,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       if (lane < 16) sums.in[wave][16 * s + li] = v;
       const float r = sc->r[16 * s + li];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) du[0][s][j] *= r;
+      for (int j = 0; j < 4; ++j) du[0][s][j] = weigh(du[0][s][j], r);
     }
     gh = sum_wave(gh);
     ud = sum_wave(ud);
@@ -602,7 +659,8 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
         for (int j = 0; j < 4; ++j) in[j] = i > 0 || q + j >= s;
         if (flagged)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) in[j] = in[j] && sc->id[q + j] == sc->id[s];
+          for (int j = 0; j < 4; ++j)
+            in[j] = in[j] && sc->id[q + j] == sc->id[s] && (!odd || sc->id[s] == pass);
 #pragma unroll
         for (int j = 0; j < 4; ++j) L[j] = fast_exp2((Sq[j] - Ss) + (Lq[j] - Ls));
         float colsum = 0.0f, dg = 0.0f;
@@ -648,13 +706,13 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     __syncthreads();
     // the next heads' states take these registers as soon as they are free:
     // their loads are the longest and come for all blocks at about one time
-    if (more) fetch_state(p.g_chunk, mine(u + SIDE), g);
+    if (more) fetch_state(p.g_chunk, mine(next), g);
     if (has_n) inter(u, Xall, false, dB);
     if constexpr (PARTS != 1) from_before();
     __syncthreads();
     put_state(h);
     phase();
-    if (more) fetch_state(p.h_chunk, mine(u + SIDE), h);
+    if (more) fetch_state(p.h_chunk, mine(next), h);
     __syncthreads();
     if (has_n) inter(u, Yall, true, dC);
     __syncthreads();
@@ -725,7 +783,13 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
     }
     }
     // dB (from C, rows of M2) and dC (from B, columns of M2) within the chunk
-    if (has_n) {
+    // of one sequence alone the others' columns are left as they are: zeros times what
+    // it holds may not be zero
+    auto within = [&](auto apart) {
+      auto put = [&](f32x4& to, const f32x4& v, bool keep) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e] = !apart || keep ? v[e] : to[e];
+      };
 #pragma unroll
       for (int x = 0; x < SIDE; ++x) {
         if (u + x >= u1) break;
@@ -751,17 +815,18 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
           for (int i = 0; i < NTW; ++i) {
 #pragma unroll
             for (int s = 0; s < QT; ++s) {
+              const bool keep = !apart || scall[x].id[16 * s + ln.i] == pass;
               if (s < 2 * ks + 2) {
                 f32x4 d[1][1] = {{dB[i][s]}};
                 mma(d, *reinterpret_cast<const Frag<PARTS>(*)[1]>(&cf[i]),
                     *reinterpret_cast<const Frag<PARTS>(*)[1]>(&rf[s]));
-                dB[i][s] = d[0][0];
+                put(dB[i][s], d[0][0], keep);
               }
               if (s >= 2 * ks) {
                 f32x4 d[1][1] = {{dC[i][s]}};
                 mma(d, *reinterpret_cast<const Frag<PARTS>(*)[1]>(&bf[i]),
                     *reinterpret_cast<const Frag<PARTS>(*)[1]>(&kf[s]));
-                dC[i][s] = d[0][0];
+                put(dC[i][s], d[0][0], keep);
               }
             }
           }
@@ -769,6 +834,12 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
         }
         }
       }
+    };
+    if (has_n) {
+      // (N > 128 has no registers for a copy of its own: 194 us for 234)
+      if constexpr (NK == 8) within(odd);
+      else if (odd) within(std::true_type{});
+      else within(std::false_type{});
     }
     // du: four columns of a token a lane
     if (live) {
@@ -785,7 +856,7 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
         f32x4 v;
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(D, y[j], w * du[0][s][j]);
-        if (16 * s + li < len && c < ncol) {
+        if (16 * s + li < len && c < ncol && (!odd || sc->id[16 * s + li] == pass)) {
           if constexpr (VEC) {
             put4<T>(reinterpret_cast<T*>(reinterpret_cast<char*>(o0 + 16 * s * row) + off), v);
           } else {
@@ -828,37 +899,60 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       wi = weigh(wi, sc->r[t]);
       const float dw = (colO + colD) + sums.diag[t] + wi;
       // F: the paths that cross into t.  Those that leave the chunk from before t
-      // and those that enter it and end from t on ...
-      const float leave = in ? w * wi : 0.0f;
-      const float pre = prefix(leave) - leave, suf = __shfl(prefix(zi), tr);
-      // ... those between t's tile and others, and over it: sums without
-      // cancellation (starts less ends over the whole chunk lost 2e-6 of dA) ...
-      const float starts = in ? w * colO : 0.0f;
-      float F = suffix16(in ? rowO : 0.0f) + (prefix16(starts) - starts);
-      if constexpr (QT == 4) {
-        // read outside any branch: a lane that is off there may hold no value
-        const float r0 = prefix16(tile >= 2 ? row[0] : 0.0f);
-        const float r1 = prefix16(tile == 3 ? row[1] : 0.0f);
-        const float r02 = lane_value(r0, 47), r03 = lane_value(r0, 63), r13 = lane_value(r1, 63);
-        F += tile == 1 ? r02 + r03 : tile == 2 ? r03 + r13 : 0.0f;
+      // and those that enter it and end from t on; those between t's tile and others,
+      // and over it: sums without cancellation (starts less ends over the whole chunk
+      // lost 2e-6 of dA); and within it, those that start before t less those that
+      // end there.
+      const float leave = in ? w * wi : 0.0f, starts = in ? w * colO : 0.0f;
+      const float ends = in ? rowO : 0.0f, x = in ? w * colD - rowD : 0.0f;
+      auto crossing = [&](float leave, float zi, float starts, float ends, float x, float row0,
+                          float row1) {
+        float F = prefix(leave) - leave + __shfl(prefix(zi), tr);
+        F += suffix16(ends) + (prefix16(starts) - starts);
+        if constexpr (QT == 4) {
+          // read outside any branch: a lane that is off there may hold no value
+          const float r0 = prefix16(tile >= 2 ? row0 : 0.0f);
+          const float r1 = prefix16(tile == 3 ? row1 : 0.0f);
+          const float r02 = lane_value(r0, 47), r03 = lane_value(r0, 63), r13 = lane_value(r1, 63);
+          F += tile == 1 ? r02 + r03 : tile == 2 ? r03 + r13 : 0.0f;
+        }
+        return F + (prefix16(x) - x);
+      };
+      float F;
+      if (flagged && __any(not_finite(leave) || not_finite(zi) || not_finite(starts) ||
+                           not_finite(ends) || not_finite(x))) {
+        // these sums run over all the chunk's sequences: each by itself
+        F = 0.0f;
+#pragma unroll 1
+        for (int n = 0; n <= flags; ++n) {
+          const bool m = sc->id[t] == n;
+          const float f = crossing(m ? leave : 0.0f, sc->id[tr] == n ? zi : 0.0f, m ? starts : 0.0f,
+                                   m ? ends : 0.0f, m ? x : 0.0f, m ? row[0] : 0.0f,
+                                   m ? row[QT == 4 ? 1 : 0] : 0.0f);
+          if (m) F = f;
+        }
+      } else {
+        F = crossing(leave, zi, starts, ends, x, row[0], row[QT == 4 ? 1 : 0]);
       }
-      // ... and within it, those that start before t less those that end there
-      const float x = in ? w * colD - rowD : 0.0f;
-      F += prefix16(x) - x;
       const float T4 =
           weigh((sums.gh[0] + sums.gh[1]) + (sums.gh[2] + sums.gh[3]), sc->dec);
-      float Fv = T4 + suf + pre + F;
+      float Fv = T4 + F;
       if (flagged && sc->id[t] != (t > 0 ? sc->id[t - 1] : 0)) Fv = 0.0f;
-      if (lane < len) {
+      if (lane < len && (!odd || sc->id[t] == pass)) {
         const int64_t o = ((b * p.H + hd) * CB + mu % CB) * p.L + t0 + lane;
         p.F[o] = Fv;
         p.W[o] = dw;
       }
-      if (lane == 0)
-        p.ud_part[(ch0 + hd) * CB + mu % CB] =
-            (sums.ud[0] + sums.ud[1]) + (sums.ud[2] + sums.ud[3]);
+      if (lane == 0) {
+        float* const o = p.ud_part + (ch0 + hd) * CB + mu % CB;
+        const float v = (sums.ud[0] + sums.ud[1]) + (sums.ud[2] + sums.ud[3]);
+        *o = pass == 0 ? v : *o + v;
+      }
     }
     __syncthreads();
+    if (odd && !again && more) copy_keys(-1);
+    pass = again ? pass + 1 : 0;
+    u = next;
   }
   // the block's shares of dB, dC
   if (has_n) {
