@@ -68,6 +68,20 @@ def _req(t, name, dtype, shape, device):
     return t
 
 
+def _own_workspace(t, device):
+    """A caller's workspace (None stays None), which kernels write as one piece of
+    this device's memory."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"workspace is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t
+
+
 def _flags(reset, shape, device):
     """Reset flags as a contiguous uint8 device tensor (None stays None)."""
     if reset is None:

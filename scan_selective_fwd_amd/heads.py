@@ -23,7 +23,7 @@ import functools
 
 import torch
 
-from . import MambaScanError, _disc_code, _dtype_code, _flags, _lib, _ptr, lib
+from . import MambaScanError, _disc_code, _dtype_code, _flags, _lib, _own_workspace, _ptr, lib
 from . import _req as _refuse
 
 _F32 = torch.float32
@@ -115,10 +115,12 @@ def _head_args(s, A, D, delta_bias, h0, dev):
 
 
 def _workspace(nbytes, shape, where, workspace, dev):
-    """A workspace of the queried size; the caller's own where it is large enough."""
+    """A workspace of the queried size; the caller's own where it is large enough
+    (a smaller one is left unused)."""
     if nbytes >= 2 ** 63:
         empty = min(shape) <= 0
         raise MambaScanError(2 if empty else 6, where)
+    workspace = _own_workspace(workspace, dev)
     if workspace is not None and workspace.numel() * workspace.element_size() >= nbytes:
         return workspace
     return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
@@ -155,8 +157,9 @@ def heads_scan_fwd(u, delta, A, B, C, D=None, delta_bias=None, h0=None, *, delta
     """Multi-head scan over a prompt.  Returns out (batch, L, heads, P), or
     (out, last_state).  `reset`: (batch, L) uint8/bool flags of packed
     sequences.  `segments`: pieces of the sequence run in parallel, 0 =
-    automatic.  `workspace`: a tensor of at least heads_fwd_workspace_bytes
-    reused across calls (allocated when absent)."""
+    automatic.  `workspace`: a contiguous GPU tensor of at least
+    heads_fwd_workspace_bytes, reused across calls (allocated when absent or
+    smaller)."""
     s, ref, dev = _shape(u, delta, B, C, delta_softplus, disc, segments)
     _head_args(s, A, D, delta_bias, h0, dev)
     reset = _flags(reset, (s.batch, s.seqlen), dev)
