@@ -147,6 +147,7 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, h0=None, *,
         last_state = torch.empty((batch, dim, N), dtype=torch.float32, device=dev)
     _req(last_state, "last_state", torch.float32, (batch, dim, N), dev)
     nbytes = fwd_workspace_bytes(batch, dim, N, L, sdt, lanes, segments)
+    workspace = _own_workspace(workspace, dev)
     if nbytes and (workspace is None or workspace.numel() < nbytes):
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     ws_ptr = workspace.data_ptr() if nbytes else None
@@ -230,6 +231,7 @@ def scan_bwd(u, delta, A, B, C, D, z, delta_bias, dout, h0=None, *, delta_softpl
         # starts at the block flags
         states = checkpoints.numel() * 4
         nbytes -= (states + 255) // 256 * 256
+    workspace = _own_workspace(workspace, dev)
     if workspace is None or workspace.numel() < nbytes:
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
     st = L_.mamba_scan_bwd_ex(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
@@ -401,6 +403,7 @@ def scan_fwd_complex(u, delta, A, B, C, D=None, z=None, delta_bias=None, h0=None
         out = torch.empty((batch, dim, L), dtype=sdt, device=dev)
     last = torch.empty((batch, dim, N), dtype=torch.complex64, device=dev)
     nbytes = fwd_complex_workspace_bytes(batch, dim, N, L, segments)
+    workspace = _own_workspace(workspace, dev)
     if nbytes and (workspace is None or workspace.numel() < nbytes):
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     ws_ptr = workspace.data_ptr() if nbytes else None
@@ -461,6 +464,7 @@ def scan_bwd_complex(u, delta, A, B, C, D, z, delta_bias, dout, h0=None, *,
         nbytes -= (states + 255) // 256 * 256
     ws_ptr, ws_bytes = None, 0
     if nbytes > 0:
+        workspace = _own_workspace(workspace, dev)
         if workspace is None or workspace.numel() < nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
