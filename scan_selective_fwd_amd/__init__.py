@@ -16,6 +16,7 @@ float32 or bfloat16 (all the same); A, D, delta_bias and states are float32.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import BF16, EULER, F32, ZOH, MambaScanError
@@ -543,6 +544,7 @@ class SelectiveScanFn(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         u, delta, A, B, C, D, z, delta_bias, ckpt = ctx.saved_tensors
         sp, disc = ctx.flags
