@@ -15,8 +15,9 @@ float32 or bfloat16 (all the same); A, D, delta_bias and states are float32.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import BF16, EULER, F32, ZOH, MambaScanError
@@ -527,6 +528,38 @@ def conv1d_silu_bwd(x, w, b, du, *, reset=None):
     return g
 
 
+class _NoDerivative(torch.autograd.Function):
+    """The first `n` tensors, as made from all the others: whoever asks for their
+    derivative gets an error."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.detach() for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the backward kernels have no derivative: gradients of this call "
+                           "cannot be differentiated again")
+
+
+def _first_order(backward):
+    """Decorates an autograd function's backward that kernels compute.  With
+    create_graph its results are tied to what they depend on, so that a second
+    derivative is refused; untied, it would be left out without a word."""
+    @functools.wraps(backward)
+    def run(ctx, *douts):
+        with torch.no_grad():
+            grads = list(backward(ctx, *douts))
+        if torch.is_grad_enabled():
+            live = [i for i, g in enumerate(grads) if g is not None]
+            tied = _NoDerivative.apply(len(live), *(grads[i] for i in live), *(
+                t for t in (*ctx.saved_tensors, *douts) if t is not None and t.requires_grad))
+            for i, g in zip(live, tied):
+                grads[i] = g
+        return tuple(grads)
+    return run
+
+
 class SelectiveScanFn(torch.autograd.Function):
     """Autograd wrapper: forward = scan_fwd, backward = scan_bwd.  Besides the
     inputs, the forward saves only the state entering every 128-step chunk;
@@ -544,7 +577,7 @@ class SelectiveScanFn(torch.autograd.Function):
         return out
 
     @staticmethod
-    @once_differentiable
+    @_first_order
     def backward(ctx, dout):
         u, delta, A, B, C, D, z, delta_bias, ckpt = ctx.saved_tensors
         sp, disc = ctx.flags

@@ -22,9 +22,9 @@ import ctypes
 import functools
 
 import torch
-from torch.autograd.function import once_differentiable
 
-from . import MambaScanError, _disc_code, _dtype_code, _flags, _lib, _own_workspace, _ptr, lib
+from . import (MambaScanError, _disc_code, _dtype_code, _first_order, _flags, _lib, _own_workspace,
+               _ptr, lib)
 from . import _req as _refuse
 
 _F32 = torch.float32
@@ -399,7 +399,7 @@ class _HeadsScanFn(torch.autograd.Function):
         return out, last
 
     @staticmethod
-    @once_differentiable
+    @_first_order
     def backward(ctx, dout, dlast):
         u, delta, A, B, C, D, delta_bias, h0, reset = ctx.saved_tensors
         sp, disc = ctx.flags
@@ -427,7 +427,7 @@ class _Conv1dTokensFn(torch.autograd.Function):
         return conv1d_tokens_fwd(x, w, b, window=window, reset=reset)
 
     @staticmethod
-    @once_differentiable
+    @_first_order
     def backward(ctx, dout):
         x, w, b, window, reset = ctx.saved_tensors
         g = conv1d_tokens_bwd(x, w, b, dout.contiguous(), window=window, reset=reset)
@@ -447,7 +447,7 @@ class _GatedNormFn(torch.autograd.Function):
         return gated_norm_fwd(x, z, weight, **ctx.flags)
 
     @staticmethod
-    @once_differentiable
+    @_first_order
     def backward(ctx, dout):
         x, z, weight = ctx.saved_tensors
         g = gated_norm_bwd(x, z, weight, dout.contiguous(), **ctx.flags)
