@@ -19,7 +19,6 @@ namespace mscan {
 
 namespace {
 
-constexpr int kFwdRun = 16;   // tokens a lane takes in the forward
 constexpr int kAhead = 4;     // rows the backward loads ahead
 
 // Weights by lag: w4[k] multiplies x_{t-k}.  The width W is a template argument:
@@ -104,14 +103,14 @@ __global__ __launch_bounds__(256) void tokconv_fwd_kernel(const TokConvParams p)
   if (run >= p.batch * p.tiles) return;
   const int64_t c = (i - run * nvec) * V;
   const int64_t b = run / p.tiles;
-  const int64_t t0 = (run - b * p.tiles) * kFwdRun;
+  const int64_t t0 = (run - b * p.tiles) * kTokConvFwdRun;
   const uint8_t* rst = RST ? p.reset + b * p.L : nullptr;
   float w4[W][V], cb[V], h[3][V];
   load_lags<W, V>(p.w, c, w4);
 #pragma unroll
   for (int v = 0; v < V; ++v) cb[v] = p.b ? p.b[c + v] : 0.0f;
   history<T, V, RST>(p, rst, b, t0, c, h);
-  const int64_t n = p.L - t0 < kFwdRun ? p.L - t0 : kFwdRun;
+  const int64_t n = p.L - t0 < kTokConvFwdRun ? p.L - t0 : kTokConvFwdRun;
   const int64_t x0 = b * p.x.batch + t0 * p.x.token + c;
   const int64_t o0 = (b * p.L + t0) * p.dim + c;
   auto step = [&](int64_t j, const Raw<T, V>& r) {
@@ -125,12 +124,12 @@ __global__ __launch_bounds__(256) void tokconv_fwd_kernel(const TokConvParams p)
     for (int v = 0; v < V; ++v) pre[v] = silu(pre[v]);
     store_vec<T, V>(p.out, o0 + j * p.dim, pre);
   };
-  if (n == kFwdRun) {
-    Raw<T, V> x[kFwdRun];
+  if (n == kTokConvFwdRun) {
+    Raw<T, V> x[kTokConvFwdRun];
 #pragma unroll
-    for (int j = 0; j < kFwdRun; ++j) x[j].load(p.x.p, x0 + j * p.x.token);
+    for (int j = 0; j < kTokConvFwdRun; ++j) x[j].load(p.x.p, x0 + j * p.x.token);
 #pragma unroll
-    for (int j = 0; j < kFwdRun; ++j) step(j, x[j]);
+    for (int j = 0; j < kTokConvFwdRun; ++j) step(j, x[j]);
   } else {
     for (int64_t j = 0; j < n; ++j) {
       Raw<T, V> x;
@@ -351,7 +350,7 @@ unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); 
 
 template <typename T, int V, int W>
 hipError_t fwd_go(TokConvParams p, hipStream_t s) {
-  p.tiles = (p.L + kFwdRun - 1) / kFwdRun;
+  p.tiles = (p.L + kTokConvFwdRun - 1) / kTokConvFwdRun;
   const dim3 grid(blocks_of(p.batch * p.tiles * (p.dim / V)));
   if (p.reset) hipLaunchKernelGGL((tokconv_fwd_kernel<T, V, W, true>), grid, dim3(256), 0, s, p);
   else hipLaunchKernelGGL((tokconv_fwd_kernel<T, V, W, false>), grid, dim3(256), 0, s, p);

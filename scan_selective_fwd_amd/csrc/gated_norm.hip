@@ -310,20 +310,31 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(const NormParams p) {
   }
 }
 
+// The rows in as few launches as hold them.
+template <typename T>
+hipError_t by_rows(void (*kernel)(const NormParams), NormParams p, int64_t per, hipStream_t s) {
+  const int64_t most = norm_launch_rows(p.groups, per);
+  for (int64_t left = p.rows; left > 0; left -= p.rows) {
+    p.rows = left < most ? left : most;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((p.rows * p.groups + per - 1) / per)), dim3(256), 0,
+                       s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    p.x = static_cast<const T*>(p.x) + p.rows * p.x_row;
+    if (p.z) p.z = static_cast<const T*>(p.z) + p.rows * p.z_row;
+    p.out = static_cast<T*>(p.out) + p.rows * p.dim;
+  }
+  return hipSuccess;
+}
+
 template <typename T, int V, int TEAM, int NV>
 hipError_t fwd_go(const NormParams& p, hipStream_t s) {
-  const int64_t teams = p.rows * p.groups, per = 256 / TEAM;
-  hipLaunchKernelGGL((norm_fwd_kernel<T, V, TEAM, NV>), dim3((unsigned)((teams + per - 1) / per)),
-                     dim3(256), 0, s, p);
-  return hipGetLastError();
+  return by_rows<T>(norm_fwd_kernel<T, V, TEAM, NV>, p, 256 / TEAM, s);
 }
 
 template <typename T, int V, int TEAM>
 hipError_t fwd_walk(const NormParams& p, hipStream_t s) {
-  const int64_t teams = p.rows * p.groups, per = 256 / TEAM;
-  hipLaunchKernelGGL((norm_fwd_walk_kernel<T, V, TEAM>),
-                     dim3((unsigned)((teams + per - 1) / per)), dim3(256), 0, s, p);
-  return hipGetLastError();
+  return by_rows<T>(norm_fwd_walk_kernel<T, V, TEAM>, p, 256 / TEAM, s);
 }
 
 template <typename T, int V>

@@ -8,6 +8,9 @@
 
 namespace mscan {
 
+// Blocks of one launch: HIP takes less than 2^32 threads along a dimension.
+constexpr int64_t max_blocks(int threads) { return (int64_t)0xFFFFFFFF / threads; }
+
 // A batch of token rows: element (b, t, i) at p[b * batch + t * token + i].
 struct Rows {
   const void* p;
@@ -83,6 +86,16 @@ struct HeadsStepParams : HeadsParams {
   void* out;
 };
 
+// Rows of a head's state that a block of the single-token form takes.
+constexpr int64_t step_rows(int64_t N) {
+  return N <= 16 ? 256 : N <= 32 ? 128 : N <= 64 ? 64 : N <= 128 ? 32 : 16;
+}
+
+// Heads that a block of the backward's chunks takes side by side, by the state's
+// width in 32s, and the blocks that sum dB and dC at most.
+constexpr int chunk_sides(int nk) { return nk == 4 ? 2 : 1; }
+constexpr int64_t kMaxSumBlocks = 1 << 20;
+
 hipError_t dispatch_heads_scal(const HeadsParams& p, int dtype, bool bwd, hipStream_t s);
 hipError_t dispatch_heads_fwd(const HeadsFwdParams& p, int dtype, hipStream_t s);
 hipError_t dispatch_heads_bwd(const HeadsBwdParams& p, int dtype, hipStream_t s);
@@ -110,6 +123,8 @@ struct TokConvParams {
   float* part;           // (batch * tiles, W + 1, dim): the tiles' shares of dw, db
 };
 
+// Tokens a thread of the forward takes.
+constexpr int kTokConvFwdRun = 16;
 // Token tile of the backward: a block's 4 waves take kTokConvRun tokens each.
 constexpr int kTokConvRun = 16;
 constexpr int kTokConvTile = 4 * kTokConvRun;
@@ -150,6 +165,11 @@ struct NormParams {
   float* part;           // (parts, dim)
   int64_t parts;
 };
+
+// Rows that one launch of the norm's forward takes, with `per` groups a block.
+inline int64_t norm_launch_rows(int64_t groups, int64_t per) {
+  return max_blocks(256) * per / groups;
+}
 
 // Blocks that share the rows of one group in the norm's backward.
 int64_t norm_parts(int64_t rows, int64_t groups);

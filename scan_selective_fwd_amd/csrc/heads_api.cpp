@@ -169,9 +169,12 @@ bool fwd_layout(const mamba_heads_shape* s, FwdLayout* l) {
   split(s, kTargetBlocks, 1, &l->nseg, &l->seg_len);
   const int64_t cols = s->batch * s->heads * map_of(s).slices;
   if (cols > kGridLim / l->nseg || cols > kGridLim / 16) return false;
+  const int64_t most = mscan::max_blocks(256), bh = s->batch * s->heads;
+  if (s->batch * s->groups * map_of(s).hblocks > most / l->nseg) return false;
+  if (l->nseg > mscan::kSelfCarry && cols > most / (pad_state(s) / 32)) return false;
   const size_t n = (size_t)cols * (size_t)(l->nseg - 1);
   const int64_t q = chunk_len(s), chunks = (s->seqlen + q - 1) / q;
-  if (chunks > kGridLim / (s->batch * s->heads)) return false;
+  if (chunks > kGridLim / bh || bh * chunks > 4 * most) return false;
   l->scal = 0;
   l->state = up256((size_t)(s->batch * s->heads * chunks) * (size_t)(28 * q + 16));
   l->dec = l->state + up256(n * (size_t)(kSlice * pad_state(s)) * 4);
@@ -195,6 +198,10 @@ bool bwd_layout(const mamba_heads_shape* s, BwdLayout* l) {
   const int64_t cb = (s->headdim + 63) / 64, units = s->heads / s->groups * cb;
   if (chunks > kGridLim / 16 / cols || cols > kGridLim / 32 / l->nseg) return false;
   if (s->batch * s->seqlen > kGridLim * 128 / (s->groups * s->dstate)) return false;
+  const int64_t most = mscan::max_blocks(256), nk = pad_state(s) / 32;
+  if (s->batch * s->groups * m.hblocks > most / 2 / l->nseg || cols > most / 2 / nk ||
+      bh * chunks > 4 * (most - mscan::kMaxSumBlocks))
+    return false;
   // The heads of a chunk are shared among as many blocks as run at once, each
   // with at least one: 2 x 2048 x 80 heads take 308 us with 256 blocks (336
   // and 387 against 330 with 512 and 1024); their shares of dB and dC are summed after.
@@ -203,6 +210,7 @@ bool bwd_layout(const mamba_heads_shape* s, BwdLayout* l) {
   if (sp > units) sp = units;
   if (sp < 1) sp = 1;
   l->splits = (int)sp;
+  if (blocks > mscan::max_blocks(256 * mscan::chunk_sides((int)nk)) / sp) return false;
   const size_t state = (size_t)(kSlice * pad_state(s)) * 4;
   const size_t bch = (size_t)(bh * chunks), bl = (size_t)s->batch * (size_t)s->seqlen;
   const size_t gn = (size_t)(s->groups * s->dstate);
@@ -250,8 +258,14 @@ int64_t conv_tiles(int64_t L, int64_t tile) { return (L + tile - 1) / tile; }
 
 // Whether (tiles of tokens) x (batch rows) x (channel tiles) is a legal grid.
 bool conv_grid_ok(int64_t batch, int64_t dim, int64_t tiles) {
-  const int64_t cb = (dim + 63) / 64;
-  return tiles <= kGridLim / batch && tiles * batch <= kGridLim / cb;
+  const int64_t cb = (dim + 63) / 64, most = mscan::max_blocks(256);
+  return tiles <= most / batch && tiles * batch <= most / cb;
+}
+
+// The same of one thread a run of tokens and `v` channels.
+bool conv_threads_ok(int64_t batch, int64_t dim, int64_t runs, int v) {
+  const int64_t most = mscan::max_blocks(256) * 256;
+  return runs <= most / batch && dim / v <= most / (runs * batch);
 }
 
 mamba_status check_norm(const void* x, int64_t x_row, const void* z, int64_t z_row,
@@ -261,7 +275,7 @@ mamba_status check_norm(const void* x, int64_t x_row, const void* z, int64_t z_r
   if (rows <= 0 || dim <= 0 || groups <= 0 || dim % groups != 0) return MAMBA_ERR_SHAPE;
   if (x_row < 0 || (z && z_row < 0)) return MAMBA_ERR_SHAPE;
   if (!(eps >= 0.0f)) return MAMBA_ERR_INVALID;
-  if (dim > (1 << 28) || rows > kLim / 16 / dim || groups > kGridLim / rows ||
+  if (dim > (1 << 28) || rows > kLim / 16 / dim || groups > mscan::max_blocks(256) ||
       !mul_ok(rows, x_row) || !mul_ok(rows, z_row))
     return MAMBA_ERR_UNSUPPORTED;
   if (!x) return MAMBA_ERR_NULL_PTR;
@@ -382,6 +396,9 @@ mamba_status mamba_heads_state_update(const mamba_heads_shape* shape, float* sta
   if (st != MAMBA_OK) return st;
   if (shape->seqlen != 1 || pool <= 0 || (!slots && pool < shape->batch)) return MAMBA_ERR_SHAPE;
   if (pool > kLim / (kMaxHeadDim * kMaxHeadState * 4) / shape->heads) return MAMBA_ERR_UNSUPPORTED;
+  const int64_t rows = mscan::step_rows(shape->dstate);
+  if (shape->batch * shape->heads > mscan::max_blocks(256) / ((shape->headdim + rows - 1) / rows))
+    return MAMBA_ERR_UNSUPPORTED;
   st = check_inputs(shape, u, delta, A, B, C, D, delta_bias, nullptr);
   if (st != MAMBA_OK) return st;
   if (!state || !out) return MAMBA_ERR_NULL_PTR;
@@ -403,9 +420,7 @@ mamba_status mamba_conv1d_tokens_fwd(const void* x, int64_t x_batch_stride,
   mamba_status st = check_conv(x, w, b, width, dt, batch, dim, seqlen);
   if (st != MAMBA_OK) return st;
   if (x_batch_stride < 0 || x_token_stride < 0) return MAMBA_ERR_SHAPE;
-  const int64_t tiles = conv_tiles(seqlen, 1);
-  if (!span_ok(batch, x_batch_stride, seqlen, x_token_stride) || !conv_grid_ok(batch, dim, tiles / 4 + 1))
-    return MAMBA_ERR_UNSUPPORTED;
+  if (!span_ok(batch, x_batch_stride, seqlen, x_token_stride)) return MAMBA_ERR_UNSUPPORTED;
   if (!out) return MAMBA_ERR_NULL_PTR;
   const int es = esize(dt);
   if (!aligned(out, (size_t)es) || !aligned(window, (size_t)es) || !aligned(window_out, (size_t)es))
@@ -418,6 +433,8 @@ mamba_status mamba_conv1d_tokens_fwd(const void* x, int64_t x_batch_stride,
   p.out = out; p.window_out = window_out;
   p.vec = rows16(x, x_batch_stride, x_token_stride, dim, es) && aligned(out, 16) &&
           aligned(window, 16) && aligned(window_out, 16) && aligned(w, 16) && aligned(b, 16);
+  if (!conv_threads_ok(batch, dim, conv_tiles(seqlen, mscan::kTokConvFwdRun), p.vec ? 4 : 1))
+    return MAMBA_ERR_UNSUPPORTED;
   return hip_status(mscan::dispatch_tokconv_fwd(p, dt == MAMBA_F32 ? 0 : 1, as_stream(stream)));
 }
 
@@ -472,8 +489,7 @@ mamba_status mamba_conv1d_tokens_update(const void* x, int64_t x_batch_stride, v
   mamba_status st = check_conv(x, w, b, width, dt, batch, dim, 1);
   if (st != MAMBA_OK) return st;
   if (x_batch_stride < 0 || pool <= 0 || (!slots && pool < batch)) return MAMBA_ERR_SHAPE;
-  if (!mul_ok(batch, x_batch_stride) || pool > kLim / 64 / dim || !conv_grid_ok(batch, dim, 1))
-    return MAMBA_ERR_UNSUPPORTED;
+  if (!mul_ok(batch, x_batch_stride) || pool > kLim / 64 / dim) return MAMBA_ERR_UNSUPPORTED;
   if (!window || !out) return MAMBA_ERR_NULL_PTR;
   const int es = esize(dt);
   if (!aligned(out, (size_t)es) || !aligned(window, (size_t)es) || !aligned(slots, 4))
@@ -483,6 +499,7 @@ mamba_status mamba_conv1d_tokens_update(const void* x, int64_t x_batch_stride, v
   p.batch = batch; p.dim = dim; p.w = w; p.b = b; p.out = out; p.W = (int)width;
   p.vec = rows16(x, x_batch_stride, 0, dim, es) && aligned(window, 16) && aligned(out, 16) &&
           aligned(w, 16) && aligned(b, 16);
+  if (!conv_threads_ok(batch, dim, 1, p.vec ? 4 : 1)) return MAMBA_ERR_UNSUPPORTED;
   return hip_status(mscan::dispatch_tokconv_step(p, dt == MAMBA_F32 ? 0 : 1, as_stream(stream)));
 }
 

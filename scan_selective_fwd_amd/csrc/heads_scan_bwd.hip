@@ -262,7 +262,7 @@ struct alignas(16) BwdSums {
 // of one head fit a CU (4 x 777 x 16 in float32: 112 -> 100 us; 2 x 2048 x 80 in
 // bfloat16: 210 -> 201); N > 128 leaves LDS for one.
 template <int NK>
-constexpr int kSide = NK == 4 ? 2 : 1;
+constexpr int kSide = chunk_sides(NK);
 
 // One chunk, its heads in turn: 190 us of the 304, 19 us a pair of heads, of which
 // the matrix units are busy 2.5; the waits for the next states (up to 3) and the
@@ -983,10 +983,9 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
   }
 }
 
-// dB, dC: the splits' shares summed in order, V elements a thread.
+// dB, dC: the splits' shares summed in order, V elements a thread and step.
 template <typename T, int V>
 __device__ __forceinline__ void sum_splits(const HeadsBwdParams& p, int64_t n, int64_t i) {
-  if (i >= n) return;
   float sB[V] = {}, sC[V] = {};
   for (int k = 0; k < p.splits; ++k) {
     float b[V], c[V];
@@ -1009,7 +1008,10 @@ template <typename T, int V>
 __global__ __launch_bounds__(256) void heads_bwd_tail_kernel(const HeadsBwdParams p, int sums) {
   constexpr int Q = Mx<T>::Q;
   if ((int)blockIdx.x < sums) {
-    sum_splits<T, V>(p, p.batch * p.L * p.G * p.N, ((int64_t)blockIdx.x * 256 + threadIdx.x) * V);
+    const int64_t n = p.batch * p.L * p.G * p.N;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; i < n;
+         i += (int64_t)sums * 256 * V)
+      sum_splits<T, V>(p, n, i);
     return;
   }
   const int64_t chunks = (p.L + Q - 1) / Q;
@@ -1096,7 +1098,8 @@ hipError_t bwd_go(const HeadsBwdParams& p, hipStream_t s) {
   // four elements a thread where they stay together
   const bool four = n % 4 == 0 &&
                     ((uintptr_t)p.dB | (uintptr_t)p.dC) % (4 * sizeof(T)) == 0;
-  const int64_t per = four ? 1024 : 256, sums = (n + per - 1) / per;
+  const int64_t per = four ? 1024 : 256;
+  const int64_t sums = (n + per - 1) / per < kMaxSumBlocks ? (n + per - 1) / per : kMaxSumBlocks;
   const dim3 grid((unsigned)(sums + (waves + 3) / 4));
   if (four)
     hipLaunchKernelGGL((heads_bwd_tail_kernel<T, 4>), grid, dim3(256), 0, s, p, (int)sums);

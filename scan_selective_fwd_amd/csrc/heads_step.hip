@@ -109,9 +109,9 @@ __global__ __launch_bounds__(256) void heads_step_kernel(const HeadsStepParams p
 
 template <typename T, int LPR>
 hipError_t step_go(const HeadsStepParams& p, bool vec, hipStream_t s) {
-  const int rows = 256 / LPR * kStepRows;
+  static_assert(step_rows(4 * LPR) == 256 / LPR * kStepRows, "the ABI layer's count of blocks");
+  const int64_t rows = step_rows(p.N);
   const int64_t blocks = p.batch * p.H * ((p.P + rows - 1) / rows);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (vec)
     hipLaunchKernelGGL((heads_step_kernel<T, LPR, true>), dim3((unsigned)blocks), dim3(256), 0, s, p);
   else
