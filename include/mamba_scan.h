@@ -531,7 +531,9 @@ typedef struct mamba_heads_shape {
 size_t mamba_heads_scan_fwd_workspace_size(const mamba_heads_shape* shape);
 size_t mamba_heads_scan_bwd_workspace_size(const mamba_heads_shape* shape);
 
-/* Forward.  D, delta_bias, h0, reset, last_state may be NULL. */
+/* Forward.  D, delta_bias, h0, reset, last_state may be NULL.  last_state may be
+ * h0 itself (the state steps in place), not a part of it; no other output may
+ * overlap an input. */
 mamba_status mamba_heads_scan_fwd(const mamba_heads_shape* shape, const void* u,
                                   const void* delta, const float* A, const void* B,
                                   const void* C, const float* D, const float* delta_bias,

@@ -47,6 +47,8 @@ struct HeadsFwdParams : HeadsParams {
   bool carried;          // a carry pass joins the segments
   void* out;
   float* last;           // nullable
+  float* h0_kept;        // nullable workspace, (batch, H, slices) states: h0 before last
+                         // takes its place
 };
 
 struct HeadsBwdParams : HeadsParams {

@@ -162,7 +162,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 struct FwdLayout {
   int nseg;
   int64_t seg_len;
-  size_t scal, state, dec, total;
+  size_t scal, state, dec, h0, total;
 };
 
 bool fwd_layout(const mamba_heads_shape* s, FwdLayout* l) {
@@ -178,7 +178,10 @@ bool fwd_layout(const mamba_heads_shape* s, FwdLayout* l) {
   l->scal = 0;
   l->state = up256((size_t)(s->batch * s->heads * chunks) * (size_t)(28 * q + 16));
   l->dec = l->state + up256(n * (size_t)(kSlice * pad_state(s)) * 4);
-  l->total = l->dec + up256(n * 4);
+  l->h0 = l->dec + up256(n * 4);
+  // used where last_state is h0: another segment's block may write one before this
+  // segment's reads the other
+  l->total = l->h0 + (l->nseg > 1 ? up256((size_t)cols * (size_t)(kSlice * pad_state(s)) * 4) : 0);
   return true;
 }
 
@@ -322,6 +325,12 @@ mamba_status mamba_heads_scan_fwd(const mamba_heads_shape* shape, const void* u,
     return MAMBA_ERR_ALIGNMENT;
   FwdLayout l;
   if (!fwd_layout(shape, &l)) return MAMBA_ERR_UNSUPPORTED;
+  if (h0 && last_state && last_state != h0) {   // in place, or apart
+    const uintptr_t a = reinterpret_cast<uintptr_t>(h0), b = reinterpret_cast<uintptr_t>(last_state);
+    if ((a < b ? b - a : a - b) <
+        (size_t)(shape->batch * shape->heads) * (size_t)(shape->headdim * shape->dstate) * 4)
+      return MAMBA_ERR_INVALID;
+  }
   if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
   mscan::HeadsFwdParams p{};
@@ -333,6 +342,8 @@ mamba_status mamba_heads_scan_fwd(const mamba_heads_shape* shape, const void* u,
   p.scal = workspace;
   p.seg_state = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.state);
   p.seg_dec = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.dec);
+  if (last_state && last_state == h0 && p.nseg > 1)
+    p.h0_kept = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.h0);
   p.out = out; p.last = last_state; p.carried = p.nseg > mscan::kSelfCarry;
   p.vec = p.vec && aligned(out, 16);
   return hip_status(mscan::dispatch_heads_fwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,

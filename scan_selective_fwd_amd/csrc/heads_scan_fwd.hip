@@ -263,7 +263,10 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
   } else if (p.carried && k.seg > 0) {
     load_frags<NK>(p.seg_state + slice_slot(p, k, p.nseg - 1, k.seg - 1) * slice_floats<NK>(), h);
   } else {
-    load_state<NK>(p.h0 ? p.h0 + (k.b * p.H + k.h) * (int64_t)p.P * p.N : nullptr, k.c0, p.P, p.N, h);
+    if (p.h0_kept)
+      load_frags<NK>(p.h0_kept + slice_slot(p, k, 1, 0) * slice_floats<NK>(), h);
+    else
+      load_state<NK>(p.h0 ? p.h0 + (k.b * p.H + k.h) * (int64_t)p.P * p.N : nullptr, k.c0, p.P, p.N, h);
     // few segments: each joins the ones before it by itself
     const int64_t slot = slice_slot(p, k, p.nseg - 1, 0);
     for (int i = 0; i < k.seg; ++i) {
@@ -516,6 +519,10 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const H
   const int sub = p.slices * kSlice, hh = wave / p.slices;
   const int64_t chunks = (p.L + Q - 1) / Q;
   f32x4 h[2 * NK][2];
+  if (p.h0_kept && k.on && k.seg == 0) {
+    load_state<NK>(p.h0 + (k.b * p.H + k.h) * (int64_t)p.P * p.N, k.c0, p.P, p.N, h);
+    store_frags<NK>(p.h0_kept + slice_slot(p, k, 1, 0) * slice_floats<NK>(), h);
+  }
   fill<NK>(h, 0.0f);
   float dec = 1.0f;
   Stage<T, Q, kCols, VEC> sx;

@@ -156,7 +156,8 @@ def heads_scan_fwd(u, delta, A, B, C, D=None, delta_bias=None, h0=None, *, delta
                    disc="zoh", reset=None, return_last_state=False, out=None, last_state=None,
                    segments=0, workspace=None):
     """Multi-head scan over a prompt.  Returns out (batch, L, heads, P), or
-    (out, last_state).  `reset`: (batch, L) uint8/bool flags of packed
+    (out, last_state).  `last_state`: a tensor to receive it, h0 itself where the
+    state is to step in place.  `reset`: (batch, L) uint8/bool flags of packed
     sequences.  `segments`: pieces of the sequence run in parallel, 0 =
     automatic.  `workspace`: a contiguous GPU tensor of at least
     heads_fwd_workspace_bytes, reused across calls (allocated when absent or
