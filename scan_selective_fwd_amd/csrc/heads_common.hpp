@@ -158,8 +158,4 @@ __device__ __forceinline__ void step_weight_grad(float dt, float A, bool zoh, fl
   by_A = (dt * e - expm1f(x) / A) / A;
 }
 
-__device__ __forceinline__ const uint8_t* reset_row(const uint8_t* reset, int64_t b, int64_t L) {
-  return reset ? reset + b * L : nullptr;
-}
-
 }  // namespace mscan

@@ -66,17 +66,11 @@ __device__ __forceinline__ float top8(float x) {
   return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
 }
 
-// Eight floats as one rounded part, as two (2^-17 of each is lost), or as three
-// exact ones.
+// Eight floats as two parts (2^-17 of each is lost) or as three exact ones.
 template <int NP>
 __device__ __forceinline__ Frag<NP> to_frag(const float (&x)[8]) {
   Frag<NP> f;
-  if constexpr (NP == 1) {
-    u32x4 r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-    f.v[0] = as_frag(r);
-  } else if constexpr (NP == 2) {
+  if constexpr (NP == 2) {
     u32x4 r[2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -221,15 +215,6 @@ struct Cols {
   __device__ __forceinline__ void load(const T* tile, int stride, int o0, int k0) {
     if constexpr (sizeof(T) == 2) raw = load_cols_raw(tile, stride, o0, k0);
     else load_cols_f32(tile, stride, o0, k0, x);
-  }
-  __device__ __forceinline__ Frag<Mx<T>::PARTS> frag() const {
-    if constexpr (sizeof(T) == 2) {
-      Frag<1> f;
-      f.v[0] = raw;
-      return f;
-    } else {
-      return to_frag<3>(x);
-    }
   }
   __device__ __forceinline__ Frag<3> weighted(const float* c, int k0) const {
     const f32x4 c0 = *reinterpret_cast<const f32x4*>(c + k0 + 4 * lane_g());
