@@ -569,7 +569,8 @@ mamba_status mamba_heads_state_update(const mamba_heads_shape* shape, float* sta
  * dim), the stage before the multi-head scan (the formula of
  * mamba_conv1d_silu_fwd; w (dim, width) and b (dim) float32, width 2..4).
  * x may be a view (batch and token strides in elements); out, dout, dx
- * (batch, seqlen, dim) are dense, of x's type.
+ * (batch, seqlen, dim) are dense, of x's type.  out may not overlap x, nor dx
+ * x or dout (the update's out may be its x).
  *   window (nullable): the width - 1 inputs before x, (batch, width - 1,
  *     dim) of x's type, oldest first; absent = zero.
  *   window_out (nullable): the last width - 1 inputs of the sequence that

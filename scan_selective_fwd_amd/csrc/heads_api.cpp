@@ -437,6 +437,8 @@ mamba_status mamba_conv1d_tokens_fwd(const void* x, int64_t x_batch_stride,
   if (!aligned(out, (size_t)es) || !aligned(window, (size_t)es) || !aligned(window_out, (size_t)es))
     return MAMBA_ERR_ALIGNMENT;
   if (window && window == window_out) return MAMBA_ERR_INVALID;
+  // a run of tokens reads the last inputs of the one before, which may have written by then
+  if (out == x) return MAMBA_ERR_INVALID;
   mscan::TokConvParams p{};
   p.x = {x, x_batch_stride, x_token_stride};
   p.w = w; p.b = b; p.window = window; p.reset = reset;

@@ -271,8 +271,8 @@ def _conv_args(x, w, b, window, reset):
 
 def conv1d_tokens_fwd(x, w, b=None, *, window=None, reset=None, return_window=False, out=None):
     """Causal depthwise convolution (w (dim, W), 2 <= W <= 4) + SiLU of x
-    (batch, L, dim).  `window` (batch, W - 1, dim): the inputs before x.
-    Returns out, or (out, the window to continue from)."""
+    (batch, L, dim).  `window` (batch, W - 1, dim): the inputs before x.  `out`
+    may not be x.  Returns out, or (out, the window to continue from)."""
     dev, batch, L, dim, W, (sb, st_), reset = _conv_args(x, w, b, window, reset)
     if out is None:
         out = torch.empty((batch, L, dim), dtype=x.dtype, device=dev)

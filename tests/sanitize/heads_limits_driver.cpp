@@ -59,7 +59,7 @@ static int step(const mamba_heads_shape& s) {
 }
 static int conv(int64_t batch, int64_t dim, int64_t L, char* x) {
   return mamba_conv1d_tokens_fwd(x, 0, 0, f32, nullptr, nullptr, nullptr, 4, MAMBA_BF16, batch, dim,
-                                 L, buf, nullptr, nullptr);
+                                 L, buf + 4096, nullptr, nullptr);
 }
 static int conv_one(int64_t batch, int64_t dim, char* x) {
   return mamba_conv1d_tokens_update(x, 0, buf, nullptr, batch, f32, nullptr, 4, MAMBA_BF16, batch,
