@@ -8,11 +8,11 @@
 // of tokens with the last three inputs (and, backwards, the open sums of dx) in
 // registers: every row is read once by its run and the three rows between runs
 // twice.  Rows are loaded ahead in groups and kept packed until used.  In
-// bfloat16 at width 4 the forward of 8 x 2048 x 1792 takes 22.4 us (118 MB at
-// 5.3 TB/s: HBM), the backward of 2 x 2047 x 5376 with flags 44.7 us (132 MB at
-// 3.0 TB/s: per value the activation's derivative, the shares of dw and the
-// flags' selects) and its sum 4 us.  With the width at run time the same took 33
-// and 58.
+// bfloat16 at width 4 the forward of 8 x 2048 x 1792 takes 24 us (118 MB at
+// 4.9 TB/s: HBM), the backward of 2 x 2047 x 5376 with flags 52 us (132 MB at
+// 2.6 TB/s; 45 with its inputs in the last-level cache, for 33 of which a SIMD issues
+// VALU: per value the activation's derivative, the shares of dw and the flags'
+// selects) and its sum 4 us.  With the width at run time they took 8 and 13 more.
 #include "heads_common.hpp"
 
 namespace mscan {
@@ -298,7 +298,10 @@ __global__ __launch_bounds__(256) void tokconv_sum_kernel(const TokConvParams p)
 // latency, so it rounds each product and sum by itself, the oldest input first,
 // and takes the library's exp and a true division: the bits that a chain of
 // elementwise float operations gives.  The result is rounded to the stored type
-// and enters a state, where one unit of bfloat16 would show.
+// and enters a state, where one unit of bfloat16 would show.  The forward over many
+// tokens is bound by HBM only with fused operations and the fast sigmoid, so 4 of
+// 100 thousand results differ between the two by that unit; both are as near to 64
+// bits (1.67e-3 in bfloat16, 7e-8 in float32).
 template <int W, int V>
 __device__ __forceinline__ void step_act(const float (&w4)[W][V], const float (&cb)[V],
                                          const float (&x)[V], const float (&h)[3][V],

@@ -11,9 +11,11 @@
 // registers: every tensor is read once and written once, and the two sums of
 // the backward come from the same pass.  Groups too long for the registers,
 // or rows not on 16 bytes, are walked twice (the second time from the cache).
-// All of it is bound by HBM: in bfloat16 the forward of 16384 rows of 1536 takes
-// 25 us (151 MB, part of it from the cache), the backward of 4096 rows of 5120 in
-// 8 groups 41 us (210 MB at 5.1 TB/s) and the sum of dw 6 us.
+// The forward is bound by HBM: 16384 rows of 1536 in bfloat16 take 28 us (151 MB,
+// 5.3 TB/s).  The backward of 4096 rows of 5120 in 8 groups takes 50 us (210 MB at
+// 4.2 TB/s), for about 36 of which a SIMD issues VALU (gate, its derivative and the
+// two passes over a value), and 42 with its inputs in the last-level cache; the sum
+// of dw takes 6.
 #include "heads_common.hpp"
 
 namespace mscan {

@@ -120,18 +120,22 @@ int64_t pad_state(const mamba_heads_shape* s) {
 
 // Segments: as many as fit `target` blocks, the ones the chip holds at once (one
 // more and they take two rounds), each of at least `least` chunks.  The forward
-// takes 1: 200 steps of 24 heads take 22.8 us in four segments and 27.6 in one,
-// 1000 steps 35.6 in 16, 37.8 in 8, 44.1 in 4.  The backward, whose segments
-// serve its states pass alone, takes 2: 512 steps take 59.4 us in four segments,
-// 62.8 in two, 57.2 in eight; 4 x 512 take 76.7 in two, 81.0 in four, 91.2 in
+// takes 1: 200 steps of 24 heads take 23.9 us in four segments and 32.1 in one,
+// 1000 steps 35.2 in 16, 38.6 in 8, 48.3 in 4.  The backward, whose segments
+// serve its states pass alone, takes 2: 512 steps take 59.3 us in four segments,
+// 61.9 in two, 57.2 in eight; 4 x 512 take 78.8 in two, 83.7 in four, 94.9 in
 // eight.
 constexpr int64_t kTargetBlocks = 512;
 // The backward's states pass runs both directions at once.  In bfloat16 with
 // N > 64 it is bound by the states it writes, more blocks gain nothing, and the
-// chunks add an entering state where a segment does not begin the row: with 160
-// blocks for 256 2 x 2048 x 80 heads take 292 us for 308, 8 x 2048 x 24 333 for
-// 346.  Otherwise the products bound it: N = 64 takes 204 us for 196, float32 242
-// for 234.
+// chunks add an entering state where a segment does not begin the row.  With 160
+// blocks for 256, of 64 channels and N = 128: 2 x 2048 x 80 heads take 319 us for
+// 332, 8 x 2048 x 24 362 for 370, 4 x 4096 x 4 94 for 103, 65536 x 4 352 for 358,
+// 16384 x 2 101 for 101, 16384 x 24 417 for 409, 65536 x 24 1512 for 1495; N = 256:
+// 8192 x 8 in two groups 214 for 254, 2 x 8192 x 12 of 128 channels 1132 for 1055.
+// Otherwise the products bound it: N = 64 takes 210 us for 204 (2 x 2048 x 80);
+// float32 648 for 677 there, 158 for 158 with 16 heads, 102 for 99 (4 x 777 x 16,
+// N = 64).
 int64_t state_blocks(const mamba_heads_shape* s) {
   return s->dtype == MAMBA_BF16 && s->dstate > 64 ? 160 : kTargetBlocks / 2;
 }
@@ -206,7 +210,7 @@ bool bwd_layout(const mamba_heads_shape* s, BwdLayout* l) {
       bh * chunks > 4 * (most - mscan::kMaxSumBlocks))
     return false;
   // The heads of a chunk are shared among as many blocks as run at once, each
-  // with at least one: 2 x 2048 x 80 heads take 308 us with 256 blocks (336
+  // with at least one: 2 x 2048 x 80 heads took 308 us with 256 blocks (336
   // and 387 against 330 with 512 and 1024); their shares of dB and dC are summed after.
   const int64_t blocks = s->batch * s->groups * chunks;
   int64_t sp = chunk_blocks(s) / blocks;

@@ -1,7 +1,8 @@
 // The scalars of every chunk of the multi-head scan (Scal, heads_mma.hpp): one
 // wave a (batch row, chunk, head), one token a lane.  Made once here, they cost
-// each pass one load instead of a scan and its exponentials a wave.  Bound by its writes, 28 bytes a token and head: 8 x 2048 tokens of
-// 24 heads take 6.8 us, 131072 of one row 29 us (88 MB, 3.0 TB/s).
+// each pass one load instead of a scan and its exponentials a wave.  Bound by its
+// writes, 28 bytes a token and head: 8 x 2048 tokens of 24 heads take 6.9 us,
+// 131072 of one row 30 us (88 MB, 2.9 TB/s).
 #include "heads_mma.hpp"
 
 namespace mscan {

@@ -18,8 +18,10 @@
 // zero, then their carries); the chunks, all independent, each block looping
 // over heads with dB and dC in registers; sums over the blocks' shares.
 //
-// 2 x 2048 tokens, 80 heads of 64, N = 128, bfloat16: 304 us in all.  Bound by the
-// states (335 MB written, then read) and by the phases of the chunks.
+// 2 x 2048 tokens, 80 heads of 64, N = 128, bfloat16: 319 us in all.  Bound by the
+// states (335 MB written, then read) and by the phases of the chunks.  In bfloat16 the
+// states are multiplied in two parts for dB and dC (rounded once, up to 1.46 times the
+// error of the results' own rounding; now 1.0, for 5 % of the time).
 #include <type_traits>
 
 #include "heads_mma.hpp"
@@ -113,7 +115,7 @@ __device__ __forceinline__ void states_of(const HeadsBwdParams& p, int block, T*
 }
 
 // Both directions in one launch, the update of the forward's pass; the state in
-// registers is written at every chunk: 98 us of the 304 (357 MB at 3.6 TB/s).
+// registers is written at every chunk: 100 us of the 319 (357 MB at 3.6 TB/s).
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_states_kernel(const HeadsBwdParams p) {
   using F = BwdTiles<T, NK>;
@@ -264,8 +266,8 @@ struct alignas(16) BwdSums {
 template <int NK>
 constexpr int kSide = chunk_sides(NK);
 
-// One chunk, its heads in turn: 190 us of the 304, 19 us a pair of heads, of which
-// the matrix units are busy 2.5; the waits for the next states (up to 3) and the
+// One chunk, its heads in turn: 205 us of the 319, 20 us a pair of heads, of which
+// the matrix units are busy 3.5 and VALU is issued for 8; the waits for the next states (up to 3) and the
 // phases between barriers, one block a CU, are the rest.
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256 * kSide<NK>, NK == 8 ? 1 : 2)
@@ -836,7 +838,8 @@ void heads_chunk_kernel(const HeadsBwdParams p) {
       }
     };
     if (has_n) {
-      // (N > 128 has no registers for a copy of its own: 194 us for 234)
+      // (N > 128 has no registers for a copy of its own: 2 x 1024 x 12 heads of 128,
+      // N = 256: 183 us for 234)
       if constexpr (NK == 8) within(odd);
       else if (odd) within(std::true_type{});
       else within(std::false_type{});
@@ -1003,7 +1006,7 @@ __device__ __forceinline__ void sum_splits(const HeadsBwdParams& p, int64_t n, i
 
 // One launch for what the chunks leave: dB and dC, and, in the blocks from `sums`
 // on, ddelta of every token from F and dw with a chunk's shares of dA, dD, dbias,
-// one wave a (batch row, chunk, head): 9 us of the 304.  Two launches took 3 us more.
+// one wave a (batch row, chunk, head): 9 us of the 319.  Two launches took 3 us more.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void heads_bwd_tail_kernel(const HeadsBwdParams p, int sums) {
   constexpr int Q = Mx<T>::Q;

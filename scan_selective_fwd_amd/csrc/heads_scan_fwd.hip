@@ -10,13 +10,16 @@
 // kSelfCarry segments the output pass joins those before its own by itself.
 //
 // What bounds it: the phases of a chunk (stage, products of C and B, the state's
-// share, the chunk's own, the update), not HBM or the matrix units.  Two blocks
-// share a CU and a chunk of both takes 21 thousand clocks, of which a SIMD issues
-// VALU for 8, MFMA for 2.5 and the LDS serves 3.7.  One block of four slices
-// fills two heads of 64 channels, so that B and C are read by half as many blocks
-// (with the scalars made once: 167 -> 110 us).  8 x 2048 tokens, 24 heads of 64,
-// N = 128, bfloat16: 95 us in all (1.2 TB/s of what has to move, 136 TFLOP/s);
-// 131072 tokens of one row 594 us (1.5 TB/s).
+// share, M, the chunk's own, the update), not HBM or the matrix units.  Two blocks
+// share a CU and a chunk of both takes 23 thousand clocks, of which a SIMD issues
+// VALU for 12, its matrix unit is busy 6.4 and the LDS serves 4.  One block of four
+// slices fills two heads of 64 channels, so that B and C are read by half as many
+// blocks (with the scalars made once: 167 -> 110 us when built).  In bfloat16 M and
+// the entering state are multiplied in two parts: rounded once each, as out is, they
+// made out's error 1.2 to 1.4 times that of its own rounding; it is 1.0 with them,
+// for 10 % of the time.  8 x 2048 tokens, 24 heads of 64, N = 128, bfloat16: 107 us in
+// all (1.1 TB/s of what has to move, 120 TFLOP/s); 131072 tokens of one row 681 us
+// (1.3 TB/s).
 #include "heads_mma.hpp"
 
 namespace mscan {
@@ -235,7 +238,7 @@ __device__ __forceinline__ void store_low(int heads, T* Mall,
 }
 
 
-// The output pass; 65 us of the 95, 403 of the 594.
+// The output pass; 80 us of 118 in the kernels' trace, 503 of 735.
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const HeadsFwdParams p) {
   using F = FwdTiles<T, NK>;
@@ -502,7 +505,7 @@ __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_fwd_kernel(const H
 }
 
 // A segment's end state from zero and its decay: the output pass's update alone,
-// which reads u and B and writes a state a segment; 30 us of the 95, 182 of the 594.
+// which reads u and B and writes a state a segment; 31 us of the 118, 188 of the 735.
 template <typename T, int NK, bool VEC>
 __global__ __launch_bounds__(256, NK == 8 ? 1 : 2) void heads_seg_kernel(const HeadsFwdParams p) {
   using F = FwdTiles<T, NK>;
