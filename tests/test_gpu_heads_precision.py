@@ -16,7 +16,8 @@ pytestmark = pytest.mark.gpu
 
 # (batch, L, heads, P, groups, N): every width of the state, one to four heads a block
 SIZES = [(2, 257, 4, 64, 2, 128), (1, 300, 2, 128, 1, 256), (3, 130, 6, 48, 3, 80),
-         (1, 700, 8, 32, 1, 64), (2, 190, 8, 20, 2, 32), (1, 640, 1, 100, 1, 200)]
+         (1, 700, 8, 32, 1, 64), (2, 190, 8, 20, 2, 32), (1, 640, 1, 100, 1, 200),
+         (2, 150, 8, 32, 1, 128), (1, 130, 5, 20, 1, 200), (1, 65, 4, 32, 1, 256)]
 ROUNDED_ONCE = 1.05
 
 
@@ -46,6 +47,17 @@ def test_bfloat16_gradients_are_rounded_once(ms, size, reset):  # noqa: F811
         got = run_bwd(ms, dev(i, torch.bfloat16), segments=segments)
         for k in ("du", "ddelta", "dB", "dC"):
             rounded_once(k, got[k], ref[k])
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_float32_of_the_same_sizes(ms, size):  # noqa: F811
+    i = R.scan_inputs(64, torch.float32, *size, h0=True, reset="random")
+    g = dev(i, torch.float32)
+    out, last = run_fwd(ms, g)
+    want, want_last = ref_fwd(i)
+    R.check("out", out, want)
+    R.check("last", last, want_last)
+    check_bwd(run_bwd(ms, g), i)
 
 
 def forgetting(seed, dtype, kind, softplus):
