@@ -626,6 +626,120 @@ mamba_status mamba_gated_norm_bwd(const void* x, int64_t x_row_stride, const voi
                                   float* dweight, void* workspace, size_t workspace_bytes,
                                   void* stream);
 
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence over token-major rows: one state a channel, its
+ * decay and its input under gates of the token.  Per batch row and channel,
+ * with s(v) = 1 / (1 + exp(-v)):
+ *
+ *   a_t = exp(A s(r_t))
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) s(i_t) x_t,   h_{-1} = h0 (or 0)
+ *   out_t = h_t                                       (h_t z_t s(z_t) with z)
+ *
+ * x, r, i, z, dout, out and the gradients dx, dr, di, dz are (batch, seqlen,
+ * dim) in `dtype` (each output rounded once, from float32); x, r, i and z may
+ * be views of wider rows (batch and token strides in elements, >= 0; a token's
+ * elements are contiguous), the rest is dense.  A, dA (dim) and h0,
+ * last_state, dlast_state, dh0 (batch, dim) are float32.  A <= 0; where A = 0
+ * the state is kept, nothing enters it, and dA is not finite.
+ * reset (nullable, (batch, seqlen) bytes): the state entering a flagged step
+ * is left out.  Non-finite values: one in a token of a packed sequence never
+ * reaches another sequence's rows, nor, in the forward, earlier rows of its
+ * own; in the backward it may reach all of its sequence's gradients in its
+ * channel, and the channel's dA.
+ * Checkpoints: the state entering every 64th step, (batch, ceil(seqlen / 64),
+ * dim) float32, written by a forward and read by the backward over the same
+ * inputs, which without them forms them again.
+ * Pointers are aligned to their element.  last_state may be h0 itself (the
+ * state steps in place), not a part of it; no other output may overlap an
+ * input.  Sums run in a fixed order: equal inputs give equal bits.
+ * ------------------------------------------------------------------------ */
+typedef struct mamba_recurrence_shape {
+  int64_t batch, seqlen, dim;
+  int64_t x_batch_stride, x_token_stride;
+  int64_t r_batch_stride, r_token_stride;
+  int64_t i_batch_stride, i_token_stride;
+  int64_t z_batch_stride, z_token_stride;   /* read where z is given */
+  int dtype;                                /* mamba_dtype */
+} mamba_recurrence_shape;
+
+/* Bytes of the checkpoints, and of device workspace (0 possible; SIZE_MAX for
+ * sizes outside the limits).  with_checkpoints: whether the backward gets
+ * them. */
+size_t mamba_gated_recurrence_checkpoint_size(const mamba_recurrence_shape* shape);
+size_t mamba_gated_recurrence_fwd_workspace_size(const mamba_recurrence_shape* shape);
+size_t mamba_gated_recurrence_bwd_workspace_size(const mamba_recurrence_shape* shape,
+                                                 int with_checkpoints);
+
+/* Forward.  z, h0, reset, last_state, checkpoints may be NULL. */
+mamba_status mamba_gated_recurrence_fwd(const mamba_recurrence_shape* shape, const void* x,
+                                        const void* r, const void* i, const float* A,
+                                        const void* z, const float* h0, const uint8_t* reset,
+                                        void* out, float* last_state, float* checkpoints,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward.  dlast_state (nullable) is the gradient into the last state.  dz
+ * is required with z; dh0 may be NULL, and is refused without h0. */
+mamba_status mamba_gated_recurrence_bwd(const mamba_recurrence_shape* shape, const void* x,
+                                        const void* r, const void* i, const float* A,
+                                        const void* z, const float* h0, const uint8_t* reset,
+                                        const void* dout, const float* dlast_state,
+                                        const float* checkpoints, void* dx, void* dr, void* di,
+                                        float* dA, void* dz, float* dh0, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* One step (shape->seqlen must be 1; the batch strides apply), in place on a
+ * pool of states (pool, dim), with slots as for mamba_heads_state_update. */
+mamba_status mamba_gated_recurrence_update(const mamba_recurrence_shape* shape, float* state,
+                                           const int32_t* slots, int64_t pool, const void* x,
+                                           const void* r, const void* i, const float* A,
+                                           const void* z, void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm of rows (rows, dim) with the residual's addition, the
+ * stage that opens a block:
+ *
+ *   res = x + residual          (rounded once to residual_dt; x without residual)
+ *   out = res / sqrt(mean(res^2) + eps) * weight
+ *
+ * x and out in dt; residual and residual_out in residual_dt: dt or MAMBA_F32.
+ * The norm is of res as it is kept.  x and residual may be views (row strides in
+ * elements); residual_out, out and the gradients are dense.  weight (nullable
+ * = 1) and dweight (dim) float32.  Without residual there is no residual_out.
+ * residual_out may be residual itself where that is dense (the stream is
+ * carried on in place); no other output may overlap an input. */
+mamba_status mamba_residual_norm_fwd(const void* x, int64_t x_row_stride, const void* residual,
+                                     int64_t residual_row_stride, const float* weight,
+                                     int64_t rows, int64_t dim, float eps, mamba_dtype dt,
+                                     mamba_dtype residual_dt, void* out, void* residual_out,
+                                     void* stream);
+
+/* The same with out in 8 bits, e4m3 (4 exponent bits, 3 mantissa bits, largest
+ * value 448, no infinities), and a float32 scale a row:
+ *   scale = max(max|out|, 2^-100) / 448, the maximum over values that are not NaN,
+ *   out8 = out / scale, to the nearest, ties to even; a NaN stays one. */
+mamba_status mamba_residual_norm_fp8(const void* x, int64_t x_row_stride, const void* residual,
+                                     int64_t residual_row_stride, const float* weight,
+                                     int64_t rows, int64_t dim, float eps, mamba_dtype dt,
+                                     mamba_dtype residual_dt, uint8_t* out8, float* scale,
+                                     void* residual_out, void* stream);
+
+size_t mamba_residual_norm_bwd_workspace_size(int64_t rows, int64_t dim);
+
+/* Backward, from res as the forward kept it (residual_dt; a view may be given):
+ * the gradient at res, with dres (nullable, dense, residual_dt) that comes to
+ * it from the stream, is that of x and of residual:
+ *   d = dres + (dout w - res mean(dout w res) / (mean(res^2) + eps))
+ *              / sqrt(mean(res^2) + eps)
+ * dx in dt.  dresidual (nullable) in residual_dt; refused where residual_dt is
+ * dt (it is dx).  dweight is required with weight.  The row statistics are
+ * formed again; sums run in a fixed order. */
+mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_row_stride,
+                                     const float* weight, const void* dout, const void* dres,
+                                     int64_t rows, int64_t dim, float eps, mamba_dtype dt,
+                                     mamba_dtype residual_dt, void* dx, void* dresidual,
+                                     float* dweight, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif

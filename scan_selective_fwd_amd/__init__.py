@@ -603,3 +603,14 @@ __all__ += ["heads_scan_fwd", "heads_scan_bwd", "heads_scan", "heads_state_updat
             "heads_fwd_workspace_bytes", "heads_bwd_workspace_bytes",
             "conv1d_tokens_fwd", "conv1d_tokens_bwd", "conv1d_tokens", "conv1d_tokens_update",
             "gated_norm_fwd", "gated_norm_bwd", "gated_norm"]
+
+from .recurrent import (gated_recurrence, gated_recurrence_bwd,  # noqa: E402
+                        gated_recurrence_bwd_workspace_bytes, gated_recurrence_checkpoint_shape,
+                        gated_recurrence_fwd, gated_recurrence_fwd_workspace_bytes,
+                        gated_recurrence_update, residual_norm, residual_norm_bwd,
+                        residual_norm_fp8, residual_norm_fwd)
+
+__all__ += ["gated_recurrence_fwd", "gated_recurrence_bwd", "gated_recurrence",
+            "gated_recurrence_update", "gated_recurrence_checkpoint_shape",
+            "gated_recurrence_fwd_workspace_bytes", "gated_recurrence_bwd_workspace_bytes",
+            "residual_norm_fwd", "residual_norm_fp8", "residual_norm_bwd", "residual_norm"]

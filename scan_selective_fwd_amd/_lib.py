@@ -39,6 +39,11 @@ EXPORTS = (
     "mamba_conv1d_tokens_fwd", "mamba_conv1d_tokens_bwd_workspace_size",
     "mamba_conv1d_tokens_bwd", "mamba_conv1d_tokens_update",
     "mamba_gated_norm_fwd", "mamba_gated_norm_bwd_workspace_size", "mamba_gated_norm_bwd",
+    "mamba_gated_recurrence_checkpoint_size", "mamba_gated_recurrence_fwd_workspace_size",
+    "mamba_gated_recurrence_bwd_workspace_size", "mamba_gated_recurrence_fwd",
+    "mamba_gated_recurrence_bwd", "mamba_gated_recurrence_update",
+    "mamba_residual_norm_fwd", "mamba_residual_norm_fp8",
+    "mamba_residual_norm_bwd_workspace_size", "mamba_residual_norm_bwd",
 )
 
 
@@ -64,6 +69,15 @@ class HeadsShape(ctypes.Structure):
         "u_batch_stride", "u_token_stride", "delta_batch_stride", "delta_token_stride",
         "B_batch_stride", "B_token_stride", "C_batch_stride", "C_token_stride")]
         + [(n, _int) for n in ("delta_softplus", "disc", "dtype", "segments")])
+
+
+class RecurrenceShape(ctypes.Structure):
+    """mamba_recurrence_shape."""
+
+    _fields_ = ([(n, _i64) for n in (
+        "batch", "seqlen", "dim", "x_batch_stride", "x_token_stride", "r_batch_stride",
+        "r_token_stride", "i_batch_stride", "i_token_stride", "z_batch_stride",
+        "z_token_stride")] + [("dtype", _int)])
 
 
 _lib = None
@@ -168,9 +182,30 @@ def load(path: str = LIB_PATH):
     lib.mamba_gated_norm_bwd_workspace_size.argtypes = [_i64] * 3
     lib.mamba_gated_norm_bwd.argtypes = ([_vp, _i64, _vp, _i64, _vp, _vp] + [_i64] * 3
                                          + [_f32, _int, _int] + [_vp] * 4 + [_sz, _vp])
+    rec = ctypes.POINTER(RecurrenceShape)
+    for name in ("mamba_gated_recurrence_checkpoint_size",
+                 "mamba_gated_recurrence_fwd_workspace_size"):
+        f = getattr(lib, name)
+        f.restype = _sz
+        f.argtypes = [rec]
+    lib.mamba_gated_recurrence_bwd_workspace_size.restype = _sz
+    lib.mamba_gated_recurrence_bwd_workspace_size.argtypes = [rec, _int]
+    lib.mamba_gated_recurrence_fwd.argtypes = [rec] + [_vp] * 11 + [_sz, _vp]
+    lib.mamba_gated_recurrence_bwd.argtypes = [rec] + [_vp] * 17 + [_sz, _vp]
+    lib.mamba_gated_recurrence_update.argtypes = [rec, _vp, _vp, _i64] + [_vp] * 7
+    norm_in = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _f32, _int, _int]
+    lib.mamba_residual_norm_fwd.argtypes = norm_in + [_vp] * 3
+    lib.mamba_residual_norm_fp8.argtypes = norm_in + [_vp] * 4
+    lib.mamba_residual_norm_bwd_workspace_size.restype = _sz
+    lib.mamba_residual_norm_bwd_workspace_size.argtypes = [_i64, _i64]
+    lib.mamba_residual_norm_bwd.argtypes = ([_vp, _i64] + [_vp] * 3 + [_i64, _i64, _f32, _int, _int]
+                                            + [_vp] * 4 + [_sz, _vp])
     for name in ("mamba_heads_scan_fwd", "mamba_heads_scan_bwd", "mamba_heads_state_update",
                  "mamba_conv1d_tokens_fwd", "mamba_conv1d_tokens_bwd",
-                 "mamba_conv1d_tokens_update", "mamba_gated_norm_fwd", "mamba_gated_norm_bwd"):
+                 "mamba_conv1d_tokens_update", "mamba_gated_norm_fwd", "mamba_gated_norm_bwd",
+                 "mamba_gated_recurrence_fwd", "mamba_gated_recurrence_bwd",
+                 "mamba_gated_recurrence_update", "mamba_residual_norm_fwd",
+                 "mamba_residual_norm_fp8", "mamba_residual_norm_bwd"):
         getattr(lib, name).restype = _int
     _lib = lib
     return lib

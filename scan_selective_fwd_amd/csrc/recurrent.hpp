@@ -1,0 +1,83 @@
+// Parameters and dispatchers of the recurrent block's operators: the gated
+// linear recurrence and the norm with the residual's addition.
+#pragma once
+
+#include "heads.hpp"
+
+namespace mscan {
+
+struct RecParams {
+  Rows x, r, i, z;       // z.p nullable
+  const float* A;
+  const float* h0;       // nullable
+  const uint8_t* reset;  // nullable
+  int64_t batch, L, dim;
+  // forward
+  void* out;
+  float* last;           // nullable
+  float* ckpt;           // nullable, (batch, tiles, dim): the state entering each kRecTile steps
+  // backward
+  const void* dout;
+  const float* dlast;    // nullable
+  const float* kept;     // the checkpoints
+  void* dx;
+  void* dr;
+  void* di;
+  void* dz;              // nullable
+  float* dA;
+  float* dh0;            // nullable
+  float* part;           // workspace, (batch, dim): the rows' shares of dA
+  float* states;         // workspace, (batch, kRecTile, dim)
+};
+
+constexpr int64_t kRecTile = 64;   // steps between checkpoints
+
+hipError_t dispatch_rec_fwd(const RecParams& p, int dtype, hipStream_t s);
+hipError_t dispatch_rec_bwd(const RecParams& p, int dtype, hipStream_t s);
+
+struct RecStepParams {
+  const void* x;
+  const void* r;
+  const void* i;
+  const void* z;         // nullable
+  int64_t x_row, r_row, i_row, z_row;
+  const float* A;
+  float* state;
+  const int32_t* slots;  // nullable
+  int64_t pool, batch, dim;
+  void* out;
+};
+
+hipError_t dispatch_rec_step(const RecStepParams& p, int dtype, hipStream_t s);
+
+struct ResNormParams {
+  const void* x;         // the backward's: nothing
+  const void* res;       // nullable in the forward; the kept sum in the backward
+  const float* w;        // nullable
+  int64_t x_row, res_row;
+  int64_t rows, dim;
+  float eps;
+  bool vec;              // every row starts on 16 bytes
+  void* out;
+  float* scale;          // 8 bits
+  void* res_out;         // nullable
+  // backward
+  const void* dout;
+  const void* dres;      // nullable
+  void* dx;
+  void* dresidual;       // nullable
+  float* dw;             // nullable
+  float* part;           // (parts, dim)
+  int64_t parts;
+};
+
+// Types of a call: x, residual and out.
+enum ResNormKind { kResF32, kResBf16, kResBf16F32 };   // x and residual alike, or bf16 on float32
+
+// Blocks that share the rows in the norm's backward.
+int64_t res_norm_parts(int64_t rows);
+
+hipError_t dispatch_res_norm_fwd(const ResNormParams& p, ResNormKind kind, bool fp8, hipStream_t s);
+hipError_t dispatch_res_norm_bwd(const ResNormParams& p, ResNormKind kind, hipStream_t s);
+
+}  // namespace mscan

@@ -1,0 +1,340 @@
+// C ABI of the recurrent block's operators: argument checks, workspace carving
+// and dispatch.  Nothing here allocates, frees or synchronizes; every launch goes
+// on the caller's stream.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mamba_scan.h"
+#include "recurrent.hpp"
+
+namespace {
+
+constexpr int64_t kLim = (int64_t)1 << 62;
+
+int esize(int dt) { return dt == MAMBA_F32 ? 4 : 2; }
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// Nullable pointers pass.
+bool aligned_f32(const void* p) { return aligned(p, 4); }
+
+mamba_status hip_status(hipError_t e) { return e == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP; }
+
+hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
+
+// a * b <= kLim for a, b >= 0.
+bool mul_ok(int64_t a, int64_t b) { return b == 0 || a <= kLim / b; }
+
+// Whether (batch, tokens) rows at these strides stay inside 2^62 elements.
+bool span_ok(int64_t batch, int64_t sb, int64_t tokens, int64_t st) {
+  return mul_ok(batch, sb) && mul_ok(tokens, st) && batch * sb <= kLim - tokens * st;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Whether [a, a + n) and [b, b + n) overlap without being the same.
+bool partly(const void* a, const void* b, size_t n) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p != q && (p < q ? q - p : p - q) < n;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a && b && (p < q ? q - p < na : p - q < nb);
+}
+
+mamba_status check_shape(const mamba_recurrence_shape* s) {
+  if (!s) return MAMBA_ERR_NULL_PTR;
+  if (s->dtype != MAMBA_F32 && s->dtype != MAMBA_BF16) return MAMBA_ERR_DTYPE;
+  if (s->batch <= 0 || s->seqlen <= 0 || s->dim <= 0) return MAMBA_ERR_SHAPE;
+  if (s->x_batch_stride < 0 || s->x_token_stride < 0 || s->r_batch_stride < 0 ||
+      s->r_token_stride < 0 || s->i_batch_stride < 0 || s->i_token_stride < 0 ||
+      s->z_batch_stride < 0 || s->z_token_stride < 0)
+    return MAMBA_ERR_SHAPE;
+  if (s->dim > (int64_t)1 << 28 || s->seqlen > kLim / 64 / s->batch ||
+      s->dim > kLim / 64 / (s->batch * s->seqlen) ||
+      s->batch * s->dim > mscan::max_blocks(256) * 256)
+    return MAMBA_ERR_UNSUPPORTED;
+  if (!span_ok(s->batch, s->x_batch_stride, s->seqlen, s->x_token_stride) ||
+      !span_ok(s->batch, s->r_batch_stride, s->seqlen, s->r_token_stride) ||
+      !span_ok(s->batch, s->i_batch_stride, s->seqlen, s->i_token_stride) ||
+      !span_ok(s->batch, s->z_batch_stride, s->seqlen, s->z_token_stride))
+    return MAMBA_ERR_UNSUPPORTED;
+  return MAMBA_OK;
+}
+
+mamba_status check_inputs(const mamba_recurrence_shape* s, const void* x, const void* r,
+                          const void* i, const float* A, const void* z, const float* h0) {
+  if (!x || !r || !i || !A) return MAMBA_ERR_NULL_PTR;
+  const size_t es = (size_t)esize(s->dtype);
+  if (!aligned(x, es) || !aligned(r, es) || !aligned(i, es) || !aligned(z, es) ||
+      !aligned_f32(A) || !aligned_f32(h0))
+    return MAMBA_ERR_ALIGNMENT;
+  return MAMBA_OK;
+}
+
+// Whether a dense output of the sequence's size lies over one of its inputs.
+bool over_inputs(const void* out, const mamba_recurrence_shape* s, const void* x, const void* r,
+                 const void* i, const void* z) {
+  const size_t es = (size_t)esize(s->dtype);
+  const size_t n = (size_t)(s->batch * s->seqlen * s->dim) * es;
+  auto span = [&](int64_t sb, int64_t st) {
+    return (size_t)((s->batch - 1) * sb + (s->seqlen - 1) * st + s->dim) * es;
+  };
+  return overlap(out, n, x, span(s->x_batch_stride, s->x_token_stride)) ||
+         overlap(out, n, r, span(s->r_batch_stride, s->r_token_stride)) ||
+         overlap(out, n, i, span(s->i_batch_stride, s->i_token_stride)) ||
+         overlap(out, n, z, span(s->z_batch_stride, s->z_token_stride));
+}
+
+int64_t tiles(const mamba_recurrence_shape* s) {
+  return (s->seqlen + mscan::kRecTile - 1) / mscan::kRecTile;
+}
+
+mscan::RecParams common(const mamba_recurrence_shape* s, const void* x, const void* r,
+                        const void* i, const float* A, const void* z, const float* h0,
+                        const uint8_t* reset) {
+  mscan::RecParams p{};
+  p.x = {x, s->x_batch_stride, s->x_token_stride};
+  p.r = {r, s->r_batch_stride, s->r_token_stride};
+  p.i = {i, s->i_batch_stride, s->i_token_stride};
+  p.z = {z, s->z_batch_stride, s->z_token_stride};
+  p.A = A; p.h0 = h0; p.reset = reset;
+  p.batch = s->batch; p.L = s->seqlen; p.dim = s->dim;
+  return p;
+}
+
+// Workspace of the backward.
+struct BwdLayout {
+  size_t part, states, ckpt, total;
+};
+
+BwdLayout bwd_layout(const mamba_recurrence_shape* s, bool given) {
+  const size_t row = (size_t)(s->batch * s->dim) * 4;
+  BwdLayout l;
+  l.part = 0;
+  l.states = up256(row);
+  l.ckpt = l.states + up256(row * (size_t)mscan::kRecTile);
+  l.total = l.ckpt + (given ? 0 : up256(row * (size_t)tiles(s)));
+  return l;
+}
+
+mamba_status check_norm(const void* x, int64_t x_row, const void* res, int64_t res_row,
+                        const float* weight, int64_t rows, int64_t dim, float eps, mamba_dtype dt,
+                        mamba_dtype rdt, mscan::ResNormKind* kind) {
+  if ((dt != MAMBA_F32 && dt != MAMBA_BF16) || (rdt != MAMBA_F32 && rdt != dt))
+    return MAMBA_ERR_DTYPE;
+  *kind = dt == MAMBA_F32 ? mscan::kResF32 : rdt == MAMBA_F32 ? mscan::kResBf16F32 : mscan::kResBf16;
+  if (rows <= 0 || dim <= 0 || x_row < 0 || res_row < 0) return MAMBA_ERR_SHAPE;
+  if (!(eps >= 0.0f)) return MAMBA_ERR_INVALID;
+  if (dim > (1 << 28) || rows > kLim / 16 / dim || !mul_ok(rows, x_row) || !mul_ok(rows, res_row))
+    return MAMBA_ERR_UNSUPPORTED;
+  if (!x) return MAMBA_ERR_NULL_PTR;
+  if (!aligned(x, (size_t)esize(dt)) || !aligned(res, (size_t)esize(rdt)) || !aligned_f32(weight))
+    return MAMBA_ERR_ALIGNMENT;
+  return MAMBA_OK;
+}
+
+// Whether rows at p start on 16 bytes.
+bool rows16(const void* p, int64_t row, int es) {
+  return aligned(p, 16) && row % (16 / es) == 0;
+}
+
+mamba_status norm_fwd(const void* x, int64_t x_row, const void* residual, int64_t res_row,
+                      const float* weight, int64_t rows, int64_t dim, float eps, mamba_dtype dt,
+                      mamba_dtype rdt, void* out, float* scale, bool fp8, void* residual_out,
+                      void* stream) {
+  mscan::ResNormKind kind;
+  mamba_status st =
+      check_norm(x, x_row, residual, residual ? res_row : 0, weight, rows, dim, eps, dt, rdt, &kind);
+  if (st != MAMBA_OK) return st;
+  if (!out || (fp8 && !scale) || (residual && !residual_out)) return MAMBA_ERR_NULL_PTR;
+  if (!residual && residual_out) return MAMBA_ERR_INVALID;
+  const int es = esize(dt), er = esize(rdt);
+  if ((!fp8 && !aligned(out, (size_t)es)) || !aligned_f32(scale) ||
+      !aligned(residual_out, (size_t)er))
+    return MAMBA_ERR_ALIGNMENT;
+  const size_t n = (size_t)(rows * dim), no = n * (fp8 ? 1 : (size_t)es), nr = n * (size_t)er;
+  const size_t sx = (size_t)((rows - 1) * x_row + dim) * (size_t)es;
+  const size_t sr = (size_t)((rows - 1) * res_row + dim) * (size_t)er;
+  if (overlap(out, no, x, sx) || (residual && overlap(out, no, residual, sr)) ||
+      (residual && overlap(residual_out, nr, x, sx)))
+    return MAMBA_ERR_INVALID;
+  // the stream is carried in place row on row, or apart
+  if (residual && overlap(residual_out, nr, residual, sr) &&
+      (residual_out != residual || (res_row != dim && rows > 1)))
+    return MAMBA_ERR_INVALID;
+  mscan::ResNormParams p{};
+  p.x = x; p.res = residual; p.w = weight; p.x_row = x_row; p.res_row = res_row;
+  p.rows = rows; p.dim = dim; p.eps = eps;
+  p.out = out; p.scale = scale; p.res_out = residual_out;
+  p.vec = dim % 8 == 0 && rows16(x, x_row, es) && (!residual || rows16(residual, res_row, er)) &&
+          aligned(weight, 16) && aligned(out, fp8 ? 8 : 16) && aligned(residual_out, 16);
+  return hip_status(mscan::dispatch_res_norm_fwd(p, kind, fp8, as_stream(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mamba_gated_recurrence_checkpoint_size(const mamba_recurrence_shape* shape) {
+  if (check_shape(shape) != MAMBA_OK) return SIZE_MAX;
+  return (size_t)(shape->batch * shape->dim) * (size_t)tiles(shape) * 4;
+}
+
+size_t mamba_gated_recurrence_fwd_workspace_size(const mamba_recurrence_shape* shape) {
+  return check_shape(shape) == MAMBA_OK ? 0 : SIZE_MAX;
+}
+
+size_t mamba_gated_recurrence_bwd_workspace_size(const mamba_recurrence_shape* shape,
+                                                 int with_checkpoints) {
+  return check_shape(shape) == MAMBA_OK ? bwd_layout(shape, with_checkpoints != 0).total : SIZE_MAX;
+}
+
+mamba_status mamba_gated_recurrence_fwd(const mamba_recurrence_shape* shape, const void* x,
+                                        const void* r, const void* i, const float* A,
+                                        const void* z, const float* h0, const uint8_t* reset,
+                                        void* out, float* last_state, float* checkpoints,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  mamba_status st = check_shape(shape);
+  if (st != MAMBA_OK) return st;
+  st = check_inputs(shape, x, r, i, A, z, h0);
+  if (st != MAMBA_OK) return st;
+  if (!out) return MAMBA_ERR_NULL_PTR;
+  if (!aligned(out, (size_t)esize(shape->dtype)) || !aligned_f32(last_state) ||
+      !aligned_f32(checkpoints))
+    return MAMBA_ERR_ALIGNMENT;
+  if (h0 && last_state && partly(h0, last_state, (size_t)(shape->batch * shape->dim) * 4))
+    return MAMBA_ERR_INVALID;
+  if (over_inputs(out, shape, x, r, i, z)) return MAMBA_ERR_INVALID;
+  const size_t need = mamba_gated_recurrence_fwd_workspace_size(shape);
+  if (need && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
+  if (need && !aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
+  mscan::RecParams p = common(shape, x, r, i, A, z, h0, reset);
+  p.out = out; p.last = last_state; p.ckpt = checkpoints;
+  return hip_status(mscan::dispatch_rec_fwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,
+                                            as_stream(stream)));
+}
+
+mamba_status mamba_gated_recurrence_bwd(const mamba_recurrence_shape* shape, const void* x,
+                                        const void* r, const void* i, const float* A,
+                                        const void* z, const float* h0, const uint8_t* reset,
+                                        const void* dout, const float* dlast_state,
+                                        const float* checkpoints, void* dx, void* dr, void* di,
+                                        float* dA, void* dz, float* dh0, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  mamba_status st = check_shape(shape);
+  if (st != MAMBA_OK) return st;
+  st = check_inputs(shape, x, r, i, A, z, h0);
+  if (st != MAMBA_OK) return st;
+  if (!dout || !dx || !dr || !di || !dA) return MAMBA_ERR_NULL_PTR;
+  if ((z != nullptr) != (dz != nullptr) || (dh0 && !h0)) return MAMBA_ERR_INVALID;
+  const size_t es = (size_t)esize(shape->dtype);
+  if (!aligned(dout, es) || !aligned(dx, es) || !aligned(dr, es) || !aligned(di, es) ||
+      !aligned(dz, es) || !aligned_f32(dlast_state) || !aligned_f32(checkpoints) ||
+      !aligned_f32(dA) || !aligned_f32(dh0))
+    return MAMBA_ERR_ALIGNMENT;
+  if (over_inputs(dx, shape, x, r, i, z) || over_inputs(dr, shape, x, r, i, z) ||
+      over_inputs(di, shape, x, r, i, z) || over_inputs(dz, shape, x, r, i, z))
+    return MAMBA_ERR_INVALID;
+  const BwdLayout l = bwd_layout(shape, checkpoints != nullptr);
+  if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
+  mscan::RecParams p = common(shape, x, r, i, A, z, h0, reset);
+  char* ws = static_cast<char*>(workspace);
+  p.dout = dout; p.dlast = dlast_state;
+  p.dx = dx; p.dr = dr; p.di = di; p.dz = dz; p.dA = dA; p.dh0 = dh0;
+  p.part = reinterpret_cast<float*>(ws + l.part);
+  p.states = reinterpret_cast<float*>(ws + l.states);
+  if (!checkpoints) p.ckpt = reinterpret_cast<float*>(ws + l.ckpt);
+  p.kept = checkpoints ? checkpoints : p.ckpt;
+  return hip_status(mscan::dispatch_rec_bwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,
+                                            as_stream(stream)));
+}
+
+mamba_status mamba_gated_recurrence_update(const mamba_recurrence_shape* shape, float* state,
+                                           const int32_t* slots, int64_t pool, const void* x,
+                                           const void* r, const void* i, const float* A,
+                                           const void* z, void* out, void* stream) {
+  mamba_status st = check_shape(shape);
+  if (st != MAMBA_OK) return st;
+  if (shape->seqlen != 1 || pool <= 0 || (!slots && pool < shape->batch)) return MAMBA_ERR_SHAPE;
+  if (pool > kLim / 16 / shape->dim) return MAMBA_ERR_UNSUPPORTED;
+  st = check_inputs(shape, x, r, i, A, z, nullptr);
+  if (st != MAMBA_OK) return st;
+  if (!state || !out) return MAMBA_ERR_NULL_PTR;
+  if (!aligned(out, (size_t)esize(shape->dtype)) || !aligned_f32(state) || !aligned(slots, 4))
+    return MAMBA_ERR_ALIGNMENT;
+  if (over_inputs(out, shape, x, r, i, z)) return MAMBA_ERR_INVALID;
+  mscan::RecStepParams p{};
+  p.x = x; p.r = r; p.i = i; p.z = z;
+  p.x_row = shape->x_batch_stride; p.r_row = shape->r_batch_stride;
+  p.i_row = shape->i_batch_stride; p.z_row = shape->z_batch_stride;
+  p.A = A; p.state = state; p.slots = slots; p.pool = pool;
+  p.batch = shape->batch; p.dim = shape->dim; p.out = out;
+  return hip_status(mscan::dispatch_rec_step(p, shape->dtype == MAMBA_F32 ? 0 : 1,
+                                             as_stream(stream)));
+}
+
+mamba_status mamba_residual_norm_fwd(const void* x, int64_t x_row_stride, const void* residual,
+                                     int64_t residual_row_stride, const float* weight,
+                                     int64_t rows, int64_t dim, float eps, mamba_dtype dt,
+                                     mamba_dtype residual_dt, void* out, void* residual_out,
+                                     void* stream) {
+  return norm_fwd(x, x_row_stride, residual, residual_row_stride, weight, rows, dim, eps, dt,
+                  residual_dt, out, nullptr, false, residual_out, stream);
+}
+
+mamba_status mamba_residual_norm_fp8(const void* x, int64_t x_row_stride, const void* residual,
+                                     int64_t residual_row_stride, const float* weight,
+                                     int64_t rows, int64_t dim, float eps, mamba_dtype dt,
+                                     mamba_dtype residual_dt, uint8_t* out8, float* scale,
+                                     void* residual_out, void* stream) {
+  return norm_fwd(x, x_row_stride, residual, residual_row_stride, weight, rows, dim, eps, dt,
+                  residual_dt, out8, scale, true, residual_out, stream);
+}
+
+size_t mamba_residual_norm_bwd_workspace_size(int64_t rows, int64_t dim) {
+  static const float dummy[4] = {};
+  mscan::ResNormKind kind;
+  if (check_norm(dummy, dim, dummy, dim, nullptr, rows, dim, 0.0f, MAMBA_F32, MAMBA_F32, &kind) !=
+      MAMBA_OK)
+    return SIZE_MAX;
+  return up256((size_t)mscan::res_norm_parts(rows) * (size_t)dim * 4);
+}
+
+mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_row_stride,
+                                     const float* weight, const void* dout, const void* dres,
+                                     int64_t rows, int64_t dim, float eps, mamba_dtype dt,
+                                     mamba_dtype residual_dt, void* dx, void* dresidual,
+                                     float* dweight, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  mscan::ResNormKind kind;
+  mamba_status st = check_norm(dout, dim, res, res_row_stride, weight, rows, dim, eps, dt,
+                               residual_dt, &kind);
+  if (st != MAMBA_OK) return st;
+  if (!res || !dx) return MAMBA_ERR_NULL_PTR;
+  if ((weight != nullptr) != (dweight != nullptr) || (dresidual && residual_dt == dt))
+    return MAMBA_ERR_INVALID;
+  const int es = esize(dt), er = esize(residual_dt);
+  if (!aligned(dres, (size_t)er) || !aligned(dx, (size_t)es) || !aligned(dresidual, (size_t)er) ||
+      !aligned_f32(dweight))
+    return MAMBA_ERR_ALIGNMENT;
+  const size_t n = (size_t)(rows * dim);
+  if (overlap(dx, n * (size_t)es, dout, n * (size_t)es) ||
+      overlap(dx, n * (size_t)es, res, (size_t)((rows - 1) * res_row_stride + dim) * (size_t)er))
+    return MAMBA_ERR_INVALID;
+  const size_t need = mamba_residual_norm_bwd_workspace_size(rows, dim);
+  if (need == SIZE_MAX) return MAMBA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
+  mscan::ResNormParams p{};
+  p.res = res; p.res_row = res_row_stride; p.w = weight; p.rows = rows; p.dim = dim; p.eps = eps;
+  p.dout = dout; p.dres = dres; p.dx = dx; p.dresidual = dresidual; p.dw = dweight;
+  p.part = static_cast<float*>(workspace);
+  p.parts = mscan::res_norm_parts(rows);
+  p.vec = dim % 8 == 0 && rows16(res, res_row_stride, er) && aligned(dout, 16) &&
+          aligned(dres, 16) && aligned(weight, 16) && aligned(dx, 16) && aligned(dresidual, 16);
+  return hip_status(mscan::dispatch_res_norm_bwd(p, kind, as_stream(stream)));
+}
+
+}  // extern "C"

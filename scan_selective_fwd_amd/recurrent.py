@@ -1,0 +1,350 @@
+"""Operators of a recurrent block over token-major rows: thin PyTorch binding.
+
+    residual_norm_*      the norm that opens a block, with the residual's addition;
+                         its output in the activations' type or in 8 bits
+    gated_recurrence_*   the gated linear recurrence: x, r, i, z (batch, L, dim),
+                         A (dim,), states (batch, dim) or a pool (pool, dim)
+
+Activations are float32 or bfloat16, all the same; x, r, i, z and the norm's x
+and residual may be views of wider rows (their last dimension contiguous).
+Weights and states are float32.  Gradients have the type of the tensor they
+belong to, each rounded once from a float32 sum.  Every call only enqueues
+kernels on the current stream of its tensors' device.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from . import MambaScanError, _dtype_code, _first_order, _flags, _lib, _ptr, lib
+from .heads import (_dims, _gpu, _req, _rows, _slots, _stream, _view, _workspace)
+
+_F32 = torch.float32
+_FP8 = torch.float8_e4m3fn
+_current = torch._C._cuda_getDevice
+
+
+def _call(name, dev, *args):
+    """The library's call with `dev` the current device, whose stream it goes on."""
+    if _current() == dev.index:
+        st = getattr(lib(), name)(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(lib(), name)(*args, _stream(dev))
+    if st:
+        _lib.check(st, name)
+
+
+@functools.lru_cache(maxsize=1024)
+def _struct(*fields):
+    """mamba_recurrence_shape of these fields, in their order, and a reference to
+    it.  The calls only read it."""
+    s = _lib.RecurrenceShape(*fields)
+    return s, ctypes.byref(s)
+
+
+def _new(like, dev, dtype=None):
+    return torch.empty(like.shape, dtype=dtype or like.dtype, device=dev)
+
+
+# --------------------------------------------------------------------------- recurrence
+
+def _shape(x, r, i, z):
+    dev = _gpu(x, "x")
+    shape = _dims(x, "x", 3)
+    dt = x.dtype
+    code = _dtype_code(x)
+    s, ref = _struct(*shape, *_view(x, "x", dt, shape, dev, 2), *_view(r, "r", dt, shape, dev, 2),
+                     *_view(i, "i", dt, shape, dev, 2),
+                     *((0, 0) if z is None else _view(z, "z", dt, shape, dev, 2)), code)
+    return s, ref, dev, shape
+
+
+def _state_args(s, A, h0, reset, dev):
+    _req(A, "A", _F32, (s.dim,), dev)
+    _req(h0, "h0", _F32, (s.batch, s.dim), dev)
+    return _flags(reset, (s.batch, s.seqlen), dev)
+
+
+def _tiles(L):
+    return -(-L // 64)
+
+
+def gated_recurrence_checkpoint_shape(batch, L, dim):
+    """Shape of the forward's checkpoints: the state entering every 64th step."""
+    return (batch, _tiles(L), dim)
+
+
+def _query(fn, batch, L, dim, dtype, *more):
+    s = _lib.RecurrenceShape(batch=batch, seqlen=L, dim=dim,
+                             dtype=0 if dtype == torch.float32 else 1)
+    n = int(getattr(lib(), fn)(ctypes.byref(s), *more))
+    if n >= 2 ** 63:
+        raise MambaScanError(2 if min(batch, L, dim) <= 0 else 6, fn)
+    return n
+
+
+def gated_recurrence_fwd_workspace_bytes(batch, L, dim, dtype=torch.float32) -> int:
+    return _query("mamba_gated_recurrence_fwd_workspace_size", batch, L, dim, dtype)
+
+
+def gated_recurrence_bwd_workspace_bytes(batch, L, dim, dtype=torch.float32,
+                                         with_checkpoints=True) -> int:
+    return _query("mamba_gated_recurrence_bwd_workspace_size", batch, L, dim, dtype,
+                  int(bool(with_checkpoints)))
+
+
+def gated_recurrence_fwd(x, r, i, A, z=None, h0=None, *, reset=None, return_last_state=False,
+                         out=None, last_state=None, checkpoints=None, workspace=None):
+    """Gated linear recurrence over a prompt, with s(v) = 1 / (1 + exp(-v)):
+
+        a_t = exp(A s(r_t)),  h_t = a_t h_{t-1} + sqrt(1 - a_t^2) s(i_t) x_t
+        out_t = h_t  (h_t z_t s(z_t) with z),  A <= 0
+
+    Returns out (batch, L, dim), or (out, last_state).  `last_state`: a tensor to
+    receive it, h0 itself where the state is to step in place.  `reset`: (batch,
+    L) uint8/bool flags of packed sequences: the state before a flagged step is
+    left out.  `checkpoints`: a float32 tensor of
+    gated_recurrence_checkpoint_shape that receives the state entering every
+    64th step, for gated_recurrence_bwd.  `workspace`: a contiguous GPU tensor of
+    at least gated_recurrence_fwd_workspace_bytes, reused across calls
+    (allocated when absent or smaller)."""
+    s, ref, dev, shape = _shape(x, r, i, z)
+    reset = _state_args(s, A, h0, reset, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    else:
+        _req(out, "out", x.dtype, shape, dev)
+    if return_last_state and last_state is None:
+        last_state = torch.empty((s.batch, s.dim), dtype=_F32, device=dev)
+    else:
+        _req(last_state, "last_state", _F32, (s.batch, s.dim), dev)
+    if checkpoints is not None:
+        _req(checkpoints, "checkpoints", _F32, (s.batch, _tiles(s.seqlen), s.dim), dev)
+    n = lib().mamba_gated_recurrence_fwd_workspace_size(ref)
+    ws = _workspace(n, shape, "mamba_gated_recurrence_fwd", workspace, dev)
+    _call("mamba_gated_recurrence_fwd", dev, ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(z),
+          _ptr(h0), _ptr(reset), _ptr(out), _ptr(last_state), _ptr(checkpoints),
+          _ptr(ws) if n else None, n)
+    return (out, last_state) if return_last_state else out
+
+
+def gated_recurrence_bwd(x, r, i, A, z, dout, h0=None, *, dlast_state=None, reset=None,
+                         checkpoints=None, workspace=None):
+    """Backward of gated_recurrence_fwd for the gradient `dout` at out and,
+    optionally, `dlast_state` at the last state.  `checkpoints`: those of the
+    forward over the same inputs; absent, they are formed again.  Returns a
+    dict: dx, dr, di (and dz) in their tensors' type, dA (and dh0) in
+    float32."""
+    s, ref, dev, shape = _shape(x, r, i, z)
+    reset = _state_args(s, A, h0, reset, dev)
+    _req(_need(dout, "dout"), "dout", x.dtype, shape, dev)
+    _req(dlast_state, "dlast_state", _F32, (s.batch, s.dim), dev)
+    if checkpoints is not None:
+        _req(checkpoints, "checkpoints", _F32, (s.batch, _tiles(s.seqlen), s.dim), dev)
+    g = dict(dx=_new(x, dev), dr=_new(x, dev), di=_new(x, dev), dA=_new(A, dev))
+    if z is not None:
+        g["dz"] = _new(x, dev)
+    if h0 is not None:
+        g["dh0"] = _new(h0, dev)
+    n = lib().mamba_gated_recurrence_bwd_workspace_size(ref, int(checkpoints is not None))
+    ws = _workspace(n, shape, "mamba_gated_recurrence_bwd", workspace, dev)
+    _call("mamba_gated_recurrence_bwd", dev, ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(z),
+          _ptr(h0), _ptr(reset), _ptr(dout), _ptr(dlast_state), _ptr(checkpoints), _ptr(g["dx"]),
+          _ptr(g["dr"]), _ptr(g["di"]), _ptr(g["dA"]), _ptr(g.get("dz")), _ptr(g.get("dh0")),
+          _ptr(ws) if n else None, n)
+    return g
+
+
+def gated_recurrence_update(state, x, r, i, A, z=None, *, slots=None, out=None):
+    """One step for a batch of sequences; `state` (pool, dim) float32 is updated
+    in place.  x, r, i, z (batch, dim).  `slots` (batch,) int32: the state of each
+    row (all different); a row whose slot lies outside the pool is left out and
+    gives zeros.  Returns out (batch, dim)."""
+    dev = _gpu(state, "state")
+    _gpu(x, "x")
+    shape = _dims(x, "x", 2)
+    batch, dim = shape
+    dt = x.dtype
+    pool = _dims(state, "state", 2)[0]
+    s, ref = _struct(batch, 1, dim, *_view(x, "x", dt, shape, dev, 1), 0,
+                     *_view(r, "r", dt, shape, dev, 1), 0, *_view(i, "i", dt, shape, dev, 1), 0,
+                     *((0,) if z is None else _view(z, "z", dt, shape, dev, 1)), 0,
+                     _dtype_code(x))
+    _req(A, "A", _F32, (dim,), dev)
+    _req(state, "state", _F32, (pool, dim), dev)
+    slots = _slots(slots, batch, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        _req(out, "out", dt, shape, dev)
+    _call("mamba_gated_recurrence_update", dev, ref, _ptr(state), _ptr(slots), pool, _ptr(x),
+          _ptr(r), _ptr(i), _ptr(A), _ptr(z), _ptr(out))
+    return out
+
+
+def _need(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t
+
+
+class _GatedRecurrenceFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, r, i, A, z, h0, reset):
+        kept = torch.empty(gated_recurrence_checkpoint_shape(*_dims(_need(x, "x"), "x", 3)),
+                           dtype=_F32, device=x.device)
+        out, last = gated_recurrence_fwd(x, r, i, A, z, h0, reset=reset, return_last_state=True,
+                                         checkpoints=kept)
+        ctx.save_for_backward(x, r, i, A, z, h0, reset, kept)
+        ctx.set_materialize_grads(False)
+        return out, last
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, dout, dlast):
+        x, r, i, A, z, h0, reset, kept = ctx.saved_tensors
+        dout = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dout is None else dout
+        g = gated_recurrence_bwd(x, r, i, A, z, dout.contiguous(), h0,
+                                 dlast_state=None if dlast is None else dlast.contiguous(),
+                                 reset=reset, checkpoints=kept)
+        return g["dx"], g["dr"], g["di"], g["dA"], g.get("dz"), g.get("dh0"), None
+
+
+def gated_recurrence(x, r, i, A, z=None, h0=None, *, reset=None, return_last_state=False):
+    """gated_recurrence_fwd with gradients (through out and the last state)."""
+    reset = reset if reset is None or reset.dtype != torch.bool else reset.to(torch.uint8)
+    out, last = _GatedRecurrenceFn.apply(x, r, i, A, z, h0, reset)
+    return (out, last) if return_last_state else out
+
+
+# --------------------------------------------------------------------------- norm
+
+def _residual_code(t, x):
+    """The code of a residual stream's type: x's, or float32."""
+    if t.dtype is not x.dtype and t.dtype is not _F32:
+        raise TypeError(f"residual has dtype {t.dtype}, expected {x.dtype} or torch.float32")
+    return _dtype_code(t)
+
+
+def _norm_args(x, residual, weight, residual_out):
+    dev = _gpu(x, "x")
+    code = rcode = _dtype_code(x)
+    x2 = _rows(x)
+    rows, dim = x2.shape
+    sx, = _view(x2, "x", x.dtype, (rows, dim), dev, 1)
+    r2, sr = None, 0
+    if residual is not None:
+        _gpu(residual, "residual")
+        rcode = _residual_code(residual, x)
+        if residual.shape != x.shape:
+            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected "
+                             f"{tuple(x.shape)}")
+        r2 = _rows(residual)
+        sr, = _view(r2, "residual", residual.dtype, (rows, dim), dev, 1)
+        if residual_out is None:
+            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=dev)
+        else:
+            _req(residual_out, "residual_out", residual.dtype, x.shape, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    _req(weight, "weight", _F32, (dim,), dev)
+    return dev, code, rcode, x2, sx, r2, sr, rows, dim, residual_out
+
+
+def residual_norm_fwd(x, residual=None, weight=None, *, eps=1e-5, out=None, residual_out=None):
+    """The residual's addition and the root-mean-square norm of the sum:
+
+        res = x + residual,  out = res / sqrt(mean(res^2) + eps) * weight
+
+    over the last dimension of x (..., dim).  `residual`: x's type or float32;
+    res is kept in it, and the norm is of what is kept.  Returns (out, res), out
+    like x; without a residual res is x itself.  `residual_out`: a tensor to
+    receive res, residual itself (dense) where the stream is carried in place."""
+    dev, code, rcode, x2, sx, r2, sr, rows, dim, kept = _norm_args(x, residual, weight,
+                                                                   residual_out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _req(out, "out", x.dtype, x.shape, dev)
+    _call("mamba_residual_norm_fwd", dev, _ptr(x2), sx, _ptr(r2), sr, _ptr(weight), rows, dim,
+          float(eps), code, rcode, _ptr(out), _ptr(kept))
+    return out, x if kept is None else kept
+
+
+def residual_norm_fp8(x, residual=None, weight=None, *, eps=1e-5, out=None, scale=None,
+                      residual_out=None):
+    """residual_norm_fwd with out in 8 bits: returns (out, scale, res), out
+    torch.float8_e4m3fn like x, scale float32 of x's shape without its last
+    dimension, max|out| / 448 of each row; out stands for out * scale."""
+    dev, code, rcode, x2, sx, r2, sr, rows, dim, kept = _norm_args(x, residual, weight,
+                                                                   residual_out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=_FP8, device=dev)
+    else:
+        _req(out, "out", _FP8, x.shape, dev)
+    if scale is None:
+        scale = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
+    else:
+        _req(scale, "scale", _F32, x.shape[:-1], dev)
+    _call("mamba_residual_norm_fp8", dev, _ptr(x2), sx, _ptr(r2), sr, _ptr(weight), rows, dim,
+          float(eps), code, rcode, _ptr(out), _ptr(scale), _ptr(kept))
+    return out, scale, x if kept is None else kept
+
+
+def residual_norm_bwd(res, weight, dout, dres=None, *, eps=1e-5, workspace=None):
+    """Backward of residual_norm_fwd from the res that it returned: `dout` (x's
+    type, dense) is the gradient at out, `dres` (res's type, dense) that which
+    comes to res from the stream.  Returns a dict: dx in dout's type, dresidual
+    in res's (dx itself where the types agree), and dweight float32 where weight
+    is given."""
+    dev = _gpu(res, "res")
+    _gpu(dout, "dout")
+    code, rcode = _dtype_code(dout), _residual_code(res, dout)
+    res2 = _rows(res)
+    rows, dim = res2.shape
+    sr, = _view(res2, "res", res.dtype, (rows, dim), dev, 1)
+    _req(weight, "weight", _F32, (dim,), dev)
+    _req(dout, "dout", dout.dtype, res.shape, dev)
+    _req(dres, "dres", res.dtype, res.shape, dev)
+    g = dict(dx=torch.empty(res.shape, dtype=dout.dtype, device=dev))
+    g["dresidual"] = g["dx"] if code == rcode else torch.empty(res.shape, dtype=_F32, device=dev)
+    if weight is not None:
+        g["dweight"] = torch.empty((dim,), dtype=_F32, device=dev)
+    n = lib().mamba_residual_norm_bwd_workspace_size(rows, dim)
+    ws = _workspace(n, (rows, dim), "mamba_residual_norm_bwd", workspace, dev)
+    _call("mamba_residual_norm_bwd", dev, _ptr(res2), sr, _ptr(weight), _ptr(dout), _ptr(dres),
+          rows, dim, float(eps), code, rcode, _ptr(g["dx"]),
+          None if code == rcode else _ptr(g["dresidual"]), _ptr(g.get("dweight")), _ptr(ws), n)
+    return g
+
+
+class _ResidualNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps):
+        out, res = residual_norm_fwd(x, residual, weight, eps=eps)
+        ctx.save_for_backward(res, weight)
+        ctx.eps, ctx.alone, ctx.x_dtype = eps, residual is None, x.dtype
+        ctx.set_materialize_grads(False)
+        return out if residual is None else (out, res)
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, dout, dres=None):
+        res, weight = ctx.saved_tensors
+        if dout is None:      # out was not used: the stream's gradient goes through
+            if dres is None:
+                return None, None, None, None
+            dout = torch.zeros(res.shape, dtype=ctx.x_dtype, device=res.device)
+        g = residual_norm_bwd(res, weight, dout.contiguous(),
+                              None if dres is None else dres.contiguous(), eps=ctx.eps)
+        return g["dx"], None if ctx.alone else g["dresidual"], g.get("dweight"), None
+
+
+def residual_norm(x, residual=None, weight=None, *, eps=1e-5):
+    """residual_norm_fwd with gradients (through out and res)."""
+    if residual is None:
+        return _ResidualNormFn.apply(x, None, weight, eps), x
+    return _ResidualNormFn.apply(x, residual, weight, eps)
