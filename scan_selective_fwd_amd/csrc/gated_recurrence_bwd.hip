@@ -1,4 +1,4 @@
-// Gated linear recurrence, forward and backward: a thread walks one channel of one
+// Gated linear recurrence, backward: a thread walks one channel of one
 // batch row, neighbours on neighbouring channels.
 #include "recurrent_common.hpp"
 
@@ -9,27 +9,6 @@ namespace {
 template <typename T>
 __device__ __forceinline__ float at(const Rows& q, int64_t b, int64_t t, int64_t d) {
   return Elem<T>::load1(static_cast<const T*>(q.p) + b * q.batch + t * q.token + d);
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void rec_fwd_kernel(const RecParams p) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= p.batch * p.dim) return;
-  const int64_t b = n / p.dim, d = n - b * p.dim;
-  const int64_t tiles = (p.L + kRecTile - 1) / kRecTile;
-  const float A2 = p.A[d] * kLog2e;
-  float h = p.h0 ? p.h0[n] : 0.0f;
-  for (int64_t t = 0; t < p.L; ++t) {
-    if (p.ckpt && t % kRecTile == 0) p.ckpt[(b * tiles + t / kRecTile) * p.dim + d] = h;
-    const RecGate g = rec_gate(at<T>(p.r, b, t, d), at<T>(p.i, b, t, d), A2);
-    const float v = __builtin_sqrtf(g.m2) * g.si * at<T>(p.x, b, t, d);
-    h = p.reset && p.reset[b * p.L + t] ? v : __builtin_fmaf(g.a, h, v);
-    if (p.out) {
-      const float y = p.z.p ? h * silu(at<T>(p.z, b, t, d)) : h;
-      Elem<T>::store1(static_cast<T*>(p.out) + (b * p.L + t) * p.dim + d, y);
-    }
-  }
-  if (p.last) p.last[n] = h;
 }
 
 template <typename T>
@@ -92,18 +71,13 @@ __global__ __launch_bounds__(256) void rec_sum_kernel(const RecParams p) {
 unsigned blocks(int64_t n) { return (unsigned)((n + 255) / 256); }
 
 template <typename T>
-hipError_t fwd_t(const RecParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((rec_fwd_kernel<T>), dim3(blocks(p.batch * p.dim)), dim3(256), 0, s, p);
-  return hipGetLastError();
-}
-
-template <typename T>
 hipError_t bwd_t(const RecParams& p, hipStream_t s) {
   if (p.ckpt) {   // the states at the tiles' starts
     RecParams f = p;
     f.out = nullptr;
     f.last = nullptr;
-    const hipError_t e = fwd_t<T>(f, s);
+    f.z.p = nullptr;
+    const hipError_t e = dispatch_rec_fwd(f, sizeof(T) == 4 ? 0 : 1, s);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((rec_bwd_kernel<T>), dim3(blocks(p.batch * p.dim)), dim3(256), 0, s, p);
@@ -114,10 +88,6 @@ hipError_t bwd_t(const RecParams& p, hipStream_t s) {
 }
 
 }  // namespace
-
-hipError_t dispatch_rec_fwd(const RecParams& p, int dtype, hipStream_t s) {
-  return dtype == 0 ? fwd_t<float>(p, s) : fwd_t<bf16_t>(p, s);
-}
 
 hipError_t dispatch_rec_bwd(const RecParams& p, int dtype, hipStream_t s) {
   return dtype == 0 ? bwd_t<float>(p, s) : bwd_t<bf16_t>(p, s);

@@ -1,0 +1,228 @@
+// Gated linear recurrence, forward.
+#include "recurrent_common.hpp"
+
+namespace mscan {
+
+namespace {
+
+constexpr int S = (int)kRecRun;
+constexpr int kMaxWaves = 16;
+
+template <typename T, int V, bool Z, bool CHAIN>
+__global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const uint32_t total) {
+  constexpr int C = 64 * V;                       // channels of a strip
+  constexpr int G = (int)kRecGroup;
+  __shared__ float sA[kMaxWaves][C], sH[kMaxWaves][C];
+  __shared__ int sCut[kMaxWaves];
+  __shared__ uint64_t sMap[CHAIN ? G : 1][CHAIN ? C : 1];
+  __shared__ uint32_t sTicket;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const uint32_t strips = (uint32_t)((p.dim + C - 1) / C);
+  const uint32_t across = strips * (uint32_t)p.batch;
+  const int64_t marks = (p.L + kRecTile - 1) / kRecTile;
+
+  for (uint32_t job = blockIdx.x;;) {
+    if constexpr (CHAIN) {
+      if (threadIdx.x == 0)
+        sTicket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      job = __builtin_amdgcn_readfirstlane(sTicket);
+    }
+    if (job >= total) return;
+    const uint32_t tile = job / across, at = job - tile * across;
+    const int64_t b = at / strips;
+    const int64_t c = (int64_t)(at - (uint32_t)b * strips) * C + lane * V;
+    const bool on = c < p.dim;
+    const int64_t cl = on ? c : 0;
+    const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
+    const int64_t left = p.L - t0;
+    const int n = left >= S ? S : left > 0 ? (int)left : 0;    // its steps
+
+    // every load of the run is in flight at once; steps past the end read the last
+    RecRaw<T, V> xr[S], rr[S], ir[S], zr[Z ? S : 1];
+    const T* x = static_cast<const T*>(p.x.p) + b * p.x.batch + cl;
+    const T* r = static_cast<const T*>(p.r.p) + b * p.r.batch + cl;
+    const T* i = static_cast<const T*>(p.i.p) + b * p.i.batch + cl;
+    const T* z = Z ? static_cast<const T*>(p.z.p) + b * p.z.batch + cl : nullptr;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int64_t t = t0 + s < p.L ? t0 + s : p.L - 1;
+      rr[s].load(r + t * p.r.token);
+      ir[s].load(i + t * p.i.token);
+      xr[s].load(x + t * p.x.token);
+      if constexpr (Z) zr[s].load(z + t * p.z.token);
+    }
+    uint32_t flags = 0;                                        // of the wave's steps
+    if (p.reset) {
+      const bool f = lane < n && p.reset[b * p.L + t0 + lane];
+      flags = (uint32_t)__ballot(f);
+    }
+    float A2[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A2[v] = p.A[cl + v] * kLog2e;
+
+    // the run's own map
+    float a[S][V], u[S][V], A[V], H[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      A[v] = 1.0f;
+      H[v] = 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const bool live = s < n, cut = flags >> s & 1;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
+        const float w = __builtin_sqrtf(g.m2) * g.si * xr[s].get(v);
+        a[s][v] = live ? g.a : 1.0f;
+        u[s][v] = live ? w : 0.0f;
+        H[v] = rec_apply(a[s][v], u[s][v], cut, H[v]);
+        A[v] *= a[s][v];
+      }
+    }
+    // the first run starts from h0, and says so by a map that leaves out what is before
+    // it: h0 is read here alone, before anything that last (h0's place, it may be) waits for
+    const bool first = t0 == 0 && p.h0;
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      h[v] = first ? p.h0[b * p.dim + cl + v] : 0.0f;
+      sA[wave][lane * V + v] = A[v];
+      sH[wave][lane * V + v] = first ? rec_apply(A[v], H[v], flags != 0, h[v]) : H[v];
+    }
+    if (lane == 0) sCut[wave] = first || flags != 0;
+    __syncthreads();
+
+    // the map of the waves before this one, and the tile's
+    float Ab[V], Hb[V], At[V], Ht[V];
+    bool cutb = false, cutt = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      Ab[v] = At[v] = 1.0f;
+      Hb[v] = Ht[v] = 0.0f;
+    }
+    for (int w = 0; w < waves; ++w) {
+      if (w == wave) {
+        cutb = cutt;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          Ab[v] = At[v];
+          Hb[v] = Ht[v];
+        }
+      }
+      const bool cw = sCut[w] != 0;
+      cutt = cutt || cw;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float Aw = sA[w][lane * V + v];
+        Ht[v] = rec_apply(Aw, sH[w][lane * V + v], cw, Ht[v]);
+        At[v] *= Aw;
+      }
+    }
+
+    // the state that enters the tile
+    if constexpr (CHAIN) {
+      const uint32_t tiles = (uint32_t)((p.L + kRecFwdTile - 1) / kRecFwdTile);
+      const uint32_t groups = (tiles + G - 1) / G;
+      const int j = tile % G;
+      const uint32_t group = tile / G;
+      uint64_t* maps = p.maps + ((uint64_t)b * tiles + tile) * p.dim + cl;
+      uint64_t* heads = p.heads + ((uint64_t)b * groups + group) * p.dim + cl;
+      if (wave == 0 && on && j != G - 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) rec_publish(maps + v, rec_pack(At[v], Ht[v], cutt));
+      }
+      // the maps of the group's earlier tiles, and the state after the group before
+      for (int k = wave; k < j; k += waves)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          sMap[k][lane * V + v] = rec_wait(maps - (int64_t)(j - k) * p.dim + v);
+      if (group && wave == (int)(j & (waves - 1)))
+#pragma unroll
+        for (int v = 0; v < V; ++v) sMap[j][lane * V + v] = rec_wait(heads - p.dim + v);
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (group) h[v] = __uint_as_float((uint32_t)sMap[j][lane * V + v]);
+      for (int k = 0; k < j; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const uint64_t m = sMap[k][lane * V + v];
+          const uint32_t hi = (uint32_t)(m >> 32) & ~kThere;
+          h[v] = rec_apply(__uint_as_float(hi), __uint_as_float((uint32_t)m), hi == kCutBits, h[v]);
+        }
+      if (j == G - 1 && wave == 0 && on)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          rec_publish(heads + v, rec_pack(0.0f, rec_apply(At[v], Ht[v], cutt, h[v]), false));
+    }
+    // and the wave's run
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = rec_apply(Ab[v], Hb[v], cutb, h[v]);
+    if (p.ckpt && on && t0 % kRecTile == 0 && n)
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.ckpt[(b * marks + t0 / kRecTile) * p.dim + c + v] = h[v];
+    if (p.out || p.last) {
+      T* out = static_cast<T*>(p.out) + (b * p.L + t0) * p.dim + c;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const bool cut = flags >> s & 1;
+        float y[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[v] = rec_apply(a[s][v], u[s][v], cut, h[v]);
+          y[v] = Z ? h[v] * silu(zr[Z ? s : 0].get(v)) : h[v];
+        }
+        if (p.out && on && s < n) rec_store<T, V>(out + s * p.dim, y);
+      }
+      if (p.last && on && left > 0 && left <= S)
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.last[b * p.dim + c + v] = h[v];
+    }
+    if constexpr (!CHAIN) return;
+    __syncthreads();     // the tile's shared memory has been read
+  }
+}
+
+__global__ __launch_bounds__(256) void rec_clear_kernel(uint64_t* p, int64_t n) {
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += step) p[k] = 0;
+}
+
+template <typename T, int V, bool Z>
+hipError_t go(const RecParams& p, hipStream_t s) {
+  const int64_t across = p.batch * rec_strips(p.dim, V == 2);
+  if (!p.ticket) {
+    const int waves = (int)((p.L + S - 1) / S);
+    hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, false>), dim3((unsigned)across), dim3(64 * waves),
+                       0, s, p, (uint32_t)across);
+    return hipGetLastError();
+  }
+  const int64_t total = across * ((p.L + kRecFwdTile - 1) / kRecFwdTile);
+  const int64_t clear = (p.words + 255) / 256;
+  hipLaunchKernelGGL(rec_clear_kernel, dim3((unsigned)(clear < 4096 ? clear : 4096)), dim3(256), 0,
+                     s, reinterpret_cast<uint64_t*>(p.ticket), p.words);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t grid = total < (1 << 20) ? total : (1 << 20);
+  hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, true>), dim3((unsigned)grid),
+                     dim3((unsigned)(kRecFwdTile / S * 64)), 0, s, p, (uint32_t)total);
+  return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t by_gate(const RecParams& p, hipStream_t s) {
+  return p.z.p ? go<T, V, true>(p, s) : go<T, V, false>(p, s);
+}
+
+}  // namespace
+
+hipError_t dispatch_rec_fwd(const RecParams& p, int dtype, hipStream_t s) {
+  if (dtype == 0) return by_gate<float, 1>(p, s);
+  return p.pairs ? by_gate<bf16_t, 2>(p, s) : by_gate<bf16_t, 1>(p, s);
+}
+
+}  // namespace mscan

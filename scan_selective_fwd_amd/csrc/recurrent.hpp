@@ -16,6 +16,12 @@ struct RecParams {
   void* out;
   float* last;           // nullable
   float* ckpt;           // nullable, (batch, tiles, dim): the state entering each kRecTile steps
+  bool pairs;            // rows start on 4 bytes and hold whole pairs of bfloat16
+  // workspace where the sequence takes several tiles
+  uint32_t* ticket;
+  uint64_t* maps;        // (batch, tiles, dim): the tiles' maps
+  uint64_t* heads;       // (batch, groups of tiles, dim): the state after each group
+  int64_t words;         // of ticket, maps and heads together, in 64 bits: cleared first
   // backward
   const void* dout;
   const float* dlast;    // nullable
@@ -31,6 +37,17 @@ struct RecParams {
 };
 
 constexpr int64_t kRecTile = 64;   // steps between checkpoints
+
+// The forward: a wave takes kRecRun steps, a block up to 16 waves of one row; longer
+// sequences take tiles of kRecFwdTile steps, joined kRecGroup at a time.
+constexpr int64_t kRecRun = 16;
+constexpr int64_t kRecOneTile = 16 * kRecRun;
+constexpr int64_t kRecFwdTile = 8 * kRecRun;
+constexpr int64_t kRecGroup = 16;
+
+constexpr int64_t rec_strips(int64_t dim, bool pairs) {
+  return pairs ? (dim + 127) / 128 : (dim + 63) / 64;
+}
 
 hipError_t dispatch_rec_fwd(const RecParams& p, int dtype, hipStream_t s);
 hipError_t dispatch_rec_bwd(const RecParams& p, int dtype, hipStream_t s);

@@ -10,6 +10,7 @@
 namespace {
 
 constexpr int64_t kLim = (int64_t)1 << 62;
+constexpr int64_t kGridLim = 0x7FFFFFFF;
 
 int esize(int dt) { return dt == MAMBA_F32 ? 4 : 2; }
 
@@ -42,6 +43,8 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a && b && (p < q ? q - p < na : p - q < nb);
 }
 
+int64_t fwd_tiles(int64_t L) { return (L + mscan::kRecFwdTile - 1) / mscan::kRecFwdTile; }
+
 mamba_status check_shape(const mamba_recurrence_shape* s) {
   if (!s) return MAMBA_ERR_NULL_PTR;
   if (s->dtype != MAMBA_F32 && s->dtype != MAMBA_BF16) return MAMBA_ERR_DTYPE;
@@ -52,7 +55,8 @@ mamba_status check_shape(const mamba_recurrence_shape* s) {
     return MAMBA_ERR_SHAPE;
   if (s->dim > (int64_t)1 << 28 || s->seqlen > kLim / 64 / s->batch ||
       s->dim > kLim / 64 / (s->batch * s->seqlen) ||
-      s->batch * s->dim > mscan::max_blocks(256) * 256)
+      s->batch > (s->seqlen > mscan::kRecOneTile ? kGridLim : mscan::max_blocks(1024)) /
+                     mscan::rec_strips(s->dim, false) / fwd_tiles(s->seqlen))
     return MAMBA_ERR_UNSUPPORTED;
   if (!span_ok(s->batch, s->x_batch_stride, s->seqlen, s->x_token_stride) ||
       !span_ok(s->batch, s->r_batch_stride, s->seqlen, s->r_token_stride) ||
@@ -103,9 +107,46 @@ mscan::RecParams common(const mamba_recurrence_shape* s, const void* x, const vo
   return p;
 }
 
+// Whether bfloat16 rows can be taken in pairs.
+bool pairs(const mamba_recurrence_shape* s, const void* x, const void* r, const void* i,
+           const void* z) {
+  auto ok = [](const void* p, int64_t sb, int64_t st) {
+    return aligned(p, 4) && sb % 2 == 0 && st % 2 == 0;
+  };
+  return s->dtype == MAMBA_BF16 && s->dim % 2 == 0 && ok(x, s->x_batch_stride, s->x_token_stride) &&
+         ok(r, s->r_batch_stride, s->r_token_stride) &&
+         ok(i, s->i_batch_stride, s->i_token_stride) &&
+         (!z || ok(z, s->z_batch_stride, s->z_token_stride));
+}
+
+// Workspace of the forward, none where one tile holds the sequence.
+struct FwdLayout {
+  size_t maps, heads, total;
+};
+
+FwdLayout fwd_layout(const mamba_recurrence_shape* s) {
+  if (s->seqlen <= mscan::kRecOneTile) return {0, 0, 0};
+  const int64_t n = fwd_tiles(s->seqlen), g = (n + mscan::kRecGroup - 1) / mscan::kRecGroup;
+  const size_t row = (size_t)(s->batch * s->dim) * 8;
+  FwdLayout l;
+  l.maps = 256;
+  l.heads = l.maps + row * (size_t)n;
+  l.total = l.heads + row * (size_t)g;
+  return l;
+}
+
+void carve(mscan::RecParams* p, const FwdLayout& l, void* workspace) {
+  if (!l.total) return;
+  char* ws = static_cast<char*>(workspace);
+  p->ticket = reinterpret_cast<uint32_t*>(ws);
+  p->maps = reinterpret_cast<uint64_t*>(ws + l.maps);
+  p->heads = reinterpret_cast<uint64_t*>(ws + l.heads);
+  p->words = (int64_t)(l.total / 8);
+}
+
 // Workspace of the backward.
 struct BwdLayout {
-  size_t part, states, ckpt, total;
+  size_t part, states, ckpt, fwd, total;
 };
 
 BwdLayout bwd_layout(const mamba_recurrence_shape* s, bool given) {
@@ -114,7 +155,8 @@ BwdLayout bwd_layout(const mamba_recurrence_shape* s, bool given) {
   l.part = 0;
   l.states = up256(row);
   l.ckpt = l.states + up256(row * (size_t)mscan::kRecTile);
-  l.total = l.ckpt + (given ? 0 : up256(row * (size_t)tiles(s)));
+  l.fwd = l.ckpt + (given ? 0 : up256(row * (size_t)tiles(s)));
+  l.total = l.fwd + (given ? 0 : up256(fwd_layout(s).total));
   return l;
 }
 
@@ -182,7 +224,7 @@ size_t mamba_gated_recurrence_checkpoint_size(const mamba_recurrence_shape* shap
 }
 
 size_t mamba_gated_recurrence_fwd_workspace_size(const mamba_recurrence_shape* shape) {
-  return check_shape(shape) == MAMBA_OK ? 0 : SIZE_MAX;
+  return check_shape(shape) == MAMBA_OK ? fwd_layout(shape).total : SIZE_MAX;
 }
 
 size_t mamba_gated_recurrence_bwd_workspace_size(const mamba_recurrence_shape* shape,
@@ -211,6 +253,8 @@ mamba_status mamba_gated_recurrence_fwd(const mamba_recurrence_shape* shape, con
   if (need && !aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
   mscan::RecParams p = common(shape, x, r, i, A, z, h0, reset);
   p.out = out; p.last = last_state; p.ckpt = checkpoints;
+  p.pairs = pairs(shape, x, r, i, z) && aligned(out, 4);
+  carve(&p, fwd_layout(shape), workspace);
   return hip_status(mscan::dispatch_rec_fwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,
                                             as_stream(stream)));
 }
@@ -245,7 +289,12 @@ mamba_status mamba_gated_recurrence_bwd(const mamba_recurrence_shape* shape, con
   p.dx = dx; p.dr = dr; p.di = di; p.dz = dz; p.dA = dA; p.dh0 = dh0;
   p.part = reinterpret_cast<float*>(ws + l.part);
   p.states = reinterpret_cast<float*>(ws + l.states);
-  if (!checkpoints) p.ckpt = reinterpret_cast<float*>(ws + l.ckpt);
+  p.pairs = pairs(shape, x, r, i, z) && aligned(dout, 4) && aligned(dx, 4) && aligned(dr, 4) &&
+            aligned(di, 4) && aligned(dz, 4);
+  if (!checkpoints) {
+    p.ckpt = reinterpret_cast<float*>(ws + l.ckpt);
+    carve(&p, fwd_layout(shape), ws + l.fwd);
+  }
   p.kept = checkpoints ? checkpoints : p.ckpt;
   return hip_status(mscan::dispatch_rec_bwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,
                                             as_stream(stream)));

@@ -42,4 +42,57 @@ __device__ __forceinline__ RecGate rec_gate(float r, float i, float A2) {
   return g;
 }
 
+// V channels of one token as they lie in memory: two bfloat16, or one element.
+template <typename T, int V>
+struct RecRaw {
+  static_assert(V == 1 || (V == 2 && sizeof(T) == 2), "V");
+  uint32_t w;
+  __device__ __forceinline__ void load(const T* q) {
+    if constexpr (V == 2) w = *reinterpret_cast<const uint32_t*>(q);
+    else if constexpr (sizeof(T) == 2) w = *q;
+    else w = __float_as_uint(*q);
+  }
+  __device__ __forceinline__ float get(int v) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+    else return v ? bf16_hi(w) : bf16_lo(w);
+  }
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void rec_store(T* q, const float (&y)[V]) {
+  if constexpr (V == 2) *reinterpret_cast<uint32_t*>(q) = pack_bf16(y[0], y[1]);
+  else store_vec<T, 1>(q, 0, y);
+}
+
+// The affine map h -> A h + H of a run of steps; `cut`: a flag in it leaves h out
+// whatever it holds.
+__device__ __forceinline__ float rec_apply(float A, float H, bool cut, float h) {
+  const float y = __builtin_fmaf(A, h, H);
+  return cut ? H : y;
+}
+
+// A run's map in one 64-bit word, whose store makes it valid: the sign of A, which is
+// never negative, says that it is there, an A of infinity that it is cut.
+constexpr uint32_t kThere = 0x80000000u, kCutBits = 0x7F800000u;
+
+__device__ __forceinline__ uint64_t rec_pack(float A, float H, bool cut) {
+  const uint32_t a = cut ? kCutBits : __float_as_uint(A);
+  return (uint64_t)(a | kThere) << 32 | __float_as_uint(H);
+}
+
+__device__ __forceinline__ void rec_publish(uint64_t* p, uint64_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Waits for the word at p.  Who writes it took an earlier ticket, so it runs already
+// and waits only for earlier tickets itself: the wait ends.
+__device__ __forceinline__ uint64_t rec_wait(uint64_t* p) {
+  uint64_t v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  while (!(v >> 63)) {
+    __builtin_amdgcn_s_sleep(1);
+    v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  return v;
+}
+
 }  // namespace mscan
