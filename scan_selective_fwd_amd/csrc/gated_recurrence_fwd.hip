@@ -8,7 +8,7 @@ namespace {
 constexpr int S = (int)kRecRun;
 constexpr int kMaxWaves = 16;
 
-template <typename T, int V, bool Z, bool CHAIN>
+template <typename T, int V, bool Z, bool RESET, bool CHAIN>
 __global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const uint32_t total) {
   constexpr int C = 64 * V;                       // channels of a strip
   constexpr int G = (int)kRecGroup;
@@ -33,29 +33,38 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const 
     if (job >= total) return;
     const uint32_t tile = job / across, at = job - tile * across;
     const int64_t b = at / strips;
-    const int64_t c = (int64_t)(at - (uint32_t)b * strips) * C + lane * V;
+    const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
     const bool on = c < p.dim;
-    const int64_t cl = on ? c : 0;
+    const uint32_t cl = on ? c : 0;
     const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
     const int64_t left = p.L - t0;
     const int n = left >= S ? S : left > 0 ? (int)left : 0;    // its steps
 
-    // every load of the run is in flight at once; steps past the end read the last
+    // every load of the run is in flight at once; steps past the end read the last.  A
+    // row's address is the same in every lane, a lane's place in it 32 bits.
     RecRaw<T, V> xr[S], rr[S], ir[S], zr[Z ? S : 1];
-    const T* x = static_cast<const T*>(p.x.p) + b * p.x.batch + cl;
-    const T* r = static_cast<const T*>(p.r.p) + b * p.r.batch + cl;
-    const T* i = static_cast<const T*>(p.i.p) + b * p.i.batch + cl;
-    const T* z = Z ? static_cast<const T*>(p.z.p) + b * p.z.batch + cl : nullptr;
+    auto row = [&](const Rows& q, int64_t t) {
+      return static_cast<const T*>(q.p) + b * q.batch + t * q.token;
+    };
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const int64_t t = t0 + s < p.L ? t0 + s : p.L - 1;
-      rr[s].load(r + t * p.r.token);
-      ir[s].load(i + t * p.i.token);
-      xr[s].load(x + t * p.x.token);
-      if constexpr (Z) zr[s].load(z + t * p.z.token);
+      rr[s].load(row(p.r, t) + cl);
+      ir[s].load(row(p.i, t) + cl);
+      xr[s].load(row(p.x, t) + cl);
+      if constexpr (Z) zr[s].load(row(p.z, t) + cl);
+    }
+    if (n < S) {                                               // those leave the state
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (s >= n) {
+          rr[s].fill(-INFINITY);
+          ir[s].fill(0.0f);
+          xr[s].fill(0.0f);
+        }
     }
     uint32_t flags = 0;                                        // of the wave's steps
-    if (p.reset) {
+    if constexpr (RESET) {
       const bool f = lane < n && p.reset[b * p.L + t0 + lane];
       flags = (uint32_t)__ballot(f);
     }
@@ -72,13 +81,12 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const 
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const bool live = s < n, cut = flags >> s & 1;
+      const bool cut = RESET && (flags >> s & 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
-        const float w = __builtin_sqrtf(g.m2) * g.si * xr[s].get(v);
-        a[s][v] = live ? g.a : 1.0f;
-        u[s][v] = live ? w : 0.0f;
+        a[s][v] = g.a;
+        u[s][v] = rec_sqrt(g.m2) * (g.si * xr[s].get(v));
         H[v] = rec_apply(a[s][v], u[s][v], cut, H[v]);
         A[v] *= a[s][v];
       }
@@ -166,17 +174,17 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const 
 #pragma unroll
       for (int v = 0; v < V; ++v) p.ckpt[(b * marks + t0 / kRecTile) * p.dim + c + v] = h[v];
     if (p.out || p.last) {
-      T* out = static_cast<T*>(p.out) + (b * p.L + t0) * p.dim + c;
+      T* out = static_cast<T*>(p.out) + (b * p.L + t0) * p.dim;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        const bool cut = flags >> s & 1;
+        const bool cut = RESET && (flags >> s & 1);
         float y[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           h[v] = rec_apply(a[s][v], u[s][v], cut, h[v]);
           y[v] = Z ? h[v] * silu(zr[Z ? s : 0].get(v)) : h[v];
         }
-        if (p.out && on && s < n) rec_store<T, V>(out + s * p.dim, y);
+        if (p.out && on && s < n) rec_store<T, V>(out + s * p.dim + c, y);
       }
       if (p.last && on && left > 0 && left <= S)
 #pragma unroll
@@ -192,12 +200,12 @@ __global__ __launch_bounds__(256) void rec_clear_kernel(uint64_t* p, int64_t n) 
   for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += step) p[k] = 0;
 }
 
-template <typename T, int V, bool Z>
+template <typename T, int V, bool Z, bool RESET>
 hipError_t go(const RecParams& p, hipStream_t s) {
   const int64_t across = p.batch * rec_strips(p.dim, V == 2);
   if (!p.ticket) {
     const int waves = (int)((p.L + S - 1) / S);
-    hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, false>), dim3((unsigned)across), dim3(64 * waves),
+    hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, false>), dim3((unsigned)across), dim3(64 * waves),
                        0, s, p, (uint32_t)across);
     return hipGetLastError();
   }
@@ -208,21 +216,22 @@ hipError_t go(const RecParams& p, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t grid = total < (1 << 20) ? total : (1 << 20);
-  hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, true>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)grid),
                      dim3((unsigned)(kRecFwdTile / S * 64)), 0, s, p, (uint32_t)total);
   return hipGetLastError();
 }
 
 template <typename T, int V>
-hipError_t by_gate(const RecParams& p, hipStream_t s) {
-  return p.z.p ? go<T, V, true>(p, s) : go<T, V, false>(p, s);
+hipError_t by_form(const RecParams& p, hipStream_t s) {
+  if (p.reset) return p.z.p ? go<T, V, true, true>(p, s) : go<T, V, false, true>(p, s);
+  return p.z.p ? go<T, V, true, false>(p, s) : go<T, V, false, false>(p, s);
 }
 
 }  // namespace
 
 hipError_t dispatch_rec_fwd(const RecParams& p, int dtype, hipStream_t s) {
-  if (dtype == 0) return by_gate<float, 1>(p, s);
-  return p.pairs ? by_gate<bf16_t, 2>(p, s) : by_gate<bf16_t, 1>(p, s);
+  if (dtype == 0) return by_form<float, 1>(p, s);
+  return p.pairs ? by_form<bf16_t, 2>(p, s) : by_form<bf16_t, 1>(p, s);
 }
 
 }  // namespace mscan

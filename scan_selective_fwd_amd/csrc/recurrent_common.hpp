@@ -24,6 +24,9 @@ struct RecGate {
   float m2;       // 1 - a^2
 };
 
+// Within one unit in the last place, as the exponentials here are.
+__device__ __forceinline__ float rec_sqrt(float x) { return __builtin_amdgcn_sqrtf(x); }
+
 // A2 = A log2(e).  1 - a^2 is formed without cancellation: from the polynomial where
 // a^2 is above e^(-1/2), from a itself below, where it keeps at least 0.39.
 __device__ __forceinline__ RecGate rec_gate(float r, float i, float A2) {
@@ -51,6 +54,10 @@ struct RecRaw {
     if constexpr (V == 2) w = *reinterpret_cast<const uint32_t*>(q);
     else if constexpr (sizeof(T) == 2) w = *q;
     else w = __float_as_uint(*q);
+  }
+  __device__ __forceinline__ void fill(float v) {   // a value that bfloat16 holds
+    w = __float_as_uint(v);
+    if constexpr (sizeof(T) == 2) w = w >> 16 | w;
   }
   __device__ __forceinline__ float get(int v) const {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w);
