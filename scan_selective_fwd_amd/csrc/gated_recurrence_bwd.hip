@@ -1,96 +1,299 @@
-// Gated linear recurrence, backward: a thread walks one channel of one
-// batch row, neighbours on neighbouring channels.
+// Gated linear recurrence, backward.
 #include "recurrent_common.hpp"
 
 namespace mscan {
 
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float at(const Rows& q, int64_t b, int64_t t, int64_t d) {
-  return Elem<T>::load1(static_cast<const T*>(q.p) + b * q.batch + t * q.token + d);
-}
+constexpr int S = (int)kRecBwdRun;
+constexpr int kMaxWaves = 16;
+constexpr int kMarkWaves = (int)kRecTile / S;   // waves between checkpoints
 
-template <typename T>
-__global__ __launch_bounds__(256) void rec_bwd_kernel(const RecParams p) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= p.batch * p.dim) return;
-  const int64_t b = n / p.dim, d = n - b * p.dim;
-  const int64_t tiles = (p.L + kRecTile - 1) / kRecTile;
-  const float A = p.A[d], A2 = A * kLog2e;
-  float* st = p.states + b * kRecTile * p.dim + d;
-  float after = p.dlast ? p.dlast[n] : 0.0f, sum = 0.0f;
-  for (int64_t k = tiles - 1; k >= 0; --k) {
-    const int64_t t0 = k * kRecTile, t1 = t0 + kRecTile < p.L ? t0 + kRecTile : p.L;
-    float h = p.kept[(b * tiles + k) * p.dim + d];
-    for (int64_t t = t0; t < t1; ++t) {
-      st[(t - t0) * p.dim] = h;
-      const RecGate g = rec_gate(at<T>(p.r, b, t, d), at<T>(p.i, b, t, d), A2);
-      const float v = __builtin_sqrtf(g.m2) * g.si * at<T>(p.x, b, t, d);
-      h = p.reset && p.reset[b * p.L + t] ? v : __builtin_fmaf(g.a, h, v);
+template <typename T, int V, bool Z, bool RESET, bool CHAIN>
+__global__ __launch_bounds__(1024) void rec_bwd_kernel(const RecParams p, const uint32_t total) {
+  constexpr int C = 64 * V;                       // channels of a strip
+  constexpr int G = (int)kRecGroup;
+  __shared__ float sA[kMaxWaves][C], sH[kMaxWaves][C], sB[kMaxWaves][C];
+  __shared__ int sCut[kMaxWaves];
+  __shared__ uint64_t sMap[CHAIN ? G : 1][CHAIN ? C : 1];
+  __shared__ float sHead[CHAIN ? C : 1];
+  __shared__ uint32_t sTicket;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const uint32_t strips = (uint32_t)((p.dim + C - 1) / C);
+  const uint32_t across = strips * (uint32_t)p.batch;
+  const uint32_t tiles = total / across;
+  const int64_t marks = (p.L + kRecTile - 1) / kRecTile;
+
+  for (uint32_t job = blockIdx.x;;) {
+    if constexpr (CHAIN) job = rec_ticket(p.ticket, &sTicket);
+    if (job >= total) return;
+    const uint32_t q = job / across, at = job - q * across;    // the last tile first
+    const uint32_t tile = tiles - 1 - q;
+    const int64_t b = at / strips;
+    const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
+    const bool on = c < p.dim;
+    const uint32_t cl = on ? c : 0;
+    const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
+    const int64_t left = p.L - t0;
+    const int n = left >= S ? S : left > 0 ? (int)left : 0;    // its steps
+
+    RecRaw<T, V> xr[S], rr[S], ir[S], yr[S], zr[Z ? S : 1];
+    auto row = [&](const Rows& q, int64_t t) {
+      return static_cast<const T*>(q.p) + b * q.batch + t * q.token;
+    };
+    const T* dout = static_cast<const T*>(p.dout) + b * p.L * p.dim;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int64_t t = t0 + s < p.L ? t0 + s : p.L - 1;
+      rr[s].load(row(p.r, t) + cl);
+      ir[s].load(row(p.i, t) + cl);
+      xr[s].load(row(p.x, t) + cl);
+      yr[s].load(dout + t * p.dim + cl);
+      if constexpr (Z) zr[s].load(row(p.z, t) + cl);
     }
-    for (int64_t t = t1 - 1; t >= t0; --t) {
-      const int64_t o = (b * p.L + t) * p.dim + d;
-      const float x = at<T>(p.x, b, t, d), before = st[(t - t0) * p.dim];
-      const RecGate g = rec_gate(at<T>(p.r, b, t, d), at<T>(p.i, b, t, d), A2);
-      const bool cut = p.reset && p.reset[b * p.L + t];
-      const float m = __builtin_sqrtf(g.m2), ix = g.si * x;
-      float dy = Elem<T>::load1(static_cast<const T*>(p.dout) + o);
-      if (p.z.p) {
-        const float z = at<T>(p.z, b, t, d), sz = sigmoid(z);
-        const float hh = cut ? m * ix : __builtin_fmaf(g.a, before, m * ix);
-        Elem<T>::store1(static_cast<T*>(p.dz) + o,
-                        dy * hh * (sz * __builtin_fmaf(z, 1.0f - sz, 1.0f)));
-        dy = dy * (z * sz);
+    // the state at the checkpoint before the run (a run past the end has none)
+    float h[V];
+    const int64_t mark = t0 / kRecTile < marks ? t0 / kRecTile : marks - 1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = p.kept[(b * marks + mark) * p.dim + cl + v];
+    if (n < S) {                                               // steps past the end
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (s >= n) {
+          rr[s].fill(-INFINITY);
+          ir[s].fill(0.0f);
+          xr[s].fill(0.0f);
+          yr[s].fill(0.0f);
+          if constexpr (Z) zr[s].fill(0.0f);
+        }
+    }
+    uint32_t flags = 0;
+    if constexpr (RESET) {
+      const bool f = lane < n && p.reset[b * p.L + t0 + lane];
+      flags = (uint32_t)__ballot(f);
+    }
+    float A2[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A2[v] = p.A[cl + v] * kLog2e;
+
+    // the run's map of the states
+    float a[S][V], u[S][V], A[V], H[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      A[v] = 1.0f;
+      H[v] = 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const bool cut = RESET && (flags >> s & 1);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
+        a[s][v] = g.a;
+        u[s][v] = rec_sqrt(g.m2) * (g.si * xr[s].get(v));
+        H[v] = rec_apply(g.a, u[s][v], cut, H[v]);
+        A[v] *= g.a;
       }
-      const float gh = dy + after;
-      after = cut ? 0.0f : g.a * gh;
-      const float y = g.lg * kLn2;
-      const float ym = g.m2 < 1e-37f ? 0.0f : y / m;
-      const float kept = cut ? 0.0f : g.a * before * y;
-      const float s = gh * __builtin_fmaf(-ix * ym, g.a * g.a, kept);
-      const float gm = gh * m * g.si;
-      Elem<T>::store1(static_cast<T*>(p.dx) + o, gm);
-      Elem<T>::store1(static_cast<T*>(p.di) + o, gm * x * (1.0f - g.si));
-      Elem<T>::store1(static_cast<T*>(p.dr) + o, s * (1.0f - g.sr));
-      sum += s;
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      sA[wave][lane * V + v] = A[v];
+      sH[wave][lane * V + v] = H[v];
+    }
+    if (lane == 0) sCut[wave] = flags != 0;
+    __syncthreads();
+    for (int w = wave / kMarkWaves * kMarkWaves; w < wave; ++w) {
+      const bool cw = sCut[w] != 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        h[v] = rec_apply(sA[w][lane * V + v], sH[w][lane * V + v], cw, h[v]);
+    }
+
+    // the states before each step (in the inputs' place), the gate on the output, and
+    // the run's map of the gradient that comes to the state from later steps
+    float dh[S][V], B[V];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const bool cut = RESET && (flags >> s & 1);
+      float dz[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float before = h[v];
+        h[v] = rec_apply(a[s][v], u[s][v], cut, before);
+        u[s][v] = before;
+        dh[s][v] = yr[s].get(v);
+        if constexpr (Z) {
+          const float z = zr[s].get(v), sz = sigmoid(z);
+          dz[v] = dh[s][v] * h[v] * (sz * __builtin_fmaf(z, 1.0f - sz, 1.0f));
+          dh[s][v] *= z * sz;
+        }
+      }
+      if constexpr (Z)
+        if (on && s < n)
+          rec_store<T, V>(static_cast<T*>(p.dz) + (b * p.L + t0 + s) * p.dim + c, dz);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) B[v] = 0.0f;
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+      const bool cut = RESET && (flags >> s & 1);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float y = a[s][v] * (dh[s][v] + B[v]);
+        B[v] = cut ? 0.0f : y;
+      }
+    }
+    // the first run of the walk starts from dlast
+    const bool first = q == 0 && wave == waves - 1 && p.dlast;
+    float after[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      after[v] = first ? p.dlast[b * p.dim + cl + v] : 0.0f;
+      sB[wave][lane * V + v] = first ? rec_apply(A[v], B[v], flags != 0, after[v]) : B[v];
+    }
+    __syncthreads();
+    float Ab[V], Bb[V], At[V], Bt[V];
+    bool cutb = false, cutt = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      Ab[v] = At[v] = 1.0f;
+      Bb[v] = Bt[v] = 0.0f;
+    }
+    for (int w = waves - 1; w >= 0; --w) {
+      if (w == wave) {
+        cutb = cutt;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          Ab[v] = At[v];
+          Bb[v] = Bt[v];
+        }
+      }
+      const bool cw = sCut[w] != 0 || (q == 0 && w == waves - 1 && p.dlast);
+      cutt = cutt || cw;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float Aw = sA[w][lane * V + v];
+        Bt[v] = rec_apply(Aw, sB[w][lane * V + v], cw, Bt[v]);
+        At[v] *= Aw;
+      }
+    }
+    if constexpr (CHAIN) {
+      const uint32_t groups = (tiles + G - 1) / G;
+      rec_chain<V, G>(p.maps + ((uint64_t)b * tiles + q) * p.dim + cl,
+                      p.heads + ((uint64_t)b * groups + q / G) * p.dim + cl, p.dim, q, At, Bt, cutt,
+                      on, wave, waves, lane, sMap, sHead, after);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) after[v] = rec_apply(Ab[v], Bb[v], cutb, after[v]);
+
+    // the gradients; the gates are formed again, which costs less than the registers
+    // that would keep them
+    float sum[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+      const bool cut = RESET && (flags >> s & 1);
+      rr[s].w = (uint32_t)opaque_int((int)rr[s].w);
+      ir[s].w = (uint32_t)opaque_int((int)ir[s].w);
+      float dx[V], dr[V], di[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float x = xr[s].get(v);
+        const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
+        // 1 / m, finite where m is 0; y / m and m from it
+        const float rs = __builtin_amdgcn_rsqf(__builtin_fmaxf(g.m2, 1e-37f));
+        const float y = g.lg * kLn2, ix = g.si * x;
+        const float gh = dh[s][v] + after[v];
+        const float next = g.a * gh;
+        after[v] = cut ? 0.0f : next;
+        const float ah = g.a * u[s][v];
+        const float kept = cut ? 0.0f : ah * y;
+        const float e = gh * __builtin_fmaf(-ix * (y * rs), g.a * g.a, kept);
+        const float gm = gh * (g.m2 * rs) * g.si;
+        dx[v] = gm;
+        di[v] = gm * x * (1.0f - g.si);
+        dr[v] = e * (1.0f - g.sr);
+        sum[v] += e;
+      }
+      if (on && s < n) {
+        const int64_t o = (b * p.L + t0 + s) * p.dim;
+        rec_store<T, V>(static_cast<T*>(p.dx) + o + c, dx);
+        rec_store<T, V>(static_cast<T*>(p.dr) + o + c, dr);
+        rec_store<T, V>(static_cast<T*>(p.di) + o + c, di);
+      }
+    }
+    if (t0 == 0 && p.dh0 && on)
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.dh0[b * p.dim + c + v] = after[v];
+    // the tile's share of dA, its runs added in order
+#pragma unroll
+    for (int v = 0; v < V; ++v) sH[wave][lane * V + v] = sum[v];
+    __syncthreads();
+    if (wave == 0 && on)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float s = sum[v];
+        for (int w = 1; w < waves; ++w) s += sH[w][lane * V + v];
+        p.part[((int64_t)b * tiles + tile) * p.dim + c + v] = s;
+      }
+    if constexpr (!CHAIN) return;
+    __syncthreads();
   }
-  p.part[n] = sum / A;
-  if (p.dh0) p.dh0[n] = after;
 }
 
-__global__ __launch_bounds__(256) void rec_sum_kernel(const RecParams p) {
-  const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (d >= p.dim) return;
-  double s = 0.0;
-  for (int64_t b = 0; b < p.batch; ++b) s += p.part[b * p.dim + d];
-  p.dA[d] = (float)s;
+// dA: the tiles' shares added in a fixed order, in 64 bits; 8 slices of them by 32
+// channels.
+__global__ __launch_bounds__(256) void rec_sum_kernel(const RecParams p, const int64_t parts) {
+  __shared__ double red[8][32];
+  const int cl = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + cl;
+  double sum = 0.0;
+  if (c < p.dim)
+    for (int64_t k = sl; k < parts; k += 8) sum += p.part[k * p.dim + c];
+  red[sl][cl] = sum;
+  __syncthreads();
+  if (sl == 0 && c < p.dim) {
+    for (int k = 1; k < 8; ++k) sum += red[k][cl];
+    p.dA[c] = (float)(sum / p.A[c]);     // the shares are A's times too large
+  }
 }
 
-unsigned blocks(int64_t n) { return (unsigned)((n + 255) / 256); }
-
-template <typename T>
-hipError_t bwd_t(const RecParams& p, hipStream_t s) {
-  if (p.ckpt) {   // the states at the tiles' starts
-    RecParams f = p;
-    f.out = nullptr;
-    f.last = nullptr;
-    f.z.p = nullptr;
-    const hipError_t e = dispatch_rec_fwd(f, sizeof(T) == 4 ? 0 : 1, s);
+template <typename T, int V, bool Z, bool RESET>
+hipError_t go(const RecParams& p, hipStream_t s) {
+  const int64_t across = p.batch * rec_strips(p.dim, V == 2);
+  const int64_t tiles = (p.L + kRecBwdTile - 1) / kRecBwdTile, total = across * tiles;
+  hipError_t e;
+  if (tiles == 1) {
+    hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, false>), dim3((unsigned)across),
+                       dim3((unsigned)((p.L + S - 1) / S * 64)), 0, s, p, (uint32_t)across);
+  } else {
+    e = rec_clear(p, s);
     if (e != hipSuccess) return e;
+    const int64_t grid = total < (1 << 20) ? total : (1 << 20);
+    hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)grid), dim3(1024), 0,
+                       s, p, (uint32_t)total);
   }
-  hipLaunchKernelGGL((rec_bwd_kernel<T>), dim3(blocks(p.batch * p.dim)), dim3(256), 0, s, p);
-  const hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rec_sum_kernel, dim3(blocks(p.dim)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(rec_sum_kernel, dim3((unsigned)((p.dim + 31) / 32)), dim3(256), 0, s, p,
+                     p.batch * tiles);
   return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t by_form(const RecParams& p, hipStream_t s) {
+  if (p.reset) return p.z.p ? go<T, V, true, true>(p, s) : go<T, V, false, true>(p, s);
+  return p.z.p ? go<T, V, true, false>(p, s) : go<T, V, false, false>(p, s);
 }
 
 }  // namespace
 
 hipError_t dispatch_rec_bwd(const RecParams& p, int dtype, hipStream_t s) {
-  return dtype == 0 ? bwd_t<float>(p, s) : bwd_t<bf16_t>(p, s);
+  if (dtype == 0) return by_form<float, 1>(p, s);
+  return p.pairs ? by_form<bf16_t, 2>(p, s) : by_form<bf16_t, 1>(p, s);
 }
 
 }  // namespace mscan

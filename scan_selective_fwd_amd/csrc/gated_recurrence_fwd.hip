@@ -15,6 +15,7 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const 
   __shared__ float sA[kMaxWaves][C], sH[kMaxWaves][C];
   __shared__ int sCut[kMaxWaves];
   __shared__ uint64_t sMap[CHAIN ? G : 1][CHAIN ? C : 1];
+  __shared__ float sHead[CHAIN ? C : 1];
   __shared__ uint32_t sTicket;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -24,12 +25,7 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const 
   const int64_t marks = (p.L + kRecTile - 1) / kRecTile;
 
   for (uint32_t job = blockIdx.x;;) {
-    if constexpr (CHAIN) {
-      if (threadIdx.x == 0)
-        sTicket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      __syncthreads();
-      job = __builtin_amdgcn_readfirstlane(sTicket);
-    }
+    if constexpr (CHAIN) job = rec_ticket(p.ticket, &sTicket);
     if (job >= total) return;
     const uint32_t tile = job / across, at = job - tile * across;
     const int64_t b = at / strips;
@@ -135,37 +131,9 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const 
     if constexpr (CHAIN) {
       const uint32_t tiles = (uint32_t)((p.L + kRecFwdTile - 1) / kRecFwdTile);
       const uint32_t groups = (tiles + G - 1) / G;
-      const int j = tile % G;
-      const uint32_t group = tile / G;
-      uint64_t* maps = p.maps + ((uint64_t)b * tiles + tile) * p.dim + cl;
-      uint64_t* heads = p.heads + ((uint64_t)b * groups + group) * p.dim + cl;
-      if (wave == 0 && on && j != G - 1) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) rec_publish(maps + v, rec_pack(At[v], Ht[v], cutt));
-      }
-      // the maps of the group's earlier tiles, and the state after the group before
-      for (int k = wave; k < j; k += waves)
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          sMap[k][lane * V + v] = rec_wait(maps - (int64_t)(j - k) * p.dim + v);
-      if (group && wave == (int)(j & (waves - 1)))
-#pragma unroll
-        for (int v = 0; v < V; ++v) sMap[j][lane * V + v] = rec_wait(heads - p.dim + v);
-      __syncthreads();
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (group) h[v] = __uint_as_float((uint32_t)sMap[j][lane * V + v]);
-      for (int k = 0; k < j; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const uint64_t m = sMap[k][lane * V + v];
-          const uint32_t hi = (uint32_t)(m >> 32) & ~kThere;
-          h[v] = rec_apply(__uint_as_float(hi), __uint_as_float((uint32_t)m), hi == kCutBits, h[v]);
-        }
-      if (j == G - 1 && wave == 0 && on)
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          rec_publish(heads + v, rec_pack(0.0f, rec_apply(At[v], Ht[v], cutt, h[v]), false));
+      rec_chain<V, G>(p.maps + ((uint64_t)b * tiles + tile) * p.dim + cl,
+                      p.heads + ((uint64_t)b * groups + tile / G) * p.dim + cl, p.dim, tile, At, Ht,
+                      cutt, on, wave, waves, lane, sMap, sHead, h);
     }
     // and the wave's run
 #pragma unroll
@@ -195,11 +163,6 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const 
   }
 }
 
-__global__ __launch_bounds__(256) void rec_clear_kernel(uint64_t* p, int64_t n) {
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += step) p[k] = 0;
-}
-
 template <typename T, int V, bool Z, bool RESET>
 hipError_t go(const RecParams& p, hipStream_t s) {
   const int64_t across = p.batch * rec_strips(p.dim, V == 2);
@@ -210,10 +173,7 @@ hipError_t go(const RecParams& p, hipStream_t s) {
     return hipGetLastError();
   }
   const int64_t total = across * ((p.L + kRecFwdTile - 1) / kRecFwdTile);
-  const int64_t clear = (p.words + 255) / 256;
-  hipLaunchKernelGGL(rec_clear_kernel, dim3((unsigned)(clear < 4096 ? clear : 4096)), dim3(256), 0,
-                     s, reinterpret_cast<uint64_t*>(p.ticket), p.words);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = rec_clear(p, s);
   if (e != hipSuccess) return e;
   const int64_t grid = total < (1 << 20) ? total : (1 << 20);
   hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)grid),
@@ -227,7 +187,20 @@ hipError_t by_form(const RecParams& p, hipStream_t s) {
   return p.z.p ? go<T, V, true, false>(p, s) : go<T, V, false, false>(p, s);
 }
 
+__global__ __launch_bounds__(256) void rec_clear_kernel(uint64_t* p, int64_t n) {
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += step) p[k] = 0;
+}
+
 }  // namespace
+
+// Clears what the tiles publish.  A kernel: it may be captured into a graph.
+hipError_t rec_clear(const RecParams& p, hipStream_t s) {
+  const int64_t n = (p.words + 255) / 256;
+  hipLaunchKernelGGL(rec_clear_kernel, dim3((unsigned)(n < 4096 ? n : 4096)), dim3(256), 0, s,
+                     reinterpret_cast<uint64_t*>(p.ticket), p.words);
+  return hipGetLastError();
+}
 
 hipError_t dispatch_rec_fwd(const RecParams& p, int dtype, hipStream_t s) {
   if (dtype == 0) return by_form<float, 1>(p, s);

@@ -32,8 +32,7 @@ struct RecParams {
   void* dz;              // nullable
   float* dA;
   float* dh0;            // nullable
-  float* part;           // workspace, (batch, dim): the rows' shares of dA
-  float* states;         // workspace, (batch, kRecTile, dim)
+  float* part;           // workspace, (batch, tiles, dim): the tiles' shares of dA
 };
 
 constexpr int64_t kRecTile = 64;   // steps between checkpoints
@@ -42,13 +41,19 @@ constexpr int64_t kRecTile = 64;   // steps between checkpoints
 // sequences take tiles of kRecFwdTile steps, joined kRecGroup at a time.
 constexpr int64_t kRecRun = 16;
 constexpr int64_t kRecOneTile = 16 * kRecRun;
-constexpr int64_t kRecFwdTile = 8 * kRecRun;
+constexpr int64_t kRecFwdTile = 16 * kRecRun;
 constexpr int64_t kRecGroup = 16;
+
+// The backward: the same with runs of kRecBwdRun steps.
+constexpr int64_t kRecBwdRun = 8;
+constexpr int64_t kRecBwdTile = 16 * kRecBwdRun;
+static_assert(kRecBwdTile % kRecTile == 0 && kRecFwdTile % kRecTile == 0, "tiles between checkpoints");
 
 constexpr int64_t rec_strips(int64_t dim, bool pairs) {
   return pairs ? (dim + 127) / 128 : (dim + 63) / 64;
 }
 
+hipError_t rec_clear(const RecParams& p, hipStream_t s);
 hipError_t dispatch_rec_fwd(const RecParams& p, int dtype, hipStream_t s);
 hipError_t dispatch_rec_bwd(const RecParams& p, int dtype, hipStream_t s);
 

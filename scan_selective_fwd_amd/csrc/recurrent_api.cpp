@@ -44,6 +44,7 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 int64_t fwd_tiles(int64_t L) { return (L + mscan::kRecFwdTile - 1) / mscan::kRecFwdTile; }
+int64_t bwd_tiles(int64_t L) { return (L + mscan::kRecBwdTile - 1) / mscan::kRecBwdTile; }
 
 mamba_status check_shape(const mamba_recurrence_shape* s) {
   if (!s) return MAMBA_ERR_NULL_PTR;
@@ -55,8 +56,8 @@ mamba_status check_shape(const mamba_recurrence_shape* s) {
     return MAMBA_ERR_SHAPE;
   if (s->dim > (int64_t)1 << 28 || s->seqlen > kLim / 64 / s->batch ||
       s->dim > kLim / 64 / (s->batch * s->seqlen) ||
-      s->batch > (s->seqlen > mscan::kRecOneTile ? kGridLim : mscan::max_blocks(1024)) /
-                     mscan::rec_strips(s->dim, false) / fwd_tiles(s->seqlen))
+      s->batch > (s->seqlen > mscan::kRecBwdTile ? kGridLim : mscan::max_blocks(1024)) /
+                     mscan::rec_strips(s->dim, false) / bwd_tiles(s->seqlen))
     return MAMBA_ERR_UNSUPPORTED;
   if (!span_ok(s->batch, s->x_batch_stride, s->seqlen, s->x_token_stride) ||
       !span_ok(s->batch, s->r_batch_stride, s->seqlen, s->r_token_stride) ||
@@ -119,23 +120,32 @@ bool pairs(const mamba_recurrence_shape* s, const void* x, const void* r, const 
          (!z || ok(z, s->z_batch_stride, s->z_token_stride));
 }
 
-// Workspace of the forward, none where one tile holds the sequence.
-struct FwdLayout {
+// Workspace of a pass in `n` tiles, none where one tile holds the sequence.
+struct ChainLayout {
   size_t maps, heads, total;
 };
 
-FwdLayout fwd_layout(const mamba_recurrence_shape* s) {
-  if (s->seqlen <= mscan::kRecOneTile) return {0, 0, 0};
-  const int64_t n = fwd_tiles(s->seqlen), g = (n + mscan::kRecGroup - 1) / mscan::kRecGroup;
+ChainLayout chain_layout(const mamba_recurrence_shape* s, int64_t n) {
+  if (n == 1) return {0, 0, 0};
+  const int64_t g = (n + mscan::kRecGroup - 1) / mscan::kRecGroup;
   const size_t row = (size_t)(s->batch * s->dim) * 8;
-  FwdLayout l;
+  ChainLayout l;
   l.maps = 256;
   l.heads = l.maps + row * (size_t)n;
   l.total = l.heads + row * (size_t)g;
   return l;
 }
 
-void carve(mscan::RecParams* p, const FwdLayout& l, void* workspace) {
+ChainLayout fwd_layout(const mamba_recurrence_shape* s) {
+  return chain_layout(s, fwd_tiles(s->seqlen));
+}
+
+ChainLayout bwd_chain(const mamba_recurrence_shape* s) {
+  return chain_layout(s, bwd_tiles(s->seqlen));
+}
+
+void carve(mscan::RecParams* p, const ChainLayout& l, void* workspace) {
+  p->ticket = nullptr;
   if (!l.total) return;
   char* ws = static_cast<char*>(workspace);
   p->ticket = reinterpret_cast<uint32_t*>(ws);
@@ -146,15 +156,15 @@ void carve(mscan::RecParams* p, const FwdLayout& l, void* workspace) {
 
 // Workspace of the backward.
 struct BwdLayout {
-  size_t part, states, ckpt, fwd, total;
+  size_t chain, part, ckpt, fwd, total;
 };
 
 BwdLayout bwd_layout(const mamba_recurrence_shape* s, bool given) {
   const size_t row = (size_t)(s->batch * s->dim) * 4;
   BwdLayout l;
-  l.part = 0;
-  l.states = up256(row);
-  l.ckpt = l.states + up256(row * (size_t)mscan::kRecTile);
+  l.chain = 0;
+  l.part = up256(bwd_chain(s).total);
+  l.ckpt = l.part + up256(row * (size_t)bwd_tiles(s->seqlen));
   l.fwd = l.ckpt + (given ? 0 : up256(row * (size_t)tiles(s)));
   l.total = l.fwd + (given ? 0 : up256(fwd_layout(s).total));
   return l;
@@ -288,14 +298,19 @@ mamba_status mamba_gated_recurrence_bwd(const mamba_recurrence_shape* shape, con
   p.dout = dout; p.dlast = dlast_state;
   p.dx = dx; p.dr = dr; p.di = di; p.dz = dz; p.dA = dA; p.dh0 = dh0;
   p.part = reinterpret_cast<float*>(ws + l.part);
-  p.states = reinterpret_cast<float*>(ws + l.states);
+  p.kept = checkpoints;
+  if (!checkpoints) {   // the forward's pass over the states alone
+    mscan::RecParams f = common(shape, x, r, i, A, nullptr, h0, reset);
+    f.pairs = pairs(shape, x, r, i, nullptr);
+    f.ckpt = reinterpret_cast<float*>(ws + l.ckpt);
+    carve(&f, fwd_layout(shape), ws + l.fwd);
+    st = hip_status(mscan::dispatch_rec_fwd(f, shape->dtype == MAMBA_F32 ? 0 : 1, as_stream(stream)));
+    if (st != MAMBA_OK) return st;
+    p.kept = f.ckpt;
+  }
+  carve(&p, bwd_chain(shape), ws + l.chain);
   p.pairs = pairs(shape, x, r, i, z) && aligned(dout, 4) && aligned(dx, 4) && aligned(dr, 4) &&
             aligned(di, 4) && aligned(dz, 4);
-  if (!checkpoints) {
-    p.ckpt = reinterpret_cast<float*>(ws + l.ckpt);
-    carve(&p, fwd_layout(shape), ws + l.fwd);
-  }
-  p.kept = checkpoints ? checkpoints : p.ckpt;
   return hip_status(mscan::dispatch_rec_bwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,
                                             as_stream(stream)));
 }

@@ -4,6 +4,10 @@
 #include "heads_common.hpp"
 #include "recurrent.hpp"
 
+// Products and sums are fused only where written so: a row gives the same bits in every
+// variant of a kernel, whatever its alignment.
+#pragma clang fp contract(off)
+
 namespace mscan {
 
 // 1 - exp2(z) for z in [-kSmallZ, 0]: -z times a polynomial of degree 4 in z, the
@@ -100,6 +104,76 @@ __device__ __forceinline__ uint64_t rec_wait(uint64_t* p) {
     v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   return v;
+}
+
+// The value that enters tile q (counted in the order of the tickets) of a row: the
+// maps of its group's earlier tiles joined, then the value behind the group before.
+// Publishes the tile's own map (At, Ht, cutt), or for the last of a group the value
+// behind it.  h: in, what enters tile 0; out, what enters this one.  The order of
+// the products does not depend on who was first, so equal inputs give equal bits.
+// maps, heads: this tile's and its group's words; `on`: whether the lane's channels exist.
+template <int V, int G>
+__device__ __forceinline__ void rec_chain(uint64_t* maps, uint64_t* heads, int64_t dim, uint32_t q,
+                                          const float (&At)[V], const float (&Ht)[V], bool cutt,
+                                          bool on, int wave, int waves, int lane,
+                                          uint64_t (*sMap)[64 * V], float* sHead, float (&h)[V]) {
+  const int j = q % G;
+  const bool later = q >= G;
+  if (wave == 0 && on && j != G - 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) rec_publish(maps + v, rec_pack(At[v], Ht[v], cutt));
+  }
+  for (int k = wave; k < j; k += waves)
+#pragma unroll
+    for (int v = 0; v < V; ++v) sMap[k][lane * V + v] = rec_wait(maps - (int64_t)(j - k) * dim + v);
+  __syncthreads();
+  float A[V], H[V];
+  bool cut[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = 1.0f;
+    H[v] = 0.0f;
+    cut[v] = false;
+  }
+  for (int k = 0; k < j; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint64_t m = sMap[k][lane * V + v];
+      const uint32_t hi = (uint32_t)(m >> 32) & ~kThere;
+      const bool c = hi == kCutBits;
+      H[v] = rec_apply(__uint_as_float(hi), __uint_as_float((uint32_t)m), c, H[v]);
+      cut[v] = cut[v] || c;
+      A[v] *= c ? 1.0f : __uint_as_float(hi);
+    }
+  if (later) {
+    // joined before the wait: the next group waits for two products after this one
+    if (wave == 0)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        h[v] = __uint_as_float((uint32_t)rec_wait(heads - dim + v));
+        sHead[lane * V + v] = h[v] = rec_apply(A[v], H[v], cut[v], h[v]);
+      }
+  } else if (j) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = H[v];
+  }
+  if (j == G - 1 && wave == 0 && on)
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      rec_publish(heads + v, rec_pack(0.0f, rec_apply(At[v], Ht[v], cutt, h[v]), false));
+  if (later) {
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = sHead[lane * V + v];
+  }
+}
+
+// The next tile of a launch over tiles in order: every thread of the block.
+__device__ __forceinline__ uint32_t rec_ticket(uint32_t* counter, uint32_t* sTicket) {
+  if (threadIdx.x == 0)
+    *sTicket = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(*sTicket);
 }
 
 }  // namespace mscan
