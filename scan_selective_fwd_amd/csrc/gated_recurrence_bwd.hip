@@ -10,7 +10,7 @@ constexpr int kMaxWaves = 16;
 constexpr int kMarkWaves = (int)kRecTile / S;   // waves between checkpoints
 
 template <typename T, int V, bool Z, bool RESET, bool CHAIN>
-__global__ __launch_bounds__(1024) void rec_bwd_kernel(const RecParams p, const uint32_t total) {
+__global__ __launch_bounds__(1024) void rec_bwd_kernel(const RecParams p) {
   constexpr int C = 64 * V;                       // channels of a strip
   constexpr int G = (int)kRecGroup;
   __shared__ float sA[kMaxWaves][C], sH[kMaxWaves][C], sB[kMaxWaves][C];
@@ -23,225 +23,219 @@ __global__ __launch_bounds__(1024) void rec_bwd_kernel(const RecParams p, const 
   const int waves = blockDim.x >> 6;
   const uint32_t strips = (uint32_t)((p.dim + C - 1) / C);
   const uint32_t across = strips * (uint32_t)p.batch;
-  const uint32_t tiles = total / across;
+  const uint32_t tiles = gridDim.x / across;
   const int64_t marks = (p.L + kRecTile - 1) / kRecTile;
+  const uint32_t at = blockIdx.x % across;
+  const uint32_t q = CHAIN ? rec_ticket(p.ticket, at, &sTicket) : 0;   // the last tile first
+  const uint32_t tile = tiles - 1 - q;
+  const int64_t b = at / strips;
+  const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
+  const bool on = c < p.dim;
+  const uint32_t cl = on ? c : 0;
+  const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
+  const int64_t left = p.L - t0;
+  const int n = left >= S ? S : left > 0 ? (int)left : 0;    // its steps
 
-  for (uint32_t job = blockIdx.x;;) {
-    if constexpr (CHAIN) job = rec_ticket(p.ticket, &sTicket);
-    if (job >= total) return;
-    const uint32_t q = job / across, at = job - q * across;    // the last tile first
-    const uint32_t tile = tiles - 1 - q;
-    const int64_t b = at / strips;
-    const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
-    const bool on = c < p.dim;
-    const uint32_t cl = on ? c : 0;
-    const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
-    const int64_t left = p.L - t0;
-    const int n = left >= S ? S : left > 0 ? (int)left : 0;    // its steps
-
-    RecRaw<T, V> xr[S], rr[S], ir[S], yr[S], zr[Z ? S : 1];
-    auto row = [&](const Rows& q, int64_t t) {
-      return static_cast<const T*>(q.p) + b * q.batch + t * q.token;
-    };
-    const T* dout = static_cast<const T*>(p.dout) + b * p.L * p.dim;
+  RecRaw<T, V> xr[S], rr[S], ir[S], yr[S], zr[Z ? S : 1];
+  auto row = [&](const Rows& q, int64_t t) {
+    return static_cast<const T*>(q.p) + b * q.batch + t * q.token;
+  };
+  const T* dout = static_cast<const T*>(p.dout) + b * p.L * p.dim;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int64_t t = t0 + s < p.L ? t0 + s : p.L - 1;
-      rr[s].load(row(p.r, t) + cl);
-      ir[s].load(row(p.i, t) + cl);
-      xr[s].load(row(p.x, t) + cl);
-      yr[s].load(dout + t * p.dim + cl);
-      if constexpr (Z) zr[s].load(row(p.z, t) + cl);
-    }
-    // the state at the checkpoint before the run (a run past the end has none)
-    float h[V];
-    const int64_t mark = t0 / kRecTile < marks ? t0 / kRecTile : marks - 1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = p.kept[(b * marks + mark) * p.dim + cl + v];
-    if (n < S) {                                               // steps past the end
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-        if (s >= n) {
-          rr[s].fill(-INFINITY);
-          ir[s].fill(0.0f);
-          xr[s].fill(0.0f);
-          yr[s].fill(0.0f);
-          if constexpr (Z) zr[s].fill(0.0f);
-        }
-    }
-    uint32_t flags = 0;
-    if constexpr (RESET) {
-      const bool f = lane < n && p.reset[b * p.L + t0 + lane];
-      flags = (uint32_t)__ballot(f);
-    }
-    float A2[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) A2[v] = p.A[cl + v] * kLog2e;
-
-    // the run's map of the states
-    float a[S][V], u[S][V], A[V], H[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      A[v] = 1.0f;
-      H[v] = 0.0f;
-    }
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const bool cut = RESET && (flags >> s & 1);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
-        a[s][v] = g.a;
-        u[s][v] = rec_sqrt(g.m2) * (g.si * xr[s].get(v));
-        H[v] = rec_apply(g.a, u[s][v], cut, H[v]);
-        A[v] *= g.a;
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      sA[wave][lane * V + v] = A[v];
-      sH[wave][lane * V + v] = H[v];
-    }
-    if (lane == 0) sCut[wave] = flags != 0;
-    __syncthreads();
-    for (int w = wave / kMarkWaves * kMarkWaves; w < wave; ++w) {
-      const bool cw = sCut[w] != 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        h[v] = rec_apply(sA[w][lane * V + v], sH[w][lane * V + v], cw, h[v]);
-    }
-
-    // the states before each step (in the inputs' place), the gate on the output, and
-    // the run's map of the gradient that comes to the state from later steps
-    float dh[S][V], B[V];
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const bool cut = RESET && (flags >> s & 1);
-      float dz[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float before = h[v];
-        h[v] = rec_apply(a[s][v], u[s][v], cut, before);
-        u[s][v] = before;
-        dh[s][v] = yr[s].get(v);
-        if constexpr (Z) {
-          const float z = zr[s].get(v), sz = sigmoid(z);
-          dz[v] = dh[s][v] * h[v] * (sz * __builtin_fmaf(z, 1.0f - sz, 1.0f));
-          dh[s][v] *= z * sz;
-        }
-      }
-      if constexpr (Z)
-        if (on && s < n)
-          rec_store<T, V>(static_cast<T*>(p.dz) + (b * p.L + t0 + s) * p.dim + c, dz);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) B[v] = 0.0f;
-#pragma unroll
-    for (int s = S - 1; s >= 0; --s) {
-      const bool cut = RESET && (flags >> s & 1);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float y = a[s][v] * (dh[s][v] + B[v]);
-        B[v] = cut ? 0.0f : y;
-      }
-    }
-    // the first run of the walk starts from dlast
-    const bool first = q == 0 && wave == waves - 1 && p.dlast;
-    float after[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      after[v] = first ? p.dlast[b * p.dim + cl + v] : 0.0f;
-      sB[wave][lane * V + v] = first ? rec_apply(A[v], B[v], flags != 0, after[v]) : B[v];
-    }
-    __syncthreads();
-    float Ab[V], Bb[V], At[V], Bt[V];
-    bool cutb = false, cutt = false;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      Ab[v] = At[v] = 1.0f;
-      Bb[v] = Bt[v] = 0.0f;
-    }
-    for (int w = waves - 1; w >= 0; --w) {
-      if (w == wave) {
-        cutb = cutt;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          Ab[v] = At[v];
-          Bb[v] = Bt[v];
-        }
-      }
-      const bool cw = sCut[w] != 0 || (q == 0 && w == waves - 1 && p.dlast);
-      cutt = cutt || cw;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float Aw = sA[w][lane * V + v];
-        Bt[v] = rec_apply(Aw, sB[w][lane * V + v], cw, Bt[v]);
-        At[v] *= Aw;
-      }
-    }
-    if constexpr (CHAIN) {
-      const uint32_t groups = (tiles + G - 1) / G;
-      rec_chain<V, G>(p.maps + ((uint64_t)b * tiles + q) * p.dim + cl,
-                      p.heads + ((uint64_t)b * groups + q / G) * p.dim + cl, p.dim, q, At, Bt, cutt,
-                      on, wave, waves, lane, sMap, sHead, after);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) after[v] = rec_apply(Ab[v], Bb[v], cutb, after[v]);
-
-    // the gradients; the gates are formed again, which costs less than the registers
-    // that would keep them
-    float sum[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) sum[v] = 0.0f;
-#pragma unroll
-    for (int s = S - 1; s >= 0; --s) {
-      const bool cut = RESET && (flags >> s & 1);
-      rr[s].w = (uint32_t)opaque_int((int)rr[s].w);
-      ir[s].w = (uint32_t)opaque_int((int)ir[s].w);
-      float dx[V], dr[V], di[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float x = xr[s].get(v);
-        const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
-        // 1 / m, finite where m is 0; y / m and m from it
-        const float rs = __builtin_amdgcn_rsqf(__builtin_fmaxf(g.m2, 1e-37f));
-        const float y = g.lg * kLn2, ix = g.si * x;
-        const float gh = dh[s][v] + after[v];
-        const float next = g.a * gh;
-        after[v] = cut ? 0.0f : next;
-        const float ah = g.a * u[s][v];
-        const float kept = cut ? 0.0f : ah * y;
-        const float e = gh * __builtin_fmaf(-ix * (y * rs), g.a * g.a, kept);
-        const float gm = gh * (g.m2 * rs) * g.si;
-        dx[v] = gm;
-        di[v] = gm * x * (1.0f - g.si);
-        dr[v] = e * (1.0f - g.sr);
-        sum[v] += e;
-      }
-      if (on && s < n) {
-        const int64_t o = (b * p.L + t0 + s) * p.dim;
-        rec_store<T, V>(static_cast<T*>(p.dx) + o + c, dx);
-        rec_store<T, V>(static_cast<T*>(p.dr) + o + c, dr);
-        rec_store<T, V>(static_cast<T*>(p.di) + o + c, di);
-      }
-    }
-    if (t0 == 0 && p.dh0 && on)
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.dh0[b * p.dim + c + v] = after[v];
-    // the tile's share of dA, its runs added in order
-#pragma unroll
-    for (int v = 0; v < V; ++v) sH[wave][lane * V + v] = sum[v];
-    __syncthreads();
-    if (wave == 0 && on)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float s = sum[v];
-        for (int w = 1; w < waves; ++w) s += sH[w][lane * V + v];
-        p.part[((int64_t)b * tiles + tile) * p.dim + c + v] = s;
-      }
-    if constexpr (!CHAIN) return;
-    __syncthreads();
+  for (int s = 0; s < S; ++s) {
+    const int64_t t = t0 + s < p.L ? t0 + s : p.L - 1;
+    rr[s].load(row(p.r, t) + cl);
+    ir[s].load(row(p.i, t) + cl);
+    xr[s].load(row(p.x, t) + cl);
+    yr[s].load(dout + t * p.dim + cl);
+    if constexpr (Z) zr[s].load(row(p.z, t) + cl);
   }
+  // the state at the checkpoint before the run (a run past the end has none)
+  float h[V];
+  const int64_t mark = t0 / kRecTile < marks ? t0 / kRecTile : marks - 1;
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = p.kept[(b * marks + mark) * p.dim + cl + v];
+  if (n < S) {                                               // steps past the end
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (s >= n) {
+        rr[s].fill(-INFINITY);
+        ir[s].fill(0.0f);
+        xr[s].fill(0.0f);
+        yr[s].fill(0.0f);
+        if constexpr (Z) zr[s].fill(0.0f);
+      }
+  }
+  uint32_t flags = 0;
+  if constexpr (RESET) {
+    const bool f = lane < n && p.reset[b * p.L + t0 + lane];
+    flags = (uint32_t)__ballot(f);
+  }
+  float A2[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) A2[v] = p.A[cl + v] * kLog2e;
+
+  // the run's map of the states
+  float a[S][V], u[S][V], A[V], H[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = 1.0f;
+    H[v] = 0.0f;
+  }
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const bool cut = RESET && (flags >> s & 1);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
+      a[s][v] = g.a;
+      u[s][v] = rec_sqrt(g.m2) * (g.si * xr[s].get(v));
+      H[v] = rec_apply(g.a, u[s][v], cut, H[v]);
+      A[v] *= g.a;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    sA[wave][lane * V + v] = A[v];
+    sH[wave][lane * V + v] = H[v];
+  }
+  if (lane == 0) sCut[wave] = flags != 0;
+  __syncthreads();
+  for (int w = wave / kMarkWaves * kMarkWaves; w < wave; ++w) {
+    const bool cw = sCut[w] != 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      h[v] = rec_apply(sA[w][lane * V + v], sH[w][lane * V + v], cw, h[v]);
+  }
+
+  // the states before each step (in the inputs' place), the gate on the output, and
+  // the run's map of the gradient that comes to the state from later steps
+  float dh[S][V], B[V];
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const bool cut = RESET && (flags >> s & 1);
+    float dz[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float before = h[v];
+      h[v] = rec_apply(a[s][v], u[s][v], cut, before);
+      u[s][v] = before;
+      dh[s][v] = yr[s].get(v);
+      if constexpr (Z) {
+        const float z = zr[s].get(v), sz = sigmoid(z);
+        dz[v] = dh[s][v] * h[v] * (sz * __builtin_fmaf(z, 1.0f - sz, 1.0f));
+        dh[s][v] *= z * sz;
+      }
+    }
+    if constexpr (Z)
+      if (on && s < n)
+        rec_store<T, V>(static_cast<T*>(p.dz) + (b * p.L + t0 + s) * p.dim + c, dz);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) B[v] = 0.0f;
+#pragma unroll
+  for (int s = S - 1; s >= 0; --s) {
+    const bool cut = RESET && (flags >> s & 1);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float y = a[s][v] * (dh[s][v] + B[v]);
+      B[v] = cut ? 0.0f : y;
+    }
+  }
+  // the first run of the walk starts from dlast
+  const bool first = q == 0 && wave == waves - 1 && p.dlast;
+  float after[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    after[v] = first ? p.dlast[b * p.dim + cl + v] : 0.0f;
+    sB[wave][lane * V + v] = first ? rec_apply(A[v], B[v], flags != 0, after[v]) : B[v];
+  }
+  __syncthreads();
+  float Ab[V], Bb[V], At[V], Bt[V];
+  bool cutb = false, cutt = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    Ab[v] = At[v] = 1.0f;
+    Bb[v] = Bt[v] = 0.0f;
+  }
+  for (int w = waves - 1; w >= 0; --w) {
+    if (w == wave) {
+      cutb = cutt;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        Ab[v] = At[v];
+        Bb[v] = Bt[v];
+      }
+    }
+    const bool cw = sCut[w] != 0 || (q == 0 && w == waves - 1 && p.dlast);
+    cutt = cutt || cw;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float Aw = sA[w][lane * V + v];
+      Bt[v] = rec_apply(Aw, sB[w][lane * V + v], cw, Bt[v]);
+      At[v] *= Aw;
+    }
+  }
+  if constexpr (CHAIN) {
+    const uint32_t groups = (tiles + G - 1) / G;
+    rec_chain<V, G>(p.maps + ((uint64_t)b * tiles + q) * p.dim + cl,
+                    p.heads + ((uint64_t)b * groups + q / G) * p.dim + cl, p.dim, q, At, Bt, cutt,
+                    on, wave, waves, lane, sMap, sHead, after);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) after[v] = rec_apply(Ab[v], Bb[v], cutb, after[v]);
+
+  // the gradients; the gates are formed again, which costs less than the registers
+  // that would keep them
+  float sum[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+#pragma unroll
+  for (int s = S - 1; s >= 0; --s) {
+    const bool cut = RESET && (flags >> s & 1);
+    rr[s].w = (uint32_t)opaque_int((int)rr[s].w);
+    ir[s].w = (uint32_t)opaque_int((int)ir[s].w);
+    float dx[V], dr[V], di[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float x = xr[s].get(v);
+      const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
+      // 1 / m, finite where m is 0; y / m and m from it
+      const float rs = __builtin_amdgcn_rsqf(__builtin_fmaxf(g.m2, 1e-37f));
+      const float y = g.lg * kLn2, ix = g.si * x;
+      const float gh = dh[s][v] + after[v];
+      const float next = g.a * gh;
+      after[v] = cut ? 0.0f : next;
+      const float ah = g.a * u[s][v];
+      const float kept = cut ? 0.0f : ah * y;
+      const float e = gh * __builtin_fmaf(-ix * (y * rs), g.a * g.a, kept);
+      const float gm = gh * (g.m2 * rs) * g.si;
+      dx[v] = gm;
+      di[v] = gm * x * (1.0f - g.si);
+      dr[v] = e * (1.0f - g.sr);
+      sum[v] += e;
+    }
+    if (on && s < n) {
+      const int64_t o = (b * p.L + t0 + s) * p.dim;
+      rec_store<T, V>(static_cast<T*>(p.dx) + o + c, dx);
+      rec_store<T, V>(static_cast<T*>(p.dr) + o + c, dr);
+      rec_store<T, V>(static_cast<T*>(p.di) + o + c, di);
+    }
+  }
+  if (t0 == 0 && p.dh0 && on)
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.dh0[b * p.dim + c + v] = after[v];
+  // the tile's share of dA, its runs added in order
+#pragma unroll
+  for (int v = 0; v < V; ++v) sH[wave][lane * V + v] = sum[v];
+  __syncthreads();
+  if (wave == 0 && on)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float s = sum[v];
+      for (int w = 1; w < waves; ++w) s += sH[w][lane * V + v];
+      p.part[((int64_t)b * tiles + tile) * p.dim + c + v] = s;
+    }
 }
 
 // dA: the tiles' shares added in a fixed order, in 64 bits; 8 slices of them by 32
@@ -268,13 +262,12 @@ hipError_t go(const RecParams& p, hipStream_t s) {
   hipError_t e;
   if (tiles == 1) {
     hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, false>), dim3((unsigned)across),
-                       dim3((unsigned)((p.L + S - 1) / S * 64)), 0, s, p, (uint32_t)across);
+                       dim3((unsigned)((p.L + S - 1) / S * 64)), 0, s, p);
   } else {
     e = rec_clear(p, s);
     if (e != hipSuccess) return e;
-    const int64_t grid = total < (1 << 20) ? total : (1 << 20);
-    hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)grid), dim3(1024), 0,
-                       s, p, (uint32_t)total);
+    hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)total), dim3(1024),
+                       0, s, p);
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -9,7 +9,7 @@ constexpr int S = (int)kRecRun;
 constexpr int kMaxWaves = 16;
 
 template <typename T, int V, bool Z, bool RESET, bool CHAIN>
-__global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const uint32_t total) {
+__global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p) {
   constexpr int C = 64 * V;                       // channels of a strip
   constexpr int G = (int)kRecGroup;
   __shared__ float sA[kMaxWaves][C], sH[kMaxWaves][C];
@@ -24,142 +24,137 @@ __global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p, const 
   const uint32_t across = strips * (uint32_t)p.batch;
   const int64_t marks = (p.L + kRecTile - 1) / kRecTile;
 
-  for (uint32_t job = blockIdx.x;;) {
-    if constexpr (CHAIN) job = rec_ticket(p.ticket, &sTicket);
-    if (job >= total) return;
-    const uint32_t tile = job / across, at = job - tile * across;
-    const int64_t b = at / strips;
-    const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
-    const bool on = c < p.dim;
-    const uint32_t cl = on ? c : 0;
-    const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
-    const int64_t left = p.L - t0;
-    const int n = left >= S ? S : left > 0 ? (int)left : 0;    // its steps
+  const uint32_t at = blockIdx.x % across;
+  const uint32_t tile = CHAIN ? rec_ticket(p.ticket, at, &sTicket) : 0;
+  const int64_t b = at / strips;
+  const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
+  const bool on = c < p.dim;
+  const uint32_t cl = on ? c : 0;
+  const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
+  const int64_t left = p.L - t0;
+  const int n = left >= S ? S : left > 0 ? (int)left : 0;    // its steps
 
-    // every load of the run is in flight at once; steps past the end read the last.  A
-    // row's address is the same in every lane, a lane's place in it 32 bits.
-    RecRaw<T, V> xr[S], rr[S], ir[S], zr[Z ? S : 1];
-    auto row = [&](const Rows& q, int64_t t) {
-      return static_cast<const T*>(q.p) + b * q.batch + t * q.token;
-    };
+  // every load of the run is in flight at once; steps past the end read the last.  A
+  // row's address is the same in every lane, a lane's place in it 32 bits.
+  RecRaw<T, V> xr[S], rr[S], ir[S], zr[Z ? S : 1];
+  auto row = [&](const Rows& q, int64_t t) {
+    return static_cast<const T*>(q.p) + b * q.batch + t * q.token;
+  };
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int64_t t = t0 + s < p.L ? t0 + s : p.L - 1;
-      rr[s].load(row(p.r, t) + cl);
-      ir[s].load(row(p.i, t) + cl);
-      xr[s].load(row(p.x, t) + cl);
-      if constexpr (Z) zr[s].load(row(p.z, t) + cl);
-    }
-    if (n < S) {                                               // those leave the state
+  for (int s = 0; s < S; ++s) {
+    const int64_t t = t0 + s < p.L ? t0 + s : p.L - 1;
+    rr[s].load(row(p.r, t) + cl);
+    ir[s].load(row(p.i, t) + cl);
+    xr[s].load(row(p.x, t) + cl);
+    if constexpr (Z) zr[s].load(row(p.z, t) + cl);
+  }
+  if (n < S) {                                               // those leave the state
 #pragma unroll
-      for (int s = 0; s < S; ++s)
-        if (s >= n) {
-          rr[s].fill(-INFINITY);
-          ir[s].fill(0.0f);
-          xr[s].fill(0.0f);
-        }
-    }
-    uint32_t flags = 0;                                        // of the wave's steps
-    if constexpr (RESET) {
-      const bool f = lane < n && p.reset[b * p.L + t0 + lane];
-      flags = (uint32_t)__ballot(f);
-    }
-    float A2[V];
+    for (int s = 0; s < S; ++s)
+      if (s >= n) {
+        rr[s].fill(-INFINITY);
+        ir[s].fill(0.0f);
+        xr[s].fill(0.0f);
+      }
+  }
+  uint32_t flags = 0;                                        // of the wave's steps
+  if constexpr (RESET) {
+    const bool f = lane < n && p.reset[b * p.L + t0 + lane];
+    flags = (uint32_t)__ballot(f);
+  }
+  float A2[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) A2[v] = p.A[cl + v] * kLog2e;
+  for (int v = 0; v < V; ++v) A2[v] = p.A[cl + v] * kLog2e;
 
-    // the run's own map
-    float a[S][V], u[S][V], A[V], H[V];
+  // the run's own map
+  float a[S][V], u[S][V], A[V], H[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = 1.0f;
+    H[v] = 0.0f;
+  }
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const bool cut = RESET && (flags >> s & 1);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      A[v] = 1.0f;
-      H[v] = 0.0f;
+      const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
+      a[s][v] = g.a;
+      u[s][v] = rec_sqrt(g.m2) * (g.si * xr[s].get(v));
+      H[v] = rec_apply(a[s][v], u[s][v], cut, H[v]);
+      A[v] *= a[s][v];
     }
+  }
+  // the first run starts from h0, and says so by a map that leaves out what is before
+  // it: h0 is read here alone, before anything that last (h0's place, it may be) waits for
+  const bool first = t0 == 0 && p.h0;
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    h[v] = first ? p.h0[b * p.dim + cl + v] : 0.0f;
+    sA[wave][lane * V + v] = A[v];
+    sH[wave][lane * V + v] = first ? rec_apply(A[v], H[v], flags != 0, h[v]) : H[v];
+  }
+  if (lane == 0) sCut[wave] = first || flags != 0;
+  __syncthreads();
+
+  // the map of the waves before this one, and the tile's
+  float Ab[V], Hb[V], At[V], Ht[V];
+  bool cutb = false, cutt = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    Ab[v] = At[v] = 1.0f;
+    Hb[v] = Ht[v] = 0.0f;
+  }
+  for (int w = 0; w < waves; ++w) {
+    if (w == wave) {
+      cutb = cutt;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        Ab[v] = At[v];
+        Hb[v] = Ht[v];
+      }
+    }
+    const bool cw = sCut[w] != 0;
+    cutt = cutt || cw;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float Aw = sA[w][lane * V + v];
+      Ht[v] = rec_apply(Aw, sH[w][lane * V + v], cw, Ht[v]);
+      At[v] *= Aw;
+    }
+  }
+
+  // the state that enters the tile
+  if constexpr (CHAIN) {
+    const uint32_t tiles = (uint32_t)((p.L + kRecFwdTile - 1) / kRecFwdTile);
+    const uint32_t groups = (tiles + G - 1) / G;
+    rec_chain<V, G>(p.maps + ((uint64_t)b * tiles + tile) * p.dim + cl,
+                    p.heads + ((uint64_t)b * groups + tile / G) * p.dim + cl, p.dim, tile, At, Ht,
+                    cutt, on, wave, waves, lane, sMap, sHead, h);
+  }
+  // and the wave's run
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = rec_apply(Ab[v], Hb[v], cutb, h[v]);
+  if (p.ckpt && on && t0 % kRecTile == 0 && n)
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.ckpt[(b * marks + t0 / kRecTile) * p.dim + c + v] = h[v];
+  if (p.out || p.last) {
+    T* out = static_cast<T*>(p.out) + (b * p.L + t0) * p.dim;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const bool cut = RESET && (flags >> s & 1);
+      float y[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
-        a[s][v] = g.a;
-        u[s][v] = rec_sqrt(g.m2) * (g.si * xr[s].get(v));
-        H[v] = rec_apply(a[s][v], u[s][v], cut, H[v]);
-        A[v] *= a[s][v];
+        h[v] = rec_apply(a[s][v], u[s][v], cut, h[v]);
+        y[v] = Z ? h[v] * silu(zr[Z ? s : 0].get(v)) : h[v];
       }
+      if (p.out && on && s < n) rec_store<T, V>(out + s * p.dim + c, y);
     }
-    // the first run starts from h0, and says so by a map that leaves out what is before
-    // it: h0 is read here alone, before anything that last (h0's place, it may be) waits for
-    const bool first = t0 == 0 && p.h0;
-    float h[V];
+    if (p.last && on && left > 0 && left <= S)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = first ? p.h0[b * p.dim + cl + v] : 0.0f;
-      sA[wave][lane * V + v] = A[v];
-      sH[wave][lane * V + v] = first ? rec_apply(A[v], H[v], flags != 0, h[v]) : H[v];
-    }
-    if (lane == 0) sCut[wave] = first || flags != 0;
-    __syncthreads();
-
-    // the map of the waves before this one, and the tile's
-    float Ab[V], Hb[V], At[V], Ht[V];
-    bool cutb = false, cutt = false;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      Ab[v] = At[v] = 1.0f;
-      Hb[v] = Ht[v] = 0.0f;
-    }
-    for (int w = 0; w < waves; ++w) {
-      if (w == wave) {
-        cutb = cutt;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          Ab[v] = At[v];
-          Hb[v] = Ht[v];
-        }
-      }
-      const bool cw = sCut[w] != 0;
-      cutt = cutt || cw;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float Aw = sA[w][lane * V + v];
-        Ht[v] = rec_apply(Aw, sH[w][lane * V + v], cw, Ht[v]);
-        At[v] *= Aw;
-      }
-    }
-
-    // the state that enters the tile
-    if constexpr (CHAIN) {
-      const uint32_t tiles = (uint32_t)((p.L + kRecFwdTile - 1) / kRecFwdTile);
-      const uint32_t groups = (tiles + G - 1) / G;
-      rec_chain<V, G>(p.maps + ((uint64_t)b * tiles + tile) * p.dim + cl,
-                      p.heads + ((uint64_t)b * groups + tile / G) * p.dim + cl, p.dim, tile, At, Ht,
-                      cutt, on, wave, waves, lane, sMap, sHead, h);
-    }
-    // and the wave's run
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = rec_apply(Ab[v], Hb[v], cutb, h[v]);
-    if (p.ckpt && on && t0 % kRecTile == 0 && n)
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.ckpt[(b * marks + t0 / kRecTile) * p.dim + c + v] = h[v];
-    if (p.out || p.last) {
-      T* out = static_cast<T*>(p.out) + (b * p.L + t0) * p.dim;
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const bool cut = RESET && (flags >> s & 1);
-        float y[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          h[v] = rec_apply(a[s][v], u[s][v], cut, h[v]);
-          y[v] = Z ? h[v] * silu(zr[Z ? s : 0].get(v)) : h[v];
-        }
-        if (p.out && on && s < n) rec_store<T, V>(out + s * p.dim + c, y);
-      }
-      if (p.last && on && left > 0 && left <= S)
-#pragma unroll
-        for (int v = 0; v < V; ++v) p.last[b * p.dim + c + v] = h[v];
-    }
-    if constexpr (!CHAIN) return;
-    __syncthreads();     // the tile's shared memory has been read
+      for (int v = 0; v < V; ++v) p.last[b * p.dim + c + v] = h[v];
   }
 }
 
@@ -169,15 +164,14 @@ hipError_t go(const RecParams& p, hipStream_t s) {
   if (!p.ticket) {
     const int waves = (int)((p.L + S - 1) / S);
     hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, false>), dim3((unsigned)across), dim3(64 * waves),
-                       0, s, p, (uint32_t)across);
+                       0, s, p);
     return hipGetLastError();
   }
   const int64_t total = across * ((p.L + kRecFwdTile - 1) / kRecFwdTile);
   const hipError_t e = rec_clear(p, s);
   if (e != hipSuccess) return e;
-  const int64_t grid = total < (1 << 20) ? total : (1 << 20);
-  hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)grid),
-                     dim3((unsigned)(kRecFwdTile / S * 64)), 0, s, p, (uint32_t)total);
+  hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)total),
+                     dim3((unsigned)(kRecFwdTile / S * 64)), 0, s, p);
   return hipGetLastError();
 }
 

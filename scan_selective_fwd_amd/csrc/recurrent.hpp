@@ -18,7 +18,7 @@ struct RecParams {
   float* ckpt;           // nullable, (batch, tiles, dim): the state entering each kRecTile steps
   bool pairs;            // rows start on 4 bytes and hold whole pairs of bfloat16
   // workspace where the sequence takes several tiles
-  uint32_t* ticket;
+  uint32_t* ticket;      // (batch * strips) counters, kTicketWords apart
   uint64_t* maps;        // (batch, tiles, dim): the tiles' maps
   uint64_t* heads;       // (batch, groups of tiles, dim): the state after each group
   int64_t words;         // of ticket, maps and heads together, in 64 bits: cleared first
@@ -48,6 +48,8 @@ constexpr int64_t kRecGroup = 16;
 constexpr int64_t kRecBwdRun = 8;
 constexpr int64_t kRecBwdTile = 16 * kRecBwdRun;
 static_assert(kRecBwdTile % kRecTile == 0 && kRecFwdTile % kRecTile == 0, "tiles between checkpoints");
+
+constexpr int kTicketWords = 32;
 
 constexpr int64_t rec_strips(int64_t dim, bool pairs) {
   return pairs ? (dim + 127) / 128 : (dim + 63) / 64;

@@ -10,7 +10,6 @@
 namespace {
 
 constexpr int64_t kLim = (int64_t)1 << 62;
-constexpr int64_t kGridLim = 0x7FFFFFFF;
 
 int esize(int dt) { return dt == MAMBA_F32 ? 4 : 2; }
 
@@ -56,8 +55,7 @@ mamba_status check_shape(const mamba_recurrence_shape* s) {
     return MAMBA_ERR_SHAPE;
   if (s->dim > (int64_t)1 << 28 || s->seqlen > kLim / 64 / s->batch ||
       s->dim > kLim / 64 / (s->batch * s->seqlen) ||
-      s->batch > (s->seqlen > mscan::kRecBwdTile ? kGridLim : mscan::max_blocks(1024)) /
-                     mscan::rec_strips(s->dim, false) / bwd_tiles(s->seqlen))
+      s->batch > mscan::max_blocks(1024) / mscan::rec_strips(s->dim, false) / bwd_tiles(s->seqlen))
     return MAMBA_ERR_UNSUPPORTED;
   if (!span_ok(s->batch, s->x_batch_stride, s->seqlen, s->x_token_stride) ||
       !span_ok(s->batch, s->r_batch_stride, s->seqlen, s->r_token_stride) ||
@@ -130,7 +128,7 @@ ChainLayout chain_layout(const mamba_recurrence_shape* s, int64_t n) {
   const int64_t g = (n + mscan::kRecGroup - 1) / mscan::kRecGroup;
   const size_t row = (size_t)(s->batch * s->dim) * 8;
   ChainLayout l;
-  l.maps = 256;
+  l.maps = (size_t)(s->batch * mscan::rec_strips(s->dim, false)) * mscan::kTicketWords * 4;
   l.heads = l.maps + row * (size_t)n;
   l.total = l.heads + row * (size_t)g;
   return l;

@@ -168,10 +168,13 @@ __device__ __forceinline__ void rec_chain(uint64_t* maps, uint64_t* heads, int64
   }
 }
 
-// The next tile of a launch over tiles in order: every thread of the block.
-__device__ __forceinline__ uint32_t rec_ticket(uint32_t* counter, uint32_t* sTicket) {
+// The next tile of a strip: the first block to come takes its first, and so on.  Each
+// strip counts for itself, on a cache line of its own.
+__device__ __forceinline__ uint32_t rec_ticket(uint32_t* tickets, uint32_t strip,
+                                               uint32_t* sTicket) {
   if (threadIdx.x == 0)
-    *sTicket = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *sTicket = __hip_atomic_fetch_add(tickets + (size_t)strip * kTicketWords, 1u, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   return __builtin_amdgcn_readfirstlane(*sTicket);
 }
