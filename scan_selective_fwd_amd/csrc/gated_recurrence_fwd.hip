@@ -6,20 +6,22 @@ namespace mscan {
 namespace {
 
 constexpr int S = (int)kRecRun;
-constexpr int kMaxWaves = 16;
+constexpr int kMaxWaves = (int)(kRecOneTile / kRecRun);
+constexpr int kTileWaves = (int)(kRecFwdTile / kRecRun);
 
 template <typename T, int V, bool Z, bool RESET, bool CHAIN>
-__global__ __launch_bounds__(1024) void rec_fwd_kernel(const RecParams p) {
+__global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64) void rec_fwd_kernel(const RecParams p) {
   constexpr int C = 64 * V;                       // channels of a strip
   constexpr int G = (int)kRecGroup;
-  __shared__ float sA[kMaxWaves][C], sH[kMaxWaves][C];
-  __shared__ int sCut[kMaxWaves];
+  constexpr int W = CHAIN ? kTileWaves : kMaxWaves;
+  __shared__ float sA[W][C], sH[W][C];
+  __shared__ int sCut[W];
   __shared__ uint64_t sMap[CHAIN ? G : 1][CHAIN ? C : 1];
   __shared__ float sHead[CHAIN ? C : 1];
   __shared__ uint32_t sTicket;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
+  const int waves = CHAIN ? kTileWaves : blockDim.x >> 6;
   const uint32_t strips = (uint32_t)((p.dim + C - 1) / C);
   const uint32_t across = strips * (uint32_t)p.batch;
   const int64_t marks = (p.L + kRecTile - 1) / kRecTile;
@@ -171,7 +173,7 @@ hipError_t go(const RecParams& p, hipStream_t s) {
   const hipError_t e = rec_clear(p, s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)total),
-                     dim3((unsigned)(kRecFwdTile / S * 64)), 0, s, p);
+                     dim3(kTileWaves * 64), 0, s, p);
   return hipGetLastError();
 }
 

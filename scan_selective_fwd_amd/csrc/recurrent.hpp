@@ -41,7 +41,7 @@ constexpr int64_t kRecTile = 64;   // steps between checkpoints
 // sequences take tiles of kRecFwdTile steps, joined kRecGroup at a time.
 constexpr int64_t kRecRun = 16;
 constexpr int64_t kRecOneTile = 16 * kRecRun;
-constexpr int64_t kRecFwdTile = 16 * kRecRun;
+constexpr int64_t kRecFwdTile = 8 * kRecRun;
 constexpr int64_t kRecGroup = 16;
 
 // The backward: the same with runs of kRecBwdRun steps.

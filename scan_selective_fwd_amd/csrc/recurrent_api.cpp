@@ -135,7 +135,7 @@ ChainLayout chain_layout(const mamba_recurrence_shape* s, int64_t n) {
 }
 
 ChainLayout fwd_layout(const mamba_recurrence_shape* s) {
-  return chain_layout(s, fwd_tiles(s->seqlen));
+  return chain_layout(s, s->seqlen <= mscan::kRecOneTile ? 1 : fwd_tiles(s->seqlen));
 }
 
 ChainLayout bwd_chain(const mamba_recurrence_shape* s) {
