@@ -217,8 +217,8 @@ mamba_status norm_fwd(const void* x, int64_t x_row, const void* residual, int64_
   p.x = x; p.res = residual; p.w = weight; p.x_row = x_row; p.res_row = res_row;
   p.rows = rows; p.dim = dim; p.eps = eps;
   p.out = out; p.scale = scale; p.res_out = residual_out;
-  p.vec = dim % 8 == 0 && rows16(x, x_row, es) && (!residual || rows16(residual, res_row, er)) &&
-          aligned(weight, 16) && aligned(out, fp8 ? 8 : 16) && aligned(residual_out, 16);
+  p.vec = dim % (16 / es) == 0 && rows16(x, x_row, es) && (!residual || rows16(residual, res_row, er)) &&
+          aligned(weight, 16) && aligned(out, fp8 ? (size_t)(16 / es) : 16) && aligned(residual_out, 16);
   return hip_status(mscan::dispatch_res_norm_fwd(p, kind, fp8, as_stream(stream)));
 }
 
@@ -394,7 +394,7 @@ mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_row_stride,
   p.dout = dout; p.dres = dres; p.dx = dx; p.dresidual = dresidual; p.dw = dweight;
   p.part = static_cast<float*>(workspace);
   p.parts = mscan::res_norm_parts(rows);
-  p.vec = dim % 8 == 0 && rows16(res, res_row_stride, er) && aligned(dout, 16) &&
+  p.vec = dim % (16 / es) == 0 && rows16(res, res_row_stride, er) && aligned(dout, 16) &&
           aligned(dres, 16) && aligned(weight, 16) && aligned(dx, 16) && aligned(dresidual, 16);
   return hip_status(mscan::dispatch_res_norm_bwd(p, kind, as_stream(stream)));
 }

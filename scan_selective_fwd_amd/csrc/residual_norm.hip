@@ -1,35 +1,48 @@
-// Root-mean-square norm with the residual's addition: a block takes a row.
+// Root-mean-square norm with the residual's addition, rows of token-major activations:
+//   res = x + residual (as it is stored),  out = res r w,  r = 1 / sqrt(mean(res^2) + eps)
+// in the activations' type, or in 8 bits under the row's scale max|out| / 448.
+// Backward, with dhat = dout w:
+//   d = dres + r (dhat - res r^2 mean(dhat res)),  dw = sum over rows of dout res r
+//
+// A team of 64 to 512 threads takes a row and keeps it in registers: every tensor is
+// read once and written once.  Rows too long for that are walked again from the cache.
 #include "recurrent_common.hpp"
 
 namespace mscan {
 
 namespace {
 
-constexpr int kParts = 512;
+constexpr int kParts = 512;        // blocks of the backward: two a CU
+constexpr int kFwdBlocks = 1 << 22;
 
-// Sum (or largest value) over the block's 256 threads, in every thread.
 template <bool MAX>
-__device__ __forceinline__ float block_join(float a, float* sh) {
+__device__ __forceinline__ float join(float a, float b) {
+  return MAX ? __builtin_fmaxf(a, b) : a + b;
+}
+
+// Sum (or largest value) over a team of TEAM threads of a block, in every thread.  `sh`
+// holds a float for each wave of the block.
+template <int TEAM, bool MAX>
+__device__ __forceinline__ float team_join(float a, float* sh) {
+  a = join<MAX>(a, dpp_mov<0xB1>(a, a));     // quad_perm 1,0,3,2
+  a = join<MAX>(a, dpp_mov<0x4E>(a, a));     // quad_perm 2,3,0,1
+  a = join<MAX>(a, dpp_mov<0x141>(a, a));    // row_half_mirror
+  a = join<MAX>(a, dpp_mov<0x140>(a, a));    // row_mirror
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(a), false, false);
+  a = join<MAX>(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(a), false, false);
+  a = join<MAX>(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  if constexpr (TEAM > 64) {
+    constexpr int W = TEAM / 64;
+    __syncthreads();   // what was joined before has been read
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = a;
+    __syncthreads();
+    const int w0 = threadIdx.x / TEAM * W;
+    a = sh[w0];
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const float o = __shfl_xor(a, off);
-    a = MAX ? __builtin_fmaxf(a, o) : a + o;
+    for (int w = 1; w < W; ++w) a = join<MAX>(a, sh[w0 + w]);
   }
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = a;
-  __syncthreads();
-  return MAX ? __builtin_fmaxf(__builtin_fmaxf(sh[0], sh[1]), __builtin_fmaxf(sh[2], sh[3]))
-             : (sh[0] + sh[1]) + (sh[2] + sh[3]);
-}
-
-template <typename T>
-__device__ __forceinline__ float rounded(float v) {
-  if constexpr (sizeof(T) == 2) return bf16_to_f32((bf16_t)pack_bf16(v, v));
-  else return v;
-}
-
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-  return (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false);
+  return a;
 }
 
 // 1 / sqrt(mean of squares + eps) from their sum.  Where that passes float32's range (or
@@ -43,110 +56,419 @@ __device__ __forceinline__ float root_of(float s2, const ResNormParams& p, F aga
   return sc / __builtin_sqrtf(again(sc) / n + p.eps * sc * sc);
 }
 
-template <typename T, typename R, bool FP8>
-__global__ __launch_bounds__(256) void res_norm_fwd_kernel(const ResNormParams p) {
-  __shared__ float sh[4];
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(p.x) + row * p.x_row;
-    const R* res = p.res ? static_cast<const R*>(p.res) + row * p.res_row : nullptr;
-    R* keep = p.res_out ? static_cast<R*>(p.res_out) + row * p.dim : nullptr;
-    auto sum = [&](int64_t k) {
-      const float v = Elem<T>::load1(x + k);
-      return res ? rounded<R>(v + Elem<R>::load1(res + k)) : v;
-    };
-    float s2 = 0.0f;
-    for (int64_t k = threadIdx.x; k < p.dim; k += 256) {
-      const float v = sum(k);
-      s2 = __builtin_fmaf(v, v, s2);
-    }
-    s2 = block_join<false>(s2, sh);
-    const float r = root_of(s2, p, [&](float sc) {
-      float t2 = 0.0f;
-      for (int64_t k = threadIdx.x; k < p.dim; k += 256) {
-        const float v = sum(k) * sc;
-        t2 = __builtin_fmaf(v, v, t2);
+// V values of x + residual as they are stored.
+template <typename R, int V>
+__device__ __forceinline__ void add_stored(float (&x)[V], const float (&r)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] += r[v];
+  if constexpr (sizeof(R) == 2) {
+    if constexpr (V == 1) {
+      x[0] = bf16_lo(pack_bf16(x[0], x[0]));
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; v += 2) {
+        const uint32_t w = pack_bf16(x[v], x[v + 1]);
+        x[v] = bf16_lo(w);
+        x[v + 1] = bf16_hi(w);
       }
-      return block_join<false>(t2, sh);
-    });
-    float inv = 1.0f;
-    if constexpr (FP8) {
-      float most = 0.0f;
-      for (int64_t k = threadIdx.x; k < p.dim; k += 256)
-        most = __builtin_fmaxf(most, __builtin_fabsf(sum(k) * r * (p.w ? p.w[k] : 1.0f)));
-      most = __builtin_fmaxf(block_join<true>(most, sh), 0x1p-100f);
-      inv = 448.0f / most;
-      if (threadIdx.x == 0) p.scale[row] = most / 448.0f;
-    }
-    for (int64_t k = threadIdx.x; k < p.dim; k += 256) {
-      const float v = sum(k), y = v * r * (p.w ? p.w[k] : 1.0f);
-      if constexpr (FP8) static_cast<uint8_t*>(p.out)[row * p.dim + k] = to_e4m3(y * inv);
-      else Elem<T>::store1(static_cast<T*>(p.out) + row * p.dim + k, y);
-      if (keep) Elem<R>::store1(keep + k, v);
     }
   }
 }
 
-template <typename T, typename R>
-__global__ __launch_bounds__(256) void res_norm_bwd_kernel(const ResNormParams p) {
+template <int V>
+__device__ __forceinline__ void store_e4m3(void* out, int64_t at, const float (&y)[V]) {
+  uint8_t* q = static_cast<uint8_t*>(out) + at;
+  if constexpr (V == 1) {
+    *q = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[0], 0, false);
+  } else {
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) {
+      int t = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k], y[4 * k + 1], 0, false);
+      w[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k + 2], y[4 * k + 3], t, true);
+    }
+    if constexpr (V == 4) *reinterpret_cast<uint32_t*>(q) = w[0];
+    else *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void load_weight(const float* w, int64_t at, float (&v)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) v[k] = 1.0f;
+  if (w) load_f32<V>(w, at, v);
+}
+
+template <typename T, typename R, bool FP8, int V, int TEAM, int NV>
+__global__ __launch_bounds__(256) void res_norm_fwd_kernel(const ResNormParams p) {
   __shared__ float sh[4];
-  float* mine = p.dw ? p.part + blockIdx.x * p.dim : nullptr;
+  constexpr int TEAMS = 256 / TEAM;
+  const int tid = threadIdx.x & (TEAM - 1);
+  const int64_t n = p.dim;
+  for (int64_t row0 = (int64_t)blockIdx.x * TEAMS; row0 < p.rows; row0 += (int64_t)gridDim.x * TEAMS) {
+    const int64_t row = row0 + threadIdx.x / TEAM;
+    const bool on = row < p.rows;                 // whole teams
+    float x[NV][V], r[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t k = (int64_t)(j * TEAM + tid) * V;
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[j][v] = r[j][v] = 0.0f;
+      if (on && k < n) {
+        load_vec<T, V>(p.x, row * p.x_row + k, x[j]);
+        if (p.res) load_vec<R, V>(p.res, row * p.res_row + k, r[j]);
+      }
+    }
+    float s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (p.res) add_stored<R, V>(x[j], r[j]);
+#pragma unroll
+      for (int v = 0; v < V; ++v) s2 = __builtin_fmaf(x[j][v], x[j][v], s2);
+    }
+    s2 = team_join<TEAM, false>(s2, sh);
+    const float root = root_of(s2, p, [&](float sc) {
+      float t2 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float t = x[j][v] * sc;
+          t2 = __builtin_fmaf(t, t, t2);
+        }
+      return team_join<TEAM, false>(t2, sh);
+    });
+    float y[NV][V], most = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t k = (int64_t)(j * TEAM + tid) * V;
+      if (on && k < n) {
+        if (p.res) store_vec<R, V>(p.res_out, row * n + k, x[j]);
+        float w[V];
+        load_weight<V>(p.w, k, w);
+#pragma unroll
+        for (int v = 0; v < V; ++v) y[j][v] = x[j][v] * root * w[v];
+        if constexpr (!FP8) store_vec<T, V>(p.out, row * n + k, y[j]);
+        else
+#pragma unroll
+          for (int v = 0; v < V; ++v) most = __builtin_fmaxf(most, __builtin_fabsf(y[j][v]));
+      }
+    }
+    if constexpr (FP8) {
+      most = __builtin_fmaxf(team_join<TEAM, true>(most, sh), 0x1p-100f);
+      const float inv = 448.0f / most;
+      if (on && tid == 0) p.scale[row] = most / 448.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int64_t k = (int64_t)(j * TEAM + tid) * V;
+        if (on && k < n) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) y[j][v] *= inv;
+          store_e4m3<V>(p.out, row * n + k, y[j]);
+        }
+      }
+    }
+  }
+}
+
+// Rows too long for the registers: walked two or three times by a block.
+template <typename T, typename R, bool FP8, int V>
+__global__ __launch_bounds__(256) void res_norm_fwd_walk_kernel(const ResNormParams p) {
+  __shared__ float sh[4];
+  const int64_t n = p.dim;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    auto sum = [&](int64_t k, float (&x)[V]) {
+      float r[V];
+      load_vec<T, V>(p.x, row * p.x_row + k, x);
+      if (p.res) {
+        load_vec<R, V>(p.res, row * p.res_row + k, r);
+        add_stored<R, V>(x, r);
+      }
+    };
+    auto squares = [&](float sc) {
+      float s2 = 0.0f;
+      for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += 256 * V) {
+        float x[V];
+        sum(k, x);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float t = x[v] * sc;
+          s2 = __builtin_fmaf(t, t, s2);
+        }
+      }
+      return team_join<256, false>(s2, sh);
+    };
+    const float root = root_of(squares(1.0f), p, squares);
+    auto normed = [&](int64_t k, float (&x)[V], float (&y)[V]) {
+      float w[V];
+      sum(k, x);
+      load_weight<V>(p.w, k, w);
+#pragma unroll
+      for (int v = 0; v < V; ++v) y[v] = x[v] * root * w[v];
+    };
+    float inv = 1.0f;
+    if constexpr (FP8) {
+      float most = 0.0f;
+      for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += 256 * V) {
+        float x[V], y[V];
+        normed(k, x, y);
+#pragma unroll
+        for (int v = 0; v < V; ++v) most = __builtin_fmaxf(most, __builtin_fabsf(y[v]));
+      }
+      most = __builtin_fmaxf(team_join<256, true>(most, sh), 0x1p-100f);
+      inv = 448.0f / most;
+      if (threadIdx.x == 0) p.scale[row] = most / 448.0f;
+    }
+    for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += 256 * V) {
+      float x[V], y[V];
+      normed(k, x, y);
+      if (p.res) store_vec<R, V>(p.res_out, row * n + k, x);
+      if constexpr (FP8) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) y[v] *= inv;
+        store_e4m3<V>(p.out, row * n + k, y);
+      } else {
+        store_vec<T, V>(p.out, row * n + k, y);
+      }
+    }
+  }
+}
+
+// Block `part`: its teams take every (parts * TEAMS)-th row, the next row's loads in
+// flight while one is worked on, and leave the block's share of dw in part.
+template <typename T, typename R, int V, int TEAM, int NV>
+__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
+    const ResNormParams p) {
+  constexpr int THREADS = TEAM > 256 ? TEAM : 256, TEAMS = THREADS / TEAM;
+  __shared__ float sh[THREADS / 64];
+  __shared__ float red[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? TEAM * NV * V : 1];
+  const int tid = threadIdx.x & (TEAM - 1), team = threadIdx.x / TEAM;
+  const int64_t n = p.dim;
+  float w[NV][V], dw[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int64_t k = (int64_t)(j * TEAM + tid) * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      w[j][v] = 1.0f;
+      dw[j][v] = 0.0f;
+    }
+    if (p.w && k < n) load_f32<V>(p.w, k, w[j]);
+  }
+  Raw<R, V> xr[NV], gr[NV];
+  Raw<T, V> yr[NV];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t k = (int64_t)(j * TEAM + tid) * V;
+      xr[j].zero();
+      gr[j].zero();
+      yr[j].zero();
+      if (k < n && row < p.rows) {
+        xr[j].load(p.res, row * p.res_row + k);
+        yr[j].load(p.dout, row * n + k);
+        if (p.dres) gr[j].load(p.dres, row * n + k);
+      }
+    }
+  };
+  const int64_t step = p.parts * TEAMS;
+  load(blockIdx.x * (int64_t)TEAMS + team);
+  // every team walks as long as the first: the joins wait for whole blocks
+  for (int64_t row0 = blockIdx.x * (int64_t)TEAMS; row0 < p.rows; row0 += step) {
+    const int64_t row = row0 + team;
+    float x[NV][V], dy[NV][V], g[NV][V];
+    float s2 = 0.0f, sv = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      xr[j].get(x[j]);
+      yr[j].get(dy[j]);
+      gr[j].get(g[j]);
+    }
+    load(row + step);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s2 = __builtin_fmaf(x[j][v], x[j][v], s2);
+        sv = __builtin_fmaf(dy[j][v] * w[j][v], x[j][v], sv);
+      }
+    s2 = team_join<TEAM, false>(s2, sh);
+    sv = team_join<TEAM, false>(sv, sh);
+    const float r = root_of(s2, p, [&](float sc) {
+      float t2 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float t = x[j][v] * sc;
+          t2 = __builtin_fmaf(t, t, t2);
+        }
+      return team_join<TEAM, false>(t2, sh);
+    });
+    const float kk = r * (sv / (float)p.dim);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t k = (int64_t)(j * TEAM + tid) * V;
+      float d[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float hat = x[j][v] * r;
+        d[v] = __builtin_fmaf(r, __builtin_fmaf(-hat, kk, dy[j][v] * w[j][v]), g[j][v]);
+        dw[j][v] = __builtin_fmaf(dy[j][v], hat, dw[j][v]);
+      }
+      if (k < n && row < p.rows) {
+        store_vec<T, V>(p.dx, row * n + k, d);
+        if (sizeof(T) != sizeof(R) && p.dresidual) store_vec<R, V>(p.dresidual, row * n + k, d);
+      }
+    }
+  }
+  if (!p.dw) return;
+  float* mine = p.part + blockIdx.x * n;
+  if constexpr (TEAMS > 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) red[team][(j * V + v) * TEAM + tid] = dw[j][v];
+    __syncthreads();
+    for (int i = threadIdx.x; i < TEAM * NV * V; i += THREADS) {
+      const int jv = i / TEAM, lane = i - jv * TEAM;
+      const int64_t k = (int64_t)((jv / V) * TEAM + lane) * V + jv % V;
+      float sum = red[0][i];
+#pragma unroll
+      for (int m = 1; m < TEAMS; ++m) sum += red[m][i];
+      if (k < n) mine[k] = sum;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t k = (int64_t)(j * TEAM + tid) * V;
+      if (k < n) store_vec<float, V>(mine, k, dw[j]);
+    }
+  }
+}
+
+// Any length and alignment: rows are walked twice by the block, dw is added up in the
+// block's own row of part.
+template <typename T, typename R>
+__global__ __launch_bounds__(256) void res_norm_bwd_walk_kernel(const ResNormParams p) {
+  __shared__ float sh[4];
+  const int64_t n = p.dim;
+  float* mine = p.dw ? p.part + blockIdx.x * n : nullptr;
   if (mine)
-    for (int64_t k = threadIdx.x; k < p.dim; k += 256) mine[k] = 0.0f;
+    for (int64_t k = threadIdx.x; k < n; k += 256) mine[k] = 0.0f;
   for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
     const R* res = static_cast<const R*>(p.res) + row * p.res_row;
-    const T* dout = static_cast<const T*>(p.dout) + row * p.dim;
+    const T* dout = static_cast<const T*>(p.dout) + row * n;
     float s2 = 0.0f, sv = 0.0f;
-    for (int64_t k = threadIdx.x; k < p.dim; k += 256) {
+    for (int64_t k = threadIdx.x; k < n; k += 256) {
       const float v = Elem<R>::load1(res + k);
       s2 = __builtin_fmaf(v, v, s2);
       sv = __builtin_fmaf(Elem<T>::load1(dout + k) * (p.w ? p.w[k] : 1.0f), v, sv);
     }
-    s2 = block_join<false>(s2, sh);
-    sv = block_join<false>(sv, sh);
+    s2 = team_join<256, false>(s2, sh);
+    sv = team_join<256, false>(sv, sh);
     const float r = root_of(s2, p, [&](float sc) {
       float t2 = 0.0f;
-      for (int64_t k = threadIdx.x; k < p.dim; k += 256) {
+      for (int64_t k = threadIdx.x; k < n; k += 256) {
         const float v = Elem<R>::load1(res + k) * sc;
         t2 = __builtin_fmaf(v, v, t2);
       }
-      return block_join<false>(t2, sh);
+      return team_join<256, false>(t2, sh);
     });
-    const float kk = r * (r * (sv / (float)p.dim));
-    for (int64_t k = threadIdx.x; k < p.dim; k += 256) {
-      const float v = Elem<R>::load1(res + k), dy = Elem<T>::load1(dout + k);
-      float d = r * __builtin_fmaf(-v, kk, dy * (p.w ? p.w[k] : 1.0f));
-      if (p.dres) d += Elem<R>::load1(static_cast<const R*>(p.dres) + row * p.dim + k);
-      Elem<T>::store1(static_cast<T*>(p.dx) + row * p.dim + k, d);
-      if (p.dresidual) Elem<R>::store1(static_cast<R*>(p.dresidual) + row * p.dim + k, d);
-      if (mine) mine[k] = __builtin_fmaf(dy, v * r, mine[k]);
+    const float kk = r * (sv / (float)p.dim);
+    for (int64_t k = threadIdx.x; k < n; k += 256) {
+      const float hat = Elem<R>::load1(res + k) * r, dy = Elem<T>::load1(dout + k);
+      const float g = p.dres ? Elem<R>::load1(static_cast<const R*>(p.dres) + row * n + k) : 0.0f;
+      const float d = __builtin_fmaf(
+          r, __builtin_fmaf(-hat, kk, dy * (p.w ? p.w[k] : 1.0f)), g);
+      Elem<T>::store1(static_cast<T*>(p.dx) + row * n + k, d);
+      if (p.dresidual) Elem<R>::store1(static_cast<R*>(p.dresidual) + row * n + k, d);
+      if (mine) mine[k] = __builtin_fmaf(dy, hat, mine[k]);
     }
   }
 }
 
-__global__ __launch_bounds__(256) void res_norm_sum_kernel(const ResNormParams p) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.dim) return;
-  float s = 0.0f;
-  for (int64_t i = 0; i < p.parts; ++i) s += p.part[i * p.dim + c];
-  p.dw[c] = s;
+// dw: the parts summed in order, 16 slices of them by 64 channels.
+__global__ __launch_bounds__(1024) void res_norm_sum_kernel(const ResNormParams p) {
+  __shared__ float red[16][64];
+  const int cl = threadIdx.x & 63, sl = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + cl;
+  float sum = 0.0f;
+  if (c < p.dim) {
+#pragma unroll 8
+    for (int64_t i = sl; i < p.parts; i += 16) sum += p.part[i * p.dim + c];
+  }
+  red[sl][cl] = sum;
+  __syncthreads();
+  if (sl == 0 && c < p.dim) {
+    for (int j = 1; j < 16; ++j) sum += red[j][cl];
+    p.dw[c] = sum;
+  }
 }
 
-template <typename T, typename R>
-hipError_t fwd_go(const ResNormParams& p, bool fp8, hipStream_t s) {
-  const dim3 grid((unsigned)(p.rows < 65536 ? p.rows : 65536));
-  if (fp8)
-    hipLaunchKernelGGL((res_norm_fwd_kernel<T, R, true>), grid, dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL((res_norm_fwd_kernel<T, R, false>), grid, dim3(256), 0, s, p);
+template <typename T, typename R, bool FP8, int V, int TEAM, int NV>
+hipError_t fwd_go(const ResNormParams& p, hipStream_t s) {
+  const int64_t blocks = (p.rows + 256 / TEAM - 1) / (256 / TEAM);
+  hipLaunchKernelGGL((res_norm_fwd_kernel<T, R, FP8, V, TEAM, NV>),
+                     dim3((unsigned)(blocks < kFwdBlocks ? blocks : kFwdBlocks)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, typename R, bool FP8, int V>
+hipError_t fwd_v(const ResNormParams& p, hipStream_t s) {
+  const int64_t nv = (p.dim + V - 1) / V;
+  if (nv <= 64) return fwd_go<T, R, FP8, V, 64, 1>(p, s);
+  if (nv <= 128) return fwd_go<T, R, FP8, V, 64, 2>(p, s);
+  if (nv <= 192) return fwd_go<T, R, FP8, V, 64, 3>(p, s);
+  if (nv <= 256) return fwd_go<T, R, FP8, V, 64, 4>(p, s);
+  if (nv <= 512) return fwd_go<T, R, FP8, V, 256, 2>(p, s);
+  if (nv <= 768) return fwd_go<T, R, FP8, V, 256, 3>(p, s);
+  if (nv <= 1024) return fwd_go<T, R, FP8, V, 256, 4>(p, s);
+  if (nv <= 2048) return fwd_go<T, R, FP8, V, 256, 8>(p, s);
+  if constexpr (V == 1)
+    if (nv <= 4096) return fwd_go<T, R, FP8, V, 256, 16>(p, s);
+  hipLaunchKernelGGL((res_norm_fwd_walk_kernel<T, R, FP8, V>),
+                     dim3((unsigned)(p.rows < kFwdBlocks ? p.rows : kFwdBlocks)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
 template <typename T, typename R>
+hipError_t fwd_t(const ResNormParams& p, bool fp8, hipStream_t s) {
+  constexpr int V = sizeof(T) == 4 ? 4 : 8;
+  if (p.vec) return fp8 ? fwd_v<T, R, true, V>(p, s) : fwd_v<T, R, false, V>(p, s);
+  return fp8 ? fwd_v<T, R, true, 1>(p, s) : fwd_v<T, R, false, 1>(p, s);
+}
+
+template <typename T, typename R, int V, int TEAM, int NV>
 hipError_t bwd_go(const ResNormParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((res_norm_bwd_kernel<T, R>), dim3((unsigned)p.parts), dim3(256), 0, s, p);
-  const hipError_t e = hipGetLastError();
+  hipLaunchKernelGGL((res_norm_bwd_kernel<T, R, V, TEAM, NV>), dim3((unsigned)p.parts),
+                     dim3(TEAM > 256 ? TEAM : 256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, typename R, int V>
+hipError_t bwd_v(const ResNormParams& p, hipStream_t s) {
+  const int64_t nv = (p.dim + V - 1) / V;
+  if (nv <= 64) return bwd_go<T, R, V, 64, 1>(p, s);
+  if (nv <= 128) return bwd_go<T, R, V, 64, 2>(p, s);
+  if (nv <= 192) return bwd_go<T, R, V, 64, 3>(p, s);
+  if (nv <= 256) return bwd_go<T, R, V, 256, 1>(p, s);
+  if (nv <= 512) return bwd_go<T, R, V, 256, 2>(p, s);
+  if (nv <= 768) return bwd_go<T, R, V, 256, 3>(p, s);
+  if (nv <= 1024) return bwd_go<T, R, V, 256, 4>(p, s);
+  if (nv <= 1280) return bwd_go<T, R, V, 256, 5>(p, s);
+  if (nv <= 1536) return bwd_go<T, R, V, 256, 6>(p, s);
+  if (nv <= 2048) return bwd_go<T, R, V, 512, 4>(p, s);
+  if (nv <= 4096) return bwd_go<T, R, V, 512, 8>(p, s);
+  hipLaunchKernelGGL((res_norm_bwd_walk_kernel<T, R>), dim3((unsigned)p.parts), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, typename R>
+hipError_t bwd_t(const ResNormParams& p, hipStream_t s) {
+  const hipError_t e = p.vec ? bwd_v<T, R, 4>(p, s) : bwd_v<T, R, 1>(p, s);
   if (e != hipSuccess || !p.dw) return e;
-  hipLaunchKernelGGL(res_norm_sum_kernel, dim3((unsigned)((p.dim + 255) / 256)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(res_norm_sum_kernel, dim3((unsigned)((p.dim + 63) / 64)), dim3(1024), 0, s, p);
   return hipGetLastError();
 }
 
@@ -157,17 +479,17 @@ int64_t res_norm_parts(int64_t rows) { return rows < kParts ? rows : kParts; }
 hipError_t dispatch_res_norm_fwd(const ResNormParams& p, ResNormKind kind, bool fp8,
                                  hipStream_t s) {
   switch (kind) {
-    case kResF32: return fwd_go<float, float>(p, fp8, s);
-    case kResBf16: return fwd_go<bf16_t, bf16_t>(p, fp8, s);
-    default: return fwd_go<bf16_t, float>(p, fp8, s);
+    case kResF32: return fwd_t<float, float>(p, fp8, s);
+    case kResBf16: return fwd_t<bf16_t, bf16_t>(p, fp8, s);
+    default: return fwd_t<bf16_t, float>(p, fp8, s);
   }
 }
 
 hipError_t dispatch_res_norm_bwd(const ResNormParams& p, ResNormKind kind, hipStream_t s) {
   switch (kind) {
-    case kResF32: return bwd_go<float, float>(p, s);
-    case kResBf16: return bwd_go<bf16_t, bf16_t>(p, s);
-    default: return bwd_go<bf16_t, float>(p, s);
+    case kResF32: return bwd_t<float, float>(p, s);
+    case kResBf16: return bwd_t<bf16_t, bf16_t>(p, s);
+    default: return bwd_t<bf16_t, float>(p, s);
   }
 }
 
