@@ -1,42 +1,58 @@
 // One step of the gated linear recurrence for a batch of sequences, in place on a
 // pool of states:  h <- a h + sqrt(1 - a^2) s(i) x,  out = h (or h silu(z)).
-// A thread takes one channel of one row.
+// A thread takes four neighbouring channels of a row (one, where rows do not start on
+// whole groups of four).
 #include "recurrent_common.hpp"
 
 namespace mscan {
 
 namespace {
 
-template <typename T>
-__global__ __launch_bounds__(256) void rec_step_kernel(const RecStepParams p) {
+template <typename T, int V>
+__global__ __launch_bounds__(256) void rec_step_kernel(const RecStepParams p, const int64_t per) {
   const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= p.batch * p.dim) return;
-  const int64_t b = n / p.dim, d = n - b * p.dim;
+  if (n >= p.batch * per) return;
+  const int64_t b = n / per, d = (n - b * per) * V;
   const int64_t slot = p.slots ? (int64_t)p.slots[b] : b;
-  T* out = static_cast<T*>(p.out) + n;
+  float x[V], r[V], i[V], z[V], A[V], h[V];
   if (slot < 0 || slot >= p.pool) {
-    *out = T(0);
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = 0.0f;
+    store_vec<T, V>(p.out, b * p.dim + d, h);
     return;
   }
-  auto in = [&](const void* q, int64_t row) {
-    return Elem<T>::load1(static_cast<const T*>(q) + b * row + d);
-  };
   float* st = p.state + slot * p.dim + d;
-  const RecGate g = rec_gate(in(p.r, p.r_row), in(p.i, p.i_row), p.A[d] * kLog2e);
-  const float h = __builtin_fmaf(g.a, *st, __builtin_sqrtf(g.m2) * g.si * in(p.x, p.x_row));
-  *st = h;
-  Elem<T>::store1(out, p.z ? h * silu(in(p.z, p.z_row)) : h);
+  load_f32<V>(st, 0, h);
+  load_vec<T, V>(p.r, b * p.r_row + d, r);
+  load_vec<T, V>(p.i, b * p.i_row + d, i);
+  load_vec<T, V>(p.x, b * p.x_row + d, x);
+  if (p.z) load_vec<T, V>(p.z, b * p.z_row + d, z);
+  load_f32<V>(p.A, d, A);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const RecGate g = rec_gate(r[v], i[v], A[v] * kLog2e);
+    h[v] = rec_apply(g.a, rec_sqrt(g.m2) * (g.si * x[v]), false, h[v]);
+  }
+  store_vec<float, V>(st, 0, h);
+  if (p.z)
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = h[v] * silu(z[v]);
+  store_vec<T, V>(p.out, b * p.dim + d, h);
+}
+
+template <typename T, int V>
+hipError_t go(const RecStepParams& p, hipStream_t s) {
+  const int64_t per = p.dim / V;
+  hipLaunchKernelGGL((rec_step_kernel<T, V>), dim3((unsigned)((p.batch * per + 255) / 256)),
+                     dim3(256), 0, s, p, per);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t dispatch_rec_step(const RecStepParams& p, int dtype, hipStream_t s) {
-  const dim3 grid((unsigned)((p.batch * p.dim + 255) / 256));
-  if (dtype == 0)
-    hipLaunchKernelGGL((rec_step_kernel<float>), grid, dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL((rec_step_kernel<bf16_t>), grid, dim3(256), 0, s, p);
-  return hipGetLastError();
+  if (dtype == 0) return p.vec ? go<float, 4>(p, s) : go<float, 1>(p, s);
+  return p.vec ? go<bf16_t, 4>(p, s) : go<bf16_t, 1>(p, s);
 }
 
 }  // namespace mscan

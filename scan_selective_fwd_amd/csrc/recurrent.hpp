@@ -69,6 +69,7 @@ struct RecStepParams {
   float* state;
   const int32_t* slots;  // nullable
   int64_t pool, batch, dim;
+  bool vec;              // groups of four channels: one load of each tensor
   void* out;
 };
 

@@ -333,6 +333,12 @@ mamba_status mamba_gated_recurrence_update(const mamba_recurrence_shape* shape, 
   p.i_row = shape->i_batch_stride; p.z_row = shape->z_batch_stride;
   p.A = A; p.state = state; p.slots = slots; p.pool = pool;
   p.batch = shape->batch; p.dim = shape->dim; p.out = out;
+  const int es = esize(shape->dtype);
+  auto four = [&](const void* q, int64_t row) {
+    return aligned(q, (size_t)(4 * es)) && row % 4 == 0;
+  };
+  p.vec = four(x, p.x_row) && four(r, p.r_row) && four(i, p.i_row) && (!z || four(z, p.z_row)) &&
+          four(out, p.dim) && aligned(state, 16) && aligned(A, 16);
   return hip_status(mscan::dispatch_rec_step(p, shape->dtype == MAMBA_F32 ? 0 : 1,
                                              as_stream(stream)));
 }

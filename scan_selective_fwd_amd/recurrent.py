@@ -26,13 +26,18 @@ _FP8 = torch.float8_e4m3fn
 _current = torch._C._cuda_getDevice
 
 
+@functools.lru_cache(maxsize=None)
+def _function(name):
+    return getattr(lib(), name)
+
+
 def _call(name, dev, *args):
     """The library's call with `dev` the current device, whose stream it goes on."""
     if _current() == dev.index:
-        st = getattr(lib(), name)(*args, _stream(dev))
+        st = _function(name)(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = getattr(lib(), name)(*args, _stream(dev))
+            st = _function(name)(*args, _stream(dev))
     if st:
         _lib.check(st, name)
 
@@ -45,8 +50,20 @@ def _struct(*fields):
     return s, ctypes.byref(s)
 
 
-def _new(like, dev, dtype=None):
-    return torch.empty(like.shape, dtype=dtype or like.dtype, device=dev)
+def _new(like, dtype=None):
+    """A dense tensor of `like`'s shape (empty_like costs half of empty, but keeps the
+    order of a permuted tensor's dimensions)."""
+    if like.is_contiguous():
+        return torch.empty_like(like, dtype=dtype)
+    return torch.empty(like.shape, dtype=dtype or like.dtype, device=like.device)
+
+
+def _strides(t, name, dtype, shape, dev):
+    """Checks a tensor that may be a view of wider rows; its strides but the last's."""
+    if isinstance(t, torch.Tensor) and t.is_contiguous() and t.shape == shape \
+            and t.dtype is dtype and t.device == dev:
+        return t.stride()[:-1]
+    return _view(t, name, dtype, shape, dev, len(shape) - 1)
 
 
 # --------------------------------------------------------------------------- recurrence
@@ -56,9 +73,9 @@ def _shape(x, r, i, z):
     shape = _dims(x, "x", 3)
     dt = x.dtype
     code = _dtype_code(x)
-    s, ref = _struct(*shape, *_view(x, "x", dt, shape, dev, 2), *_view(r, "r", dt, shape, dev, 2),
-                     *_view(i, "i", dt, shape, dev, 2),
-                     *((0, 0) if z is None else _view(z, "z", dt, shape, dev, 2)), code)
+    s, ref = _struct(*shape, *_strides(x, "x", dt, shape, dev), *_strides(r, "r", dt, shape, dev),
+                     *_strides(i, "i", dt, shape, dev),
+                     *((0, 0) if z is None else _strides(z, "z", dt, shape, dev)), code)
     return s, ref, dev, shape
 
 
@@ -114,16 +131,17 @@ def gated_recurrence_fwd(x, r, i, A, z=None, h0=None, *, reset=None, return_last
     s, ref, dev, shape = _shape(x, r, i, z)
     reset = _state_args(s, A, h0, reset, dev)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
+        out = _new(x)
     else:
         _req(out, "out", x.dtype, shape, dev)
     if return_last_state and last_state is None:
-        last_state = torch.empty((s.batch, s.dim), dtype=_F32, device=dev)
+        last_state = torch.empty((s.batch, s.dim), dtype=_F32, device=dev) if h0 is None \
+            else torch.empty_like(h0)
     else:
         _req(last_state, "last_state", _F32, (s.batch, s.dim), dev)
     if checkpoints is not None:
         _req(checkpoints, "checkpoints", _F32, (s.batch, _tiles(s.seqlen), s.dim), dev)
-    n = lib().mamba_gated_recurrence_fwd_workspace_size(ref)
+    n = _function("mamba_gated_recurrence_fwd_workspace_size")(ref)
     ws = _workspace(n, shape, "mamba_gated_recurrence_fwd", workspace, dev)
     _call("mamba_gated_recurrence_fwd", dev, ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(z),
           _ptr(h0), _ptr(reset), _ptr(out), _ptr(last_state), _ptr(checkpoints),
@@ -144,12 +162,12 @@ def gated_recurrence_bwd(x, r, i, A, z, dout, h0=None, *, dlast_state=None, rese
     _req(dlast_state, "dlast_state", _F32, (s.batch, s.dim), dev)
     if checkpoints is not None:
         _req(checkpoints, "checkpoints", _F32, (s.batch, _tiles(s.seqlen), s.dim), dev)
-    g = dict(dx=_new(x, dev), dr=_new(x, dev), di=_new(x, dev), dA=_new(A, dev))
+    g = dict(dx=_new(x), dr=_new(x), di=_new(x), dA=_new(A))
     if z is not None:
-        g["dz"] = _new(x, dev)
+        g["dz"] = _new(x)
     if h0 is not None:
-        g["dh0"] = _new(h0, dev)
-    n = lib().mamba_gated_recurrence_bwd_workspace_size(ref, int(checkpoints is not None))
+        g["dh0"] = _new(h0)
+    n = _function("mamba_gated_recurrence_bwd_workspace_size")(ref, int(checkpoints is not None))
     ws = _workspace(n, shape, "mamba_gated_recurrence_bwd", workspace, dev)
     _call("mamba_gated_recurrence_bwd", dev, ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(z),
           _ptr(h0), _ptr(reset), _ptr(dout), _ptr(dlast_state), _ptr(checkpoints), _ptr(g["dx"]),
@@ -169,15 +187,15 @@ def gated_recurrence_update(state, x, r, i, A, z=None, *, slots=None, out=None):
     batch, dim = shape
     dt = x.dtype
     pool = _dims(state, "state", 2)[0]
-    s, ref = _struct(batch, 1, dim, *_view(x, "x", dt, shape, dev, 1), 0,
-                     *_view(r, "r", dt, shape, dev, 1), 0, *_view(i, "i", dt, shape, dev, 1), 0,
-                     *((0,) if z is None else _view(z, "z", dt, shape, dev, 1)), 0,
+    s, ref = _struct(batch, 1, dim, *_strides(x, "x", dt, shape, dev), 0,
+                     *_strides(r, "r", dt, shape, dev), 0, *_strides(i, "i", dt, shape, dev), 0,
+                     *((0,) if z is None else _strides(z, "z", dt, shape, dev)), 0,
                      _dtype_code(x))
     _req(A, "A", _F32, (dim,), dev)
     _req(state, "state", _F32, (pool, dim), dev)
     slots = _slots(slots, batch, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = _new(x)
     else:
         _req(out, "out", dt, shape, dev)
     _call("mamba_gated_recurrence_update", dev, ref, _ptr(state), _ptr(slots), pool, _ptr(x),
@@ -229,29 +247,40 @@ def _residual_code(t, x):
     return _dtype_code(t)
 
 
+def _row_stride(t, name, dtype, dev):
+    """The distance of the rows of a (..., dim) tensor, which may be a view."""
+    if t.is_contiguous():
+        return t.shape[-1]
+    t = _rows(t)
+    return _view(t, name, dtype, t.shape, dev, 1)[0]
+
+
 def _norm_args(x, residual, weight, residual_out):
     dev = _gpu(x, "x")
+    dt, shape = x.dtype, x.shape
     code = rcode = _dtype_code(x)
-    x2 = _rows(x)
-    rows, dim = x2.shape
-    sx, = _view(x2, "x", x.dtype, (rows, dim), dev, 1)
-    r2, sr = None, 0
+    if not shape:
+        raise ValueError("the norm needs at least one dimension")
+    dim = shape[-1]
+    rows = x.numel() // dim if dim else 0
+    sx, sr = _row_stride(x, "x", dt, dev), 0
     if residual is not None:
-        _gpu(residual, "residual")
-        rcode = _residual_code(residual, x)
-        if residual.shape != x.shape:
+        if _gpu(residual, "residual") != dev:
+            raise ValueError(f"residual is on {residual.device}, expected {dev}")
+        if residual.dtype is not dt:
+            rcode = _residual_code(residual, x)
+        if residual.shape != shape:
             raise ValueError(f"residual has shape {tuple(residual.shape)}, expected "
-                             f"{tuple(x.shape)}")
-        r2 = _rows(residual)
-        sr, = _view(r2, "residual", residual.dtype, (rows, dim), dev, 1)
+                             f"{tuple(shape)}")
+        sr = _row_stride(residual, "residual", residual.dtype, dev)
         if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=dev)
+            residual_out = _new(residual)
         else:
-            _req(residual_out, "residual_out", residual.dtype, x.shape, dev)
+            _req(residual_out, "residual_out", residual.dtype, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     _req(weight, "weight", _F32, (dim,), dev)
-    return dev, code, rcode, x2, sx, r2, sr, rows, dim, residual_out
+    return dev, code, rcode, sx, sr, rows, dim, residual_out
 
 
 def residual_norm_fwd(x, residual=None, weight=None, *, eps=1e-5, out=None, residual_out=None):
@@ -263,13 +292,12 @@ def residual_norm_fwd(x, residual=None, weight=None, *, eps=1e-5, out=None, resi
     res is kept in it, and the norm is of what is kept.  Returns (out, res), out
     like x; without a residual res is x itself.  `residual_out`: a tensor to
     receive res, residual itself (dense) where the stream is carried in place."""
-    dev, code, rcode, x2, sx, r2, sr, rows, dim, kept = _norm_args(x, residual, weight,
-                                                                   residual_out)
+    dev, code, rcode, sx, sr, rows, dim, kept = _norm_args(x, residual, weight, residual_out)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = _new(x)
     else:
         _req(out, "out", x.dtype, x.shape, dev)
-    _call("mamba_residual_norm_fwd", dev, _ptr(x2), sx, _ptr(r2), sr, _ptr(weight), rows, dim,
+    _call("mamba_residual_norm_fwd", dev, _ptr(x), sx, _ptr(residual), sr, _ptr(weight), rows, dim,
           float(eps), code, rcode, _ptr(out), _ptr(kept))
     return out, x if kept is None else kept
 
@@ -279,17 +307,16 @@ def residual_norm_fp8(x, residual=None, weight=None, *, eps=1e-5, out=None, scal
     """residual_norm_fwd with out in 8 bits: returns (out, scale, res), out
     torch.float8_e4m3fn like x, scale float32 of x's shape without its last
     dimension, max|out| / 448 of each row; out stands for out * scale."""
-    dev, code, rcode, x2, sx, r2, sr, rows, dim, kept = _norm_args(x, residual, weight,
-                                                                   residual_out)
+    dev, code, rcode, sx, sr, rows, dim, kept = _norm_args(x, residual, weight, residual_out)
     if out is None:
-        out = torch.empty(x.shape, dtype=_FP8, device=dev)
+        out = _new(x, _FP8)
     else:
         _req(out, "out", _FP8, x.shape, dev)
     if scale is None:
         scale = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
     else:
         _req(scale, "scale", _F32, x.shape[:-1], dev)
-    _call("mamba_residual_norm_fp8", dev, _ptr(x2), sx, _ptr(r2), sr, _ptr(weight), rows, dim,
+    _call("mamba_residual_norm_fp8", dev, _ptr(x), sx, _ptr(residual), sr, _ptr(weight), rows, dim,
           float(eps), code, rcode, _ptr(out), _ptr(scale), _ptr(kept))
     return out, scale, x if kept is None else kept
 
@@ -303,19 +330,21 @@ def residual_norm_bwd(res, weight, dout, dres=None, *, eps=1e-5, workspace=None)
     dev = _gpu(res, "res")
     _gpu(dout, "dout")
     code, rcode = _dtype_code(dout), _residual_code(res, dout)
-    res2 = _rows(res)
-    rows, dim = res2.shape
-    sr, = _view(res2, "res", res.dtype, (rows, dim), dev, 1)
+    if not res.shape:
+        raise ValueError("the norm needs at least one dimension")
+    dim = res.shape[-1]
+    rows = res.numel() // dim if dim else 0
+    sr = _row_stride(res, "res", res.dtype, dev)
     _req(weight, "weight", _F32, (dim,), dev)
     _req(dout, "dout", dout.dtype, res.shape, dev)
     _req(dres, "dres", res.dtype, res.shape, dev)
-    g = dict(dx=torch.empty(res.shape, dtype=dout.dtype, device=dev))
-    g["dresidual"] = g["dx"] if code == rcode else torch.empty(res.shape, dtype=_F32, device=dev)
+    g = dict(dx=_new(dout))
+    g["dresidual"] = g["dx"] if code == rcode else _new(res)
     if weight is not None:
         g["dweight"] = torch.empty((dim,), dtype=_F32, device=dev)
-    n = lib().mamba_residual_norm_bwd_workspace_size(rows, dim)
+    n = _function("mamba_residual_norm_bwd_workspace_size")(rows, dim)
     ws = _workspace(n, (rows, dim), "mamba_residual_norm_bwd", workspace, dev)
-    _call("mamba_residual_norm_bwd", dev, _ptr(res2), sr, _ptr(weight), _ptr(dout), _ptr(dres),
+    _call("mamba_residual_norm_bwd", dev, _ptr(res), sr, _ptr(weight), _ptr(dout), _ptr(dres),
           rows, dim, float(eps), code, rcode, _ptr(g["dx"]),
           None if code == rcode else _ptr(g["dresidual"]), _ptr(g.get("dweight")), _ptr(ws), n)
     return g
