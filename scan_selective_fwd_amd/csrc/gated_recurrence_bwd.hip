@@ -6,21 +6,23 @@ namespace mscan {
 namespace {
 
 constexpr int S = (int)kRecBwdRun;
-constexpr int kMaxWaves = 16;
+constexpr int kMaxWaves = (int)(kRecBwdOneTile / kRecBwdRun);
+constexpr int kTileWaves = (int)(kRecBwdTile / kRecBwdRun);
 constexpr int kMarkWaves = (int)kRecTile / S;   // waves between checkpoints
 
 template <typename T, int V, bool Z, bool RESET, bool CHAIN>
-__global__ __launch_bounds__(1024) void rec_bwd_kernel(const RecParams p) {
+__global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void rec_bwd_kernel(const RecParams p) {
   constexpr int C = 64 * V;                       // channels of a strip
   constexpr int G = (int)kRecGroup;
-  __shared__ float sA[kMaxWaves][C], sH[kMaxWaves][C], sB[kMaxWaves][C];
-  __shared__ int sCut[kMaxWaves];
+  constexpr int W = CHAIN ? kTileWaves : kMaxWaves;
+  __shared__ float sA[W][C], sH[W][C], sB[W][C];
+  __shared__ int sCut[W];
   __shared__ uint64_t sMap[CHAIN ? G : 1][CHAIN ? C : 1];
   __shared__ float sHead[CHAIN ? C : 1];
   __shared__ uint32_t sTicket;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
+  const int waves = CHAIN ? kTileWaves : blockDim.x >> 6;
   const uint32_t strips = (uint32_t)((p.dim + C - 1) / C);
   const uint32_t across = strips * (uint32_t)p.batch;
   const uint32_t tiles = gridDim.x / across;
@@ -75,8 +77,13 @@ __global__ __launch_bounds__(1024) void rec_bwd_kernel(const RecParams p) {
 #pragma unroll
   for (int v = 0; v < V; ++v) A2[v] = p.A[cl + v] * kLog2e;
 
-  // the run's map of the states
+  // the run's map of the states, and what the gradients take of the gates: with g the
+  // gradient at a state and y the log of its decay
+  //   dx = g m s(i),  di = g u (1 - s(i)),  u = m s(i) x
+  //   d(log a) y = g a (y before - u a y / m^2),  dr of it times 1 - s(r)
+  // y / m^2 is -1/2 where the decay is 1, and u vanishes there
   float a[S][V], u[S][V], A[V], H[V];
+  float by_x[S][V], by_i[S][V], y[S][V], own[S][V], by_r[S][V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     A[v] = 1.0f;
@@ -89,7 +96,13 @@ __global__ __launch_bounds__(1024) void rec_bwd_kernel(const RecParams p) {
     for (int v = 0; v < V; ++v) {
       const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
       a[s][v] = g.a;
-      u[s][v] = rec_sqrt(g.m2) * (g.si * xr[s].get(v));
+      by_x[s][v] = rec_sqrt(g.m2) * g.si;
+      u[s][v] = by_x[s][v] * xr[s].get(v);
+      by_i[s][v] = u[s][v] * (1.0f - g.si);
+      y[s][v] = g.lg * kLn2;
+      const float ym = y[s][v] * fast_rcp(__builtin_fmaxf(g.m2, 1e-37f));
+      own[s][v] = u[s][v] * g.a * ym;
+      by_r[s][v] = 1.0f - g.sr;
       H[v] = rec_apply(g.a, u[s][v], cut, H[v]);
       A[v] *= g.a;
     }
@@ -185,34 +198,22 @@ __global__ __launch_bounds__(1024) void rec_bwd_kernel(const RecParams p) {
 #pragma unroll
   for (int v = 0; v < V; ++v) after[v] = rec_apply(Ab[v], Bb[v], cutb, after[v]);
 
-  // the gradients; the gates are formed again, which costs less than the registers
-  // that would keep them
   float sum[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) sum[v] = 0.0f;
 #pragma unroll
   for (int s = S - 1; s >= 0; --s) {
     const bool cut = RESET && (flags >> s & 1);
-    rr[s].w = (uint32_t)opaque_int((int)rr[s].w);
-    ir[s].w = (uint32_t)opaque_int((int)ir[s].w);
     float dx[V], dr[V], di[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float x = xr[s].get(v);
-      const RecGate g = rec_gate(rr[s].get(v), ir[s].get(v), A2[v]);
-      // 1 / m, finite where m is 0; y / m and m from it
-      const float rs = __builtin_amdgcn_rsqf(__builtin_fmaxf(g.m2, 1e-37f));
-      const float y = g.lg * kLn2, ix = g.si * x;
-      const float gh = dh[s][v] + after[v];
-      const float next = g.a * gh;
-      after[v] = cut ? 0.0f : next;
-      const float ah = g.a * u[s][v];
-      const float kept = cut ? 0.0f : ah * y;
-      const float e = gh * __builtin_fmaf(-ix * (y * rs), g.a * g.a, kept);
-      const float gm = gh * (g.m2 * rs) * g.si;
-      dx[v] = gm;
-      di[v] = gm * x * (1.0f - g.si);
-      dr[v] = e * (1.0f - g.sr);
+      const float g = dh[s][v] + after[v], ag = a[s][v] * g;
+      const float kept = __builtin_fmaf(y[s][v], u[s][v], -own[s][v]);
+      const float e = ag * (cut ? -own[s][v] : kept);
+      after[v] = cut ? 0.0f : ag;
+      dx[v] = g * by_x[s][v];
+      di[v] = g * by_i[s][v];
+      dr[v] = e * by_r[s][v];
       sum[v] += e;
     }
     if (on && s < n) {
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(256) void rec_sum_kernel(const RecParams p, const i
 template <typename T, int V, bool Z, bool RESET>
 hipError_t go(const RecParams& p, hipStream_t s) {
   const int64_t across = p.batch * rec_strips(p.dim, V == 2);
-  const int64_t tiles = (p.L + kRecBwdTile - 1) / kRecBwdTile, total = across * tiles;
+  const int64_t tiles = rec_bwd_tiles(p.L), total = across * tiles;
   hipError_t e;
   if (tiles == 1) {
     hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, false>), dim3((unsigned)across),
@@ -266,8 +267,8 @@ hipError_t go(const RecParams& p, hipStream_t s) {
   } else {
     e = rec_clear(p, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)total), dim3(1024),
-                       0, s, p);
+    hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)total),
+                       dim3(kTileWaves * 64), 0, s, p);
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -286,7 +287,7 @@ hipError_t by_form(const RecParams& p, hipStream_t s) {
 
 hipError_t dispatch_rec_bwd(const RecParams& p, int dtype, hipStream_t s) {
   if (dtype == 0) return by_form<float, 1>(p, s);
-  return p.pairs ? by_form<bf16_t, 2>(p, s) : by_form<bf16_t, 1>(p, s);
+  return by_form<bf16_t, 1>(p, s);
 }
 
 }  // namespace mscan

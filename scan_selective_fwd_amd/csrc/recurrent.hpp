@@ -46,8 +46,17 @@ constexpr int64_t kRecGroup = 16;
 
 // The backward: the same with runs of kRecBwdRun steps.
 constexpr int64_t kRecBwdRun = 8;
-constexpr int64_t kRecBwdTile = 16 * kRecBwdRun;
+constexpr int64_t kRecBwdOneTile = 16 * kRecBwdRun;
+constexpr int64_t kRecBwdTile = 8 * kRecBwdRun;
 static_assert(kRecBwdTile % kRecTile == 0 && kRecFwdTile % kRecTile == 0, "tiles between checkpoints");
+
+// Tiles of a sequence in either pass.
+constexpr int64_t rec_fwd_tiles(int64_t L) {
+  return L <= kRecOneTile ? 1 : (L + kRecFwdTile - 1) / kRecFwdTile;
+}
+constexpr int64_t rec_bwd_tiles(int64_t L) {
+  return L <= kRecBwdOneTile ? 1 : (L + kRecBwdTile - 1) / kRecBwdTile;
+}
 
 constexpr int kTicketWords = 32;
 

@@ -42,9 +42,6 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a && b && (p < q ? q - p < na : p - q < nb);
 }
 
-int64_t fwd_tiles(int64_t L) { return (L + mscan::kRecFwdTile - 1) / mscan::kRecFwdTile; }
-int64_t bwd_tiles(int64_t L) { return (L + mscan::kRecBwdTile - 1) / mscan::kRecBwdTile; }
-
 mamba_status check_shape(const mamba_recurrence_shape* s) {
   if (!s) return MAMBA_ERR_NULL_PTR;
   if (s->dtype != MAMBA_F32 && s->dtype != MAMBA_BF16) return MAMBA_ERR_DTYPE;
@@ -55,7 +52,7 @@ mamba_status check_shape(const mamba_recurrence_shape* s) {
     return MAMBA_ERR_SHAPE;
   if (s->dim > (int64_t)1 << 28 || s->seqlen > kLim / 64 / s->batch ||
       s->dim > kLim / 64 / (s->batch * s->seqlen) ||
-      s->batch > mscan::max_blocks(1024) / mscan::rec_strips(s->dim, false) / bwd_tiles(s->seqlen))
+      s->batch > mscan::max_blocks(1024) / mscan::rec_strips(s->dim, false) / mscan::rec_bwd_tiles(s->seqlen))
     return MAMBA_ERR_UNSUPPORTED;
   if (!span_ok(s->batch, s->x_batch_stride, s->seqlen, s->x_token_stride) ||
       !span_ok(s->batch, s->r_batch_stride, s->seqlen, s->r_token_stride) ||
@@ -135,11 +132,11 @@ ChainLayout chain_layout(const mamba_recurrence_shape* s, int64_t n) {
 }
 
 ChainLayout fwd_layout(const mamba_recurrence_shape* s) {
-  return chain_layout(s, s->seqlen <= mscan::kRecOneTile ? 1 : fwd_tiles(s->seqlen));
+  return chain_layout(s, mscan::rec_fwd_tiles(s->seqlen));
 }
 
 ChainLayout bwd_chain(const mamba_recurrence_shape* s) {
-  return chain_layout(s, bwd_tiles(s->seqlen));
+  return chain_layout(s, mscan::rec_bwd_tiles(s->seqlen));
 }
 
 void carve(mscan::RecParams* p, const ChainLayout& l, void* workspace) {
@@ -162,7 +159,7 @@ BwdLayout bwd_layout(const mamba_recurrence_shape* s, bool given) {
   BwdLayout l;
   l.chain = 0;
   l.part = up256(bwd_chain(s).total);
-  l.ckpt = l.part + up256(row * (size_t)bwd_tiles(s->seqlen));
+  l.ckpt = l.part + up256(row * (size_t)mscan::rec_bwd_tiles(s->seqlen));
   l.fwd = l.ckpt + (given ? 0 : up256(row * (size_t)tiles(s)));
   l.total = l.fwd + (given ? 0 : up256(fwd_layout(s).total));
   return l;
