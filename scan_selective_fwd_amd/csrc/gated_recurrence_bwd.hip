@@ -25,32 +25,35 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
   const int waves = CHAIN ? kTileWaves : blockDim.x >> 6;
   const uint32_t strips = (uint32_t)((p.dim + C - 1) / C);
   const uint32_t across = strips * (uint32_t)p.batch;
-  const uint32_t tiles = gridDim.x / across;
+  const uint32_t tiles = uniform(gridDim.x / across);
   const int64_t marks = (p.L + kRecTile - 1) / kRecTile;
-  const uint32_t at = blockIdx.x % across;
+  const uint32_t at = uniform(blockIdx.x % across);
   const uint32_t q = CHAIN ? rec_ticket(p.ticket, at, &sTicket) : 0;   // the last tile first
   const uint32_t tile = tiles - 1 - q;
-  const int64_t b = at / strips;
+  const int64_t b = uniform(at / strips);
   const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
   const bool on = c < p.dim;
-  const uint32_t cl = on ? c : 0;
+  const uint32_t cl = on ? c : 0, cb = cl * (uint32_t)sizeof(T);
   const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
   const int64_t left = p.L - t0;
-  const int n = left >= S ? S : left > 0 ? (int)left : 0;    // its steps
+  const int n = uniform(left >= S ? S : left > 0 ? (int)left : 0);   // its steps
 
   RecRaw<T, V> xr[S], rr[S], ir[S], yr[S], zr[Z ? S : 1];
-  auto row = [&](const Rows& q, int64_t t) {
-    return static_cast<const T*>(q.p) + b * q.batch + t * q.token;
-  };
-  const T* dout = static_cast<const T*>(p.dout) + b * p.L * p.dim;
+  const int64_t ts = n ? t0 : p.L - 1;
+  RecWalk<T> x(p.x, b, ts), r(p.r, b, ts), i(p.i, b, ts), z(p.z, b, ts),
+      dy({p.dout, p.L * p.dim, p.dim}, b, ts);
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    const int64_t t = t0 + s < p.L ? t0 + s : p.L - 1;
-    rr[s].load(row(p.r, t) + cl);
-    ir[s].load(row(p.i, t) + cl);
-    xr[s].load(row(p.x, t) + cl);
-    yr[s].load(dout + t * p.dim + cl);
-    if constexpr (Z) zr[s].load(row(p.z, t) + cl);
+    rr[s].load(r.p, cb);
+    ir[s].load(i.p, cb);
+    xr[s].load(x.p, cb);
+    yr[s].load(dy.p, cb);
+    if constexpr (Z) zr[s].load(z.p, cb);
+    r.next(s, n);
+    i.next(s, n);
+    x.next(s, n);
+    dy.next(s, n);
+    z.next(s, n);
   }
   // the state at the checkpoint before the run (a run past the end has none)
   float h[V];
@@ -124,26 +127,33 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
   // the states before each step (in the inputs' place), the gate on the output, and
   // the run's map of the gradient that comes to the state from later steps
   float dh[S][V], B[V];
+  const int64_t row = p.dim * (int64_t)sizeof(T), row0 = (b * p.L + t0) * row;
+  auto states = [&](const int steps) {
+    char* to = static_cast<char*>(p.dz) + row0;
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const bool cut = RESET && (flags >> s & 1);
-    float dz[V];
+    for (int s = 0; s < S; ++s) {
+      const bool cut = RESET && (flags >> s & 1);
+      float dz[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float before = h[v];
-      h[v] = rec_apply(a[s][v], u[s][v], cut, before);
-      u[s][v] = before;
-      dh[s][v] = yr[s].get(v);
+      for (int v = 0; v < V; ++v) {
+        const float before = h[v];
+        h[v] = rec_apply(a[s][v], u[s][v], cut, before);
+        u[s][v] = before;
+        dh[s][v] = yr[s].get(v);
+        if constexpr (Z) {
+          const float z = zr[s].get(v), sz = sigmoid(z);
+          dz[v] = dh[s][v] * h[v] * (sz * __builtin_fmaf(z, 1.0f - sz, 1.0f));
+          dh[s][v] *= z * sz;
+        }
+      }
       if constexpr (Z) {
-        const float z = zr[s].get(v), sz = sigmoid(z);
-        dz[v] = dh[s][v] * h[v] * (sz * __builtin_fmaf(z, 1.0f - sz, 1.0f));
-        dh[s][v] *= z * sz;
+        if (on && s < steps) rec_store<T, V>(to, cb, dz);
+        to += row;
       }
     }
-    if constexpr (Z)
-      if (on && s < n)
-        rec_store<T, V>(static_cast<T*>(p.dz) + (b * p.L + t0 + s) * p.dim + c, dz);
-  }
+  };
+  if (n == S) states(S);
+  else states(n);
 #pragma unroll
   for (int v = 0; v < V; ++v) B[v] = 0.0f;
 #pragma unroll
@@ -201,27 +211,38 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
   float sum[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+  auto grads = [&](const int steps) {
+    char* dx_to = static_cast<char*>(p.dx) + row0 + (S - 1) * row;
+    char* dr_to = static_cast<char*>(p.dr) + row0 + (S - 1) * row;
+    char* di_to = static_cast<char*>(p.di) + row0 + (S - 1) * row;
 #pragma unroll
-  for (int s = S - 1; s >= 0; --s) {
-    const bool cut = RESET && (flags >> s & 1);
-    float dx[V], dr[V], di[V];
+    for (int s = S - 1; s >= 0; --s) {
+      const bool cut = RESET && (flags >> s & 1);
+      float dx[V], dr[V], di[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float g = dh[s][v] + after[v], ag = a[s][v] * g;
-      const float kept = __builtin_fmaf(y[s][v], u[s][v], -own[s][v]);
-      const float e = ag * (cut ? -own[s][v] : kept);
-      after[v] = cut ? 0.0f : ag;
-      dx[v] = g * by_x[s][v];
-      di[v] = g * by_i[s][v];
-      dr[v] = e * by_r[s][v];
-      sum[v] += e;
+      for (int v = 0; v < V; ++v) {
+        const float g = dh[s][v] + after[v], ag = a[s][v] * g;
+        const float kept = __builtin_fmaf(y[s][v], u[s][v], -own[s][v]);
+        const float e = ag * (cut ? -own[s][v] : kept);
+        after[v] = cut ? 0.0f : ag;
+        dx[v] = g * by_x[s][v];
+        di[v] = g * by_i[s][v];
+        dr[v] = e * by_r[s][v];
+        sum[v] += e;
+      }
+      if (s < steps) {
+        rec_store<T, V>(dx_to, cb, dx);
+        rec_store<T, V>(dr_to, cb, dr);
+        rec_store<T, V>(di_to, cb, di);
+      }
+      dx_to -= row;
+      dr_to -= row;
+      di_to -= row;
     }
-    if (on && s < n) {
-      const int64_t o = (b * p.L + t0 + s) * p.dim;
-      rec_store<T, V>(static_cast<T*>(p.dx) + o + c, dx);
-      rec_store<T, V>(static_cast<T*>(p.dr) + o + c, dr);
-      rec_store<T, V>(static_cast<T*>(p.di) + o + c, di);
-    }
+  };
+  if (on) {
+    if (n == S) grads(S);
+    else grads(n);
   }
   if (t0 == 0 && p.dh0 && on)
 #pragma unroll

@@ -26,29 +26,30 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64) void rec_
   const uint32_t across = strips * (uint32_t)p.batch;
   const int64_t marks = (p.L + kRecTile - 1) / kRecTile;
 
-  const uint32_t at = blockIdx.x % across;
+  const uint32_t at = uniform(blockIdx.x % across);
   const uint32_t tile = CHAIN ? rec_ticket(p.ticket, at, &sTicket) : 0;
-  const int64_t b = at / strips;
+  const int64_t b = uniform(at / strips);
   const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
   const bool on = c < p.dim;
-  const uint32_t cl = on ? c : 0;
+  const uint32_t cl = on ? c : 0, cb = cl * (uint32_t)sizeof(T);
   const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
   const int64_t left = p.L - t0;
-  const int n = left >= S ? S : left > 0 ? (int)left : 0;    // its steps
+  const int n = uniform(left >= S ? S : left > 0 ? (int)left : 0);   // its steps
 
-  // every load of the run is in flight at once; steps past the end read the last.  A
-  // row's address is the same in every lane, a lane's place in it 32 bits.
+  // every load of the run is in flight at once
   RecRaw<T, V> xr[S], rr[S], ir[S], zr[Z ? S : 1];
-  auto row = [&](const Rows& q, int64_t t) {
-    return static_cast<const T*>(q.p) + b * q.batch + t * q.token;
-  };
+  const int64_t ts = n ? t0 : p.L - 1;
+  RecWalk<T> x(p.x, b, ts), r(p.r, b, ts), i(p.i, b, ts), z(p.z, b, ts);
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    const int64_t t = t0 + s < p.L ? t0 + s : p.L - 1;
-    rr[s].load(row(p.r, t) + cl);
-    ir[s].load(row(p.i, t) + cl);
-    xr[s].load(row(p.x, t) + cl);
-    if constexpr (Z) zr[s].load(row(p.z, t) + cl);
+    rr[s].load(r.p, cb);
+    ir[s].load(i.p, cb);
+    xr[s].load(x.p, cb);
+    if constexpr (Z) zr[s].load(z.p, cb);
+    r.next(s, n);
+    i.next(s, n);
+    x.next(s, n);
+    z.next(s, n);
   }
   if (n < S) {                                               // those leave the state
 #pragma unroll
@@ -141,8 +142,9 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64) void rec_
   if (p.ckpt && on && t0 % kRecTile == 0 && n)
 #pragma unroll
     for (int v = 0; v < V; ++v) p.ckpt[(b * marks + t0 / kRecTile) * p.dim + c + v] = h[v];
-  if (p.out || p.last) {
-    T* out = static_cast<T*>(p.out) + (b * p.L + t0) * p.dim;
+  if (!on || !(p.out || p.last)) return;
+  char* out = static_cast<char*>(p.out) + (b * p.L + t0) * p.dim * (int64_t)sizeof(T);
+  auto outputs = [&](const int steps) {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const bool cut = RESET && (flags >> s & 1);
@@ -152,12 +154,15 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64) void rec_
         h[v] = rec_apply(a[s][v], u[s][v], cut, h[v]);
         y[v] = Z ? h[v] * silu(zr[Z ? s : 0].get(v)) : h[v];
       }
-      if (p.out && on && s < n) rec_store<T, V>(out + s * p.dim + c, y);
+      if (s < steps) rec_store<T, V>(out, cb, y);
+      out += p.dim * (int64_t)sizeof(T);
     }
-    if (p.last && on && left > 0 && left <= S)
+  };
+  if (n == S && p.out) outputs(S);
+  else outputs(p.out ? n : 0);
+  if (p.last && left > 0 && left <= S)
 #pragma unroll
-      for (int v = 0; v < V; ++v) p.last[b * p.dim + c + v] = h[v];
-  }
+    for (int v = 0; v < V; ++v) p.last[b * p.dim + c + v] = h[v];
 }
 
 template <typename T, int V, bool Z, bool RESET>

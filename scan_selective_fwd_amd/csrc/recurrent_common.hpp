@@ -49,15 +49,25 @@ __device__ __forceinline__ RecGate rec_gate(float r, float i, float A2) {
   return g;
 }
 
+// A value that is the same in every lane, but was formed where lanes have their own
+// (quotients are): from here on it is kept, and what is made of it formed, once a wave.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // V channels of one token as they lie in memory: two bfloat16, or one element.
 template <typename T, int V>
 struct RecRaw {
   static_assert(V == 1 || (V == 2 && sizeof(T) == 2), "V");
   uint32_t w;
-  __device__ __forceinline__ void load(const T* q) {
+  // The row's address is the same in every lane, the lane's place in it 32 bits: then
+  // the sum is formed by the load itself.
+  __device__ __forceinline__ void load(const char* row, uint32_t at) {
+    const char* q = row + at;
     if constexpr (V == 2) w = *reinterpret_cast<const uint32_t*>(q);
-    else if constexpr (sizeof(T) == 2) w = *q;
-    else w = __float_as_uint(*q);
+    else if constexpr (sizeof(T) == 2) w = *reinterpret_cast<const T*>(q);
+    else w = __float_as_uint(*reinterpret_cast<const T*>(q));
   }
   __device__ __forceinline__ void fill(float v) {   // a value that bfloat16 holds
     w = __float_as_uint(v);
@@ -70,10 +80,23 @@ struct RecRaw {
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void rec_store(T* q, const float (&y)[V]) {
+__device__ __forceinline__ void rec_store(char* row, uint32_t at, const float (&y)[V]) {
+  char* q = row + at;
   if constexpr (V == 2) *reinterpret_cast<uint32_t*>(q) = pack_bf16(y[0], y[1]);
-  else store_vec<T, 1>(q, 0, y);
+  else if constexpr (sizeof(T) == 2) *reinterpret_cast<T*>(q) = (T)pack_bf16(y[0], y[0]);
+  else *reinterpret_cast<T*>(q) = y[0];
 }
+
+// The rows of a run of n steps, one after another; behind the last it stays there.
+template <typename T>
+struct RecWalk {
+  const char* p;
+  int64_t step;
+  __device__ __forceinline__ RecWalk(const Rows& q, int64_t b, int64_t t)
+      : p(static_cast<const char*>(q.p) + (b * q.batch + t * q.token) * (int64_t)sizeof(T)),
+        step(q.token * (int64_t)sizeof(T)) {}
+  __device__ __forceinline__ void next(int s, int n) { p += s + 1 < n ? step : 0; }
+};
 
 // The affine map h -> A h + H of a run of steps; `cut`: a flag in it leaves h out
 // whatever it holds.
