@@ -18,26 +18,27 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
   __shared__ float sA[W][C], sH[W][C], sB[W][C];
   __shared__ int sCut[W];
   __shared__ uint64_t sMap[CHAIN ? G : 1][CHAIN ? C : 1];
-  __shared__ float sHead[CHAIN ? C : 1];
   __shared__ uint32_t sTicket;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = CHAIN ? kTileWaves : blockDim.x >> 6;
   const uint32_t strips = (uint32_t)((p.dim + C - 1) / C);
   const uint32_t across = strips * (uint32_t)p.batch;
-  const uint32_t tiles = uniform(gridDim.x / across);
+  const uint32_t tiles = CHAIN ? (uint32_t)((p.L + kRecBwdTile - 1) / kRecBwdTile) : 1;
   const int64_t marks = (p.L + kRecTile - 1) / kRecTile;
-  const uint32_t at = uniform(blockIdx.x % across);
-  const uint32_t q = CHAIN ? rec_ticket(p.ticket, at, &sTicket) : 0;   // the last tile first
-  const uint32_t tile = tiles - 1 - q;
+  const uint32_t at = rec_strip(across, p.by_die);
+  if (at >= across) return;
+  const uint32_t q = CHAIN ? rec_ticket(p.ticket, at, &sTicket) : 0;
+  const uint32_t tile = tiles - 1 - q;                        // the last tile first
   const int64_t b = uniform(at / strips);
   const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
   const bool on = c < p.dim;
   const uint32_t cl = on ? c : 0, cb = cl * (uint32_t)sizeof(T);
-  const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
+  const int64_t t0 = ((int64_t)tile * waves + wave) * S;      // the wave's first step
   const int64_t left = p.L - t0;
   const int n = uniform(left >= S ? S : left > 0 ? (int)left : 0);   // its steps
 
+  // every load of the run is in flight at once
   RecRaw<T, V> xr[S], rr[S], ir[S], yr[S], zr[Z ? S : 1];
   const int64_t ts = n ? t0 : p.L - 1;
   RecWalk<T> x(p.x, b, ts), r(p.r, b, ts), i(p.i, b, ts), z(p.z, b, ts),
@@ -201,9 +202,9 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
   }
   if constexpr (CHAIN) {
     const uint32_t groups = (tiles + G - 1) / G;
-    rec_chain<V, G>(p.maps + ((uint64_t)b * tiles + q) * p.dim + cl,
+    rec_chain<V, G, kTileWaves>(p.maps + ((uint64_t)b * tiles + q) * p.dim + cl,
                     p.heads + ((uint64_t)b * groups + q / G) * p.dim + cl, p.dim, q, At, Bt, cutt,
-                    on, wave, waves, lane, sMap, sHead, after);
+                    on, wave, lane, sMap, after);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) after[v] = rec_apply(Ab[v], Bb[v], cutb, after[v]);
@@ -278,17 +279,17 @@ __global__ __launch_bounds__(256) void rec_sum_kernel(const RecParams p, const i
 }
 
 template <typename T, int V, bool Z, bool RESET>
-hipError_t go(const RecParams& p, hipStream_t s) {
-  const int64_t across = p.batch * rec_strips(p.dim, V == 2);
-  const int64_t tiles = rec_bwd_tiles(p.L), total = across * tiles;
+hipError_t go(RecParams p, hipStream_t s) {
+  const int64_t tiles = rec_bwd_tiles(p.L);
+  const int64_t grid = rec_grid(&p, p.batch * rec_strips(p.dim, V == 2), tiles, sizeof(T));
   hipError_t e;
-  if (tiles == 1) {
-    hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, false>), dim3((unsigned)across),
+  if (!p.ticket) {
+    hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, false>), dim3((unsigned)grid),
                        dim3((unsigned)((p.L + S - 1) / S * 64)), 0, s, p);
   } else {
     e = rec_clear(p, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)total),
+    hipLaunchKernelGGL((rec_bwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)grid),
                        dim3(kTileWaves * 64), 0, s, p);
   }
   e = hipGetLastError();
@@ -298,17 +299,17 @@ hipError_t go(const RecParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int V>
+// Single elements: pairs would take more registers than let two blocks share a CU.
+template <typename T>
 hipError_t by_form(const RecParams& p, hipStream_t s) {
-  if (p.reset) return p.z.p ? go<T, V, true, true>(p, s) : go<T, V, false, true>(p, s);
-  return p.z.p ? go<T, V, true, false>(p, s) : go<T, V, false, false>(p, s);
+  if (p.reset) return p.z.p ? go<T, 1, true, true>(p, s) : go<T, 1, false, true>(p, s);
+  return p.z.p ? go<T, 1, true, false>(p, s) : go<T, 1, false, false>(p, s);
 }
 
 }  // namespace
 
 hipError_t dispatch_rec_bwd(const RecParams& p, int dtype, hipStream_t s) {
-  if (dtype == 0) return by_form<float, 1>(p, s);
-  return by_form<bf16_t, 1>(p, s);
+  return dtype == 0 ? by_form<float>(p, s) : by_form<bf16_t>(p, s);
 }
 
 }  // namespace mscan

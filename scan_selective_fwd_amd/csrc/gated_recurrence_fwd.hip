@@ -10,14 +10,14 @@ constexpr int kMaxWaves = (int)(kRecOneTile / kRecRun);
 constexpr int kTileWaves = (int)(kRecFwdTile / kRecRun);
 
 template <typename T, int V, bool Z, bool RESET, bool CHAIN>
-__global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64) void rec_fwd_kernel(const RecParams p) {
+__global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void rec_fwd_kernel(
+    const RecParams p) {
   constexpr int C = 64 * V;                       // channels of a strip
   constexpr int G = (int)kRecGroup;
   constexpr int W = CHAIN ? kTileWaves : kMaxWaves;
   __shared__ float sA[W][C], sH[W][C];
   __shared__ int sCut[W];
   __shared__ uint64_t sMap[CHAIN ? G : 1][CHAIN ? C : 1];
-  __shared__ float sHead[CHAIN ? C : 1];
   __shared__ uint32_t sTicket;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -26,13 +26,14 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64) void rec_
   const uint32_t across = strips * (uint32_t)p.batch;
   const int64_t marks = (p.L + kRecTile - 1) / kRecTile;
 
-  const uint32_t at = uniform(blockIdx.x % across);
+  const uint32_t at = rec_strip(across, p.by_die);
+  if (at >= across) return;
   const uint32_t tile = CHAIN ? rec_ticket(p.ticket, at, &sTicket) : 0;
   const int64_t b = uniform(at / strips);
   const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
   const bool on = c < p.dim;
   const uint32_t cl = on ? c : 0, cb = cl * (uint32_t)sizeof(T);
-  const int64_t t0 = ((int64_t)tile * waves + wave) * S;     // the wave's first step
+  const int64_t t0 = ((int64_t)tile * waves + wave) * S;      // the wave's first step
   const int64_t left = p.L - t0;
   const int n = uniform(left >= S ? S : left > 0 ? (int)left : 0);   // its steps
 
@@ -132,9 +133,9 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64) void rec_
   if constexpr (CHAIN) {
     const uint32_t tiles = (uint32_t)((p.L + kRecFwdTile - 1) / kRecFwdTile);
     const uint32_t groups = (tiles + G - 1) / G;
-    rec_chain<V, G>(p.maps + ((uint64_t)b * tiles + tile) * p.dim + cl,
+    rec_chain<V, G, kTileWaves>(p.maps + ((uint64_t)b * tiles + tile) * p.dim + cl,
                     p.heads + ((uint64_t)b * groups + tile / G) * p.dim + cl, p.dim, tile, At, Ht,
-                    cutt, on, wave, waves, lane, sMap, sHead, h);
+                    cutt, on, wave, lane, sMap, h);
   }
   // and the wave's run
 #pragma unroll
@@ -166,18 +167,16 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64) void rec_
 }
 
 template <typename T, int V, bool Z, bool RESET>
-hipError_t go(const RecParams& p, hipStream_t s) {
-  const int64_t across = p.batch * rec_strips(p.dim, V == 2);
+hipError_t go(RecParams p, hipStream_t s) {
+  const int64_t grid = rec_grid(&p, p.batch * rec_strips(p.dim, V == 2), rec_fwd_tiles(p.L), sizeof(T));
   if (!p.ticket) {
-    const int waves = (int)((p.L + S - 1) / S);
-    hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, false>), dim3((unsigned)across), dim3(64 * waves),
-                       0, s, p);
+    hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, false>), dim3((unsigned)grid),
+                       dim3((unsigned)((p.L + S - 1) / S * 64)), 0, s, p);
     return hipGetLastError();
   }
-  const int64_t total = across * ((p.L + kRecFwdTile - 1) / kRecFwdTile);
   const hipError_t e = rec_clear(p, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)total),
+  hipLaunchKernelGGL((rec_fwd_kernel<T, V, Z, RESET, true>), dim3((unsigned)grid),
                      dim3(kTileWaves * 64), 0, s, p);
   return hipGetLastError();
 }

@@ -22,6 +22,7 @@ struct RecParams {
   uint64_t* maps;        // (batch, tiles, dim): the tiles' maps
   uint64_t* heads;       // (batch, groups of tiles, dim): the state after each group
   int64_t words;         // of ticket, maps and heads together, in 64 bits: cleared first
+  uint32_t by_die;       // strips that a die takes one after another; 0: in turn
   // backward
   const void* dout;
   const float* dlast;    // nullable
@@ -62,6 +63,17 @@ constexpr int kTicketWords = 32;
 
 constexpr int64_t rec_strips(int64_t dim, bool pairs) {
   return pairs ? (dim + 127) / 128 : (dim + 63) / 64;
+}
+
+// Blocks go to the chip's eight dies in turn.  Neighbouring strips share the cache lines
+// between them where rows do not start on one, and then go to the same die, as long as
+// that leaves no die without work (backward of 8 x 2048 x 1538 187 -> 120 us, forward 66 ->
+// 56, bfloat16).  Returns the blocks of a launch over `tiles` tiles of `across` strips.
+inline int64_t rec_grid(RecParams* p, int64_t across, int64_t tiles, int es) {
+  const bool apart = p->dim * es % 128 == 0;
+  const bool by_die = across % 8 == 0 || (!apart && across >= 32);
+  p->by_die = by_die ? (uint32_t)((across + 7) / 8) : 0;
+  return (by_die ? 8 * (int64_t)p->by_die : across) * tiles;
 }
 
 hipError_t rec_clear(const RecParams& p, hipStream_t s);

@@ -52,7 +52,8 @@ mamba_status check_shape(const mamba_recurrence_shape* s) {
     return MAMBA_ERR_SHAPE;
   if (s->dim > (int64_t)1 << 28 || s->seqlen > kLim / 64 / s->batch ||
       s->dim > kLim / 64 / (s->batch * s->seqlen) ||
-      s->batch > mscan::max_blocks(1024) / mscan::rec_strips(s->dim, false) / mscan::rec_bwd_tiles(s->seqlen))
+      s->batch > mscan::max_blocks(1024) / 2 / mscan::rec_strips(s->dim, false) /
+                     mscan::rec_bwd_tiles(s->seqlen))   // some blocks may have no strip
     return MAMBA_ERR_UNSUPPORTED;
   if (!span_ok(s->batch, s->x_batch_stride, s->seqlen, s->x_token_stride) ||
       !span_ok(s->batch, s->r_batch_stride, s->seqlen, s->r_token_stride) ||
@@ -103,13 +104,16 @@ mscan::RecParams common(const mamba_recurrence_shape* s, const void* x, const vo
   return p;
 }
 
-// Whether bfloat16 rows can be taken in pairs.
+// Whether bfloat16 rows can be taken in pairs.  One tile a row on few blocks is bound by
+// the work of each, and takes single elements.
 bool pairs(const mamba_recurrence_shape* s, const void* x, const void* r, const void* i,
            const void* z) {
   auto ok = [](const void* p, int64_t sb, int64_t st) {
     return aligned(p, 4) && sb % 2 == 0 && st % 2 == 0;
   };
-  return s->dtype == MAMBA_BF16 && s->dim % 2 == 0 && ok(x, s->x_batch_stride, s->x_token_stride) &&
+  const bool few = s->seqlen <= mscan::kRecOneTile && s->batch * mscan::rec_strips(s->dim, true) < 256;
+  return s->dtype == MAMBA_BF16 && !few && s->dim % 2 == 0 &&
+         ok(x, s->x_batch_stride, s->x_token_stride) &&
          ok(r, s->r_batch_stride, s->r_token_stride) &&
          ok(i, s->i_batch_stride, s->i_token_stride) &&
          (!z || ok(z, s->z_batch_stride, s->z_token_stride));
@@ -304,8 +308,6 @@ mamba_status mamba_gated_recurrence_bwd(const mamba_recurrence_shape* shape, con
     p.kept = f.ckpt;
   }
   carve(&p, bwd_chain(shape), ws + l.chain);
-  p.pairs = pairs(shape, x, r, i, z) && aligned(dout, 4) && aligned(dx, 4) && aligned(dr, 4) &&
-            aligned(di, 4) && aligned(dz, 4);
   return hip_status(mscan::dispatch_rec_bwd(p, shape->dtype == MAMBA_F32 ? 0 : 1,
                                             as_stream(stream)));
 }

@@ -79,12 +79,15 @@ struct RecRaw {
   }
 };
 
+// Outputs pass by the second-level cache (backward of 2 x 2048 x 5120 with its gate 104 ->
+// 102 us, forward 57 -> 53).  Inputs do not: that gains 5 % where they come from memory and
+// loses up to 27 % where they are in the last-level cache.
 template <typename T, int V>
 __device__ __forceinline__ void rec_store(char* row, uint32_t at, const float (&y)[V]) {
   char* q = row + at;
-  if constexpr (V == 2) *reinterpret_cast<uint32_t*>(q) = pack_bf16(y[0], y[1]);
-  else if constexpr (sizeof(T) == 2) *reinterpret_cast<T*>(q) = (T)pack_bf16(y[0], y[0]);
-  else *reinterpret_cast<T*>(q) = y[0];
+  if constexpr (V == 2) __builtin_nontemporal_store(pack_bf16(y[0], y[1]), reinterpret_cast<uint32_t*>(q));
+  else if constexpr (sizeof(T) == 2) __builtin_nontemporal_store((T)pack_bf16(y[0], y[0]), reinterpret_cast<T*>(q));
+  else __builtin_nontemporal_store((T)y[0], reinterpret_cast<T*>(q));
 }
 
 // The rows of a run of n steps, one after another; behind the last it stays there.
@@ -118,88 +121,93 @@ __device__ __forceinline__ void rec_publish(uint64_t* p, uint64_t v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Waits for the word at p.  Who writes it took an earlier ticket, so it runs already
-// and waits only for earlier tickets itself: the wait ends.
-__device__ __forceinline__ uint64_t rec_wait(uint64_t* p) {
-  uint64_t v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ uint64_t rec_look(uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Waits for the word at p, v what was seen there.  Who writes it took an earlier ticket,
+// so it runs already and waits only for earlier tickets itself: the wait ends.
+__device__ __forceinline__ uint64_t rec_wait(uint64_t* p, uint64_t v) {
   while (!(v >> 63)) {
     __builtin_amdgcn_s_sleep(1);
-    v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    v = rec_look(p);
   }
   return v;
 }
 
-// The value that enters tile q (counted in the order of the tickets) of a row: the
-// maps of its group's earlier tiles joined, then the value behind the group before.
+// The value that enters tile q (counted in the order of the tickets) of a row: that
+// behind the group before, and the maps of its group's earlier tiles.
 // Publishes the tile's own map (At, Ht, cutt), or for the last of a group the value
 // behind it.  h: in, what enters tile 0; out, what enters this one.  The order of
 // the products does not depend on who was first, so equal inputs give equal bits.
-// maps, heads: this tile's and its group's words; `on`: whether the lane's channels exist.
-template <int V, int G>
+// maps, heads: this tile's and its group's words; `on`: whether the lane's channels exist;
+// W: the block's waves.
+template <int V, int G, int W>
 __device__ __forceinline__ void rec_chain(uint64_t* maps, uint64_t* heads, int64_t dim, uint32_t q,
                                           const float (&At)[V], const float (&Ht)[V], bool cutt,
-                                          bool on, int wave, int waves, int lane,
-                                          uint64_t (*sMap)[64 * V], float* sHead, float (&h)[V]) {
+                                          bool on, int wave, int lane, uint64_t (*sMap)[64 * V],
+                                          float (&h)[V]) {
+  static_assert(G <= 2 * W, "a wave fetches two words at most");
   const int j = q % G;
   const bool later = q >= G;
   if (wave == 0 && on && j != G - 1) {
 #pragma unroll
     for (int v = 0; v < V; ++v) rec_publish(maps + v, rec_pack(At[v], Ht[v], cutt));
   }
-  for (int k = wave; k < j; k += waves)
+  // word k < j is the map of the group's tile k, word j the value behind the group before;
+  // all are asked for at once
+  const int items = later ? j + 1 : j;
+  uint64_t m[2][V];
+  uint64_t* from[2];
 #pragma unroll
-    for (int v = 0; v < V; ++v) sMap[k][lane * V + v] = rec_wait(maps - (int64_t)(j - k) * dim + v);
-  __syncthreads();
-  float A[V], H[V];
-  bool cut[V];
+  for (int e = 0; e < 2; ++e) {
+    const int k = wave + e * W;
+    from[e] = k < j ? maps - (int64_t)(j - k) * dim : heads - dim;
+    if (k < items)
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    A[v] = 1.0f;
-    H[v] = 0.0f;
-    cut[v] = false;
+      for (int v = 0; v < V; ++v) m[e][v] = rec_look(from[e] + v);
   }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int k = wave + e * W;
+    if (k < items)
+#pragma unroll
+      for (int v = 0; v < V; ++v) sMap[k][lane * V + v] = rec_wait(from[e] + v, m[e][v]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (later) h[v] = __uint_as_float((uint32_t)sMap[j][lane * V + v]);
   for (int k = 0; k < j; ++k)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const uint64_t m = sMap[k][lane * V + v];
-      const uint32_t hi = (uint32_t)(m >> 32) & ~kThere;
-      const bool c = hi == kCutBits;
-      H[v] = rec_apply(__uint_as_float(hi), __uint_as_float((uint32_t)m), c, H[v]);
-      cut[v] = cut[v] || c;
-      A[v] *= c ? 1.0f : __uint_as_float(hi);
+      const uint64_t w = sMap[k][lane * V + v];
+      const uint32_t hi = (uint32_t)(w >> 32) & ~kThere;
+      h[v] = rec_apply(__uint_as_float(hi), __uint_as_float((uint32_t)w), hi == kCutBits, h[v]);
     }
-  if (later) {
-    // joined before the wait: the next group waits for two products after this one
-    if (wave == 0)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[v] = __uint_as_float((uint32_t)rec_wait(heads - dim + v));
-        sHead[lane * V + v] = h[v] = rec_apply(A[v], H[v], cut[v], h[v]);
-      }
-  } else if (j) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = H[v];
-  }
   if (j == G - 1 && wave == 0 && on)
 #pragma unroll
     for (int v = 0; v < V; ++v)
       rec_publish(heads + v, rec_pack(0.0f, rec_apply(At[v], Ht[v], cutt, h[v]), false));
-  if (later) {
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = sHead[lane * V + v];
-  }
 }
 
-// The next tile of a strip: the first block to come takes its first, and so on.  Each
-// strip counts for itself, on a cache line of its own.
+// The strip of a block; one past the last for the few blocks that have none.
+__device__ __forceinline__ uint32_t rec_strip(uint32_t across, uint32_t by_die) {
+  if (!by_die) return uniform(blockIdx.x % across);
+  const uint32_t at = uniform(blockIdx.x % (8 * by_die));
+  return at % 8 * by_die + at / 8;
+}
+
+// The tile of a block, by the tickets of its strip: who comes first takes the first, and
+// so on.  Each strip counts for itself, on a cache line of its own (with one counter for
+// all a tile took 27 to 40 ns of it).
 __device__ __forceinline__ uint32_t rec_ticket(uint32_t* tickets, uint32_t strip,
                                                uint32_t* sTicket) {
   if (threadIdx.x == 0)
     *sTicket = __hip_atomic_fetch_add(tickets + (size_t)strip * kTicketWords, 1u, __ATOMIC_RELAXED,
                                       __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(*sTicket);
+  return uniform(*sTicket);
 }
 
 }  // namespace mscan
