@@ -695,34 +695,39 @@ mamba_status mamba_gated_recurrence_update(const mamba_recurrence_shape* shape, 
                                            const void* z, void* out, void* stream);
 
 /* ------------------------------------------------------------------------
- * Root-mean-square norm of rows (rows, dim) with the residual's addition, the
+ * Root-mean-square norm of rows (batch, rows, dim) with the residual's addition, the
  * stage that opens a block:
  *
  *   res = x + residual          (rounded once to residual_dt; x without residual)
  *   out = res / sqrt(mean(res^2) + eps) * weight
  *
  * x and out in dt; residual and residual_out in residual_dt: dt or MAMBA_F32.
- * The norm is of res as it is kept.  x and residual may be views (row strides in
- * elements); residual_out, out and the gradients are dense.  weight (nullable
- * = 1) and dweight (dim) float32.  Without residual there is no residual_out.
- * residual_out may be residual itself where that is dense (the stream is
- * carried on in place); no other output may overlap an input. */
-mamba_status mamba_residual_norm_fwd(const void* x, int64_t x_row_stride, const void* residual,
+ * The norm is of res as it is kept.  x and residual may be views (batch and row
+ * strides in elements, >= 0; a row's elements are contiguous); residual_out, out
+ * and the gradients are dense.  weight (nullable = 1) and dweight (dim) float32.
+ * Without residual there is no residual_out.  residual_out may be residual itself
+ * where that is dense (the stream is carried on in place); no other output may
+ * overlap an input. */
+mamba_status mamba_residual_norm_fwd(const void* x, int64_t x_batch_stride, int64_t x_row_stride,
+                                     const void* residual, int64_t residual_batch_stride,
                                      int64_t residual_row_stride, const float* weight,
-                                     int64_t rows, int64_t dim, float eps, mamba_dtype dt,
-                                     mamba_dtype residual_dt, void* out, void* residual_out,
-                                     void* stream);
+                                     int64_t batch, int64_t rows, int64_t dim, float eps,
+                                     mamba_dtype dt, mamba_dtype residual_dt, void* out,
+                                     void* residual_out, void* stream);
 
 /* The same with out in 8 bits, e4m3 (4 exponent bits, 3 mantissa bits, largest
  * value 448, no infinities), and a float32 scale a row:
  *   scale = max(max|out|, 2^-100) / 448, the maximum over values that are not NaN,
  *   out8 = out / scale, to the nearest, ties to even; a NaN stays one. */
-mamba_status mamba_residual_norm_fp8(const void* x, int64_t x_row_stride, const void* residual,
+mamba_status mamba_residual_norm_fp8(const void* x, int64_t x_batch_stride, int64_t x_row_stride,
+                                     const void* residual, int64_t residual_batch_stride,
                                      int64_t residual_row_stride, const float* weight,
-                                     int64_t rows, int64_t dim, float eps, mamba_dtype dt,
-                                     mamba_dtype residual_dt, uint8_t* out8, float* scale,
-                                     void* residual_out, void* stream);
+                                     int64_t batch, int64_t rows, int64_t dim, float eps,
+                                     mamba_dtype dt, mamba_dtype residual_dt, uint8_t* out8,
+                                     float* scale, void* residual_out, void* stream);
 
+/* Bytes of device workspace of the backward over so many rows in all (SIZE_MAX if
+ * unsupported). */
 size_t mamba_residual_norm_bwd_workspace_size(int64_t rows, int64_t dim);
 
 /* Backward, from res as the forward kept it (residual_dt; a view may be given):
@@ -733,8 +738,9 @@ size_t mamba_residual_norm_bwd_workspace_size(int64_t rows, int64_t dim);
  * dx in dt.  dresidual (nullable) in residual_dt; refused where residual_dt is
  * dt (it is dx).  dweight is required with weight.  The row statistics are
  * formed again; sums run in a fixed order. */
-mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_row_stride,
-                                     const float* weight, const void* dout, const void* dres,
+mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_batch_stride,
+                                     int64_t res_row_stride, const float* weight,
+                                     const void* dout, const void* dres, int64_t batch,
                                      int64_t rows, int64_t dim, float eps, mamba_dtype dt,
                                      mamba_dtype residual_dt, void* dx, void* dresidual,
                                      float* dweight, void* workspace, size_t workspace_bytes,

@@ -193,12 +193,12 @@ def load(path: str = LIB_PATH):
     lib.mamba_gated_recurrence_fwd.argtypes = [rec] + [_vp] * 11 + [_sz, _vp]
     lib.mamba_gated_recurrence_bwd.argtypes = [rec] + [_vp] * 17 + [_sz, _vp]
     lib.mamba_gated_recurrence_update.argtypes = [rec, _vp, _vp, _i64] + [_vp] * 7
-    norm_in = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _f32, _int, _int]
+    norm_in = [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _f32, _int, _int]
     lib.mamba_residual_norm_fwd.argtypes = norm_in + [_vp] * 3
     lib.mamba_residual_norm_fp8.argtypes = norm_in + [_vp] * 4
     lib.mamba_residual_norm_bwd_workspace_size.restype = _sz
     lib.mamba_residual_norm_bwd_workspace_size.argtypes = [_i64, _i64]
-    lib.mamba_residual_norm_bwd.argtypes = ([_vp, _i64] + [_vp] * 3 + [_i64, _i64, _f32, _int, _int]
+    lib.mamba_residual_norm_bwd.argtypes = ([_vp, _i64, _i64] + [_vp] * 3 + [_i64] * 3 + [_f32, _int, _int]
                                             + [_vp] * 4 + [_sz, _vp])
     for name in ("mamba_heads_scan_fwd", "mamba_heads_scan_bwd", "mamba_heads_state_update",
                  "mamba_conv1d_tokens_fwd", "mamba_conv1d_tokens_bwd",

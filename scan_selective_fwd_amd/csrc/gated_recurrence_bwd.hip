@@ -79,7 +79,7 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
   }
   float A2[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) A2[v] = p.A[cl + v] * kLog2e;
+  for (int v = 0; v < V; ++v) A2[v] = rec_log2(p.A[cl + v]);
 
   // the run's map of the states, and what the gradients take of the gates: with g the
   // gradient at a state and y the log of its decay
@@ -261,21 +261,26 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
     }
 }
 
-// dA: the tiles' shares added in a fixed order, in 64 bits; 8 slices of them by 32
+// dA: the tiles' shares added in a fixed order, in 64 bits; 32 slices of them by 32
 // channels.
-__global__ __launch_bounds__(256) void rec_sum_kernel(const RecParams p, const int64_t parts) {
-  __shared__ double red[8][32];
+__global__ __launch_bounds__(1024) void rec_sum_kernel(const RecParams p, const int64_t parts) {
+  __shared__ double red[32][33];
   const int cl = threadIdx.x & 31, sl = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + cl;
   double sum = 0.0;
-  if (c < p.dim)
-    for (int64_t k = sl; k < parts; k += 8) sum += p.part[k * p.dim + c];
-  red[sl][cl] = sum;
-  __syncthreads();
-  if (sl == 0 && c < p.dim) {
-    for (int k = 1; k < 8; ++k) sum += red[k][cl];
-    p.dA[c] = (float)(sum / p.A[c]);     // the shares are A's times too large
+  if (c < p.dim) {
+#pragma unroll 4
+    for (int64_t k = sl; k < parts; k += 32) sum += p.part[k * p.dim + c];
   }
+  red[cl][sl] = sum;
+  __syncthreads();
+  // a wave takes two channels' slices
+  const int ch = threadIdx.x >> 5, at = threadIdx.x & 31;
+  sum = red[ch][at];
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+  const int64_t to = (int64_t)blockIdx.x * 32 + ch;
+  if (at == 0 && to < p.dim) p.dA[to] = (float)sum / p.A[to];   // the shares are A times too large
 }
 
 template <typename T, int V, bool Z, bool RESET>
@@ -294,7 +299,7 @@ hipError_t go(RecParams p, hipStream_t s) {
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rec_sum_kernel, dim3((unsigned)((p.dim + 31) / 32)), dim3(256), 0, s, p,
+  hipLaunchKernelGGL(rec_sum_kernel, dim3((unsigned)((p.dim + 31) / 32)), dim3(1024), 0, s, p,
                      p.batch * tiles);
   return hipGetLastError();
 }

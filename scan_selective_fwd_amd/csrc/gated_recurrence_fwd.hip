@@ -68,7 +68,7 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
   }
   float A2[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) A2[v] = p.A[cl + v] * kLog2e;
+  for (int v = 0; v < V; ++v) A2[v] = rec_log2(p.A[cl + v]);
 
   // the run's own map
   float a[S][V], u[S][V], A[V], H[V];

@@ -30,7 +30,7 @@ __global__ __launch_bounds__(256) void rec_step_kernel(const RecStepParams p, co
   load_f32<V>(p.A, d, A);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const RecGate g = rec_gate(r[v], i[v], A[v] * kLog2e);
+    const RecGate g = rec_gate(r[v], i[v], rec_log2(A[v]));
     h[v] = rec_apply(g.a, rec_sqrt(g.m2) * (g.si * x[v]), false, h[v]);
   }
   store_vec<float, V>(st, 0, h);

@@ -101,7 +101,9 @@ struct ResNormParams {
   const void* res;       // nullable in the forward; the kept sum in the backward
   const float* w;        // nullable
   int64_t x_row, res_row;
-  int64_t rows, dim;
+  int64_t inner;         // rows of a batch row where x_batch, res_batch part them; 0: one run
+  int64_t x_batch, res_batch;
+  int64_t rows, dim;     // rows in all
   float eps;
   bool vec;              // every row starts on 16 bytes
   void* out;

@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int64_t kLim = (int64_t)1 << 62;
+constexpr int64_t kLim = (int64_t)1 << 60;   // elements: their bytes fit 64 bits
 
 int esize(int dt) { return dt == MAMBA_F32 ? 4 : 2; }
 
@@ -24,7 +24,7 @@ hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 // a * b <= kLim for a, b >= 0.
 bool mul_ok(int64_t a, int64_t b) { return b == 0 || a <= kLim / b; }
 
-// Whether (batch, tokens) rows at these strides stay inside 2^62 elements.
+// Whether (batch, tokens) rows at these strides stay inside 2^60 elements.
 bool span_ok(int64_t batch, int64_t sb, int64_t tokens, int64_t st) {
   return mul_ok(batch, sb) && mul_ok(tokens, st) && batch * sb <= kLim - tokens * st;
 }
@@ -37,6 +37,7 @@ bool partly(const void* a, const void* b, size_t n) {
   return p != q && (p < q ? q - p : p - q) < n;
 }
 
+// Whether [a, a + na) and [b, b + nb) overlap; absent ones do not.
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
   return a && b && (p < q ? q - p < na : p - q < nb);
@@ -51,9 +52,7 @@ mamba_status check_shape(const mamba_recurrence_shape* s) {
       s->z_batch_stride < 0 || s->z_token_stride < 0)
     return MAMBA_ERR_SHAPE;
   if (s->dim > (int64_t)1 << 28 || s->seqlen > kLim / 64 / s->batch ||
-      s->dim > kLim / 64 / (s->batch * s->seqlen) ||
-      s->batch > mscan::max_blocks(1024) / 2 / mscan::rec_strips(s->dim, false) /
-                     mscan::rec_bwd_tiles(s->seqlen))   // some blocks may have no strip
+      s->dim > kLim / 64 / (s->batch * s->seqlen))
     return MAMBA_ERR_UNSUPPORTED;
   if (!span_ok(s->batch, s->x_batch_stride, s->seqlen, s->x_token_stride) ||
       !span_ok(s->batch, s->r_batch_stride, s->seqlen, s->r_token_stride) ||
@@ -61,6 +60,23 @@ mamba_status check_shape(const mamba_recurrence_shape* s) {
       !span_ok(s->batch, s->z_batch_stride, s->seqlen, s->z_token_stride))
     return MAMBA_ERR_UNSUPPORTED;
   return MAMBA_OK;
+}
+
+// Whether a pass in `tiles` tiles of up to `waves` waves is a legal grid, with the blocks
+// that may be without a strip.
+bool grid_ok(const mamba_recurrence_shape* s, int64_t tiles, int64_t waves) {
+  return s->batch <= mscan::max_blocks((int)(64 * waves)) / 2 /
+                         mscan::rec_strips(s->dim, false) / tiles;
+}
+bool fwd_ok(const mamba_recurrence_shape* s) {
+  const int64_t tiles = mscan::rec_fwd_tiles(s->seqlen);
+  return grid_ok(s, tiles, tiles > 1 ? mscan::kRecFwdTile / mscan::kRecRun
+                                     : (s->seqlen + mscan::kRecRun - 1) / mscan::kRecRun);
+}
+bool bwd_ok(const mamba_recurrence_shape* s) {
+  const int64_t tiles = mscan::rec_bwd_tiles(s->seqlen);
+  return grid_ok(s, tiles, tiles > 1 ? mscan::kRecBwdTile / mscan::kRecBwdRun
+                                     : (s->seqlen + mscan::kRecBwdRun - 1) / mscan::kRecBwdRun);
 }
 
 mamba_status check_inputs(const mamba_recurrence_shape* s, const void* x, const void* r,
@@ -169,57 +185,74 @@ BwdLayout bwd_layout(const mamba_recurrence_shape* s, bool given) {
   return l;
 }
 
-mamba_status check_norm(const void* x, int64_t x_row, const void* res, int64_t res_row,
-                        const float* weight, int64_t rows, int64_t dim, float eps, mamba_dtype dt,
-                        mamba_dtype rdt, mscan::ResNormKind* kind) {
+// Rows of a view: element (b, t, i) at p[b * batch + t * row + i].
+struct View {
+  const void* p;
+  int64_t batch, row;
+};
+
+mamba_status check_norm(const View& x, const View& res, const float* weight, int64_t batch,
+                        int64_t rows, int64_t dim, float eps, mamba_dtype dt, mamba_dtype rdt,
+                        mscan::ResNormKind* kind) {
   if ((dt != MAMBA_F32 && dt != MAMBA_BF16) || (rdt != MAMBA_F32 && rdt != dt))
     return MAMBA_ERR_DTYPE;
   *kind = dt == MAMBA_F32 ? mscan::kResF32 : rdt == MAMBA_F32 ? mscan::kResBf16F32 : mscan::kResBf16;
-  if (rows <= 0 || dim <= 0 || x_row < 0 || res_row < 0) return MAMBA_ERR_SHAPE;
+  if (batch <= 0 || rows <= 0 || dim <= 0 || x.batch < 0 || x.row < 0 || res.batch < 0 || res.row < 0)
+    return MAMBA_ERR_SHAPE;
   if (!(eps >= 0.0f)) return MAMBA_ERR_INVALID;
-  if (dim > (1 << 28) || rows > kLim / 16 / dim || !mul_ok(rows, x_row) || !mul_ok(rows, res_row))
+  if (dim > (1 << 28) || rows > kLim / 16 / dim || batch > kLim / 16 / dim / rows ||
+      !span_ok(batch, x.batch, rows, x.row) || !span_ok(batch, res.batch, rows, res.row))
     return MAMBA_ERR_UNSUPPORTED;
-  if (!x) return MAMBA_ERR_NULL_PTR;
-  if (!aligned(x, (size_t)esize(dt)) || !aligned(res, (size_t)esize(rdt)) || !aligned_f32(weight))
+  if (!x.p) return MAMBA_ERR_NULL_PTR;
+  if (!aligned(x.p, (size_t)esize(dt)) || !aligned(res.p, (size_t)esize(rdt)) || !aligned_f32(weight))
     return MAMBA_ERR_ALIGNMENT;
   return MAMBA_OK;
 }
 
-// Whether rows at p start on 16 bytes.
-bool rows16(const void* p, int64_t row, int es) {
-  return aligned(p, 16) && row % (16 / es) == 0;
+// Bytes from the first element to the end of the last row.
+size_t span(const View& v, int64_t batch, int64_t rows, int64_t dim, int es) {
+  return (size_t)((batch - 1) * v.batch + (rows - 1) * v.row + dim) * (size_t)es;
 }
 
-mamba_status norm_fwd(const void* x, int64_t x_row, const void* residual, int64_t res_row,
-                      const float* weight, int64_t rows, int64_t dim, float eps, mamba_dtype dt,
-                      mamba_dtype rdt, void* out, float* scale, bool fp8, void* residual_out,
-                      void* stream) {
+bool one_run(const View& v, int64_t batch, int64_t rows) {
+  return !v.p || batch == 1 || v.batch == rows * v.row;
+}
+
+// Whether every row starts on 16 bytes.
+bool rows16(const View& v, int es) {
+  return aligned(v.p, 16) && v.batch % (16 / es) == 0 && v.row % (16 / es) == 0;
+}
+
+mamba_status norm_fwd(const View& x, View res, const float* weight, int64_t batch, int64_t rows,
+                      int64_t dim, float eps, mamba_dtype dt, mamba_dtype rdt, void* out,
+                      float* scale, bool fp8, void* residual_out, void* stream) {
   mscan::ResNormKind kind;
-  mamba_status st =
-      check_norm(x, x_row, residual, residual ? res_row : 0, weight, rows, dim, eps, dt, rdt, &kind);
+  if (!res.p) res = {nullptr, 0, 0};
+  const mamba_status st = check_norm(x, res, weight, batch, rows, dim, eps, dt, rdt, &kind);
   if (st != MAMBA_OK) return st;
-  if (!out || (fp8 && !scale) || (residual && !residual_out)) return MAMBA_ERR_NULL_PTR;
-  if (!residual && residual_out) return MAMBA_ERR_INVALID;
+  if (!out || (fp8 && !scale) || (res.p && !residual_out)) return MAMBA_ERR_NULL_PTR;
+  if (!res.p && residual_out) return MAMBA_ERR_INVALID;
   const int es = esize(dt), er = esize(rdt);
   if ((!fp8 && !aligned(out, (size_t)es)) || !aligned_f32(scale) ||
       !aligned(residual_out, (size_t)er))
     return MAMBA_ERR_ALIGNMENT;
-  const size_t n = (size_t)(rows * dim), no = n * (fp8 ? 1 : (size_t)es), nr = n * (size_t)er;
-  const size_t sx = (size_t)((rows - 1) * x_row + dim) * (size_t)es;
-  const size_t sr = (size_t)((rows - 1) * res_row + dim) * (size_t)er;
-  if (overlap(out, no, x, sx) || (residual && overlap(out, no, residual, sr)) ||
-      (residual && overlap(residual_out, nr, x, sx)))
+  const size_t n = (size_t)(batch * rows * dim), no = n * (fp8 ? 1 : (size_t)es), nr = n * (size_t)er;
+  const size_t sx = span(x, batch, rows, dim, es), sr = span(res, batch, rows, dim, er);
+  if (overlap(out, no, x.p, sx) || overlap(out, no, res.p, sr) || overlap(residual_out, nr, x.p, sx))
     return MAMBA_ERR_INVALID;
   // the stream is carried in place row on row, or apart
-  if (residual && overlap(residual_out, nr, residual, sr) &&
-      (residual_out != residual || (res_row != dim && rows > 1)))
+  const bool dense = (rows == 1 || res.row == dim) && (batch == 1 || res.batch == rows * dim);
+  if (overlap(residual_out, nr, res.p, sr) && (residual_out != res.p || !dense))
     return MAMBA_ERR_INVALID;
   mscan::ResNormParams p{};
-  p.x = x; p.res = residual; p.w = weight; p.x_row = x_row; p.res_row = res_row;
-  p.rows = rows; p.dim = dim; p.eps = eps;
+  p.x = x.p; p.x_batch = x.batch; p.x_row = x.row;
+  p.res = res.p; p.res_batch = res.batch; p.res_row = res.row;
+  p.inner = one_run(x, batch, rows) && one_run(res, batch, rows) ? 0 : rows;
+  p.w = weight; p.rows = batch * rows; p.dim = dim; p.eps = eps;
   p.out = out; p.scale = scale; p.res_out = residual_out;
-  p.vec = dim % (16 / es) == 0 && rows16(x, x_row, es) && (!residual || rows16(residual, res_row, er)) &&
-          aligned(weight, 16) && aligned(out, fp8 ? (size_t)(16 / es) : 16) && aligned(residual_out, 16);
+  p.vec = dim % (16 / es) == 0 && rows16(x, es) && (!res.p || rows16(res, er)) &&
+          aligned(weight, 16) && aligned(out, fp8 ? (size_t)(16 / es) : 16) &&
+          aligned(residual_out, 16);
   return hip_status(mscan::dispatch_res_norm_fwd(p, kind, fp8, as_stream(stream)));
 }
 
@@ -228,17 +261,19 @@ mamba_status norm_fwd(const void* x, int64_t x_row, const void* residual, int64_
 extern "C" {
 
 size_t mamba_gated_recurrence_checkpoint_size(const mamba_recurrence_shape* shape) {
-  if (check_shape(shape) != MAMBA_OK) return SIZE_MAX;
+  if (check_shape(shape) != MAMBA_OK || !fwd_ok(shape)) return SIZE_MAX;
   return (size_t)(shape->batch * shape->dim) * (size_t)tiles(shape) * 4;
 }
 
 size_t mamba_gated_recurrence_fwd_workspace_size(const mamba_recurrence_shape* shape) {
-  return check_shape(shape) == MAMBA_OK ? fwd_layout(shape).total : SIZE_MAX;
+  return check_shape(shape) == MAMBA_OK && fwd_ok(shape) ? fwd_layout(shape).total : SIZE_MAX;
 }
 
 size_t mamba_gated_recurrence_bwd_workspace_size(const mamba_recurrence_shape* shape,
                                                  int with_checkpoints) {
-  return check_shape(shape) == MAMBA_OK ? bwd_layout(shape, with_checkpoints != 0).total : SIZE_MAX;
+  return check_shape(shape) == MAMBA_OK && bwd_ok(shape) && (with_checkpoints || fwd_ok(shape))
+             ? bwd_layout(shape, with_checkpoints != 0).total
+             : SIZE_MAX;
 }
 
 mamba_status mamba_gated_recurrence_fwd(const mamba_recurrence_shape* shape, const void* x,
@@ -256,8 +291,9 @@ mamba_status mamba_gated_recurrence_fwd(const mamba_recurrence_shape* shape, con
     return MAMBA_ERR_ALIGNMENT;
   if (h0 && last_state && partly(h0, last_state, (size_t)(shape->batch * shape->dim) * 4))
     return MAMBA_ERR_INVALID;
-  if (over_inputs(out, shape, x, r, i, z)) return MAMBA_ERR_INVALID;
   const size_t need = mamba_gated_recurrence_fwd_workspace_size(shape);
+  if (need == SIZE_MAX) return MAMBA_ERR_UNSUPPORTED;
+  if (over_inputs(out, shape, x, r, i, z)) return MAMBA_ERR_INVALID;
   if (need && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
   if (need && !aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
   mscan::RecParams p = common(shape, x, r, i, A, z, h0, reset);
@@ -286,6 +322,7 @@ mamba_status mamba_gated_recurrence_bwd(const mamba_recurrence_shape* shape, con
       !aligned(dz, es) || !aligned_f32(dlast_state) || !aligned_f32(checkpoints) ||
       !aligned_f32(dA) || !aligned_f32(dh0))
     return MAMBA_ERR_ALIGNMENT;
+  if (!bwd_ok(shape) || (!checkpoints && !fwd_ok(shape))) return MAMBA_ERR_UNSUPPORTED;
   if (over_inputs(dx, shape, x, r, i, z) || over_inputs(dr, shape, x, r, i, z) ||
       over_inputs(di, shape, x, r, i, z) || over_inputs(dz, shape, x, r, i, z))
     return MAMBA_ERR_INVALID;
@@ -319,7 +356,8 @@ mamba_status mamba_gated_recurrence_update(const mamba_recurrence_shape* shape, 
   mamba_status st = check_shape(shape);
   if (st != MAMBA_OK) return st;
   if (shape->seqlen != 1 || pool <= 0 || (!slots && pool < shape->batch)) return MAMBA_ERR_SHAPE;
-  if (pool > kLim / 16 / shape->dim) return MAMBA_ERR_UNSUPPORTED;
+  if (pool > kLim / 16 / shape->dim || shape->batch > mscan::max_blocks(256) * 256 / shape->dim)
+    return MAMBA_ERR_UNSUPPORTED;
   st = check_inputs(shape, x, r, i, A, z, nullptr);
   if (st != MAMBA_OK) return st;
   if (!state || !out) return MAMBA_ERR_NULL_PTR;
@@ -342,42 +380,48 @@ mamba_status mamba_gated_recurrence_update(const mamba_recurrence_shape* shape, 
                                              as_stream(stream)));
 }
 
-mamba_status mamba_residual_norm_fwd(const void* x, int64_t x_row_stride, const void* residual,
+mamba_status mamba_residual_norm_fwd(const void* x, int64_t x_batch_stride, int64_t x_row_stride,
+                                     const void* residual, int64_t residual_batch_stride,
                                      int64_t residual_row_stride, const float* weight,
-                                     int64_t rows, int64_t dim, float eps, mamba_dtype dt,
-                                     mamba_dtype residual_dt, void* out, void* residual_out,
-                                     void* stream) {
-  return norm_fwd(x, x_row_stride, residual, residual_row_stride, weight, rows, dim, eps, dt,
-                  residual_dt, out, nullptr, false, residual_out, stream);
+                                     int64_t batch, int64_t rows, int64_t dim, float eps,
+                                     mamba_dtype dt, mamba_dtype residual_dt, void* out,
+                                     void* residual_out, void* stream) {
+  return norm_fwd({x, x_batch_stride, x_row_stride},
+                  {residual, residual_batch_stride, residual_row_stride}, weight, batch, rows, dim,
+                  eps, dt, residual_dt, out, nullptr, false, residual_out, stream);
 }
 
-mamba_status mamba_residual_norm_fp8(const void* x, int64_t x_row_stride, const void* residual,
+mamba_status mamba_residual_norm_fp8(const void* x, int64_t x_batch_stride, int64_t x_row_stride,
+                                     const void* residual, int64_t residual_batch_stride,
                                      int64_t residual_row_stride, const float* weight,
-                                     int64_t rows, int64_t dim, float eps, mamba_dtype dt,
-                                     mamba_dtype residual_dt, uint8_t* out8, float* scale,
-                                     void* residual_out, void* stream) {
-  return norm_fwd(x, x_row_stride, residual, residual_row_stride, weight, rows, dim, eps, dt,
-                  residual_dt, out8, scale, true, residual_out, stream);
+                                     int64_t batch, int64_t rows, int64_t dim, float eps,
+                                     mamba_dtype dt, mamba_dtype residual_dt, uint8_t* out8,
+                                     float* scale, void* residual_out, void* stream) {
+  return norm_fwd({x, x_batch_stride, x_row_stride},
+                  {residual, residual_batch_stride, residual_row_stride}, weight, batch, rows, dim,
+                  eps, dt, residual_dt, out8, scale, true, residual_out, stream);
 }
 
 size_t mamba_residual_norm_bwd_workspace_size(int64_t rows, int64_t dim) {
   static const float dummy[4] = {};
   mscan::ResNormKind kind;
-  if (check_norm(dummy, dim, dummy, dim, nullptr, rows, dim, 0.0f, MAMBA_F32, MAMBA_F32, &kind) !=
-      MAMBA_OK)
+  if (check_norm({dummy, 0, 0}, {dummy, 0, 0}, nullptr, 1, rows, dim, 0.0f, MAMBA_F32, MAMBA_F32,
+                 &kind) != MAMBA_OK)
     return SIZE_MAX;
   return up256((size_t)mscan::res_norm_parts(rows) * (size_t)dim * 4);
 }
 
-mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_row_stride,
-                                     const float* weight, const void* dout, const void* dres,
+mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_batch_stride,
+                                     int64_t res_row_stride, const float* weight,
+                                     const void* dout, const void* dres, int64_t batch,
                                      int64_t rows, int64_t dim, float eps, mamba_dtype dt,
                                      mamba_dtype residual_dt, void* dx, void* dresidual,
                                      float* dweight, void* workspace, size_t workspace_bytes,
                                      void* stream) {
   mscan::ResNormKind kind;
-  mamba_status st = check_norm(dout, dim, res, res_row_stride, weight, rows, dim, eps, dt,
-                               residual_dt, &kind);
+  const View r = {res, res_batch_stride, res_row_stride};
+  const mamba_status st =
+      check_norm({dout, 0, 0}, r, weight, batch, rows, dim, eps, dt, residual_dt, &kind);
   if (st != MAMBA_OK) return st;
   if (!res || !dx) return MAMBA_ERR_NULL_PTR;
   if ((weight != nullptr) != (dweight != nullptr) || (dresidual && residual_dt == dt))
@@ -386,21 +430,23 @@ mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_row_stride,
   if (!aligned(dres, (size_t)er) || !aligned(dx, (size_t)es) || !aligned(dresidual, (size_t)er) ||
       !aligned_f32(dweight))
     return MAMBA_ERR_ALIGNMENT;
-  const size_t n = (size_t)(rows * dim);
-  if (overlap(dx, n * (size_t)es, dout, n * (size_t)es) ||
-      overlap(dx, n * (size_t)es, res, (size_t)((rows - 1) * res_row_stride + dim) * (size_t)er))
+  const size_t n = (size_t)(batch * rows * dim), sr = span(r, batch, rows, dim, er);
+  if (overlap(dx, n * (size_t)es, dout, n * (size_t)es) || overlap(dx, n * (size_t)es, res, sr) ||
+      overlap(dresidual, n * (size_t)er, res, sr))
     return MAMBA_ERR_INVALID;
-  const size_t need = mamba_residual_norm_bwd_workspace_size(rows, dim);
+  const size_t need = mamba_residual_norm_bwd_workspace_size(batch * rows, dim);
   if (need == SIZE_MAX) return MAMBA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
   mscan::ResNormParams p{};
-  p.res = res; p.res_row = res_row_stride; p.w = weight; p.rows = rows; p.dim = dim; p.eps = eps;
+  p.res = res; p.res_batch = r.batch; p.res_row = r.row;
+  p.inner = one_run(r, batch, rows) ? 0 : rows;
+  p.w = weight; p.rows = batch * rows; p.dim = dim; p.eps = eps;
   p.dout = dout; p.dres = dres; p.dx = dx; p.dresidual = dresidual; p.dw = dweight;
   p.part = static_cast<float*>(workspace);
-  p.parts = mscan::res_norm_parts(rows);
-  p.vec = dim % (16 / es) == 0 && rows16(res, res_row_stride, er) && aligned(dout, 16) &&
-          aligned(dres, 16) && aligned(weight, 16) && aligned(dx, 16) && aligned(dresidual, 16);
+  p.parts = mscan::res_norm_parts(p.rows);
+  p.vec = dim % (16 / es) == 0 && rows16(r, er) && aligned(dout, 16) && aligned(dres, 16) &&
+          aligned(weight, 16) && aligned(dx, 16) && aligned(dresidual, 16);
   return hip_status(mscan::dispatch_res_norm_bwd(p, kind, as_stream(stream)));
 }
 

@@ -31,7 +31,14 @@ struct RecGate {
 // Within one unit in the last place, as the exponentials here are.
 __device__ __forceinline__ float rec_sqrt(float x) { return __builtin_amdgcn_sqrtf(x); }
 
-// A2 = A log2(e).  1 - a^2 is formed without cancellation: from the polynomial where
+// A in the units of exp2, held in range: a step past the end has a gate of 0 and keeps the
+// state whatever A is.  A NaN stays.
+__device__ __forceinline__ float rec_log2(float A) {
+  const float a = A * kLog2e;
+  return a < -3e38f ? -3e38f : a;
+}
+
+// A2 = rec_log2(A).  1 - a^2 is formed without cancellation: from the polynomial where
 // a^2 is above e^(-1/2), from a itself below, where it keeps at least 0.39.
 __device__ __forceinline__ RecGate rec_gate(float r, float i, float A2) {
   RecGate g;

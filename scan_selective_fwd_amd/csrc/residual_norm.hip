@@ -15,6 +15,14 @@ namespace {
 constexpr int kParts = 512;        // blocks of the backward: two a CU
 constexpr int kFwdBlocks = 1 << 22;
 
+// Where row `row` of a view starts.
+__device__ __forceinline__ int64_t row_at(const ResNormParams& p, int64_t row, int64_t batch,
+                                          int64_t step) {
+  if (!p.inner) return row * step;
+  const int64_t b = row / p.inner;
+  return b * batch + (row - b * p.inner) * step;
+}
+
 template <bool MAX>
 __device__ __forceinline__ float join(float a, float b) {
   return MAX ? __builtin_fmaxf(a, b) : a + b;
@@ -108,6 +116,8 @@ __global__ __launch_bounds__(256) void res_norm_fwd_kernel(const ResNormParams p
   for (int64_t row0 = (int64_t)blockIdx.x * TEAMS; row0 < p.rows; row0 += (int64_t)gridDim.x * TEAMS) {
     const int64_t row = row0 + threadIdx.x / TEAM;
     const bool on = row < p.rows;                 // whole teams
+    const int64_t x0 = row_at(p, row, p.x_batch, p.x_row);
+    const int64_t r0 = row_at(p, row, p.res_batch, p.res_row);
     float x[NV][V], r[NV][V];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -115,8 +125,8 @@ __global__ __launch_bounds__(256) void res_norm_fwd_kernel(const ResNormParams p
 #pragma unroll
       for (int v = 0; v < V; ++v) x[j][v] = r[j][v] = 0.0f;
       if (on && k < n) {
-        load_vec<T, V>(p.x, row * p.x_row + k, x[j]);
-        if (p.res) load_vec<R, V>(p.res, row * p.res_row + k, r[j]);
+        load_vec<T, V>(p.x, x0 + k, x[j]);
+        if (p.res) load_vec<R, V>(p.res, r0 + k, r[j]);
       }
     }
     float s2 = 0.0f;
@@ -177,11 +187,13 @@ __global__ __launch_bounds__(256) void res_norm_fwd_walk_kernel(const ResNormPar
   __shared__ float sh[4];
   const int64_t n = p.dim;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t x0 = row_at(p, row, p.x_batch, p.x_row);
+    const int64_t r0 = row_at(p, row, p.res_batch, p.res_row);
     auto sum = [&](int64_t k, float (&x)[V]) {
       float r[V];
-      load_vec<T, V>(p.x, row * p.x_row + k, x);
+      load_vec<T, V>(p.x, x0 + k, x);
       if (p.res) {
-        load_vec<R, V>(p.res, row * p.res_row + k, r);
+        load_vec<R, V>(p.res, r0 + k, r);
         add_stored<R, V>(x, r);
       }
     };
@@ -235,10 +247,12 @@ __global__ __launch_bounds__(256) void res_norm_fwd_walk_kernel(const ResNormPar
 }
 
 // Block `part`: its teams take every (parts * TEAMS)-th row, the next row's loads in
-// flight while one is worked on, and leave the block's share of dw in part.
+// flight while one is worked on (where the registers hold both), and leave the block's
+// share of dw in part.
 template <typename T, typename R, int V, int TEAM, int NV>
 __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     const ResNormParams p) {
+  constexpr bool AHEAD = NV * V <= 24;
   constexpr int THREADS = TEAM > 256 ? TEAM : 256, TEAMS = THREADS / TEAM;
   __shared__ float sh[THREADS / 64];
   __shared__ float red[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? TEAM * NV * V : 1];
@@ -253,38 +267,58 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
       w[j][v] = 1.0f;
       dw[j][v] = 0.0f;
     }
-    if (p.w && k < n) load_f32<V>(p.w, k, w[j]);
+    if (AHEAD && p.w && k < n) load_f32<V>(p.w, k, w[j]);
   }
   Raw<R, V> xr[NV], gr[NV];
   Raw<T, V> yr[NV];
   auto load = [&](int64_t row) {
+    const int64_t r0 = row_at(p, row, p.res_batch, p.res_row);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int64_t k = (int64_t)(j * TEAM + tid) * V;
       xr[j].zero();
-      gr[j].zero();
       yr[j].zero();
       if (k < n && row < p.rows) {
-        xr[j].load(p.res, row * p.res_row + k);
+        xr[j].load(p.res, r0 + k);
         yr[j].load(p.dout, row * n + k);
-        if (p.dres) gr[j].load(p.dres, row * n + k);
       }
     }
   };
+  auto load_dres = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t k = (int64_t)(j * TEAM + tid) * V;
+      gr[j].zero();
+      if (p.dres && k < n && row < p.rows) gr[j].load(p.dres, row * n + k);
+    }
+  };
   const int64_t step = p.parts * TEAMS;
-  load(blockIdx.x * (int64_t)TEAMS + team);
+  if (AHEAD) {
+    load(blockIdx.x * (int64_t)TEAMS + team);
+    load_dres(blockIdx.x * (int64_t)TEAMS + team);
+  }
   // every team walks as long as the first: the joins wait for whole blocks
   for (int64_t row0 = blockIdx.x * (int64_t)TEAMS; row0 < p.rows; row0 += step) {
     const int64_t row = row0 + team;
     float x[NV][V], dy[NV][V], g[NV][V];
     float s2 = 0.0f, sv = 0.0f;
+    if (!AHEAD) load(row);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       xr[j].get(x[j]);
       yr[j].get(dy[j]);
-      gr[j].get(g[j]);
+      if (AHEAD) gr[j].get(g[j]);
     }
-    load(row + step);
+    if (AHEAD) {
+      load(row + step);
+      load_dres(row + step);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {       // from the cache, row by row
+        const int64_t k = (int64_t)(j * TEAM + tid) * V;
+        if (p.w && k < n) load_f32<V>(p.w, k, w[j]);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -306,10 +340,15 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
       return team_join<TEAM, false>(t2, sh);
     });
     const float kk = r * (sv / (float)p.dim);
+    if (!AHEAD) {
+      mem_fence_compiler();                // not before the sums, which need registers
+      load_dres(row);
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int64_t k = (int64_t)(j * TEAM + tid) * V;
       float d[V];
+      if (!AHEAD) gr[j].get(g[j]);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float hat = x[j][v] * r;
@@ -357,7 +396,7 @@ __global__ __launch_bounds__(256) void res_norm_bwd_walk_kernel(const ResNormPar
   if (mine)
     for (int64_t k = threadIdx.x; k < n; k += 256) mine[k] = 0.0f;
   for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
-    const R* res = static_cast<const R*>(p.res) + row * p.res_row;
+    const R* res = static_cast<const R*>(p.res) + row_at(p, row, p.res_batch, p.res_row);
     const T* dout = static_cast<const T*>(p.dout) + row * n;
     float s2 = 0.0f, sv = 0.0f;
     for (int64_t k = threadIdx.x; k < n; k += 256) {

@@ -19,7 +19,7 @@ import functools
 import torch
 
 from . import MambaScanError, _dtype_code, _first_order, _flags, _lib, _ptr, lib
-from .heads import (_dims, _gpu, _req, _rows, _slots, _stream, _view, _workspace)
+from .heads import _dims, _gpu, _req, _slots, _stream, _view, _workspace
 
 _F32 = torch.float32
 _FP8 = torch.float8_e4m3fn
@@ -247,12 +247,35 @@ def _residual_code(t, x):
     return _dtype_code(t)
 
 
-def _row_stride(t, name, dtype, dev):
-    """The distance of the rows of a (..., dim) tensor, which may be a view."""
+def _row_strides(t, name):
+    """Batch and row stride of a (..., dim) tensor, dense or a view: its rows are one run,
+    or one for each index of the first dimension."""
     if t.is_contiguous():
-        return t.shape[-1]
-    t = _rows(t)
-    return _view(t, name, dtype, t.shape, dev, 1)[0]
+        return 0, t.shape[-1]
+    for lead in (1, t.shape[0]):
+        try:
+            v = t.view(lead, -1, t.shape[-1])
+        except RuntimeError:
+            continue
+        if t.shape[-1] == 1 or t.stride(-1) == 1:
+            return (v.stride(0) if lead > 1 else 0), (v.stride(1) if v.shape[1] > 1 else 0)
+    raise ValueError(f"rows of {name} must be contiguous, and a step apart in each index of its "
+                     "first dimension")
+
+
+def _planes(t, *views):
+    """(batch, rows, dim) of t: one run of rows where none of the strides needs more."""
+    dim = t.shape[-1]
+    rows = t.numel() // dim if dim else 0
+    if not rows or not any(sb for sb, _ in views):
+        return (1 if rows else 0), rows, dim
+    return t.shape[0], rows // t.shape[0], dim
+
+
+def _in_planes(strides, batch, rows):
+    """The batch stride of rows that are one run, where another tensor's are not."""
+    sb, sr = strides
+    return (rows * sr if batch > 1 and sb == 0 else sb), sr
 
 
 def _norm_args(x, residual, weight, residual_out):
@@ -261,9 +284,7 @@ def _norm_args(x, residual, weight, residual_out):
     code = rcode = _dtype_code(x)
     if not shape:
         raise ValueError("the norm needs at least one dimension")
-    dim = shape[-1]
-    rows = x.numel() // dim if dim else 0
-    sx, sr = _row_stride(x, "x", dt, dev), 0
+    sx, sr = _row_strides(x, "x"), (0, 0)
     if residual is not None:
         if _gpu(residual, "residual") != dev:
             raise ValueError(f"residual is on {residual.device}, expected {dev}")
@@ -272,15 +293,18 @@ def _norm_args(x, residual, weight, residual_out):
         if residual.shape != shape:
             raise ValueError(f"residual has shape {tuple(residual.shape)}, expected "
                              f"{tuple(shape)}")
-        sr = _row_stride(residual, "residual", residual.dtype, dev)
+        sr = _row_strides(residual, "residual")
         if residual_out is None:
             residual_out = _new(residual)
         else:
             _req(residual_out, "residual_out", residual.dtype, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
+    batch, rows, dim = _planes(x, sx, sr)
+    if batch > 1:
+        sx, sr = _in_planes(sx, batch, rows), _in_planes(sr, batch, rows)
     _req(weight, "weight", _F32, (dim,), dev)
-    return dev, code, rcode, sx, sr, rows, dim, residual_out
+    return dev, code, rcode, sx, sr, (batch, rows, dim), residual_out
 
 
 def residual_norm_fwd(x, residual=None, weight=None, *, eps=1e-5, out=None, residual_out=None):
@@ -292,12 +316,12 @@ def residual_norm_fwd(x, residual=None, weight=None, *, eps=1e-5, out=None, resi
     res is kept in it, and the norm is of what is kept.  Returns (out, res), out
     like x; without a residual res is x itself.  `residual_out`: a tensor to
     receive res, residual itself (dense) where the stream is carried in place."""
-    dev, code, rcode, sx, sr, rows, dim, kept = _norm_args(x, residual, weight, residual_out)
+    dev, code, rcode, sx, sr, sizes, kept = _norm_args(x, residual, weight, residual_out)
     if out is None:
         out = _new(x)
     else:
         _req(out, "out", x.dtype, x.shape, dev)
-    _call("mamba_residual_norm_fwd", dev, _ptr(x), sx, _ptr(residual), sr, _ptr(weight), rows, dim,
+    _call("mamba_residual_norm_fwd", dev, _ptr(x), *sx, _ptr(residual), *sr, _ptr(weight), *sizes,
           float(eps), code, rcode, _ptr(out), _ptr(kept))
     return out, x if kept is None else kept
 
@@ -307,7 +331,7 @@ def residual_norm_fp8(x, residual=None, weight=None, *, eps=1e-5, out=None, scal
     """residual_norm_fwd with out in 8 bits: returns (out, scale, res), out
     torch.float8_e4m3fn like x, scale float32 of x's shape without its last
     dimension, max|out| / 448 of each row; out stands for out * scale."""
-    dev, code, rcode, sx, sr, rows, dim, kept = _norm_args(x, residual, weight, residual_out)
+    dev, code, rcode, sx, sr, sizes, kept = _norm_args(x, residual, weight, residual_out)
     if out is None:
         out = _new(x, _FP8)
     else:
@@ -316,7 +340,7 @@ def residual_norm_fp8(x, residual=None, weight=None, *, eps=1e-5, out=None, scal
         scale = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
     else:
         _req(scale, "scale", _F32, x.shape[:-1], dev)
-    _call("mamba_residual_norm_fp8", dev, _ptr(x), sx, _ptr(residual), sr, _ptr(weight), rows, dim,
+    _call("mamba_residual_norm_fp8", dev, _ptr(x), *sx, _ptr(residual), *sr, _ptr(weight), *sizes,
           float(eps), code, rcode, _ptr(out), _ptr(scale), _ptr(kept))
     return out, scale, x if kept is None else kept
 
@@ -332,9 +356,8 @@ def residual_norm_bwd(res, weight, dout, dres=None, *, eps=1e-5, workspace=None)
     code, rcode = _dtype_code(dout), _residual_code(res, dout)
     if not res.shape:
         raise ValueError("the norm needs at least one dimension")
-    dim = res.shape[-1]
-    rows = res.numel() // dim if dim else 0
-    sr = _row_stride(res, "res", res.dtype, dev)
+    sr = _row_strides(res, "res")
+    batch, rows, dim = _planes(res, sr)
     _req(weight, "weight", _F32, (dim,), dev)
     _req(dout, "dout", dout.dtype, res.shape, dev)
     _req(dres, "dres", res.dtype, res.shape, dev)
@@ -342,10 +365,10 @@ def residual_norm_bwd(res, weight, dout, dres=None, *, eps=1e-5, workspace=None)
     g["dresidual"] = g["dx"] if code == rcode else _new(res)
     if weight is not None:
         g["dweight"] = torch.empty((dim,), dtype=_F32, device=dev)
-    n = _function("mamba_residual_norm_bwd_workspace_size")(rows, dim)
+    n = _function("mamba_residual_norm_bwd_workspace_size")(batch * rows, dim)
     ws = _workspace(n, (rows, dim), "mamba_residual_norm_bwd", workspace, dev)
-    _call("mamba_residual_norm_bwd", dev, _ptr(res), sr, _ptr(weight), _ptr(dout), _ptr(dres),
-          rows, dim, float(eps), code, rcode, _ptr(g["dx"]),
+    _call("mamba_residual_norm_bwd", dev, _ptr(res), *sr, _ptr(weight), _ptr(dout), _ptr(dres),
+          batch, rows, dim, float(eps), code, rcode, _ptr(g["dx"]),
           None if code == rcode else _ptr(g["dresidual"]), _ptr(g.get("dweight")), _ptr(ws), n)
     return g
 

@@ -122,11 +122,21 @@ def test_views_of_wider_rows(ms, dim, off, types):
     R.check("dx", got["dx"], d, terms)
     R.check("dresidual", got["dresidual"], d, terms)
     R.check("dweight", got["dweight"], dw, dw_abs)
-    # one row for every row
-    x = g["x"][:1, :1].expand(2, 9, dim)
-    with pytest.raises(RuntimeError):       # no one row stride says this
-        ms.residual_norm_fwd(x.transpose(0, 1)[:, :, :].expand(9, 2, dim).transpose(0, 1)[:, ::2],
-                             g["residual"][:, ::2], g["weight"])
+    # parts of batch rows, together with dense ones, and one row for every row
+    dense = lambda t: t.contiguous()  # noqa: E731
+    for a, b in ((g["x"][:, 2:7], dense(g["residual"][:, 2:7])),
+                 (dense(g["x"][:, ::2]), g["residual"][:, ::2]),
+                 (g["x"][:, 3:5], g["residual"][:, 1:3]),
+                 (g["x"][:1, :1].expand(2, 9, dim), g["residual"])):
+        for call in (ms.residual_norm_fwd, ms.residual_norm_fp8):
+            for p, q in zip(call(a, b, g["weight"]), call(dense(a), dense(b), g["weight"])):
+                assert torch.equal(p.float(), q.float())
+    part, dpart = g["residual"][:, 2:7], dense(g["dout"][:, 2:7])
+    p, q = (ms.residual_norm_bwd(r, g["weight"], dpart) for r in (part, dense(part)))
+    assert all(torch.equal(p[k], q[k]) for k in p)
+    for bad in (g["x"].unsqueeze(0).expand(3, 2, 9, dim).transpose(0, 2), g["x"].transpose(1, 2)):
+        with pytest.raises(ValueError):     # no two strides say this
+            ms.residual_norm_fwd(bad)
     row = g["x"][0, :1].expand(9, dim)
     a, _ = ms.residual_norm_fwd(row, g["residual"][0], g["weight"])
     b, _ = ms.residual_norm_fwd(row.contiguous(), g["residual"][0], g["weight"])
