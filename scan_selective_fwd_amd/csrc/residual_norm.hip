@@ -23,6 +23,17 @@ __device__ __forceinline__ int64_t row_at(const ResNormParams& p, int64_t row, i
   return b * batch + (row - b * p.inner) * step;
 }
 
+// Element k of the row that starts `row` elements behind p.  The row is the block's, the
+// place in it 32 bits: the access forms the sum.
+template <typename E>
+__device__ __forceinline__ const void* place(const void* p, int64_t row, uint32_t k) {
+  return static_cast<const char*>(p) + row * (int64_t)sizeof(E) + (uint32_t)(k * sizeof(E));
+}
+template <typename E>
+__device__ __forceinline__ void* place(void* p, int64_t row, uint32_t k) {
+  return static_cast<char*>(p) + row * (int64_t)sizeof(E) + (uint32_t)(k * sizeof(E));
+}
+
 template <bool MAX>
 __device__ __forceinline__ float join(float a, float b) {
   return MAX ? __builtin_fmaxf(a, b) : a + b;
@@ -257,17 +268,17 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
   __shared__ float sh[THREADS / 64];
   __shared__ float red[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? TEAM * NV * V : 1];
   const int tid = threadIdx.x & (TEAM - 1), team = threadIdx.x / TEAM;
-  const int64_t n = p.dim;
+  const int64_t n = p.dim;         // at most 16384 here
   float w[NV][V], dw[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t k = (int64_t)(j * TEAM + tid) * V;
+    const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       w[j][v] = 1.0f;
       dw[j][v] = 0.0f;
     }
-    if (AHEAD && p.w && k < n) load_f32<V>(p.w, k, w[j]);
+    if (AHEAD && p.w && k < n) load_f32<V>(static_cast<const float*>(place<float>(p.w, 0, k)), 0, w[j]);
   }
   Raw<R, V> xr[NV], gr[NV];
   Raw<T, V> yr[NV];
@@ -275,21 +286,21 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     const int64_t r0 = row_at(p, row, p.res_batch, p.res_row);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t k = (int64_t)(j * TEAM + tid) * V;
+      const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
       xr[j].zero();
       yr[j].zero();
       if (k < n && row < p.rows) {
-        xr[j].load(p.res, r0 + k);
-        yr[j].load(p.dout, row * n + k);
+        xr[j].load(place<R>(p.res, r0, k), 0);
+        yr[j].load(place<T>(p.dout, row * n, k), 0);
       }
     }
   };
   auto load_dres = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t k = (int64_t)(j * TEAM + tid) * V;
+      const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
       gr[j].zero();
-      if (p.dres && k < n && row < p.rows) gr[j].load(p.dres, row * n + k);
+      if (p.dres && k < n && row < p.rows) gr[j].load(place<R>(p.dres, row * n, k), 0);
     }
   };
   const int64_t step = p.parts * TEAMS;
@@ -315,8 +326,8 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     } else {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {       // from the cache, row by row
-        const int64_t k = (int64_t)(j * TEAM + tid) * V;
-        if (p.w && k < n) load_f32<V>(p.w, k, w[j]);
+        const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
+        if (p.w && k < n) load_f32<V>(static_cast<const float*>(place<float>(p.w, 0, k)), 0, w[j]);
       }
     }
 #pragma unroll
@@ -346,7 +357,7 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t k = (int64_t)(j * TEAM + tid) * V;
+      const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
       float d[V];
       if (!AHEAD) gr[j].get(g[j]);
 #pragma unroll
@@ -356,8 +367,8 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
         dw[j][v] = __builtin_fmaf(dy[j][v], hat, dw[j][v]);
       }
       if (k < n && row < p.rows) {
-        store_vec<T, V>(p.dx, row * n + k, d);
-        if (sizeof(T) != sizeof(R) && p.dresidual) store_vec<R, V>(p.dresidual, row * n + k, d);
+        store_vec<T, V>(place<T>(p.dx, row * n, k), 0, d);
+        if (sizeof(T) != sizeof(R) && p.dresidual) store_vec<R, V>(place<R>(p.dresidual, row * n, k), 0, d);
       }
     }
   }
@@ -380,7 +391,7 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t k = (int64_t)(j * TEAM + tid) * V;
+      const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
       if (k < n) store_vec<float, V>(mine, k, dw[j]);
     }
   }

@@ -50,6 +50,17 @@ def _struct(*fields):
     return s, ctypes.byref(s)
 
 
+@functools.lru_cache(maxsize=1024)
+def _fwd_bytes(*fields):
+    """The forward's workspace for these fields."""
+    return _function("mamba_gated_recurrence_fwd_workspace_size")(_struct(*fields)[1])
+
+
+@functools.lru_cache(maxsize=1024)
+def _bwd_bytes(kept, *fields):
+    return _function("mamba_gated_recurrence_bwd_workspace_size")(_struct(*fields)[1], kept)
+
+
 def _new(like, dtype=None):
     """A dense tensor of `like`'s shape (empty_like costs half of empty, but keeps the
     order of a permuted tensor's dimensions)."""
@@ -60,9 +71,10 @@ def _new(like, dtype=None):
 
 def _strides(t, name, dtype, shape, dev):
     """Checks a tensor that may be a view of wider rows; its strides but the last's."""
-    if isinstance(t, torch.Tensor) and t.is_contiguous() and t.shape == shape \
-            and t.dtype is dtype and t.device == dev:
-        return t.stride()[:-1]
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == dev:
+        st = t.stride()
+        if st[-1] == 1:
+            return st[:-1]
     return _view(t, name, dtype, shape, dev, len(shape) - 1)
 
 
@@ -73,16 +85,17 @@ def _shape(x, r, i, z):
     shape = _dims(x, "x", 3)
     dt = x.dtype
     code = _dtype_code(x)
-    s, ref = _struct(*shape, *_strides(x, "x", dt, shape, dev), *_strides(r, "r", dt, shape, dev),
-                     *_strides(i, "i", dt, shape, dev),
-                     *((0, 0) if z is None else _strides(z, "z", dt, shape, dev)), code)
-    return s, ref, dev, shape
+    fields = (*shape, *_strides(x, "x", dt, shape, dev), *_strides(r, "r", dt, shape, dev),
+              *_strides(i, "i", dt, shape, dev),
+              *((0, 0) if z is None else _strides(z, "z", dt, shape, dev)), code)
+    return _struct(*fields)[1], fields, dev, shape
 
 
-def _state_args(s, A, h0, reset, dev):
-    _req(A, "A", _F32, (s.dim,), dev)
-    _req(h0, "h0", _F32, (s.batch, s.dim), dev)
-    return _flags(reset, (s.batch, s.seqlen), dev)
+def _state_args(shape, A, h0, reset, dev):
+    batch, L, dim = shape
+    _req(A, "A", _F32, (dim,), dev)
+    _req(h0, "h0", _F32, (batch, dim), dev)
+    return _flags(reset, (batch, L), dev)
 
 
 def _tiles(L):
@@ -128,20 +141,21 @@ def gated_recurrence_fwd(x, r, i, A, z=None, h0=None, *, reset=None, return_last
     64th step, for gated_recurrence_bwd.  `workspace`: a contiguous GPU tensor of
     at least gated_recurrence_fwd_workspace_bytes, reused across calls
     (allocated when absent or smaller)."""
-    s, ref, dev, shape = _shape(x, r, i, z)
-    reset = _state_args(s, A, h0, reset, dev)
+    ref, fields, dev, shape = _shape(x, r, i, z)
+    reset = _state_args(shape, A, h0, reset, dev)
+    batch, L, dim = shape
     if out is None:
         out = _new(x)
     else:
         _req(out, "out", x.dtype, shape, dev)
     if return_last_state and last_state is None:
-        last_state = torch.empty((s.batch, s.dim), dtype=_F32, device=dev) if h0 is None \
+        last_state = torch.empty((batch, dim), dtype=_F32, device=dev) if h0 is None \
             else torch.empty_like(h0)
     else:
-        _req(last_state, "last_state", _F32, (s.batch, s.dim), dev)
+        _req(last_state, "last_state", _F32, (batch, dim), dev)
     if checkpoints is not None:
-        _req(checkpoints, "checkpoints", _F32, (s.batch, _tiles(s.seqlen), s.dim), dev)
-    n = _function("mamba_gated_recurrence_fwd_workspace_size")(ref)
+        _req(checkpoints, "checkpoints", _F32, (batch, _tiles(L), dim), dev)
+    n = _fwd_bytes(*fields)
     ws = _workspace(n, shape, "mamba_gated_recurrence_fwd", workspace, dev)
     _call("mamba_gated_recurrence_fwd", dev, ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(z),
           _ptr(h0), _ptr(reset), _ptr(out), _ptr(last_state), _ptr(checkpoints),
@@ -156,18 +170,19 @@ def gated_recurrence_bwd(x, r, i, A, z, dout, h0=None, *, dlast_state=None, rese
     forward over the same inputs; absent, they are formed again.  Returns a
     dict: dx, dr, di (and dz) in their tensors' type, dA (and dh0) in
     float32."""
-    s, ref, dev, shape = _shape(x, r, i, z)
-    reset = _state_args(s, A, h0, reset, dev)
+    ref, fields, dev, shape = _shape(x, r, i, z)
+    reset = _state_args(shape, A, h0, reset, dev)
+    batch, L, dim = shape
     _req(_need(dout, "dout"), "dout", x.dtype, shape, dev)
-    _req(dlast_state, "dlast_state", _F32, (s.batch, s.dim), dev)
+    _req(dlast_state, "dlast_state", _F32, (batch, dim), dev)
     if checkpoints is not None:
-        _req(checkpoints, "checkpoints", _F32, (s.batch, _tiles(s.seqlen), s.dim), dev)
+        _req(checkpoints, "checkpoints", _F32, (batch, _tiles(L), dim), dev)
     g = dict(dx=_new(x), dr=_new(x), di=_new(x), dA=_new(A))
     if z is not None:
         g["dz"] = _new(x)
     if h0 is not None:
         g["dh0"] = _new(h0)
-    n = _function("mamba_gated_recurrence_bwd_workspace_size")(ref, int(checkpoints is not None))
+    n = _bwd_bytes(int(checkpoints is not None), *fields)
     ws = _workspace(n, shape, "mamba_gated_recurrence_bwd", workspace, dev)
     _call("mamba_gated_recurrence_bwd", dev, ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(z),
           _ptr(h0), _ptr(reset), _ptr(dout), _ptr(dlast_state), _ptr(checkpoints), _ptr(g["dx"]),
@@ -187,10 +202,10 @@ def gated_recurrence_update(state, x, r, i, A, z=None, *, slots=None, out=None):
     batch, dim = shape
     dt = x.dtype
     pool = _dims(state, "state", 2)[0]
-    s, ref = _struct(batch, 1, dim, *_strides(x, "x", dt, shape, dev), 0,
-                     *_strides(r, "r", dt, shape, dev), 0, *_strides(i, "i", dt, shape, dev), 0,
-                     *((0,) if z is None else _strides(z, "z", dt, shape, dev)), 0,
-                     _dtype_code(x))
+    ref = _struct(batch, 1, dim, *_strides(x, "x", dt, shape, dev), 0,
+                  *_strides(r, "r", dt, shape, dev), 0, *_strides(i, "i", dt, shape, dev), 0,
+                  *((0,) if z is None else _strides(z, "z", dt, shape, dev)), 0,
+                  _dtype_code(x))[1]
     _req(A, "A", _F32, (dim,), dev)
     _req(state, "state", _F32, (pool, dim), dev)
     slots = _slots(slots, batch, dev)

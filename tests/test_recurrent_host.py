@@ -169,8 +169,7 @@ def test_the_binding_refuses_before_any_call():
 
 
 def test_kernels_keep_their_registers():
-    """Two blocks of 8 waves share a CU at 128 registers a lane; nothing spills, but the
-    norm's backward of rows of 8193 to 16384 on a float32 stream, a little."""
+    """Two blocks of 8 waves share a CU at 128 registers a lane; nothing spills."""
     res = kernel_resources(os.path.join(ROOT, "scan_selective_fwd_amd", "libmamba_scan.so"))
     tiles = {k: v for k, v in res.items() if re.search(r"rec_(fwd|bwd)_kernelI.*Lb1EEE", k)}
     assert len(tiles) == 12 + 8
@@ -178,9 +177,7 @@ def test_kernels_keep_their_registers():
     rest = {k: v for k, v in res.items() if re.search(r"rec_(fwd|bwd|step|sum|clear)_kernel", k)}
     assert len(rest) == 2 * (12 + 8) + 4 + 2 and not [k for k, v in rest.items() if v["scratch"]]
     norms = {k: v for k, v in res.items() if "res_norm" in k}
-    longest = re.compile(r"res_norm_bwd_kernelI[ft]fLi4ELi512ELi8E")
-    assert len(norms) > 60
-    assert not [k for k, v in norms.items() if v["scratch"] > (64 if longest.search(k) else 0)]
+    assert len(norms) > 60 and not [k for k, v in norms.items() if v["scratch"]]
 
 
 @pytest.mark.skipif(shutil.which("g++") is None or
