@@ -13,7 +13,8 @@ namespace mscan {
 namespace {
 
 constexpr int kParts = 512;        // blocks of the backward: two a CU
-constexpr int kFwdBlocks = 1 << 22;
+constexpr int kFwdBlocks = (1 << 22) - 1;   // of up to 1024 threads in one launch
+constexpr int kWalk = 1024;
 
 // Where row `row` of a view starts.
 __device__ __forceinline__ int64_t row_at(const ResNormParams& p, int64_t row, int64_t batch,
@@ -194,8 +195,8 @@ __global__ __launch_bounds__(256) void res_norm_fwd_kernel(const ResNormParams p
 
 // Rows too long for the registers: walked two or three times by a block.
 template <typename T, typename R, bool FP8, int V>
-__global__ __launch_bounds__(256) void res_norm_fwd_walk_kernel(const ResNormParams p) {
-  __shared__ float sh[4];
+__global__ __launch_bounds__(kWalk) void res_norm_fwd_walk_kernel(const ResNormParams p) {
+  __shared__ float sh[kWalk / 64];
   const int64_t n = p.dim;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const int64_t x0 = row_at(p, row, p.x_batch, p.x_row);
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(256) void res_norm_fwd_walk_kernel(const ResNormPar
     };
     auto squares = [&](float sc) {
       float s2 = 0.0f;
-      for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += 256 * V) {
+      for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += kWalk * V) {
         float x[V];
         sum(k, x);
 #pragma unroll
@@ -219,7 +220,7 @@ __global__ __launch_bounds__(256) void res_norm_fwd_walk_kernel(const ResNormPar
           s2 = __builtin_fmaf(t, t, s2);
         }
       }
-      return team_join<256, false>(s2, sh);
+      return team_join<kWalk, false>(s2, sh);
     };
     const float root = root_of(squares(1.0f), p, squares);
     auto normed = [&](int64_t k, float (&x)[V], float (&y)[V]) {
@@ -232,17 +233,17 @@ __global__ __launch_bounds__(256) void res_norm_fwd_walk_kernel(const ResNormPar
     float inv = 1.0f;
     if constexpr (FP8) {
       float most = 0.0f;
-      for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += 256 * V) {
+      for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += kWalk * V) {
         float x[V], y[V];
         normed(k, x, y);
 #pragma unroll
         for (int v = 0; v < V; ++v) most = __builtin_fmaxf(most, __builtin_fabsf(y[v]));
       }
-      most = __builtin_fmaxf(team_join<256, true>(most, sh), 0x1p-100f);
+      most = __builtin_fmaxf(team_join<kWalk, true>(most, sh), 0x1p-100f);
       inv = 448.0f / most;
       if (threadIdx.x == 0) p.scale[row] = most / 448.0f;
     }
-    for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += 256 * V) {
+    for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += kWalk * V) {
       float x[V], y[V];
       normed(k, x, y);
       if (p.res) store_vec<R, V>(p.res_out, row * n + k, x);
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(256) void res_norm_fwd_walk_kernel(const ResNormPar
 template <typename T, typename R, int V, int TEAM, int NV>
 __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     const ResNormParams p) {
-  constexpr bool AHEAD = NV * V <= 24;
+  constexpr bool AHEAD = NV * V <= (V == 1 ? 8 : 24);
   constexpr int THREADS = TEAM > 256 ? TEAM : 256, TEAMS = THREADS / TEAM;
   __shared__ float sh[THREADS / 64];
   __shared__ float red[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? TEAM * NV * V : 1];
@@ -400,33 +401,33 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
 // Any length and alignment: rows are walked twice by the block, dw is added up in the
 // block's own row of part.
 template <typename T, typename R>
-__global__ __launch_bounds__(256) void res_norm_bwd_walk_kernel(const ResNormParams p) {
-  __shared__ float sh[4];
+__global__ __launch_bounds__(kWalk) void res_norm_bwd_walk_kernel(const ResNormParams p) {
+  __shared__ float sh[kWalk / 64];
   const int64_t n = p.dim;
   float* mine = p.dw ? p.part + blockIdx.x * n : nullptr;
   if (mine)
-    for (int64_t k = threadIdx.x; k < n; k += 256) mine[k] = 0.0f;
+    for (int64_t k = threadIdx.x; k < n; k += kWalk) mine[k] = 0.0f;
   for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
     const R* res = static_cast<const R*>(p.res) + row_at(p, row, p.res_batch, p.res_row);
     const T* dout = static_cast<const T*>(p.dout) + row * n;
     float s2 = 0.0f, sv = 0.0f;
-    for (int64_t k = threadIdx.x; k < n; k += 256) {
+    for (int64_t k = threadIdx.x; k < n; k += kWalk) {
       const float v = Elem<R>::load1(res + k);
       s2 = __builtin_fmaf(v, v, s2);
       sv = __builtin_fmaf(Elem<T>::load1(dout + k) * (p.w ? p.w[k] : 1.0f), v, sv);
     }
-    s2 = team_join<256, false>(s2, sh);
-    sv = team_join<256, false>(sv, sh);
+    s2 = team_join<kWalk, false>(s2, sh);
+    sv = team_join<kWalk, false>(sv, sh);
     const float r = root_of(s2, p, [&](float sc) {
       float t2 = 0.0f;
-      for (int64_t k = threadIdx.x; k < n; k += 256) {
+      for (int64_t k = threadIdx.x; k < n; k += kWalk) {
         const float v = Elem<R>::load1(res + k) * sc;
         t2 = __builtin_fmaf(v, v, t2);
       }
-      return team_join<256, false>(t2, sh);
+      return team_join<kWalk, false>(t2, sh);
     });
     const float kk = r * (sv / (float)p.dim);
-    for (int64_t k = threadIdx.x; k < n; k += 256) {
+    for (int64_t k = threadIdx.x; k < n; k += kWalk) {
       const float hat = Elem<R>::load1(res + k) * r, dy = Elem<T>::load1(dout + k);
       const float g = p.dres ? Elem<R>::load1(static_cast<const R*>(p.dres) + row * n + k) : 0.0f;
       const float d = __builtin_fmaf(
@@ -475,10 +476,12 @@ hipError_t fwd_v(const ResNormParams& p, hipStream_t s) {
   if (nv <= 768) return fwd_go<T, R, FP8, V, 256, 3>(p, s);
   if (nv <= 1024) return fwd_go<T, R, FP8, V, 256, 4>(p, s);
   if (nv <= 2048) return fwd_go<T, R, FP8, V, 256, 8>(p, s);
-  if constexpr (V == 1)
+  if constexpr (V == 1) {
     if (nv <= 4096) return fwd_go<T, R, FP8, V, 256, 16>(p, s);
+    if (nv <= 8192) return fwd_go<T, R, FP8, V, 256, 32>(p, s);
+  }
   hipLaunchKernelGGL((res_norm_fwd_walk_kernel<T, R, FP8, V>),
-                     dim3((unsigned)(p.rows < kFwdBlocks ? p.rows : kFwdBlocks)), dim3(256), 0, s, p);
+                     dim3((unsigned)(p.rows < kFwdBlocks ? p.rows : kFwdBlocks)), dim3(kWalk), 0, s, p);
   return hipGetLastError();
 }
 
@@ -510,7 +513,9 @@ hipError_t bwd_v(const ResNormParams& p, hipStream_t s) {
   if (nv <= 1536) return bwd_go<T, R, V, 256, 6>(p, s);
   if (nv <= 2048) return bwd_go<T, R, V, 512, 4>(p, s);
   if (nv <= 4096) return bwd_go<T, R, V, 512, 8>(p, s);
-  hipLaunchKernelGGL((res_norm_bwd_walk_kernel<T, R>), dim3((unsigned)p.parts), dim3(256), 0, s, p);
+  if constexpr (V == 1)
+    if (nv <= 8192) return bwd_go<T, R, V, 512, 16>(p, s);
+  hipLaunchKernelGGL((res_norm_bwd_walk_kernel<T, R>), dim3((unsigned)p.parts), dim3(kWalk), 0, s, p);
   return hipGetLastError();
 }
 
