@@ -51,9 +51,10 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
   const uint32_t q = CHAIN ? rec_ticket(p.ticket, at, &sTicket) : 0;
   const uint32_t tile = tiles - 1 - q;                        // the last tile first
   const int64_t b = uniform(at / strips);
-  const uint32_t c = (at - (uint32_t)b * strips) * C + lane * V;
+  const uint32_t c0 = (at - (uint32_t)b * strips) * C, c = c0 + lane * V;
   const bool on = c < p.dim;
-  const uint32_t cl = on ? c : 0, cb = cl * (uint32_t)sizeof(T);
+  // a lane past the last channel reads, and waits for, the first of its own strip
+  const uint32_t cl = on ? c : c0, cb = cl * (uint32_t)sizeof(T);
   const int64_t t0 = ((int64_t)tile * waves + wave) * S;      // the wave's first step
   const int64_t left = p.L - t0;
   const int n = uniform(left >= S ? S : left > 0 ? (int)left : 0);   // its steps

@@ -132,8 +132,9 @@ __device__ __forceinline__ uint64_t rec_look(uint64_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Waits for the word at p, v what was seen there.  Who writes it took an earlier ticket,
-// so it runs already and waits only for earlier tickets itself: the wait ends.
+// Waits for the word at p, v what was seen there.  Who writes it took an earlier ticket of
+// the same strip, so it runs already and waits only for earlier tickets of that strip
+// itself: the wait ends.
 __device__ __forceinline__ uint64_t rec_wait(uint64_t* p, uint64_t v) {
   while (!(v >> 63)) {
     __builtin_amdgcn_s_sleep(1);
