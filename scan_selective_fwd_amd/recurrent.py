@@ -9,7 +9,9 @@ Activations are float32 or bfloat16, all the same; x, r, i, z and the norm's x
 and residual may be views of wider rows (their last dimension contiguous).
 Weights and states are float32.  Gradients have the type of the tensor they
 belong to, each rounded once from a float32 sum.  Every call only enqueues
-kernels on the current stream of its tensors' device.
+kernels on the current stream of its tensors' device, so it may be captured into a
+graph.  A backward through autograd is captured only once no eager graph of the same
+leaves is alive: the leaves' accumulation would run on that graph's stream.
 """
 from __future__ import annotations
 
@@ -263,34 +265,34 @@ def _residual_code(t, x):
 
 
 def _row_strides(t, name):
-    """Batch and row stride of a (..., dim) tensor, dense or a view: its rows are one run,
-    or one for each index of the first dimension."""
+    """Batch and row stride of a (..., dim) tensor, dense or a view: its rows are one run
+    (the batch stride is None then), or one for each index of the first dimension, of
+    whatever stride, a broadcast one's 0 too."""
     if t.is_contiguous():
-        return 0, t.shape[-1]
+        return None, t.shape[-1]
     for lead in (1, t.shape[0]):
         try:
             v = t.view(lead, -1, t.shape[-1])
         except RuntimeError:
             continue
         if t.shape[-1] == 1 or t.stride(-1) == 1:
-            return (v.stride(0) if lead > 1 else 0), (v.stride(1) if v.shape[1] > 1 else 0)
+            return (v.stride(0) if lead > 1 else None), (v.stride(1) if v.shape[1] > 1 else 0)
     raise ValueError(f"rows of {name} must be contiguous, and a step apart in each index of its "
                      "first dimension")
 
 
-def _planes(t, *views):
-    """(batch, rows, dim) of t: one run of rows where none of the strides needs more."""
+def _planes(t, a, b):
+    """(batch, rows, dim) of t, one run of rows where the views are, and the views' batch
+    and row strides among them."""
     dim = t.shape[-1]
     rows = t.numel() // dim if dim else 0
-    if not rows or not any(sb for sb, _ in views):
-        return (1 if rows else 0), rows, dim
-    return t.shape[0], rows // t.shape[0], dim
-
-
-def _in_planes(strides, batch, rows):
-    """The batch stride of rows that are one run, where another tensor's are not."""
-    sb, sr = strides
-    return (rows * sr if batch > 1 and sb == 0 else sb), sr
+    (ab, ar), (bb, br) = a, b
+    if ab is None and bb is None or not rows:
+        return (1 if rows else 0, rows, dim), (0, ar), (0, br)
+    batch = t.shape[0]
+    rows //= batch
+    return ((batch, rows, dim), (rows * ar if ab is None else ab, ar),
+            (rows * br if bb is None else bb, br))
 
 
 def _norm_args(x, residual, weight, residual_out):
@@ -299,7 +301,7 @@ def _norm_args(x, residual, weight, residual_out):
     code = rcode = _dtype_code(x)
     if not shape:
         raise ValueError("the norm needs at least one dimension")
-    sx, sr = _row_strides(x, "x"), (0, 0)
+    sx, sr = _row_strides(x, "x"), (None, 0)
     if residual is not None:
         if _gpu(residual, "residual") != dev:
             raise ValueError(f"residual is on {residual.device}, expected {dev}")
@@ -315,11 +317,9 @@ def _norm_args(x, residual, weight, residual_out):
             _req(residual_out, "residual_out", residual.dtype, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    batch, rows, dim = _planes(x, sx, sr)
-    if batch > 1:
-        sx, sr = _in_planes(sx, batch, rows), _in_planes(sr, batch, rows)
-    _req(weight, "weight", _F32, (dim,), dev)
-    return dev, code, rcode, sx, sr, (batch, rows, dim), residual_out
+    sizes, sx, sr = _planes(x, sx, sr)
+    _req(weight, "weight", _F32, sizes[2:], dev)
+    return dev, code, rcode, sx, sr, sizes, residual_out
 
 
 def residual_norm_fwd(x, residual=None, weight=None, *, eps=1e-5, out=None, residual_out=None):
@@ -371,8 +371,7 @@ def residual_norm_bwd(res, weight, dout, dres=None, *, eps=1e-5, workspace=None)
     code, rcode = _dtype_code(dout), _residual_code(res, dout)
     if not res.shape:
         raise ValueError("the norm needs at least one dimension")
-    sr = _row_strides(res, "res")
-    batch, rows, dim = _planes(res, sr)
+    (batch, rows, dim), sr, _ = _planes(res, _row_strides(res, "res"), (None, 0))
     _req(weight, "weight", _F32, (dim,), dev)
     _req(dout, "dout", dout.dtype, res.shape, dev)
     _req(dres, "dres", res.dtype, res.shape, dev)

@@ -334,3 +334,21 @@ def test_refusals(ms):
         ms.residual_norm_bwd(g["residual"].double(), g["weight"], g["dout"])
     with pytest.raises(ValueError):
         ms.residual_norm_bwd(g["residual"], g["weight"], g["dout"], workspace=torch.empty(64))
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("dim", [33, 1024])
+def test_a_batch_broadcast_from_one(ms, dim, types):
+    """Every batch row the same rows, in memory once: as x, as the residual, as both, and as
+    the backward's res."""
+    t = TYPES[types]
+    g = dev(R.norm_inputs(11, *t, 3, 7, dim), t)
+    one, two = g["x"][:1].expand(3, 7, dim), g["residual"][:1].expand(3, 7, dim)
+    for x, res in ((one, None), (one, g["residual"]), (g["x"], two), (one, two)):
+        full = None if res is None else res.contiguous()
+        for call in (ms.residual_norm_fwd, ms.residual_norm_fp8):
+            for p, q in zip(call(x, res, g["weight"]), call(x.contiguous(), full, g["weight"])):
+                assert torch.equal(p.float(), q.float())
+    p, q = (ms.residual_norm_bwd(r, g["weight"], g["dout"], g["dres"])
+            for r in (two, two.contiguous()))
+    assert all(torch.equal(p[k], q[k]) for k in p)

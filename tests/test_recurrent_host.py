@@ -168,6 +168,32 @@ def test_the_binding_refuses_before_any_call():
         ms.gated_recurrence_fwd_workspace_bytes(1, 2 ** 60, 64)
 
 
+def test_rows_of_views_are_where_the_strides_say():
+    """The norm's batch and row strides give each row of a view, and no element outside it:
+    broadcast batches and rows, slices, steps, and views together with dense tensors."""
+    from scan_selective_fwd_amd import recurrent as rec
+    wide = torch.arange(4 * 6 * 11, dtype=torch.float32).view(4, 6, 11)
+    views = [wide, wide[..., 2:7], wide[:, 1:4], wide[:, ::2], wide[:, 3:4], wide[1:2, 1:4],
+             wide[:1].expand(4, 6, 11), wide[:1, 2:5].expand(4, 3, 11), wide[:1].expand(1, 6, 11),
+             wide[:, :1].expand(4, 6, 11), wide[:1, :1].expand(4, 6, 11), wide[0], wide[0, 0],
+             wide[0, :1].expand(5, 11), wide[..., :1], wide[:1, :, :1].expand(4, 6, 1), wide[::2],
+             wide.view(2, 2, 6, 11), wide.view(4, 2, 3, 11)[:1].expand(3, 2, 3, 11)]
+    for v in views:
+        for other in (v.contiguous(), v):
+            sizes, a, b = rec._planes(v, rec._row_strides(v, "v"), rec._row_strides(other, "other"))
+            assert sizes[0] * sizes[1] * sizes[2] == v.numel()
+            for t, (sb, sr) in ((v, a), (other, b)):
+                last = (sizes[0] - 1) * sb + (sizes[1] - 1) * sr + sizes[2]
+                assert t.storage_offset() + last <= t.untyped_storage().nbytes() // 4
+                assert torch.equal(t.as_strided(sizes, (sb, sr, 1)).reshape(v.shape), t)
+    for v in (wide.transpose(1, 2), wide.transpose(0, 1), wide[..., ::2], wide[0, 0, ::2]):
+        try:
+            sizes, a, _ = rec._planes(v, rec._row_strides(v, "v"), (None, 0))
+        except ValueError:
+            continue
+        assert torch.equal(v.as_strided(sizes, (*a, 1)).reshape(v.shape), v)
+
+
 def test_kernels_keep_their_registers():
     """Two blocks of 8 waves share a CU at 128 registers a lane; nothing spills."""
     res = kernel_resources(os.path.join(ROOT, "scan_selective_fwd_amd", "libmamba_scan.so"))
