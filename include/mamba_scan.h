@@ -652,6 +652,8 @@ mamba_status mamba_gated_norm_bwd(const void* x, int64_t x_row_stride, const voi
  * Pointers are aligned to their element.  last_state may be h0 itself (the
  * state steps in place), not a part of it; no other output may overlap an
  * input.  Sums run in a fixed order: equal inputs give equal bits.
+ * The blocks of a call wait for one another through its workspace, which no
+ * other call may use until this one has ended.
  * ------------------------------------------------------------------------ */
 typedef struct mamba_recurrence_shape {
   int64_t batch, seqlen, dim;

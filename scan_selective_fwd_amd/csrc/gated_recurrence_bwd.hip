@@ -49,6 +49,7 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
   const uint32_t at = rec_strip(across, p.by_die);
   if (at >= across) return;
   const uint32_t q = CHAIN ? rec_ticket(p.ticket, at, &sTicket) : 0;
+  if (CHAIN && q >= tiles) return;      // another call took tickets here: none of ours is left
   const uint32_t tile = tiles - 1 - q;                        // the last tile first
   const int64_t b = uniform(at / strips);
   const uint32_t c0 = (at - (uint32_t)b * strips) * C, c = c0 + lane * V;

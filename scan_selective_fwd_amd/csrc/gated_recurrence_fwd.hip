@@ -50,7 +50,9 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
 
   const uint32_t at = rec_strip(across, p.by_die);
   if (at >= across) return;
+  const uint32_t tiles = CHAIN ? (uint32_t)((p.L + kRecFwdTile - 1) / kRecFwdTile) : 1;
   const uint32_t tile = CHAIN ? rec_ticket(p.ticket, at, &sTicket) : 0;
+  if (CHAIN && tile >= tiles) return;   // another call took tickets here: none of ours is left
   const int64_t b = uniform(at / strips);
   const uint32_t c0 = (at - (uint32_t)b * strips) * C, c = c0 + lane * V;
   const bool on = c < p.dim;
@@ -155,7 +157,6 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
 
   // the state that enters the tile
   if constexpr (CHAIN) {
-    const uint32_t tiles = (uint32_t)((p.L + kRecFwdTile - 1) / kRecFwdTile);
     const uint32_t groups = (tiles + G - 1) / G;
     rec_chain<V, G, kTileWaves>(p.maps + ((uint64_t)b * tiles + tile) * p.dim + cl,
                     p.heads + ((uint64_t)b * groups + tile / G) * p.dim + cl, p.dim, tile, At, Ht,

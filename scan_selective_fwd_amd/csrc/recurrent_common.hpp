@@ -134,9 +134,12 @@ __device__ __forceinline__ uint64_t rec_look(uint64_t* p) {
 
 // Waits for the word at p, v what was seen there.  Who writes it took an earlier ticket of
 // the same strip, so it runs already and waits only for earlier tickets of that strip
-// itself: the wait ends.
+// itself: the wait ends.  Where the words are lost, which takes another call on the same
+// workspace at the same time, it ends after many seconds, with a NaN.
+constexpr uint32_t kRecPatience = 1u << 24;
 __device__ __forceinline__ uint64_t rec_wait(uint64_t* p, uint64_t v) {
-  while (!(v >> 63)) {
+  for (uint32_t n = 0; !(v >> 63); ++n) {
+    if (n == kRecPatience) return (uint64_t)(kThere | kCutBits) << 32 | 0x7FC00000u;
     __builtin_amdgcn_s_sleep(1);
     v = rec_look(p);
   }

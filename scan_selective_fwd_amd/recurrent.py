@@ -141,8 +141,8 @@ def gated_recurrence_fwd(x, r, i, A, z=None, h0=None, *, reset=None, return_last
     left out.  `checkpoints`: a float32 tensor of
     gated_recurrence_checkpoint_shape that receives the state entering every
     64th step, for gated_recurrence_bwd.  `workspace`: a contiguous GPU tensor of
-    at least gated_recurrence_fwd_workspace_bytes, reused across calls
-    (allocated when absent or smaller)."""
+    at least gated_recurrence_fwd_workspace_bytes, reused across calls that follow
+    one another on a stream (allocated when absent or smaller)."""
     ref, fields, dev, shape = _shape(x, r, i, z)
     reset = _state_args(shape, A, h0, reset, dev)
     batch, L, dim = shape
