@@ -5,12 +5,14 @@
 //   d = dres + r (dhat - res r^2 mean(dhat res)),  dw = sum over rows of dout res r
 //
 // A team of 64 to 512 threads takes a row and keeps it in registers: every tensor is
-// read once and written once, and the largest value of 8 bits is found on the way.  Rows
-// too long for that are walked again from the cache.  Bound by HBM: the forward of 16384
-// rows of 1536 in bfloat16 takes 38 us (201 MB, 5.3 TB/s), of 4096 of 5120 on a float32
-// stream into 8 bits 47 (231 MB, 4.9 TB/s); the backward of 4096 of 5120 in bfloat16 29 to
-// 34 (168 MB, 5.0 TB/s or more), and 4 for the sum of dw.  Rows that do not start on 16
-// bytes are read element by element (4096 of 6001 take 118 us for 39).
+// read once and written once, all of a row's loads are in flight together, and the largest
+// value of 8 bits is found on the way.  Rows too long for that are walked again from the
+// cache.  Bound by HBM: the forward of 16384 rows of 1536 in bfloat16 takes 31 to 34 us (201
+// MB, 5.9 TB/s or more; 36 to 37 where each group's loads wait for those before), of 4096 of
+// 5120 on a float32 stream into 8 bits 38 to 40 (231 MB, 5.8; 47); the backward of 4096 of 5120
+// in bfloat16 29 to 32 (168 MB, 5.2), and 4 for the sum of dw.  Rows that start anywhere are
+// read as wide: 4096 of 6001 in bfloat16 take 32 us forward, 52 backward (element by element
+// 122 and 120), 2000 of 8191 24 and 36 (75 and 75).
 #include "recurrent_common.hpp"
 
 namespace mscan {
@@ -20,6 +22,10 @@ namespace {
 constexpr int kParts = 512;        // blocks of the backward: two a CU
 constexpr int kFwdBlocks = (1 << 22) - 1;   // of up to 1024 threads in one launch
 constexpr int kWalk = 1024;
+// Rows up to here go by single elements, one a lane: 27941 of 38 in bfloat16 take 8.0 us
+// forward and 13.5 backward (11.2 and 15.6 in groups), 16000 of 64 5.5 and 9.6 (6.7 and
+// 10.4); 64000 of 128 24 and 30 by two elements a lane, 20 and 30 in groups.
+constexpr int kNarrow = 64;
 
 // Where row `row` of a view starts.
 __device__ __forceinline__ int64_t row_at(const ResNormParams& p, int64_t row, int64_t batch,
@@ -81,6 +87,76 @@ __device__ __forceinline__ float root_of(float s2, const ResNormParams& p, F aga
   return sc / __builtin_sqrtf(again(sc) / n + p.eps * sc * sc);
 }
 
+// V elements of a row.  EVEN: every row starts on 16 bytes and is whole groups of V.
+// Otherwise the place is any element's: the memory takes wide accesses there too.
+template <bool EVEN, typename T, int V>
+struct Words {   // as they lie in memory: kept so while loads are in flight
+  static constexpr int N = V * sizeof(T) <= 4 ? 1 : V * sizeof(T) / 4;
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const void* p) {
+    constexpr int bytes = V * sizeof(T);
+    const void* q = __builtin_assume_aligned(p, !EVEN ? sizeof(T) : bytes < 16 ? bytes : 16);
+    if constexpr (bytes == 2) {
+      uint16_t one;
+      __builtin_memcpy(&one, q, 2);
+      w[0] = one;
+    } else {
+      __builtin_memcpy(w, q, bytes);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
+      else v[i] = i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    }
+  }
+};
+
+template <bool EVEN, typename T, int V>
+__device__ __forceinline__ void load_row(const void* p, int64_t at, float (&v)[V]) {
+  Words<EVEN, T, V> r;
+  r.load(static_cast<const T*>(p) + at);
+  r.get(v);
+}
+
+template <bool EVEN, typename T, int V>
+__device__ __forceinline__ void store_row(void* p, int64_t at, const float (&v)[V]) {
+  if constexpr (EVEN || V == 1) {
+    store_vec<T, V>(p, at, v);
+  } else if constexpr (sizeof(T) == 4) {
+    __builtin_memcpy(static_cast<T*>(p) + at, v, V * sizeof(T));
+  } else {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    __builtin_memcpy(static_cast<T*>(p) + at, w, V * sizeof(T));
+  }
+}
+
+// The group of V elements that a thread takes: `k0` by its number.  A row's last group ends
+// with the row, whatever that leaves of it: its first `drop` elements are another thread's
+// too, which counts them in its sums; both store the same values.
+template <bool EVEN, int V>
+struct Group {
+  uint32_t k;
+  int drop;
+  bool in;
+  __device__ __forceinline__ Group(uint32_t k0, uint32_t n) : k(k0), drop(0), in(k0 < n) {
+    if constexpr (!EVEN && V > 1) {
+      drop = (int)k0 - (int)(n - V);
+      if (drop > 0) k = n - V;
+    }
+  }
+  __device__ __forceinline__ float own(int v, float x) const {
+    return !EVEN && V > 1 && v < drop ? 0.0f : x;
+  }
+};
+
 // V values of x + residual as they are stored: the norm is of what the stream keeps, so
 // that the backward, which has only that, forms the same statistics.
 template <typename R, int V>
@@ -103,7 +179,7 @@ __device__ __forceinline__ void add_stored(float (&x)[V], const float (&r)[V]) {
 
 // To the nearest of e4m3, ties to even (v_cvt_pk_fp8_f32): |y| is at most 448 and one
 // unit of float32 in its last place, which rounds to 448; a NaN stays one.
-template <int V>
+template <bool EVEN, int V>
 __device__ __forceinline__ void store_e4m3(void* out, int64_t at, const float (&y)[V]) {
   uint8_t* q = static_cast<uint8_t*>(out) + at;
   if constexpr (V == 1) {
@@ -115,70 +191,97 @@ __device__ __forceinline__ void store_e4m3(void* out, int64_t at, const float (&
       int t = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k], y[4 * k + 1], 0, false);
       w[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k + 2], y[4 * k + 3], t, true);
     }
-    if constexpr (V == 4) *reinterpret_cast<uint32_t*>(q) = w[0];
+    if constexpr (!EVEN) __builtin_memcpy(q, w, V);
+    else if constexpr (V == 4) *reinterpret_cast<uint32_t*>(q) = w[0];
     else *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
   }
 }
 
-template <int V>
+template <bool EVEN, int V>
 __device__ __forceinline__ void load_weight(const float* w, int64_t at, float (&v)[V]) {
 #pragma unroll
   for (int k = 0; k < V; ++k) v[k] = 1.0f;
-  if (w) load_f32<V>(w, at, v);
+  if (w) load_row<EVEN, float, V>(w, at, v);
 }
 
-template <typename T, typename R, bool FP8, int V, int TEAM, int NV>
+template <typename T, typename R, bool FP8, bool EVEN, int V, int TEAM, int NV>
 __global__ __launch_bounds__(256) void res_norm_fwd_kernel(const ResNormParams p) {
   __shared__ float sh[4];
   constexpr int TEAMS = 256 / TEAM;
+  constexpr bool EARLY = NV * V <= 32;
   const int tid = threadIdx.x & (TEAM - 1);
   const int64_t n = p.dim;
-  for (int64_t row0 = (int64_t)blockIdx.x * TEAMS; row0 < p.rows; row0 += (int64_t)gridDim.x * TEAMS) {
+  const int64_t step = (int64_t)gridDim.x * TEAMS;
+  for (int64_t row0 = (int64_t)blockIdx.x * TEAMS; row0 < p.rows; row0 += step) {
     const int64_t row = row0 + threadIdx.x / TEAM;
     const bool on = row < p.rows;                 // whole teams
     const int64_t x0 = row_at(p, row, p.x_batch, p.x_row);
     const int64_t r0 = row_at(p, row, p.res_batch, p.res_row);
-    float x[NV][V], r[NV][V];
+    // every load of the row is in flight at once, the weights' too where there is room
+    Words<EVEN, T, V> xr[NV];
+    Words<EVEN, R, V> rr[NV];
+    float x[NV][V], w[NV][V];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t k = (int64_t)(j * TEAM + tid) * V;
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[j][v] = r[j][v] = 0.0f;
-      if (on && k < n) {
-        load_vec<T, V>(p.x, x0 + k, x[j]);
-        if (p.res) load_vec<R, V>(p.res, r0 + k, r[j]);
-      }
+      const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+      xr[j].zero();
+      if (on && g.in) xr[j].load(place<T>(p.x, x0, g.k));
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+      rr[j].zero();
+      if (p.res && on && g.in) rr[j].load(place<R>(p.res, r0, g.k));
+    }
+    auto weights = [&](int j) {
+      const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+#pragma unroll
+      for (int v = 0; v < V; ++v) w[j][v] = 1.0f;
+      if (p.w && g.in) load_row<EVEN, float, V>(place<float>(p.w, 0, g.k), 0, w[j]);
+    };
+    if constexpr (EARLY)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) weights(j);
     float s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (p.res) add_stored<R, V>(x[j], r[j]);
+      const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+      xr[j].get(x[j]);
+      if (p.res) {
+        float r[V];
+        rr[j].get(r);
+        add_stored<R, V>(x[j], r);
+      }
 #pragma unroll
-      for (int v = 0; v < V; ++v) s2 = __builtin_fmaf(x[j][v], x[j][v], s2);
+      for (int v = 0; v < V; ++v) {
+        const float t = g.own(v, x[j][v]);
+        s2 = __builtin_fmaf(t, t, s2);
+      }
     }
     s2 = team_join<TEAM, false>(s2, sh);
     const float root = root_of(s2, p, [&](float sc) {
       float t2 = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float t = x[j][v] * sc;
+          const float t = g.own(v, x[j][v]) * sc;
           t2 = __builtin_fmaf(t, t, t2);
         }
+      }
       return team_join<TEAM, false>(t2, sh);
     });
     float y[NV][V], most = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t k = (int64_t)(j * TEAM + tid) * V;
-      if (on && k < n) {
-        if (p.res) store_vec<R, V>(p.res_out, row * n + k, x[j]);
-        float w[V];
-        load_weight<V>(p.w, k, w);
+      const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+      if (on && g.in) {
+        if (p.res) store_row<EVEN, R, V>(p.res_out, row * n + g.k, x[j]);
+        if constexpr (!EARLY) weights(j);
 #pragma unroll
-        for (int v = 0; v < V; ++v) y[j][v] = x[j][v] * root * w[v];
-        if constexpr (!FP8) store_vec<T, V>(p.out, row * n + k, y[j]);
+        for (int v = 0; v < V; ++v) y[j][v] = x[j][v] * root * w[j][v];
+        if constexpr (!FP8) store_row<EVEN, T, V>(p.out, row * n + g.k, y[j]);
         else
 #pragma unroll
           for (int v = 0; v < V; ++v) most = __builtin_fmaxf(most, __builtin_fabsf(y[j][v]));
@@ -190,11 +293,11 @@ __global__ __launch_bounds__(256) void res_norm_fwd_kernel(const ResNormParams p
       if (on && tid == 0) p.scale[row] = most / 448.0f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int64_t k = (int64_t)(j * TEAM + tid) * V;
-        if (on && k < n) {
+        const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+        if (on && g.in) {
 #pragma unroll
           for (int v = 0; v < V; ++v) y[j][v] *= inv;
-          store_e4m3<V>(p.out, row * n + k, y[j]);
+          store_e4m3<EVEN, V>(p.out, row * n + g.k, y[j]);
         }
       }
     }
@@ -202,77 +305,84 @@ __global__ __launch_bounds__(256) void res_norm_fwd_kernel(const ResNormParams p
 }
 
 // Rows too long for the registers: walked two or three times by a block.
-template <typename T, typename R, bool FP8, int V>
+template <typename T, typename R, bool FP8, bool EVEN, int V>
 __global__ __launch_bounds__(kWalk) void res_norm_fwd_walk_kernel(const ResNormParams p) {
   __shared__ float sh[kWalk / 64];
   const int64_t n = p.dim;
+  // every group of V elements, and one by one what is left behind the last
+  auto walk = [&](auto step) {
+    float x[V], one[1];
+    int64_t k = (int64_t)threadIdx.x * V;
+    for (; k + V <= n; k += kWalk * V) step(k, x);
+    if constexpr (!EVEN) {
+      k = n / V * V + threadIdx.x;
+      if (k < n) step(k, one);
+    }
+  };
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const int64_t x0 = row_at(p, row, p.x_batch, p.x_row);
     const int64_t r0 = row_at(p, row, p.res_batch, p.res_row);
-    auto sum = [&](int64_t k, float (&x)[V]) {
-      float r[V];
-      load_vec<T, V>(p.x, x0 + k, x);
+    auto sum = [&](int64_t k, auto& x) {
+      constexpr int W = sizeof(x) / 4;
+      float r[W];
+      load_row<EVEN, T, W>(p.x, x0 + k, x);
       if (p.res) {
-        load_vec<R, V>(p.res, r0 + k, r);
-        add_stored<R, V>(x, r);
+        load_row<EVEN, R, W>(p.res, r0 + k, r);
+        add_stored<R, W>(x, r);
       }
     };
     auto squares = [&](float sc) {
       float s2 = 0.0f;
-      for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += kWalk * V) {
-        float x[V];
+      walk([&](int64_t k, auto& x) {
         sum(k, x);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float t = x[v] * sc;
-          s2 = __builtin_fmaf(t, t, s2);
-        }
-      }
+        for (float v : x) s2 = __builtin_fmaf(v * sc, v * sc, s2);
+      });
       return team_join<kWalk, false>(s2, sh);
     };
     const float root = root_of(squares(1.0f), p, squares);
-    auto normed = [&](int64_t k, float (&x)[V], float (&y)[V]) {
-      float w[V];
+    auto normed = [&](int64_t k, auto& x, auto& y) {
+      constexpr int W = sizeof(x) / 4;
+      float w[W];
       sum(k, x);
-      load_weight<V>(p.w, k, w);
+      load_weight<EVEN, W>(p.w, k, w);
 #pragma unroll
-      for (int v = 0; v < V; ++v) y[v] = x[v] * root * w[v];
+      for (int v = 0; v < W; ++v) y[v] = x[v] * root * w[v];
     };
     float inv = 1.0f;
     if constexpr (FP8) {
       float most = 0.0f;
-      for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += kWalk * V) {
-        float x[V], y[V];
-        normed(k, x, y);
-#pragma unroll
-        for (int v = 0; v < V; ++v) most = __builtin_fmaxf(most, __builtin_fabsf(y[v]));
-      }
+      walk([&](int64_t k, auto& x) {
+        normed(k, x, x);
+        for (float v : x) most = __builtin_fmaxf(most, __builtin_fabsf(v));
+      });
       most = __builtin_fmaxf(team_join<kWalk, true>(most, sh), 0x1p-100f);
       inv = 448.0f / most;
       if (threadIdx.x == 0) p.scale[row] = most / 448.0f;
     }
-    for (int64_t k = (int64_t)threadIdx.x * V; k < n; k += kWalk * V) {
-      float x[V], y[V];
+    walk([&](int64_t k, auto& x) {
+      constexpr int W = sizeof(x) / 4;
+      float y[W];
       normed(k, x, y);
-      if (p.res) store_vec<R, V>(p.res_out, row * n + k, x);
+      if (p.res) store_row<EVEN, R, W>(p.res_out, row * n + k, x);
       if constexpr (FP8) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) y[v] *= inv;
-        store_e4m3<V>(p.out, row * n + k, y);
+        for (int v = 0; v < W; ++v) y[v] *= inv;
+        store_e4m3<EVEN, W>(p.out, row * n + k, y);
       } else {
-        store_vec<T, V>(p.out, row * n + k, y);
+        store_row<EVEN, T, W>(p.out, row * n + k, y);
       }
-    }
+    });
   }
 }
 
 // Block `part`: its teams take every (parts * TEAMS)-th row, the next row's loads in
 // flight while one is worked on (where the registers hold both), and leave the block's
 // share of dw in part.
-template <typename T, typename R, int V, int TEAM, int NV>
+template <typename T, typename R, bool EVEN, int V, int TEAM, int NV>
 __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     const ResNormParams p) {
-  constexpr bool AHEAD = NV * V <= (V == 1 ? 8 : 24);
+  constexpr bool AHEAD = NV * V <= 24;
+  static_assert(EVEN || AHEAD, "a row is read whole before any of it is written");
   constexpr int THREADS = TEAM > 256 ? TEAM : 256, TEAMS = THREADS / TEAM;
   __shared__ float sh[THREADS / 64];
   __shared__ float red[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? TEAM * NV * V : 1];
@@ -281,35 +391,35 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
   float w[NV][V], dw[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
+    const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       w[j][v] = 1.0f;
       dw[j][v] = 0.0f;
     }
-    if (AHEAD && p.w && k < n) load_f32<V>(static_cast<const float*>(place<float>(p.w, 0, k)), 0, w[j]);
+    if (AHEAD && p.w && g.in) load_row<EVEN, float, V>(place<float>(p.w, 0, g.k), 0, w[j]);
   }
-  Raw<R, V> xr[NV], gr[NV];
-  Raw<T, V> yr[NV];
+  Words<EVEN, R, V> xr[NV], gr[NV];
+  Words<EVEN, T, V> yr[NV];
   auto load = [&](int64_t row) {
     const int64_t r0 = row_at(p, row, p.res_batch, p.res_row);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
+      const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
       xr[j].zero();
       yr[j].zero();
-      if (k < n && row < p.rows) {
-        xr[j].load(place<R>(p.res, r0, k), 0);
-        yr[j].load(place<T>(p.dout, row * n, k), 0);
+      if (g.in && row < p.rows) {
+        xr[j].load(place<R>(p.res, r0, g.k));
+        yr[j].load(place<T>(p.dout, row * n, g.k));
       }
     }
   };
   auto load_dres = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
+      const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
       gr[j].zero();
-      if (p.dres && k < n && row < p.rows) gr[j].load(place<R>(p.dres, row * n, k), 0);
+      if (p.dres && g.in && row < p.rows) gr[j].load(place<R>(p.dres, row * n, g.k));
     }
   };
   const int64_t step = p.parts * TEAMS;
@@ -320,14 +430,14 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
   // every team walks as long as the first: the joins wait for whole blocks
   for (int64_t row0 = blockIdx.x * (int64_t)TEAMS; row0 < p.rows; row0 += step) {
     const int64_t row = row0 + team;
-    float x[NV][V], dy[NV][V], g[NV][V];
+    float x[NV][V], dy[NV][V], ds[NV][V];
     float s2 = 0.0f, sv = 0.0f;
     if (!AHEAD) load(row);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       xr[j].get(x[j]);
       yr[j].get(dy[j]);
-      if (AHEAD) gr[j].get(g[j]);
+      if (AHEAD) gr[j].get(ds[j]);
     }
     if (AHEAD) {
       load(row + step);
@@ -335,28 +445,33 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     } else {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {       // from the cache, row by row
-        const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
-        if (p.w && k < n) load_f32<V>(static_cast<const float*>(place<float>(p.w, 0, k)), 0, w[j]);
+        const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+        if (p.w && g.in) load_row<EVEN, float, V>(place<float>(p.w, 0, g.k), 0, w[j]);
       }
     }
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        s2 = __builtin_fmaf(x[j][v], x[j][v], s2);
-        sv = __builtin_fmaf(dy[j][v] * w[j][v], x[j][v], sv);
+        const float t = g.own(v, x[j][v]);
+        s2 = __builtin_fmaf(t, t, s2);
+        sv = __builtin_fmaf(g.own(v, dy[j][v] * w[j][v]), t, sv);
       }
+    }
     s2 = team_join<TEAM, false>(s2, sh);
     sv = team_join<TEAM, false>(sv, sh);
     const float r = root_of(s2, p, [&](float sc) {
       float t2 = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float t = x[j][v] * sc;
+          const float t = g.own(v, x[j][v]) * sc;
           t2 = __builtin_fmaf(t, t, t2);
         }
+      }
       return team_join<TEAM, false>(t2, sh);
     });
     const float kk = r * (sv / (float)p.dim);
@@ -366,18 +481,19 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
+      const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
       float d[V];
-      if (!AHEAD) gr[j].get(g[j]);
+      if (!AHEAD) gr[j].get(ds[j]);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float hat = x[j][v] * r;
-        d[v] = __builtin_fmaf(r, __builtin_fmaf(-hat, kk, dy[j][v] * w[j][v]), g[j][v]);
+        d[v] = __builtin_fmaf(r, __builtin_fmaf(-hat, kk, dy[j][v] * w[j][v]), ds[j][v]);
         dw[j][v] = __builtin_fmaf(dy[j][v], hat, dw[j][v]);
       }
-      if (k < n && row < p.rows) {
-        store_vec<T, V>(place<T>(p.dx, row * n, k), 0, d);
-        if (sizeof(T) != sizeof(R) && p.dresidual) store_vec<R, V>(place<R>(p.dresidual, row * n, k), 0, d);
+      if (g.in && row < p.rows) {
+        store_row<EVEN, T, V>(place<T>(p.dx, row * n, g.k), 0, d);
+        if (sizeof(T) != sizeof(R) && p.dresidual)
+          store_row<EVEN, R, V>(place<R>(p.dresidual, row * n, g.k), 0, d);
       }
     }
   }
@@ -391,59 +507,83 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     __syncthreads();
     for (int i = threadIdx.x; i < TEAM * NV * V; i += THREADS) {
       const int jv = i / TEAM, lane = i - jv * TEAM;
-      const int64_t k = (int64_t)((jv / V) * TEAM + lane) * V + jv % V;
+      const Group<EVEN, V> g(((jv / V) * TEAM + lane) * V, (uint32_t)n);
       float sum = red[0][i];
 #pragma unroll
       for (int m = 1; m < TEAMS; ++m) sum += red[m][i];
-      if (k < n) mine[k] = sum;
+      if (g.in) mine[g.k + jv % V] = sum;
     }
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint32_t k = (uint32_t)(j * TEAM + tid) * V;
-      if (k < n) store_vec<float, V>(mine, k, dw[j]);
+      const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+      if (g.in) store_row<EVEN, float, V>(mine, g.k, dw[j]);
     }
   }
 }
 
 // Any length and alignment: rows are walked twice by the block, dw is added up in the
-// block's own row of part.
+// block's own row of part, each thread at its own places.
 template <typename T, typename R>
 __global__ __launch_bounds__(kWalk) void res_norm_bwd_walk_kernel(const ResNormParams p) {
+  constexpr int V = 4;
   __shared__ float sh[kWalk / 64];
   const int64_t n = p.dim;
   float* mine = p.dw ? p.part + blockIdx.x * n : nullptr;
-  if (mine)
-    for (int64_t k = threadIdx.x; k < n; k += kWalk) mine[k] = 0.0f;
+  // every group of V elements, and one by one what is left behind the last
+  auto walk = [&](auto step) {
+    float x[V], one[1];
+    int64_t k = (int64_t)threadIdx.x * V;
+    for (; k + V <= n; k += kWalk * V) step(k, x);
+    k = n / V * V + threadIdx.x;
+    if (k < n) step(k, one);
+  };
   for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
-    const R* res = static_cast<const R*>(p.res) + row_at(p, row, p.res_batch, p.res_row);
-    const T* dout = static_cast<const T*>(p.dout) + row * n;
+    const int64_t r0 = row_at(p, row, p.res_batch, p.res_row), d0 = row * n;
     float s2 = 0.0f, sv = 0.0f;
-    for (int64_t k = threadIdx.x; k < n; k += kWalk) {
-      const float v = Elem<R>::load1(res + k);
-      s2 = __builtin_fmaf(v, v, s2);
-      sv = __builtin_fmaf(Elem<T>::load1(dout + k) * (p.w ? p.w[k] : 1.0f), v, sv);
-    }
+    walk([&](int64_t k, auto& x) {
+      constexpr int W = sizeof(x) / 4;
+      float dy[W], w[W];
+      load_row<false, R, W>(p.res, r0 + k, x);
+      load_row<false, T, W>(p.dout, d0 + k, dy);
+      load_weight<false, W>(p.w, k, w);
+#pragma unroll
+      for (int v = 0; v < W; ++v) {
+        s2 = __builtin_fmaf(x[v], x[v], s2);
+        sv = __builtin_fmaf(dy[v] * w[v], x[v], sv);
+      }
+    });
     s2 = team_join<kWalk, false>(s2, sh);
     sv = team_join<kWalk, false>(sv, sh);
     const float r = root_of(s2, p, [&](float sc) {
       float t2 = 0.0f;
-      for (int64_t k = threadIdx.x; k < n; k += kWalk) {
-        const float v = Elem<R>::load1(res + k) * sc;
-        t2 = __builtin_fmaf(v, v, t2);
-      }
+      walk([&](int64_t k, auto& x) {
+        load_row<false, R, sizeof(x) / 4>(p.res, r0 + k, x);
+        for (float v : x) t2 = __builtin_fmaf(v * sc, v * sc, t2);
+      });
       return team_join<kWalk, false>(t2, sh);
     });
     const float kk = r * (sv / (float)p.dim);
-    for (int64_t k = threadIdx.x; k < n; k += kWalk) {
-      const float hat = Elem<R>::load1(res + k) * r, dy = Elem<T>::load1(dout + k);
-      const float g = p.dres ? Elem<R>::load1(static_cast<const R*>(p.dres) + row * n + k) : 0.0f;
-      const float d = __builtin_fmaf(
-          r, __builtin_fmaf(-hat, kk, dy * (p.w ? p.w[k] : 1.0f)), g);
-      Elem<T>::store1(static_cast<T*>(p.dx) + row * n + k, d);
-      if (p.dresidual) Elem<R>::store1(static_cast<R*>(p.dresidual) + row * n + k, d);
-      if (mine) mine[k] = __builtin_fmaf(dy, hat, mine[k]);
-    }
+    walk([&](int64_t k, auto& x) {
+      constexpr int W = sizeof(x) / 4;
+      float dy[W], w[W], ds[W], dw[W], d[W];
+      load_row<false, R, W>(p.res, r0 + k, x);
+      load_row<false, T, W>(p.dout, d0 + k, dy);
+      load_weight<false, W>(p.w, k, w);
+#pragma unroll
+      for (int v = 0; v < W; ++v) ds[v] = dw[v] = 0.0f;
+      if (p.dres) load_row<false, R, W>(p.dres, d0 + k, ds);
+      if (mine && row != blockIdx.x) load_row<false, float, W>(mine, k, dw);
+#pragma unroll
+      for (int v = 0; v < W; ++v) {
+        const float hat = x[v] * r;
+        d[v] = __builtin_fmaf(r, __builtin_fmaf(-hat, kk, dy[v] * w[v]), ds[v]);
+        dw[v] = __builtin_fmaf(dy[v], hat, dw[v]);
+      }
+      store_row<false, T, W>(p.dx, d0 + k, d);
+      if (p.dresidual) store_row<false, R, W>(p.dresidual, d0 + k, d);
+      if (mine) store_row<false, float, W>(mine, k, dw);
+    });
   }
 }
 
@@ -465,71 +605,72 @@ __global__ __launch_bounds__(1024) void res_norm_sum_kernel(const ResNormParams 
   }
 }
 
-template <typename T, typename R, bool FP8, int V, int TEAM, int NV>
+template <typename T, typename R, bool FP8, bool EVEN, int V, int TEAM, int NV>
 hipError_t fwd_go(const ResNormParams& p, hipStream_t s) {
   const int64_t blocks = (p.rows + 256 / TEAM - 1) / (256 / TEAM);
-  hipLaunchKernelGGL((res_norm_fwd_kernel<T, R, FP8, V, TEAM, NV>),
+  hipLaunchKernelGGL((res_norm_fwd_kernel<T, R, FP8, EVEN, V, TEAM, NV>),
                      dim3((unsigned)(blocks < kFwdBlocks ? blocks : kFwdBlocks)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
-template <typename T, typename R, bool FP8, int V>
+template <typename T, typename R, bool FP8, bool EVEN>
 hipError_t fwd_v(const ResNormParams& p, hipStream_t s) {
+  constexpr int V = sizeof(T) == 4 ? 4 : 8;
   const int64_t nv = (p.dim + V - 1) / V;
-  if (nv <= 64) return fwd_go<T, R, FP8, V, 64, 1>(p, s);
-  if (nv <= 128) return fwd_go<T, R, FP8, V, 64, 2>(p, s);
-  if (nv <= 192) return fwd_go<T, R, FP8, V, 64, 3>(p, s);
-  if (nv <= 256) return fwd_go<T, R, FP8, V, 64, 4>(p, s);
-  if (nv <= 512) return fwd_go<T, R, FP8, V, 256, 2>(p, s);
-  if (nv <= 768) return fwd_go<T, R, FP8, V, 256, 3>(p, s);
-  if (nv <= 1024) return fwd_go<T, R, FP8, V, 256, 4>(p, s);
-  if (nv <= 2048) return fwd_go<T, R, FP8, V, 256, 8>(p, s);
-  if constexpr (V == 1) {
-    if (nv <= 4096) return fwd_go<T, R, FP8, V, 256, 16>(p, s);
-    if (nv <= 8192) return fwd_go<T, R, FP8, V, 256, 32>(p, s);
-  }
-  hipLaunchKernelGGL((res_norm_fwd_walk_kernel<T, R, FP8, V>),
+  if (nv <= 64) return fwd_go<T, R, FP8, EVEN, V, 64, 1>(p, s);
+  if (nv <= 128) return fwd_go<T, R, FP8, EVEN, V, 64, 2>(p, s);
+  if (nv <= 192) return fwd_go<T, R, FP8, EVEN, V, 64, 3>(p, s);
+  if (nv <= 256) return fwd_go<T, R, FP8, EVEN, V, 64, 4>(p, s);
+  if (nv <= 512) return fwd_go<T, R, FP8, EVEN, V, 256, 2>(p, s);
+  if (nv <= 768) return fwd_go<T, R, FP8, EVEN, V, 256, 3>(p, s);
+  if (nv <= 1024) return fwd_go<T, R, FP8, EVEN, V, 256, 4>(p, s);
+  if (nv <= 2048) return fwd_go<T, R, FP8, EVEN, V, 256, 8>(p, s);
+  hipLaunchKernelGGL((res_norm_fwd_walk_kernel<T, R, FP8, EVEN, V>),
                      dim3((unsigned)(p.rows < kFwdBlocks ? p.rows : kFwdBlocks)), dim3(kWalk), 0, s, p);
   return hipGetLastError();
 }
 
 template <typename T, typename R>
 hipError_t fwd_t(const ResNormParams& p, bool fp8, hipStream_t s) {
-  constexpr int V = sizeof(T) == 4 ? 4 : 8;
-  if (p.vec) return fp8 ? fwd_v<T, R, true, V>(p, s) : fwd_v<T, R, false, V>(p, s);
-  return fp8 ? fwd_v<T, R, true, 1>(p, s) : fwd_v<T, R, false, 1>(p, s);
+  if (p.dim <= kNarrow)
+    return fp8 ? fwd_go<T, R, true, false, 1, 64, 1>(p, s)
+               : fwd_go<T, R, false, false, 1, 64, 1>(p, s);
+  if (p.vec) return fp8 ? fwd_v<T, R, true, true>(p, s) : fwd_v<T, R, false, true>(p, s);
+  return fp8 ? fwd_v<T, R, true, false>(p, s) : fwd_v<T, R, false, false>(p, s);
 }
 
-template <typename T, typename R, int V, int TEAM, int NV>
+template <typename T, typename R, bool EVEN, int V, int TEAM, int NV>
 hipError_t bwd_go(const ResNormParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((res_norm_bwd_kernel<T, R, V, TEAM, NV>), dim3((unsigned)p.parts),
+  hipLaunchKernelGGL((res_norm_bwd_kernel<T, R, EVEN, V, TEAM, NV>), dim3((unsigned)p.parts),
                      dim3(TEAM > 256 ? TEAM : 256), 0, s, p);
   return hipGetLastError();
 }
 
-template <typename T, typename R, int V>
+template <typename T, typename R, bool EVEN>
 hipError_t bwd_v(const ResNormParams& p, hipStream_t s) {
+  constexpr int V = 4;
   const int64_t nv = (p.dim + V - 1) / V;
-  if (nv <= 64) return bwd_go<T, R, V, 64, 1>(p, s);
-  if (nv <= 128) return bwd_go<T, R, V, 64, 2>(p, s);
-  if (nv <= 192) return bwd_go<T, R, V, 64, 3>(p, s);
-  if (nv <= 256) return bwd_go<T, R, V, 256, 1>(p, s);
-  if (nv <= 512) return bwd_go<T, R, V, 256, 2>(p, s);
-  if (nv <= 768) return bwd_go<T, R, V, 256, 3>(p, s);
-  if (nv <= 1024) return bwd_go<T, R, V, 256, 4>(p, s);
-  if (nv <= 1280) return bwd_go<T, R, V, 256, 5>(p, s);
-  if (nv <= 1536) return bwd_go<T, R, V, 256, 6>(p, s);
-  if (nv <= 2048) return bwd_go<T, R, V, 512, 4>(p, s);
-  if (nv <= 4096) return bwd_go<T, R, V, 512, 8>(p, s);
-  if constexpr (V == 1)
-    if (nv <= 8192) return bwd_go<T, R, V, 512, 16>(p, s);
+  if (nv <= 64) return bwd_go<T, R, EVEN, V, 64, 1>(p, s);
+  if (nv <= 128) return bwd_go<T, R, EVEN, V, 64, 2>(p, s);
+  if (nv <= 192) return bwd_go<T, R, EVEN, V, 64, 3>(p, s);
+  if (nv <= 256) return bwd_go<T, R, EVEN, V, 256, 1>(p, s);
+  if (nv <= 512) return bwd_go<T, R, EVEN, V, 256, 2>(p, s);
+  if (nv <= 768) return bwd_go<T, R, EVEN, V, 256, 3>(p, s);
+  if (nv <= 1024) return bwd_go<T, R, EVEN, V, 256, 4>(p, s);
+  if (nv <= 1280) return bwd_go<T, R, EVEN, V, 256, 5>(p, s);
+  if (nv <= 1536) return bwd_go<T, R, EVEN, V, 256, 6>(p, s);
+  if (nv <= 2048) return bwd_go<T, R, EVEN, V, 512, 4>(p, s);
+  if constexpr (EVEN)    // the others would spill
+    if (nv <= 4096) return bwd_go<T, R, EVEN, V, 512, 8>(p, s);
   hipLaunchKernelGGL((res_norm_bwd_walk_kernel<T, R>), dim3((unsigned)p.parts), dim3(kWalk), 0, s, p);
   return hipGetLastError();
 }
 
 template <typename T, typename R>
 hipError_t bwd_t(const ResNormParams& p, hipStream_t s) {
-  const hipError_t e = p.vec ? bwd_v<T, R, 4>(p, s) : bwd_v<T, R, 1>(p, s);
+  const hipError_t e = p.dim <= kNarrow ? bwd_go<T, R, false, 1, 64, 1>(p, s)
+                       : p.vec          ? bwd_v<T, R, true>(p, s)
+                                        : bwd_v<T, R, false>(p, s);
   if (e != hipSuccess || !p.dw) return e;
   hipLaunchKernelGGL(res_norm_sum_kernel, dim3((unsigned)((p.dim + 63) / 64)), dim3(1024), 0, s, p);
   return hipGetLastError();

@@ -352,3 +352,44 @@ def test_a_batch_broadcast_from_one(ms, dim, types):
     p, q = (ms.residual_norm_bwd(r, g["weight"], g["dout"], g["dres"])
             for r in (two, two.contiguous()))
     assert all(torch.equal(p[k], q[k]) for k in p)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("dim", [1, 3, 4, 5, 7, 8, 9, 13, 63, 64, 65, 128, 129, 132, 255, 511,
+                                 513, 770, 1025, 1537, 2046, 2049, 4099, 6001, 8191, 8194,
+                                 16381, 16387])
+def test_rows_that_start_anywhere(ms, dim, types):
+    """Widths around whole groups: a row's last group ends with it, and nothing beside the
+    rows is written."""
+    t = TYPES[types]
+    i = R.norm_inputs(12, *t, 5, dim)
+    g = dev(i, t)
+
+    def inside(like, dtype=None):     # a tensor between values that have to stay
+        n, dtype = like.numel(), dtype or like.dtype
+        wide = torch.full((n + 64,), 3.0, device="cuda").to(dtype)
+        return wide, wide[32:32 + n].view(like.shape)
+
+    for shift in (0, 1):              # with rows of whole groups too
+        w, x = inside(torch.empty(5 * dim + shift, dtype=t[0], device="cuda"))
+        x = x[shift:].view(5, dim).copy_(g["x"])
+        (wo, out), (wr, kept), (w8, o8) = (inside(g["x"]), inside(g["residual"]),
+                                           inside(g["x"], torch.float8_e4m3fn))
+        kept.copy_(g["residual"])
+        _, res = ms.residual_norm_fwd(x, kept, g["weight"], out=out, residual_out=kept)
+        check_res(res, i["x"] + i["residual"], t[1])
+        y = R.norm_fwd(res.double().cpu(), None, i["weight"], EPS, t[1])[0]
+        R.check("out", out, y)
+        kept.copy_(g["residual"])
+        _, scale, again = ms.residual_norm_fp8(x, kept, g["weight"], out=o8, residual_out=kept)
+        assert torch.equal(again, res)
+        check_fp8(o8, scale, y)
+        for wide in (wo, wr, w8):
+            ends = torch.cat([wide[:32].float(), wide[-32:].float()])
+            assert bool((ends == 3.0).all())
+    got = ms.residual_norm_bwd(g["residual"], g["weight"], g["dout"], g["dres"])
+    d, dw, dw_abs = R.norm_bwd(i["residual"], i["weight"], i["dout"], i["dres"], EPS)
+    terms = R.norm_terms(i["residual"], i["weight"], i["dout"], i["dres"], EPS)
+    R.check("dx", got["dx"], d, terms)
+    R.check("dresidual", got["dresidual"], d, terms)
+    R.check("dweight", got["dweight"], dw, dw_abs)
