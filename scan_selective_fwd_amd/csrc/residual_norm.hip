@@ -461,7 +461,7 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     }
     s2 = team_join<TEAM, false>(s2, sh);
     sv = team_join<TEAM, false>(sv, sh);
-    const float r = root_of(s2, p, [&](float sc) {
+    float r = root_of(s2, p, [&](float sc) {
       float t2 = 0.0f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -474,6 +474,8 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
       }
       return team_join<TEAM, false>(t2, sh);
     });
+    // a team without a row has zeros, and without eps no root of them: it adds nothing to dw
+    if (TEAMS > 1 && row >= p.rows) r = 0.0f;
     const float kk = r * (sv / (float)p.dim);
     if (!AHEAD) {
       mem_fence_compiler();                // not before the sums, which need registers
