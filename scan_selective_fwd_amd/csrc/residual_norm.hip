@@ -77,13 +77,15 @@ __device__ __forceinline__ float team_join(float a, float* sh) {
 }
 
 // 1 / sqrt(mean of squares + eps) from their sum.  Where that passes float32's range (or
-// vanishes beside an eps that does), `again` forms it from values times a scale.
+// vanishes beside an eps that does), `again` forms it from values times a scale: 2^28
+// squares of up to (2^128 2^-90)^2 stay below 2^104, and of a sum past the range the root
+// mean square is 2^50 at least, times the scale 2^-40.
 template <typename F>
 __device__ __forceinline__ float root_of(float s2, const ResNormParams& p, F again) {
   const float n = (float)p.dim;
   if (__builtin_expect(s2 < 3e38f && (s2 > 0x1p-80f || p.eps > 0x1p-90f), 1))
     return 1.0f / __builtin_sqrtf(s2 / n + p.eps);
-  const float sc = s2 < 1.0f ? 0x1p70f : 0x1p-70f;
+  const float sc = s2 < 1.0f ? 0x1p70f : 0x1p-90f;
   return sc / __builtin_sqrtf(again(sc) / n + p.eps * sc * sc);
 }
 

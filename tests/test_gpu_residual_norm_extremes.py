@@ -1,4 +1,5 @@
-"""The residual norm where its statistics come near the ends of float32 or vanish."""
+"""The residual norm where its statistics come near the ends of float32 or vanish: no eps,
+and rows whose squares' sum passes the type's range."""
 import pytest
 import torch
 
@@ -36,3 +37,31 @@ def test_backward_without_eps(ms, rows, dim, types):
     kind = dict(x=t[0], dout=t[0], residual=t[1], dres=t[1], weight=torch.float32)
     g = {k: v.to(kind[k]).cuda() for k, v in i.items()}
     check_bwd(ms.residual_norm_bwd(g["residual"], g["weight"], g["dout"], g["dres"], eps=0.0), i, 0.0)
+
+
+def extreme_rows(dim, dtype):
+    """Rows whose squares' sum leaves float32, or vanishes."""
+    top = torch.finfo(torch.bfloat16).max            # what masks are made of; float32 has it too
+    sign = 1.0 - 2.0 * (torch.arange(dim) % 3 == 0)
+    x = torch.stack([sign * top, torch.full((dim,), -top), sign * 1e37, sign * 1e18, sign * 0,
+                     sign * 1e-30, sign * 2.0 ** -120])
+    x[4, dim // 2] = -3e19
+    return R.stored(x, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dim", [5, 64, 2048, 5120, 6001, 8191, 12000, 16392])
+def test_forward_of_extreme_rows(ms, dim, dtype):
+    """Every row is finite, and so is its norm.  eps = 0: also where the squares vanish."""
+    x = extreme_rows(dim, dtype)
+    w = 1 + 0.3 * torch.randn(dim, generator=torch.Generator().manual_seed(1)).double()
+    w = w.float().double()
+    for eps in (1e-5, 0.0):
+        g = x.to(dtype).cuda()
+        out, _ = ms.residual_norm_fwd(g, None, w.float().cuda(), eps=eps)
+        o8, scale, _ = ms.residual_norm_fp8(g, None, w.float().cuda(), eps=eps)
+        y, _, _ = R.norm_fwd(x, None, w, eps, dtype)
+        for k in range(len(x)):
+            R.check(f"row {k}", out[k], y[k])
+            R.check(f"scale {k}", scale[k], torch.clamp_min(y[k].abs().max(), 2.0 ** -100) / 448)
+            R.check(f"row {k} in 8 bits", o8[k], y[k] / scale[k].double().cpu())
