@@ -80,13 +80,27 @@ __device__ __forceinline__ float team_join(float a, float* sh) {
 // vanishes beside an eps that does), `again` forms it from values times a scale: 2^28
 // squares of up to (2^128 2^-90)^2 stay below 2^104, and of a sum past the range the root
 // mean square is 2^50 at least, times the scale 2^-40.
+__device__ __forceinline__ bool in_range(float s2, const ResNormParams& p) {
+  return __builtin_expect(s2 < 3e38f && (s2 > 0x1p-80f || p.eps > 0x1p-90f), 1);
+}
 template <typename F>
 __device__ __forceinline__ float root_of(float s2, const ResNormParams& p, F again) {
   const float n = (float)p.dim;
-  if (__builtin_expect(s2 < 3e38f && (s2 > 0x1p-80f || p.eps > 0x1p-90f), 1))
+  if (in_range(s2, p))
     return 1.0f / __builtin_sqrtf(s2 / n + p.eps);
   const float sc = s2 < 1.0f ? 0x1p70f : 0x1p-90f;
   return sc / __builtin_sqrtf(again(sc) / n + p.eps * sc * sc);
+}
+
+// The mean of dhat times the normed row, from sv = sum(dhat res) and r.  Where a product
+// or a sum passes float32's range, or the squares did, `again` forms the sum from res r,
+// whose values are sqrt(dim) at most.
+template <typename F>
+__device__ __forceinline__ float mean_of(float sv, float s2, float r, const ResNormParams& p,
+                                         F again) {
+  const float n = (float)p.dim;
+  if (in_range(s2, p) && __builtin_expect(__builtin_fabsf(sv) < 3e38f, 1)) return r * (sv / n);
+  return again() / n;
 }
 
 // V elements of a row.  EVEN: every row starts on 16 bytes and is whole groups of V.
@@ -478,7 +492,17 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     });
     // a team without a row has zeros, and without eps no root of them: it adds nothing to dw
     if (TEAMS > 1 && row >= p.rows) r = 0.0f;
-    const float kk = r * (sv / (float)p.dim);
+    const float kk = mean_of(sv, s2, r, p, [&]() {
+      float t = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          t = __builtin_fmaf(g.own(v, dy[j][v] * w[j][v]), x[j][v] * r, t);
+      }
+      return team_join<TEAM, false>(t, sh);
+    });
     if (!AHEAD) {
       mem_fence_compiler();                // not before the sums, which need registers
       load_dres(row);
@@ -567,7 +591,19 @@ __global__ __launch_bounds__(kWalk) void res_norm_bwd_walk_kernel(const ResNormP
       });
       return team_join<kWalk, false>(t2, sh);
     });
-    const float kk = r * (sv / (float)p.dim);
+    const float kk = mean_of(sv, s2, r, p, [&]() {
+      float t = 0.0f;
+      walk([&](int64_t k, auto& x) {
+        constexpr int W = sizeof(x) / 4;
+        float dy[W], w[W];
+        load_row<false, R, W>(p.res, r0 + k, x);
+        load_row<false, T, W>(p.dout, d0 + k, dy);
+        load_weight<false, W>(p.w, k, w);
+#pragma unroll
+        for (int v = 0; v < W; ++v) t = __builtin_fmaf(dy[v] * w[v], x[v] * r, t);
+      });
+      return team_join<kWalk, false>(t, sh);
+    });
     walk([&](int64_t k, auto& x) {
       constexpr int W = sizeof(x) / 4;
       float dy[W], w[W], ds[W], dw[W], d[W];

@@ -1,5 +1,5 @@
 """The residual norm where its statistics come near the ends of float32 or vanish: no eps,
-and rows whose squares' sum passes the type's range."""
+and rows whose squares' or products' sums pass the type's range."""
 import pytest
 import torch
 
@@ -65,3 +65,30 @@ def test_forward_of_extreme_rows(ms, dim, dtype):
             R.check(f"row {k}", out[k], y[k])
             R.check(f"scale {k}", scale[k], torch.clamp_min(y[k].abs().max(), 2.0 ** -100) / 448)
             R.check(f"row {k} in 8 bits", o8[k], y[k] / scale[k].double().cpu())
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("dim", [5, 256, 768, 2048, 6001, 8191, 12000, 16392])
+def test_backward_of_extreme_rows(ms, dim, types):
+    """The gradient at out is large where the row is, so that neither side of the
+    comparison is lost below float32's normal values."""
+    t = TYPES[types]
+    x = extreme_rows(dim, t[1])
+    i = R.norm_inputs(22, *t, len(x), dim)
+    size = torch.tensor([1e20, 1e20, 1e25, 1e5, 1e5, 1, 1]).double()
+    i.update(residual=x, dout=R.stored(i["dout"] * size[:, None], t[0]), dres=None)
+    g = {k: v.to(d).cuda() for k, v, d in (("residual", i["residual"], t[1]),
+                                           ("dout", i["dout"], t[0]),
+                                           ("weight", i["weight"], torch.float32))}
+    for eps in (1e-5, 0.0):
+        got = ms.residual_norm_bwd(g["residual"], g["weight"], g["dout"], eps=eps)
+        d, _, _ = R.norm_bwd(i["residual"], i["weight"], i["dout"], None, eps)
+        terms = R.norm_terms(i["residual"], i["weight"], i["dout"], None, eps)
+        for n in range(len(x)):
+            one = {k: i[k][n:n + 1] for k in ("residual", "dout")}
+            R.check(f"dx {n}", got["dx"][n], d[n], terms[n])
+            R.check(f"dresidual {n}", got["dresidual"][n], d[n], terms[n])
+            alone = ms.residual_norm_bwd(g["residual"][n:n + 1], g["weight"], g["dout"][n:n + 1],
+                                         eps=eps)
+            _, dw, dw_abs = R.norm_bwd(one["residual"], i["weight"], one["dout"], None, eps)
+            R.check(f"dweight {n}", alone["dweight"], dw, dw_abs)
