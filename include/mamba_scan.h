@@ -720,7 +720,8 @@ mamba_status mamba_residual_norm_fwd(const void* x, int64_t x_batch_stride, int6
 /* The same with out in 8 bits, e4m3 (4 exponent bits, 3 mantissa bits, largest
  * value 448, no infinities), and a float32 scale a row:
  *   scale = max(max|out|, 2^-100) / 448, the maximum over values that are not NaN,
- *   out8 = out / scale, to the nearest, ties to even; a NaN stays one. */
+ *   out8 = out / scale, the quotient in float32 rounded to the nearest, ties to
+ *   even; a NaN stays one. */
 mamba_status mamba_residual_norm_fp8(const void* x, int64_t x_batch_stride, int64_t x_row_stride,
                                      const void* residual, int64_t residual_batch_stride,
                                      int64_t residual_row_stride, const float* weight,

@@ -1,5 +1,6 @@
 """The residual norm where its statistics come near the ends of float32 or vanish: no eps,
-and rows whose squares' or products' sums pass the type's range."""
+and rows whose squares' or products' sums pass the type's range; and what its 8 bits
+are rounded from."""
 import pytest
 import torch
 
@@ -92,3 +93,22 @@ def test_backward_of_extreme_rows(ms, dim, types):
                                          eps=eps)
             _, dw, dw_abs = R.norm_bwd(one["residual"], i["weight"], one["dout"], None, eps)
             R.check(f"dweight {n}", alone["dweight"], dw, dw_abs)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dim", [40, 512, 1003, 2048, 6001, 16392])
+def test_eight_bits_are_the_quotient_by_the_scale(ms, dim, dtype):
+    """Bit by bit.  Quarters up to 7: their squares' sum is exact in any order, so that the
+    float32 call's out is what the 8-bit call divides; over 7 / 448 many of them lie within
+    a unit of float32 of the middle between two values of 8 bits."""
+    r = torch.Generator().manual_seed(23)
+    x = torch.randint(-28, 29, (300, dim), generator=r).float() / 4
+    x[:, 0] = 7
+    for w in (None, torch.randn(dim, generator=r).cuda()):
+        y, _ = ms.residual_norm_fwd(x.cuda(), None, w)
+        out, scale, _ = ms.residual_norm_fp8(x.to(dtype).cuda(), None, w)
+        want = y.cpu().abs().amax(-1) / 448
+        assert torch.equal(scale.cpu(), want)
+        q = (y.cpu() / want[:, None]).to(torch.float8_e4m3fn)
+        far = out.cpu().float() != q.float()
+        assert not far.any(), (int(far.sum()), far.numel())
