@@ -124,11 +124,11 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
       a[s][v] = g.a;
       by_x[s][v] = rec_sqrt(g.m2) * g.si;
       u[s][v] = by_x[s][v] * xr[s].get(v);
-      by_i[s][v] = u[s][v] * (1.0f - g.si);
+      by_i[s][v] = u[s][v] * g.i.complement();
       y[s][v] = g.lg * kLn2;
       const float ym = y[s][v] * fast_rcp(__builtin_fmaxf(g.m2, 1e-37f));
       own[s][v] = u[s][v] * g.a * ym;
-      by_r[s][v] = 1.0f - g.sr;
+      by_r[s][v] = g.r.complement();
       H[v] = rec_apply(g.a, u[s][v], cut, H[v]);
       A[v] *= g.a;
     }
@@ -267,9 +267,12 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
     if (n == S) grads(S);
     else grads(n);
   }
+  // the lane's channel again, from the lane's number: kept over the gates, it would be spilled
+  const uint32_t zero = opaque_int(0);
+  const uint32_t end = c0 + __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero)) * V;
   if (t0 == 0 && p.dh0 && on)
 #pragma unroll
-    for (int v = 0; v < V; ++v) p.dh0[b * p.dim + c + v] = after[v];
+    for (int v = 0; v < V; ++v) p.dh0[b * p.dim + end + v] = after[v];
   // the tile's share of dA, its runs added in order
 #pragma unroll
   for (int v = 0; v < V; ++v) sH[wave][lane * V + v] = sum[v];
@@ -279,7 +282,7 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
     for (int v = 0; v < V; ++v) {
       float s = sum[v];
       for (int w = 1; w < waves; ++w) s += sH[w][lane * V + v];
-      p.part[((int64_t)b * tiles + tile) * p.dim + c + v] = s;
+      p.part[((int64_t)b * tiles + tile) * p.dim + end + v] = s;
     }
 }
 

@@ -20,8 +20,20 @@ constexpr float kOneMinus2 = 0.0554646403f;
 constexpr float kOneMinus3 = 0.0094645340f;
 constexpr float kOneMinus4 = 0.0010833843f;
 
+// A sigmoid s(v) = 1 / (1 + e), e = exp(-v), and its complement 1 - s(v) = e s(v): the
+// difference would keep few digits of an open gate's, or none.  A gate so far shut that e is
+// infinite and s is 0 gives 0, which stands beside factors that are 0 there.
+struct RecSigmoid {
+  float s, e;
+  __device__ __forceinline__ explicit RecSigmoid(float v) : e(fast_exp(-v)) {
+    s = fast_rcp(1.0f + e);
+  }
+  __device__ __forceinline__ float complement() const { return __builtin_fminf(e, 1e38f) * s; }
+};
+
 // The gates of one step and what they make of it.
 struct RecGate {
+  RecSigmoid r, i;
   float sr, si;   // sigmoids of r and i
   float lg;       // log2 of the decay
   float a;        // the decay
@@ -41,9 +53,9 @@ __device__ __forceinline__ float rec_log2(float A) {
 // A2 = rec_log2(A).  1 - a^2 is formed without cancellation: from the polynomial where
 // a^2 is above e^(-1/2), from a itself below, where it keeps at least 0.39.
 __device__ __forceinline__ RecGate rec_gate(float r, float i, float A2) {
-  RecGate g;
-  g.sr = sigmoid(r);
-  g.si = sigmoid(i);
+  RecGate g{RecSigmoid(r), RecSigmoid(i)};
+  g.sr = g.r.s;
+  g.si = g.i.s;
   g.lg = A2 * g.sr;
   g.a = fast_exp2(g.lg);
   const float z = g.lg + g.lg;
