@@ -107,7 +107,8 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
   // gradient at a state and y the log of its decay
   //   dx = g m s(i),  di = g u (1 - s(i)),  u = m s(i) x
   //   d(log a) y = g a (y before - u a y / m^2),  dr of it times 1 - s(r)
-  // y / m^2 is -1/2 where the decay is 1, and u vanishes there
+  // y / m^2 is -1/2 where the decay is 1, and u vanishes there; m^2 is held at float32's
+  // smallest normal value, below which y loses its digits
   float a[S][V], u[S][V], A[V], H[V];
   float by_x[S][V], by_i[S][V], y[S][V], own[S][V], by_r[S][V];
 #pragma unroll
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
       u[s][v] = by_x[s][v] * xr[s].get(v);
       by_i[s][v] = u[s][v] * g.i.complement();
       y[s][v] = g.lg * kLn2;
-      const float ym = y[s][v] * fast_rcp(__builtin_fmaxf(g.m2, 1e-37f));
+      const float ym = y[s][v] * fast_rcp(__builtin_fmaxf(g.m2, 0x1p-126f));
       own[s][v] = u[s][v] * g.a * ym;
       by_r[s][v] = g.r.complement();
       H[v] = rec_apply(g.a, u[s][v], cut, H[v]);

@@ -1,5 +1,5 @@
-"""Gradients of the gated linear recurrence's gates where they are nearly open,
-each element against its own size.  Every step is a sequence of its own, so that
+"""Gradients of the gated linear recurrence's gates where they are nearly open or nearly
+shut, each element against its own size.  Every step is a sequence of its own, so that
 dr and di are products, without a sum that would hide a small one behind large ones."""
 import pytest
 import torch
@@ -63,3 +63,13 @@ def test_gates_nearly_open(ms, size, dtype):
     n, got, dr, di = run(ms, 41, dtype, size, (6, 30), (6, 30))
     close("di", got["di"], di, n["i"], BY_I, DT[dtype])
     close("dr", got["dr"], dr, n["r"], BY_R, DT[dtype])
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("size", [(70, 1, 66), (2, 100, 130), (2, 700, 33)])
+def test_gates_nearly_shut(ms, size, dtype):
+    """Log decays down to 2^-126, the smallest normal number, 1 - a^2 above it."""
+    n, got, dr, di = run(ms, 42, dtype, size, (-84, -20), (-20, 2))
+    # beside a gate's own exponential there is the other's: |r| at half in m, |i|
+    close("di", got["di"], di, n["i"], BY_I + 42, DT[dtype])
+    close("dr", got["dr"], dr, n["r"], BY_R + 20, DT[dtype])
