@@ -335,7 +335,9 @@ __global__ __launch_bounds__(256) void res_norm_fwd_kernel(const ResNormParams p
   }
 }
 
-// Rows too long for the registers: walked two or three times by a block.
+// Rows too long for the registers: walked two or three times by a block.  A thread's share
+// of a sum has no bound on its terms and is held in 64 bits (in 32 a row of 2^28 squares lost
+// 6e-5 of their sum: small ones beside a large sum are rounded to nothing).
 template <typename T, typename R, bool FP8, bool EVEN, int V>
 __global__ __launch_bounds__(kWalk) void res_norm_fwd_walk_kernel(const ResNormParams p) {
   __shared__ float sh[kWalk / 64];
@@ -363,12 +365,14 @@ __global__ __launch_bounds__(kWalk) void res_norm_fwd_walk_kernel(const ResNormP
       }
     };
     auto squares = [&](float sc) {
-      float s2 = 0.0f;
+      double s2 = 0.0;
       walk([&](int64_t k, auto& x) {
+        float t = 0.0f;
         sum(k, x);
-        for (float v : x) s2 = __builtin_fmaf(v * sc, v * sc, s2);
+        for (float v : x) t = __builtin_fmaf(v * sc, v * sc, t);
+        s2 += t;
       });
-      return team_join<kWalk, false>(s2, sh);
+      return team_join<kWalk, false>((float)s2, sh);
     };
     const float root = root_of(squares(1.0f), p, squares);
     auto normed = [&](int64_t k, auto& x, auto& y) {
@@ -564,8 +568,9 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
   }
 }
 
-// Any length and alignment: rows are walked twice by the block, dw is added up in the
-// block's own row of part, each thread at its own places.
+// Any length and alignment: rows are walked twice by the block, sums held as in the
+// forward's walk; dw is added up in the block's own row of part, each thread at its own
+// places.
 template <typename T, typename R>
 __global__ __launch_bounds__(kWalk) void res_norm_bwd_walk_kernel(const ResNormParams p) {
   constexpr int V = 4;
@@ -582,41 +587,46 @@ __global__ __launch_bounds__(kWalk) void res_norm_bwd_walk_kernel(const ResNormP
   };
   for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
     const int64_t r0 = row_at(p, row, p.res_batch, p.res_row), d0 = row * n;
-    float s2 = 0.0f, sv = 0.0f;
+    double s2d = 0.0, svd = 0.0;
     walk([&](int64_t k, auto& x) {
       constexpr int W = sizeof(x) / 4;
-      float dy[W], w[W];
+      float dy[W], w[W], t2 = 0.0f, tv = 0.0f;
       load_row<false, R, W>(p.res, r0 + k, x);
       load_row<false, T, W>(p.dout, d0 + k, dy);
       load_weight<false, W>(p.w, k, w);
 #pragma unroll
       for (int v = 0; v < W; ++v) {
-        s2 = __builtin_fmaf(x[v], x[v], s2);
-        sv = __builtin_fmaf(dy[v] * w[v], x[v], sv);
+        t2 = __builtin_fmaf(x[v], x[v], t2);
+        tv = __builtin_fmaf(dy[v] * w[v], x[v], tv);
       }
+      s2d += t2;
+      svd += tv;
     });
-    s2 = team_join<kWalk, false>(s2, sh);
-    sv = team_join<kWalk, false>(sv, sh);
+    const float s2 = team_join<kWalk, false>((float)s2d, sh);
+    const float sv = team_join<kWalk, false>((float)svd, sh);
     const float r = root_of(s2, p, [&](float sc) {
-      float t2 = 0.0f;
+      double t2 = 0.0;
       walk([&](int64_t k, auto& x) {
+        float t = 0.0f;
         load_row<false, R, sizeof(x) / 4>(p.res, r0 + k, x);
-        for (float v : x) t2 = __builtin_fmaf(v * sc, v * sc, t2);
+        for (float v : x) t = __builtin_fmaf(v * sc, v * sc, t);
+        t2 += t;
       });
-      return team_join<kWalk, false>(t2, sh);
+      return team_join<kWalk, false>((float)t2, sh);
     });
     const float kk = mean_of(sv, s2, r, p, [&]() {
-      float t = 0.0f;
+      double t = 0.0;
       walk([&](int64_t k, auto& x) {
         constexpr int W = sizeof(x) / 4;
-        float dy[W], w[W];
+        float dy[W], w[W], tv = 0.0f;
         load_row<false, R, W>(p.res, r0 + k, x);
         load_row<false, T, W>(p.dout, d0 + k, dy);
         load_weight<false, W>(p.w, k, w);
 #pragma unroll
-        for (int v = 0; v < W; ++v) t = __builtin_fmaf(dy[v] * w[v], x[v] * r, t);
+        for (int v = 0; v < W; ++v) tv = __builtin_fmaf(dy[v] * w[v], x[v] * r, tv);
+        t += tv;
       });
-      return team_join<kWalk, false>(t, sh);
+      return team_join<kWalk, false>((float)t, sh);
     });
     walk([&](int64_t k, auto& x) {
       constexpr int W = sizeof(x) / 4;
