@@ -288,11 +288,13 @@ __global__ __launch_bounds__(CHAIN ? kTileWaves * 64 : kMaxWaves * 64, 4) void r
 }
 
 // dA: the tiles' shares added in a fixed order, in 64 bits; 32 slices of them by 32
-// channels.
-__global__ __launch_bounds__(1024) void rec_sum_kernel(const RecParams p, const int64_t parts) {
+// channels, from channel c0 on.
+constexpr int kSumChannels = 32, kSumThreads = 1024;
+__global__ __launch_bounds__(kSumThreads) void rec_sum_kernel(const RecParams p, const int64_t parts,
+                                                              const int64_t c0) {
   __shared__ double red[32][33];
   const int cl = threadIdx.x & 31, sl = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + cl;
+  const int64_t c = c0 + (int64_t)blockIdx.x * kSumChannels + cl;
   double sum = 0.0;
   if (c < p.dim) {
 #pragma unroll 4
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(1024) void rec_sum_kernel(const RecParams p, const 
   sum = red[ch][at];
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
-  const int64_t to = (int64_t)blockIdx.x * 32 + ch;
+  const int64_t to = c0 + (int64_t)blockIdx.x * kSumChannels + ch;
   if (at == 0 && to < p.dim) p.dA[to] = (float)sum / p.A[to];   // the shares are A times too large
 }
 
@@ -324,10 +326,15 @@ hipError_t go(RecParams p, hipStream_t s) {
                        dim3(kTileWaves * 64), 0, s, p);
   }
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rec_sum_kernel, dim3((unsigned)((p.dim + 31) / 32)), dim3(1024), 0, s, p,
-                     p.batch * tiles);
-  return hipGetLastError();
+  // as many launches as hold the channels: one, up to 2^27 - 32 of them
+  constexpr int64_t most = kSumChannels * max_blocks(kSumThreads);
+  for (int64_t c0 = 0; c0 < p.dim && e == hipSuccess; c0 += most) {
+    const int64_t n = p.dim - c0 < most ? p.dim - c0 : most;
+    hipLaunchKernelGGL(rec_sum_kernel, dim3((unsigned)((n + kSumChannels - 1) / kSumChannels)),
+                       dim3(kSumThreads), 0, s, p, p.batch * tiles, c0);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 // Single elements: pairs would take more registers than let two blocks share a CU.

@@ -651,11 +651,13 @@ __global__ __launch_bounds__(kWalk) void res_norm_bwd_walk_kernel(const ResNormP
   }
 }
 
-// dw: the parts summed in order, 16 slices of them by 64 channels.
-__global__ __launch_bounds__(1024) void res_norm_sum_kernel(const ResNormParams p) {
+// dw: the parts summed in order, 16 slices of them by 64 channels, from channel c0 on.
+constexpr int kSumChannels = 64, kSumThreads = 1024;
+__global__ __launch_bounds__(kSumThreads) void res_norm_sum_kernel(const ResNormParams p,
+                                                                   const int64_t c0) {
   __shared__ float red[16][64];
   const int cl = threadIdx.x & 63, sl = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + cl;
+  const int64_t c = c0 + (int64_t)blockIdx.x * kSumChannels + cl;
   float sum = 0.0f;
   if (c < p.dim) {
 #pragma unroll 8
@@ -732,12 +734,19 @@ hipError_t bwd_v(const ResNormParams& p, hipStream_t s) {
 
 template <typename T, typename R>
 hipError_t bwd_t(const ResNormParams& p, hipStream_t s) {
-  const hipError_t e = p.dim <= kNarrow ? bwd_go<T, R, false, 1, 64, 1>(p, s)
-                       : p.vec          ? bwd_v<T, R, true>(p, s)
-                                        : bwd_v<T, R, false>(p, s);
-  if (e != hipSuccess || !p.dw) return e;
-  hipLaunchKernelGGL(res_norm_sum_kernel, dim3((unsigned)((p.dim + 63) / 64)), dim3(1024), 0, s, p);
-  return hipGetLastError();
+  hipError_t e = p.dim <= kNarrow ? bwd_go<T, R, false, 1, 64, 1>(p, s)
+                 : p.vec          ? bwd_v<T, R, true>(p, s)
+                                  : bwd_v<T, R, false>(p, s);
+  if (!p.dw) return e;
+  // as many launches as hold the channels: one, up to 2^28 - 64 of them
+  constexpr int64_t most = kSumChannels * max_blocks(kSumThreads);
+  for (int64_t c0 = 0; c0 < p.dim && e == hipSuccess; c0 += most) {
+    const int64_t n = p.dim - c0 < most ? p.dim - c0 : most;
+    hipLaunchKernelGGL(res_norm_sum_kernel, dim3((unsigned)((n + kSumChannels - 1) / kSumChannels)),
+                       dim3(kSumThreads), 0, s, p, c0);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace
