@@ -740,7 +740,8 @@ size_t mamba_residual_norm_bwd_workspace_size(int64_t rows, int64_t dim);
  *              / sqrt(mean(res^2) + eps)
  * dx in dt.  dresidual (nullable) in residual_dt; refused where residual_dt is
  * dt (it is dx).  dweight is required with weight.  The row statistics are
- * formed again; sums run in a fixed order. */
+ * formed again; sums run in a fixed order.  Where a row's sum of squares stays
+ * within float32, its sum of dout w res has to as well. */
 mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_batch_stride,
                                      int64_t res_row_stride, const float* weight,
                                      const void* dout, const void* dres, int64_t batch,

@@ -92,16 +92,27 @@ __device__ __forceinline__ float root_of(float s2, const ResNormParams& p, F aga
   return sc / __builtin_sqrtf(again(sc) / n + p.eps * sc * sc);
 }
 
-// The mean of dhat times the normed row, from sv = sum(dhat res) and r.  Where a product
-// or a sum passes float32's range, or the squares did, `again` forms the sum from res r,
-// whose values are sqrt(dim) at most.
-template <typename F>
-__device__ __forceinline__ float mean_of(float sv, float s2, float r, const ResNormParams& p,
-                                         F again) {
-  const float n = (float)p.dim;
-  if (in_range(s2, p) && __builtin_expect(__builtin_fabsf(sv) < 3e38f, 1)) return r * (sv / n);
-  return again() / n;
-}
+// What the backward takes of a row's two sums: r = 1 / sqrt(mean(res^2) + eps), and
+// mean(dhat res) r, the mean of dhat times the normed row.  Where the squares' sum passes
+// float32's range, `squares` forms r as root_of does, and `normed` the second sum from res r,
+// whose values are sqrt(dim) at most.  `on`: whether there is a row; the zeros of none have
+// no root without eps, and are to add nothing to dw.
+struct RowGrad {
+  float r, kk;
+  template <typename F, typename G>
+  __device__ __forceinline__ RowGrad(float s2, float sv, const ResNormParams& p, bool on, F squares,
+                                     G normed) {
+    const float n = (float)p.dim;
+    if (in_range(s2, p)) {
+      r = 1.0f / __builtin_sqrtf(s2 / n + p.eps);
+      kk = r * (sv / n);
+    } else {
+      r = root_of(s2, p, squares);
+      if (!on) r = 0.0f;
+      kk = normed(r) / n;
+    }
+  }
+};
 
 // V elements of a row.  EVEN: every row starts on 16 bytes and is whole groups of V.
 // Otherwise the place is any element's: the memory takes wide accesses there too.
@@ -214,19 +225,18 @@ __device__ __forceinline__ void store_e4m3(void* out, int64_t at, const float (&
 }
 
 // What a row's values are divided by for 8 bits: its scale, at least 2^-100 / 448.  The
-// quotients are those that a division rounds to: a first one by the reciprocal, and its
-// remainder's share added (times the reciprocal alone 2.4 % of rows of quarters up to 7
-// went to the other neighbour of a middle).  An infinite scale leaves no remainder: values
-// over it are zeros, infinities NaN.
+// quotient is the sum of the products with a reciprocal in two floats, rounded once (the
+// product with one took 2.4 % of rows of quarters up to 7 to the other neighbour of a
+// middle).  Over an infinite scale finite values are zeros, infinities NaN.
 struct RowScale {
-  float scale, inv, by;
+  float scale, hi, lo;
   __device__ __forceinline__ explicit RowScale(float most)
-      : scale(__builtin_fmaxf(most, 0x1p-100f) / 448.0f), inv(1.0f / scale),
-        by(scale < __builtin_inff() ? scale : 0.0f) {}
-  __device__ __forceinline__ float over(float y) const {
-    const float q = y * inv;
-    return __builtin_fmaf(__builtin_fmaf(-q, by, y), inv, q);
+      : scale(__builtin_fmaxf(most, 0x1p-100f) / 448.0f) {
+    const float by = scale < __builtin_inff() ? scale : 0.0f, first = fast_rcp(scale);
+    hi = __builtin_fmaf(__builtin_fmaf(-by, first, 1.0f), first, first);
+    lo = __builtin_fmaf(-by, hi, 1.0f) * hi;
   }
+  __device__ __forceinline__ float over(float y) const { return __builtin_fmaf(y, hi, y * lo); }
 };
 
 template <bool EVEN, int V>
@@ -495,32 +505,33 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void res_norm_bwd_kernel(
     }
     s2 = team_join<TEAM, false>(s2, sh);
     sv = team_join<TEAM, false>(sv, sh);
-    float r = root_of(s2, p, [&](float sc) {
-      float t2 = 0.0f;
+    const RowGrad row_grad(
+        s2, sv, p, TEAMS == 1 || row < p.rows,
+        [&](float sc) {
+          float t2 = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+          for (int j = 0; j < NV; ++j) {
+            const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float t = g.own(v, x[j][v]) * sc;
-          t2 = __builtin_fmaf(t, t, t2);
-        }
-      }
-      return team_join<TEAM, false>(t2, sh);
-    });
-    // a team without a row has zeros, and without eps no root of them: it adds nothing to dw
-    if (TEAMS > 1 && row >= p.rows) r = 0.0f;
-    const float kk = mean_of(sv, s2, r, p, [&]() {
-      float t = 0.0f;
+            for (int v = 0; v < V; ++v) {
+              const float t = g.own(v, x[j][v]) * sc;
+              t2 = __builtin_fmaf(t, t, t2);
+            }
+          }
+          return team_join<TEAM, false>(t2, sh);
+        },
+        [&](float r) {
+          float t = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
+          for (int j = 0; j < NV; ++j) {
+            const Group<EVEN, V> g((j * TEAM + tid) * V, (uint32_t)n);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          t = __builtin_fmaf(g.own(v, dy[j][v] * w[j][v]), x[j][v] * r, t);
-      }
-      return team_join<TEAM, false>(t, sh);
-    });
+            for (int v = 0; v < V; ++v)
+              t = __builtin_fmaf(g.own(v, dy[j][v] * w[j][v]), x[j][v] * r, t);
+          }
+          return team_join<TEAM, false>(t, sh);
+        });
+    const float r = row_grad.r, kk = row_grad.kk;
     if (!AHEAD) {
       mem_fence_compiler();                // not before the sums, which need registers
       load_dres(row);
@@ -604,30 +615,33 @@ __global__ __launch_bounds__(kWalk) void res_norm_bwd_walk_kernel(const ResNormP
     });
     const float s2 = team_join<kWalk, false>((float)s2d, sh);
     const float sv = team_join<kWalk, false>((float)svd, sh);
-    const float r = root_of(s2, p, [&](float sc) {
-      double t2 = 0.0;
-      walk([&](int64_t k, auto& x) {
-        float t = 0.0f;
-        load_row<false, R, sizeof(x) / 4>(p.res, r0 + k, x);
-        for (float v : x) t = __builtin_fmaf(v * sc, v * sc, t);
-        t2 += t;
-      });
-      return team_join<kWalk, false>((float)t2, sh);
-    });
-    const float kk = mean_of(sv, s2, r, p, [&]() {
-      double t = 0.0;
-      walk([&](int64_t k, auto& x) {
-        constexpr int W = sizeof(x) / 4;
-        float dy[W], w[W], tv = 0.0f;
-        load_row<false, R, W>(p.res, r0 + k, x);
-        load_row<false, T, W>(p.dout, d0 + k, dy);
-        load_weight<false, W>(p.w, k, w);
+    const RowGrad row_grad(
+        s2, sv, p, true,
+        [&](float sc) {
+          double t2 = 0.0;
+          walk([&](int64_t k, auto& x) {
+            float t = 0.0f;
+            load_row<false, R, sizeof(x) / 4>(p.res, r0 + k, x);
+            for (float v : x) t = __builtin_fmaf(v * sc, v * sc, t);
+            t2 += t;
+          });
+          return team_join<kWalk, false>((float)t2, sh);
+        },
+        [&](float r) {
+          double t = 0.0;
+          walk([&](int64_t k, auto& x) {
+            constexpr int W = sizeof(x) / 4;
+            float dy[W], w[W], tv = 0.0f;
+            load_row<false, R, W>(p.res, r0 + k, x);
+            load_row<false, T, W>(p.dout, d0 + k, dy);
+            load_weight<false, W>(p.w, k, w);
 #pragma unroll
-        for (int v = 0; v < W; ++v) tv = __builtin_fmaf(dy[v] * w[v], x[v] * r, tv);
-        t += tv;
-      });
-      return team_join<kWalk, false>((float)t, sh);
-    });
+            for (int v = 0; v < W; ++v) tv = __builtin_fmaf(dy[v] * w[v], x[v] * r, tv);
+            t += tv;
+          });
+          return team_join<kWalk, false>((float)t, sh);
+        });
+    const float r = row_grad.r, kk = row_grad.kk;
     walk([&](int64_t k, auto& x) {
       constexpr int W = sizeof(x) / 4;
       float dy[W], w[W], ds[W], dw[W], d[W];
