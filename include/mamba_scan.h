@@ -690,7 +690,8 @@ mamba_status mamba_gated_recurrence_bwd(const mamba_recurrence_shape* shape, con
                                         size_t workspace_bytes, void* stream);
 
 /* One step (shape->seqlen must be 1; the batch strides apply), in place on a
- * pool of states (pool, dim), with slots as for mamba_heads_state_update. */
+ * pool of states (pool, dim), with slots as for mamba_heads_state_update.  out
+ * may not overlap the pool, nor the pool an input. */
 mamba_status mamba_gated_recurrence_update(const mamba_recurrence_shape* shape, float* state,
                                            const int32_t* slots, int64_t pool, const void* x,
                                            const void* r, const void* i, const float* A,

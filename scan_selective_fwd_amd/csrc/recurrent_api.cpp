@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "mamba_scan.h"
 #include "recurrent.hpp"
 
@@ -89,18 +91,40 @@ mamba_status check_inputs(const mamba_recurrence_shape* s, const void* x, const 
   return MAMBA_OK;
 }
 
-// Whether a dense output of the sequence's size lies over one of its inputs.
-bool over_inputs(const void* out, const mamba_recurrence_shape* s, const void* x, const void* r,
-                 const void* i, const void* z) {
-  const size_t es = (size_t)esize(s->dtype);
-  const size_t n = (size_t)(s->batch * s->seqlen * s->dim) * es;
-  auto span = [&](int64_t sb, int64_t st) {
-    return (size_t)((s->batch - 1) * sb + (s->seqlen - 1) * st + s->dim) * es;
-  };
-  return overlap(out, n, x, span(s->x_batch_stride, s->x_token_stride)) ||
-         overlap(out, n, r, span(s->r_batch_stride, s->r_token_stride)) ||
-         overlap(out, n, i, span(s->i_batch_stride, s->i_token_stride)) ||
-         overlap(out, n, z, span(s->z_batch_stride, s->z_token_stride));
+// Bytes that a call reads or writes; of an absent tensor p is null.
+struct Region {
+  const void* p;
+  size_t n;
+};
+
+// Whether one of the outputs lies over one of the inputs.
+bool over_inputs(std::initializer_list<Region> outputs, std::initializer_list<Region> inputs) {
+  for (const Region& o : outputs)
+    for (const Region& i : inputs)
+      if (overlap(o.p, o.n, i.p, i.n)) return true;
+  return false;
+}
+
+size_t sequence_bytes(const mamba_recurrence_shape* s) {
+  return (size_t)(s->batch * s->seqlen * s->dim) * (size_t)esize(s->dtype);
+}
+
+size_t state_bytes(const mamba_recurrence_shape* s) { return (size_t)(s->batch * s->dim) * 4; }
+
+// From the first element of a view of rows to the end of its last.
+Region rows(const mamba_recurrence_shape* s, const void* p, int64_t sb, int64_t st) {
+  return {p, (size_t)((s->batch - 1) * sb + (s->seqlen - 1) * st + s->dim) *
+                 (size_t)esize(s->dtype)};
+}
+
+// Whether one of the outputs lies over what every call of the recurrence reads.
+bool over_shared(std::initializer_list<Region> outputs, const mamba_recurrence_shape* s,
+                 const void* x, const void* r, const void* i, const float* A, const void* z) {
+  return over_inputs(outputs, {rows(s, x, s->x_batch_stride, s->x_token_stride),
+                               rows(s, r, s->r_batch_stride, s->r_token_stride),
+                               rows(s, i, s->i_batch_stride, s->i_token_stride),
+                               rows(s, z, s->z_batch_stride, s->z_token_stride),
+                               {A, (size_t)s->dim * 4}});
 }
 
 int64_t tiles(const mamba_recurrence_shape* s) {
@@ -239,7 +263,9 @@ mamba_status norm_fwd(const View& x, View res, const float* weight, int64_t batc
     return MAMBA_ERR_ALIGNMENT;
   const size_t n = (size_t)(batch * rows * dim), no = n * (fp8 ? 1 : (size_t)es), nr = n * (size_t)er;
   const size_t sx = span(x, batch, rows, dim, es), sr = span(res, batch, rows, dim, er);
-  if (overlap(out, no, x.p, sx) || overlap(out, no, res.p, sr) || overlap(residual_out, nr, x.p, sx))
+  const Region o = {out, no}, sc = {scale, (size_t)(batch * rows) * 4}, k = {residual_out, nr};
+  if (over_inputs({o, sc, k}, {{x.p, sx}, {weight, (size_t)dim * 4}}) ||
+      over_inputs({o, sc}, {{res.p, sr}}))
     return MAMBA_ERR_INVALID;
   // the stream is carried in place row on row, or apart
   const bool dense = (rows == 1 || res.row == dim) && (batch == 1 || res.batch == rows * dim);
@@ -294,7 +320,13 @@ mamba_status mamba_gated_recurrence_fwd(const mamba_recurrence_shape* shape, con
     return MAMBA_ERR_INVALID;
   const size_t need = mamba_gated_recurrence_fwd_workspace_size(shape);
   if (need == SIZE_MAX) return MAMBA_ERR_UNSUPPORTED;
-  if (over_inputs(out, shape, x, r, i, z)) return MAMBA_ERR_INVALID;
+  const size_t seq = sequence_bytes(shape), state = state_bytes(shape);
+  const size_t marks = mamba_gated_recurrence_checkpoint_size(shape);
+  const Region o = {out, seq}, l = {last_state, state}, c = {checkpoints, marks};
+  const Region flags = {reset, (size_t)(shape->batch * shape->seqlen)};
+  if (over_shared({o, l, c}, shape, x, r, i, A, z) || over_inputs({o, l, c}, {flags}) ||
+      over_inputs({o, c}, {{h0, state}}))
+    return MAMBA_ERR_INVALID;
   if (need && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
   if (need && !aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
   mscan::RecParams p = common(shape, x, r, i, A, z, h0, reset);
@@ -324,8 +356,14 @@ mamba_status mamba_gated_recurrence_bwd(const mamba_recurrence_shape* shape, con
       !aligned_f32(dA) || !aligned_f32(dh0))
     return MAMBA_ERR_ALIGNMENT;
   if (!bwd_ok(shape) || (!checkpoints && !fwd_ok(shape))) return MAMBA_ERR_UNSUPPORTED;
-  if (over_inputs(dx, shape, x, r, i, z) || over_inputs(dr, shape, x, r, i, z) ||
-      over_inputs(di, shape, x, r, i, z) || over_inputs(dz, shape, x, r, i, z))
+  const size_t seq = sequence_bytes(shape), state = state_bytes(shape);
+  const size_t marks = (size_t)(shape->batch * shape->dim) * (size_t)tiles(shape) * 4;
+  const Region x_ = {dx, seq}, r_ = {dr, seq}, i_ = {di, seq}, z_ = {dz, seq};
+  const Region a_ = {dA, (size_t)shape->dim * 4}, h_ = {dh0, state};
+  if (over_shared({x_, r_, i_, z_, a_, h_}, shape, x, r, i, A, z) ||
+      over_inputs({x_, r_, i_, z_, a_, h_},
+                  {{h0, state}, {reset, (size_t)(shape->batch * shape->seqlen)}, {dout, seq},
+                   {dlast_state, state}, {checkpoints, marks}}))
     return MAMBA_ERR_INVALID;
   const BwdLayout l = bwd_layout(shape, checkpoints != nullptr);
   if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
@@ -364,7 +402,10 @@ mamba_status mamba_gated_recurrence_update(const mamba_recurrence_shape* shape, 
   if (!state || !out) return MAMBA_ERR_NULL_PTR;
   if (!aligned(out, (size_t)esize(shape->dtype)) || !aligned_f32(state) || !aligned(slots, 4))
     return MAMBA_ERR_ALIGNMENT;
-  if (over_inputs(out, shape, x, r, i, z)) return MAMBA_ERR_INVALID;
+  const Region o = {out, sequence_bytes(shape)}, st_ = {state, (size_t)(pool * shape->dim) * 4};
+  if (over_shared({o, st_}, shape, x, r, i, A, z) ||
+      over_inputs({o, st_}, {{slots, (size_t)shape->batch * 4}}) || over_inputs({o}, {st_}))
+    return MAMBA_ERR_INVALID;
   mscan::RecStepParams p{};
   p.x = x; p.r = r; p.i = i; p.z = z;
   p.x_row = shape->x_batch_stride; p.r_row = shape->r_batch_stride;
@@ -432,8 +473,9 @@ mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_batch_stride,
       !aligned_f32(dweight))
     return MAMBA_ERR_ALIGNMENT;
   const size_t n = (size_t)(batch * rows * dim), sr = span(r, batch, rows, dim, er);
-  if (overlap(dx, n * (size_t)es, dout, n * (size_t)es) || overlap(dx, n * (size_t)es, res, sr) ||
-      overlap(dresidual, n * (size_t)er, res, sr))
+  const size_t wide = (size_t)dim * 4;
+  if (over_inputs({{dx, n * (size_t)es}, {dresidual, n * (size_t)er}, {dweight, wide}},
+                  {{res, sr}, {weight, wide}, {dout, n * (size_t)es}, {dres, n * (size_t)er}}))
     return MAMBA_ERR_INVALID;
   const size_t need = mamba_residual_norm_bwd_workspace_size(batch * rows, dim);
   if (need == SIZE_MAX) return MAMBA_ERR_UNSUPPORTED;
