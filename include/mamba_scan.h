@@ -651,7 +651,8 @@ mamba_status mamba_gated_norm_bwd(const void* x, int64_t x_row_stride, const voi
  * inputs, which without them forms them again.
  * Pointers are aligned to their element.  last_state may be h0 itself (the
  * state steps in place), not a part of it; no other output may overlap an
- * input.  Sums run in a fixed order: equal inputs give equal bits.
+ * input, nor another output or the workspace, and the workspace overlaps
+ * nothing.  Sums run in a fixed order: equal inputs give equal bits.
  * The blocks of a call wait for one another through its workspace, which no
  * other call may use until this one has ended.
  * ------------------------------------------------------------------------ */
@@ -710,7 +711,8 @@ mamba_status mamba_gated_recurrence_update(const mamba_recurrence_shape* shape, 
  * and the gradients are dense.  weight (nullable = 1) and dweight (dim) float32.
  * Without residual there is no residual_out.  residual_out may be residual itself
  * where that is dense (the stream is carried on in place); no other output may
- * overlap an input. */
+ * overlap an input, nor another output or the workspace, and the workspace
+ * overlaps nothing. */
 mamba_status mamba_residual_norm_fwd(const void* x, int64_t x_batch_stride, int64_t x_row_stride,
                                      const void* residual, int64_t residual_batch_stride,
                                      int64_t residual_row_stride, const float* weight,

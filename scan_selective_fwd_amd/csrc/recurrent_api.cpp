@@ -105,6 +105,14 @@ bool over_inputs(std::initializer_list<Region> outputs, std::initializer_list<Re
   return false;
 }
 
+// Whether two of the outputs lie over one another.
+bool over_each_other(std::initializer_list<Region> outputs) {
+  for (const Region* a = outputs.begin(); a != outputs.end(); ++a)
+    for (const Region* b = a + 1; b != outputs.end(); ++b)
+      if (overlap(a->p, a->n, b->p, b->n)) return true;
+  return false;
+}
+
 size_t sequence_bytes(const mamba_recurrence_shape* s) {
   return (size_t)(s->batch * s->seqlen * s->dim) * (size_t)esize(s->dtype);
 }
@@ -265,7 +273,7 @@ mamba_status norm_fwd(const View& x, View res, const float* weight, int64_t batc
   const size_t sx = span(x, batch, rows, dim, es), sr = span(res, batch, rows, dim, er);
   const Region o = {out, no}, sc = {scale, (size_t)(batch * rows) * 4}, k = {residual_out, nr};
   if (over_inputs({o, sc, k}, {{x.p, sx}, {weight, (size_t)dim * 4}}) ||
-      over_inputs({o, sc}, {{res.p, sr}}))
+      over_inputs({o, sc}, {{res.p, sr}}) || over_each_other({o, sc, k}))
     return MAMBA_ERR_INVALID;
   // the stream is carried in place row on row, or apart
   const bool dense = (rows == 1 || res.row == dim) && (batch == 1 || res.batch == rows * dim);
@@ -323,12 +331,15 @@ mamba_status mamba_gated_recurrence_fwd(const mamba_recurrence_shape* shape, con
   const size_t seq = sequence_bytes(shape), state = state_bytes(shape);
   const size_t marks = mamba_gated_recurrence_checkpoint_size(shape);
   const Region o = {out, seq}, l = {last_state, state}, c = {checkpoints, marks};
+  const Region w = {need ? workspace : nullptr, need};
   const Region flags = {reset, (size_t)(shape->batch * shape->seqlen)};
   if (over_shared({o, l, c}, shape, x, r, i, A, z) || over_inputs({o, l, c}, {flags}) ||
-      over_inputs({o, c}, {{h0, state}}))
+      over_inputs({o, c}, {{h0, state}}) || over_each_other({o, l, c}))
     return MAMBA_ERR_INVALID;
   if (need && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
   if (need && !aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
+  if (over_shared({w}, shape, x, r, i, A, z) || over_inputs({w}, {flags, {h0, state}, o, l, c}))
+    return MAMBA_ERR_INVALID;
   mscan::RecParams p = common(shape, x, r, i, A, z, h0, reset);
   p.out = out; p.last = last_state; p.ckpt = checkpoints;
   p.pairs = pairs(shape, x, r, i, z) && aligned(out, 4);
@@ -360,14 +371,19 @@ mamba_status mamba_gated_recurrence_bwd(const mamba_recurrence_shape* shape, con
   const size_t marks = (size_t)(shape->batch * shape->dim) * (size_t)tiles(shape) * 4;
   const Region x_ = {dx, seq}, r_ = {dr, seq}, i_ = {di, seq}, z_ = {dz, seq};
   const Region a_ = {dA, (size_t)shape->dim * 4}, h_ = {dh0, state};
+  const Region h = {h0, state}, flags = {reset, (size_t)(shape->batch * shape->seqlen)};
+  const Region d = {dout, seq}, l_ = {dlast_state, state}, c = {checkpoints, marks};
   if (over_shared({x_, r_, i_, z_, a_, h_}, shape, x, r, i, A, z) ||
-      over_inputs({x_, r_, i_, z_, a_, h_},
-                  {{h0, state}, {reset, (size_t)(shape->batch * shape->seqlen)}, {dout, seq},
-                   {dlast_state, state}, {checkpoints, marks}}))
+      over_inputs({x_, r_, i_, z_, a_, h_}, {h, flags, d, l_, c}) ||
+      over_each_other({x_, r_, i_, z_, a_, h_}))
     return MAMBA_ERR_INVALID;
   const BwdLayout l = bwd_layout(shape, checkpoints != nullptr);
   if (!workspace || workspace_bytes < l.total) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
+  const Region w = {workspace, l.total};
+  if (over_shared({w}, shape, x, r, i, A, z) ||
+      over_inputs({w}, {h, flags, d, l_, c, x_, r_, i_, z_, a_, h_}))
+    return MAMBA_ERR_INVALID;
   mscan::RecParams p = common(shape, x, r, i, A, z, h0, reset);
   char* ws = static_cast<char*>(workspace);
   p.dout = dout; p.dlast = dlast_state;
@@ -474,13 +490,15 @@ mamba_status mamba_residual_norm_bwd(const void* res, int64_t res_batch_stride,
     return MAMBA_ERR_ALIGNMENT;
   const size_t n = (size_t)(batch * rows * dim), sr = span(r, batch, rows, dim, er);
   const size_t wide = (size_t)dim * 4;
-  if (over_inputs({{dx, n * (size_t)es}, {dresidual, n * (size_t)er}, {dweight, wide}},
-                  {{res, sr}, {weight, wide}, {dout, n * (size_t)es}, {dres, n * (size_t)er}}))
+  const Region x_ = {dx, n * (size_t)es}, r_ = {dresidual, n * (size_t)er}, w_ = {dweight, wide};
+  const Region in = {res, sr}, g = {weight, wide}, d = {dout, n * (size_t)es}, s = {dres, n * (size_t)er};
+  if (over_inputs({x_, r_, w_}, {in, g, d, s}) || over_each_other({x_, r_, w_}))
     return MAMBA_ERR_INVALID;
   const size_t need = mamba_residual_norm_bwd_workspace_size(batch * rows, dim);
   if (need == SIZE_MAX) return MAMBA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return MAMBA_ERR_ALIGNMENT;
+  if (over_inputs({{workspace, need}}, {in, g, d, s, x_, r_, w_})) return MAMBA_ERR_INVALID;
   mscan::ResNormParams p{};
   p.res = res; p.res_batch = r.batch; p.res_row = r.row;
   p.inner = one_run(r, batch, rows) ? 0 : rows;
