@@ -641,6 +641,7 @@ mamba_status mamba_gated_norm_bwd(const void* x, int64_t x_row_stride, const voi
  * elements are contiguous), the rest is dense.  A, dA (dim) and h0,
  * last_state, dlast_state, dh0 (batch, dim) are float32.  A <= 0; where A = 0
  * the state is kept, nothing enters it, and dA is not finite.
+ * The backward forms A s(r) times states, which has to stay within float32.
  * reset (nullable, (batch, seqlen) bytes): the state entering a flagged step
  * is left out.  Non-finite values: one in a token of a packed sequence never
  * reaches another sequence's rows, nor, in the forward, earlier rows of its

@@ -12,9 +12,9 @@
 // A lane takes one channel, a wave 8 steps, a block 8 waves: what a step's gradients take
 // of its gates (seven values) then fits 128 registers beside the loads, and two blocks
 // share a CU.  Every tensor is read once and written once.  2 x 2048 x 5120 in bfloat16
-// with z take 95 us (378 MB, 4.0 TB/s; without the joining and the gates' arithmetic the
-// same loads and stores take 94), 4 x 777 x 1025 in float32 with flags 23; a SIMD issues
-// VALU for 55 us of the first.  A block lives 9 us: 0.6 for its ticket, 2.6 until its gates
+// with z take 95 to 97 us (378 MB, 4.0 TB/s; without the joining and the gates' arithmetic the
+// same loads and stores take 94), 4 x 777 x 1025 in float32 with flags 24 (884 tiles, 1.7
+// times those that fit at once); a SIMD issues VALU for 57 us of the first.  A block lives 9 us: 0.6 for its ticket, 2.6 until its gates
 // are formed, 2.6 for the states and both sums of maps, 1.9 for the tiles behind it, 1.3
 // for the gradients.  Tried: two channels a lane (243 us, spills), the gates formed a
 // second time instead of kept (132), tiles of 128 steps and one block a CU (158), three

@@ -15,7 +15,7 @@
 // Bound by HBM and by what joins the tiles: 8 x 2048 x 1536 in bfloat16 with z take 59 us
 // (252 MB, 4.3 TB/s; without the joining and the gates' arithmetic the same loads and
 // stores take 55), 131072 x 1536 without z 360 (1.61 GB, 4.5 TB/s; 312), 2 x 2048 x 5120
-// with z 49, 3 x 1000 x 1003 in float32 with z and flags 16.  A SIMD issues VALU for 28 us
+// with z 49, 3 x 1000 x 1003 in float32 with z and flags 15 (384 tiles on 256 CUs).  A SIMD issues VALU for 28 us
 // of the first (36 instructions and 8 transcendental ones an element).  Tried: tiles of 64
 // steps (four blocks a CU, 509 us for the long one), of 256 (one block a CU, 436), groups
 // of 8 and 32 tiles (380, 442), blocks that take tile after tile (88 us for 49: a loop's

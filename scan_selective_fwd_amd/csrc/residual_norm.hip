@@ -9,7 +9,7 @@
 // value of 8 bits is found on the way.  Rows too long for that are walked again from the
 // cache.  Bound by HBM: the forward of 16384 rows of 1536 in bfloat16 takes 31 to 34 us (201
 // MB, 5.9 TB/s or more; 36 to 37 where each group's loads wait for those before), of 4096 of
-// 5120 on a float32 stream into 8 bits 38 to 40 (231 MB, 5.8; 47); the backward of 4096 of 5120
+// 5120 on a float32 stream into 8 bits 39 to 41 (231 MB, 5.7; 47); the backward of 4096 of 5120
 // in bfloat16 29 to 32 (168 MB, 5.2), and 4 for the sum of dw.  Rows that start anywhere are
 // read as wide: 4096 of 6001 in bfloat16 take 32 us forward, 52 backward (element by element
 // 122 and 120), 2000 of 8191 24 and 36 (75 and 75).
@@ -23,8 +23,9 @@ constexpr int kParts = 512;        // blocks of the backward: two a CU
 constexpr int kFwdBlocks = (1 << 22) - 1;   // of up to 1024 threads in one launch
 constexpr int kWalk = 1024;
 // Rows up to here go by single elements, one a lane: 27941 of 38 in bfloat16 take 8.0 us
-// forward and 13.5 backward (11.2 and 15.6 in groups), 16000 of 64 5.5 and 9.6 (6.7 and
-// 10.4); 64000 of 128 24 and 30 by two elements a lane, 20 and 30 in groups.
+// forward and 13.5 backward (11.2 and 15.6 in groups; their bytes 1.7 at 5.0 TB/s), 16000 of
+// 64 5.5 and 9.6 (6.7 and 10.4; 1.6); 64000 of 128 24 and 30 by two elements a lane, 20 and
+// 29 in groups (13).  What is left above the bytes is lanes without work: a row is a wave's.
 constexpr int kNarrow = 64;
 
 // Where row `row` of a view starts.
